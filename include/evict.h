@@ -302,6 +302,161 @@ int evict_qfilters_filters(evict_handle* h, float* out_host, int* n_rows);
  * methods. */
 int evict_curdkv_scores(evict_handle* h, float* attn, float* leverage, int* n_rows);
 
+/* --------------------------------------------------------------------------
+ * Around the kept cache: position rotation, pages of own rows, attention
+ * --------------------------------------------------------------------------
+ * The cache takes keys that are already rotated at their absolute positions
+ * and returns the rows to attend to. The calls below are the steps on either
+ * side: rotating queries and keys, appending a batch's own rows to pages, and
+ * the attention of a batch over a kept prefix that its sequences share and
+ * over each sequence's own pages.
+ *
+ * They keep the conventions above, except that they hold no handle of a
+ * cache: every call names its stream (cudaStream_t; NULL = legacy default),
+ * which belongs to the current device, as do all its pointers. Nothing is
+ * allocated, synchronised or read back, so every call may be captured; no
+ * call keeps anything for the next one. */
+
+/* Rows [batch, heads, m, 128] of one tensor; strides in elements. */
+typedef struct evict_rows {
+  void* data;
+  int64_t stride_b, stride_h, stride_m;
+  int heads;
+} evict_rows;
+
+/* Rotary positions. Pair i (0 <= i < rotary_dim / 2) of a row turns by the
+ * angle pos[axis[i]] * inv_freq[i]:
+ *     (x, y) -> scale * (x cos a - y sin a, x sin a + y cos a).
+ * Its elements are (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with `adjacent`.
+ * Elements from rotary_dim on are copied unchanged, bit for bit. With several axes (time,
+ * height, width of a video's tokens) each frequency follows the axis that
+ * `axis` names. */
+typedef struct evict_rotary_config {
+  int rotary_dim;          /* even, 2 .. 128 */
+  int adjacent;            /* 0 or 1 */
+  int n_axes;              /* 1 .. 4 position axes */
+  float scale;             /* multiplies cos and sin (1 for a pure rotation) */
+  const double* inv_freq;  /* HOST [rotary_dim / 2] radians per position, finite; copied */
+  const uint8_t* axis;     /* HOST [rotary_dim / 2], each < n_axes; copied. NULL = all 0 */
+} evict_rotary_config;
+
+/* A rotation's tables. Host memory only and never written after init: one
+ * object serves any device, stream, captured graph or thread at once. */
+typedef struct evict_rotary evict_rotary;
+
+/* EVICT_EINVAL: bad rotary_dim, adjacent, n_axes or axis, non-finite scale or inv_freq. */
+int evict_rotary_init(const evict_rotary_config* cfg, evict_rotary** out);
+void evict_rotary_destroy(evict_rotary* r);
+
+/* Rotate n_tensors (1 or 2: queries and keys) tensors of `batch` x m rows in
+ * one launch: out[i] <- rotation of x[i]. pos [n_axes, batch, m] device int32,
+ * or NULL (then every axis has pos_base + t at token t). transpose = 1 turns
+ * by the negative angle, with the same scale: the rotation's gradient, and
+ * (scale 1) its inverse. Angles are exact to fp32 for every int32 position:
+ * they are held as 64-bit fractions of a turn. Arithmetic is fp32, rounded
+ * once to `dtype`.
+ * out[i] may be x[i] itself (same data and strides); otherwise they must not
+ * overlap. Rows whose addresses and strides are multiples of 16 bytes, with
+ * rotary_dim a multiple of 16, move in 16-byte pieces; any other layout is
+ * taken an element at a time.
+ * EVICT_EINVAL: NULL or misaligned pointers, bad sizes, out[i].heads !=
+ * x[i].heads. EVICT_ELIMIT: batch * m * heads of 2^31 or more. batch or m of
+ * 0 is a no-op. */
+int evict_rotate(const evict_rotary* r, int dtype, int batch, int m, const int32_t* pos, int64_t pos_base,
+                 int transpose, const evict_rows* x, const evict_rows* out, int n_tensors, void* stream);
+
+/* A batch's own rows in pages of a shared pool. Page p, head h, row i of it
+ * are at k + p * page_stride + (h * page_size + i) * 128, v alike. Row j of
+ * sequence b lies in page table[b * table_stride + j / page_size], row
+ * j % page_size. Pages may be shared between sequences by any call that only
+ * reads them. */
+typedef struct evict_pages {
+  void* k;                 /* device, 16-byte aligned */
+  void* v;
+  int64_t page_stride;     /* elements between pages, a multiple of 8 (0 = n_kv_heads * page_size * 128) */
+  int n_pages;
+  int page_size;           /* 16, 32, 64, 128 or 256 rows */
+  int n_kv_heads;
+  int dtype;               /* evict_dtype */
+  const int32_t* table;    /* device [batch, table_width] */
+  int64_t table_stride;    /* elements between its rows (0 = table_width) */
+  int table_width;
+  const int32_t* lens;     /* device [batch]: rows of each sequence, the call's new rows included */
+  int32_t* error;          /* device word for the first device error, cleared by evict_pages_status; may be NULL */
+} evict_pages;
+
+/* Append the new rows of a batch: token t < n_new[b] of sequence b goes to
+ * its row lens[b] - n_new[b] + t; `lens` already counts the new rows. n_new
+ * [batch] device int32, or NULL (m new rows each); tokens from n_new[b] on
+ * are padding, neither read nor written anywhere.
+ * With `r`, keys are rotated on the way, by pos [n_axes, batch, m], or with
+ * pos NULL by pos_base + the row's index in its sequence (behind a shared
+ * prompt: pos_base = the prompt's offset). Values are copied. r = NULL copies
+ * the keys, too. q (with q_out; both may be NULL) are the step's queries
+ * [batch, q->heads, m, 128], rotated alike in the same launch.
+ * Two rows of one call that fall on the same page row leave either of them.
+ * A table entry outside the pool, or a row outside the table, is skipped and
+ * reported through pages->error as kind "index" (EVICT_EDEVICE of
+ * evict_pages_status); so are n_new[b] outside [0, m], taken as the nearest
+ * of these.
+ * EVICT_EINVAL and EVICT_ELIMIT as evict_rotate, or bad pages. */
+int evict_paged_append(const evict_pages* pages, int batch, int m, const int32_t* n_new, const evict_rotary* r,
+                       const int32_t* pos, int64_t pos_base, const evict_rows* k, const evict_rows* v,
+                       const evict_rows* q, const evict_rows* q_out, void* stream);
+
+/* Synchronise `stream`, read `error` (a device word as in evict_pages) and
+ * clear it: EVICT_OK, or EVICT_EDEVICE if a kernel has reported an error. */
+int evict_pages_status(int32_t* error, void* stream);
+
+/* Attention of a batch over a shared prefix and its own pages (bf16). Query t
+ * of sequence b and query head g sees, with KV head g / (n_q_heads /
+ * n_kv_heads):
+ *   - the n_prefix rows of prefix b / (batch / prefix_batch), all of them
+ *     (each prefix serves batch / prefix_batch sequences and is read for all
+ *     of them at once), e.g. the view of an evict_handle;
+ *   - its own rows j <= lens[b] - n_new[b] + t.
+ * out = softmax(scale * q . k) v over the rows it sees; lse = the natural
+ * logarithm of the sum of exp(scale * q . k). A query that sees no row gets
+ * out = 0 and lse = -inf. Rows a query does not see do not reach its result,
+ * whatever they hold (infinities and NaN included). Tokens from n_new[b] on
+ * are padding: their rows of out and lse are left as they were.
+ * Either part may be absent: pages = NULL (attention over kept rows only;
+ * n_new still marks padding) or n_prefix = 0. Logits, softmax statistics and
+ * sums are fp32; the result is rounded once to bf16. Results do not depend on
+ * anything but the arguments (no order of atomics). */
+typedef struct evict_attention {
+  int batch, m, n_q_heads, n_kv_heads;
+  evict_rows q;              /* bf16; addresses and strides multiples of 16 bytes */
+  evict_rows out;            /* bf16, likewise; must not overlap any input */
+  float* lse;                /* device [batch, n_q_heads, m], or NULL */
+  float scale;               /* 0 = 1 / sqrt(128) */
+  const void* prefix_k;      /* device bf16 [prefix_batch, n_kv_heads, n_prefix, 128], rows 128 apart */
+  const void* prefix_v;
+  int64_t prefix_stride_b;   /* elements, multiples of 8 */
+  int64_t prefix_stride_h;
+  int n_prefix;
+  int prefix_batch;          /* divides batch */
+  const evict_pages* pages;  /* bf16; or NULL */
+  const int32_t* n_new;      /* device [batch], or NULL (m each) */
+  void* workspace;           /* device, 256-byte aligned; in use until the call's work is done */
+  size_t workspace_bytes;    /* at least evict_shared_attention_workspace() */
+  int32_t* error;            /* device word as in evict_pages, or NULL */
+  void* stream;
+} evict_attention;
+
+/* Bytes of workspace that a call with these sizes needs on the current device (a bound for every
+ * lens and n_new): reads batch, m, the head counts, n_prefix, prefix_batch and pages' sizes. */
+int evict_shared_attention_workspace(const evict_attention* a, size_t* bytes);
+
+/* EVICT_EINVAL: NULL or misaligned pointers, bad sizes or strides, head counts that do not divide,
+ * pages that are not bf16, a workspace that is too small; EVICT_ELIMIT: batch above
+ * EVICT_MAX_ATTEND_BATCH, or batch * n_q_heads * m of 2^31 or more. batch or m of 0 is a no-op.
+ * Device errors (a table entry outside the pool, read as zeros; lens beyond the table, cut to it;
+ * n_new outside [0, m], taken as the nearest of these; a bounded wait that gave up) are reported
+ * through `error`. */
+int evict_shared_attention(const evict_attention* a);
+#define EVICT_MAX_ATTEND_BATCH 4096
+
 /* Process-wide count of kernels this library has launched. */
 int64_t evict_launch_count(void);
 

@@ -51,6 +51,34 @@ class EvictKernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char_p), ("launches", ctypes.c_int64), ("total_ms", ctypes.c_double)]
 
 
+class EvictRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_m", ctypes.c_int64), ("heads", ctypes.c_int)]
+
+
+class EvictRotaryConfig(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("adjacent", ctypes.c_int), ("n_axes", ctypes.c_int),
+                ("scale", ctypes.c_float), ("inv_freq", ctypes.POINTER(ctypes.c_double)),
+                ("axis", ctypes.POINTER(ctypes.c_uint8))]
+
+
+class EvictPages(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("table_width", ctypes.c_int), ("lens", ctypes.c_void_p), ("error", ctypes.c_void_p)]
+
+
+class EvictAttention(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("m", ctypes.c_int), ("n_q_heads", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("q", EvictRows), ("out", EvictRows), ("lse", ctypes.c_void_p),
+                ("scale", ctypes.c_float), ("prefix_k", ctypes.c_void_p), ("prefix_v", ctypes.c_void_p),
+                ("prefix_stride_b", ctypes.c_int64), ("prefix_stride_h", ctypes.c_int64),
+                ("n_prefix", ctypes.c_int), ("prefix_batch", ctypes.c_int), ("pages", ctypes.POINTER(EvictPages)),
+                ("n_new", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+                ("error", ctypes.c_void_p), ("stream", ctypes.c_void_p)]
+
+
 class EvictError(RuntimeError):
     def __init__(self, code, msg):
         super().__init__(f"libevict error {code}: {msg}")
@@ -82,6 +110,16 @@ _SIGNATURES = {
     "evict_noalloc_status": (_I, [_P]),
     "evict_curdkv_scores": (_I, [_P, _P, _P, ctypes.POINTER(_I)]),
     "evict_qfilters_filters": (_I, [_P, _P, ctypes.POINTER(_I)]),
+    "evict_rotary_init": (_I, [ctypes.POINTER(EvictRotaryConfig), ctypes.POINTER(_P)]),
+    "evict_rotary_destroy": (None, [_P]),
+    "evict_rotate": (_I, [_P, _I, _I, _I, _P, ctypes.c_int64, _I, ctypes.POINTER(EvictRows),
+                          ctypes.POINTER(EvictRows), _I, _P]),
+    "evict_paged_append": (_I, [ctypes.POINTER(EvictPages), _I, _I, _P, _P, _P, ctypes.c_int64,
+                                ctypes.POINTER(EvictRows), ctypes.POINTER(EvictRows), ctypes.POINTER(EvictRows),
+                                ctypes.POINTER(EvictRows), _P]),
+    "evict_pages_status": (_I, [_P, _P]),
+    "evict_shared_attention_workspace": (_I, [ctypes.POINTER(EvictAttention), ctypes.POINTER(ctypes.c_size_t)]),
+    "evict_shared_attention": (_I, [ctypes.POINTER(EvictAttention)]),
     "evict_launch_count": (ctypes.c_int64, []),
     "evict_last_error": (ctypes.c_char_p, []),
 }
@@ -226,6 +264,42 @@ def evict_qfilters_filters(h):
     return out
 
 
+def evict_rotary_init(cfg: EvictRotaryConfig) -> int:
+    r = _P()
+    check(load().evict_rotary_init(ctypes.byref(cfg), ctypes.byref(r)))
+    return r.value
+
+
+def evict_rotary_destroy(r):
+    load().evict_rotary_destroy(r)
+
+
+def evict_rotate(r, dtype, batch, m, pos_ptr, pos_base, transpose, x, out, n_tensors, stream):
+    """x, out: ctypes arrays of EvictRows."""
+    check(load().evict_rotate(r, dtype, batch, m, pos_ptr, pos_base, transpose, x, out, n_tensors, stream))
+
+
+def evict_paged_append(pages: EvictPages, batch, m, n_new_ptr, r, pos_ptr, pos_base, k, v, q, q_out, stream):
+    """k, v, q, q_out: EvictRows (q and q_out may be None)."""
+    check(load().evict_paged_append(pages, batch, m, n_new_ptr, r, pos_ptr, pos_base, k, v, q, q_out, stream))
+
+
+def evict_pages_status(error_ptr, stream=None):
+    """Synchronise `stream`; raise EvictError(EVICT_EDEVICE) if a kernel reported an error through
+    the device word `error_ptr` (which is then cleared)."""
+    check(load().evict_pages_status(error_ptr, stream))
+
+
+def evict_shared_attention_workspace(a: EvictAttention) -> int:
+    n = ctypes.c_size_t()
+    check(load().evict_shared_attention_workspace(a, n))
+    return n.value
+
+
+def evict_shared_attention(a: EvictAttention):
+    check(load().evict_shared_attention(a))
+
+
 def evict_launch_count() -> int:
     return load().evict_launch_count()
 
@@ -310,6 +384,14 @@ class EvictCache:
         pos_ptr = pos.data_ptr() if pos is not None else None
         view = evict_update_and_fetch(self.handle, k.data_ptr(), v.data_ptr(), pos_ptr, m)
         return view_tensors(view, self.batch, self.heads, self.dtype)
+
+    def attend(self, q, n_new=None, scale=None, out=None, lse=None):
+        """Attention of the queries q [batch, n_q_heads, m, 128] (bf16, rotated) over this cache's
+        kept rows, all of which every query sees: paged.shared_attention without pages. A batch
+        that is a multiple of the cache's gives every kept prefix to that many sequences."""
+        from . import paged
+        k, v, _, _ = self.view()
+        return paged.shared_attention(q, prefix=(k, v), n_new=n_new, scale=scale, out=out, lse=lse)
 
     def view(self):
         return view_tensors(evict_get_view(self.handle), self.batch, self.heads, self.dtype)

@@ -1,0 +1,25 @@
+// Tables of a rotation (see rotary.cu) and the checks shared by the calls on pages.
+#pragma once
+
+#include <stdint.h>
+
+#include "../../include/evict.h"
+
+namespace evict {
+
+struct RotaryTable {
+  uint64_t freq[EVICT_HEAD_DIM / 2];   // turns per position, as a fraction of 2^64
+  uint8_t axis[EVICT_HEAD_DIM / 2];
+  int half;                            // pairs that turn
+  int adjacent;
+  int n_axes;
+  float scale;
+};
+
+int check_pages(const evict_pages* pages);
+
+}  // namespace evict
+
+struct evict_rotary {
+  evict::RotaryTable t;
+};

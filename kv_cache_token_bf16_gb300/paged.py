@@ -1,0 +1,366 @@
+"""The steps around a kept cache: rotary positions, pages of a batch's own rows, attention.
+
+An ``EvictCache`` takes keys that are already rotated and returns the rows to attend to. Here are
+the calls on either side of it, as thin wrappers of the C calls of include/evict.h:
+
+* ``Rotary`` and ``rotate``: rotary positions of one to four axes (time, height, width of a video's
+  tokens), whole or partial heads, both pairings, forwards and transposed;
+* ``PagedCache``: own rows of a batch's sequences in pages, appended with the rotation applied on
+  the way, and the attention over them behind a prefix that the sequences share;
+* ``shared_attention``: that attention on its own, e.g. over an ``EvictCache``'s kept rows.
+
+A decode step behind a shared prompt that an ``EvictCache`` of batch 1 has absorbed::
+
+    rotary = paged.Rotary(base=500000.0)
+    own = paged.PagedCache(n_pages=4096, page_size=16, n_kv_heads=8, batch=32, max_rows=2048)
+    ...
+    own.grow(1)                                              # a row more for every sequence
+    own.append(k, v, rotary=rotary, pos_base=prompt.stats()["offset"], q=q, q_out=q)
+    out = own.attend(q, prefix=prompt.view()[:2])
+
+Work goes on the current stream of the tensors' device; nothing is synchronised. Tensors are
+[batch, heads, m, 128] with any strides whose innermost is 1, so a projection's
+[batch, m, heads, 128] is passed as ``x.transpose(1, 2)``.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import binding
+from .binding import EVICT_BF16, EVICT_FP32, HEAD_DIM, EvictAttention, EvictPages, EvictRotaryConfig, EvictRows
+
+PAGE_SIZES = (16, 32, 64, 128, 256)
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _dtype(t):
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return EVICT_BF16
+    if t.dtype == torch.float32:
+        return EVICT_FP32
+    raise ValueError(f"bf16 or fp32 tensors only, not {t.dtype}")
+
+
+def _rows(t, name, batch=None, m=None):
+    """EvictRows of a tensor [batch, heads, m, 128]."""
+    if t.dim() != 4 or t.shape[3] != HEAD_DIM:
+        raise ValueError(f"{name} must be [batch, heads, m, {HEAD_DIM}], not {tuple(t.shape)}")
+    if (batch is not None and t.shape[0] != batch) or (m is not None and t.shape[2] != m):
+        raise ValueError(f"{name} is {tuple(t.shape)}: batch or m differ from the other tensors")
+    sb, sh, sm, se = t.stride()
+    if se != 1:
+        raise ValueError(f"{name}: the 128 elements of a row must be adjacent")
+    return EvictRows(t.data_ptr(), sb, sh, sm, t.shape[1])
+
+
+def _like(t, name, shape, dtype, device):
+    """An int32 or fp32 side tensor: dense, of this shape, on this device. Its pointer."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _same_device(first, *others):
+    if not first.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    return first.device
+
+
+class _on:
+    """Makes a device current for the call (nothing to do where it already is)."""
+
+    def __init__(self, device):
+        torch = _torch()
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard:
+            self.guard.__enter__()
+        return _torch().cuda.current_stream().cuda_stream
+
+    def __exit__(self, *e):
+        if self.guard:
+            self.guard.__exit__(*e)
+
+
+class Rotary:
+    """The tables of a rotation (host memory; usable on any device and stream).
+
+    Pair i of a row turns by pos[axis[i]] * inv_freq[i]. ``inv_freq`` defaults to
+    base ** (-2 i / rotary_dim), rounded to fp32 as models hold it; ``axis`` names the position
+    axis of every pair, or ``sections`` gives how many pairs in a row each axis has. ``pairs``:
+    "half" pairs element i with i + rotary_dim / 2, "adjacent" 2 i with 2 i + 1. ``scale``
+    multiplies cos and sin.
+    """
+
+    def __init__(self, rotary_dim: int = HEAD_DIM, base: float = 10000.0, inv_freq=None, axis=None, sections=None,
+                 n_axes: int | None = None, pairs: str = "half", scale: float = 1.0):
+        self.handle = None
+        if pairs not in ("half", "adjacent"):
+            raise ValueError('pairs must be "half" or "adjacent"')
+        n = max(rotary_dim // 2, 0)
+        if inv_freq is None:
+            inv_freq = [ctypes.c_float(base ** (-2.0 * i / rotary_dim)).value for i in range(n)]
+        inv_freq = [float(x) for x in inv_freq]
+        if sections is not None:
+            if axis is not None:
+                raise ValueError("axis and sections exclude each other")
+            axis = [a for a, count in enumerate(sections) for _ in range(count)]
+        axis = [0] * n if axis is None else [int(a) for a in axis]
+        if len(inv_freq) != n or len(axis) != n:
+            raise ValueError(f"need {n} frequencies and axes, got {len(inv_freq)} and {len(axis)}")
+        if any(not 0 <= a < 256 for a in axis):
+            raise ValueError("axis must be >= 0")
+        self.rotary_dim, self.pairs = rotary_dim, pairs
+        self.n_axes = n_axes if n_axes is not None else (len(sections) if sections is not None else max(axis, default=0) + 1)
+        cfg = EvictRotaryConfig(rotary_dim=rotary_dim, adjacent=int(pairs == "adjacent"), n_axes=self.n_axes, scale=scale,
+                                inv_freq=(ctypes.c_double * max(n, 1))(*inv_freq), axis=(ctypes.c_uint8 * max(n, 1))(*axis))
+        self.handle = binding.evict_rotary_init(cfg)
+
+    def __del__(self):
+        try:
+            if self.handle:
+                binding.evict_rotary_destroy(self.handle)
+                self.handle = None
+        except Exception:
+            pass
+
+
+def rotate(rotary: Rotary, x, pos=None, pos_base: int = 0, out=None, transpose: bool = False):
+    """Rotate x [batch, heads, m, 128], or a pair of such tensors (queries and keys) in one launch.
+
+    pos [n_axes, batch, m] int32 (with one axis also [batch, m]), or None: token t of every
+    sequence is at pos_base + t. ``out`` (a tensor or pair; x itself rotates in place) defaults to
+    new dense tensors. ``transpose`` turns by the negative angle: the gradient of the rotation,
+    and with scale 1 its inverse.
+    """
+    torch = _torch()
+    one = torch.is_tensor(x)
+    xs = (x,) if one else tuple(x)
+    if out is None:
+        outs = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in xs)
+    else:
+        outs = (out,) if torch.is_tensor(out) else tuple(out)
+    if len(outs) != len(xs) or not 1 <= len(xs) <= 2:
+        raise ValueError("one or two tensors, and as many outputs")
+    device = _same_device(xs[0], *xs[1:], *outs)
+    batch, m = xs[0].shape[0], xs[0].shape[2]
+    for t, o in zip(xs, outs):
+        if t.dtype != xs[0].dtype or o.dtype != t.dtype or o.shape != t.shape:
+            raise ValueError("all tensors need one dtype, and outputs their input's shape")
+    ins = (EvictRows * len(xs))(*[_rows(t, "x", batch, m) for t in xs])
+    ous = (EvictRows * len(xs))(*[_rows(t, "out", batch, m) for t in outs])
+    with _on(device) as stream:
+        binding.evict_rotate(rotary.handle, _dtype(xs[0]), batch, m, _pos(pos, rotary, batch, m, device), pos_base,
+                             int(transpose), ins, ous, len(xs), stream)
+    return outs[0] if one else outs
+
+
+def _pos(pos, rotary, batch, m, device):
+    if pos is None:
+        return None
+    n_axes = rotary.n_axes if rotary is not None else 1
+    shape = (batch, m) if pos.dim() == 2 and n_axes == 1 else (n_axes, batch, m)
+    return _like(pos, "pos", shape, _torch().int32, device)
+
+
+def shared_attention(q, prefix=None, pages: "PagedCache | None" = None, n_new=None, scale=None, out=None, lse=None):
+    """Attention of q [batch, n_q_heads, m, 128] (bf16) over a shared prefix and own pages.
+
+    prefix: (K, V) [prefix_batch, n_kv_heads, n, 128], e.g. ``EvictCache.view()[:2]``; prefix p
+    serves the batch / prefix_batch sequences from p * (batch / prefix_batch) on. pages: a
+    PagedCache whose lens count the m (or n_new[b]) query tokens' own rows, which they see up to
+    their own. Padding queries (t >= n_new[b]) leave their rows of ``out`` and ``lse`` as they are;
+    a new ``out`` has zeros there. lse: fp32 [batch, n_q_heads, m] for the log-sum-exp. Returns out.
+    """
+    torch = _torch()
+    device = _same_device(q, out, lse, n_new)
+    if q.dtype != torch.bfloat16:
+        raise ValueError(f"q must be bf16, not {q.dtype}")
+    batch, hq, m = q.shape[0], q.shape[1], q.shape[2] if q.dim() == 4 else 0
+    if out is None:
+        out = (torch.empty if n_new is None else torch.zeros)(q.shape, dtype=q.dtype, device=device)
+    elif out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError("out must have q's shape and dtype")
+    a = EvictAttention(batch=batch, m=m, n_q_heads=hq, q=_rows(q, "q"), out=_rows(out, "out"),
+                       lse=_like(lse, "lse", (batch, hq, m), torch.float32, device),
+                       n_new=_like(n_new, "n_new", (batch,), torch.int32, device))
+    if scale is not None:
+        if scale == 0:
+            raise ValueError("scale must not be 0")
+        a.scale = scale
+    if pages is not None:
+        if pages.batch != batch or pages.device != device:
+            raise ValueError(f"the pages are for {pages.batch} sequences on {pages.device}")
+        a.pages = ctypes.pointer(pages.struct)
+        a.error = pages.error.data_ptr()
+        a.n_kv_heads = pages.n_kv_heads
+    if prefix is not None:
+        k, v = prefix
+        if k.dtype != q.dtype or v.dtype != q.dtype or k.shape != v.shape or k.dim() != 4 or k.shape[3] != HEAD_DIM:
+            raise ValueError(f"the prefix must be two bf16 tensors [prefix_batch, n_kv_heads, n, {HEAD_DIM}]")
+        _same_device(q, k, v)
+        if k.shape[2] > 0:
+            if pages is not None and k.shape[1] != pages.n_kv_heads:
+                raise ValueError(f"the prefix has {k.shape[1]} KV heads, the pages {pages.n_kv_heads}")
+            sb, sh, sn, se = k.stride()
+            if (v.stride(0), v.stride(1)) != (sb, sh) or se != 1 or v.stride(3) != 1 or \
+                    (k.shape[2] > 1 and (sn != HEAD_DIM or v.stride(2) != HEAD_DIM)):
+                raise ValueError("the prefix's rows must be adjacent, K and V with the same strides")
+            a.prefix_k, a.prefix_v, a.prefix_stride_b, a.prefix_stride_h = k.data_ptr(), v.data_ptr(), sb, sh
+            a.n_prefix, a.prefix_batch = k.shape[2], k.shape[0]
+        a.n_kv_heads = k.shape[1]
+    if a.n_kv_heads == 0:
+        raise ValueError("neither a prefix nor pages: nothing to attend to")
+    with _on(device) as stream:
+        a.stream = stream
+        bytes_ = binding.evict_shared_attention_workspace(a)
+        # from torch's allocator: reused in stream order, private to a graph that is being captured
+        ws = torch.empty(bytes_, dtype=torch.uint8, device=device)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), bytes_
+        binding.evict_shared_attention(a)
+    return out
+
+
+class PagedCache:
+    """Own rows of a batch of sequences, in pages of a pool.
+
+    Either ``PagedCache(n_pages=, page_size=, n_kv_heads=, batch=, max_rows=, dtype=)`` makes the
+    tensors (zeros, no rows), and ``grow`` / ``release`` hand out the pages; or the caller brings
+    ``k_pages``, ``v_pages`` [n_pages, n_kv_heads, page_size, 128] (a page's rows dense, pages any
+    stride apart), ``table`` [batch, width] int32 and ``lens`` [batch] int32, and keeps the last
+    two up to date: row j of sequence b is row j % page_size of page table[b, j // page_size], and
+    lens counts a call's new rows before the call.
+    """
+
+    def __init__(self, n_pages: int | None = None, page_size: int | None = None, n_kv_heads: int | None = None,
+                 batch: int | None = None, max_rows: int | None = None, dtype: str = "bf16", device=None,
+                 k_pages=None, v_pages=None, table=None, lens=None):
+        torch = _torch()
+        given = [x is not None for x in (k_pages, v_pages, table, lens)]
+        if any(given) and not all(given):
+            raise ValueError("k_pages, v_pages, table and lens go together")
+        self._free = self._rows = None
+        if not any(given):
+            if min(n_pages or 0, page_size or 0, n_kv_heads or 0, batch or 0, max_rows or 0) < 1:
+                raise ValueError("n_pages, page_size, n_kv_heads, batch and max_rows must be >= 1")
+            if page_size not in PAGE_SIZES:
+                raise ValueError(f"page_size must be one of {PAGE_SIZES}")
+            t = {"bf16": torch.bfloat16, "fp32": torch.float32}[dtype]
+            device = torch.device("cuda" if device is None else device)
+            k_pages = torch.zeros(n_pages, n_kv_heads, page_size, HEAD_DIM, dtype=t, device=device)
+            v_pages = torch.zeros_like(k_pages)
+            table = torch.zeros(batch, -(-max_rows // page_size), dtype=torch.int32, device=device)
+            lens = torch.zeros(batch, dtype=torch.int32, device=device)
+            self._free = list(range(n_pages - 1, -1, -1))
+            self._rows, self._pages = [0] * batch, [[] for _ in range(batch)]
+        self.device = _same_device(k_pages, v_pages, table, lens)
+        if k_pages.dim() != 4 or k_pages.shape[3] != HEAD_DIM or v_pages.shape != k_pages.shape or \
+                v_pages.dtype != k_pages.dtype or v_pages.stride() != k_pages.stride():
+            raise ValueError(f"pages must be two tensors [n_pages, n_kv_heads, page_size, {HEAD_DIM}] alike")
+        self.n_pages, self.n_kv_heads, self.page_size, _ = k_pages.shape
+        sp, sh, sr, se = k_pages.stride()
+        if (sh, sr, se) != (self.page_size * HEAD_DIM, HEAD_DIM, 1) and self.n_pages * self.n_kv_heads > 0:
+            raise ValueError("the rows of a page must be dense")
+        if table.dim() != 2 or table.dtype != torch.int32 or table.stride(1) != 1:
+            raise ValueError("table must be int32 [batch, width] with adjacent entries")
+        self.batch = table.shape[0]
+        _like(lens, "lens", (self.batch,), torch.int32, self.device)
+        self.k_pages, self.v_pages, self.table, self.lens = k_pages, v_pages, table, lens
+        self.error = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.struct = EvictPages(k=k_pages.data_ptr(), v=v_pages.data_ptr(), page_stride=sp, n_pages=self.n_pages,
+                                 page_size=self.page_size, n_kv_heads=self.n_kv_heads, dtype=_dtype(k_pages),
+                                 table=table.data_ptr(), table_stride=table.stride(0), table_width=table.shape[1],
+                                 lens=lens.data_ptr(), error=self.error.data_ptr())
+
+    # --- pages ------------------------------------------------------------------------------
+    def _managed(self):
+        if self._free is None:
+            raise ValueError("the caller keeps this cache's table and lens")
+
+    def _upload(self, rows):
+        """Table rows and all lens to the device, in stream order."""
+        torch = _torch()
+        with _on(self.device):
+            self.lens.copy_(torch.tensor(self._rows, dtype=torch.int32))
+            for b in rows:
+                if self._pages[b]:
+                    self.table[b, :len(self._pages[b])].copy_(torch.tensor(self._pages[b], dtype=torch.int32))
+
+    def grow(self, n_new):
+        """Count n_new (a number, or one for every sequence) new rows in, taking pages for them.
+        Raises ValueError, with nothing changed, where the pool or the table has no room."""
+        self._managed()
+        new = [int(n_new)] * self.batch if isinstance(n_new, int) else [int(n) for n in n_new]
+        if len(new) != self.batch or min(new, default=0) < 0:
+            raise ValueError("n_new must be one number >= 0 for every sequence")
+        need = [-(-(r + n) // self.page_size) - len(p) for r, n, p in zip(self._rows, new, self._pages)]
+        if any(len(p) + x > self.table.shape[1] for p, x in zip(self._pages, need)):
+            raise ValueError(f"a sequence would have more than {self.table.shape[1]} pages")
+        if sum(need) > len(self._free):
+            raise ValueError(f"{sum(need)} pages needed, {len(self._free)} free")
+        for b, x in enumerate(need):
+            self._pages[b] += [self._free.pop() for _ in range(x)]
+            self._rows[b] += new[b]
+        self._upload([b for b, x in enumerate(need) if x])
+
+    def release(self, b: int):
+        """Sequence b ends: its pages are free and it has no rows."""
+        self._managed()
+        self._free += reversed(self._pages[b])
+        self._pages[b], self._rows[b] = [], 0
+        self._upload([])
+
+    def rows(self):
+        """Rows of every sequence, as grow and release count them."""
+        self._managed()
+        return list(self._rows)
+
+    # --- calls ------------------------------------------------------------------------------
+    def append(self, k, v, rotary: Rotary | None = None, pos=None, pos_base: int = 0, n_new=None, q=None, q_out=None):
+        """Append k, v [batch, n_kv_heads, m, 128] (the last n_new[b], or m, of lens' rows).
+
+        With ``rotary``, keys turn by pos ([n_axes, batch, m] int32) or by pos_base + their row's
+        index in the sequence; values are copied. q [batch, n_q_heads, m, 128] is rotated alike
+        in the same launch, into q_out (q itself: in place; None: a new tensor). Returns q_out.
+        """
+        torch = _torch()
+        device = _same_device(self.k_pages, k, v, q, q_out)
+        batch, m = self.batch, k.shape[2] if k.dim() == 4 else 0
+        if k.dtype != self.k_pages.dtype or v.dtype != k.dtype:
+            raise ValueError(f"k and v must be {self.k_pages.dtype}, as the pages")
+        kr, vr = _rows(k, "k", batch, m), _rows(v, "v", batch, m)
+        qr = qo = None
+        if q is not None:
+            if q_out is None:
+                q_out = (torch.empty if n_new is None else torch.zeros)(q.shape, dtype=q.dtype, device=device)
+            if q.dtype != k.dtype or q_out.dtype != k.dtype or q_out.shape != q.shape:
+                raise ValueError("q and q_out must have one shape and the pages' dtype")
+            qr, qo = _rows(q, "q", batch, m), _rows(q_out, "q_out", batch, m)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        with _on(device) as stream:
+            binding.evict_paged_append(self.struct, batch, m, _like(n_new, "n_new", (batch,), torch.int32, device),
+                                       rotary.handle if rotary is not None else None,
+                                       _pos(pos, rotary, batch, m, device), pos_base, kr, vr, qr, qo, stream)
+        return q_out
+
+    def attend(self, q, prefix=None, n_new=None, scale=None, out=None, lse=None):
+        """shared_attention of q over ``prefix`` and these pages."""
+        return shared_attention(q, prefix=prefix, pages=self, n_new=n_new, scale=scale, out=out, lse=lse)
+
+    def sync(self):
+        """Synchronise the current stream; raises EvictError(EVICT_EDEVICE) if a call's kernel has
+        reported an error (a table entry outside the pool, rows outside the table) since the last."""
+        with _on(self.device) as stream:
+            binding.evict_pages_status(self.error.data_ptr(), stream)

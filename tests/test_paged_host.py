@@ -1,0 +1,219 @@
+"""Rotary positions, pages and shared-prefix attention: what the host decides (no GPU needed).
+
+Every refusal runs before any CUDA call, so the pointers below are made-up addresses that nothing
+dereferences."""
+import ctypes
+import math
+import os
+import subprocess
+
+import pytest
+
+from kv_cache_token_bf16_gb300 import binding, paged
+from kv_cache_token_bf16_gb300.binding import (EVICT_BF16, EVICT_EINVAL, EVICT_ELIMIT, EVICT_FP32, EvictAttention,
+                                               EvictPages, EvictRows)
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+A = 0x100000                        # an aligned address
+
+
+def refused(code, match, fn, *args):
+    with pytest.raises(binding.EvictError, match=match) as e:
+        fn(*args)
+    assert e.value.code == code
+
+
+@pytest.mark.parametrize("struct", ["evict_rows", "evict_rotary_config", "evict_pages", "evict_attention"])
+def test_binding_structs_have_the_headers_layout(struct, tmp_path):
+    cls = {"evict_rows": EvictRows, "evict_rotary_config": binding.EvictRotaryConfig, "evict_pages": EvictPages,
+           "evict_attention": EvictAttention}[struct]
+    fields = [f[0] for f in cls._fields_]
+    src = tmp_path / "s.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "evict.h"\nint main(void){printf("%zu", sizeof('
+                   + struct + "));" + "".join(f'printf(" %zu", offsetof({struct}, {f}));' for f in fields)
+                   + "return 0;}")
+    exe = tmp_path / "s"
+    subprocess.run(["gcc", "-I", os.path.join(os.path.dirname(HERE), "include"), str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+    assert got == [ctypes.sizeof(cls)] + [getattr(cls, f).offset for f in fields]
+
+
+# --- rotations ------------------------------------------------------------------------------
+@pytest.mark.parametrize("kw,match", [
+    (dict(rotary_dim=0), "rotary_dim"), (dict(rotary_dim=130), "rotary_dim"),
+    (dict(rotary_dim=63, inv_freq=[1.0] * 31), "rotary_dim"),
+    (dict(n_axes=0), "n_axes"), (dict(n_axes=5), "n_axes"),
+    (dict(rotary_dim=4, axis=[0, 2], n_axes=2), "axis 2 of 2"),
+    (dict(scale=math.inf), "scale"), (dict(scale=math.nan), "scale"),
+    (dict(rotary_dim=4, inv_freq=[1.0, math.nan]), "inv_freq"), (dict(rotary_dim=4, inv_freq=[1.0, 1e6]), "inv_freq"),
+])
+def test_bad_rotations_are_refused(lib, kw, match):
+    refused(EVICT_EINVAL, match, lambda: paged.Rotary(**kw))
+
+
+@pytest.mark.parametrize("kw", [dict(pairs="other"), dict(rotary_dim=8, inv_freq=[1.0] * 3),
+                                dict(rotary_dim=8, axis=[0] * 5), dict(rotary_dim=8, axis=[0] * 4, sections=[4]),
+                                dict(rotary_dim=8, sections=[1, 2]), dict(rotary_dim=4, axis=[0, -1])])
+def test_bad_rotation_arguments_are_refused(lib, kw):
+    with pytest.raises(ValueError):
+        paged.Rotary(**kw)
+
+
+def test_sections_name_the_axes(lib):
+    r = paged.Rotary(rotary_dim=16, sections=[4, 2, 2])
+    assert r.n_axes == 3
+    assert paged.Rotary(rotary_dim=16).n_axes == 1
+
+
+def test_null_rotation_arguments(lib):
+    assert lib.evict_rotary_init(None, None) == EVICT_EINVAL
+    out = ctypes.c_void_p()
+    assert lib.evict_rotary_init(None, out) == EVICT_EINVAL and out.value is None
+    lib.evict_rotary_destroy(None)
+
+
+def rows(data=A, heads=4, stride_m=128, stride_h=1024, stride_b=4096):
+    return EvictRows(data, stride_b, stride_h, stride_m, heads)
+
+
+@pytest.fixture
+def rot(lib):
+    return paged.Rotary(rotary_dim=64)
+
+
+@pytest.mark.parametrize("kw,code,match", [
+    (dict(dtype=2), EVICT_EINVAL, "dtype"), (dict(batch=-1), EVICT_EINVAL, "batch"), (dict(m=-1), EVICT_EINVAL, "m must"),
+    (dict(pos=A + 2), EVICT_EINVAL, "pos"), (dict(transpose=2), EVICT_EINVAL, "transpose"),
+    (dict(x=rows(None)), EVICT_EINVAL, "NULL"), (dict(out=rows(None)), EVICT_EINVAL, "NULL"),
+    (dict(x=rows(A + 1)), EVICT_EINVAL, "aligned"), (dict(x=rows(heads=3)), EVICT_EINVAL, "heads"),
+    (dict(x=rows(heads=0), out=rows(heads=0)), EVICT_EINVAL, "heads"),
+    (dict(out=rows(A, stride_m=256)), EVICT_EINVAL, "in place"),
+    (dict(batch=1 << 15, m=1 << 14), EVICT_ELIMIT, "rows"),
+    (dict(n=0), EVICT_EINVAL, "tensors"), (dict(n=3), EVICT_EINVAL, "tensors"),
+])
+def test_bad_rotate_calls_are_refused(rot, kw, code, match):
+    a = dict(dtype=EVICT_BF16, batch=2, m=8, pos=None, transpose=0, x=rows(), out=rows(2 * A), n=1)
+    a.update(kw)
+    refused(code, match, binding.evict_rotate, rot.handle, a["dtype"], a["batch"], a["m"], a["pos"], 0, a["transpose"],
+            a["x"], a["out"], a["n"], None)
+
+
+def test_nothing_to_rotate_is_no_launch(rot, lib):
+    before = lib.evict_launch_count()
+    binding.evict_rotate(rot.handle, EVICT_BF16, 0, 8, None, 0, 0, rows(), rows(2 * A), 1, None)
+    binding.evict_rotate(rot.handle, EVICT_FP32, 2, 0, None, 0, 0, rows(), rows(2 * A), 1, None)
+    assert lib.evict_launch_count() == before
+    assert lib.evict_rotate(None, 0, 1, 1, None, 0, 0, rows(), rows(2 * A), 1, None) == EVICT_EINVAL
+
+
+# --- pages ----------------------------------------------------------------------------------
+def pages(**kw):
+    a = dict(k=A, v=2 * A, page_stride=0, n_pages=8, page_size=16, n_kv_heads=4, dtype=EVICT_BF16, table=3 * A,
+             table_stride=0, table_width=4, lens=4 * A, error=None)
+    a.update(kw)
+    return EvictPages(**a)
+
+
+BAD_PAGES = [
+    (dict(dtype=7), EVICT_EINVAL, "dtype"), (dict(n_pages=0), EVICT_EINVAL, "n_pages"),
+    (dict(n_kv_heads=0), EVICT_EINVAL, "n_kv_heads"), (dict(table_width=0), EVICT_EINVAL, "table_width"),
+    (dict(page_size=8), EVICT_EINVAL, "page_size"), (dict(page_size=48), EVICT_EINVAL, "page_size"),
+    (dict(page_size=512), EVICT_EINVAL, "page_size"), (dict(table_width=1 << 27), EVICT_ELIMIT, "table_width"),
+    (dict(k=None), EVICT_EINVAL, "NULL"), (dict(v=None), EVICT_EINVAL, "NULL"), (dict(table=None), EVICT_EINVAL, "NULL"),
+    (dict(lens=None), EVICT_EINVAL, "NULL"), (dict(k=A + 8), EVICT_EINVAL, "16-byte"),
+    (dict(lens=A + 2), EVICT_EINVAL, "4-byte"), (dict(error=A + 2), EVICT_EINVAL, "4-byte"),
+    (dict(page_stride=4 * 16 * 128 - 8), EVICT_EINVAL, "page_stride"),
+    (dict(page_stride=4 * 16 * 128 + 4), EVICT_EINVAL, "page_stride"), (dict(table_stride=3), EVICT_EINVAL, "table_stride"),
+]
+
+
+@pytest.mark.parametrize("kw,code,match", BAD_PAGES)
+def test_bad_pages_are_refused_by_both_calls(lib, kw, code, match):
+    refused(code, match, binding.evict_paged_append, pages(**kw), 2, 1, None, None, None, 0, rows(), rows(), None, None,
+            None)
+    refused(code, match, binding.evict_shared_attention, attention(pages=pages(**kw)))
+
+
+@pytest.mark.parametrize("kw,code,match", [
+    (dict(k=rows(heads=3)), EVICT_EINVAL, "heads"), (dict(v=rows(heads=8)), EVICT_EINVAL, "heads"),
+    (dict(k=rows(None)), EVICT_EINVAL, "NULL"), (dict(v=None), EVICT_EINVAL, "NULL"),
+    (dict(q=rows(5 * A)), EVICT_EINVAL, "together"), (dict(q_out=rows(5 * A)), EVICT_EINVAL, "together"),
+    (dict(q=rows(5 * A), q_out=rows(6 * A, heads=2)), EVICT_EINVAL, "heads"),
+    (dict(q=rows(5 * A), q_out=rows(5 * A, stride_b=8192)), EVICT_EINVAL, "in place"),
+    (dict(n_new=A + 1), EVICT_EINVAL, "n_new"), (dict(pos=A + 1), EVICT_EINVAL, "pos"), (dict(m=-2), EVICT_EINVAL, "m must"),
+    (dict(batch=1 << 15, m=1 << 14), EVICT_ELIMIT, "rows"),
+])
+def test_bad_appends_are_refused(rot, kw, code, match):
+    a = dict(batch=2, m=1, n_new=None, pos=None, k=rows(5 * A), v=rows(6 * A), q=None, q_out=None)
+    a.update(kw)
+    refused(code, match, binding.evict_paged_append, pages(), a["batch"], a["m"], a["n_new"], rot.handle, a["pos"], 0,
+            a["k"], a["v"], a["q"], a["q_out"], None)
+
+
+def test_appending_nothing_is_no_launch(lib):
+    before = lib.evict_launch_count()
+    binding.evict_paged_append(pages(), 0, 1, None, None, None, 0, rows(), rows(), None, None, None)
+    binding.evict_paged_append(pages(), 2, 0, None, None, None, 0, rows(), rows(), None, None, None)
+    assert lib.evict_launch_count() == before
+
+
+def test_status_needs_a_word(lib):
+    assert lib.evict_pages_status(None, None) == EVICT_EINVAL
+    assert lib.evict_pages_status(A + 1, None) == EVICT_EINVAL
+
+
+# --- attention ------------------------------------------------------------------------------
+def attention(**kw):
+    a = EvictAttention(batch=4, m=2, n_q_heads=8, n_kv_heads=4, q=rows(A, heads=8), out=rows(2 * A, heads=8),
+                       prefix_k=3 * A, prefix_v=4 * A, prefix_stride_b=4 * 64 * 128, prefix_stride_h=64 * 128, n_prefix=64,
+                       prefix_batch=2, workspace=5 * A, workspace_bytes=1 << 40)
+    g = kw.pop("pages", None)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    if g is not None:
+        a.pages = ctypes.pointer(g)
+    return a
+
+
+@pytest.mark.parametrize("kw,code,match", [
+    (dict(batch=-1), EVICT_EINVAL, "batch"), (dict(m=-1), EVICT_EINVAL, "m must"),
+    (dict(n_q_heads=6), EVICT_EINVAL, "multiple|heads"), (dict(n_kv_heads=0), EVICT_EINVAL, "multiple"),
+    (dict(prefix_batch=3), EVICT_EINVAL, "divide"), (dict(prefix_batch=0), EVICT_EINVAL, "divide"),
+    (dict(n_prefix=-1), EVICT_EINVAL, "n_prefix"), (dict(prefix_k=None), EVICT_EINVAL, "NULL"),
+    (dict(prefix_v=A + 4), EVICT_EINVAL, "16-byte"), (dict(prefix_stride_h=100), EVICT_EINVAL, "multiples"),
+    (dict(prefix_stride_b=-8), EVICT_EINVAL, "multiples"),
+    (dict(q=rows(None, heads=8)), EVICT_EINVAL, "NULL"), (dict(q=rows(A, heads=4)), EVICT_EINVAL, "heads"),
+    (dict(q=rows(A + 8, heads=8)), EVICT_EINVAL, "16 bytes"), (dict(out=rows(A, heads=8, stride_m=132)), EVICT_EINVAL, "16 bytes"),
+    (dict(scale=math.nan), EVICT_EINVAL, "scale"), (dict(lse=A + 2), EVICT_EINVAL, "4-byte"),
+    (dict(batch=5000, prefix_batch=1), EVICT_ELIMIT, "4096"),
+    (dict(batch=4096, m=1 << 16), EVICT_ELIMIT, "2\\^31"),
+    (dict(pages=pages(dtype=EVICT_FP32)), EVICT_EINVAL, "bf16"), (dict(pages=pages(n_kv_heads=2)), EVICT_EINVAL, "KV heads"),
+])
+def test_bad_attention_calls_are_refused(lib, kw, code, match):
+    refused(code, match, binding.evict_shared_attention, attention(**kw))
+
+
+def test_attention_of_nothing_is_no_launch(lib):
+    before = lib.evict_launch_count()
+    binding.evict_shared_attention(attention(batch=0))
+    binding.evict_shared_attention(attention(m=0))
+    assert lib.evict_launch_count() == before
+    assert lib.evict_shared_attention(None) == EVICT_EINVAL
+    assert lib.evict_shared_attention_workspace(None, None) == EVICT_EINVAL
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(n_pages=4), dict(n_pages=4, page_size=16, n_kv_heads=2, batch=0, max_rows=9),
+                                dict(n_pages=4, page_size=20, n_kv_heads=2, batch=1, max_rows=9),
+                                dict(k_pages=object())])
+def test_bad_caches_are_refused(kw):
+    with pytest.raises(ValueError):
+        paged.PagedCache(**kw)
+
+
+def test_host_tensors_are_refused(lib):
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(1, 2, 3, 128)
+    with pytest.raises(ValueError, match="CUDA"):
+        paged.rotate(paged.Rotary(), x)
+    with pytest.raises(ValueError, match="CUDA"):
+        paged.shared_attention(x.bfloat16(), prefix=(x, x))
