@@ -28,6 +28,7 @@
 
 #include "api_internal.h"
 #include "attend.h"
+#include "attend.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "pipeline.cuh"
@@ -67,106 +68,25 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-__device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int x, int y, int z, int w, int v,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
-      "%6}], [%7];" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(tc::smem_u32(bar))
-      : "memory");
-}
-// Bit 0: the lower bf16 of the pair is an infinity or NaN; bit 1: the upper.
-__device__ __forceinline__ uint32_t nonfinite2(uint32_t x) {
-  return ((x & 0x7f80u) == 0x7f80u ? 1u : 0u) | ((x & 0x7f800000u) == 0x7f800000u ? 2u : 0u);
-}
-
-// Where a weight meets no finite maximum (no row seen yet, or every logit -inf or NaN) the
-// exponent is taken against 0, so that masked rows stay 0 and NaN stays NaN.
-__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
-__device__ __forceinline__ float weight_of(float m, float to) { return m == to ? 1.f : ex2(m - base_of(to)); }
-
-// New rows and visible rows of a sequence.
-struct Seq {
-  int n, len;                        // new tokens; rows, the new ones included
-};
-__device__ __forceinline__ Seq sequence(const AttendParams& p, int b, bool report) {
-  int n = p.n_new ? p.n_new[b] : p.m;
-  bool odd = n < 0 || n > p.m;
-  n = n < 0 ? 0 : n > p.m ? p.m : n;
-  int len = p.own ? p.lens[b] : 0;
-  const int room = p.own ? p.table_width << p.page_shift : 0;
-  odd = odd || len < 0 || len > room;
-  len = len < 0 ? 0 : len > room ? room : len;
-  if (odd && report) raise_device_error(p.err, kDevBadIndex);
-  return {n, len};
-}
-
-// Stream s: row tiles of a unit and steps of a row tile.
-template <int kRows>
-struct Stream {
-  int tiles, steps, n, len;
-  __device__ void load(const AttendParams& p, int s, bool report = false) {
-    if (s < p.prefixes) {
-      n = p.m;
-      len = p.n_prefix;
-      tiles = p.prefix_tiles;
-    } else {
-      const Seq q = sequence(p, s - p.prefixes, report);
-      n = q.n;
-      len = q.len;
-      tiles = (n * p.group + kRows - 1) / kRows;
-    }
-    steps = (len + kStepTokens - 1) / kStepTokens;
-    if (tiles == 0 || steps == 0) tiles = steps = 0;
-  }
-  __device__ long long work(const AttendParams& p) const { return (long long)tiles * steps * p.hkv; }
-};
-
-// Position in the line of steps.
-template <int kRows>
-struct Cursor {
-  int s, h, tile, step;
-  Stream<kRows> st;
-  __device__ void next(const AttendParams& p, int streams) {
-    if (++step < st.steps) return;
-    step = 0;
-    if (++tile < st.tiles) return;
-    tile = 0;
-    if (++h < p.hkv) return;
-    h = 0;
-    do {
-      if (++s >= streams) return;
-      st.load(p, s);
-    } while (st.steps == 0);
-  }
-};
-
-// Rows of this tile see own rows up to `last`: row r of the unit is token r / group.
-template <int kRows>
-__device__ __forceinline__ int last_row(const AttendParams& p, const Cursor<kRows>& c, int r) {
-  if (c.s < p.prefixes) return p.n_prefix - 1;
-  const int t = r / p.group;
-  return t < c.st.n ? c.st.len - c.st.n + t : -1;
-}
-
 struct FewShared {
   uint64_t full[kWarps][kStages];
-  long long begin, total;
-  int s;
-  long long rest, unit;
-  long long sums[kWarps], usums[kWarps];
+  ScanShared scan;
   int fail;
 };
+
+// Last row that row r of the tile sees (-1: none; rows behind the unit's last see none).
+template <int kRows>
+__device__ __forceinline__ int last_row(const AttendParams& p, const StreamSet& set, const Cursor<kRows>& c, int r) {
+  const int t = (c.tile * kRows + r) / p.group;
+  if (c.s < set.prefixes) return c.st.pre - 1;
+  return t < c.st.n ? c.st.len - c.st.n + t : -1;
+}
 
 template <int kTiles>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ AttendParams p) {
   constexpr int kRows = 16 * kTiles;
   constexpr int kCols = merge_cols(kTiles);
-  pdl_wait();
+  if (!p.late_wait) pdl_wait();
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ FewShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -174,90 +94,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   unsigned char* qs = ring + kRingBytes;
   float* red = reinterpret_cast<float*>(qs + kRows * kQPitch);          // [warp][row][kCols + 4]
   float2* red_ml = reinterpret_cast<float2*>(red + kWarps * kRows * (kCols + 4));
-  const int streams = p.prefixes + (p.own ? p.batch : 0);
+  const StreamSet& set = p.set;
 
   if (tid < kWarps * kStages) tc::mbar_init(&sh.full[tid / kStages][tid % kStages], 1);
   if (tid == 0) sh.fail = 0;
-
-  // --- this CTA's share: a block scan over the streams' steps and units ---
-  {
-    const int per = (streams + kThreads - 1) / kThreads;
-    const int s0 = min(tid * per, streams), s1 = min(s0 + per, streams);
-    long long steps = 0, units = 0;
-    Stream<kRows> st;
-    for (int s = s0; s < s1; ++s) {
-      st.load(p, s, blockIdx.x == 0);
-      steps += st.work(p);
-      units += (long long)st.tiles * p.hkv;
-    }
-    long long a = steps, u = units;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, a, d), y = __shfl_up_sync(0xffffffffu, u, d);
-      if (lane >= d) a += x, u += y;
-    }
-    if (lane == 31) sh.sums[warp] = a, sh.usums[warp] = u;
-    __syncthreads();
-    long long total = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) a += sh.sums[w], u += sh.usums[w];
-      total += sh.sums[w];
-    }
-    a -= steps;
-    u -= units;
-    const long long ctas = total < p.ctas ? total : p.ctas;
-    const long long mine = ctas ? total * blockIdx.x / ctas : 0;
-    if (blockIdx.x == 0) {                        // where the join finds every stream
-      long long x = a, y = u;
-      for (int s = s0; s < s1; ++s) {
-        st.load(p, s);
-        p.step_base[s] = x;
-        p.unit_base[s] = y;
-        x += st.work(p);
-        y += (long long)st.tiles * p.hkv;
-      }
-      if (tid == kThreads - 1) p.step_base[streams] = total;
-    }
-    if (tid == 0) sh.total = total;
-    if (blockIdx.x < ctas && mine >= a && mine < a + steps) {
-      int s = s0;
-      for (; s < s1; ++s) {
-        st.load(p, s);
-        if (mine < a + st.work(p)) break;
-        a += st.work(p);
-        u += (long long)st.tiles * p.hkv;
-      }
-      sh.s = s;
-      sh.rest = mine - a;
-      sh.unit = u;
-      sh.begin = mine;
-    }
-    __syncthreads();
-    if (blockIdx.x >= ctas) return;
-  }
-  const long long ctas = sh.total < p.ctas ? sh.total : p.ctas;
-  const int count = (int)(sh.total * (blockIdx.x + 1) / ctas - sh.begin);    // steps of this CTA
-
   Cursor<kRows> cur;
-  cur.s = sh.s;
-  cur.st.load(p, cur.s);
-  {
-    const long long per_head = (long long)cur.st.tiles * cur.st.steps;
-    cur.h = (int)(sh.rest / per_head);
-    const int r = (int)(sh.rest - cur.h * per_head);
-    cur.tile = r / cur.st.steps;
-    cur.step = r - cur.tile * cur.st.steps;
-  }
-  long long unit = sh.unit + (long long)cur.h * cur.st.tiles + cur.tile;
+  const int count = find_share<kRows, kThreads>(p, set, sh.scan, cur);
 
-  // Does this warp have rows to read at this step? (its box begins inside the stream, and the
-  // tile's last token sees its first row)
+  // Does this warp have rows to read at this step? (its box begins inside what the tile sees)
   auto active = [&](const Cursor<kRows>& c) {
     const int row0 = c.step * kStepTokens + kBoxTokens * warp;
-    if (row0 >= c.st.len) return false;
-    if (c.s < p.prefixes) return true;
-    const int t = min((kRows * (c.tile + 1) - 1) / p.group, c.st.n - 1);
-    return row0 <= c.st.len - c.st.n + t;
+    return c.s < set.prefixes ? row0 < c.st.pre : row0 <= c.st.reach(p, c.tile);
   };
 
   // --- the ring: boxes are requested in the order in which they are used ---
@@ -267,11 +114,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   // advance `ahead` to the next box of this warp and look its page up
   auto seek = [&] {
     while (ahead_left > 0 && !active(ahead)) {
-      ahead.next(p, streams);
+      ahead.next(p, set);
       --ahead_left;
     }
-    if (ahead_left > 0 && ahead.s >= p.prefixes && lane == 0)
-      page = p.table[(long long)(ahead.s - p.prefixes) * p.table_stride +
+    if (ahead_left > 0 && ahead.s >= set.prefixes && lane == 0)
+      page = p.table[(long long)(ahead.s - set.prefixes) * p.table_stride +
                      ((ahead.step * kStepTokens + kBoxTokens * warp) >> p.page_shift)];
   };
   auto request = [&](int stage) {
@@ -281,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       const uint32_t dst = my_ring + stage * 2 * kBoxBytes;
       const int row = ahead.step * kStepTokens + kBoxTokens * warp;
       tc::mbar_arrive_expect_tx(bar, 2 * kBoxBytes);
-      if (ahead.s < p.prefixes) {
+      if (ahead.s < set.prefixes) {
         tma_load_5d(dst, &p.tm_pk, 0, row, 0, ahead.h, ahead.s, bar);
         tma_load_5d(dst + kBoxBytes, &p.tm_pv, 0, row, 0, ahead.h, ahead.s, bar);
       } else {
@@ -293,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         tma_load_5d(dst + kBoxBytes, &p.tm_v, 0, y, 0, ahead.h, at, bar);
       }
     }
-    ahead.next(p, streams);
+    ahead.next(p, set);
     --ahead_left;
     seek();
   };
@@ -312,21 +159,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     if (fresh) {                                  // a new unit: its queries
       fresh = false;
       for (int e = tid; e < kRows * 16; e += kThreads) {
-        const int r = e >> 4, c = e & 15, ur = cur.tile * kRows + r;
-        const bool pre = cur.s < p.prefixes;
-        const int per_seq = p.m * p.group;
-        const int b = pre ? cur.s * p.fan + ur / per_seq : cur.s - p.prefixes;
-        const int rr = pre ? ur % per_seq : ur;
-        const int t = rr / p.group, hq = cur.h * p.group + rr % p.group;
-        const bool real = pre ? ur < p.fan * per_seq : t < cur.st.n;
+        const int r = e >> 4, c = e & 15;
+        const QueryRow qr = query_row(p, set, cur, r);
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (real)
-          x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)b * p.qb +
-                                              (long long)hq * p.qh + (long long)t * p.qm + c * 8);
+        if (qr.real)
+          x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)qr.b * p.qb +
+                                              (long long)qr.hq * p.qh + (long long)qr.t * p.qm + c * 8);
         *reinterpret_cast<uint4*>(qs + r * kQPitch + c * 16) = x;
       }
       __syncthreads();
-      low = cur.s < p.prefixes ? p.n_prefix - 1 : last_row(p, cur, cur.tile * kRows);
+      low = last_row(p, set, cur, 0);
 #pragma unroll
       for (int x = 0; x < kTiles; ++x) {
 #pragma unroll
@@ -340,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         for (int k = 0; k < 2; ++k) {
           mx[x][k] = -INFINITY;
           sum[x][k] = 0.f;
-          last[x][k] = last_row(p, cur, cur.tile * kRows + 16 * x + (lane >> 2) + 8 * k);
+          last[x][k] = last_row(p, set, cur, 16 * x + (lane >> 2) + 8 * k);
         }
       }
     }
@@ -438,14 +280,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         // V of rows behind the stream's end may hold anything: zeros in its place
         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
         if (!full) {
-          const int r0 = row0 + 2 * (lane & 3);
-          auto mask = [&](int r) { return (r < cur.st.len ? 0xffffu : 0u) | (r + 1 < cur.st.len ? 0xffff0000u : 0u); };
+          const int r0 = row0 + 2 * (lane & 3), end = cur.s < set.prefixes ? cur.st.pre : cur.st.len;
+          auto mask = [&](int r) { return (r < end ? 0xffffu : 0u) | (r + 1 < end ? 0xffff0000u : 0u); };
           keep0 = mask(r0);
           keep1 = mask(r0 + 8);
         }
         const int vrow = lane & 15, vchunk = lane >> 4;
         uint32_t bad = 0;                         // tokens of the box whose V holds an infinity or NaN
-        if (!full && p.m > 1 && cur.s >= p.prefixes) {
+        if (!full && p.m > 1 && cur.s >= set.prefixes) {
           // A query that does not see such a row gives it weight 0, but 0 * infinity is not 0: the
           // products leave these rows out, and the queries that see them take them afterwards.
 #pragma unroll
@@ -502,8 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     }
 
     // --- the CTA leaves the unit: the warps' results meet ---
-    if (cur.step == cur.st.steps - 1 || i == count - 1) {
-      const long long slot = unit + blockIdx.x;
+    if (cur.step == cur.steps - 1 || i == count - 1) {
+      const long long slot = cur.unit + blockIdx.x;
 #pragma unroll
       for (int x = 0; x < kTiles; ++x)
 #pragma unroll
@@ -527,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         float top = -INFINITY, t = 0.f;
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red_ml[w * kRows + tid].x);
         for (int w = 0; w < kWarps; ++w) t += red_ml[w * kRows + tid].y * weight_of(red_ml[w * kRows + tid].x, top);
-        p.part_ml[slot * kRows + tid] = make_float2(top, t);
+        set.part_ml[slot * kRows + tid] = make_float2(top, t);
       }
 #pragma unroll
       for (int c = 0; c < kHeadDim / kCols; ++c) {
@@ -551,73 +393,69 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             a.x += y.x;
             a.y += y.y;
           }
-          *reinterpret_cast<float2*>(p.part_o + (slot * kRows + r) * kHeadDim + c * kCols + cc) = a;
+          *reinterpret_cast<float2*>(set.part_o + (slot * kRows + r) * kHeadDim + c * kCols + cc) = a;
         }
         __syncthreads();
       }
       fresh = true;
-      ++unit;
     }
-    cur.next(p, streams);
+    cur.next(p, set);
   }
+  if (p.late_wait) pdl_wait();
 }
 
-// Partial results of one output row: `count` slots from `first`, row `row` of each.
+// Partial results of one output row in one unit: `count` slots from `slot` on, row `row` of each;
+// `twice`: rows row and row + 128 (the wide kernel's two groups took turns).
 struct Parts {
-  long long first;
-  int count, row;
+  const float2* ml;
+  const float* o;
+  long long slot;
+  int count, rows, row, twice;
+  __device__ long long at(int k) const {
+    return twice ? (slot + (k >> 1)) * rows + row + (k & 1) * 128 : (slot + k) * rows + row;
+  }
+  __device__ int parts() const { return count << twice; }
 };
 
+// Row r of stream s and head h.
 template <int kRows>
-__device__ __forceinline__ Parts find_parts(const AttendParams& p, long long total, long long ctas, int s, int h,
-                                            int tiles, int steps, int r) {
-  const int tile = r / kRows;
-  const long long g = p.step_base[s] + ((long long)h * tiles + tile) * steps;
+__device__ __forceinline__ Parts find_parts(const AttendParams& p, const StreamSet& set, int s, int h, long long r) {
+  Stream<kRows> st;
+  st.load(p, set, s);
+  const int tile = (int)(r / kRows);
+  const int steps = st.steps(p, set, tile);
+  if (steps == 0) return Parts{nullptr, nullptr, 0, 0, kRows, 0, 0};
+  const long long total = set.step_base[set.prefixes + set.own];
+  const long long ctas = total < set.ctas ? total : set.ctas;
+  long long g = set.step_base[s] + (long long)h * st.head_work(p, set);
+  if (st.len == 0) g += (long long)tile * steps;
+  else
+    for (int i = 0; i < tile; ++i) g += st.steps(p, set, i);
   const int c0 = (int)(((g + 1) * ctas - 1) / total), c1 = (int)(((g + steps) * ctas - 1) / total);
-  return {p.unit_base[s] + (long long)h * tiles + tile + c0, c1 - c0 + 1, r % kRows};
+  const bool twice = kRows == kWideRows && (long long)st.n * p.group - (long long)tile * kRows <= 128;
+  return Parts{set.part_ml, set.part_o, set.unit_base[s] + (long long)h * st.tiles + tile + c0, c1 - c0 + 1, kRows,
+               (int)(r % kRows), twice};
 }
 
 constexpr int kJoinWarps = 8;
 
-template <int kRows>
-__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const __grid_constant__ AttendParams p) {
-  pdl_wait();
+// A warp merges the parts of one output row, in their order, and writes it.
+__device__ __forceinline__ void join_row(const AttendParams& p, const Parts* parts, int np, int b, int t, int hq, bool sees) {
   const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= (long long)p.batch * p.hq * p.m) return;
-  const int t = (int)(row % p.m), hq = (int)(row / p.m % p.hq), b = (int)(row / p.m / p.hq);
-  const Seq q = sequence(p, b, !p.own && t == 0 && hq == 0 && lane == 0);
-  if (t >= q.n) return;
-  const int h = hq / p.group, g = hq - h * p.group;
-  const int streams = p.prefixes + (p.own ? p.batch : 0);
-  const long long total = p.step_base[streams];
-  const long long ctas = total < p.ctas ? total : p.ctas;
-  Parts parts[2];
-  int np = 0;
-  if (p.prefixes) {
-    const int s = b / p.fan, steps = (p.n_prefix + kStepTokens - 1) / kStepTokens;
-    parts[np++] = find_parts<kRows>(p, total, ctas, s, h, p.prefix_tiles, steps,
-                                    ((b - s * p.fan) * p.m + t) * p.group + g);
-  }
-  const bool sees_own = q.len - q.n + t >= 0 && q.len > 0;
-  if (sees_own) {
-    const int tiles = (q.n * p.group + kRows - 1) / kRows, steps = (q.len + kStepTokens - 1) / kStepTokens;
-    parts[np++] = find_parts<kRows>(p, total, ctas, p.prefixes + b, h, tiles, steps, t * p.group + g);
-  }
   float top = -INFINITY;
   for (int x = 0; x < np; ++x)
-    for (int k = lane; k < parts[x].count; k += 32)
-      top = fmaxf(top, p.part_ml[(parts[x].first + k) * kRows + parts[x].row].x);
+    for (int k = lane; k < parts[x].parts(); k += 32) top = fmaxf(top, parts[x].ml[parts[x].at(k)].x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
   for (int x = 0; x < np; ++x) {
+    const int n = parts[x].parts();
 #pragma unroll 4
-    for (int k = 0; k < parts[x].count; ++k) {
-      const long long at = (parts[x].first + k) * kRows + parts[x].row;
-      const float2 ml = p.part_ml[at];
-      const float4 v = reinterpret_cast<const float4*>(p.part_o + at * kHeadDim)[lane];
+    for (int k = 0; k < n; ++k) {
+      const long long at = parts[x].at(k);
+      const float2 ml = parts[x].ml[at];
+      const float4 v = reinterpret_cast<const float4*>(parts[x].o + at * kHeadDim)[lane];
       const float w = weight_of(ml.x, top);
       sum += ml.y * w;
       acc.x += v.x * w;
@@ -626,19 +464,90 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const __gr
       acc.w += v.w * w;
     }
   }
-  const float inv = np ? 1.f / sum : 0.f;         // a query that sees no row: zeros
+  const float inv = sees ? 1.f / sum : 0.f;       // a query that sees no row: zeros
   uint2 y = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + (long long)b * p.ob + (long long)hq * p.oh +
                             (long long)t * p.om + 4 * lane) = y;
-  if (p.lse && lane == 0) p.lse[row] = np ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  if (p.lse && lane == 0)
+    p.lse[((long long)b * p.hq + hq) * p.m + t] = sees ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
 }
 
-// Boxes of 16 rows: two halves of 64 elements, each row 128 bytes, 128-byte swizzle.
+// Every output row: the parts of its prefix unit and of its own.
+template <int kRows>
+__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const __grid_constant__ AttendParams p) {
+  pdl_wait();
+  const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (row >= (long long)p.batch * p.hq * p.m) return;
+  const int t = (int)(row % p.m), hq = (int)(row / p.m % p.hq), b = (int)(row / p.m / p.hq);
+  const Seq q = sequence(p, b, !p.pages && t == 0 && hq == 0 && (threadIdx.x & 31) == 0);
+  if (t >= q.n) return;
+  const int h = hq / p.group, g = hq - h * p.group;
+  Parts parts[2];
+  int np = 0;
+  if (p.fan) {
+    const int s = b / p.fan;
+    const long long r = (long long)(tokens_before(p, b) - tokens_before(p, s * p.fan) + t) * p.group + g;
+    if (p.wide.prefixes) parts[np++] = find_parts<kWideRows>(p, p.wide, s, h, r);
+    else parts[np++] = find_parts<kRows>(p, p.set, s, h, r);
+  }
+  if (q.len - q.n + t >= 0 && q.len > 0) {
+    const long long r = (long long)t * p.group + g;
+    if (p.wide.own) parts[np++] = find_parts<kWideRows>(p, p.wide, p.wide.prefixes + b, h, r);
+    else parts[np++] = find_parts<kRows>(p, p.set, p.set.prefixes + b, h, r);
+  }
+  join_row(p, parts, np, b, t, hq, np > 0);
+}
+
+// Joint units: only those that two or more CTAs share have parts to merge. Block (c, y) takes 32 rows of
+// the unit that CTA c + 1 begins inside, where that is the first CTA to begin inside it.
+__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_split_kernel(const __grid_constant__ AttendParams p) {
+  pdl_wait();
+  const StreamSet& set = p.wide;
+  const int streams = set.prefixes + set.own;
+  const long long total = set.step_base[streams];
+  const long long ctas = total < set.ctas ? total : set.ctas;
+  const int c = blockIdx.x + 1;
+  if (c >= ctas) return;
+  const long long begin = total * c / ctas;
+  int lo = 0, hi = streams;                       // the last stream that begins at or before this step
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (set.step_base[mid] <= begin) lo = mid;
+    else hi = mid;
+  }
+  Cursor<kWideRows> cur;
+  cur.s = lo;
+  cur.st.load(p, set, lo);
+  const long long per_head = cur.st.head_work(p, set);
+  long long r = begin - set.step_base[lo];
+  cur.h = (int)(r / per_head);
+  r -= cur.h * per_head;
+  for (cur.tile = 0;; ++cur.tile) {
+    cur.steps = cur.st.steps(p, set, cur.tile);
+    if (r < cur.steps) break;
+    r -= cur.steps;
+  }
+  if (r == 0) return;                             // CTA c begins with the unit
+  const long long first = begin - r;              // the unit's first step
+  if (c > 1 && total * (c - 1) / ctas > first) return;
+  const int c1 = (int)(((first + cur.steps) * ctas - 1) / total);
+  const Parts part = {set.part_ml, set.part_o, set.unit_base[lo] + (long long)cur.h * cur.st.tiles + cur.tile + c - 1,
+                      c1 - (c - 1) + 1, kWideRows, 0, 0};
+  for (int i = threadIdx.x >> 5; i < 32; i += kJoinWarps) {
+    Parts one = part;
+    one.row = blockIdx.y * 32 + i;
+    const QueryRow q = query_row(p, set, cur, one.row);
+    if (!q.real) continue;
+    join_row(p, &one, 1, q.b, q.t, q.hq, cur.st.pre > 0 || cur.st.len - cur.st.n + q.t >= 0);
+  }
+}
+
+// Boxes of `rows_box` rows of `halves` halves of 64 elements, each row 128 bytes, 128-byte swizzle.
 bool encode_boxes(CUtensorMap* tm, const void* base, int rows, int heads, long long head_stride, int planes,
-                  long long plane_stride) {
+                  long long plane_stride, int rows_box, int halves) {
   const cuuint64_t dims[5] = {64, (cuuint64_t)rows, 2, (cuuint64_t)heads, (cuuint64_t)planes};
   const cuuint64_t strides[4] = {(cuuint64_t)kHeadDim * 2, 128, (cuuint64_t)head_stride * 2, (cuuint64_t)plane_stride * 2};
-  const cuuint32_t box[5] = {64, (cuuint32_t)kBoxTokens, 2, 1, 1};
+  const cuuint32_t box[5] = {64, (cuuint32_t)rows_box, (cuuint32_t)halves, 1, 1};
   const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   return encode_tiled()(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -647,14 +556,42 @@ bool encode_boxes(CUtensorMap* tm, const void* base, int rows, int heads, long l
 
 bool multiple(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Query rows from which the wide kernel takes a unit, and above which a sequence fills one.
+constexpr int kWideFrom = 33, kJointFrom = 128;
+
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Plan {
-  int tiles;                // query tiles of 16 rows a unit
-  int prefixes, prefix_tiles, streams, ctas;
-  long long slots;
-  size_t off_unit, off_ml, off_o, bytes;
+  int few_tiles;            // query tiles of 16 rows of a unit of the few-row kernel
+  StreamSet few, wide;      // counts, and offsets into the workspace in place of pointers
+  size_t bytes;
+  bool runs(const StreamSet& s) const { return s.prefixes + s.own > 0; }
 };
+
+// Room for a kernel's streams and partial results; sets the set's pointers (from a null base).
+void lay_out(StreamSet& s, long long units, int rows, size_t& off) {
+  const long long streams = s.prefixes + s.own, slots = units + s.ctas;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += round256(bytes);
+    return at;
+  };
+  if (!streams) return;
+  s.step_base = reinterpret_cast<long long*>(take((size_t)(streams + 1) * 8));
+  s.unit_base = reinterpret_cast<long long*>(take((size_t)streams * 8));
+  s.part_ml = reinterpret_cast<float2*>(take((size_t)slots * rows * sizeof(float2)));
+  s.part_o = reinterpret_cast<float*>(take((size_t)slots * rows * kHeadDim * sizeof(float)));
+}
+template <typename T>
+void rebase(T*& x, char* base) { x = reinterpret_cast<T*>(base + reinterpret_cast<size_t>(x)); }
+void rebase(StreamSet& s, char* base) {
+  rebase(s.step_base, base);
+  rebase(s.unit_base, base);
+  rebase(s.part_ml, base);
+  rebase(s.part_o, base);
+}
+
+constexpr size_t kWorkHead = 256;                 // an error word, for callers without one
 
 // Sizes alone decide: lens and n_new are the device's.
 int make_plan(const evict_attention* a, Plan* out) {
@@ -669,30 +606,39 @@ int make_plan(const evict_attention* a, Plan* out) {
   if (a->n_prefix < 0 || a->n_prefix > (1 << 30)) return fail(EVICT_EINVAL, "n_prefix must be in [0, 2^30]");
   if (a->n_prefix > 0 && (a->prefix_batch < 1 || a->batch % a->prefix_batch))
     return fail(EVICT_EINVAL, "prefix_batch (%d) must divide batch (%d)", a->prefix_batch, a->batch);
+  Plan& P = *out;
+  P = Plan();
+  if (a->batch == 0 || a->m == 0) return EVICT_OK;
   const int group = a->n_q_heads / a->n_kv_heads;
   const bool pre = a->n_prefix > 0;
-  Plan& P = *out;
-  P.bytes = 0;
-  if (a->batch == 0 || a->m == 0) return EVICT_OK;
-  P.prefixes = pre ? a->prefix_batch : 0;
-  const long long fan = pre ? a->batch / a->prefix_batch : 0;
-  const long long most = std::max(pre ? fan * a->m * group : 0, a->pages ? (long long)a->m * group : 0);
+  int dev = 0, ctas = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&ctas, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "looking up the device");
+  P.few.ctas = P.wide.ctas = ctas;
+
+  // Which kernel takes a unit goes by its query rows, the wide one from kWideFrom on. Sequences of
+  // more than kJointFrom rows fill a wide unit by themselves: their units take the prefix along
+  // (no partial results to merge); below that, rows of several sequences share the prefix's units.
+  const long long own_rows = (long long)a->m * group, pre_rows = pre ? own_rows * (a->batch / a->prefix_batch) : 0;
+  if (own_rows > kJointFrom && (pre || a->pages)) {
+    P.wide.joint = 1;
+    P.wide.own = a->batch;
+  } else {
+    if (pre) (pre_rows >= kWideFrom ? P.wide : P.few).prefixes = a->prefix_batch;
+    if (a->pages) (own_rows >= kWideFrom ? P.wide : P.few).own = a->batch;
+  }
+  const long long few_rows = std::max(P.few.prefixes ? pre_rows : 0, P.few.own ? own_rows : 0);
   // One tile of 16 query rows where that holds every row; two (each box of K and V then serves
   // twice the rows) otherwise.
-  P.tiles = most <= 16 ? 1 : 2;
-  const int rows = 16 * P.tiles;
-  P.prefix_tiles = pre ? (int)((fan * a->m * group + rows - 1) / rows) : 0;
-  P.streams = P.prefixes + (a->pages ? a->batch : 0);
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P.ctas, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_fail(e, "looking up the device");
-  const long long own_tiles = a->pages ? ((long long)a->m * group + rows - 1) / rows : 0;
-  P.slots = ((long long)P.prefixes * P.prefix_tiles + (a->pages ? a->batch : 0) * own_tiles) * a->n_kv_heads + P.ctas;
-  P.off_unit = 256 + round256((size_t)(P.streams + 1) * 8);
-  P.off_ml = P.off_unit + round256((size_t)P.streams * 8 + 8);
-  P.off_o = P.off_ml + round256((size_t)P.slots * rows * sizeof(float2));
-  P.bytes = P.off_o + (size_t)P.slots * rows * kHeadDim * sizeof(float);
+  P.few_tiles = few_rows <= 16 ? 1 : 2;
+  auto units = [&](const StreamSet& s, int rows) {
+    return (s.prefixes * ((pre_rows + rows - 1) / rows) + s.own * ((own_rows + rows - 1) / rows)) * a->n_kv_heads;
+  };
+  size_t off = kWorkHead + round256((size_t)(a->batch + 1) * sizeof(int));
+  lay_out(P.few, units(P.few, 16 * P.few_tiles), 16 * P.few_tiles, off);
+  lay_out(P.wide, units(P.wide, kWideRows), kWideRows, off);
+  P.bytes = off;
   return EVICT_OK;
 }
 
@@ -702,11 +648,6 @@ int check_rows(const evict_rows& x, int heads, const char* name) {
   if (!multiple(x.data, 16) || x.stride_b % 8 || x.stride_h % 8 || x.stride_m % 8)
     return fail(EVICT_EINVAL, "%s: addresses and strides must be multiples of 16 bytes", name);
   return EVICT_OK;
-}
-
-template <typename Kernel>
-cudaError_t allow_smem(Kernel kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 }  // namespace
@@ -755,10 +696,9 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
   memset(&P, 0, sizeof(P));
   char* ws = static_cast<char*>(a->workspace);
   P.err = a->error ? a->error : reinterpret_cast<int*>(ws);
-  P.step_base = reinterpret_cast<long long*>(ws + 256);
-  P.unit_base = reinterpret_cast<long long*>(ws + plan.off_unit);
-  P.part_ml = reinterpret_cast<float2*>(ws + plan.off_ml);
-  P.part_o = reinterpret_cast<float*>(ws + plan.off_o);
+  P.tok_base = reinterpret_cast<int*>(ws + kWorkHead);
+  rebase(plan.few, ws);
+  rebase(plan.wide, ws);
   P.q = a->q.data;
   P.qb = a->q.stride_b, P.qh = a->q.stride_h, P.qm = a->q.stride_m;
   P.out = a->out.data;
@@ -766,49 +706,78 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
   P.lse = a->lse;
   P.batch = a->batch, P.m = a->m, P.hq = a->n_q_heads, P.hkv = a->n_kv_heads;
   P.group = a->n_q_heads / a->n_kv_heads;
-  P.prefixes = plan.prefixes;
-  P.fan = plan.prefixes ? a->batch / plan.prefixes : 1;
-  P.n_prefix = plan.prefixes ? a->n_prefix : 0;
-  P.prefix_tiles = plan.prefix_tiles;
+  if (a->n_prefix > 0) {
+    P.prefix_batch = a->prefix_batch;
+    P.fan = a->batch / a->prefix_batch;
+    P.n_prefix = a->n_prefix;
+  }
   P.scale2 = (a->scale == 0.f ? 0.08838834764831845f : a->scale) * kLog2e;
   P.n_new = a->n_new;
-  P.ctas = plan.ctas;
-  if (plan.prefixes) {
-    // a dimension of extent 1 is never stepped over, but its stride still has to be one the encoder takes
-    const long long hs = a->n_kv_heads > 1 ? a->prefix_stride_h : (long long)a->n_prefix * kHeadDim;
-    const long long bs = plan.prefixes > 1 ? a->prefix_stride_b : (long long)a->n_kv_heads * hs;
-    if (!encode_boxes(&P.tm_pk, a->prefix_k, a->n_prefix, a->n_kv_heads, hs, plan.prefixes, bs) ||
-        !encode_boxes(&P.tm_pv, a->prefix_v, a->n_prefix, a->n_kv_heads, hs, plan.prefixes, bs))
-      return fail(EVICT_EINVAL, "the prefix has sizes or strides beyond a tensor map's");
-  }
-  if (a->pages) {
-    const evict_pages* g = a->pages;
-    const long long ps = g->page_stride ? g->page_stride : (long long)g->n_kv_heads * g->page_size * kHeadDim;
-    const long long hs = (long long)g->page_size * kHeadDim;
-    if (!encode_boxes(&P.tm_k, g->k, g->page_size, g->n_kv_heads, hs, g->n_pages, ps) ||
-        !encode_boxes(&P.tm_v, g->v, g->page_size, g->n_kv_heads, hs, g->n_pages, ps))
-      return fail(EVICT_EINVAL, "the pages have sizes or strides beyond a tensor map's");
-    P.own = 1;
+  const evict_pages* g = a->pages;
+  if (g) {
+    P.pages = 1;
     P.table = g->table;
     P.table_stride = g->table_stride ? g->table_stride : g->table_width;
     P.table_width = g->table_width;
     P.page_shift = __builtin_ctz((unsigned)g->page_size);
     P.n_pages = g->n_pages;
     P.lens = g->lens;
+    P.page_k = g->k;
+    P.page_v = g->v;
+    P.page_stride = g->page_stride ? g->page_stride : (long long)g->n_kv_heads * g->page_size * kHeadDim;
   }
+  // The boxes of one of the kernels: 16 whole rows, or up to 128 rows of one half.
+  auto encode = [&](bool wide, const StreamSet& s) {
+    if (s.prefixes || (s.joint && P.fan)) {
+      // a dimension of extent 1 is never stepped over, but its stride still has to be one the encoder takes
+      const long long hs = P.hkv > 1 ? a->prefix_stride_h : (long long)P.n_prefix * kHeadDim;
+      const long long bs = P.prefix_batch > 1 ? a->prefix_stride_b : P.hkv * hs;
+      for (int v = 0; v < 2; ++v)
+        if (!encode_boxes(v ? &P.tm_pv : &P.tm_pk, v ? a->prefix_v : a->prefix_k, P.n_prefix, P.hkv, hs, P.prefix_batch, bs,
+                          wide ? kStepTokens : kBoxTokens, wide ? 1 : 2))
+          return fail(EVICT_EINVAL, "the prefix has sizes or strides beyond a tensor map's");
+    }
+    if (s.own && g) {
+      P.box_rows = std::min(g->page_size, kStepTokens);
+      for (int v = 0; v < 2; ++v)
+        if (!encode_boxes(v ? &P.tm_v : &P.tm_k, v ? g->v : g->k, g->page_size, P.hkv, (long long)g->page_size * kHeadDim,
+                          g->n_pages, P.page_stride, wide ? P.box_rows : kBoxTokens, wide ? 1 : 2))
+          return fail(EVICT_EINVAL, "the pages have sizes or strides beyond a tensor map's");
+    }
+    return (int)EVICT_OK;
+  };
   cudaStream_t st = static_cast<cudaStream_t>(a->stream);
-  cudaError_t e;
-  const long long out_rows = (long long)a->batch * a->n_q_heads * a->m;
-  const dim3 join((unsigned)((out_rows + kJoinWarps - 1) / kJoinWarps));
-  if (plan.tiles == 1) {
-    if ((e = allow_smem(attend_kernel<1>, few_smem(1))) != cudaSuccess) return cuda_fail(e, "attention kernel attribute");
-    e = launch_pdl(attend_kernel<1>, dim3(plan.ctas), dim3(kThreads), few_smem(1), st, nullptr, P);
-    if (e == cudaSuccess) e = launch_pdl(attend_join_kernel<16>, join, dim3(kJoinWarps * 32), 0, st, nullptr, P);
-  } else {
-    if ((e = allow_smem(attend_kernel<2>, few_smem(2))) != cudaSuccess) return cuda_fail(e, "attention kernel attribute");
-    e = launch_pdl(attend_kernel<2>, dim3(plan.ctas), dim3(kThreads), few_smem(2), st, nullptr, P);
-    if (e == cudaSuccess) e = launch_pdl(attend_join_kernel<32>, join, dim3(kJoinWarps * 32), 0, st, nullptr, P);
+  cudaError_t e = cudaSuccess;
+  const bool few = plan.runs(plan.few), wide = plan.runs(plan.wide);
+  if (wide) {
+    if ((rc = encode(true, plan.wide))) return rc;
+    P.set = plan.wide;
+    if ((e = prepare_wide()) != cudaSuccess || (e = launch_wide(P, few, st)) != cudaSuccess)
+      return cuda_fail(e, "wide attention kernel launch");
+    g_launches.fetch_add(1);
+    P.late_wait = 1;                              // the few-row kernel needs nothing of the wide one's
   }
-  g_launches.fetch_add(2);
+  P.set = plan.few;
+  P.wide = plan.wide;
+  if (few) {
+    if ((rc = encode(false, plan.few))) return rc;
+    auto go = [&](auto kernel, int tiles) {
+      const cudaError_t x = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem(tiles));
+      return x != cudaSuccess ? x : launch_pdl(kernel, dim3(plan.few.ctas), dim3(kThreads), few_smem(tiles), st, nullptr, P);
+    };
+    e = plan.few_tiles == 1 ? go(attend_kernel<1>, 1) : go(attend_kernel<2>, 2);
+    if (e != cudaSuccess) return cuda_fail(e, "attention kernel launch");
+    g_launches.fetch_add(1);
+  }
+  if (plan.wide.joint) {
+    if (plan.wide.ctas > 1)
+      e = launch_pdl(attend_join_split_kernel, dim3(plan.wide.ctas - 1, kWideRows / 32), dim3(kJoinWarps * 32), 0, st, nullptr, P);
+  } else {
+    const long long rows = (long long)a->batch * a->n_q_heads * a->m;
+    const dim3 grid((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), block(kJoinWarps * 32);
+    e = plan.few_tiles == 1 ? launch_pdl(attend_join_kernel<16>, grid, block, 0, st, nullptr, P)
+                            : launch_pdl(attend_join_kernel<32>, grid, block, 0, st, nullptr, P);
+  }
+  g_launches.fetch_add(1);
   return e == cudaSuccess ? EVICT_OK : cuda_fail(e, "attention kernel launch");
 }

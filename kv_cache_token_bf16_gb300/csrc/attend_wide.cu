@@ -1,0 +1,582 @@
+// Attention of many query rows over a shared prefix or a sequence's rows
+// (see attend.cu for the operator and the other kernels): tcgen05 tensor cores.
+//
+// attend_wide_kernel: persistent, one CTA of ten warps per SM. A unit is a
+// (stream, KV head, tile of 256 query rows); K and V stream through a ring of
+// five 32 KB tiles of 128 rows (TMA). Warps 0-3 and 4-7 are two softmax
+// groups, a thread per query row, each with its own 128 x 128 logits and
+// 128 x 128 output accumulator in tensor memory (512 columns in all); warp 8
+// issues the MMAs, warp 9 the TMA loads. A "job" is one group's work on one
+// step:
+//     S = Q K^T (MMA) -> P = 2^(S scale - ref) as bf16 over S in tensor memory
+//     (softmax group) -> O += P V (MMA, P read from tensor memory).
+// Jobs alternate between the groups, S of the next job is issued before the
+// product with V of the last, so the tensor cores work on one group's job
+// while the other group exponentiates. A unit of more than 128 rows gives each
+// group 128 rows and both groups every step; a smaller one gives both the same
+// rows and every other step each (two partial results).
+//
+// The exponent's reference is the running maximum where it was last moved: it
+// moves only when a row's maximum passes it by more than 2^32, which costs the
+// group a read and write of its O in tensor memory (in practice only a unit's
+// first step moves it). Weights, sums and O are relative to it and floating, so
+// the result does not depend on where it stands. Weights enter the product
+// with V as bf16 (half a step: 2^-9 of a weight), at twice the rate of the
+// split that the few-row kernel uses; their roundings are independent, so the
+// output's error grows from one rounding to the root of two.
+//
+// Bound: the tensor cores (2 x 512 clocks a job) with many rows, HBM with few.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "attend.cuh"
+#include "attend.h"
+#include "common.cuh"
+#include "launch.h"
+#include "pipeline.cuh"
+#include "tcgen05.cuh"
+
+namespace evict {
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kTileBytes = kTile * kHeadDim * 2;
+constexpr int kRing = 5;
+constexpr int kWideThreads = 10 * 32;
+constexpr int kMmaWarp = 8, kTmaWarp = 9;
+constexpr int kBadWords = 9;                      // 257 tokens and more
+constexpr float kRefSlack = 32.f;                 // log2 of the largest weight
+
+struct WideShared {
+  uint64_t kv_full[kRing], kv_empty[kRing];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done;
+  uint32_t tmem_base;
+  int fail;
+  uint32_t bad[2][2][kBadWords];                  // [group][segment parity]
+  ScanShared scan;
+};
+
+using WideCursor = Cursor<kWideRows>;
+
+// The part of a unit that this CTA takes.
+struct Segment {
+  int steps;                                      // from the cursor's on
+  bool two, alt;                                  // both groups on every step; or taking turns
+  __device__ Segment(const StreamSet& set, const AttendParams& p, const WideCursor& c, int left) {
+    steps = min(c.steps - c.step, left);
+    const long long rows = (long long)c.st.n * p.group - (long long)c.tile * kWideRows;
+    two = rows > kTile;
+    alt = !two && !set.joint;
+  }
+  __device__ bool has(int w, int i) const { return two || (alt ? (i & 1) == w : w == 0); }
+  __device__ int jobs(int w) const { return two ? steps : alt ? (steps + 1 - w) / 2 : w == 0 ? steps : 0; }
+};
+// On to the first step behind the segment.
+__device__ __forceinline__ void skip(WideCursor& c, const AttendParams& p, const StreamSet& set, int steps) {
+  c.step += steps - 1;
+  c.next(p, set);
+}
+
+// Rows of K and V of a step: prefix rows, or own rows from row0 on.
+struct Step {
+  bool pre;
+  int row0;
+  __device__ Step(const WideCursor& c, int step) {
+    const int ps = c.st.pre_steps();
+    pre = step < ps;
+    row0 = (pre ? step : step - ps) * kStepTokens;
+  }
+};
+
+// The unit's first query sees own rows before this one; from here to the last query's, rows with
+// infinities or NaN in V are marked (at most 256 tokens).
+__device__ __forceinline__ int first_marked(const AttendParams& p, const WideCursor& c) {
+  return c.st.len - c.st.n + (int)((long long)c.tile * kWideRows / p.group) + 1;
+}
+
+__device__ void producer(const AttendParams& p, WideShared& sh, WideCursor c, int count, uint32_t ring) {
+  const StreamSet& set = p.set;
+  const int lane = threadIdx.x & 31;
+  long long used = 0;
+  bool ok = true;
+  while (count > 0 && ok) {
+    const Segment g(set, p, c, count);
+    for (int i = 0; i < g.steps && ok; ++i) {
+      const Step st(c, c.step + i);
+      int page = 0;
+      const int box = p.box_rows, boxes = kTile / box;
+      const int row = st.row0 + lane * box;       // this lane's page
+      if (!st.pre && lane < boxes) {
+        page = p.n_pages;                         // outside the pool: zeros
+        if (row < c.st.len) {
+          page = p.table[(long long)(c.s - set.prefixes) * p.table_stride + (row >> p.page_shift)];
+          if (page < 0 || page >= p.n_pages) {
+            raise_device_error(p.err, kDevBadIndex);
+            page = p.n_pages;
+          }
+        }
+      }
+      for (int kv = 0; kv < 2 && ok; ++kv, ++used) {
+        const int slot = (int)(used % kRing);
+        ok = wait_phase(&sh.kv_empty[slot], (uint32_t)(((used / kRing) & 1) ^ 1), &sh.fail, p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        uint64_t* bar = &sh.kv_full[slot];
+        const uint32_t dst = ring + slot * kTileBytes;
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar, kTileBytes);
+        __syncwarp();
+        if (st.pre) {
+          const int plane = c.s < set.prefixes ? c.s : (c.s - set.prefixes) / p.fan;
+          if (lane < 2)
+            tma_load_5d(dst + lane * (kTileBytes / 2), kv ? &p.tm_pv : &p.tm_pk, 0, st.row0, lane, c.h, plane, bar);
+        } else if (lane < boxes) {
+          for (int hf = 0; hf < 2; ++hf)
+            tma_load_5d(dst + hf * (kTileBytes / 2) + lane * box * 128, kv ? &p.tm_v : &p.tm_k, 0,
+                        row & ((1 << p.page_shift) - 1), hf, c.h, page, bar);
+        }
+      }
+    }
+    count -= g.steps;
+    if (count > 0) skip(c, p, set, g.steps);
+  }
+  // every copy issued must land before the CTA may release its shared memory
+  for (int i = 0; i < kRing; ++i) {
+    const long long n = used > i ? (used - i + kRing - 1) / kRing : 0;       // uses of slot i
+    if (n > 0) drain_phase(&sh.kv_full[i], (uint32_t)((n - 1) & 1), p.err);
+  }
+}
+
+// S = Q K^T: both K-major.
+__device__ __forceinline__ void issue_qk(uint32_t d, uint32_t q, uint32_t k) {
+  constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile);
+#pragma unroll
+  for (int s = 0; s < 8; ++s) {
+    const uint32_t off = (uint32_t)((s >> 2) * kTile * 128 + (s & 3) * 32);
+    tc::mma_bf16(d, tc::sw128_desc(q + off), tc::sw128_desc(k + off), idesc, s > 0 ? 1u : 0u);
+  }
+}
+// O (+)= P V: P in tensor memory (two weights a column), V with its rows as the product's
+// depth (MN-major). 16 rows of V are 2048 bytes of each half.
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pt, uint32_t v, bool accumulate) {
+  constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile) | (1u << 16);
+#pragma unroll
+  for (int s = 0; s < 8; ++s) {
+    const uint64_t bd = tc::sw128_desc_mn(v + s * 2048, kTileBytes / 2, 1024);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "r"(pt + s * 8), "l"(bd), "r"(idesc), "r"(accumulate || s > 0 ? 1u : 0u)
+        : "memory");
+  }
+}
+
+__device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, int count, uint32_t tmem, uint32_t qbuf,
+                           uint32_t ring) {
+  const StreamSet& set = p.set;
+  const int lane = threadIdx.x & 31;
+  uint32_t p_waits[2] = {0, 0};
+  long long used = 0;                             // ring tiles of the steps before
+  int segments = 0;
+  bool ok = true;
+  struct Job {
+    int w;
+    bool first, last, first_v, last_v;
+    long long v;                                  // ring tile
+    int from;                                     // rows of the tile from here on lie behind the sequence's end
+    int mark0, parity;                            // the tile's row of the first token that may be marked (128: none)
+  };
+  Job pend = {};
+  bool pending = false;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    ok = ok && wait_phase(bar, parity, &sh.fail, p.err);
+    ok = __all_sync(0xffffffffu, ok);
+    return ok;
+  };
+  auto flush = [&] {                              // the pending job's product with V
+    pending = false;
+    const int slot = (int)(pend.v % kRing);
+    if (!wait(&sh.p_full[pend.w], p_waits[pend.w]++ & 1)) return;
+    if (!wait(&sh.kv_full[slot], (uint32_t)((pend.v / kRing) & 1))) return;
+    const uint32_t v = ring + slot * kTileBytes;
+    if (pend.first_v) {
+      // rows behind the sequence's end, and rows with infinities or NaN that some queries do not
+      // see, meet weights of 0: zeros in their place
+      const uint32_t at = v + ((lane >> 3) & 1) * (kTileBytes / 2) + (lane & 7) * 16;
+      auto blank = [&](int r) {
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + r * 128), "r"(0u) : "memory");
+      };
+      bool wrote = pend.from < kTile;
+      for (int r = pend.from + (lane >> 4); r < kTile; r += 2) blank(r);
+      if (pend.mark0 < kTile) {
+        const uint32_t* bad = sh.bad[pend.w][pend.parity];
+        uint32_t any = 0;
+        for (int k = 0; k < kBadWords; ++k) any |= bad[k];
+        if (any) {
+          wrote = true;
+          for (int k = max(0, -pend.mark0); k < 32 * kBadWords && pend.mark0 + k < kTile; ++k)
+            if ((bad[k >> 5] >> (k & 31)) & 1) blank(pend.mark0 + k);
+        }
+      }
+      if (wrote) tc::fence_proxy_async_smem();
+      __syncwarp();
+    }
+    tc::fence_after_sync();
+    if (lane == 0) {
+      issue_pv(tmem + 2 * kTile + pend.w * kTile, tmem + pend.w * kTile, v, !pend.first);
+      if (pend.last_v) tc::mma_commit(&sh.kv_empty[slot]);
+      if (pend.last) tc::mma_commit(&sh.o_full[pend.w]);
+    }
+    __syncwarp();
+  };
+  while (count > 0 && ok) {
+    const Segment g(set, p, c, count);
+    int done[2] = {0, 0};
+    for (int i = 0; i < g.steps && ok; ++i, used += 2) {
+      const Step st(c, c.step + i);
+      const int slot = (int)(used % kRing);
+      bool first_use = true;
+      for (int w = 0; w < 2 && ok; ++w) {
+        if (!g.has(w, i)) continue;
+        const bool last_use = w == 1 || !g.two;
+        if (pending && pend.w == w) flush();      // S of this group still holds that job's weights
+        if (!ok) break;
+        if (first_use && !wait(&sh.kv_full[slot], (uint32_t)((used / kRing) & 1))) break;
+        if (done[w] == 0 && !wait(&sh.q_full[w], (uint32_t)(segments & 1))) break;
+        tc::fence_after_sync();
+        if (lane == 0) {
+          issue_qk(tmem + w * kTile, qbuf + w * kTileBytes, ring + slot * kTileBytes);
+          tc::mma_commit(&sh.s_full[w]);
+          if (last_use) tc::mma_commit(&sh.kv_empty[slot]);
+        }
+        __syncwarp();
+        if (pending) flush();
+        if (!ok) break;
+        pend.w = w;
+        pend.v = used + 1;
+        pend.first = done[w] == 0;
+        pend.last = ++done[w] == g.jobs(w);
+        pend.first_v = first_use;
+        pend.last_v = last_use;
+        pend.from = kTile;
+        pend.mark0 = kTile;
+        pend.parity = segments & 1;
+        if (!st.pre) {
+          pend.from = min(kTile, max(0, c.st.len - st.row0));
+          if (p.m > 1 && c.st.reach(p, c.tile) >= 0) pend.mark0 = first_marked(p, c) - st.row0;
+        }
+        pending = true;
+        first_use = false;
+      }
+    }
+    for (int w = 0; w < 2 && ok; ++w)             // a group without a job has still loaded its queries
+      if (done[w] == 0) wait(&sh.q_full[w], (uint32_t)(segments & 1));
+    ++segments;
+    count -= g.steps;
+    if (count > 0) skip(c, p, set, g.steps);
+  }
+  if (pending && ok) flush();
+  // every MMA must finish before tensor and shared memory are released
+  if (lane == 0) {
+    tc::mma_commit(&sh.done);
+    drain_phase(&sh.done, 0, p.err);
+  }
+  __syncwarp();
+}
+
+// 64 columns of this thread's row; the load and its wait are one statement, so that nothing uses
+// the registers before the data is there.
+__device__ __forceinline__ void load64(uint32_t taddr, float* v) {
+  uint32_t r[64];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void store32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// One softmax group: thread `row` of group w.
+__device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor c, int count, int w, int row, uint32_t tmem,
+                              unsigned char* qbuf) {
+  const StreamSet& set = p.set;
+  const int warp = row >> 5;
+  const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+  const uint32_t s_at = tmem + lanes + (uint32_t)(w * kTile), o_at = s_at + 2 * kTile;
+  const uint32_t flip = p.scale2 < 0.f ? 0x80008000u : 0u;   // a negative scale: of -Q, so that maxima stay maxima
+  const float scale = fabsf(p.scale2);
+  unsigned char* q_mine = qbuf + w * kTileBytes;
+
+  // this row's query into the group's tile, and which rows with infinities or NaN in V some
+  // queries of the unit do not see
+  auto load_query = [&](const WideCursor& cu, const Segment& g, int parity) {
+    const int r = g.two ? w * kTile + row : row;
+    const QueryRow q = query_row(p, set, cu, r);
+    const bool real = q.real && (g.two || g.alt || w == 0);
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)q.b * p.qb +
+                                                      (long long)q.hq * p.qh + (long long)q.t * p.qm);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (real) x = src[j];
+      x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
+      *reinterpret_cast<uint4*>(q_mine + tc::sw128_offset(row, j, kTile)) = x;
+    }
+    const int reach = cu.st.reach(p, cu.tile);
+    if (p.m > 1 && reach >= 0) {
+      const int first = first_marked(p, cu);
+      uint32_t* bad = sh.bad[w][parity];
+      if (row < kBadWords) bad[row] = 0;
+      tc::named_sync(1 + w, kTile);
+      const int b = cu.s - set.prefixes;
+      for (int e = row; e < 16 * (reach + 1 - first); e += kTile) {
+        const int tok = first + (e >> 4);
+        if (tok < 0) continue;
+        const int page = p.table[(long long)b * p.table_stride + (tok >> p.page_shift)];
+        if (page < 0 || page >= p.n_pages) continue;
+        const uint4 x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.page_v) +
+                                                       (long long)page * p.page_stride +
+                                                       (((long long)cu.h << p.page_shift) +
+                                                        (tok & ((1 << p.page_shift) - 1))) * kHeadDim)[e & 15];
+        if (nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w))
+          atomicOr(&bad[(tok - first) >> 5], 1u << ((tok - first) & 31));
+      }
+    }
+    tc::fence_proxy_async_smem();
+    tc::mbar_arrive(&sh.q_full[w]);
+    return q;
+  };
+
+  int s_waits = 0, o_waits = 0, segments = 0;
+  bool ok = true;
+  Segment g(set, p, c, count);
+  QueryRow q = load_query(c, g, 0);
+  while (count > 0) {
+    const int jobs = g.jobs(w);
+    const int limit = q.real ? c.st.len - c.st.n + q.t : -1;     // last own row that this query sees
+    float ref = -INFINITY, sum = 0.f;
+    bool begun = false;
+    for (int i = 0; i < g.steps && ok; ++i) {
+      if (!g.has(w, i)) continue;
+      const Step st(c, c.step + i);
+      ok = wait_phase(&sh.s_full[w], (uint32_t)(s_waits++ & 1), &sh.fail, p.err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const int seen = (st.pre ? c.st.pre - 1 : limit) - st.row0;     // columns 0 .. seen
+      const bool masked = __any_sync(0xffffffffu, seen < kTile - 1);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {      // 64 columns at a time: their registers are few enough
+        float v[64];
+        load64(s_at + 64 * half, v);
+        if (masked) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k)
+            if (64 * half + k > seen) v[k] = -INFINITY;
+        }
+        float mx[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = fmax3(v[j], v[j + 4], v[j + 8]);
+#pragma unroll
+        for (int k = 12; k < 60; k += 8)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = fmax3(mx[j], v[k + j], v[k + 4 + j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], v[60 + j]);
+        const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * scale;
+        if (__any_sync(0xffffffffu, top > ref + kRefSlack)) {         // also from no reference to the first
+          const float to = fmaxf(ref, top), f = weight_of(ref, to);
+          ref = to;
+          sum *= f;
+          if (begun) {
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {
+              float o[32];
+              tc::tmem_ld32(o_at + 32 * h, o);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] *= f;
+              store32(o_at + 32 * h, reinterpret_cast<const uint32_t*>(o));
+            }
+          }
+          if (half == 1) {                        // the first half's weights, too
+            float o[32];
+            wait_stores();
+            tc::tmem_ld32(s_at, o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const uint32_t x = __float_as_uint(o[k]);
+              o[k] = __uint_as_float(pack_bf16(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f));
+            }
+            store32(s_at, reinterpret_cast<const uint32_t*>(o));
+          }
+        }
+        const float base = base_of(ref);
+        const uint64_t sc2 = pack_f32x2(scale, scale), nb2 = pack_f32x2(-base, -base);
+        uint64_t acc[2] = {0ull, 0ull};
+        uint32_t pk[32];
+#pragma unroll
+        for (int k = 0; k < 64; k += 2) {
+          const uint64_t e = ex2_f32x2(fma_f32x2(pack_f32x2(v[k], v[k + 1]), sc2, nb2));
+          acc[(k >> 1) & 1] = add_f32x2(acc[(k >> 1) & 1], e);
+          float a, b;
+          split_f32x2(e, a, b);
+          pk[k >> 1] = pack_bf16(a, b);
+        }
+        // over columns that are in registers by now: half 0 over 0 .. 31, half 1 over 32 .. 63
+        store32(s_at + 32 * half, pk);
+        float a0, a1;
+        split_f32x2(add_f32x2(acc[0], acc[1]), a0, a1);
+        sum += a0 + a1;
+      }
+      begun = true;
+      wait_stores();
+      tc::fence_before_sync();
+      tc::mbar_arrive(&sh.p_full[w]);
+    }
+    // the next unit's queries: this group's last S is in registers, so its tile is free
+    const int left = count - g.steps;
+    const WideCursor at = c;
+    const Segment part = g;
+    const QueryRow mine = q;
+    if (left > 0 && ok) {
+      skip(c, p, set, g.steps);
+      g = Segment(set, p, c, left);
+      q = load_query(c, g, (segments + 1) & 1);
+    }
+    count = left;
+    if (ok && jobs > 0) {
+      ok = wait_phase(&sh.o_full[w], (uint32_t)(o_waits++ & 1), &sh.fail, p.err);
+      ok = __all_sync(0xffffffffu, ok);
+    }
+    if (!ok) break;
+    tc::fence_after_sync();
+    const bool whole = set.joint && part.steps == at.steps;     // no other part, no other unit for these rows
+    const bool write = mine.real && (part.two || part.alt || w == 0);
+    const long long prow = ((at.unit + blockIdx.x) * 2 + w) * kTile + row;
+    const float inv = at.st.pre > 0 || limit >= 0 ? 1.f / sum : 0.f;
+    uint32_t any_bad = 0;
+    const int first = first_marked(p, at);
+    const uint32_t* bad = sh.bad[w][segments & 1];
+    if (p.m > 1 && at.st.reach(p, at.tile) >= 0)
+      for (int k = 0; k < kBadWords; ++k) any_bad |= bad[k];
+#pragma unroll 1
+    for (int h = 0; h < 4; ++h) {
+      float o[32];
+      if (jobs > 0) {
+        tc::tmem_ld32(o_at + 32 * h, o);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = 0.f;
+      }
+      if (any_bad && write) {
+        // rare: the rows that were blanked, for the queries that see them, where the steps of this
+        // part (of this group) hold them
+        for (int k = 0; k < 32 * kBadWords; ++k) {
+          const int tok = first + k;
+          if (!((bad[k >> 5] >> (k & 31)) & 1) || tok < 0 || tok > limit) continue;
+          const int step = at.st.pre_steps() + tok / kStepTokens - at.step;
+          if (step < 0 || step >= part.steps || !part.has(w, step)) continue;
+          const int page = p.table[(long long)(at.s - set.prefixes) * p.table_stride + (tok >> p.page_shift)];
+          const long long e = (long long)page * p.page_stride +
+                              (((long long)at.h << p.page_shift) + (tok & ((1 << p.page_shift) - 1))) * kHeadDim;
+          const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(p.page_k) + e;
+          const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.page_v) + e + 32 * h;
+          const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q) + (long long)mine.b * p.qb +
+                                    (long long)mine.hq * p.qh + (long long)mine.t * p.qm;
+          float z = 0.f;
+          for (int d = 0; d < kHeadDim; ++d) z += __bfloat162float(qr[d]) * __bfloat162float(kr[d]);
+          const float wt = ex2(z * p.scale2 - base_of(ref));
+#pragma unroll
+          for (int d = 0; d < 32; ++d) o[d] += wt * __bfloat162float(vr[d]);
+        }
+      }
+      if (!write) continue;
+      if (whole) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (long long)mine.b * p.ob +
+                                              (long long)mine.hq * p.oh + (long long)mine.t * p.om + 32 * h);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          dst[k] = make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                              pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+      } else {
+        float4* dst = reinterpret_cast<float4*>(set.part_o + prow * kHeadDim + 32 * h);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      }
+    }
+    if (write) {
+      if (!whole) {
+        set.part_ml[prow] = make_float2(ref, sum);
+      } else if (p.lse) {
+        p.lse[((long long)mine.b * p.hq + mine.hq) * p.m + mine.t] =
+            at.st.pre > 0 || limit >= 0 ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+      }
+    }
+    ++segments;
+  }
+}
+
+__global__ void __launch_bounds__(kWideThreads, 1) attend_wide_kernel(const __grid_constant__ AttendParams p, int early) {
+  pdl_wait();
+  // what comes next may start on an SM as soon as this kernel leaves it
+  if (early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ WideShared sh;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  unsigned char* qbuf = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const uint32_t q_at = tc::smem_u32(qbuf), ring = q_at + 2 * kTileBytes;
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      tc::mbar_init(&sh.kv_full[i], 1);
+      tc::mbar_init(&sh.kv_empty[i], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      tc::mbar_init(&sh.q_full[w], kTile);
+      tc::mbar_init(&sh.s_full[w], 1);
+      tc::mbar_init(&sh.p_full[w], kTile);
+      tc::mbar_init(&sh.o_full[w], 1);
+    }
+    tc::mbar_init(&sh.done, 1);
+    sh.fail = 0;
+  }
+  WideCursor c;
+  const int count = find_share<kWideRows, kWideThreads>(p, p.set, sh.scan, c);
+  if (count == 0) return;
+  if (warp == 0) tc::tmem_alloc(&sh.tmem_base, 4 * kTile);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = sh.tmem_base;
+  if (warp == kTmaWarp) producer(p, sh, c, count, ring);
+  else if (warp == kMmaWarp) mma_issuer(p, sh, c, count, tmem, q_at, ring);
+  else softmax_group(p, sh, c, count, warp >> 2, tid & (kTile - 1), tmem, qbuf);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 0) tc::tmem_dealloc(tmem, 4 * kTile);
+}
+
+}  // namespace
+
+int wide_smem() { return (2 + kRing) * kTileBytes + 1024; }
+
+cudaError_t prepare_wide() {
+  return cudaFuncSetAttribute(attend_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wide_smem());
+}
+
+// early: the next kernel in the stream waits for this one by itself (late_wait).
+cudaError_t launch_wide(const AttendParams& p, bool early, cudaStream_t st) {
+  return launch_pdl(attend_wide_kernel, dim3(p.set.ctas), dim3(kWideThreads), wide_smem(), st, nullptr, p, early ? 1 : 0);
+}
+
+}  // namespace evict
