@@ -175,7 +175,7 @@ __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, 
                            uint32_t ring) {
   const StreamSet& set = p.set;
   const int lane = threadIdx.x & 31;
-  uint32_t p_waits[2] = {0, 0};
+  uint32_t p_waits[2] = {0, 0}, q_waits[2] = {0, 0};
   long long used = 0;                             // ring tiles of the steps before
   int segments = 0;
   bool ok = true;
@@ -183,7 +183,7 @@ __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, 
     int w;
     bool first, last, first_v, last_v;
     long long v;                                  // ring tile
-    int from;                                     // rows of the tile from here on lie behind the sequence's end
+    int from;                                     // rows of the tile from here on are seen by none of the unit's queries
     int mark0, parity;                            // the tile's row of the first token that may be marked (128: none)
   };
   Job pend = {};
@@ -200,8 +200,8 @@ __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, 
     if (!wait(&sh.kv_full[slot], (uint32_t)((pend.v / kRing) & 1))) return;
     const uint32_t v = ring + slot * kTileBytes;
     if (pend.first_v) {
-      // rows behind the sequence's end, and rows with infinities or NaN that some queries do not
-      // see, meet weights of 0: zeros in their place
+      // rows that no query sees, and rows with infinities or NaN that some queries do not see, meet
+      // weights of 0: zeros in their place
       const uint32_t at = v + ((lane >> 3) & 1) * (kTileBytes / 2) + (lane & 7) * 16;
       auto blank = [&](int r) {
         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + r * 128), "r"(0u) : "memory");
@@ -242,7 +242,7 @@ __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, 
         if (pending && pend.w == w) flush();      // S of this group still holds that job's weights
         if (!ok) break;
         if (first_use && !wait(&sh.kv_full[slot], (uint32_t)((used / kRing) & 1))) break;
-        if (done[w] == 0 && !wait(&sh.q_full[w], (uint32_t)(segments & 1))) break;
+        if (done[w] == 0 && !wait(&sh.q_full[w], q_waits[w]++ & 1)) break;
         tc::fence_after_sync();
         if (lane == 0) {
           issue_qk(tmem + w * kTile, qbuf + w * kTileBytes, ring + slot * kTileBytes);
@@ -262,15 +262,14 @@ __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, 
         pend.mark0 = kTile;
         pend.parity = segments & 1;
         if (!st.pre) {
-          pend.from = min(kTile, max(0, c.st.len - st.row0));
-          if (p.m > 1 && c.st.reach(p, c.tile) >= 0) pend.mark0 = first_marked(p, c) - st.row0;
+          const int reach = c.st.reach(p, c.tile);
+          pend.from = min(kTile, max(0, reach + 1 - st.row0));
+          if (p.m > 1 && reach >= 0) pend.mark0 = first_marked(p, c) - st.row0;
         }
         pending = true;
         first_use = false;
       }
     }
-    for (int w = 0; w < 2 && ok; ++w)             // a group without a job has still loaded its queries
-      if (done[w] == 0) wait(&sh.q_full[w], (uint32_t)(segments & 1));
     ++segments;
     count -= g.steps;
     if (count > 0) skip(c, p, set, g.steps);
@@ -322,13 +321,15 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
   auto load_query = [&](const WideCursor& cu, const Segment& g, int parity) {
     const int r = g.two ? w * kTile + row : row;
     const QueryRow q = query_row(p, set, cu, r);
-    const bool real = q.real && (g.two || g.alt || w == 0);
+    // A group without a job in this part announces nothing (it could announce twice before the
+    // MMA warp has looked once).
+    if (g.jobs(w) == 0) return q;
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)q.b * p.qb +
                                                       (long long)q.hq * p.qh + (long long)q.t * p.qm);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       uint4 x = make_uint4(0, 0, 0, 0);
-      if (real) x = src[j];
+      if (q.real) x = src[j];
       x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
       *reinterpret_cast<uint4*>(q_mine + tc::sw128_offset(row, j, kTile)) = x;
     }

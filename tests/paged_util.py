@@ -75,17 +75,21 @@ def attend64(q, prefix, own, n_new=None, scale=None):
             rows = ks[-1].shape[1]
         k, v = torch.cat(ks, 1), torch.cat(vs, 1)
         g = hq // k.shape[0]
-        for t in range(n):
-            see = n_pre + max(0, rows - n + t + 1) if own is not None else n_pre
-            for h in range(hq):
-                if see == 0:
-                    out[b, h, t], wt[b, h, t], lse[b, h, t] = 0, 0, -math.inf
-                    continue
-                z = scale * (k[h // g, :see] @ q[b, h, t])
-                p = torch.softmax(z, 0)
-                out[b, h, t] = p @ v[h // g, :see]
-                wt[b, h, t] = p @ v[h // g, :see].abs()
-                lse[b, h, t] = torch.logsumexp(z, 0)
+        if n == 0:
+            continue
+        see = torch.full((n,), n_pre)
+        if own is not None:
+            see = n_pre + (rows - n + torch.arange(n) + 1).clamp(min=0)
+        hide = torch.arange(k.shape[1])[None] >= see[:, None]
+        for h in range(hq):
+            z = (scale * (q[b, h, :n] @ k[h // g].T)).masked_fill(hide, -math.inf)
+            top = z.amax(1, keepdim=True) if z.shape[1] else torch.full((n, 1), -math.inf, dtype=torch.float64)
+            w = torch.exp(z - torch.where(top == -math.inf, 0.0, top))
+            l = w.sum(1, keepdim=True)
+            p = w / torch.where(see[:, None] > 0, l, 1.0)
+            vh = torch.where(hide.all(0)[:, None], 0.0, v[h // g])      # rows that no query sees
+            out[b, h, :n], wt[b, h, :n] = p @ vh, p @ vh.abs()
+            lse[b, h, :n] = (top + torch.log(l))[:, 0]
     return out, lse, wt
 
 

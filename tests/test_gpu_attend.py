@@ -94,6 +94,15 @@ CASES = [
     (3, 4, 2, 2, 0, 1, 16, [1, 0, 40], [2, 2, 2]),     # a query before the first row sees nothing
     (2, 64, 1, 2, 513, 1, 64, [3, 700], None),
     (3, 4, 2, 130, 100, 1, 64, [130, 400, 131], [130, 129, 3]),
+    # more units than CTAs: the wide kernel's parts of units, with a group that has no work in some
+    (12, 8, 8, 300, 200, 1, 16, [300, 20, 700, 3, 0, 310, 256, 299, 33, 64, 1, 500],
+     [300, 0, 290, 3, 0, 44, 256, 2, 33, 0, 1, 257]),
+    (64, 160, 8, 1, 100, 32, 16, None, None),
+    (64, 160, 8, 1, 300, 32, 16, [b % 40 for b in range(64)], [b % 2 for b in range(64)]),
+    (2, 8, 2, 300, 0, 1, 128, [300, 1200], None),
+    (3, 4, 1, 64, 0, 1, 32, [0, 64, 30], [64, 64, 64]),
+    (2, 36, 1, 2, 700, 2, 16, [2, 450], None),
+    (5, 2, 1, 300, 1, 1, 16, None, [300, 0, 1, 129, 128]),
 ]
 
 
@@ -106,16 +115,38 @@ def test_attention_matches_the_definition(case, layout):
 
 
 @pytest.mark.parametrize("scale", [0.3, -0.05, 1e-3])
-def test_other_scales(scale):
-    s = make(120, 3, 8, 2, 2, 150, 1, 16, [2, 40, 133])
+@pytest.mark.parametrize("hq", [8, 40, 200], ids=["few", "wide", "joint"])
+def test_other_scales(scale, hq):
+    s = make(120, 3, hq, 2, 2, 150, 1, 16, [2, 40, 133])
     check(s, *attend(s, scale=scale), scale=scale)
 
 
-def test_large_logits_keep_their_order():
+@pytest.mark.parametrize("hq", [8, 100, 260], ids=["few", "wide", "joint"])
+def test_large_logits_keep_their_order(hq):
     # logits up to hundreds: a running maximum that moves by far, weights that vanish
-    s = make(121, 4, 8, 2, 1, 700, 1, 16, [1, 100, 300, 17])
+    s = make(121, 4, hq, 2, 1, 700, 1, 16, [1, 100, 300, 17])
     s["q"].mul_(30)
     check(s, *attend(s))
+
+
+@pytest.mark.parametrize("hq", [8, 100, 260], ids=["few", "wide", "joint"])
+def test_rising_logits(hq):
+    # keys that grow along the prefix: the maximum rises at every step, by far more than fp32's range
+    s = make(122, 4, hq, 2, 1, 1000, 1, 16, [1, 100, 300, 17])
+    k = s["prefix"][0]
+    q = s["q"]
+    q.copy_(q.abs())
+    k.copy_((k.abs() * torch.linspace(0.01, 60, 1000, device="cuda")[:, None]).to(torch.bfloat16))
+    check(s, *attend(s))
+
+
+@pytest.mark.parametrize("hq", [8, 100, 260], ids=["few", "wide", "joint"])
+def test_results_are_the_same_every_time(hq):
+    s = make(123, 7, hq, 2, 3, 3000, 1, 16, [3 + 100 * b for b in range(7)])
+    a, la = attend(s)
+    for _ in range(5):
+        b, lb = attend(s)
+        assert torch.equal(a, b) and torch.equal(la, lb)
 
 
 def test_kept_rows_of_a_cache():
@@ -132,10 +163,11 @@ def test_kept_rows_of_a_cache():
     cache.close()
 
 
-def test_masked_rows_may_hold_anything():
+@pytest.mark.parametrize("hq", [4, 40, 400], ids=["few", "wide", "joint"])
+def test_masked_rows_may_hold_anything(hq):
     # new rows with infinities and NaN: queries before them are untouched, queries from them on see them
     m, lens = 6, [6, 50]
-    s = make(140, 2, 4, 2, m, 60, 1, 16, lens)
+    s = make(140, 2, hq, 2, m, 60, 1, 16, lens)
     clean, _ = attend(s)
     page = 16
     for b, j, val in ((0, 4, math.nan), (1, 47, math.inf), (1, 49, math.nan)):
@@ -154,8 +186,9 @@ def test_masked_rows_may_hold_anything():
     assert bool(got[1, :, 5].isnan().all())
 
 
-def test_visible_infinite_logits():
-    s = make(141, 1, 2, 1, 1, 40, 1, 16, [20])
+@pytest.mark.parametrize("hq", [2, 50, 200], ids=["few", "wide", "joint"])
+def test_visible_infinite_logits(hq):
+    s = make(141, 1, hq, 1, 1, 40, 1, 16, [20])
     s["prefix"][0][0, 0, 3] = math.inf          # some logit is an infinity or NaN: so is the result
     out, lse = attend(s)
     assert bool(out.isnan().all()) and bool((lse.isnan() | (lse == math.inf)).all())
@@ -231,7 +264,7 @@ def test_pages_beyond_32_bit_offsets():
     check({"q": q, "prefix": None, "new": None, "own": [(k[0], v[0]), (k[1, :, :299], v[1, :, :299])]}, out, lse)
 
 
-@pytest.mark.parametrize("m", [1, 4])
+@pytest.mark.parametrize("m", [1, 4, 40])
 def test_two_streams_and_two_graphs_at_once(m):
     a = make(150, 8, 8, 2, m, 900, 1, 16, [m + 7 * b for b in range(8)])
     b = make(151, 8, 8, 2, m, 500, 2, 16, [m + 11 * b for b in range(8)])
