@@ -450,7 +450,7 @@ int evict_shared_attention_workspace(const evict_attention* a, size_t* bytes);
 
 /* EVICT_EINVAL: NULL or misaligned pointers, bad sizes or strides, head counts that do not divide,
  * pages that are not bf16, a workspace that is too small; EVICT_ELIMIT: batch above
- * EVICT_MAX_ATTEND_BATCH, or batch * n_q_heads * m of 2^31 or more. batch or m of 0 is a no-op.
+ * EVICT_MAX_ATTEND_BATCH, or batch * n_q_heads * m of 2^30 or more, or rows of tables beyond 2^31 steps of 16 in all. batch or m of 0 is a no-op.
  * Device errors (a table entry outside the pool, read as zeros; lens beyond the table, cut to it;
  * n_new outside [0, m], taken as the nearest of these; a bounded wait that gave up) are reported
  * through `error`. */

@@ -4,18 +4,19 @@
 // over the rows a query sees, in one pass over K and V with a running maximum
 // and sum; logits are kept in base 2 (scale * log2 e), so p = 2^(x - m).
 //
-// attend_kernel: persistent, one CTA of eight warps per SM. All the batch's
-// rows of K and V, prefix and pages alike, are cut into steps of 128 rows that
-// are laid end to end, and every CTA takes an equal share of them whatever the
-// sequences' lengths are: the lengths live on the device, so the shares are
-// found there, by one block scan over the batch. Warp w takes rows
-// 16 w .. 16 w + 15 of every step and works alone, with its own running
-// maximum, sum and output and its own ring of TMA boxes (16 rows x 128
-// elements of K and of V, 8 KB); the eight results meet only where the CTA
-// leaves a unit. A 16-row box never crosses a page. Bound: HBM; a warp has up
-// to kStages - 1 boxes in flight (128 KB an SM) while it computes on another,
-// and the tensor cores (m16n8k16, queries as rows, one or two tiles of 16)
-// need about a quarter of the time its box needs from memory.
+// attend_kernel (units of up to 32 query rows): persistent, one CTA per SM. All
+// the rows of K and V that the batch reads, prefix and pages alike, are laid
+// end to end in boxes of 16 rows, and every warp of the grid takes an equal
+// share of them, whatever the sequences' lengths are: the lengths live on the
+// device, so the shares are found there, by one block scan. A warp works by
+// itself from there on: its own ring of TMA boxes (16 rows of K and of V, 8
+// KB; a box never crosses a page), its own running maximum, sum and output,
+// and no barrier, so that one warp's start or end of a unit hides behind the
+// others' rows. Queries are the rows of m16n8k16 products (one or two tiles of
+// 16). Bound: HBM; a warp has a box or two in flight while it computes on
+// another (96 to 128 KB an SM).
+//
+// attend_wide_kernel (attend_wide.cu): units of more query rows.
 //
 // attend_join_kernel: a warp per output row merges the partial results of the
 // row's units, in the order of their slots.
@@ -38,21 +39,12 @@
 namespace evict {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kBoxTokens = 16;
 constexpr int kBoxBytes = kBoxTokens * kHeadDim * 2;       // of K or of V
-constexpr int kStages = 3;
-constexpr int kRingBytes = kWarps * kStages * 2 * kBoxBytes;
-constexpr int kQPitch = kHeadDim * 2 + 16;                 // bytes: ldmatrix rows on different banks
 
-// Columns of the warps' results that are merged at a time, and the dynamic shared memory, for
-// `tiles` tiles of 16 query rows: the ring, the queries and the merge's buffers.
-__host__ __device__ constexpr int merge_cols(int tiles) { return tiles == 1 ? 32 : 16; }
-constexpr int few_smem(int tiles) {
-  return kRingBytes + 1024 + 16 * tiles * kQPitch + kWarps * 16 * tiles * (merge_cols(tiles) + 4) * 4 +
-         kWarps * 16 * tiles * 8;
-}
+// Warps and boxes of a warp's ring for `tiles` tiles of 16 query rows, by the registers they take.
+__host__ __device__ constexpr int few_warps(int tiles) { return tiles == 1 ? 12 : 8; }
+__host__ __device__ constexpr int few_stages(int tiles) { return tiles == 1 ? 2 : 3; }
+constexpr int few_smem(int tiles) { return few_warps(tiles) * few_stages(tiles) * 2 * kBoxBytes + 1024; }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -68,143 +60,130 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+template <int kTiles>
 struct FewShared {
-  uint64_t full[kWarps][kStages];
+  uint64_t full[few_warps(kTiles)][few_stages(kTiles)];
   ScanShared scan;
   int fail;
 };
 
-// Last row that row r of the tile sees (-1: none; rows behind the unit's last see none).
-template <int kRows>
-__device__ __forceinline__ int last_row(const AttendParams& p, const StreamSet& set, const Cursor<kRows>& c, int r) {
-  const int t = (c.tile * kRows + r) / p.group;
-  if (c.s < set.prefixes) return c.st.pre - 1;
-  return t < c.st.n ? c.st.len - c.st.n + t : -1;
-}
-
 template <int kTiles>
-__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ AttendParams p) {
-  constexpr int kRows = 16 * kTiles;
-  constexpr int kCols = merge_cols(kTiles);
+__global__ void __launch_bounds__(few_warps(kTiles) * 32, 1) attend_kernel(const __grid_constant__ AttendParams p) {
+  constexpr int kRows = 16 * kTiles, kWarps = few_warps(kTiles), kStages = few_stages(kTiles);
+  using Cur = Cursor<kRows, kBoxTokens>;
   if (!p.late_wait) pdl_wait();
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ FewShared sh;
+  __shared__ FewShared<kTiles> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  unsigned char* ring = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  unsigned char* qs = ring + kRingBytes;
-  float* red = reinterpret_cast<float*>(qs + kRows * kQPitch);          // [warp][row][kCols + 4]
-  float2* red_ml = reinterpret_cast<float2*>(red + kWarps * kRows * (kCols + 4));
-  const StreamSet& set = p.set;
+  const uint32_t ring = ((tc::smem_u32(smem_raw) + 1023) & ~1023u) + warp * kStages * 2 * kBoxBytes;
+  const WorkSet& set = p.set;
+  const int blocks = set.blocks();
 
   if (tid < kWarps * kStages) tc::mbar_init(&sh.full[tid / kStages][tid % kStages], 1);
   if (tid == 0) sh.fail = 0;
-  Cursor<kRows> cur;
-  const int count = find_share<kRows, kThreads>(p, set, sh.scan, cur);
+  const Shares shares = find_shares<kRows, kBoxTokens, kWarps * 32, kWarps>(p, set, sh.scan);
+  const int share = blockIdx.x * kWarps + warp;
+  if (share < shares.count) {
+    int left = shares.begin(share + 1) - shares.begin(share);
+    Cur cur = place<kRows, kBoxTokens>(p, set, sh.scan.e[warp], sh.scan.rest[warp]);
 
-  // Does this warp have rows to read at this step? (its box begins inside what the tile sees)
-  auto active = [&](const Cursor<kRows>& c) {
-    const int row0 = c.step * kStepTokens + kBoxTokens * warp;
-    return c.s < set.prefixes ? row0 < c.st.pre : row0 <= c.st.reach(p, c.tile);
-  };
-
-  // --- the ring: boxes are requested in the order in which they are used ---
-  const uint32_t my_ring = tc::smem_u32(ring) + warp * kStages * 2 * kBoxBytes;
-  Cursor<kRows> ahead = cur;
-  int ahead_left = count, page = 0;
-  // advance `ahead` to the next box of this warp and look its page up
-  auto seek = [&] {
-    while (ahead_left > 0 && !active(ahead)) {
-      ahead.next(p, set);
-      --ahead_left;
-    }
-    if (ahead_left > 0 && ahead.s >= set.prefixes && lane == 0)
-      page = p.table[(long long)(ahead.s - set.prefixes) * p.table_stride +
-                     ((ahead.step * kStepTokens + kBoxTokens * warp) >> p.page_shift)];
-  };
-  auto request = [&](int stage) {
-    if (ahead_left <= 0) return;
-    if (lane == 0) {
-      uint64_t* bar = &sh.full[warp][stage];
-      const uint32_t dst = my_ring + stage * 2 * kBoxBytes;
-      const int row = ahead.step * kStepTokens + kBoxTokens * warp;
-      tc::mbar_arrive_expect_tx(bar, 2 * kBoxBytes);
-      if (ahead.s < set.prefixes) {
-        tma_load_5d(dst, &p.tm_pk, 0, row, 0, ahead.h, ahead.s, bar);
-        tma_load_5d(dst + kBoxBytes, &p.tm_pv, 0, row, 0, ahead.h, ahead.s, bar);
-      } else {
-        const bool in_pool = page >= 0 && page < p.n_pages;
-        if (!in_pool) raise_device_error(p.err, kDevBadIndex);
-        const int at = in_pool ? page : p.n_pages;                 // outside: the box is zeros
-        const int y = row & ((1 << p.page_shift) - 1);
-        tma_load_5d(dst, &p.tm_k, 0, y, 0, ahead.h, at, bar);
-        tma_load_5d(dst + kBoxBytes, &p.tm_v, 0, y, 0, ahead.h, at, bar);
+    // --- the ring: boxes are requested in the order in which they are used ---
+    Cur ahead = cur;
+    int ahead_left = left, page = 0;
+    auto look_up = [&] {                          // the page of the next box to request
+      if (lane == 0 && ahead_left > 0 && ahead.k.s >= set.prefixes)
+        page = p.table[(long long)(ahead.k.s - set.prefixes) * p.table_stride + ((ahead.step * kBoxTokens) >> p.page_shift)];
+    };
+    auto request = [&](int stage) {
+      if (lane == 0) {
+        uint64_t* bar = &sh.full[warp][stage];
+        const uint32_t dst = ring + stage * 2 * kBoxBytes;
+        int row = ahead.step * kBoxTokens, plane = ahead.k.s;
+        const bool pre = ahead.k.s < set.prefixes;
+        if (!pre) {
+          if (page < 0 || page >= p.n_pages) {
+            raise_device_error(p.err, kDevBadIndex);
+            page = p.n_pages;                     // outside the pool: the box is zeros
+          }
+          plane = page;
+          row &= (1 << p.page_shift) - 1;
+        }
+        tc::mbar_arrive_expect_tx(bar, 2 * kBoxBytes);
+        tma_load_5d(dst, pre ? &p.tm_pk : &p.tm_k, 0, row, 0, ahead.h, plane, bar);
+        tma_load_5d(dst + kBoxBytes, pre ? &p.tm_pv : &p.tm_v, 0, row, 0, ahead.h, plane, bar);
       }
-    }
-    ahead.next(p, set);
-    --ahead_left;
-    seek();
-  };
-  int waited = 0, requested = 0;
-  seek();
-  for (int i = 0; i < kStages - 1; ++i)
-    if (ahead_left > 0) request(requested++ % kStages);
+      if (--ahead_left > 0 && ++ahead.step == ahead.k.steps) ahead.next_unit(p, set, blocks);
+      look_up();
+    };
+    look_up();
+    int requested = 0, flying = 0;                // the stage that the next request takes; boxes in the ring
+    for (; requested < kStages - 1 && ahead_left > 0; ++requested, ++flying) request(requested);
 
-  bool dead = false;
-  uint32_t q[kTiles][8][4];
-  float o[kTiles][16][4], mx[kTiles][2], sum[kTiles][2];
-  int last[kTiles][2], low = 0;                   // each row's last visible row; the tile's lowest
-  bool fresh = true;
+    // addresses of this lane's rows for ldmatrix: 16-byte chunk j of a row sits at j ^ (row % 8), so a
+    // chunk's address is the lane's own xor 16 j (and 2 KB on for the second half)
+    const uint32_t k_at = tc::sw128_offset((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1, kBoxTokens);
+    const uint32_t v_at = kBoxBytes + tc::sw128_offset(lane & 15, lane >> 4, kBoxTokens);
+    int stage = 0;
+    uint32_t parity = 0;
+    bool dead = false;
 
-  for (int i = 0; i < count; ++i) {
-    if (fresh) {                                  // a new unit: its queries
-      fresh = false;
-      for (int e = tid; e < kRows * 16; e += kThreads) {
-        const int r = e >> 4, c = e & 15;
-        const QueryRow qr = query_row(p, set, cur, r);
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (qr.real)
-          x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)qr.b * p.qb +
-                                              (long long)qr.hq * p.qh + (long long)qr.t * p.qm + c * 8);
-        *reinterpret_cast<uint4*>(qs + r * kQPitch + c * 16) = x;
-      }
-      __syncthreads();
-      low = last_row(p, set, cur, 0);
+    while (left > 0) {
+      const int boxes = min(cur.k.steps - cur.step, left);
+      const bool own = cur.k.s >= set.prefixes;
+      // this lane's queries (rows lane / 4 and 8 on of each tile) and the last row each sees
+      uint32_t q[kTiles][8][4];
+      float o[kTiles][16][4], mx[kTiles][2], sum[kTiles][2];
+      int last[kTiles][2];
 #pragma unroll
-      for (int x = 0; x < kTiles; ++x) {
+      for (int x = 0; x < kTiles; ++x)
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
-          ldsm4(tc::smem_u32(qs) + (16 * x + (lane & 15)) * kQPitch + s * 32 + (lane >> 4) * 16, q[x][s]);
+        for (int k = 0; k < 2; ++k) {
+          const QueryRow r = query_row<kRows>(p, set, cur.k, 16 * x + (lane >> 2) + 8 * k);
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)r.b * p.qb +
+                                                                  (long long)(cur.h * p.group + r.g) * p.qh +
+                                                                  (long long)r.t * p.qm) + (lane & 3);
+#pragma unroll
+          for (int s = 0; s < 8; ++s) {
+            q[x][s][k] = r.real ? src[8 * s] : 0u;
+            q[x][s][2 + k] = r.real ? src[8 * s + 4] : 0u;
+          }
+          last[x][k] = !own ? cur.k.pre - 1 : r.real ? cur.k.len - cur.k.n + r.t : -1;
+          mx[x][k] = -INFINITY;
+          sum[x][k] = 0.f;
+        }
+#pragma unroll
+      for (int x = 0; x < kTiles; ++x)
 #pragma unroll
         for (int j = 0; j < 16; ++j)
 #pragma unroll
           for (int k = 0; k < 4; ++k) o[x][j][k] = 0.f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          mx[x][k] = -INFINITY;
-          sum[x][k] = 0.f;
-          last[x][k] = last_row(p, set, cur, 16 * x + (lane >> 2) + 8 * k);
-        }
-      }
-    }
+      const int low = __shfl_sync(0xffffffffu, last[0][0], 0);     // the first row's: the lowest
 
-    if (active(cur)) {
-      const int stage = waited % kStages;
-      // the next box goes where the last one was: every lane has read it
-      __syncwarp();
-      if (ahead_left > 0 && !dead) request(requested++ % kStages);
-      if (!dead) {
-        const bool ok = wait_phase(&sh.full[warp][stage], (uint32_t)((waited / kStages) & 1), &sh.fail, p.err);
-        if (!__all_sync(0xffffffffu, ok)) {
-          // copies in flight must land before this CTA may end
-          for (int w = waited; w < requested; ++w)
-            drain_phase(&sh.full[warp][w % kStages], (uint32_t)((w / kStages) & 1), p.err);
-          dead = true;
+      for (int i = 0; i < boxes; ++i) {
+        __syncwarp();                             // every lane has read the box that the next one replaces
+        if (ahead_left > 0 && !dead) {
+          request(requested);
+          requested = requested == kStages - 1 ? 0 : requested + 1;
+          ++flying;
         }
-      }
-      ++waited;
-      if (!dead) {
-        const uint32_t kb = my_ring + stage * 2 * kBoxBytes, vb = kb + kBoxBytes;
-        const int row0 = cur.step * kStepTokens + kBoxTokens * warp;
+        if (!dead) {
+          const bool ok = wait_phase(&sh.full[warp][stage], parity, &sh.fail, p.err);
+          if (!__all_sync(0xffffffffu, ok)) {
+            // the copies in flight must land before this CTA may end
+            for (int w = 0, s = stage; w < flying; ++w) {
+              drain_phase(&sh.full[warp][s], s >= stage ? parity : parity ^ 1, p.err);
+              s = s == kStages - 1 ? 0 : s + 1;
+            }
+            dead = true;
+          }
+        }
+        const uint32_t kb = ring + stage * 2 * kBoxBytes;
+        if (++stage == kStages) stage = 0, parity ^= 1;
+        --flying;
+        const int row0 = (cur.step + i) * kBoxTokens;
+        if (dead) continue;
+
         const bool full = row0 + kBoxTokens - 1 <= low;            // every query sees every row
         float z[kTiles][2][4];
 #pragma unroll
@@ -216,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
           uint32_t k4[4];
-          ldsm4(kb + tc::sw128_offset((lane & 7) + ((lane >> 4) << 3), 2 * s + ((lane >> 3) & 1), kBoxTokens), k4);
+          ldsm4(((kb + k_at) ^ ((s & 3) * 32)) + (s >> 2) * (kBoxTokens * 128), k4);
 #pragma unroll
           for (int x = 0; x < kTiles; ++x) {
             mma16816(z[x][0], q[x][s], k4[0], k4[1]);
@@ -236,16 +215,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
               z[x][j][k] = v;
               rm[k >> 1] = fmaxf(rm[k >> 1], v);
             }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            rm[k] = fmaxf(rm[k], __shfl_xor_sync(0xffffffffu, rm[k], 1));
-            rm[k] = fmaxf(rm[k], __shfl_xor_sync(0xffffffffu, rm[k], 2));
-          }
-          const bool up = rm[0] > mx[x][0] || rm[1] > mx[x][1];
-          if (__any_sync(0xffffffffu, up)) {
+          // the running maximum moves only when a logit passes it (it needs not be the lane's own)
+          if (__any_sync(0xffffffffu, rm[0] > mx[x][0] || rm[1] > mx[x][1])) {
             float f[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
+              rm[k] = fmaxf(rm[k], __shfl_xor_sync(0xffffffffu, rm[k], 1));
+              rm[k] = fmaxf(rm[k], __shfl_xor_sync(0xffffffffu, rm[k], 2));
               const float nm = fmaxf(mx[x][k], rm[k]);
               f[k] = weight_of(mx[x][k], nm);
               mx[x][k] = nm;
@@ -278,28 +254,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           }
         }
         // V of rows behind the stream's end may hold anything: zeros in its place
-        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu, bad = 0;
         if (!full) {
-          const int r0 = row0 + 2 * (lane & 3), end = cur.s < set.prefixes ? cur.st.pre : cur.st.len;
+          const int r0 = row0 + 2 * (lane & 3), end = own ? cur.k.len : cur.k.pre;
           auto mask = [&](int r) { return (r < end ? 0xffffu : 0u) | (r + 1 < end ? 0xffff0000u : 0u); };
           keep0 = mask(r0);
           keep1 = mask(r0 + 8);
-        }
-        const int vrow = lane & 15, vchunk = lane >> 4;
-        uint32_t bad = 0;                         // tokens of the box whose V holds an infinity or NaN
-        if (!full && p.m > 1 && cur.s >= set.prefixes) {
-          // A query that does not see such a row gives it weight 0, but 0 * infinity is not 0: the
-          // products leave these rows out, and the queries that see them take them afterwards.
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint32_t v4[4];
-            ldsm4_t(vb + tc::sw128_offset(vrow, 2 * j + vchunk, kBoxTokens), v4);
-            const uint32_t odd0 = nonfinite2(v4[0] & keep0) | nonfinite2(v4[2] & keep0);
-            const uint32_t odd1 = nonfinite2(v4[1] & keep1) | nonfinite2(v4[3] & keep1);
-            bad |= (odd0 | odd1 << 8) << (2 * (lane & 3));
-          }
-          bad = __reduce_or_sync(0xffffffffu, bad);
-          if (bad) {
+          if (p.m > 1 && own) {
+            // A query that does not see a row gives it weight 0, but 0 * infinity is not 0: the
+            // products leave rows with infinities or NaN out (`bad`), and the queries that see them
+            // take them afterwards.
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+              uint32_t v4[4];
+              ldsm4_t(((kb + v_at) ^ ((j & 3) * 32)) + (j >> 2) * (kBoxTokens * 128), v4);
+              const uint32_t odd0 = nonfinite2(v4[0] & keep0) | nonfinite2(v4[2] & keep0);
+              const uint32_t odd1 = nonfinite2(v4[1] & keep1) | nonfinite2(v4[3] & keep1);
+              bad |= (odd0 | odd1 << 8) << (2 * (lane & 3));
+            }
+            bad = __reduce_or_sync(0xffffffffu, bad);
             auto drop = [&](uint32_t two) { return (two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u); };
             keep0 &= ~drop(bad >> (2 * (lane & 3)));
             keep1 &= ~drop(bad >> (2 * (lane & 3) + 8));
@@ -308,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           uint32_t v4[4];
-          ldsm4_t(vb + tc::sw128_offset(vrow, 2 * j + vchunk, kBoxTokens), v4);
+          ldsm4_t(((kb + v_at) ^ ((j & 3) * 32)) + (j >> 2) * (kBoxTokens * 128), v4);
           if (!full) v4[0] &= keep0, v4[1] &= keep1, v4[2] &= keep0, v4[3] &= keep1;
 #pragma unroll
           for (int x = 0; x < kTiles; ++x) {
@@ -318,34 +291,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             mma16816(o[x][2 * j + 1], lo[x], v4[2], v4[3]);
           }
         }
-        if (bad) {
+#pragma unroll 1
+        for (; bad; bad &= bad - 1) {             // rare
+          const int k = __ffs(bad) - 1, from = (lane & 28) | ((k & 7) >> 1);
 #pragma unroll
-          for (int k = 0; k < kBoxTokens; ++k) {
-            if (!(bad >> k & 1)) continue;
-            const int from = (lane & 28) | ((k & 7) >> 1);
+          for (int x = 0; x < kTiles; ++x) {
+            const float a0 = k & 1 ? z[x][0][1] : z[x][0][0], a1 = k & 1 ? z[x][1][1] : z[x][1][0];
+            const float b0 = k & 1 ? z[x][0][3] : z[x][0][2], b1 = k & 1 ? z[x][1][3] : z[x][1][2];
+            const float w0 = __shfl_sync(0xffffffffu, k & 8 ? a1 : a0, from);
+            const float w1 = __shfl_sync(0xffffffffu, k & 8 ? b1 : b0, from);
+            const bool s0 = row0 + k <= last[x][0], s1 = row0 + k <= last[x][1];
 #pragma unroll
-            for (int x = 0; x < kTiles; ++x) {
-              const float w0 = __shfl_sync(0xffffffffu, z[x][k >> 3][k & 1], from);
-              const float w1 = __shfl_sync(0xffffffffu, z[x][k >> 3][2 + (k & 1)], from);
-              const bool s0 = row0 + k <= last[x][0], s1 = row0 + k <= last[x][1];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                uint32_t v;
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v)
-                             : "r"(vb + tc::sw128_offset(k, j, kBoxTokens) + 4 * (lane & 3)) : "memory");
-                const float v0 = __uint_as_float(v << 16), v1 = __uint_as_float(v & 0xffff0000u);
-                if (s0) o[x][j][0] += w0 * v0, o[x][j][1] += w0 * v1;
-                if (s1) o[x][j][2] += w1 * v0, o[x][j][3] += w1 * v1;
-              }
+            for (int j = 0; j < 16; ++j) {
+              uint32_t v;
+              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v)
+                           : "r"(kb + kBoxBytes + tc::sw128_offset(k, j, kBoxTokens) + 4 * (lane & 3)) : "memory");
+              const float v0 = __uint_as_float(v << 16), v1 = __uint_as_float(v & 0xffff0000u);
+              if (s0) o[x][j][0] += w0 * v0, o[x][j][1] += w0 * v1;
+              if (s1) o[x][j][2] += w1 * v0, o[x][j][3] += w1 * v1;
             }
           }
         }
       }
-    }
 
-    // --- the CTA leaves the unit: the warps' results meet ---
-    if (cur.step == cur.steps - 1 || i == count - 1) {
-      const long long slot = cur.unit + blockIdx.x;
+      // --- the share leaves the unit: its part of the result ---
+      const size_t slot = (size_t)(cur.unit + share) * kRows;
+      const int rows = min(kRows, cur.k.n * p.group - cur.k.tile * kRows);
 #pragma unroll
       for (int x = 0; x < kTiles; ++x)
 #pragma unroll
@@ -353,53 +324,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           float t = sum[x][k];
           t += __shfl_xor_sync(0xffffffffu, t, 1);
           t += __shfl_xor_sync(0xffffffffu, t, 2);
-          if ((lane & 3) == 0) red_ml[warp * kRows + 16 * x + (lane >> 2) + 8 * k] = make_float2(mx[x][k], t);
-        }
-      __syncthreads();
-      float f[kTiles][2];
+          const int r = 16 * x + (lane >> 2) + 8 * k;
+          if (r < rows) {
+            if ((lane & 3) == 0) set.part_ml[slot + r] = make_float2(mx[x][k], t);
+            float2* dst = reinterpret_cast<float2*>(set.part_o + (slot + r) * kHeadDim) + (lane & 3);
 #pragma unroll
-      for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float top = -INFINITY;
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red_ml[w * kRows + 16 * x + (lane >> 2) + 8 * k].x);
-          f[x][k] = weight_of(mx[x][k], top);
-        }
-      if (tid < kRows) {
-        float top = -INFINITY, t = 0.f;
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red_ml[w * kRows + tid].x);
-        for (int w = 0; w < kWarps; ++w) t += red_ml[w * kRows + tid].y * weight_of(red_ml[w * kRows + tid].x, top);
-        set.part_ml[slot * kRows + tid] = make_float2(top, t);
-      }
-#pragma unroll
-      for (int c = 0; c < kHeadDim / kCols; ++c) {
-#pragma unroll
-        for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-          for (int j = 0; j < kCols / 8; ++j) {
-            const float* v = o[x][c * (kCols / 8) + j];
-            float* d = red + (warp * kRows + 16 * x + (lane >> 2)) * (kCols + 4) + 8 * j + 2 * (lane & 3);
-            *reinterpret_cast<float2*>(d) = make_float2(v[0] * f[x][0], v[1] * f[x][0]);
-            *reinterpret_cast<float2*>(d + 8 * (kCols + 4)) = make_float2(v[2] * f[x][1], v[3] * f[x][1]);
+            for (int j = 0; j < 16; ++j) dst[4 * j] = make_float2(o[x][j][2 * k], o[x][j][2 * k + 1]);
           }
-        __syncthreads();
-#pragma unroll
-        for (int e = tid; e < kRows * kCols / 2; e += kThreads) {
-          const int r = e / (kCols / 2), cc = 2 * (e % (kCols / 2));
-          float2 a = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float2 y = *reinterpret_cast<const float2*>(red + (w * kRows + r) * (kCols + 4) + cc);
-            a.x += y.x;
-            a.y += y.y;
-          }
-          *reinterpret_cast<float2*>(set.part_o + (slot * kRows + r) * kHeadDim + c * kCols + cc) = a;
         }
-        __syncthreads();
-      }
-      fresh = true;
+      left -= boxes;
+      if (left > 0) cur.next_unit(p, set, blocks);
     }
-    cur.next(p, set);
   }
   if (p.late_wait) pdl_wait();
 }
@@ -409,32 +344,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 struct Parts {
   const float2* ml;
   const float* o;
-  long long slot;
-  int count, rows, row, twice;
-  __device__ long long at(int k) const {
-    return twice ? (slot + (k >> 1)) * rows + row + (k & 1) * 128 : (slot + k) * rows + row;
-  }
+  int slot, count, rows, row, twice;
+  __device__ size_t at(int k) const { return (size_t)(slot + (k >> twice)) * rows + row + (twice ? (k & 1) * 128 : 0); }
   __device__ int parts() const { return count << twice; }
 };
 
-// Row r of stream s and head h.
+// Row r of block e (its tile) and head h.
 template <int kRows>
-__device__ __forceinline__ Parts find_parts(const AttendParams& p, const StreamSet& set, int s, int h, long long r) {
-  Stream<kRows> st;
-  st.load(p, set, s);
-  const int tile = (int)(r / kRows);
-  const int steps = st.steps(p, set, tile);
-  if (steps == 0) return Parts{nullptr, nullptr, 0, 0, kRows, 0, 0};
-  const long long total = set.step_base[set.prefixes + set.own];
-  const long long ctas = total < set.ctas ? total : set.ctas;
-  long long g = set.step_base[s] + (long long)h * st.head_work(p, set);
-  if (st.len == 0) g += (long long)tile * steps;
-  else
-    for (int i = 0; i < tile; ++i) g += st.steps(p, set, i);
-  const int c0 = (int)(((g + 1) * ctas - 1) / total), c1 = (int)(((g + steps) * ctas - 1) / total);
-  const bool twice = kRows == kWideRows && (long long)st.n * p.group - (long long)tile * kRows <= 128;
-  return Parts{set.part_ml, set.part_o, set.unit_base[s] + (long long)h * st.tiles + tile + c0, c1 - c0 + 1, kRows,
-               (int)(r % kRows), twice};
+__device__ __forceinline__ Parts find_parts(const AttendParams& p, const WorkSet& set, int e, int h, int r, int block_rows) {
+  const int g0 = set.base[e], steps = (set.base[e + 1] - g0) / p.hkv;
+  const Shares shares(set, set.base[set.blocks()]);
+  const int g = g0 + h * steps;
+  const int c0 = shares.of(g), c1 = shares.of(g + steps - 1);
+  return Parts{set.part_ml, set.part_o, e * p.hkv + h + c0, c1 - c0 + 1, kRows, r, kRows == kWideRows && block_rows <= 128};
 }
 
 constexpr int kJoinWarps = 8;
@@ -453,7 +375,7 @@ __device__ __forceinline__ void join_row(const AttendParams& p, const Parts* par
     const int n = parts[x].parts();
 #pragma unroll 4
     for (int k = 0; k < n; ++k) {
-      const long long at = parts[x].at(k);
+      const size_t at = parts[x].at(k);
       const float2 ml = parts[x].ml[at];
       const float4 v = reinterpret_cast<const float4*>(parts[x].o + at * kHeadDim)[lane];
       const float w = weight_of(ml.x, top);
@@ -476,69 +398,64 @@ __device__ __forceinline__ void join_row(const AttendParams& p, const Parts* par
 template <int kRows>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const __grid_constant__ AttendParams p) {
   pdl_wait();
-  const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= (long long)p.batch * p.hq * p.m) return;
-  const int t = (int)(row % p.m), hq = (int)(row / p.m % p.hq), b = (int)(row / p.m / p.hq);
+  const int row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+  if (row >= p.batch * p.hq * p.m) return;
+  const int bh = row / p.m, t = row - bh * p.m, b = bh / p.hq, hq = bh - b * p.hq;
   const Seq q = sequence(p, b, !p.pages && t == 0 && hq == 0 && (threadIdx.x & 31) == 0);
   if (t >= q.n) return;
   const int h = hq / p.group, g = hq - h * p.group;
   Parts parts[2];
   int np = 0;
   if (p.fan) {
-    const int s = b / p.fan;
-    const long long r = (long long)(tokens_before(p, b) - tokens_before(p, s * p.fan) + t) * p.group + g;
-    if (p.wide.prefixes) parts[np++] = find_parts<kWideRows>(p, p.wide, s, h, r);
-    else parts[np++] = find_parts<kRows>(p, p.set, s, h, r);
+    const int s = b / p.fan, before = tokens_before(p, s * p.fan);
+    const int r = (tokens_before(p, b) - before + t) * p.group + g, all = (tokens_before(p, (s + 1) * p.fan) - before) * p.group;
+    if (p.wide.prefixes) {
+      const int tile = r / kWideRows;
+      parts[np++] = find_parts<kWideRows>(p, p.wide, s * p.wide.prefix_tiles + tile, h, r % kWideRows, all - tile * kWideRows);
+    } else {
+      parts[np++] = find_parts<kRows>(p, p.set, s * p.set.prefix_tiles + r / kRows, h, r % kRows, 0);
+    }
   }
   if (q.len - q.n + t >= 0 && q.len > 0) {
-    const long long r = (long long)t * p.group + g;
-    if (p.wide.own) parts[np++] = find_parts<kWideRows>(p, p.wide, p.wide.prefixes + b, h, r);
-    else parts[np++] = find_parts<kRows>(p, p.set, p.set.prefixes + b, h, r);
+    const int r = t * p.group + g;
+    if (p.wide.seqs)                              // at most 128 rows of a sequence: one tile
+      parts[np++] = find_parts<kWideRows>(p, p.wide, p.wide.prefixes * p.wide.prefix_tiles + b, h, r, q.n * p.group);
+    else
+      parts[np++] = find_parts<kRows>(p, p.set, p.set.prefixes * p.set.prefix_tiles + b * p.set.seq_tiles + r / kRows, h,
+                                      r % kRows, 0);
   }
   join_row(p, parts, np, b, t, hq, np > 0);
 }
 
 // Joint units: only those that two or more CTAs share have parts to merge. Block (c, y) takes 32 rows of
-// the unit that CTA c + 1 begins inside, where that is the first CTA to begin inside it.
+// the unit that share c + 1 begins inside, where that is the first share to begin inside it.
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_split_kernel(const __grid_constant__ AttendParams p) {
   pdl_wait();
-  const StreamSet& set = p.wide;
-  const int streams = set.prefixes + set.own;
-  const long long total = set.step_base[streams];
-  const long long ctas = total < set.ctas ? total : set.ctas;
+  const WorkSet& set = p.wide;
+  const int blocks = set.blocks();
+  const Shares shares(set, set.base[blocks]);
   const int c = blockIdx.x + 1;
-  if (c >= ctas) return;
-  const long long begin = total * c / ctas;
-  int lo = 0, hi = streams;                       // the last stream that begins at or before this step
+  if (c >= shares.count) return;
+  const int begin = shares.begin(c);
+  int lo = 0, hi = blocks;                        // the last block that begins at or before this step
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (set.step_base[mid] <= begin) lo = mid;
+    if (set.base[mid] <= begin) lo = mid;
     else hi = mid;
   }
-  Cursor<kWideRows> cur;
-  cur.s = lo;
-  cur.st.load(p, set, lo);
-  const long long per_head = cur.st.head_work(p, set);
-  long long r = begin - set.step_base[lo];
-  cur.h = (int)(r / per_head);
-  r -= cur.h * per_head;
-  for (cur.tile = 0;; ++cur.tile) {
-    cur.steps = cur.st.steps(p, set, cur.tile);
-    if (r < cur.steps) break;
-    r -= cur.steps;
-  }
-  if (r == 0) return;                             // CTA c begins with the unit
-  const long long first = begin - r;              // the unit's first step
-  if (c > 1 && total * (c - 1) / ctas > first) return;
-  const int c1 = (int)(((first + cur.steps) * ctas - 1) / total);
-  const Parts part = {set.part_ml, set.part_o, set.unit_base[lo] + (long long)cur.h * cur.st.tiles + cur.tile + c - 1,
-                      c1 - (c - 1) + 1, kWideRows, 0, 0};
+  Block k;
+  load_block<kWideRows, kWideTokens>(p, set, lo, k);
+  const int h = (begin - set.base[lo]) / k.steps, r = begin - set.base[lo] - h * k.steps;
+  if (r == 0) return;                             // the share begins with the unit
+  const int first = begin - r;                    // the unit's first step
+  if (c > 1 && shares.begin(c - 1) > first) return;
+  const int c1 = shares.of(first + k.steps - 1);
+  Parts part = {set.part_ml, set.part_o, lo * p.hkv + h + c - 1, c1 - (c - 1) + 1, kWideRows, 0, 0};
   for (int i = threadIdx.x >> 5; i < 32; i += kJoinWarps) {
-    Parts one = part;
-    one.row = blockIdx.y * 32 + i;
-    const QueryRow q = query_row(p, set, cur, one.row);
+    part.row = blockIdx.y * 32 + i;
+    const QueryRow q = query_row<kWideRows>(p, set, k, part.row);
     if (!q.real) continue;
-    join_row(p, &one, 1, q.b, q.t, q.hq, cur.st.pre > 0 || cur.st.len - cur.st.n + q.t >= 0);
+    join_row(p, &part, 1, q.b, q.t, h * p.group + q.g, k.pre > 0 || k.len - k.n + q.t >= 0);
   }
 }
 
@@ -563,35 +480,36 @@ size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Plan {
   int few_tiles;            // query tiles of 16 rows of a unit of the few-row kernel
-  StreamSet few, wide;      // counts, and offsets into the workspace in place of pointers
+  int sms;
+  WorkSet few, wide;        // counts, and offsets into the workspace in place of pointers
   size_t bytes;
-  bool runs(const StreamSet& s) const { return s.prefixes + s.own > 0; }
 };
 
-// Room for a kernel's streams and partial results; sets the set's pointers (from a null base).
-void lay_out(StreamSet& s, long long units, int rows, size_t& off) {
-  const long long streams = s.prefixes + s.own, slots = units + s.ctas;
+// Room for a kernel's blocks and partial results; sets the set's pointers (from a null base).
+void lay_out(WorkSet& s, int kv_heads, int rows, size_t& off) {
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off += round256(bytes);
     return at;
   };
-  if (!streams) return;
-  s.step_base = reinterpret_cast<long long*>(take((size_t)(streams + 1) * 8));
-  s.unit_base = reinterpret_cast<long long*>(take((size_t)streams * 8));
-  s.part_ml = reinterpret_cast<float2*>(take((size_t)slots * rows * sizeof(float2)));
-  s.part_o = reinterpret_cast<float*>(take((size_t)slots * rows * kHeadDim * sizeof(float)));
+  if (s.blocks() == 0) return;
+  const size_t slots = (size_t)s.blocks() * kv_heads + s.max_shares;
+  s.base = reinterpret_cast<int*>(take((size_t)(s.blocks() + 1) * sizeof(int)));
+  s.part_ml = reinterpret_cast<float2*>(take(slots * rows * sizeof(float2)));
+  s.part_o = reinterpret_cast<float*>(take(slots * rows * kHeadDim * sizeof(float)));
 }
 template <typename T>
 void rebase(T*& x, char* base) { x = reinterpret_cast<T*>(base + reinterpret_cast<size_t>(x)); }
-void rebase(StreamSet& s, char* base) {
-  rebase(s.step_base, base);
-  rebase(s.unit_base, base);
+void rebase(WorkSet& s, char* base) {
+  rebase(s.base, base);
   rebase(s.part_ml, base);
   rebase(s.part_o, base);
 }
 
 constexpr size_t kWorkHead = 256;                 // an error word, for callers without one
+// Boxes that a share of the few-row kernel has at least: fewer would leave more partial results to
+// merge than rows to read.
+constexpr int kFewMinBoxes = 4;
 
 // Sizes alone decide: lens and n_new are the device's.
 int make_plan(const evict_attention* a, Plan* out) {
@@ -601,8 +519,8 @@ int make_plan(const evict_attention* a, Plan* out) {
     return fail(EVICT_EINVAL, "n_q_heads (%d) must be a multiple of n_kv_heads (%d)", a->n_q_heads, a->n_kv_heads);
   if (a->batch > EVICT_MAX_ATTEND_BATCH)
     return fail(EVICT_ELIMIT, "batch %d is above %d", a->batch, EVICT_MAX_ATTEND_BATCH);
-  if ((long long)a->batch * a->m >= (1ll << 31) || (long long)a->batch * a->m * a->n_q_heads >= (1ll << 31))
-    return fail(EVICT_ELIMIT, "batch * n_q_heads * m is 2^31 or more");
+  if ((long long)a->batch * a->m >= (1ll << 30) || (long long)a->batch * a->m * a->n_q_heads >= (1ll << 30))
+    return fail(EVICT_ELIMIT, "batch * n_q_heads * m is 2^30 or more");
   if (a->n_prefix < 0 || a->n_prefix > (1 << 30)) return fail(EVICT_EINVAL, "n_prefix must be in [0, 2^30]");
   if (a->n_prefix > 0 && (a->prefix_batch < 1 || a->batch % a->prefix_batch))
     return fail(EVICT_EINVAL, "prefix_batch (%d) must divide batch (%d)", a->prefix_batch, a->batch);
@@ -611,33 +529,44 @@ int make_plan(const evict_attention* a, Plan* out) {
   if (a->batch == 0 || a->m == 0) return EVICT_OK;
   const int group = a->n_q_heads / a->n_kv_heads;
   const bool pre = a->n_prefix > 0;
-  int dev = 0, ctas = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&ctas, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return cuda_fail(e, "looking up the device");
-  P.few.ctas = P.wide.ctas = ctas;
 
   // Which kernel takes a unit goes by its query rows, the wide one from kWideFrom on. Sequences of
   // more than kJointFrom rows fill a wide unit by themselves: their units take the prefix along
   // (no partial results to merge); below that, rows of several sequences share the prefix's units.
-  const long long own_rows = (long long)a->m * group, pre_rows = pre ? own_rows * (a->batch / a->prefix_batch) : 0;
+  const int own_rows = a->m * group, pre_rows = pre ? own_rows * (a->batch / a->prefix_batch) : 0;
   if (own_rows > kJointFrom && (pre || a->pages)) {
     P.wide.joint = 1;
-    P.wide.own = a->batch;
+    P.wide.seqs = a->batch;
   } else {
     if (pre) (pre_rows >= kWideFrom ? P.wide : P.few).prefixes = a->prefix_batch;
-    if (a->pages) (own_rows >= kWideFrom ? P.wide : P.few).own = a->batch;
+    if (a->pages) (own_rows >= kWideFrom ? P.wide : P.few).seqs = a->batch;
   }
-  const long long few_rows = std::max(P.few.prefixes ? pre_rows : 0, P.few.own ? own_rows : 0);
+  const int few_rows = std::max(P.few.prefixes ? pre_rows : 0, P.few.seqs ? own_rows : 0);
   // One tile of 16 query rows where that holds every row; two (each box of K and V then serves
   // twice the rows) otherwise.
   P.few_tiles = few_rows <= 16 ? 1 : 2;
-  auto units = [&](const StreamSet& s, int rows) {
-    return (s.prefixes * ((pre_rows + rows - 1) / rows) + s.own * ((own_rows + rows - 1) / rows)) * a->n_kv_heads;
+  const long long seq_tokens = a->pages ? (long long)a->pages->table_width * a->pages->page_size : 0;
+  auto tiles = [&](WorkSet& s, int rows, int tokens) {
+    s.prefix_tiles = (pre_rows + rows - 1) / rows;
+    s.seq_tiles = (own_rows + rows - 1) / rows;
+    const long long pre_steps = (a->n_prefix + tokens - 1) / tokens, seq_steps = (seq_tokens + tokens - 1) / tokens + 1;
+    const long long work = ((long long)s.prefixes * s.prefix_tiles * pre_steps +
+                            (long long)s.seqs * s.seq_tiles * (seq_steps + (s.joint ? pre_steps : 0))) * a->n_kv_heads;
+    return work < (1ll << 31) && ((long long)s.blocks() + 1) * a->n_kv_heads < (1ll << 30);
   };
+  if (!tiles(P.few, 16 * P.few_tiles, kBoxTokens) || !tiles(P.wide, kWideRows, kWideTokens))
+    return fail(EVICT_ELIMIT, "the batch's heads and rows (to the tables' width) are too many for one call");
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P.sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "looking up the device");
+  P.few.max_shares = P.sms * few_warps(P.few_tiles);
+  P.few.min_steps = kFewMinBoxes;
+  P.wide.max_shares = P.sms;
+  P.wide.min_steps = 1;
   size_t off = kWorkHead + round256((size_t)(a->batch + 1) * sizeof(int));
-  lay_out(P.few, units(P.few, 16 * P.few_tiles), 16 * P.few_tiles, off);
-  lay_out(P.wide, units(P.wide, kWideRows), kWideRows, off);
+  lay_out(P.few, a->n_kv_heads, 16 * P.few_tiles, off);
+  lay_out(P.wide, a->n_kv_heads, kWideRows, off);
   P.bytes = off;
   return EVICT_OK;
 }
@@ -727,18 +656,18 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
     P.page_stride = g->page_stride ? g->page_stride : (long long)g->n_kv_heads * g->page_size * kHeadDim;
   }
   // The boxes of one of the kernels: 16 whole rows, or up to 128 rows of one half.
-  auto encode = [&](bool wide, const StreamSet& s) {
+  auto encode = [&](bool wide, const WorkSet& s) {
     if (s.prefixes || (s.joint && P.fan)) {
       // a dimension of extent 1 is never stepped over, but its stride still has to be one the encoder takes
       const long long hs = P.hkv > 1 ? a->prefix_stride_h : (long long)P.n_prefix * kHeadDim;
       const long long bs = P.prefix_batch > 1 ? a->prefix_stride_b : P.hkv * hs;
       for (int v = 0; v < 2; ++v)
         if (!encode_boxes(v ? &P.tm_pv : &P.tm_pk, v ? a->prefix_v : a->prefix_k, P.n_prefix, P.hkv, hs, P.prefix_batch, bs,
-                          wide ? kStepTokens : kBoxTokens, wide ? 1 : 2))
+                          wide ? kWideTokens : kBoxTokens, wide ? 1 : 2))
           return fail(EVICT_EINVAL, "the prefix has sizes or strides beyond a tensor map's");
     }
-    if (s.own && g) {
-      P.box_rows = std::min(g->page_size, kStepTokens);
+    if (s.seqs && g) {
+      P.box_rows = std::min(g->page_size, kWideTokens);
       for (int v = 0; v < 2; ++v)
         if (!encode_boxes(v ? &P.tm_v : &P.tm_k, v ? g->v : g->k, g->page_size, P.hkv, (long long)g->page_size * kHeadDim,
                           g->n_pages, P.page_stride, wide ? P.box_rows : kBoxTokens, wide ? 1 : 2))
@@ -748,11 +677,11 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
   };
   cudaStream_t st = static_cast<cudaStream_t>(a->stream);
   cudaError_t e = cudaSuccess;
-  const bool few = plan.runs(plan.few), wide = plan.runs(plan.wide);
+  const bool few = plan.few.blocks() > 0, wide = plan.wide.blocks() > 0;
   if (wide) {
     if ((rc = encode(true, plan.wide))) return rc;
     P.set = plan.wide;
-    if ((e = prepare_wide()) != cudaSuccess || (e = launch_wide(P, few, st)) != cudaSuccess)
+    if ((e = prepare_wide()) != cudaSuccess || (e = launch_wide(P, plan.sms, few, st)) != cudaSuccess)
       return cuda_fail(e, "wide attention kernel launch");
     g_launches.fetch_add(1);
     P.late_wait = 1;                              // the few-row kernel needs nothing of the wide one's
@@ -763,15 +692,15 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
     if ((rc = encode(false, plan.few))) return rc;
     auto go = [&](auto kernel, int tiles) {
       const cudaError_t x = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem(tiles));
-      return x != cudaSuccess ? x : launch_pdl(kernel, dim3(plan.few.ctas), dim3(kThreads), few_smem(tiles), st, nullptr, P);
+      return x != cudaSuccess ? x : launch_pdl(kernel, dim3(plan.sms), dim3(few_warps(tiles) * 32), few_smem(tiles), st, nullptr, P);
     };
     e = plan.few_tiles == 1 ? go(attend_kernel<1>, 1) : go(attend_kernel<2>, 2);
     if (e != cudaSuccess) return cuda_fail(e, "attention kernel launch");
     g_launches.fetch_add(1);
   }
   if (plan.wide.joint) {
-    if (plan.wide.ctas > 1)
-      e = launch_pdl(attend_join_split_kernel, dim3(plan.wide.ctas - 1, kWideRows / 32), dim3(kJoinWarps * 32), 0, st, nullptr, P);
+    if (plan.sms > 1)
+      e = launch_pdl(attend_join_split_kernel, dim3(plan.sms - 1, kWideRows / 32), dim3(kJoinWarps * 32), 0, st, nullptr, P);
   } else {
     const long long rows = (long long)a->batch * a->n_q_heads * a->m;
     const dim3 grid((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), block(kJoinWarps * 32);

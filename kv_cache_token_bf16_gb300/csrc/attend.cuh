@@ -1,5 +1,6 @@
-// Device side of the attention kernels' schedule: streams, units, steps and
-// the share of them that a CTA takes (see attend.h).
+// Device side of the attention kernels' schedule: blocks, units, steps and the
+// share of them that a warp or CTA takes (see attend.h). Counts of steps and
+// rows fit 31 bits (the host refuses calls that might pass them).
 #pragma once
 
 #include "attend.h"
@@ -38,212 +39,207 @@ struct Seq {
 };
 __device__ __forceinline__ Seq sequence(const AttendParams& p, int b, bool report) {
   int n = p.n_new ? p.n_new[b] : p.m;
-  bool odd = n < 0 || n > p.m;
-  n = n < 0 ? 0 : n > p.m ? p.m : n;
   int len = p.pages ? p.lens[b] : 0;
   const int room = p.pages ? p.table_width << p.page_shift : 0;
-  odd = odd || len < 0 || len > room;
-  len = len < 0 ? 0 : len > room ? room : len;
-  if (odd && report) raise_device_error(p.err, kDevBadIndex);
-  return {n, len};
+  const int n1 = min(max(n, 0), p.m), len1 = min(max(len, 0), room);
+  if (report && (n1 != n || len1 != len)) raise_device_error(p.err, kDevBadIndex);
+  return {n1, len1};
 }
 // New tokens of the sequences before b. Padding is left out of a prefix's query rows.
 __device__ __forceinline__ int tokens_before(const AttendParams& p, int b) {
   return p.n_new ? p.tok_base[b] : b * p.m;
 }
 
-template <int kRows>
-struct Stream {
-  int n, pre, len, tiles;            // query tokens, prefix rows, own rows, row tiles
-  __device__ void load(const AttendParams& p, const StreamSet& set, int s, bool report = false) {
-    if (s < set.prefixes) {
-      n = tokens_before(p, (s + 1) * p.fan) - tokens_before(p, s * p.fan);
-      pre = p.n_prefix;
-      len = 0;
-    } else {
-      const Seq q = sequence(p, s - set.prefixes, report);
-      n = q.n;
-      len = q.len;
-      pre = set.joint ? p.n_prefix : 0;
-    }
-    tiles = (int)(((long long)n * p.group + kRows - 1) / kRows);
-  }
-  __device__ int pre_steps() const { return (pre + kStepTokens - 1) / kStepTokens; }
-  // Last own row that the tile's last token sees (-1: none).
-  __device__ int reach(const AttendParams& p, int tile) const {
-    if (len == 0) return -1;
-    const long long t = ((long long)kRows * (tile + 1) - 1) / p.group;
-    const int v = len - n + (int)(t < n - 1 ? t : n - 1);
-    return v < -1 ? -1 : v;
-  }
-  __device__ int steps(const AttendParams& p, const StreamSet& set, int tile) const {
-    const int k = pre_steps() + (reach(p, tile) + kStepTokens) / kStepTokens;
-    return set.joint && k == 0 ? 1 : k;            // joint units write their rows themselves: all need a step
-  }
-  __device__ long long head_work(const AttendParams& p, const StreamSet& set) const {
-    if (len == 0) return (long long)tiles * steps(p, set, 0);
-    long long w = 0;
-    for (int i = 0; i < tiles; ++i) w += steps(p, set, i);
-    return w;
-  }
+// A block: a tile of query rows of a stream.
+struct Block {
+  int s, tile;                       // prefix, or prefixes + sequence
+  int n, len;                        // query tokens of the stream; own rows
+  int pre;                           // prefix rows
+  int reach;                         // last own row that the tile's last token sees (-1: none)
+  int steps;                         // of each of its units
 };
+template <int kRows, int kTokens>
+__device__ __forceinline__ void load_block(const AttendParams& p, const WorkSet& set, int e, Block& k,
+                                           bool report = false) {
+  const int pe = set.prefixes * set.prefix_tiles;
+  if (e < pe) {
+    k.s = e / set.prefix_tiles;
+    k.tile = e - k.s * set.prefix_tiles;
+    k.n = tokens_before(p, (k.s + 1) * p.fan) - tokens_before(p, k.s * p.fan);
+    k.len = 0;
+    k.pre = p.n_prefix;
+  } else {
+    const int b = set.seq_tiles == 1 ? e - pe : (e - pe) / set.seq_tiles;
+    k.s = set.prefixes + b;
+    k.tile = e - pe - b * set.seq_tiles;
+    const Seq q = sequence(p, b, report && k.tile == 0);
+    k.n = q.n;
+    k.len = q.len;
+    k.pre = set.joint ? p.n_prefix : 0;
+  }
+  k.reach = -1;
+  k.steps = 0;
+  if (kRows * k.tile < k.n * p.group) {
+    if (k.len > 0) {
+      const int t = (kRows * (k.tile + 1) - 1) / p.group;
+      k.reach = max(-1, k.len - k.n + min(t, k.n - 1));
+    }
+    k.steps = (k.pre + kTokens - 1) / kTokens + (k.reach + kTokens) / kTokens;
+    if (set.joint) k.steps = max(k.steps, 1);     // joint units write their rows themselves: all need a step
+  }
+}
 
 // A position in the line of steps.
-template <int kRows>
+template <int kRows, int kTokens>
 struct Cursor {
-  int s, h, tile, step, steps;       // steps of the unit
-  long long unit;
-  Stream<kRows> st;
-  __device__ void next(const AttendParams& p, const StreamSet& set) {
-    if (++step < steps) return;
+  int e, h, step, unit;
+  Block k;
+  // on to the next unit
+  __device__ __forceinline__ void next_unit(const AttendParams& p, const WorkSet& set, int blocks) {
     step = 0;
-    do {
-      ++unit;
-      if (++tile >= st.tiles) {
-        tile = 0;
-        if (++h >= p.hkv) {
-          h = 0;
-          do {
-            if (++s >= set.prefixes + set.own) return;
-            st.load(p, set, s);
-          } while (st.tiles == 0);
-        }
-      }
-      steps = st.steps(p, set, tile);
-    } while (steps == 0);
+    ++unit;
+    if (++h < p.hkv) return;
+    h = 0;
+    for (;;) {
+      if (++e >= blocks) return;
+      load_block<kRows, kTokens>(p, set, e, k);
+      if (k.steps) break;
+      unit += p.hkv;
+    }
   }
 };
 
-struct ScanShared {
-  long long a[32], u[32];
-  long long begin, rest, unit, total;
-  int s;
+// Equal shares of `total` steps: the first `extra` have one step more.
+struct Shares {
+  int count, each, extra;
+  __device__ __forceinline__ Shares(const WorkSet& set, int total) {
+    count = min(set.max_shares, total / set.min_steps);
+    if (count == 0) count = total > 0 ? 1 : 0;
+    each = count ? total / count : 0;
+    extra = total - each * count;
+  }
+  __device__ __forceinline__ int begin(int i) const { return i * each + min(i, extra); }
+  __device__ __forceinline__ int of(int g) const {                 // the share that holds step g
+    const int cut = extra * (each + 1);
+    return g < cut ? g / (each + 1) : extra + (g - cut) / each;
+  }
 };
 
-// Exclusive sums of (a, u) over the block's threads, and the total of a.
+constexpr int kMaxWarps = 12;
+struct ScanShared {
+  int a[32];
+  int total;
+  int e[kMaxWarps], rest[kMaxWarps];              // where the shares of this CTA begin
+};
+
+// Exclusive sum of `a` over the block's threads, and the total.
 template <int kThreads>
-__device__ __forceinline__ void block_scan(long long& a, long long& u, long long& total, ScanShared& sh) {
+__device__ __forceinline__ int block_scan(int a, int& total, ScanShared& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long a0 = a, u0 = u;
+  int x = a;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, a, d), y = __shfl_up_sync(0xffffffffu, u, d);
-    if (lane >= d) a += x, u += y;
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
   }
-  if (lane == 31) sh.a[warp] = a, sh.u[warp] = u;
+  if (lane == 31) sh.a[warp] = x;
   __syncthreads();
   total = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) a += sh.a[w], u += sh.u[w];
+    if (w < warp) x += sh.a[w];
     total += sh.a[w];
   }
-  a -= a0;
-  u -= u0;
   __syncthreads();
+  return x - a;
 }
 
-// This CTA's share of the steps, found from the lengths on the device: `count` steps from `cur`.
-// All threads call it; CTA 0 leaves the streams' first steps and units for the join.
-template <int kRows, int kThreads>
-__device__ __forceinline__ int find_share(const AttendParams& p, const StreamSet& set, ScanShared& sh,
-                                          Cursor<kRows>& cur) {
+// Where the shares first .. first + kPer - 1 of this CTA begin, found from the lengths on the
+// device (sh.e, sh.rest; all threads call it). CTA 0 leaves the blocks' first steps for the join.
+template <int kRows, int kTokens, int kThreads, int kPer>
+__device__ __forceinline__ Shares find_shares(const AttendParams& p, const WorkSet& set, ScanShared& sh) {
   const int tid = threadIdx.x;
-  long long a, u, total;
+  int total;
   if (p.n_new && p.fan) {
     // every CTA writes the same sums, and reads back its own
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
-    a = 0;
-    u = 0;
+    int a = 0;
     for (int b = b0; b < b1; ++b) a += sequence(p, b, false).n;
-    block_scan<kThreads>(a, u, total, sh);
+    a = block_scan<kThreads>(a, total, sh);
     for (int b = b0; b < b1; ++b) {
-      p.tok_base[b] = (int)a;
+      p.tok_base[b] = a;
       a += sequence(p, b, false).n;
     }
-    if (tid == 0) p.tok_base[p.batch] = (int)total;
+    if (tid == 0) p.tok_base[p.batch] = total;
     __syncthreads();
   }
-  const int streams = set.prefixes + set.own;
-  const int per = (streams + kThreads - 1) / kThreads;
-  const int s0 = min(tid * per, streams), s1 = min(s0 + per, streams);
-  Stream<kRows> st;
-  a = 0;
-  u = 0;
-  for (int s = s0; s < s1; ++s) {
-    st.load(p, set, s, blockIdx.x == 0);
-    a += st.head_work(p, set) * p.hkv;
-    u += (long long)st.tiles * p.hkv;
+  const int blocks = set.blocks();
+  const int per = (blocks + kThreads - 1) / kThreads;
+  const int e0 = min(tid * per, blocks), e1 = min(e0 + per, blocks);
+  Block k;
+  int work = 0;
+  for (int e = e0; e < e1; ++e) {
+    load_block<kRows, kTokens>(p, set, e, k, blockIdx.x == 0);
+    work += k.steps * p.hkv;
   }
-  const long long mine_work = a;
-  block_scan<kThreads>(a, u, total, sh);
-  const long long ctas = total < set.ctas ? total : set.ctas;
-  const long long begin = ctas ? total * blockIdx.x / ctas : 0;
-  if (blockIdx.x == 0) {
-    long long x = a, y = u;
-    for (int s = s0; s < s1; ++s) {
-      st.load(p, set, s);
-      set.step_base[s] = x;
-      set.unit_base[s] = y;
-      x += st.head_work(p, set) * p.hkv;
-      y += (long long)st.tiles * p.hkv;
-    }
-    if (tid == 0) set.step_base[streams] = total;
-  }
-  if (blockIdx.x < ctas && begin >= a && begin < a + mine_work) {
-    int s = s0;
-    for (; s < s1; ++s) {
-      st.load(p, set, s);
-      const long long w = st.head_work(p, set) * p.hkv;
-      if (begin < a + w) break;
+  int a = block_scan<kThreads>(work, total, sh);
+  const Shares shares(set, total);
+  const int first = blockIdx.x * kPer;
+  const int lo = shares.begin(min(first, shares.count)), hi = shares.begin(min(first + kPer, shares.count));
+  if (blockIdx.x == 0 || (a < hi && a + work > lo)) {
+    for (int e = e0; e < e1; ++e) {
+      int w = work;
+      if (per > 1) {
+        load_block<kRows, kTokens>(p, set, e, k);
+        w = k.steps * p.hkv;
+      }
+      if (blockIdx.x == 0) set.base[e] = a;
+      for (int i = 0; i < kPer && first + i < shares.count; ++i) {
+        const int g = shares.begin(first + i);
+        if (g >= a && g < a + w) sh.e[i] = e, sh.rest[i] = g - a;
+      }
       a += w;
-      u += (long long)st.tiles * p.hkv;
     }
-    sh.s = s;
-    sh.rest = begin - a;
-    sh.unit = u;
-    sh.begin = begin;
   }
+  if (blockIdx.x == 0 && tid == 0) set.base[blocks] = total;
   __syncthreads();
-  if (blockIdx.x >= ctas) return 0;
-  cur.s = sh.s;
-  cur.st.load(p, set, cur.s);
-  const long long per_head = cur.st.head_work(p, set);
-  cur.h = (int)(sh.rest / per_head);
-  long long r = sh.rest - cur.h * per_head;
-  cur.tile = 0;
-  for (;; ++cur.tile) {
-    cur.steps = cur.st.steps(p, set, cur.tile);
-    if (r < cur.steps) break;
-    r -= cur.steps;
-  }
-  cur.step = (int)r;
-  cur.unit = sh.unit + (long long)cur.h * cur.st.tiles + cur.tile;
-  return (int)(total * (blockIdx.x + 1) / ctas - sh.begin);
+  return shares;
 }
 
-// A query row of a unit.
+template <int kRows, int kTokens>
+__device__ __forceinline__ Cursor<kRows, kTokens> place(const AttendParams& p, const WorkSet& set, int e, int rest) {
+  Cursor<kRows, kTokens> c;
+  c.e = e;
+  load_block<kRows, kTokens>(p, set, e, c.k);
+  c.h = rest / c.k.steps;
+  c.step = rest - c.h * c.k.steps;
+  c.unit = e * p.hkv + c.h;
+  return c;
+}
+
+// A query row of a block: row r is token r / group of the stream, head r % group of the KV head's.
 struct QueryRow {
-  int b, t, hq;
+  int b, t, g;
   bool real;
 };
 template <int kRows>
-__device__ __forceinline__ QueryRow query_row(const AttendParams& p, const StreamSet& set, const Cursor<kRows>& c, int r) {
-  const long long ur = (long long)c.tile * kRows + r;
-  const int tok = (int)(ur / p.group);
+__device__ __forceinline__ QueryRow query_row(const AttendParams& p, const WorkSet& set, const Block& k, int r) {
+  const int ur = k.tile * kRows + r;
+  const int tok = ur / p.group;
   QueryRow q;
-  q.hq = c.h * p.group + (int)(ur - (long long)tok * p.group);
-  q.real = tok < c.st.n;
-  q.b = c.s - set.prefixes;
+  q.g = ur - tok * p.group;
+  q.real = tok < k.n;
+  q.b = k.s - set.prefixes;
   q.t = tok;
-  if (c.s < set.prefixes) {
-    const int b0 = c.s * p.fan;
+  if (k.s < set.prefixes) {
+    const int b0 = k.s * p.fan;
     if (!p.n_new) {
-      q.b = b0 + tok / p.m;
-      q.t = tok % p.m;
+      const int i = tok / p.m;
+      q.b = b0 + i;
+      q.t = tok - i * p.m;
     } else {
       int lo = b0, hi = b0 + p.fan;               // the last sequence that begins at or before the token
-      const int at = tokens_before(p, b0) + tok;
+      const int at = p.tok_base[b0] + tok;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (p.tok_base[mid] <= at) lo = mid;

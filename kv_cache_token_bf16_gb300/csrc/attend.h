@@ -9,32 +9,35 @@
 
 namespace evict {
 
-constexpr int kStepTokens = 128;     // rows of K and V that a CTA takes at a time ("step")
+constexpr int kBoxTokens = 16;       // rows of K and V that a warp of the few-row kernel takes at a time
+constexpr int kWideTokens = 128;     // rows that a CTA of the wide kernel takes at a time
 constexpr int kWideRows = 256;       // query rows of a unit of the wide kernel (two MMA tiles)
 
-// The work of one kernel. Streams: one per prefix (all query rows of its
-// sequences), then one per sequence (its own pages; `joint`: behind the prefix
-// as well). A unit is one (stream, KV head, tile of query rows); its work is
-// the rows of K and V that the tile sees, in steps. The steps of all units are
-// laid end to end and every CTA takes an equal contiguous share. The part of a
-// unit that one CTA takes leaves one partial result in slot unit + CTA: from
-// one part to the next either the unit or the CTA goes up, so slots are unique.
-struct StreamSet {
-  int prefixes;                      // streams of prefixes
-  int own;                           // streams of sequences: 0 or the batch
+// The work of one kernel. A block is a tile of query rows of one stream; the
+// streams are the prefixes (all query rows of their sequences), then the
+// sequences (their own pages; `joint`: behind the prefix as well). A unit is a
+// block and a KV head, and its work the rows of K and V that the tile sees, in
+// steps of 16 (few-row kernel) or 128 (wide kernel) rows. The steps of all
+// units, in the order of blocks and heads, are laid end to end and cut into
+// equal contiguous shares, one for every warp (few-row kernel) or CTA (wide).
+// What a share holds of a unit leaves one partial result, in slot unit +
+// share: from one part to the next either of them goes up, so slots are unique.
+struct WorkSet {
+  int prefixes, prefix_tiles;        // streams of prefixes, blocks of one
+  int seqs, seq_tiles;               // streams of sequences: 0 or the batch; blocks of one
   int joint;                         // a sequence's stream begins with its prefix
-  int ctas;
-  long long* step_base;              // [streams + 1] first step of every stream, then their total
-  long long* unit_base;              // [streams] first unit
+  int max_shares, min_steps;         // of a share
+  int* base;                         // [blocks + 1] first step of every block, then their total
   float2* part_ml;                   // [slots][tile rows] running maximum (base 2) and sum
   float* part_o;                     // [slots][tile rows][128]
+  __host__ __device__ int blocks() const { return prefixes * prefix_tiles + seqs * seq_tiles; }
 };
 
 struct AttendParams {
   CUtensorMap tm_pk, tm_pv;          // prefix [prefix_batch][n_kv_heads][n_prefix][128]
   CUtensorMap tm_k, tm_v;            // pages [n_pages][n_kv_heads][page_size][128]
-  StreamSet set;                     // of this launch (the join: of the few-row kernel)
-  StreamSet wide;                    // the join: of the wide kernel
+  WorkSet set;                       // of this launch (the join: of the few-row kernel)
+  WorkSet wide;                      // the join: of the wide kernel
   const void* q;
   void* out;
   float* lse;
@@ -51,15 +54,14 @@ struct AttendParams {
   const void* page_k;                // (the wide kernel's rare path)
   const void* page_v;
   long long page_stride;
-  int box_rows;                      // rows of a box of the pages
+  int box_rows;                      // rows of a box of the pages (wide kernel)
   float scale2;                      // log2(e) * scale
   int* tok_base;                     // [batch + 1] new tokens of the sequences before (with n_new)
   int late_wait;                     // this kernel may start before its predecessor has ended
   int* err;
 };
 
-int wide_smem();
 cudaError_t prepare_wide();
-cudaError_t launch_wide(const AttendParams& p, bool early, cudaStream_t st);
+cudaError_t launch_wide(const AttendParams& p, int ctas, bool early, cudaStream_t st);
 
 }  // namespace evict

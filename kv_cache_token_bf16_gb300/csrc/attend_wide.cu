@@ -43,6 +43,7 @@ constexpr int kTile = 128;
 constexpr int kTileBytes = kTile * kHeadDim * 2;
 constexpr int kRing = 5;
 constexpr int kWideThreads = 10 * 32;
+constexpr int kWideSmem = (2 + kRing) * kTileBytes + 1024;
 constexpr int kMmaWarp = 8, kTmaWarp = 9;
 constexpr int kBadWords = 9;                      // 257 tokens and more
 constexpr float kRefSlack = 32.f;                 // log2 of the largest weight
@@ -56,223 +57,225 @@ struct WideShared {
   ScanShared scan;
 };
 
-using WideCursor = Cursor<kWideRows>;
+using WideCursor = Cursor<kWideRows, kWideTokens>;
 
 // The part of a unit that this CTA takes.
 struct Segment {
   int steps;                                      // from the cursor's on
+  int pre_steps;                                  // of the unit
   bool two, alt;                                  // both groups on every step; or taking turns
-  __device__ Segment(const StreamSet& set, const AttendParams& p, const WideCursor& c, int left) {
-    steps = min(c.steps - c.step, left);
-    const long long rows = (long long)c.st.n * p.group - (long long)c.tile * kWideRows;
-    two = rows > kTile;
-    alt = !two && !set.joint;
+  __device__ __forceinline__ Segment(const AttendParams& p, const WideCursor& c, int left) {
+    steps = min(c.k.steps - c.step, left);
+    pre_steps = (c.k.pre + kWideTokens - 1) / kWideTokens;
+    two = c.k.n * p.group - c.k.tile * kWideRows > kTile;
+    alt = !two && !p.set.joint;
   }
-  __device__ bool has(int w, int i) const { return two || (alt ? (i & 1) == w : w == 0); }
-  __device__ int jobs(int w) const { return two ? steps : alt ? (steps + 1 - w) / 2 : w == 0 ? steps : 0; }
-};
-// On to the first step behind the segment.
-__device__ __forceinline__ void skip(WideCursor& c, const AttendParams& p, const StreamSet& set, int steps) {
-  c.step += steps - 1;
-  c.next(p, set);
-}
-
-// Rows of K and V of a step: prefix rows, or own rows from row0 on.
-struct Step {
-  bool pre;
-  int row0;
-  __device__ Step(const WideCursor& c, int step) {
-    const int ps = c.st.pre_steps();
-    pre = step < ps;
-    row0 = (pre ? step : step - ps) * kStepTokens;
-  }
+  __device__ __forceinline__ bool has(int w, int i) const { return two || (alt ? (i & 1) == w : w == 0); }
+  __device__ __forceinline__ int jobs(int w) const { return two ? steps : alt ? (steps + 1 - w) / 2 : w == 0 ? steps : 0; }
 };
 
 // The unit's first query sees own rows before this one; from here to the last query's, rows with
 // infinities or NaN in V are marked (at most 256 tokens).
 __device__ __forceinline__ int first_marked(const AttendParams& p, const WideCursor& c) {
-  return c.st.len - c.st.n + (int)((long long)c.tile * kWideRows / p.group) + 1;
+  return c.k.len - c.k.n + (c.k.tile * kWideRows) / p.group + 1;
 }
 
+// A position in the ring of K and V tiles, and the parity of the phase that fills it.
+struct Slot {
+  int i = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == kRing) i = 0, parity ^= 1;
+  }
+};
+
 __device__ void producer(const AttendParams& p, WideShared& sh, WideCursor c, int count, uint32_t ring) {
-  const StreamSet& set = p.set;
-  const int lane = threadIdx.x & 31;
-  long long used = 0;
+  const WorkSet& set = p.set;
+  const int lane = threadIdx.x & 31, blocks = set.blocks();
+  const int box = p.box_rows, boxes = box ? kTile / box : 0;
+  Slot slot;
+  int used = 0;
   bool ok = true;
-  while (count > 0 && ok) {
-    const Segment g(set, p, c, count);
+  while (ok) {
+    const Segment g(p, c, count);
+    const int plane = c.k.s < set.prefixes ? c.k.s : p.fan ? (c.k.s - set.prefixes) / p.fan : 0;
+    const int32_t* table = p.table + (long long)(c.k.s - set.prefixes) * p.table_stride;
     for (int i = 0; i < g.steps && ok; ++i) {
-      const Step st(c, c.step + i);
-      int page = 0;
-      const int box = p.box_rows, boxes = kTile / box;
-      const int row = st.row0 + lane * box;       // this lane's page
-      if (!st.pre && lane < boxes) {
-        page = p.n_pages;                         // outside the pool: zeros
-        if (row < c.st.len) {
-          page = p.table[(long long)(c.s - set.prefixes) * p.table_stride + (row >> p.page_shift)];
-          if (page < 0 || page >= p.n_pages) {
-            raise_device_error(p.err, kDevBadIndex);
-            page = p.n_pages;
-          }
+      const int step = c.step + i;
+      const bool pre = step < g.pre_steps;
+      const int row0 = (pre ? step : step - g.pre_steps) * kWideTokens, row = row0 + lane * box;   // this lane's page
+      int page = p.n_pages;                       // outside the pool: zeros
+      if (!pre && lane < boxes && row < c.k.len) {
+        page = table[row >> p.page_shift];
+        if (page < 0 || page >= p.n_pages) {
+          raise_device_error(p.err, kDevBadIndex);
+          page = p.n_pages;
         }
       }
-      for (int kv = 0; kv < 2 && ok; ++kv, ++used) {
-        const int slot = (int)(used % kRing);
-        ok = wait_phase(&sh.kv_empty[slot], (uint32_t)(((used / kRing) & 1) ^ 1), &sh.fail, p.err);
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        ok = wait_phase(&sh.kv_empty[slot.i], slot.parity ^ 1, &sh.fail, p.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        uint64_t* bar = &sh.kv_full[slot];
-        const uint32_t dst = ring + slot * kTileBytes;
+        uint64_t* bar = &sh.kv_full[slot.i];
+        const uint32_t dst = ring + slot.i * kTileBytes;
         if (lane == 0) tc::mbar_arrive_expect_tx(bar, kTileBytes);
         __syncwarp();
-        if (st.pre) {
-          const int plane = c.s < set.prefixes ? c.s : (c.s - set.prefixes) / p.fan;
+        if (pre) {
           if (lane < 2)
-            tma_load_5d(dst + lane * (kTileBytes / 2), kv ? &p.tm_pv : &p.tm_pk, 0, st.row0, lane, c.h, plane, bar);
+            tma_load_5d(dst + lane * (kTileBytes / 2), kv ? &p.tm_pv : &p.tm_pk, 0, row0, lane, c.h, plane, bar);
         } else if (lane < boxes) {
           for (int hf = 0; hf < 2; ++hf)
             tma_load_5d(dst + hf * (kTileBytes / 2) + lane * box * 128, kv ? &p.tm_v : &p.tm_k, 0,
                         row & ((1 << p.page_shift) - 1), hf, c.h, page, bar);
         }
+        slot.next();
+        ++used;
       }
     }
     count -= g.steps;
-    if (count > 0) skip(c, p, set, g.steps);
+    if (count == 0) break;
+    c.next_unit(p, set, blocks);
   }
   // every copy issued must land before the CTA may release its shared memory
-  for (int i = 0; i < kRing; ++i) {
-    const long long n = used > i ? (used - i + kRing - 1) / kRing : 0;       // uses of slot i
-    if (n > 0) drain_phase(&sh.kv_full[i], (uint32_t)((n - 1) & 1), p.err);
-  }
+  for (int i = 0; i < kRing && i < used; ++i) drain_phase(&sh.kv_full[i], ((used - 1 - i) / kRing) & 1, p.err);
 }
 
-// S = Q K^T: both K-major.
-__device__ __forceinline__ void issue_qk(uint32_t d, uint32_t q, uint32_t k) {
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return (uint64_t)lo | ((uint64_t)hi << 32); }
+
+// S = Q K^T, both K-major; q and k: the tiles' descriptors' low words (their steps differ in the
+// start address alone, which does not carry over).
+__device__ __forceinline__ void issue_qk(uint32_t d, uint32_t q, uint32_t k, uint32_t hi) {
   constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile);
 #pragma unroll
   for (int s = 0; s < 8; ++s) {
-    const uint32_t off = (uint32_t)((s >> 2) * kTile * 128 + (s & 3) * 32);
-    tc::mma_bf16(d, tc::sw128_desc(q + off), tc::sw128_desc(k + off), idesc, s > 0 ? 1u : 0u);
+    const uint32_t off = (uint32_t)((s >> 2) * kTile * 128 + (s & 3) * 32) >> 4;
+    tc::mma_bf16(d, desc_of(q + off, hi), desc_of(k + off, hi), idesc, s > 0 ? 1u : 0u);
   }
 }
 // O (+)= P V: P in tensor memory (two weights a column), V with its rows as the product's
 // depth (MN-major). 16 rows of V are 2048 bytes of each half.
-__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pt, uint32_t v, bool accumulate) {
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pt, uint32_t v, uint32_t hi, bool accumulate) {
   constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile) | (1u << 16);
 #pragma unroll
   for (int s = 0; s < 8; ++s) {
-    const uint64_t bd = tc::sw128_desc_mn(v + s * 2048, kTileBytes / 2, 1024);
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-        "r"(pt + s * 8), "l"(bd), "r"(idesc), "r"(accumulate || s > 0 ? 1u : 0u)
+        "r"(pt + s * 8), "l"(desc_of(v + s * 128, hi)), "r"(idesc), "r"(accumulate || s > 0 ? 1u : 0u)
         : "memory");
   }
 }
 
 __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, int count, uint32_t tmem, uint32_t qbuf,
                            uint32_t ring) {
-  const StreamSet& set = p.set;
-  const int lane = threadIdx.x & 31;
-  uint32_t p_waits[2] = {0, 0}, q_waits[2] = {0, 0};
-  long long used = 0;                             // ring tiles of the steps before
-  int segments = 0;
+  const WorkSet& set = p.set;
+  const int lane = threadIdx.x & 31, blocks = set.blocks();
+  const uint64_t qk = tc::sw128_desc(qbuf), pv = tc::sw128_desc_mn(ring, kTileBytes / 2, 1024);
+  const uint32_t q_lo = (uint32_t)qk, k_lo = (uint32_t)tc::sw128_desc(ring), qk_hi = (uint32_t)(qk >> 32);
+  const uint32_t v_lo = (uint32_t)pv, v_hi = (uint32_t)(pv >> 32);
+  uint32_t p_parity = 0, q_parity = 0;            // bit w: group w's
+  Slot slot;                                      // of the step's K
+  int segment = 0;
   bool ok = true;
   struct Job {
     int w;
     bool first, last, first_v, last_v;
-    long long v;                                  // ring tile
-    int from;                                     // rows of the tile from here on are seen by none of the unit's queries
-    int mark0, parity;                            // the tile's row of the first token that may be marked (128: none)
+    Slot v;
+    int from;                                     // rows of V from here on are seen by none of the unit's queries
+    int mark0, segment;                           // the tile's row of the first token that may be marked (128: none)
   };
   Job pend = {};
   bool pending = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    ok = ok && wait_phase(bar, parity, &sh.fail, p.err);
+    ok = wait_phase(bar, parity, &sh.fail, p.err);
     ok = __all_sync(0xffffffffu, ok);
     return ok;
   };
   auto flush = [&] {                              // the pending job's product with V
     pending = false;
-    const int slot = (int)(pend.v % kRing);
-    if (!wait(&sh.p_full[pend.w], p_waits[pend.w]++ & 1)) return;
-    if (!wait(&sh.kv_full[slot], (uint32_t)((pend.v / kRing) & 1))) return;
-    const uint32_t v = ring + slot * kTileBytes;
-    if (pend.first_v) {
+    if (!wait(&sh.kv_full[pend.v.i], pend.v.parity)) return;
+    if (pend.first_v && (pend.from < kTile || pend.mark0 < kTile)) {
       // rows that no query sees, and rows with infinities or NaN that some queries do not see, meet
       // weights of 0: zeros in their place
-      const uint32_t at = v + ((lane >> 3) & 1) * (kTileBytes / 2) + (lane & 7) * 16;
+      const uint32_t at = ring + pend.v.i * kTileBytes + ((lane >> 3) & 1) * (kTileBytes / 2) + (lane & 7) * 16;
       auto blank = [&](int r) {
         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + r * 128), "r"(0u) : "memory");
       };
-      bool wrote = pend.from < kTile;
       for (int r = pend.from + (lane >> 4); r < kTile; r += 2) blank(r);
       if (pend.mark0 < kTile) {
-        const uint32_t* bad = sh.bad[pend.w][pend.parity];
+        const uint32_t* bad = sh.bad[pend.w][pend.segment & 1];
         uint32_t any = 0;
         for (int k = 0; k < kBadWords; ++k) any |= bad[k];
-        if (any) {
-          wrote = true;
+        if (any)
           for (int k = max(0, -pend.mark0); k < 32 * kBadWords && pend.mark0 + k < kTile; ++k)
             if ((bad[k >> 5] >> (k & 31)) & 1) blank(pend.mark0 + k);
-        }
       }
-      if (wrote) tc::fence_proxy_async_smem();
+      tc::fence_proxy_async_smem();
       __syncwarp();
     }
+    if (!wait(&sh.p_full[pend.w], (p_parity >> pend.w) & 1)) return;
+    p_parity ^= 1u << pend.w;
     tc::fence_after_sync();
     if (lane == 0) {
-      issue_pv(tmem + 2 * kTile + pend.w * kTile, tmem + pend.w * kTile, v, !pend.first);
-      if (pend.last_v) tc::mma_commit(&sh.kv_empty[slot]);
+      issue_pv(tmem + 2 * kTile + pend.w * kTile, tmem + pend.w * kTile, v_lo + pend.v.i * (kTileBytes >> 4), v_hi, !pend.first);
+      if (pend.last_v) tc::mma_commit(&sh.kv_empty[pend.v.i]);
       if (pend.last) tc::mma_commit(&sh.o_full[pend.w]);
     }
     __syncwarp();
   };
-  while (count > 0 && ok) {
-    const Segment g(set, p, c, count);
-    int done[2] = {0, 0};
-    for (int i = 0; i < g.steps && ok; ++i, used += 2) {
-      const Step st(c, c.step + i);
-      const int slot = (int)(used % kRing);
+  while (ok) {
+    const Segment g(p, c, count);
+    const int jobs0 = g.jobs(0), jobs1 = g.jobs(1);
+    int done0 = 0, done1 = 0;
+    const int mark = p.m > 1 && c.k.reach >= 0 ? first_marked(p, c) : 1 << 30;
+    for (int i = 0; i < g.steps && ok; ++i) {
+      const int own0 = (c.step + i - g.pre_steps) * kWideTokens;           // < 0: rows of the prefix
       bool first_use = true;
-      for (int w = 0; w < 2 && ok; ++w) {
-        if (!g.has(w, i)) continue;
+#pragma unroll 1
+      for (int w = 0; w < 2; ++w) {
+        if (!g.has(w, i) || !ok) continue;
+        const int done = w ? done1 : done0;
         const bool last_use = w == 1 || !g.two;
         if (pending && pend.w == w) flush();      // S of this group still holds that job's weights
         if (!ok) break;
-        if (first_use && !wait(&sh.kv_full[slot], (uint32_t)((used / kRing) & 1))) break;
-        if (done[w] == 0 && !wait(&sh.q_full[w], q_waits[w]++ & 1)) break;
+        if (first_use && !wait(&sh.kv_full[slot.i], slot.parity)) break;
+        if (done == 0) {
+          if (!wait(&sh.q_full[w], (q_parity >> w) & 1)) break;
+          q_parity ^= 1u << w;
+        }
         tc::fence_after_sync();
         if (lane == 0) {
-          issue_qk(tmem + w * kTile, qbuf + w * kTileBytes, ring + slot * kTileBytes);
+          issue_qk(tmem + w * kTile, q_lo + w * (kTileBytes >> 4), k_lo + slot.i * (kTileBytes >> 4), qk_hi);
           tc::mma_commit(&sh.s_full[w]);
-          if (last_use) tc::mma_commit(&sh.kv_empty[slot]);
+          if (last_use) tc::mma_commit(&sh.kv_empty[slot.i]);
         }
         __syncwarp();
         if (pending) flush();
         if (!ok) break;
         pend.w = w;
-        pend.v = used + 1;
-        pend.first = done[w] == 0;
-        pend.last = ++done[w] == g.jobs(w);
+        pend.v = slot;
+        pend.v.next();
+        pend.first = done == 0;
+        pend.last = done + 1 == (w ? jobs1 : jobs0);
+        done0 += w ^ 1;
+        done1 += w;
         pend.first_v = first_use;
         pend.last_v = last_use;
-        pend.from = kTile;
-        pend.mark0 = kTile;
-        pend.parity = segments & 1;
-        if (!st.pre) {
-          const int reach = c.st.reach(p, c.tile);
-          pend.from = min(kTile, max(0, reach + 1 - st.row0));
-          if (p.m > 1 && reach >= 0) pend.mark0 = first_marked(p, c) - st.row0;
-        }
+        pend.from = own0 >= 0 ? min(kTile, max(0, c.k.reach + 1 - own0)) : kTile;
+        pend.mark0 = own0 >= 0 ? max(mark - own0, -(1 << 29)) : kTile;
+        pend.segment = segment;
         pending = true;
         first_use = false;
       }
+      slot.next();
+      slot.next();
     }
-    ++segments;
+    ++segment;
     count -= g.steps;
-    if (count > 0) skip(c, p, set, g.steps);
+    if (count == 0) break;
+    c.next_unit(p, set, blocks);
   }
   if (pending && ok) flush();
   // every MMA must finish before tensor and shared memory are released
@@ -308,8 +311,8 @@ __device__ __forceinline__ void wait_stores() { asm volatile("tcgen05.wait::st.s
 // One softmax group: thread `row` of group w.
 __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor c, int count, int w, int row, uint32_t tmem,
                               unsigned char* qbuf) {
-  const StreamSet& set = p.set;
-  const int warp = row >> 5;
+  const WorkSet& set = p.set;
+  const int warp = row >> 5, blocks = set.blocks();
   const uint32_t lanes = (uint32_t)(32 * warp) << 16;
   const uint32_t s_at = tmem + lanes + (uint32_t)(w * kTile), o_at = s_at + 2 * kTile;
   const uint32_t flip = p.scale2 < 0.f ? 0x80008000u : 0u;   // a negative scale: of -Q, so that maxima stay maxima
@@ -318,38 +321,38 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
 
   // this row's query into the group's tile, and which rows with infinities or NaN in V some
   // queries of the unit do not see
-  auto load_query = [&](const WideCursor& cu, const Segment& g, int parity) {
-    const int r = g.two ? w * kTile + row : row;
-    const QueryRow q = query_row(p, set, cu, r);
+  auto load_query = [&](const WideCursor& cu, const Segment& g, int segment) {
+    const QueryRow q = query_row<kWideRows>(p, set, cu.k, g.two ? w * kTile + row : row);
     // A group without a job in this part announces nothing (it could announce twice before the
     // MMA warp has looked once).
     if (g.jobs(w) == 0) return q;
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)q.b * p.qb +
-                                                      (long long)q.hq * p.qh + (long long)q.t * p.qm);
+                                                      (long long)(cu.h * p.group + q.g) * p.qh + (long long)q.t * p.qm);
+    uint4 x[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = q.real ? src[j] : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (q.real) x = src[j];
-      x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-      *reinterpret_cast<uint4*>(q_mine + tc::sw128_offset(row, j, kTile)) = x;
+      x[j].x ^= flip, x[j].y ^= flip, x[j].z ^= flip, x[j].w ^= flip;
+      *reinterpret_cast<uint4*>(q_mine + tc::sw128_offset(row, j, kTile)) = x[j];
     }
-    const int reach = cu.st.reach(p, cu.tile);
-    if (p.m > 1 && reach >= 0) {
+    if (p.m > 1 && cu.k.reach >= 0) {
       const int first = first_marked(p, cu);
-      uint32_t* bad = sh.bad[w][parity];
+      uint32_t* bad = sh.bad[w][segment & 1];
       if (row < kBadWords) bad[row] = 0;
       tc::named_sync(1 + w, kTile);
-      const int b = cu.s - set.prefixes;
-      for (int e = row; e < 16 * (reach + 1 - first); e += kTile) {
+      const int32_t* table = p.table + (long long)(cu.k.s - set.prefixes) * p.table_stride;
+#pragma unroll 1
+      for (int e = row; e < 16 * (cu.k.reach + 1 - first); e += kTile) {
         const int tok = first + (e >> 4);
         if (tok < 0) continue;
-        const int page = p.table[(long long)b * p.table_stride + (tok >> p.page_shift)];
+        const int page = table[tok >> p.page_shift];
         if (page < 0 || page >= p.n_pages) continue;
-        const uint4 x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.page_v) +
+        const uint4 v = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.page_v) +
                                                        (long long)page * p.page_stride +
                                                        (((long long)cu.h << p.page_shift) +
                                                         (tok & ((1 << p.page_shift) - 1))) * kHeadDim)[e & 15];
-        if (nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w))
+        if (nonfinite2(v.x) | nonfinite2(v.y) | nonfinite2(v.z) | nonfinite2(v.w))
           atomicOr(&bad[(tok - first) >> 5], 1u << ((tok - first) & 31));
       }
     }
@@ -358,25 +361,28 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
     return q;
   };
 
-  int s_waits = 0, o_waits = 0, segments = 0;
+  uint32_t s_parity = 0, o_parity = 0;
+  int segment = 0;
   bool ok = true;
-  Segment g(set, p, c, count);
+  Segment g(p, c, count);
   QueryRow q = load_query(c, g, 0);
-  while (count > 0) {
+  for (;;) {
     const int jobs = g.jobs(w);
-    const int limit = q.real ? c.st.len - c.st.n + q.t : -1;     // last own row that this query sees
+    const int limit = q.real ? c.k.len - c.k.n + q.t : -1;       // last own row that this query sees
     float ref = -INFINITY, sum = 0.f;
     bool begun = false;
+#pragma unroll 1
     for (int i = 0; i < g.steps && ok; ++i) {
       if (!g.has(w, i)) continue;
-      const Step st(c, c.step + i);
-      ok = wait_phase(&sh.s_full[w], (uint32_t)(s_waits++ & 1), &sh.fail, p.err);
+      ok = wait_phase(&sh.s_full[w], s_parity, &sh.fail, p.err);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
+      s_parity ^= 1;
       tc::fence_after_sync();
-      const int seen = (st.pre ? c.st.pre - 1 : limit) - st.row0;     // columns 0 .. seen
+      const int own0 = (c.step + i - g.pre_steps) * kWideTokens;
+      const int seen = own0 < 0 ? c.k.pre - 1 - (c.step + i) * kWideTokens : limit - own0;   // columns 0 .. seen
       const bool masked = __any_sync(0xffffffffu, seen < kTile - 1);
-#pragma unroll
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {      // 64 columns at a time: their registers are few enough
         float v[64];
         load64(s_at + 64 * half, v);
@@ -445,30 +451,32 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
       tc::mbar_arrive(&sh.p_full[w]);
     }
     // the next unit's queries: this group's last S is in registers, so its tile is free
-    const int left = count - g.steps;
     const WideCursor at = c;
     const Segment part = g;
     const QueryRow mine = q;
-    if (left > 0 && ok) {
-      skip(c, p, set, g.steps);
-      g = Segment(set, p, c, left);
-      q = load_query(c, g, (segments + 1) & 1);
+    count -= g.steps;
+    if (count > 0 && ok) {
+      c.next_unit(p, set, blocks);
+      g = Segment(p, c, count);
+      q = load_query(c, g, segment + 1);
     }
-    count = left;
     if (ok && jobs > 0) {
-      ok = wait_phase(&sh.o_full[w], (uint32_t)(o_waits++ & 1), &sh.fail, p.err);
+      ok = wait_phase(&sh.o_full[w], o_parity, &sh.fail, p.err);
       ok = __all_sync(0xffffffffu, ok);
+      o_parity ^= 1;
     }
     if (!ok) break;
     tc::fence_after_sync();
-    const bool whole = set.joint && part.steps == at.steps;     // no other part, no other unit for these rows
+    const bool whole = set.joint && part.steps == at.k.steps;     // no other part, no other unit for these rows
     const bool write = mine.real && (part.two || part.alt || w == 0);
-    const long long prow = ((at.unit + blockIdx.x) * 2 + w) * kTile + row;
-    const float inv = at.st.pre > 0 || limit >= 0 ? 1.f / sum : 0.f;
+    const size_t prow = (size_t)(at.unit + blockIdx.x) * kWideRows + w * kTile + row;
+    const bool sees = at.k.pre > 0 || limit >= 0;
+    const int hq = at.h * p.group + mine.g;
+    const float inv = sees ? 1.f / sum : 0.f;
     uint32_t any_bad = 0;
     const int first = first_marked(p, at);
-    const uint32_t* bad = sh.bad[w][segments & 1];
-    if (p.m > 1 && at.st.reach(p, at.tile) >= 0)
+    const uint32_t* bad = sh.bad[w][segment & 1];
+    if (p.m > 1 && at.k.reach >= 0 && jobs > 0)
       for (int k = 0; k < kBadWords; ++k) any_bad |= bad[k];
 #pragma unroll 1
     for (int h = 0; h < 4; ++h) {
@@ -482,19 +490,21 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
       if (any_bad && write) {
         // rare: the rows that were blanked, for the queries that see them, where the steps of this
         // part (of this group) hold them
+#pragma unroll 1
         for (int k = 0; k < 32 * kBadWords; ++k) {
           const int tok = first + k;
           if (!((bad[k >> 5] >> (k & 31)) & 1) || tok < 0 || tok > limit) continue;
-          const int step = at.st.pre_steps() + tok / kStepTokens - at.step;
+          const int step = part.pre_steps + tok / kWideTokens - at.step;
           if (step < 0 || step >= part.steps || !part.has(w, step)) continue;
-          const int page = p.table[(long long)(at.s - set.prefixes) * p.table_stride + (tok >> p.page_shift)];
+          const int page = p.table[(long long)(at.k.s - set.prefixes) * p.table_stride + (tok >> p.page_shift)];
           const long long e = (long long)page * p.page_stride +
                               (((long long)at.h << p.page_shift) + (tok & ((1 << p.page_shift) - 1))) * kHeadDim;
           const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(p.page_k) + e;
           const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.page_v) + e + 32 * h;
           const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q) + (long long)mine.b * p.qb +
-                                    (long long)mine.hq * p.qh + (long long)mine.t * p.qm;
+                                    (long long)hq * p.qh + (long long)mine.t * p.qm;
           float z = 0.f;
+#pragma unroll 1
           for (int d = 0; d < kHeadDim; ++d) z += __bfloat162float(qr[d]) * __bfloat162float(kr[d]);
           const float wt = ex2(z * p.scale2 - base_of(ref));
 #pragma unroll
@@ -504,7 +514,7 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
       if (!write) continue;
       if (whole) {
         uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (long long)mine.b * p.ob +
-                                              (long long)mine.hq * p.oh + (long long)mine.t * p.om + 32 * h);
+                                              (long long)hq * p.oh + (long long)mine.t * p.om + 32 * h);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           dst[k] = make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
@@ -519,11 +529,12 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
       if (!whole) {
         set.part_ml[prow] = make_float2(ref, sum);
       } else if (p.lse) {
-        p.lse[((long long)mine.b * p.hq + mine.hq) * p.m + mine.t] =
-            at.st.pre > 0 || limit >= 0 ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        p.lse[((long long)mine.b * p.hq + hq) * p.m + mine.t] =
+            sees ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
       }
     }
-    ++segments;
+    ++segment;
+    if (count == 0) break;
   }
 }
 
@@ -550,9 +561,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) attend_wide_kernel(const __gr
     tc::mbar_init(&sh.done, 1);
     sh.fail = 0;
   }
-  WideCursor c;
-  const int count = find_share<kWideRows, kWideThreads>(p, p.set, sh.scan, c);
-  if (count == 0) return;
+  const Shares shares = find_shares<kWideRows, kWideTokens, kWideThreads, 1>(p, p.set, sh.scan);
+  if ((int)blockIdx.x >= shares.count) return;
+  const int count = shares.begin(blockIdx.x + 1) - shares.begin(blockIdx.x);
+  const WideCursor c = place<kWideRows, kWideTokens>(p, p.set, sh.scan.e[0], sh.scan.rest[0]);
   if (warp == 0) tc::tmem_alloc(&sh.tmem_base, 4 * kTile);
   tc::fence_before_sync();
   __syncthreads();
@@ -569,15 +581,13 @@ __global__ void __launch_bounds__(kWideThreads, 1) attend_wide_kernel(const __gr
 
 }  // namespace
 
-int wide_smem() { return (2 + kRing) * kTileBytes + 1024; }
-
 cudaError_t prepare_wide() {
-  return cudaFuncSetAttribute(attend_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, wide_smem());
+  return cudaFuncSetAttribute(attend_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
 }
 
 // early: the next kernel in the stream waits for this one by itself (late_wait).
-cudaError_t launch_wide(const AttendParams& p, bool early, cudaStream_t st) {
-  return launch_pdl(attend_wide_kernel, dim3(p.set.ctas), dim3(kWideThreads), wide_smem(), st, nullptr, p, early ? 1 : 0);
+cudaError_t launch_wide(const AttendParams& p, int ctas, bool early, cudaStream_t st) {
+  return launch_pdl(attend_wide_kernel, dim3(ctas), dim3(kWideThreads), kWideSmem, st, nullptr, p, early ? 1 : 0);
 }
 
 }  // namespace evict

@@ -186,7 +186,7 @@ def attention(**kw):
     (dict(q=rows(A + 8, heads=8)), EVICT_EINVAL, "16 bytes"), (dict(out=rows(A, heads=8, stride_m=132)), EVICT_EINVAL, "16 bytes"),
     (dict(scale=math.nan), EVICT_EINVAL, "scale"), (dict(lse=A + 2), EVICT_EINVAL, "4-byte"),
     (dict(batch=5000, prefix_batch=1), EVICT_ELIMIT, "4096"),
-    (dict(batch=4096, m=1 << 16), EVICT_ELIMIT, "2\\^31"),
+    (dict(batch=4096, m=1 << 16), EVICT_ELIMIT, "2\\^30"),
     (dict(pages=pages(dtype=EVICT_FP32)), EVICT_EINVAL, "bf16"), (dict(pages=pages(n_kv_heads=2)), EVICT_EINVAL, "KV heads"),
 ])
 def test_bad_attention_calls_are_refused(lib, kw, code, match):
