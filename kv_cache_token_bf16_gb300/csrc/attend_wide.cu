@@ -1,7 +1,7 @@
 // Attention of many query rows over a shared prefix or a sequence's rows
 // (see attend.cu for the operator and the other kernels): tcgen05 tensor cores.
 //
-// attend_wide_kernel: persistent, one CTA of ten warps per SM. A unit is a
+// attend_wide_kernel: persistent, one CTA of eleven warps per SM. A unit is a
 // (stream, KV head, tile of 256 query rows); K and V stream through a ring of
 // five 32 KB tiles of 128 rows (TMA). Warps 0-3 and 4-7 are two softmax
 // groups, a thread per query row, each with its own 128 x 128 logits and
@@ -10,11 +10,10 @@
 // step:
 //     S = Q K^T (MMA) -> P = 2^(S scale - ref) as bf16 over S in tensor memory
 //     (softmax group) -> O += P V (MMA, P read from tensor memory).
-// Jobs alternate between the groups, S of the next job is issued before the
-// product with V of the last, so the tensor cores work on one group's job
-// while the other group exponentiates. A unit of more than 128 rows gives each
-// group 128 rows and both groups every step; a smaller one gives both the same
-// rows and every other step each (two partial results).
+// The tensor cores work on one group's job while the other group exponentiates.
+// A unit of more than 128 rows gives each group 128 rows and both groups every
+// step; a smaller one gives both the same rows and every other step each (two
+// partial results).
 //
 // The exponent's reference is the running maximum where it was last moved: it
 // moves only when a row's maximum passes it by more than 2^32, which costs the
@@ -42,15 +41,15 @@ namespace {
 constexpr int kTile = 128;
 constexpr int kTileBytes = kTile * kHeadDim * 2;
 constexpr int kRing = 5;
-constexpr int kWideThreads = 10 * 32;
+constexpr int kWideThreads = 11 * 32;
 constexpr int kWideSmem = (2 + kRing) * kTileBytes + 1024;
-constexpr int kMmaWarp = 8, kTmaWarp = 9;
+constexpr int kMmaWarp = 8, kTmaWarp = 10;
 constexpr int kBadWords = 9;                      // 257 tokens and more
 constexpr float kRefSlack = 32.f;                 // log2 of the largest weight
 
 struct WideShared {
   uint64_t kv_full[kRing], kv_empty[kRing];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done;
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done[2];
   uint32_t tmem_base;
   int fail;
   uint32_t bad[2][2][kBadWords];                  // [group][segment parity]
@@ -168,108 +167,89 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pt, uint32_t v, ui
   }
 }
 
-__device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, int count, uint32_t tmem, uint32_t qbuf,
-                           uint32_t ring) {
+// The MMAs of group w, issued by one warp of its own: S = Q K^T of a step as soon as the product
+// with V of the step before has been issued (it reads the weights that lie where S goes; MMAs run
+// in order), then, with the group's weights, that step's product with V.
+__device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, int count, int w, uint32_t tmem,
+                           uint32_t qbuf, uint32_t ring) {
   const WorkSet& set = p.set;
   const int lane = threadIdx.x & 31, blocks = set.blocks();
-  const uint64_t qk = tc::sw128_desc(qbuf), pv = tc::sw128_desc_mn(ring, kTileBytes / 2, 1024);
+  const uint64_t qk = tc::sw128_desc(qbuf + w * kTileBytes), pv = tc::sw128_desc_mn(ring, kTileBytes / 2, 1024);
   const uint32_t q_lo = (uint32_t)qk, k_lo = (uint32_t)tc::sw128_desc(ring), qk_hi = (uint32_t)(qk >> 32);
   const uint32_t v_lo = (uint32_t)pv, v_hi = (uint32_t)(pv >> 32);
-  uint32_t p_parity = 0, q_parity = 0;            // bit w: group w's
-  Slot slot;                                      // of the step's K
+  const uint32_t s_at = tmem + w * kTile, o_at = s_at + 2 * kTile;
+  uint32_t p_parity = 0, q_parity = 0;
+  Slot slot;
   int segment = 0;
   bool ok = true;
-  struct Job {
-    int w;
-    bool first, last, first_v, last_v;
-    Slot v;
-    int from;                                     // rows of V from here on are seen by none of the unit's queries
-    int mark0, segment;                           // the tile's row of the first token that may be marked (128: none)
-  };
-  Job pend = {};
-  bool pending = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     ok = wait_phase(bar, parity, &sh.fail, p.err);
     ok = __all_sync(0xffffffffu, ok);
     return ok;
   };
-  auto flush = [&] {                              // the pending job's product with V
-    pending = false;
-    if (!wait(&sh.kv_full[pend.v.i], pend.v.parity)) return;
-    if (pend.first_v && (pend.from < kTile || pend.mark0 < kTile)) {
-      // rows that no query sees, and rows with infinities or NaN that some queries do not see, meet
-      // weights of 0: zeros in their place
-      const uint32_t at = ring + pend.v.i * kTileBytes + ((lane >> 3) & 1) * (kTileBytes / 2) + (lane & 7) * 16;
-      auto blank = [&](int r) {
-        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + r * 128), "r"(0u) : "memory");
-      };
-      for (int r = pend.from + (lane >> 4); r < kTile; r += 2) blank(r);
-      if (pend.mark0 < kTile) {
-        const uint32_t* bad = sh.bad[pend.w][pend.segment & 1];
-        uint32_t any = 0;
-        for (int k = 0; k < kBadWords; ++k) any |= bad[k];
-        if (any)
-          for (int k = max(0, -pend.mark0); k < 32 * kBadWords && pend.mark0 + k < kTile; ++k)
-            if ((bad[k >> 5] >> (k & 31)) & 1) blank(pend.mark0 + k);
-      }
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-    }
-    if (!wait(&sh.p_full[pend.w], (p_parity >> pend.w) & 1)) return;
-    p_parity ^= 1u << pend.w;
-    tc::fence_after_sync();
-    if (lane == 0) {
-      issue_pv(tmem + 2 * kTile + pend.w * kTile, tmem + pend.w * kTile, v_lo + pend.v.i * (kTileBytes >> 4), v_hi, !pend.first);
-      if (pend.last_v) tc::mma_commit(&sh.kv_empty[pend.v.i]);
-      if (pend.last) tc::mma_commit(&sh.o_full[pend.w]);
-    }
-    __syncwarp();
-  };
   while (ok) {
     const Segment g(p, c, count);
-    const int jobs0 = g.jobs(0), jobs1 = g.jobs(1);
-    int done0 = 0, done1 = 0;
-    const int mark = p.m > 1 && c.k.reach >= 0 ? first_marked(p, c) : 1 << 30;
-    for (int i = 0; i < g.steps && ok; ++i) {
-      const int own0 = (c.step + i - g.pre_steps) * kWideTokens;           // < 0: rows of the prefix
-      bool first_use = true;
+    const int jobs = g.jobs(w);
+    if (jobs > 0) {
+      if (!wait(&sh.q_full[w], q_parity)) break;
+      q_parity ^= 1;
+    }
+    int done = 0;
 #pragma unroll 1
-      for (int w = 0; w < 2; ++w) {
-        if (!g.has(w, i) || !ok) continue;
-        const int done = w ? done1 : done0;
-        const bool last_use = w == 1 || !g.two;
-        if (pending && pend.w == w) flush();      // S of this group still holds that job's weights
+    for (int i = 0; i < g.steps; ++i) {
+      if (!g.has(w, i)) {                         // the other group's step: this one lets go of its tiles
+#pragma unroll 1
+        for (int kv = 0; kv < 2 && wait(&sh.kv_full[slot.i], slot.parity); ++kv, slot.next())
+          if (lane == 0) tc::mbar_arrive(&sh.kv_empty[slot.i]);
         if (!ok) break;
-        if (first_use && !wait(&sh.kv_full[slot.i], slot.parity)) break;
-        if (done == 0) {
-          if (!wait(&sh.q_full[w], (q_parity >> w) & 1)) break;
-          q_parity ^= 1u << w;
-        }
-        tc::fence_after_sync();
-        if (lane == 0) {
-          issue_qk(tmem + w * kTile, q_lo + w * (kTileBytes >> 4), k_lo + slot.i * (kTileBytes >> 4), qk_hi);
-          tc::mma_commit(&sh.s_full[w]);
-          if (last_use) tc::mma_commit(&sh.kv_empty[slot.i]);
-        }
-        __syncwarp();
-        if (pending) flush();
-        if (!ok) break;
-        pend.w = w;
-        pend.v = slot;
-        pend.v.next();
-        pend.first = done == 0;
-        pend.last = done + 1 == (w ? jobs1 : jobs0);
-        done0 += w ^ 1;
-        done1 += w;
-        pend.first_v = first_use;
-        pend.last_v = last_use;
-        pend.from = own0 >= 0 ? min(kTile, max(0, c.k.reach + 1 - own0)) : kTile;
-        pend.mark0 = own0 >= 0 ? max(mark - own0, -(1 << 29)) : kTile;
-        pend.segment = segment;
-        pending = true;
-        first_use = false;
+        continue;
       }
+      if (!wait(&sh.kv_full[slot.i], slot.parity)) break;
+      tc::fence_after_sync();
+      if (lane == 0) {
+        issue_qk(s_at, q_lo, k_lo + slot.i * (kTileBytes >> 4), qk_hi);
+        tc::mma_commit(&sh.s_full[w]);
+        tc::mma_commit(&sh.kv_empty[slot.i]);
+      }
+      __syncwarp();
       slot.next();
+      if (!wait(&sh.kv_full[slot.i], slot.parity)) break;
+      const int own0 = (c.step + i - g.pre_steps) * kWideTokens;           // < 0: rows of the prefix
+      if (own0 >= 0) {
+        // rows that no query of the unit sees, and rows with infinities or NaN that some queries do
+        // not see, meet weights of 0: zeros in their place (both groups' warps write the same zeros)
+        const uint32_t at = ring + slot.i * kTileBytes + ((lane >> 3) & 1) * (kTileBytes / 2) + (lane & 7) * 16;
+        auto blank = [&](int r) {
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + r * 128), "r"(0u) : "memory");
+        };
+        bool wrote = false;
+#pragma unroll 1
+        for (int r = max(0, c.k.reach + 1 - own0) + (lane >> 4); r < kTile; r += 2) blank(r), wrote = true;
+        const int mark0 = p.m > 1 && c.k.reach >= 0 ? first_marked(p, c) - own0 : kTile;
+        if (mark0 < kTile) {
+          const uint32_t* bad = sh.bad[w][segment & 1];
+          uint32_t any = 0;
+          for (int k = 0; k < kBadWords; ++k) any |= bad[k];
+          if (any) {
+            wrote = true;
+#pragma unroll 1
+            for (int k = max(0, -mark0); k < 32 * kBadWords && mark0 + k < kTile; ++k)
+              if ((bad[k >> 5] >> (k & 31)) & 1) blank(mark0 + k);
+          }
+        }
+        if (__any_sync(0xffffffffu, wrote)) tc::fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (!wait(&sh.p_full[w], p_parity)) break;
+      p_parity ^= 1;
+      tc::fence_after_sync();
+      ++done;
+      if (lane == 0) {
+        issue_pv(o_at, s_at, v_lo + slot.i * (kTileBytes >> 4), v_hi, done > 1);
+        tc::mma_commit(&sh.kv_empty[slot.i]);
+        if (done == jobs) tc::mma_commit(&sh.o_full[w]);
+      }
+      __syncwarp();
       slot.next();
     }
     ++segment;
@@ -277,11 +257,10 @@ __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, 
     if (count == 0) break;
     c.next_unit(p, set, blocks);
   }
-  if (pending && ok) flush();
   // every MMA must finish before tensor and shared memory are released
   if (lane == 0) {
-    tc::mma_commit(&sh.done);
-    drain_phase(&sh.done, 0, p.err);
+    tc::mma_commit(&sh.done[w]);
+    drain_phase(&sh.done[w], 0, p.err);
   }
   __syncwarp();
 }
@@ -550,15 +529,15 @@ __global__ void __launch_bounds__(kWideThreads, 1) attend_wide_kernel(const __gr
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       tc::mbar_init(&sh.kv_full[i], 1);
-      tc::mbar_init(&sh.kv_empty[i], 1);
+      tc::mbar_init(&sh.kv_empty[i], 2);          // both groups' MMA warps
     }
     for (int w = 0; w < 2; ++w) {
       tc::mbar_init(&sh.q_full[w], kTile);
       tc::mbar_init(&sh.s_full[w], 1);
       tc::mbar_init(&sh.p_full[w], kTile);
       tc::mbar_init(&sh.o_full[w], 1);
+      tc::mbar_init(&sh.done[w], 1);
     }
-    tc::mbar_init(&sh.done, 1);
     sh.fail = 0;
   }
   const Shares shares = find_shares<kWideRows, kWideTokens, kWideThreads, 1>(p, p.set, sh.scan);
@@ -571,7 +550,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attend_wide_kernel(const __gr
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem_base;
   if (warp == kTmaWarp) producer(p, sh, c, count, ring);
-  else if (warp == kMmaWarp) mma_issuer(p, sh, c, count, tmem, q_at, ring);
+  else if (warp >= kMmaWarp) mma_issuer(p, sh, c, count, warp - kMmaWarp, tmem, q_at, ring);
   else softmax_group(p, sh, c, count, warp >> 2, tid & (kTile - 1), tmem, qbuf);
   tc::fence_before_sync();
   __syncthreads();
