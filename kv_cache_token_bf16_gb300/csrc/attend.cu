@@ -118,7 +118,6 @@ __global__ void __launch_bounds__(few_warps(kTiles) * 32, 1) attend_kernel(const
     };
     look_up();
     int requested = 0, flying = 0;                // the stage that the next request takes; boxes in the ring
-    for (; requested < kStages - 1 && ahead_left > 0; ++requested, ++flying) request(requested);
 
     // addresses of this lane's rows for ldmatrix: 16-byte chunk j of a row sits at j ^ (row % 8), so a
     // chunk's address is the lane's own xor 16 j (and 2 KB on for the second half)
@@ -134,38 +133,46 @@ __global__ void __launch_bounds__(few_warps(kTiles) * 32, 1) attend_kernel(const
       // this lane's queries (rows lane / 4 and 8 on of each tile) and the last row each sees
       uint32_t q[kTiles][8][4];
       float o[kTiles][16][4], mx[kTiles][2], sum[kTiles][2];
-      int last[kTiles][2];
-#pragma unroll
-      for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const QueryRow r = query_row<kRows>(p, set, cur.k, 16 * x + (lane >> 2) + 8 * k);
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)r.b * p.qb +
-                                                                  (long long)(cur.h * p.group + r.g) * p.qh +
-                                                                  (long long)r.t * p.qm) + (lane & 3);
-#pragma unroll
-          for (int s = 0; s < 8; ++s) {
-            q[x][s][k] = r.real ? src[8 * s] : 0u;
-            q[x][s][2 + k] = r.real ? src[8 * s + 4] : 0u;
-          }
-          last[x][k] = !own ? cur.k.pre - 1 : r.real ? cur.k.len - cur.k.n + r.t : -1;
-          mx[x][k] = -INFINITY;
-          sum[x][k] = 0.f;
-        }
-#pragma unroll
-      for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[x][j][k] = 0.f;
-      const int low = __shfl_sync(0xffffffffu, last[0][0], 0);     // the first row's: the lowest
+      int last[kTiles][2], low = 0;
 
+#pragma unroll 1
       for (int i = 0; i < boxes; ++i) {
         __syncwarp();                             // every lane has read the box that the next one replaces
-        if (ahead_left > 0 && !dead) {
+#pragma unroll 1
+        while (flying < kStages && ahead_left > 0 && !dead) {
           request(requested);
           requested = requested == kStages - 1 ? 0 : requested + 1;
           ++flying;
+        }
+        if (i == 0) {
+#pragma unroll
+          for (int x = 0; x < kTiles; ++x)
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) {
+              const QueryRow r = query_row<kRows>(p, set, cur.k, 16 * x + (lane >> 2) + 8 * k);
+              const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)r.b * p.qb +
+                                                                      (long long)(cur.h * p.group + r.g) * p.qh +
+                                                                      (long long)r.t * p.qm) + (lane & 3);
+              const int l = !own ? cur.k.pre - 1 : r.real ? cur.k.len - cur.k.n + r.t : -1;
+#pragma unroll
+              for (int s = 0; s < 8; ++s) {
+                const uint32_t a = r.real ? src[8 * s] : 0u, c = r.real ? src[8 * s + 4] : 0u;
+                if (k == 0) q[x][s][0] = a, q[x][s][2] = c;
+                else q[x][s][1] = a, q[x][s][3] = c;
+              }
+              if (k == 0) last[x][0] = l;
+              else last[x][1] = l;
+            }
+#pragma unroll
+          for (int x = 0; x < kTiles; ++x) {
+            mx[x][0] = mx[x][1] = -INFINITY;
+            sum[x][0] = sum[x][1] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[x][j][k] = 0.f;
+          }
+          low = __shfl_sync(0xffffffffu, last[0][0], 0);           // the first row's: the lowest
         }
         if (!dead) {
           const bool ok = wait_phase(&sh.full[warp][stage], parity, &sh.fail, p.err);
@@ -365,15 +372,18 @@ constexpr int kJoinWarps = 8;
 __device__ __forceinline__ void join_row(const AttendParams& p, const Parts* parts, int np, int b, int t, int hq, bool sees) {
   const int lane = threadIdx.x & 31;
   float top = -INFINITY;
+#pragma unroll 1
   for (int x = 0; x < np; ++x)
+#pragma unroll 1
     for (int k = lane; k < parts[x].parts(); k += 32) top = fmaxf(top, parts[x].ml[parts[x].at(k)].x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
+#pragma unroll 1
   for (int x = 0; x < np; ++x) {
     const int n = parts[x].parts();
-#pragma unroll 4
+#pragma unroll 2
     for (int k = 0; k < n; ++k) {
       const size_t at = parts[x].at(k);
       const float2 ml = parts[x].ml[at];
@@ -451,6 +461,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_split_kernel(cons
   if (c > 1 && shares.begin(c - 1) > first) return;
   const int c1 = shares.of(first + k.steps - 1);
   Parts part = {set.part_ml, set.part_o, lo * p.hkv + h + c - 1, c1 - (c - 1) + 1, kWideRows, 0, 0};
+#pragma unroll 1
   for (int i = threadIdx.x >> 5; i < 32; i += kJoinWarps) {
     part.row = blockIdx.y * 32 + i;
     const QueryRow q = query_row<kWideRows>(p, set, k, part.row);
@@ -632,6 +643,7 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
   P.qb = a->q.stride_b, P.qh = a->q.stride_h, P.qm = a->q.stride_m;
   P.out = a->out.data;
   P.ob = a->out.stride_b, P.oh = a->out.stride_h, P.om = a->out.stride_m;
+  P.out_sectors = multiple(a->out.data, 32) && a->out.stride_b % 16 == 0 && a->out.stride_h % 16 == 0 && a->out.stride_m % 16 == 0;
   P.lse = a->lse;
   P.batch = a->batch, P.m = a->m, P.hq = a->n_q_heads, P.hkv = a->n_kv_heads;
   P.group = a->n_q_heads / a->n_kv_heads;

@@ -100,6 +100,7 @@ struct Cursor {
     ++unit;
     if (++h < p.hkv) return;
     h = 0;
+#pragma unroll 1
     for (;;) {
       if (++e >= blocks) return;
       load_block<kRows, kTokens>(p, set, e, k);
@@ -111,7 +112,8 @@ struct Cursor {
 
 // Equal shares of `total` steps: the first `extra` have one step more.
 struct Shares {
-  int count, each, extra;
+  int count = 0, each = 0, extra = 0;
+  Shares() = default;
   __device__ __forceinline__ Shares(const WorkSet& set, int total) {
     count = min(set.max_shares, total / set.min_steps);
     if (count == 0) count = total > 0 ? 1 : 0;
@@ -145,6 +147,7 @@ __device__ __forceinline__ int block_scan(int a, int& total, ScanShared& sh) {
   if (lane == 31) sh.a[warp] = x;
   __syncthreads();
   total = 0;
+#pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) x += sh.a[w];
     total += sh.a[w];
@@ -159,13 +162,15 @@ template <int kRows, int kTokens, int kThreads, int kPer>
 __device__ __forceinline__ Shares find_shares(const AttendParams& p, const WorkSet& set, ScanShared& sh) {
   const int tid = threadIdx.x;
   int total;
-  if (p.n_new && p.fan) {
+  if (p.n_new && set.prefixes) {
     // every CTA writes the same sums, and reads back its own
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
     int a = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) a += sequence(p, b, false).n;
     a = block_scan<kThreads>(a, total, sh);
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       p.tok_base[b] = a;
       a += sequence(p, b, false).n;
@@ -177,23 +182,29 @@ __device__ __forceinline__ Shares find_shares(const AttendParams& p, const WorkS
   const int per = (blocks + kThreads - 1) / kThreads;
   const int e0 = min(tid * per, blocks), e1 = min(e0 + per, blocks);
   Block k;
-  int work = 0;
-  for (int e = e0; e < e1; ++e) {
-    load_block<kRows, kTokens>(p, set, e, k, blockIdx.x == 0);
-    work += k.steps * p.hkv;
-  }
-  int a = block_scan<kThreads>(work, total, sh);
-  const Shares shares(set, total);
+  int work = 0, a = 0, lo = 0, hi = 0;
+  Shares shares;
   const int first = blockIdx.x * kPer;
-  const int lo = shares.begin(min(first, shares.count)), hi = shares.begin(min(first + kPer, shares.count));
-  if (blockIdx.x == 0 || (a < hi && a + work > lo)) {
+  // two passes over this thread's blocks: their sum, then (with the sums before) what begins in them
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass == 1) {
+      a = block_scan<kThreads>(work, total, sh);
+      shares = Shares(set, total);
+      lo = shares.begin(min(first, shares.count));
+      hi = shares.begin(min(first + kPer, shares.count));
+      if (blockIdx.x != 0 && (a >= hi || a + work <= lo)) break;
+    }
+#pragma unroll 1
     for (int e = e0; e < e1; ++e) {
-      int w = work;
-      if (per > 1) {
-        load_block<kRows, kTokens>(p, set, e, k);
-        w = k.steps * p.hkv;
+      if (pass == 0 || per > 1) load_block<kRows, kTokens>(p, set, e, k, blockIdx.x == 0 && pass == 0);
+      const int w = k.steps * p.hkv;
+      if (pass == 0) {
+        work += w;
+        continue;
       }
       if (blockIdx.x == 0) set.base[e] = a;
+#pragma unroll 1
       for (int i = 0; i < kPer && first + i < shares.count; ++i) {
         const int g = shares.begin(first + i);
         if (g >= a && g < a + w) sh.e[i] = e, sh.rest[i] = g - a;
@@ -240,6 +251,7 @@ __device__ __forceinline__ QueryRow query_row(const AttendParams& p, const WorkS
     } else {
       int lo = b0, hi = b0 + p.fan;               // the last sequence that begins at or before the token
       const int at = p.tok_base[b0] + tok;
+#pragma unroll 1
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (p.tok_base[mid] <= at) lo = mid;

@@ -55,6 +55,7 @@ struct AttendParams {
   const void* page_v;
   long long page_stride;
   int box_rows;                      // rows of a box of the pages (wide kernel)
+  int out_sectors;                   // every row of out begins on a multiple of 32 bytes
   float scale2;                      // log2(e) * scale
   int* tok_base;                     // [batch + 1] new tokens of the sequences before (with n_new)
   int late_wait;                     // this kernel may start before its predecessor has ended

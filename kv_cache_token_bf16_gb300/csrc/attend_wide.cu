@@ -15,11 +15,12 @@
 // step; a smaller one gives both the same rows and every other step each (two
 // partial results).
 //
-// The exponent's reference is the running maximum where it was last moved: it
-// moves only when a row's maximum passes it by more than 2^32, which costs the
-// group a read and write of its O in tensor memory (in practice only a unit's
-// first step moves it). Weights, sums and O are relative to it and floating, so
-// the result does not depend on where it stands. Weights enter the product
+// The exponent's reference is a row's maximum over the first 64 columns that it
+// sees, and stays there: later columns are taken against it without a maximum
+// of their own while the sum of 64 of their weights is below 2^12, and it moves
+// to the running maximum (with a read and write of O in tensor memory) where
+// that is passed. Weights, sums and O are relative to it and floating, so the
+// result does not depend on where it stands. Weights enter the product
 // with V as bf16 (half a step: 2^-9 of a weight), at twice the rate of the
 // split that the few-row kernel uses; their roundings are independent, so the
 // output's error grows from one rounding to the root of two.
@@ -45,14 +46,15 @@ constexpr int kWideThreads = 11 * 32;
 constexpr int kWideSmem = (2 + kRing) * kTileBytes + 1024;
 constexpr int kMmaWarp = 8, kTmaWarp = 10;
 constexpr int kBadWords = 9;                      // 257 tokens and more
-constexpr float kRefSlack = 32.f;                 // log2 of the largest weight
+constexpr int kBadSets = 16;                      // segments in flight, by far
+constexpr float kMoveAbove = 4096.f;              // sum of 64 weights that makes the reference move
 
 struct WideShared {
   uint64_t kv_full[kRing], kv_empty[kRing];
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done[2];
   uint32_t tmem_base;
-  int fail;
-  uint32_t bad[2][2][kBadWords];                  // [group][segment parity]
+  int fail, turn;
+  uint32_t bad[kBadSets][kBadWords];              // of the segments in turn: rows of V that were blanked
   ScanShared scan;
 };
 
@@ -140,6 +142,24 @@ __device__ void producer(const AttendParams& p, WideShared& sh, WideCursor c, in
   for (int i = 0; i < kRing && i < used; ++i) drain_phase(&sh.kv_full[i], ((used - 1 - i) / kRing) & 1, p.err);
 }
 
+// The lock of the MMA warps' turns (bounded, like every wait; the clock is read rarely).
+__device__ __forceinline__ bool take_turn(WideShared& sh, int* err) {
+  uint64_t t0 = 0;
+  for (uint32_t spins = 0; atomicCAS(&sh.turn, 0, 1) != 0; ++spins) {
+    if ((spins & 1023) != 1023) continue;
+    if (*(volatile int*)&sh.fail) return false;
+    const uint64_t t = tc::global_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitLimitNs) {
+      *(volatile int*)&sh.fail = 1;
+      raise_device_error(err, kDevWaitTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ void end_turn(WideShared& sh) { atomicExch(&sh.turn, 0); }
+
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return (uint64_t)lo | ((uint64_t)hi << 32); }
 
 // S = Q K^T, both K-major; q and k: the tiles' descriptors' low words (their steps differ in the
@@ -167,129 +187,148 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pt, uint32_t v, ui
   }
 }
 
-// The MMAs of group w, issued by one warp of its own: S = Q K^T of a step as soon as the product
-// with V of the step before has been issued (it reads the weights that lie where S goes; MMAs run
-// in order), then, with the group's weights, that step's product with V.
+// The MMAs of group w, issued by one warp of its own: the product with V of a job and S = Q K^T of
+// the group's next one right behind it (S goes where the weights lay, and MMAs run in order). Where
+// both groups work on every step they take turns at this pair, under a lock: the tensor cores then
+// finish one group's pair and that group exponentiates while they work on the other's; issued side
+// by side, both pairs would end together and the tensor cores wait for both groups.
 __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, int count, int w, uint32_t tmem,
                            uint32_t qbuf, uint32_t ring) {
   const WorkSet& set = p.set;
-  const int lane = threadIdx.x & 31, blocks = set.blocks();
+  const int blocks = set.blocks();
   const uint64_t qk = tc::sw128_desc(qbuf + w * kTileBytes), pv = tc::sw128_desc_mn(ring, kTileBytes / 2, 1024);
   const uint32_t q_lo = (uint32_t)qk, k_lo = (uint32_t)tc::sw128_desc(ring), qk_hi = (uint32_t)(qk >> 32);
   const uint32_t v_lo = (uint32_t)pv, v_hi = (uint32_t)(pv >> 32);
   const uint32_t s_at = tmem + w * kTile, o_at = s_at + 2 * kTile;
   uint32_t p_parity = 0, q_parity = 0;
   Slot slot;
-  int segment = 0;
   bool ok = true;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    ok = wait_phase(bar, parity, &sh.fail, p.err);
-    ok = __all_sync(0xffffffffu, ok);
-    return ok;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = wait_phase(bar, parity, &sh.fail, p.err); };
+  auto release = [&](int tiles) {                 // tiles of the other group's steps: this one lets go of them
+#pragma unroll 1
+    for (; tiles > 0 && wait(&sh.kv_full[slot.i], slot.parity); --tiles, slot.next()) tc::mbar_arrive(&sh.kv_empty[slot.i]);
   };
   while (ok) {
     const Segment g(p, c, count);
     const int jobs = g.jobs(w);
-    if (jobs > 0) {
-      if (!wait(&sh.q_full[w], q_parity)) break;
-      q_parity ^= 1;
-    }
-    int done = 0;
+    Slot v;
+    int at = 0;                                   // steps passed
 #pragma unroll 1
-    for (int i = 0; i < g.steps; ++i) {
-      if (!g.has(w, i)) {                         // the other group's step: this one lets go of its tiles
-#pragma unroll 1
-        for (int kv = 0; kv < 2 && wait(&sh.kv_full[slot.i], slot.parity); ++kv, slot.next())
-          if (lane == 0) tc::mbar_arrive(&sh.kv_empty[slot.i]);
-        if (!ok) break;
-        continue;
+    for (int j = 0; j <= jobs && jobs > 0; ++j) {
+      if (j < jobs) {
+        if (g.alt && (j > 0 || w == 1)) {
+          release(2);
+          if (!ok) break;
+          ++at;
+        }
+        if (!wait(&sh.kv_full[slot.i], slot.parity)) break;
+        if (j == 0) {
+          if (!wait(&sh.q_full[w], q_parity)) break;
+          q_parity ^= 1;
+        }
       }
-      if (!wait(&sh.kv_full[slot.i], slot.parity)) break;
+      if (j > 0) {
+        if (!wait(&sh.kv_full[v.i], v.parity) || !wait(&sh.p_full[w], p_parity)) break;
+        p_parity ^= 1;
+      }
+      if (g.two && !take_turn(sh, p.err)) {
+        ok = false;
+        break;
+      }
       tc::fence_after_sync();
-      if (lane == 0) {
+      if (j > 0) issue_pv(o_at, s_at, v_lo + v.i * (kTileBytes >> 4), v_hi, j > 1);
+      if (j < jobs) {
         issue_qk(s_at, q_lo, k_lo + slot.i * (kTileBytes >> 4), qk_hi);
         tc::mma_commit(&sh.s_full[w]);
+      }
+      if (g.two) end_turn(sh);
+      if (j == jobs) tc::mma_commit(&sh.o_full[w]);
+      if (j > 0) tc::mma_commit(&sh.kv_empty[v.i]);
+      if (j < jobs) {
         tc::mma_commit(&sh.kv_empty[slot.i]);
+        ++at;
+        slot.next();
+        v = slot;
+        slot.next();
       }
-      __syncwarp();
-      slot.next();
-      if (!wait(&sh.kv_full[slot.i], slot.parity)) break;
-      const int own0 = (c.step + i - g.pre_steps) * kWideTokens;           // < 0: rows of the prefix
-      if (own0 >= 0) {
-        // rows that no query of the unit sees, and rows with infinities or NaN that some queries do
-        // not see, meet weights of 0: zeros in their place (both groups' warps write the same zeros)
-        const uint32_t at = ring + slot.i * kTileBytes + ((lane >> 3) & 1) * (kTileBytes / 2) + (lane & 7) * 16;
-        auto blank = [&](int r) {
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + r * 128), "r"(0u) : "memory");
-        };
-        bool wrote = false;
-#pragma unroll 1
-        for (int r = max(0, c.k.reach + 1 - own0) + (lane >> 4); r < kTile; r += 2) blank(r), wrote = true;
-        const int mark0 = p.m > 1 && c.k.reach >= 0 ? first_marked(p, c) - own0 : kTile;
-        if (mark0 < kTile) {
-          const uint32_t* bad = sh.bad[w][segment & 1];
-          uint32_t any = 0;
-          for (int k = 0; k < kBadWords; ++k) any |= bad[k];
-          if (any) {
-            wrote = true;
-#pragma unroll 1
-            for (int k = max(0, -mark0); k < 32 * kBadWords && mark0 + k < kTile; ++k)
-              if ((bad[k >> 5] >> (k & 31)) & 1) blank(mark0 + k);
-          }
-        }
-        if (__any_sync(0xffffffffu, wrote)) tc::fence_proxy_async_smem();
-        __syncwarp();
-      }
-      if (!wait(&sh.p_full[w], p_parity)) break;
-      p_parity ^= 1;
-      tc::fence_after_sync();
-      ++done;
-      if (lane == 0) {
-        issue_pv(o_at, s_at, v_lo + slot.i * (kTileBytes >> 4), v_hi, done > 1);
-        tc::mma_commit(&sh.kv_empty[slot.i]);
-        if (done == jobs) tc::mma_commit(&sh.o_full[w]);
-      }
-      __syncwarp();
-      slot.next();
     }
-    ++segment;
+    if (ok) release(2 * (g.steps - at));
     count -= g.steps;
-    if (count == 0) break;
+    if (count == 0 || !ok) break;
     c.next_unit(p, set, blocks);
   }
   // every MMA must finish before tensor and shared memory are released
-  if (lane == 0) {
-    tc::mma_commit(&sh.done[w]);
-    drain_phase(&sh.done[w], 0, p.err);
-  }
-  __syncwarp();
+  tc::mma_commit(&sh.done[w]);
+  drain_phase(&sh.done[w], 0, p.err);
 }
 
-// 64 columns of this thread's row; the load and its wait are one statement, so that nothing uses
-// the registers before the data is there.
-__device__ __forceinline__ void load64(uint32_t taddr, float* v) {
-  uint32_t r[64];
+// 32 columns of this thread's row. The load runs on; nothing may use the registers before wait32,
+// which has them as operands to that end.
+__device__ __forceinline__ void load32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-      : "r"(taddr)
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr) : "memory");
 #pragma unroll
-  for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void wait32(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :: "memory");
 }
 __device__ __forceinline__ void store32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
       ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void store16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// 32 bytes to global memory, 32-byte aligned: a whole sector from each thread
+__device__ __forceinline__ void store_sector(void* dst, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
+// 16 columns, complete on return
+__device__ __forceinline__ void load16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr) : "memory");
+}
 __device__ __forceinline__ void wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// The reference of a row's exponents moved: its O (where there is one) and the step's weights so
+// far (`columns` of them) follow by the factor f. Whole warp; rare after a unit's first step.
+__device__ __noinline__ void move_reference(uint32_t s_at, int columns, uint32_t o_at, float f) {
+  wait_stores();
+  uint32_t x[16];
+  for (int c = 0; c < columns; c += 16) {
+    load16(s_at + c, x);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = pack_bf16(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xffff0000u) * f);
+    store16(s_at + c, x);
+  }
+  if (o_at) {
+    for (int c = 0; c < kHeadDim; c += 16) {
+      load16(o_at + c, x);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+      store16(o_at + c, x);
+    }
+  }
+}
 
 // One softmax group: thread `row` of group w.
 __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor c, int count, int w, int row, uint32_t tmem,
-                              unsigned char* qbuf) {
+                              unsigned char* qbuf, uint32_t ring) {
   const WorkSet& set = p.set;
   const int warp = row >> 5, blocks = set.blocks();
   const uint32_t lanes = (uint32_t)(32 * warp) << 16;
@@ -298,9 +337,8 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
   const float scale = fabsf(p.scale2);
   unsigned char* q_mine = qbuf + w * kTileBytes;
 
-  // this row's query into the group's tile, and which rows with infinities or NaN in V some
-  // queries of the unit do not see
-  auto load_query = [&](const WideCursor& cu, const Segment& g, int segment) {
+  // this row's query into the group's tile
+  auto load_query = [&](const WideCursor& cu, const Segment& g) {
     const QueryRow q = query_row<kWideRows>(p, set, cu.k, g.two ? w * kTile + row : row);
     // A group without a job in this part announces nothing (it could announce twice before the
     // MMA warp has looked once).
@@ -315,43 +353,163 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
       x[j].x ^= flip, x[j].y ^= flip, x[j].z ^= flip, x[j].w ^= flip;
       *reinterpret_cast<uint4*>(q_mine + tc::sw128_offset(row, j, kTile)) = x[j];
     }
-    if (p.m > 1 && cu.k.reach >= 0) {
-      const int first = first_marked(p, cu);
-      uint32_t* bad = sh.bad[w][segment & 1];
-      if (row < kBadWords) bad[row] = 0;
-      tc::named_sync(1 + w, kTile);
-      const int32_t* table = p.table + (long long)(cu.k.s - set.prefixes) * p.table_stride;
-#pragma unroll 1
-      for (int e = row; e < 16 * (cu.k.reach + 1 - first); e += kTile) {
-        const int tok = first + (e >> 4);
-        if (tok < 0) continue;
-        const int page = table[tok >> p.page_shift];
-        if (page < 0 || page >= p.n_pages) continue;
-        const uint4 v = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.page_v) +
-                                                       (long long)page * p.page_stride +
-                                                       (((long long)cu.h << p.page_shift) +
-                                                        (tok & ((1 << p.page_shift) - 1))) * kHeadDim)[e & 15];
-        if (nonfinite2(v.x) | nonfinite2(v.y) | nonfinite2(v.z) | nonfinite2(v.w))
-          atomicOr(&bad[(tok - first) >> 5], 1u << ((tok - first) & 31));
-      }
-    }
     tc::fence_proxy_async_smem();
     tc::mbar_arrive(&sh.q_full[w]);
     return q;
   };
 
+  // A step's rows of V that no query of the unit sees may hold anything, and so may rows that some
+  // queries do not see: both meet weights of 0, but 0 * infinity is not 0. This thread looks at the
+  // tile's row `row` and writes zeros over it in the first case and, where it holds infinities or
+  // NaN, in the second, with a mark for the queries that do see it. Both groups may do so; the mark
+  // is there before the zeros are, so a group that finds zeros finds the mark, too.
+  auto blank_rows = [&](int slot, int own0, int first, uint32_t* bad) {
+    const uint32_t at = ring + slot * kTileBytes + row * 128;
+    const int tok = own0 + row;
+    bool blank = tok > c.k.reach;
+    if (!blank && tok >= first && tok >= 0) {
+#pragma unroll 1
+      for (int j = 0; j < 16 && !blank; ++j) {
+        uint4 x;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                     : "r"(at + (j >> 3) * (kTileBytes / 2) + ((j + row) & 7) * 16) : "memory");
+        blank = nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w);
+      }
+      if (blank) {
+        atomicOr(&bad[(tok - first) >> 5], 1u << ((tok - first) & 31));
+        __threadfence_block();
+      }
+    }
+    if (blank) {
+#pragma unroll 1
+      for (int j = 0; j < 16; ++j)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + (j >> 3) * (kTileBytes / 2) + ((j + row) & 7) * 16),
+                     "r"(0u) : "memory");
+      tc::fence_proxy_async_smem();
+    }
+  };
+
   uint32_t s_parity = 0, o_parity = 0;
-  int segment = 0;
   bool ok = true;
   Segment g(p, c, count);
-  QueryRow q = load_query(c, g, 0);
-  for (;;) {
-    const int jobs = g.jobs(w);
-    const int limit = q.real ? c.k.len - c.k.n + q.t : -1;       // last own row that this query sees
-    float ref = -INFINITY, sum = 0.f;
-    bool begun = false;
+  QueryRow q = {};
+  int limit = -1;                                 // last own row that this query sees
+  float ref = -INFINITY, sum = 0.f;
+  bool marks = false;                             // the segment holds rows that may have been marked
+  Slot slot;                                      // of the segment's first tile
+  for (int segment = -1;; ++segment) {            // -1: only the first unit's queries
+    // The next unit's queries: this group's last S is in registers, so its tile is free.
+    const WideCursor at = c;
+    const Segment part = g;
+    const QueryRow mine = q;
+    const bool more = segment < 0 || count > part.steps;
+    if (segment >= 0) count -= part.steps;
+    if (more) {
+      if (segment >= 0) {
+        c.next_unit(p, set, blocks);
+        g = Segment(p, c, count);
+      }
+      q = load_query(c, g);
+    }
+    if (segment >= 0) {
+      const int jobs = part.jobs(w);
+      if (jobs > 0) {
+        ok = wait_phase(&sh.o_full[w], o_parity, &sh.fail, p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        o_parity ^= 1;
+      }
+      if (!ok) break;
+      tc::fence_after_sync();
+      const bool whole = set.joint && part.steps == at.k.steps;     // no other part, no other unit for these rows
+      const bool write = mine.real && (part.two || part.alt || w == 0);
+      const size_t prow = (size_t)(at.unit + blockIdx.x) * kWideRows + w * kTile + row;
+      const bool sees = at.k.pre > 0 || limit >= 0;
+      const int hq = at.h * p.group + mine.g;
+      const float inv = sees ? 1.f / sum : 0.f;
+      uint32_t any_bad = 0;
+      const int first = first_marked(p, at);
+      const uint32_t* bad = sh.bad[segment & (kBadSets - 1)];
+      if (marks)
+        for (int k = 0; k < kBadWords; ++k) any_bad |= bad[k];
 #pragma unroll 1
-    for (int i = 0; i < g.steps && ok; ++i) {
+      for (int h = 0; h < 4; ++h) {
+        float o[32];
+        if (jobs > 0) {
+          tc::tmem_ld32(o_at + 32 * h, o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0.f;
+        }
+        if (any_bad && write) {
+          // rare: the rows that were blanked, for the queries that see them, where the steps of this
+          // part (of this group) hold them
+#pragma unroll 1
+          for (int k = 0; k < 32 * kBadWords; ++k) {
+            const int tok = first + k;
+            if (!((bad[k >> 5] >> (k & 31)) & 1) || tok < 0 || tok > limit) continue;
+            const int step = part.pre_steps + tok / kWideTokens - at.step;
+            if (step < 0 || step >= part.steps || !part.has(w, step)) continue;
+            const int page = p.table[(long long)(at.k.s - set.prefixes) * p.table_stride + (tok >> p.page_shift)];
+            const long long e = (long long)page * p.page_stride +
+                                (((long long)at.h << p.page_shift) + (tok & ((1 << p.page_shift) - 1))) * kHeadDim;
+            const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(p.page_k) + e;
+            const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.page_v) + e + 32 * h;
+            const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q) + (long long)mine.b * p.qb +
+                                      (long long)hq * p.qh + (long long)mine.t * p.qm;
+            float z = 0.f;
+#pragma unroll 1
+            for (int d = 0; d < kHeadDim; ++d) z += __bfloat162float(qr[d]) * __bfloat162float(kr[d]);
+            const float wt = ex2(z * p.scale2 - base_of(ref));
+#pragma unroll
+            for (int d = 0; d < 32; ++d) o[d] += wt * __bfloat162float(vr[d]);
+          }
+        }
+        if (!write) continue;
+        if (whole) {
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (long long)mine.b * p.ob + (long long)hq * p.oh +
+                               (long long)mine.t * p.om + 32 * h;
+          uint32_t y[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) y[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
+          if (p.out_sectors) {
+            store_sector(dst, y);
+            store_sector(dst + 16, y + 8);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              reinterpret_cast<uint4*>(dst)[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+          }
+        } else {
+          float* dst = set.part_o + prow * kHeadDim + 32 * h;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) store_sector(dst + 8 * k, reinterpret_cast<const uint32_t*>(o) + 8 * k);
+        }
+      }
+      if (write) {
+        if (!whole) {
+          set.part_ml[prow] = make_float2(ref, sum);
+        } else if (p.lse) {
+          p.lse[((long long)mine.b * p.hq + hq) * p.m + mine.t] =
+              sees ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+    }
+    if (!more) break;
+
+    limit = q.real ? c.k.len - c.k.n + q.t : -1;
+    ref = q.real ? -INFINITY : 0.f;               // rows without a query never wait for a maximum
+    sum = 0.f;
+    marks = false;
+    bool begun = false;
+    const int first = p.m > 1 && c.k.reach >= 0 ? first_marked(p, c) : 1 << 30;
+    uint32_t* bad = sh.bad[(segment + 1) & (kBadSets - 1)];
+    if (w == 0 && row < kBadWords) sh.bad[(segment + 1 + kBadSets / 2) & (kBadSets - 1)][row] = 0;
+#pragma unroll 1
+    for (int i = 0; i < g.steps; ++i) {
+      slot.next();                                // the step's V
+      const int v_slot = slot.i;
+      const uint32_t v_parity = slot.parity;
+      slot.next();
       if (!g.has(w, i)) continue;
       ok = wait_phase(&sh.s_full[w], s_parity, &sh.fail, p.err);
       ok = __all_sync(0xffffffffu, ok);
@@ -361,159 +519,74 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
       const int own0 = (c.step + i - g.pre_steps) * kWideTokens;
       const int seen = own0 < 0 ? c.k.pre - 1 - (c.step + i) * kWideTokens : limit - own0;   // columns 0 .. seen
       const bool masked = __any_sync(0xffffffffu, seen < kTile - 1);
+      // 64 columns at a time, in two loads of 32: each is on its way while the one before is at work
+      float x[2][32];
+      load32(s_at, x[0]);
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {      // 64 columns at a time: their registers are few enough
-        float v[64];
-        load64(s_at + 64 * half, v);
-        if (masked) {
+      for (int half = 0; half < 2; ++half) {
+        const uint64_t sc2 = pack_f32x2(scale, scale);
+        float nb = -base_of(ref);
+        uint32_t pk[32];
+        float got;
+        // weights of the columns against the reference, packed, and their sum
+        auto weights = [&](int k0) {
+          const uint64_t nb2 = pack_f32x2(nb, nb);
+          uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
-          for (int k = 0; k < 64; ++k)
-            if (64 * half + k > seen) v[k] = -INFINITY;
-        }
-        float mx[4];
+          for (int k = 0; k < 32; k += 2) {
+            const uint64_t e = ex2_f32x2(fma_f32x2(pack_f32x2(x[k0][k], x[k0][k + 1]), sc2, nb2));
+            acc[(k >> 1) & 1] = add_f32x2(acc[(k >> 1) & 1], e);
+            float a, b;
+            split_f32x2(e, a, b);
+            pk[16 * k0 + (k >> 1)] = pack_bf16(a, b);
+          }
+          float a0, a1;
+          split_f32x2(add_f32x2(acc[0], acc[1]), a0, a1);
+          return a0 + a1;
+        };
+        auto hide = [&](int k0) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) mx[j] = fmax3(v[j], v[j + 4], v[j + 8]);
+          for (int k = 0; k < 32; ++k)
+            if (64 * half + 32 * k0 + k > seen) x[k0][k] = -INFINITY;
+        };
+        wait32(x[0]);
+        load32(s_at + 64 * half + 32, x[1]);
+        if (masked) hide(0);
+        got = weights(0);
+        wait32(x[1]);
+        if (masked) hide(1);
+        got += weights(1);
+        // no reference yet, or a sum that says that it has fallen far behind the maximum (NaN as well)
+        if (__any_sync(0xffffffffu, ref == -INFINITY || !(got < kMoveAbove))) {
+          float top = -INFINITY;
 #pragma unroll
-        for (int k = 12; k < 60; k += 8)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mx[j] = fmax3(mx[j], v[k + j], v[k + 4 + j]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], v[60 + j]);
-        const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * scale;
-        if (__any_sync(0xffffffffu, top > ref + kRefSlack)) {         // also from no reference to the first
-          const float to = fmaxf(ref, top), f = weight_of(ref, to);
+          for (int k = 0; k < 32; ++k) top = fmax3(top, x[0][k], x[1][k]);
+          const float to = fmaxf(ref, top * scale), f = weight_of(ref, to);
           ref = to;
           sum *= f;
-          if (begun) {
-#pragma unroll 1
-            for (int h = 0; h < 4; ++h) {
-              float o[32];
-              tc::tmem_ld32(o_at + 32 * h, o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= f;
-              store32(o_at + 32 * h, reinterpret_cast<const uint32_t*>(o));
-            }
-          }
-          if (half == 1) {                        // the first half's weights, too
-            float o[32];
-            wait_stores();
-            tc::tmem_ld32(s_at, o);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const uint32_t x = __float_as_uint(o[k]);
-              o[k] = __uint_as_float(pack_bf16(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f));
-            }
-            store32(s_at, reinterpret_cast<const uint32_t*>(o));
-          }
+          move_reference(s_at, 32 * half, begun ? o_at : 0, f);
+          nb = -base_of(ref);
+          got = weights(0);
+          got += weights(1);
         }
-        const float base = base_of(ref);
-        const uint64_t sc2 = pack_f32x2(scale, scale), nb2 = pack_f32x2(-base, -base);
-        uint64_t acc[2] = {0ull, 0ull};
-        uint32_t pk[32];
-#pragma unroll
-        for (int k = 0; k < 64; k += 2) {
-          const uint64_t e = ex2_f32x2(fma_f32x2(pack_f32x2(v[k], v[k + 1]), sc2, nb2));
-          acc[(k >> 1) & 1] = add_f32x2(acc[(k >> 1) & 1], e);
-          float a, b;
-          split_f32x2(e, a, b);
-          pk[k >> 1] = pack_bf16(a, b);
-        }
+        sum += got;
         // over columns that are in registers by now: half 0 over 0 .. 31, half 1 over 32 .. 63
         store32(s_at + 32 * half, pk);
-        float a0, a1;
-        split_f32x2(add_f32x2(acc[0], acc[1]), a0, a1);
-        sum += a0 + a1;
+        if (half == 0) load32(s_at + 64, x[0]);
       }
       begun = true;
+      if (own0 >= 0 && (own0 + kTile - 1 > c.k.reach || own0 + kTile > first)) {
+        ok = wait_phase(&sh.kv_full[v_slot], v_parity, &sh.fail, p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        blank_rows(v_slot, own0, first, bad);
+        marks = marks || own0 + kTile > first;
+      }
       wait_stores();
       tc::fence_before_sync();
       tc::mbar_arrive(&sh.p_full[w]);
     }
-    // the next unit's queries: this group's last S is in registers, so its tile is free
-    const WideCursor at = c;
-    const Segment part = g;
-    const QueryRow mine = q;
-    count -= g.steps;
-    if (count > 0 && ok) {
-      c.next_unit(p, set, blocks);
-      g = Segment(p, c, count);
-      q = load_query(c, g, segment + 1);
-    }
-    if (ok && jobs > 0) {
-      ok = wait_phase(&sh.o_full[w], o_parity, &sh.fail, p.err);
-      ok = __all_sync(0xffffffffu, ok);
-      o_parity ^= 1;
-    }
     if (!ok) break;
-    tc::fence_after_sync();
-    const bool whole = set.joint && part.steps == at.k.steps;     // no other part, no other unit for these rows
-    const bool write = mine.real && (part.two || part.alt || w == 0);
-    const size_t prow = (size_t)(at.unit + blockIdx.x) * kWideRows + w * kTile + row;
-    const bool sees = at.k.pre > 0 || limit >= 0;
-    const int hq = at.h * p.group + mine.g;
-    const float inv = sees ? 1.f / sum : 0.f;
-    uint32_t any_bad = 0;
-    const int first = first_marked(p, at);
-    const uint32_t* bad = sh.bad[w][segment & 1];
-    if (p.m > 1 && at.k.reach >= 0 && jobs > 0)
-      for (int k = 0; k < kBadWords; ++k) any_bad |= bad[k];
-#pragma unroll 1
-    for (int h = 0; h < 4; ++h) {
-      float o[32];
-      if (jobs > 0) {
-        tc::tmem_ld32(o_at + 32 * h, o);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = 0.f;
-      }
-      if (any_bad && write) {
-        // rare: the rows that were blanked, for the queries that see them, where the steps of this
-        // part (of this group) hold them
-#pragma unroll 1
-        for (int k = 0; k < 32 * kBadWords; ++k) {
-          const int tok = first + k;
-          if (!((bad[k >> 5] >> (k & 31)) & 1) || tok < 0 || tok > limit) continue;
-          const int step = part.pre_steps + tok / kWideTokens - at.step;
-          if (step < 0 || step >= part.steps || !part.has(w, step)) continue;
-          const int page = p.table[(long long)(at.k.s - set.prefixes) * p.table_stride + (tok >> p.page_shift)];
-          const long long e = (long long)page * p.page_stride +
-                              (((long long)at.h << p.page_shift) + (tok & ((1 << p.page_shift) - 1))) * kHeadDim;
-          const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(p.page_k) + e;
-          const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.page_v) + e + 32 * h;
-          const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q) + (long long)mine.b * p.qb +
-                                    (long long)hq * p.qh + (long long)mine.t * p.qm;
-          float z = 0.f;
-#pragma unroll 1
-          for (int d = 0; d < kHeadDim; ++d) z += __bfloat162float(qr[d]) * __bfloat162float(kr[d]);
-          const float wt = ex2(z * p.scale2 - base_of(ref));
-#pragma unroll
-          for (int d = 0; d < 32; ++d) o[d] += wt * __bfloat162float(vr[d]);
-        }
-      }
-      if (!write) continue;
-      if (whole) {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + (long long)mine.b * p.ob +
-                                              (long long)hq * p.oh + (long long)mine.t * p.om + 32 * h);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          dst[k] = make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv), pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                              pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv), pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
-      } else {
-        float4* dst = reinterpret_cast<float4*>(set.part_o + prow * kHeadDim + 32 * h);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-      }
-    }
-    if (write) {
-      if (!whole) {
-        set.part_ml[prow] = make_float2(ref, sum);
-      } else if (p.lse) {
-        p.lse[((long long)mine.b * p.hq + hq) * p.m + mine.t] =
-            sees ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-      }
-    }
-    ++segment;
-    if (count == 0) break;
   }
 }
 
@@ -539,6 +612,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) attend_wide_kernel(const __gr
       tc::mbar_init(&sh.done[w], 1);
     }
     sh.fail = 0;
+    sh.turn = 0;
+    for (int i = 0; i < kBadSets * kBadWords; ++i) (&sh.bad[0][0])[i] = 0;
   }
   const Shares shares = find_shares<kWideRows, kWideTokens, kWideThreads, 1>(p, p.set, sh.scan);
   if ((int)blockIdx.x >= shares.count) return;
@@ -550,8 +625,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) attend_wide_kernel(const __gr
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem_base;
   if (warp == kTmaWarp) producer(p, sh, c, count, ring);
-  else if (warp >= kMmaWarp) mma_issuer(p, sh, c, count, warp - kMmaWarp, tmem, q_at, ring);
-  else softmax_group(p, sh, c, count, warp >> 2, tid & (kTile - 1), tmem, qbuf);
+  else if (warp >= kMmaWarp) {
+    if ((tid & 31) == 0) mma_issuer(p, sh, c, count, warp - kMmaWarp, tmem, q_at, ring);
+    __syncwarp();
+  }
+  else softmax_group(p, sh, c, count, warp >> 2, tid & (kTile - 1), tmem, qbuf, ring);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
