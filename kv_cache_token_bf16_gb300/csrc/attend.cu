@@ -61,6 +61,18 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Four lanes with four words each: lane i's word j and lane j's word i change places.
+__device__ __forceinline__ void quad_transpose(uint4& v, int lane) {
+  const bool o1 = lane & 1, o2 = lane & 2;
+  uint32_t a = __shfl_xor_sync(0xffffffffu, o1 ? v.x : v.y, 1), b = __shfl_xor_sync(0xffffffffu, o1 ? v.z : v.w, 1);
+  if (o1) v.x = a, v.z = b;
+  else v.y = a, v.w = b;
+  a = __shfl_xor_sync(0xffffffffu, o2 ? v.x : v.z, 2);
+  b = __shfl_xor_sync(0xffffffffu, o2 ? v.y : v.w, 2);
+  if (o2) v.x = a, v.y = b;
+  else v.z = a, v.w = b;
+}
+
 template <int kTiles>
 struct FewShared {
   uint64_t full[few_warps(kTiles)][few_stages(kTiles)];
@@ -72,7 +84,6 @@ template <int kTiles>
 __global__ void __launch_bounds__(few_warps(kTiles) * 32, 1) attend_kernel(const __grid_constant__ AttendParams p) {
   constexpr int kRows = 16 * kTiles, kWarps = few_warps(kTiles), kStages = few_stages(kTiles);
   using Cur = Cursor<kRows, kBoxTokens>;
-  if (!p.late_wait) pdl_wait();
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ FewShared<kTiles> sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -82,6 +93,8 @@ __global__ void __launch_bounds__(few_warps(kTiles) * 32, 1) attend_kernel(const
 
   if (tid < kWarps * kStages) tc::mbar_init(&sh.full[tid / kStages][tid % kStages], 1);
   if (tid == 0) sh.fail = 0;
+  if (warp == 1) prefetch_maps(p, set, lane);
+  if (!p.late_wait) pdl_wait();
   const Shares shares = find_shares<kRows, kBoxTokens, kWarps * 32, kWarps>(p, set, sh.scan);
   const int share = blockIdx.x * kWarps + warp;
   if (share < shares.count) {
@@ -147,21 +160,24 @@ __global__ void __launch_bounds__(few_warps(kTiles) * 32, 1) attend_kernel(const
         if (i == 0) {
 #pragma unroll
           for (int x = 0; x < kTiles; ++x)
-#pragma unroll 1
+#pragma unroll
             for (int k = 0; k < 2; ++k) {
               const QueryRow r = query_row<kRows>(p, set, cur.k, 16 * x + (lane >> 2) + 8 * k);
-              const uint32_t* src = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)r.b * p.qb +
-                                                                      (long long)(cur.h * p.group + r.g) * p.qh +
-                                                                      (long long)r.t * p.qm) + (lane & 3);
-              const int l = !own ? cur.k.pre - 1 : r.real ? cur.k.len - cur.k.n + r.t : -1;
+              const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)r.b * p.qb +
+                                                                (long long)(cur.h * p.group + r.g) * p.qh +
+                                                                (long long)r.t * p.qm) + (lane & 3);
+              uint4 c[4];                         // chunks (lane % 4) + 4 i of the row
 #pragma unroll
-              for (int s = 0; s < 8; ++s) {
-                const uint32_t a = r.real ? src[8 * s] : 0u, c = r.real ? src[8 * s + 4] : 0u;
-                if (k == 0) q[x][s][0] = a, q[x][s][2] = c;
-                else q[x][s][1] = a, q[x][s][3] = c;
+              for (int i = 0; i < 4; ++i) c[i] = r.real ? src[4 * i] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {       // to word (lane % 4) of chunks 4 i .. 4 i + 3
+                quad_transpose(c[i], lane);
+                q[x][2 * i][k] = c[i].x;
+                q[x][2 * i][2 + k] = c[i].y;
+                q[x][2 * i + 1][k] = c[i].z;
+                q[x][2 * i + 1][2 + k] = c[i].w;
               }
-              if (k == 0) last[x][0] = l;
-              else last[x][1] = l;
+              last[x][k] = !own ? cur.k.pre - 1 : r.real ? cur.k.len - cur.k.n + r.t : -1;
             }
 #pragma unroll
           for (int x = 0; x < kTiles; ++x) {
@@ -368,73 +384,102 @@ __device__ __forceinline__ Parts find_parts(const AttendParams& p, const WorkSet
 
 constexpr int kJoinWarps = 8;
 
-// A warp merges the parts of one output row, in their order, and writes it.
-__device__ __forceinline__ void join_row(const AttendParams& p, const Parts* parts, int np, int b, int t, int hq, bool sees) {
-  const int lane = threadIdx.x & 31;
-  float top = -INFINITY;
-#pragma unroll 1
-  for (int x = 0; x < np; ++x)
-#pragma unroll 1
-    for (int k = lane; k < parts[x].parts(); k += 32) top = fmaxf(top, parts[x].ml[parts[x].at(k)].x);
-#pragma unroll
-  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+// One output row's running merge: lane l holds columns 4 l .. 4 l + 3.
+struct Merge {
+  float top = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
+  __device__ __forceinline__ void add(float2 ml, float4 v) {
+    const float to = fmaxf(top, ml.x), f = weight_of(top, to), w = weight_of(ml.x, to);
+    top = to;
+    sum = sum * f + ml.y * w;
+    acc.x = acc.x * f + v.x * w;
+    acc.y = acc.y * f + v.y * w;
+    acc.z = acc.z * f + v.z * w;
+    acc.w = acc.w * f + v.w * w;
+  }
+  // parts first, first + step, ... in this order, four of them in flight
+  __device__ __forceinline__ void add_parts(const Parts& x, int first, int step) {
+    const int lane = threadIdx.x & 31, n = x.parts();
 #pragma unroll 1
-  for (int x = 0; x < np; ++x) {
-    const int n = parts[x].parts();
-#pragma unroll 2
-    for (int k = 0; k < n; ++k) {
-      const size_t at = parts[x].at(k);
-      const float2 ml = parts[x].ml[at];
-      const float4 v = reinterpret_cast<const float4*>(parts[x].o + at * kHeadDim)[lane];
-      const float w = weight_of(ml.x, top);
-      sum += ml.y * w;
-      acc.x += v.x * w;
-      acc.y += v.y * w;
-      acc.z += v.z * w;
-      acc.w += v.w * w;
+    for (int k = first; k < n; k += 4 * step) {
+      float2 ml[4];
+      float4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k + i * step < n) {
+          const size_t at = x.at(k + i * step);
+          ml[i] = x.ml[at];
+          v[i] = reinterpret_cast<const float4*>(x.o + at * kHeadDim)[lane];
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (k + i * step < n) add(ml[i], v[i]);
     }
   }
-  const float inv = sees ? 1.f / sum : 0.f;       // a query that sees no row: zeros
-  uint2 y = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + (long long)b * p.ob + (long long)hq * p.oh +
-                            (long long)t * p.om + 4 * lane) = y;
-  if (p.lse && lane == 0)
-    p.lse[((long long)b * p.hq + hq) * p.m + t] = sees ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-}
+  __device__ __forceinline__ void write(const AttendParams& p, int b, int t, int hq, bool sees) const {
+    const int lane = threadIdx.x & 31;
+    const float inv = sees ? 1.f / sum : 0.f;     // a query that sees no row: zeros
+    const uint2 y = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + (long long)b * p.ob + (long long)hq * p.oh +
+                              (long long)t * p.om + 4 * lane) = y;
+    if (p.lse && lane == 0)
+      p.lse[((long long)b * p.hq + hq) * p.m + t] = sees ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  }
+};
 
-// Every output row: the parts of its prefix unit and of its own.
-template <int kRows>
+// Every output row: the parts of its prefix unit and of its own. kSplit warps share a row's parts
+// (few rows have many parts each, and one warp would wait for memory part after part) and their
+// results meet in shared memory, in the order of the warps.
+template <int kRows, int kSplit>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const __grid_constant__ AttendParams p) {
+  __shared__ float4 acc[kJoinWarps][32];
+  __shared__ float2 ml[kJoinWarps];
   pdl_wait();
-  const int row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= p.batch * p.hq * p.m) return;
-  const int bh = row / p.m, t = row - bh * p.m, b = bh / p.hq, hq = bh - b * p.hq;
-  const Seq q = sequence(p, b, !p.pages && t == 0 && hq == 0 && (threadIdx.x & 31) == 0);
-  if (t >= q.n) return;
-  const int h = hq / p.group, g = hq - h * p.group;
-  Parts parts[2];
-  int np = 0;
-  if (p.fan) {
-    const int s = b / p.fan, before = tokens_before(p, s * p.fan);
-    const int r = (tokens_before(p, b) - before + t) * p.group + g, all = (tokens_before(p, (s + 1) * p.fan) - before) * p.group;
-    if (p.wide.prefixes) {
-      const int tile = r / kWideRows;
-      parts[np++] = find_parts<kWideRows>(p, p.wide, s * p.wide.prefix_tiles + tile, h, r % kWideRows, all - tile * kWideRows);
-    } else {
-      parts[np++] = find_parts<kRows>(p, p.set, s * p.set.prefix_tiles + r / kRows, h, r % kRows, 0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % kSplit;
+  const int row = blockIdx.x * (kJoinWarps / kSplit) + warp / kSplit;
+  const bool in = row < p.batch * p.hq * p.m;
+  const int bh = row / p.m, t = row - bh * p.m, b = in ? bh / p.hq : 0, hq = bh - b * p.hq;
+  const Seq q = sequence(p, b, in && !p.pages && t == 0 && hq == 0 && lane == 0 && part == 0);
+  const bool real = in && t < q.n;
+  Merge m;
+  bool sees = false;
+  if (real) {
+    const int h = hq / p.group, g = hq - h * p.group;
+    if (p.fan) {
+      const int s = b / p.fan, before = tokens_before(p, s * p.fan);
+      const int r = (tokens_before(p, b) - before + t) * p.group + g;
+      Parts x;
+      if (p.wide.prefixes) {
+        const int all = (tokens_before(p, (s + 1) * p.fan) - before) * p.group, tile = r / kWideRows;
+        x = find_parts<kWideRows>(p, p.wide, s * p.wide.prefix_tiles + tile, h, r % kWideRows, all - tile * kWideRows);
+      } else {
+        x = find_parts<kRows>(p, p.set, s * p.set.prefix_tiles + r / kRows, h, r % kRows, 0);
+      }
+      m.add_parts(x, part, kSplit);
+      sees = true;
+    }
+    if (q.len - q.n + t >= 0 && q.len > 0) {
+      const int r = t * p.group + g;
+      Parts x;
+      if (p.wide.seqs)                            // at most 128 rows of a sequence: one tile
+        x = find_parts<kWideRows>(p, p.wide, p.wide.prefixes * p.wide.prefix_tiles + b, h, r, q.n * p.group);
+      else
+        x = find_parts<kRows>(p, p.set, p.set.prefixes * p.set.prefix_tiles + b * p.set.seq_tiles + r / kRows, h, r % kRows, 0);
+      m.add_parts(x, part, kSplit);
+      sees = true;
     }
   }
-  if (q.len - q.n + t >= 0 && q.len > 0) {
-    const int r = t * p.group + g;
-    if (p.wide.seqs)                              // at most 128 rows of a sequence: one tile
-      parts[np++] = find_parts<kWideRows>(p, p.wide, p.wide.prefixes * p.wide.prefix_tiles + b, h, r, q.n * p.group);
-    else
-      parts[np++] = find_parts<kRows>(p, p.set, p.set.prefixes * p.set.prefix_tiles + b * p.set.seq_tiles + r / kRows, h,
-                                      r % kRows, 0);
+  if constexpr (kSplit > 1) {
+    if (part > 0) {
+      acc[warp][lane] = m.acc;
+      if (lane == 0) ml[warp] = make_float2(m.top, m.sum);
+    }
+    __syncthreads();
+    if (part > 0) return;
+#pragma unroll
+    for (int i = 1; i < kSplit; ++i) m.add(ml[warp + i], acc[warp + i][lane]);
   }
-  join_row(p, parts, np, b, t, hq, np > 0);
+  if (real) m.write(p, b, t, hq, sees);
 }
 
 // Joint units: only those that two or more CTAs share have parts to merge. Block (c, y) takes 32 rows of
@@ -466,7 +511,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_split_kernel(cons
     part.row = blockIdx.y * 32 + i;
     const QueryRow q = query_row<kWideRows>(p, set, k, part.row);
     if (!q.real) continue;
-    join_row(p, &part, 1, q.b, q.t, h * p.group + q.g, k.pre > 0 || k.len - k.n + q.t >= 0);
+    Merge m;
+    m.add_parts(part, 0, 1);
+    m.write(p, q.b, q.t, h * p.group + q.g, k.pre > 0 || k.len - k.n + q.t >= 0);
   }
 }
 
@@ -518,9 +565,10 @@ void rebase(WorkSet& s, char* base) {
 }
 
 constexpr size_t kWorkHead = 256;                 // an error word, for callers without one
-// Boxes that a share of the few-row kernel has at least: fewer would leave more partial results to
-// merge than rows to read.
+// Boxes (steps) that a share has at least: fewer would leave more partial results to merge than rows
+// to read.
 constexpr int kFewMinBoxes = 4;
+constexpr int kWideMinSteps = 4;
 
 // Sizes alone decide: lens and n_new are the device's.
 int make_plan(const evict_attention* a, Plan* out) {
@@ -574,7 +622,7 @@ int make_plan(const evict_attention* a, Plan* out) {
   P.few.max_shares = P.sms * few_warps(P.few_tiles);
   P.few.min_steps = kFewMinBoxes;
   P.wide.max_shares = P.sms;
-  P.wide.min_steps = 1;
+  P.wide.min_steps = kWideMinSteps;
   size_t off = kWorkHead + round256((size_t)(a->batch + 1) * sizeof(int));
   lay_out(P.few, a->n_kv_heads, 16 * P.few_tiles, off);
   lay_out(P.wide, a->n_kv_heads, kWideRows, off);
@@ -714,10 +762,12 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
     if (plan.sms > 1)
       e = launch_pdl(attend_join_split_kernel, dim3(plan.sms - 1, kWideRows / 32), dim3(kJoinWarps * 32), 0, st, nullptr, P);
   } else {
-    const long long rows = (long long)a->batch * a->n_q_heads * a->m;
-    const dim3 grid((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), block(kJoinWarps * 32);
-    e = plan.few_tiles == 1 ? launch_pdl(attend_join_kernel<16>, grid, block, 0, st, nullptr, P)
-                            : launch_pdl(attend_join_kernel<32>, grid, block, 0, st, nullptr, P);
+    // four warps a row while that is no more than two waves of blocks
+    const int rows = a->batch * a->n_q_heads * a->m, split = rows <= plan.sms * 8 * 2 * (kJoinWarps / 4) ? 4 : 1;
+    const dim3 grid((rows * split + kJoinWarps - 1) / kJoinWarps), block(kJoinWarps * 32);
+    auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, st, nullptr, P); };
+    if (plan.few_tiles == 1) e = split == 4 ? go(attend_join_kernel<16, 4>) : go(attend_join_kernel<16, 1>);
+    else e = split == 4 ? go(attend_join_kernel<32, 4>) : go(attend_join_kernel<32, 1>);
   }
   g_launches.fetch_add(1);
   return e == cudaSuccess ? EVICT_OK : cuda_fail(e, "attention kernel launch");

@@ -23,6 +23,11 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int 
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(tc::smem_u32(bar))
       : "memory");
 }
+// The first lanes of a warp fetch the maps that this launch uses.
+__device__ __forceinline__ void prefetch_maps(const AttendParams& p, const WorkSet& set, int lane) {
+  if (lane < 2 && p.pages && set.seqs) tc::tma_prefetch_desc(lane == 0 ? &p.tm_k : &p.tm_v);
+  if (lane >= 2 && lane < 4 && p.fan && (set.prefixes || set.joint)) tc::tma_prefetch_desc(lane == 2 ? &p.tm_pk : &p.tm_pv);
+}
 // Bit 0: the lower bf16 of the pair is an infinity or NaN; bit 1: the upper.
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t x) {
   return ((x & 0x7f80u) == 0x7f80u ? 1u : 0u) | ((x & 0x7f800000u) == 0x7f800000u ? 2u : 0u);

@@ -591,45 +591,50 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
 }
 
 __global__ void __launch_bounds__(kWideThreads, 1) attend_wide_kernel(const __grid_constant__ AttendParams p, int early) {
-  pdl_wait();
-  // what comes next may start on an SM as soon as this kernel leaves it
-  if (early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ WideShared sh;
   const int tid = threadIdx.x, warp = tid >> 5;
   unsigned char* qbuf = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const uint32_t q_at = tc::smem_u32(qbuf), ring = q_at + 2 * kTileBytes;
-  if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      tc::mbar_init(&sh.kv_full[i], 1);
-      tc::mbar_init(&sh.kv_empty[i], 2);          // both groups' MMA warps
-    }
-    for (int w = 0; w < 2; ++w) {
-      tc::mbar_init(&sh.q_full[w], kTile);
-      tc::mbar_init(&sh.s_full[w], 1);
-      tc::mbar_init(&sh.p_full[w], kTile);
-      tc::mbar_init(&sh.o_full[w], 1);
-      tc::mbar_init(&sh.done[w], 1);
-    }
-    sh.fail = 0;
-    sh.turn = 0;
-    for (int i = 0; i < kBadSets * kBadWords; ++i) (&sh.bad[0][0])[i] = 0;
-  }
-  const Shares shares = find_shares<kWideRows, kWideTokens, kWideThreads, 1>(p, p.set, sh.scan);
-  if ((int)blockIdx.x >= shares.count) return;
-  const int count = shares.begin(blockIdx.x + 1) - shares.begin(blockIdx.x);
-  const WideCursor c = place<kWideRows, kWideTokens>(p, p.set, sh.scan.e[0], sh.scan.rest[0]);
   if (warp == 0) tc::tmem_alloc(&sh.tmem_base, 4 * kTile);
+  if (warp == 1 && (tid & 31) < kRing) {
+    tc::mbar_init(&sh.kv_full[tid & 31], 1);
+    tc::mbar_init(&sh.kv_empty[tid & 31], 2);     // both groups' MMA warps
+  }
+  if (warp == 2 && (tid & 31) < 2) {
+    const int w = tid & 31;
+    tc::mbar_init(&sh.q_full[w], kTile);
+    tc::mbar_init(&sh.s_full[w], 1);
+    tc::mbar_init(&sh.p_full[w], kTile);
+    tc::mbar_init(&sh.o_full[w], 1);
+    tc::mbar_init(&sh.done[w], 1);
+  }
+  if (warp == 3) prefetch_maps(p, p.set, tid & 31);
+  if (warp > 3) {
+    for (int i = tid - 128; i < kBadSets * kBadWords; i += kWideThreads - 128) (&sh.bad[0][0])[i] = 0;
+    if (tid == 128) sh.fail = sh.turn = 0;
+  }
+  pdl_wait();
+  // what comes next may start on an SM as soon as this kernel leaves it
+  if (early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Shares shares = find_shares<kWideRows, kWideTokens, kWideThreads, 1>(p, p.set, sh.scan);
+  const int mine = blockIdx.x;
+  const int count = mine < shares.count ? shares.begin(mine + 1) - shares.begin(mine) : 0;
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem_base;
-  if (warp == kTmaWarp) producer(p, sh, c, count, ring);
-  else if (warp >= kMmaWarp) {
-    if ((tid & 31) == 0) mma_issuer(p, sh, c, count, warp - kMmaWarp, tmem, q_at, ring);
-    __syncwarp();
+  if (count > 0) {
+    const WideCursor c = place<kWideRows, kWideTokens>(p, p.set, sh.scan.e[0], sh.scan.rest[0]);
+    if (warp == kTmaWarp) {
+      producer(p, sh, c, count, ring);
+    } else if (warp >= kMmaWarp) {
+      if ((tid & 31) == 0) mma_issuer(p, sh, c, count, warp - kMmaWarp, tmem, q_at, ring);
+      __syncwarp();
+    } else {
+      softmax_group(p, sh, c, count, warp >> 2, tid & (kTile - 1), tmem, qbuf, ring);
+    }
   }
-  else softmax_group(p, sh, c, count, warp >> 2, tid & (kTile - 1), tmem, qbuf, ring);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
