@@ -4,7 +4,7 @@
 // over the rows a query sees, in one pass over K and V with a running maximum
 // and sum; logits are kept in base 2 (scale * log2 e), so p = 2^(x - m).
 //
-// attend_kernel (units of up to 32 query rows): persistent, one CTA per SM. All
+// attend_kernel (units of up to 16 query rows): persistent, one CTA per SM. All
 // the rows of K and V that the batch reads, prefix and pages alike, are laid
 // end to end in boxes of 16 rows, and every warp of the grid takes an equal
 // share of them, whatever the sequences' lengths are: the lengths live on the
@@ -12,9 +12,8 @@
 // itself from there on: its own ring of TMA boxes (16 rows of K and of V, 8
 // KB; a box never crosses a page), its own running maximum, sum and output,
 // and no barrier, so that one warp's start or end of a unit hides behind the
-// others' rows. Queries are the rows of m16n8k16 products (one or two tiles of
-// 16). Bound: HBM; a warp has a box or two in flight while it computes on
-// another (96 to 128 KB an SM).
+// others' rows. Queries are the rows of m16n8k16 products. Bound: HBM; a warp
+// has one box in flight while it computes on another (96 KB an SM).
 //
 // attend_wide_kernel (attend_wide.cu): units of more query rows.
 //
@@ -41,10 +40,10 @@ namespace {
 
 constexpr int kBoxBytes = kBoxTokens * kHeadDim * 2;       // of K or of V
 
-// Warps and boxes of a warp's ring for `tiles` tiles of 16 query rows, by the registers they take.
-__host__ __device__ constexpr int few_warps(int tiles) { return tiles == 1 ? 12 : 8; }
-__host__ __device__ constexpr int few_stages(int tiles) { return tiles == 1 ? 2 : 3; }
-constexpr int few_smem(int tiles) { return few_warps(tiles) * few_stages(tiles) * 2 * kBoxBytes + 1024; }
+constexpr int kRows = 16;                         // query rows of a unit
+constexpr int kWarps = 12;
+constexpr int kStages = 2;                        // boxes of a warp's ring
+constexpr int kFewSmem = kWarps * kStages * 2 * kBoxBytes + 1024;
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -61,31 +60,16 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Four lanes with four words each: lane i's word j and lane j's word i change places.
-__device__ __forceinline__ void quad_transpose(uint4& v, int lane) {
-  const bool o1 = lane & 1, o2 = lane & 2;
-  uint32_t a = __shfl_xor_sync(0xffffffffu, o1 ? v.x : v.y, 1), b = __shfl_xor_sync(0xffffffffu, o1 ? v.z : v.w, 1);
-  if (o1) v.x = a, v.z = b;
-  else v.y = a, v.w = b;
-  a = __shfl_xor_sync(0xffffffffu, o2 ? v.x : v.z, 2);
-  b = __shfl_xor_sync(0xffffffffu, o2 ? v.y : v.w, 2);
-  if (o2) v.x = a, v.y = b;
-  else v.z = a, v.w = b;
-}
-
-template <int kTiles>
 struct FewShared {
-  uint64_t full[few_warps(kTiles)][few_stages(kTiles)];
+  uint64_t full[kWarps][kStages];
   ScanShared scan;
   int fail;
 };
 
-template <int kTiles>
-__global__ void __launch_bounds__(few_warps(kTiles) * 32, 1) attend_kernel(const __grid_constant__ AttendParams p) {
-  constexpr int kRows = 16 * kTiles, kWarps = few_warps(kTiles), kStages = few_stages(kTiles);
+__global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_constant__ AttendParams p) {
   using Cur = Cursor<kRows, kBoxTokens>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ FewShared<kTiles> sh;
+  __shared__ FewShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = ((tc::smem_u32(smem_raw) + 1023) & ~1023u) + warp * kStages * 2 * kBoxBytes;
   const WorkSet& set = p.set;
@@ -143,52 +127,50 @@ __global__ void __launch_bounds__(few_warps(kTiles) * 32, 1) attend_kernel(const
     while (left > 0) {
       const int boxes = min(cur.k.steps - cur.step, left);
       const bool own = cur.k.s >= set.prefixes;
-      // this lane's queries (rows lane / 4 and 8 on of each tile) and the last row each sees
-      uint32_t q[kTiles][8][4];
-      float o[kTiles][16][4], mx[kTiles][2], sum[kTiles][2];
-      int last[kTiles][2], low = 0;
+      // this lane's queries (rows lane / 4 and 8 on) and the last row each sees
+      uint32_t q[8][4];
+      float o[16][4], mx[2], sum[2];
+      int last[2], low = 0;
 
 #pragma unroll 1
       for (int i = 0; i < boxes; ++i) {
         __syncwarp();                             // every lane has read the box that the next one replaces
+        const int room = i == 0 ? kStages - 1 : kStages;           // a unit's queries pass through a stage first
 #pragma unroll 1
-        while (flying < kStages && ahead_left > 0 && !dead) {
+        while (flying < room && ahead_left > 0 && !dead) {
           request(requested);
           requested = requested == kStages - 1 ? 0 : requested + 1;
           ++flying;
         }
         if (i == 0) {
-#pragma unroll
-          for (int x = 0; x < kTiles; ++x)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const QueryRow r = query_row<kRows>(p, set, cur.k, 16 * x + (lane >> 2) + 8 * k);
-              const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)r.b * p.qb +
-                                                                (long long)(cur.h * p.group + r.g) * p.qh +
-                                                                (long long)r.t * p.qm) + (lane & 3);
-              uint4 c[4];                         // chunks (lane % 4) + 4 i of the row
-#pragma unroll
-              for (int i = 0; i < 4; ++i) c[i] = r.real ? src[4 * i] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {       // to word (lane % 4) of chunks 4 i .. 4 i + 3
-                quad_transpose(c[i], lane);
-                q[x][2 * i][k] = c[i].x;
-                q[x][2 * i][2 + k] = c[i].y;
-                q[x][2 * i + 1][k] = c[i].z;
-                q[x][2 * i + 1][2 + k] = c[i].w;
-              }
-              last[x][k] = !own ? cur.k.pre - 1 : r.real ? cur.k.len - cur.k.n + r.t : -1;
-            }
-#pragma unroll
-          for (int x = 0; x < kTiles; ++x) {
-            mx[x][0] = mx[x][1] = -INFINITY;
-            sum[x][0] = sum[x][1] = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[x][j][k] = 0.f;
+          const uint32_t at = ring + requested * 2 * kBoxBytes;
+#pragma unroll 4
+          for (int e = lane; e < kRows * 16; e += 32) {
+            const QueryRow r = query_row<kRows>(p, set, cur.k, e >> 4);
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (r.real)
+              x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)r.b * p.qb +
+                                                 (long long)(cur.h * p.group + r.g) * p.qh + (long long)r.t * p.qm)[e & 15];
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + tc::sw128_offset(e >> 4, e & 15, kRows)),
+                         "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
           }
-          low = __shfl_sync(0xffffffffu, last[0][0], 0);           // the first row's: the lowest
+          __syncwarp();
+          const uint32_t q_at = at + tc::sw128_offset(lane & 15, lane >> 4, kRows);
+#pragma unroll
+          for (int s = 0; s < 8; ++s) ldsm4((q_at ^ ((s & 3) * 32)) + (s >> 2) * (kRows * 128), q[s]);
+          tc::fence_proxy_async_smem();           // the stage's next content comes by TMA
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int t = p.by_group.div(cur.k.tile * kRows + (lane >> 2) + 8 * k);
+            last[k] = !own ? cur.k.pre - 1 : t < cur.k.n ? cur.k.len - cur.k.n + t : -1;
+            mx[k] = -INFINITY;
+            sum[k] = 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
+          low = __shfl_sync(0xffffffffu, last[0], 0);              // the first row's: the lowest
         }
         if (!dead) {
           const bool ok = wait_phase(&sh.full[warp][stage], parity, &sh.fail, p.err);
@@ -208,72 +190,64 @@ __global__ void __launch_bounds__(few_warps(kTiles) * 32, 1) attend_kernel(const
         if (dead) continue;
 
         const bool full = row0 + kBoxTokens - 1 <= low;            // every query sees every row
-        float z[kTiles][2][4];
+        float z[2][4];
 #pragma unroll
-        for (int x = 0; x < kTiles; ++x)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) z[x][j][k] = 0.f;
+          for (int k = 0; k < 4; ++k) z[j][k] = 0.f;
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
           uint32_t k4[4];
           ldsm4(((kb + k_at) ^ ((s & 3) * 32)) + (s >> 2) * (kBoxTokens * 128), k4);
+          mma16816(z[0], q[s], k4[0], k4[1]);
+          mma16816(z[1], q[s], k4[2], k4[3]);
+        }
+        float rm[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int x = 0; x < kTiles; ++x) {
-            mma16816(z[x][0], q[x][s], k4[0], k4[1]);
-            mma16816(z[x][1], q[x][s], k4[2], k4[3]);
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float v = z[j][k] * p.scale2;
+            if (!full && row0 + 8 * j + 2 * (lane & 3) + (k & 1) > last[k >> 1]) v = -INFINITY;
+            z[j][k] = v;
+            rm[k >> 1] = fmaxf(rm[k >> 1], v);
+          }
+        // the running maximum moves only when a logit passes it
+        if (__any_sync(0xffffffffu, rm[0] > mx[0] || rm[1] > mx[1])) {
+          float f[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            rm[k] = fmaxf(rm[k], __shfl_xor_sync(0xffffffffu, rm[k], 1));
+            rm[k] = fmaxf(rm[k], __shfl_xor_sync(0xffffffffu, rm[k], 2));
+            const float nm = fmaxf(mx[k], rm[k]);
+            f[k] = weight_of(mx[k], nm);
+            mx[k] = nm;
+            sum[k] *= f[k];
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            o[j][0] *= f[0];
+            o[j][1] *= f[0];
+            o[j][2] *= f[1];
+            o[j][3] *= f[1];
           }
         }
-        uint32_t hi[kTiles][4], lo[kTiles][4];
+        const float m0 = base_of(mx[0]), m1 = base_of(mx[1]);
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int x = 0; x < kTiles; ++x) {
-          float rm[2] = {-INFINITY, -INFINITY};
+        for (int j = 0; j < 2; ++j) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int k = 0; k < 4; ++k) z[j][k] = ex2(z[j][k] - (k < 2 ? m0 : m1));
+          sum[0] += z[j][0] + z[j][1];
+          sum[1] += z[j][2] + z[j][3];
+          // weights as bf16 pairs hi + lo: 16 bits of each, so that their rounding does not add to the
+          // output's own (the tensor cores wait for memory here anyway)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float v = z[x][j][k] * p.scale2;
-              if (!full && row0 + 8 * j + 2 * (lane & 3) + (k & 1) > last[x][k >> 1]) v = -INFINITY;
-              z[x][j][k] = v;
-              rm[k >> 1] = fmaxf(rm[k >> 1], v);
-            }
-          // the running maximum moves only when a logit passes it (it needs not be the lane's own)
-          if (__any_sync(0xffffffffu, rm[0] > mx[x][0] || rm[1] > mx[x][1])) {
-            float f[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              rm[k] = fmaxf(rm[k], __shfl_xor_sync(0xffffffffu, rm[k], 1));
-              rm[k] = fmaxf(rm[k], __shfl_xor_sync(0xffffffffu, rm[k], 2));
-              const float nm = fmaxf(mx[x][k], rm[k]);
-              f[k] = weight_of(mx[x][k], nm);
-              mx[x][k] = nm;
-              sum[x][k] *= f[k];
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              o[x][j][0] *= f[0];
-              o[x][j][1] *= f[0];
-              o[x][j][2] *= f[1];
-              o[x][j][3] *= f[1];
-            }
-          }
-          const float m0 = base_of(mx[x][0]), m1 = base_of(mx[x][1]);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) z[x][j][k] = ex2(z[x][j][k] - (k < 2 ? m0 : m1));
-            sum[x][0] += z[x][j][0] + z[x][j][1];
-            sum[x][1] += z[x][j][2] + z[x][j][3];
-            // weights as bf16 pairs hi + lo: 16 bits of each, so that their rounding does not
-            // add to the output's own (the tensor cores wait for memory here anyway)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float a = z[x][j][2 * k], b = z[x][j][2 * k + 1];
-              const uint32_t h2 = pack_bf16(a, b);
-              hi[x][2 * j + k] = h2;
-              lo[x][2 * j + k] = pack_bf16(a - __uint_as_float(h2 << 16), b - __uint_as_float(h2 & 0xffff0000u));
-            }
+          for (int k = 0; k < 2; ++k) {
+            const float a = z[j][2 * k], b = z[j][2 * k + 1];
+            const uint32_t h2 = pack_bf16(a, b);
+            hi[2 * j + k] = h2;
+            lo[2 * j + k] = pack_bf16(a - __uint_as_float(h2 << 16), b - __uint_as_float(h2 & 0xffff0000u));
           }
         }
         // V of rows behind the stream's end may hold anything: zeros in its place
@@ -306,33 +280,27 @@ __global__ void __launch_bounds__(few_warps(kTiles) * 32, 1) attend_kernel(const
           uint32_t v4[4];
           ldsm4_t(((kb + v_at) ^ ((j & 3) * 32)) + (j >> 2) * (kBoxTokens * 128), v4);
           if (!full) v4[0] &= keep0, v4[1] &= keep1, v4[2] &= keep0, v4[3] &= keep1;
-#pragma unroll
-          for (int x = 0; x < kTiles; ++x) {
-            mma16816(o[x][2 * j], hi[x], v4[0], v4[1]);
-            mma16816(o[x][2 * j + 1], hi[x], v4[2], v4[3]);
-            mma16816(o[x][2 * j], lo[x], v4[0], v4[1]);
-            mma16816(o[x][2 * j + 1], lo[x], v4[2], v4[3]);
-          }
+          mma16816(o[2 * j], hi, v4[0], v4[1]);
+          mma16816(o[2 * j + 1], hi, v4[2], v4[3]);
+          mma16816(o[2 * j], lo, v4[0], v4[1]);
+          mma16816(o[2 * j + 1], lo, v4[2], v4[3]);
         }
 #pragma unroll 1
         for (; bad; bad &= bad - 1) {             // rare
           const int k = __ffs(bad) - 1, from = (lane & 28) | ((k & 7) >> 1);
+          const float a0 = k & 1 ? z[0][1] : z[0][0], a1 = k & 1 ? z[1][1] : z[1][0];
+          const float b0 = k & 1 ? z[0][3] : z[0][2], b1 = k & 1 ? z[1][3] : z[1][2];
+          const float w0 = __shfl_sync(0xffffffffu, k & 8 ? a1 : a0, from);
+          const float w1 = __shfl_sync(0xffffffffu, k & 8 ? b1 : b0, from);
+          const bool s0 = row0 + k <= last[0], s1 = row0 + k <= last[1];
 #pragma unroll
-          for (int x = 0; x < kTiles; ++x) {
-            const float a0 = k & 1 ? z[x][0][1] : z[x][0][0], a1 = k & 1 ? z[x][1][1] : z[x][1][0];
-            const float b0 = k & 1 ? z[x][0][3] : z[x][0][2], b1 = k & 1 ? z[x][1][3] : z[x][1][2];
-            const float w0 = __shfl_sync(0xffffffffu, k & 8 ? a1 : a0, from);
-            const float w1 = __shfl_sync(0xffffffffu, k & 8 ? b1 : b0, from);
-            const bool s0 = row0 + k <= last[x][0], s1 = row0 + k <= last[x][1];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              uint32_t v;
-              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v)
-                           : "r"(kb + kBoxBytes + tc::sw128_offset(k, j, kBoxTokens) + 4 * (lane & 3)) : "memory");
-              const float v0 = __uint_as_float(v << 16), v1 = __uint_as_float(v & 0xffff0000u);
-              if (s0) o[x][j][0] += w0 * v0, o[x][j][1] += w0 * v1;
-              if (s1) o[x][j][2] += w1 * v0, o[x][j][3] += w1 * v1;
-            }
+          for (int j = 0; j < 16; ++j) {
+            uint32_t v;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v)
+                         : "r"(kb + kBoxBytes + tc::sw128_offset(k, j, kBoxTokens) + 4 * (lane & 3)) : "memory");
+            const float v0 = __uint_as_float(v << 16), v1 = __uint_as_float(v & 0xffff0000u);
+            if (s0) o[j][0] += w0 * v0, o[j][1] += w0 * v1;
+            if (s1) o[j][2] += w1 * v0, o[j][3] += w1 * v1;
           }
         }
       }
@@ -341,20 +309,18 @@ __global__ void __launch_bounds__(few_warps(kTiles) * 32, 1) attend_kernel(const
       const size_t slot = (size_t)(cur.unit + share) * kRows;
       const int rows = min(kRows, cur.k.n * p.group - cur.k.tile * kRows);
 #pragma unroll
-      for (int x = 0; x < kTiles; ++x)
+      for (int k = 0; k < 2; ++k) {
+        float t = sum[k];
+        t += __shfl_xor_sync(0xffffffffu, t, 1);
+        t += __shfl_xor_sync(0xffffffffu, t, 2);
+        const int r = (lane >> 2) + 8 * k;
+        if (r < rows) {
+          if ((lane & 3) == 0) set.part_ml[slot + r] = make_float2(mx[k], t);
+          float2* dst = reinterpret_cast<float2*>(set.part_o + (slot + r) * kHeadDim) + (lane & 3);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float t = sum[x][k];
-          t += __shfl_xor_sync(0xffffffffu, t, 1);
-          t += __shfl_xor_sync(0xffffffffu, t, 2);
-          const int r = 16 * x + (lane >> 2) + 8 * k;
-          if (r < rows) {
-            if ((lane & 3) == 0) set.part_ml[slot + r] = make_float2(mx[x][k], t);
-            float2* dst = reinterpret_cast<float2*>(set.part_o + (slot + r) * kHeadDim) + (lane & 3);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) dst[4 * j] = make_float2(o[x][j][2 * k], o[x][j][2 * k + 1]);
-          }
+          for (int j = 0; j < 16; ++j) dst[4 * j] = make_float2(o[j][2 * k], o[j][2 * k + 1]);
         }
+      }
       left -= boxes;
       if (left > 0) cur.next_unit(p, set, blocks);
     }
@@ -372,14 +338,14 @@ struct Parts {
   __device__ int parts() const { return count << twice; }
 };
 
-// Row r of block e (its tile) and head h.
-template <int kRows>
-__device__ __forceinline__ Parts find_parts(const AttendParams& p, const WorkSet& set, int e, int h, int r, int block_rows) {
-  const int g0 = set.base[e], steps = (set.base[e + 1] - g0) / p.hkv;
+// Row r of block e (its tile, of `rows` rows) and head h.
+__device__ __forceinline__ Parts find_parts(const AttendParams& p, const WorkSet& set, int rows, int e, int h, int r,
+                                            int block_rows) {
+  const int g0 = set.base[e], steps = p.by_hkv.div(set.base[e + 1] - g0);
   const Shares shares(set, set.base[set.blocks()]);
   const int g = g0 + h * steps;
   const int c0 = shares.of(g), c1 = shares.of(g + steps - 1);
-  return Parts{set.part_ml, set.part_o, e * p.hkv + h + c0, c1 - c0 + 1, kRows, r, kRows == kWideRows && block_rows <= 128};
+  return Parts{set.part_ml, set.part_o, e * p.hkv + h + c0, c1 - c0 + 1, rows, r, rows == kWideRows && block_rows <= 128};
 }
 
 constexpr int kJoinWarps = 8;
@@ -430,7 +396,7 @@ struct Merge {
 // Every output row: the parts of its prefix unit and of its own. kSplit warps share a row's parts
 // (few rows have many parts each, and one warp would wait for memory part after part) and their
 // results meet in shared memory, in the order of the warps.
-template <int kRows, int kSplit>
+template <int kSplit>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const __grid_constant__ AttendParams p) {
   __shared__ float4 acc[kJoinWarps][32];
   __shared__ float2 ml[kJoinWarps];
@@ -438,34 +404,30 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const __gr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % kSplit;
   const int row = blockIdx.x * (kJoinWarps / kSplit) + warp / kSplit;
   const bool in = row < p.batch * p.hq * p.m;
-  const int bh = row / p.m, t = row - bh * p.m, b = in ? bh / p.hq : 0, hq = bh - b * p.hq;
+  const int bh = in ? p.by_m.div(row) : 0, t = row - bh * p.m, b = p.by_hq.div(bh), hq = bh - b * p.hq;
   const Seq q = sequence(p, b, in && !p.pages && t == 0 && hq == 0 && lane == 0 && part == 0);
   const bool real = in && t < q.n;
   Merge m;
   bool sees = false;
   if (real) {
-    const int h = hq / p.group, g = hq - h * p.group;
-    if (p.fan) {
-      const int s = b / p.fan, before = tokens_before(p, s * p.fan);
-      const int r = (tokens_before(p, b) - before + t) * p.group + g;
-      Parts x;
-      if (p.wide.prefixes) {
-        const int all = (tokens_before(p, (s + 1) * p.fan) - before) * p.group, tile = r / kWideRows;
-        x = find_parts<kWideRows>(p, p.wide, s * p.wide.prefix_tiles + tile, h, r % kWideRows, all - tile * kWideRows);
-      } else {
-        x = find_parts<kRows>(p, p.set, s * p.set.prefix_tiles + r / kRows, h, r % kRows, 0);
+    const int h = p.by_group.div(hq), g = hq - h * p.group;
+#pragma unroll 1
+    for (int part_of = 0; part_of < 2; ++part_of) {                // the prefix's rows, its own
+      int r = t * p.group + g, all = q.n * p.group, s = b;
+      if (part_of == 0) {
+        if (!p.fan) continue;
+        s = p.by_fan.div(b);
+        const int before = tokens_before(p, s * p.fan);
+        r += (tokens_before(p, b) - before) * p.group;
+        all = (tokens_before(p, (s + 1) * p.fan) - before) * p.group;
+      } else if (q.len - q.n + t < 0 || q.len == 0) {
+        continue;
       }
-      m.add_parts(x, part, kSplit);
-      sees = true;
-    }
-    if (q.len - q.n + t >= 0 && q.len > 0) {
-      const int r = t * p.group + g;
-      Parts x;
-      if (p.wide.seqs)                            // at most 128 rows of a sequence: one tile
-        x = find_parts<kWideRows>(p, p.wide, p.wide.prefixes * p.wide.prefix_tiles + b, h, r, q.n * p.group);
-      else
-        x = find_parts<kRows>(p, p.set, p.set.prefixes * p.set.prefix_tiles + b * p.set.seq_tiles + r / kRows, h, r % kRows, 0);
-      m.add_parts(x, part, kSplit);
+      const bool wide = part_of == 0 ? p.wide.prefixes > 0 : p.wide.seqs > 0;
+      const WorkSet& set = wide ? p.wide : p.set;
+      const int rows = wide ? kWideRows : kRows, tile = wide ? r / kWideRows : r / kRows;
+      const int e = part_of == 0 ? s * set.prefix_tiles + tile : set.prefixes * set.prefix_tiles + s * set.seq_tiles + tile;
+      m.add_parts(find_parts(p, set, rows, e, h, r - tile * rows, all - tile * rows), part, kSplit);
       sees = true;
     }
   }
@@ -482,39 +444,27 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const __gr
   if (real) m.write(p, b, t, hq, sees);
 }
 
-// Joint units: only those that two or more CTAs share have parts to merge. Block (c, y) takes 32 rows of
-// the unit that share c + 1 begins inside, where that is the first share to begin inside it.
+// Joint units: only those that two or more CTAs share have parts to merge. Block (c, y) takes eight
+// rows of the unit that share c + 1 begins inside, where that is the first share to begin inside it.
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_split_kernel(const __grid_constant__ AttendParams p) {
   pdl_wait();
   const WorkSet& set = p.wide;
-  const int blocks = set.blocks();
-  const Shares shares(set, set.base[blocks]);
+  const Shares shares(set, set.base[set.blocks()]);
   const int c = blockIdx.x + 1;
   if (c >= shares.count) return;
-  const int begin = shares.begin(c);
-  int lo = 0, hi = blocks;                        // the last block that begins at or before this step
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (set.base[mid] <= begin) lo = mid;
-    else hi = mid;
-  }
+  const int2 at = set.start[c];
   Block k;
-  load_block<kWideRows, kWideTokens>(p, set, lo, k);
-  const int h = (begin - set.base[lo]) / k.steps, r = begin - set.base[lo] - h * k.steps;
+  load_block<kWideRows, kWideTokens>(p, set, at.x, k);
+  const int h = at.y / k.steps, r = at.y - h * k.steps;
   if (r == 0) return;                             // the share begins with the unit
-  const int first = begin - r;                    // the unit's first step
+  const int first = shares.begin(c) - r;          // the unit's first step
   if (c > 1 && shares.begin(c - 1) > first) return;
-  const int c1 = shares.of(first + k.steps - 1);
-  Parts part = {set.part_ml, set.part_o, lo * p.hkv + h + c - 1, c1 - (c - 1) + 1, kWideRows, 0, 0};
-#pragma unroll 1
-  for (int i = threadIdx.x >> 5; i < 32; i += kJoinWarps) {
-    part.row = blockIdx.y * 32 + i;
-    const QueryRow q = query_row<kWideRows>(p, set, k, part.row);
-    if (!q.real) continue;
-    Merge m;
-    m.add_parts(part, 0, 1);
-    m.write(p, q.b, q.t, h * p.group + q.g, k.pre > 0 || k.len - k.n + q.t >= 0);
-  }
+  const int c1 = shares.of(first + k.steps - 1), row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  const QueryRow q = query_row<kWideRows>(p, set, k, row);
+  if (!q.real) return;
+  Merge m;
+  m.add_parts(Parts{set.part_ml, set.part_o, at.x * p.hkv + h + c - 1, c1 - (c - 1) + 1, kWideRows, row, 0}, 0, 1);
+  m.write(p, q.b, q.t, h * p.group + q.g, k.pre > 0 || k.len - k.n + q.t >= 0);
 }
 
 // Boxes of `rows_box` rows of `halves` halves of 64 elements, each row 128 bytes, 128-byte swizzle.
@@ -532,12 +482,11 @@ bool encode_boxes(CUtensorMap* tm, const void* base, int rows, int heads, long l
 bool multiple(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Query rows from which the wide kernel takes a unit, and above which a sequence fills one.
-constexpr int kWideFrom = 33, kJointFrom = 128;
+constexpr int kWideFrom = kRows + 1, kJointFrom = 128;
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Plan {
-  int few_tiles;            // query tiles of 16 rows of a unit of the few-row kernel
   int sms;
   WorkSet few, wide;        // counts, and offsets into the workspace in place of pointers
   size_t bytes;
@@ -553,6 +502,7 @@ void lay_out(WorkSet& s, int kv_heads, int rows, size_t& off) {
   if (s.blocks() == 0) return;
   const size_t slots = (size_t)s.blocks() * kv_heads + s.max_shares;
   s.base = reinterpret_cast<int*>(take((size_t)(s.blocks() + 1) * sizeof(int)));
+  s.start = reinterpret_cast<int2*>(take((size_t)s.max_shares * sizeof(int2)));
   s.part_ml = reinterpret_cast<float2*>(take(slots * rows * sizeof(float2)));
   s.part_o = reinterpret_cast<float*>(take(slots * rows * kHeadDim * sizeof(float)));
 }
@@ -560,6 +510,7 @@ template <typename T>
 void rebase(T*& x, char* base) { x = reinterpret_cast<T*>(base + reinterpret_cast<size_t>(x)); }
 void rebase(WorkSet& s, char* base) {
   rebase(s.base, base);
+  rebase(s.start, base);
   rebase(s.part_ml, base);
   rebase(s.part_o, base);
 }
@@ -600,31 +551,29 @@ int make_plan(const evict_attention* a, Plan* out) {
     if (pre) (pre_rows >= kWideFrom ? P.wide : P.few).prefixes = a->prefix_batch;
     if (a->pages) (own_rows >= kWideFrom ? P.wide : P.few).seqs = a->batch;
   }
-  const int few_rows = std::max(P.few.prefixes ? pre_rows : 0, P.few.seqs ? own_rows : 0);
-  // One tile of 16 query rows where that holds every row; two (each box of K and V then serves
-  // twice the rows) otherwise.
-  P.few_tiles = few_rows <= 16 ? 1 : 2;
   const long long seq_tokens = a->pages ? (long long)a->pages->table_width * a->pages->page_size : 0;
   auto tiles = [&](WorkSet& s, int rows, int tokens) {
     s.prefix_tiles = (pre_rows + rows - 1) / rows;
     s.seq_tiles = (own_rows + rows - 1) / rows;
+    s.by_prefix_tiles = Divisor(s.prefix_tiles);
+    s.by_seq_tiles = Divisor(s.seq_tiles);
     const long long pre_steps = (a->n_prefix + tokens - 1) / tokens, seq_steps = (seq_tokens + tokens - 1) / tokens + 1;
     const long long work = ((long long)s.prefixes * s.prefix_tiles * pre_steps +
                             (long long)s.seqs * s.seq_tiles * (seq_steps + (s.joint ? pre_steps : 0))) * a->n_kv_heads;
     return work < (1ll << 31) && ((long long)s.blocks() + 1) * a->n_kv_heads < (1ll << 30);
   };
-  if (!tiles(P.few, 16 * P.few_tiles, kBoxTokens) || !tiles(P.wide, kWideRows, kWideTokens))
+  if (!tiles(P.few, kRows, kBoxTokens) || !tiles(P.wide, kWideRows, kWideTokens))
     return fail(EVICT_ELIMIT, "the batch's heads and rows (to the tables' width) are too many for one call");
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P.sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e, "looking up the device");
-  P.few.max_shares = P.sms * few_warps(P.few_tiles);
+  P.few.max_shares = P.sms * kWarps;
   P.few.min_steps = kFewMinBoxes;
   P.wide.max_shares = P.sms;
   P.wide.min_steps = kWideMinSteps;
   size_t off = kWorkHead + round256((size_t)(a->batch + 1) * sizeof(int));
-  lay_out(P.few, a->n_kv_heads, 16 * P.few_tiles, off);
+  lay_out(P.few, a->n_kv_heads, kRows, off);
   lay_out(P.wide, a->n_kv_heads, kWideRows, off);
   P.bytes = off;
   return EVICT_OK;
@@ -700,6 +649,11 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
     P.fan = a->batch / a->prefix_batch;
     P.n_prefix = a->n_prefix;
   }
+  P.by_m = Divisor(P.m);
+  P.by_hq = Divisor(P.hq);
+  P.by_hkv = Divisor(P.hkv);
+  P.by_group = Divisor(P.group);
+  P.by_fan = Divisor(P.fan);
   P.scale2 = (a->scale == 0.f ? 0.08838834764831845f : a->scale) * kLog2e;
   P.n_new = a->n_new;
   const evict_pages* g = a->pages;
@@ -750,24 +704,20 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
   P.wide = plan.wide;
   if (few) {
     if ((rc = encode(false, plan.few))) return rc;
-    auto go = [&](auto kernel, int tiles) {
-      const cudaError_t x = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem(tiles));
-      return x != cudaSuccess ? x : launch_pdl(kernel, dim3(plan.sms), dim3(few_warps(tiles) * 32), few_smem(tiles), st, nullptr, P);
-    };
-    e = plan.few_tiles == 1 ? go(attend_kernel<1>, 1) : go(attend_kernel<2>, 2);
+    e = cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+    if (e == cudaSuccess) e = launch_pdl(attend_kernel, dim3(plan.sms), dim3(kWarps * 32), kFewSmem, st, nullptr, P);
     if (e != cudaSuccess) return cuda_fail(e, "attention kernel launch");
     g_launches.fetch_add(1);
   }
   if (plan.wide.joint) {
     if (plan.sms > 1)
-      e = launch_pdl(attend_join_split_kernel, dim3(plan.sms - 1, kWideRows / 32), dim3(kJoinWarps * 32), 0, st, nullptr, P);
+      e = launch_pdl(attend_join_split_kernel, dim3(plan.sms - 1, kWideRows / kJoinWarps), dim3(kJoinWarps * 32), 0, st, nullptr, P);
   } else {
-    // four warps a row while that is no more than two waves of blocks
-    const int rows = a->batch * a->n_q_heads * a->m, split = rows <= plan.sms * 8 * 2 * (kJoinWarps / 4) ? 4 : 1;
+    // four warps a row while the rows are few
+    const int rows = a->batch * a->n_q_heads * a->m, split = rows <= plan.sms * kJoinWarps ? 4 : 1;
     const dim3 grid((rows * split + kJoinWarps - 1) / kJoinWarps), block(kJoinWarps * 32);
-    auto go = [&](auto kernel) { return launch_pdl(kernel, grid, block, 0, st, nullptr, P); };
-    if (plan.few_tiles == 1) e = split == 4 ? go(attend_join_kernel<16, 4>) : go(attend_join_kernel<16, 1>);
-    else e = split == 4 ? go(attend_join_kernel<32, 4>) : go(attend_join_kernel<32, 1>);
+    e = split == 4 ? launch_pdl(attend_join_kernel<4>, grid, block, 0, st, nullptr, P)
+                   : launch_pdl(attend_join_kernel<1>, grid, block, 0, st, nullptr, P);
   }
   g_launches.fetch_add(1);
   return e == cudaSuccess ? EVICT_OK : cuda_fail(e, "attention kernel launch");

@@ -68,13 +68,13 @@ __device__ __forceinline__ void load_block(const AttendParams& p, const WorkSet&
                                            bool report = false) {
   const int pe = set.prefixes * set.prefix_tiles;
   if (e < pe) {
-    k.s = e / set.prefix_tiles;
+    k.s = set.by_prefix_tiles.div(e);
     k.tile = e - k.s * set.prefix_tiles;
     k.n = tokens_before(p, (k.s + 1) * p.fan) - tokens_before(p, k.s * p.fan);
     k.len = 0;
     k.pre = p.n_prefix;
   } else {
-    const int b = set.seq_tiles == 1 ? e - pe : (e - pe) / set.seq_tiles;
+    const int b = set.by_seq_tiles.div(e - pe);
     k.s = set.prefixes + b;
     k.tile = e - pe - b * set.seq_tiles;
     const Seq q = sequence(p, b, report && k.tile == 0);
@@ -86,7 +86,7 @@ __device__ __forceinline__ void load_block(const AttendParams& p, const WorkSet&
   k.steps = 0;
   if (kRows * k.tile < k.n * p.group) {
     if (k.len > 0) {
-      const int t = (kRows * (k.tile + 1) - 1) / p.group;
+      const int t = p.by_group.div(kRows * (k.tile + 1) - 1);
       k.reach = max(-1, k.len - k.n + min(t, k.n - 1));
     }
     k.steps = (k.pre + kTokens - 1) / kTokens + (k.reach + kTokens) / kTokens;
@@ -212,7 +212,11 @@ __device__ __forceinline__ Shares find_shares(const AttendParams& p, const WorkS
 #pragma unroll 1
       for (int i = 0; i < kPer && first + i < shares.count; ++i) {
         const int g = shares.begin(first + i);
-        if (g >= a && g < a + w) sh.e[i] = e, sh.rest[i] = g - a;
+        if (g >= a && g < a + w) {
+          sh.e[i] = e;
+          sh.rest[i] = g - a;
+          if (set.start) set.start[first + i] = make_int2(e, g - a);
+        }
       }
       a += w;
     }
@@ -241,7 +245,7 @@ struct QueryRow {
 template <int kRows>
 __device__ __forceinline__ QueryRow query_row(const AttendParams& p, const WorkSet& set, const Block& k, int r) {
   const int ur = k.tile * kRows + r;
-  const int tok = ur / p.group;
+  const int tok = p.by_group.div(ur);
   QueryRow q;
   q.g = ur - tok * p.group;
   q.real = tok < k.n;
@@ -250,7 +254,7 @@ __device__ __forceinline__ QueryRow query_row(const AttendParams& p, const WorkS
   if (k.s < set.prefixes) {
     const int b0 = k.s * p.fan;
     if (!p.n_new) {
-      const int i = tok / p.m;
+      const int i = p.by_m.div(tok);
       q.b = b0 + i;
       q.t = tok - i * p.m;
     } else {

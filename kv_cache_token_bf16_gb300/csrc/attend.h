@@ -13,6 +13,23 @@ constexpr int kBoxTokens = 16;       // rows of K and V that a warp of the few-r
 constexpr int kWideTokens = 128;     // rows that a CTA of the wide kernel takes at a time
 constexpr int kWideRows = 256;       // query rows of a unit of the wide kernel (two MMA tiles)
 
+// Quotient by a divisor that the host knows, for dividends below 2^31: a multiplication and a shift.
+struct Divisor {
+  uint32_t by, mul, one, shift;
+  Divisor() = default;
+  __host__ explicit Divisor(int d) : by(d), mul(0), one(0), shift(0) {
+    if (d == 1) {
+      one = ~0u;
+    } else if (d > 1) {
+      while ((2u << shift) < by) ++shift;         // ceil(log2 d) - 1
+      mul = (uint32_t)(((1ull << (32 + shift)) + by - 1) / by);
+    }
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, mul) + ((uint32_t)n & one)) >> shift); }
+#endif
+};
+
 // The work of one kernel. A block is a tile of query rows of one stream; the
 // streams are the prefixes (all query rows of their sequences), then the
 // sequences (their own pages; `joint`: behind the prefix as well). A unit is a
@@ -27,7 +44,9 @@ struct WorkSet {
   int seqs, seq_tiles;               // streams of sequences: 0 or the batch; blocks of one
   int joint;                         // a sequence's stream begins with its prefix
   int max_shares, min_steps;         // of a share
+  Divisor by_prefix_tiles, by_seq_tiles;
   int* base;                         // [blocks + 1] first step of every block, then their total
+  int2* start;                       // [shares] block and step in it where every share begins
   float2* part_ml;                   // [slots][tile rows] running maximum (base 2) and sum
   float* part_o;                     // [slots][tile rows][128]
   __host__ __device__ int blocks() const { return prefixes * prefix_tiles + seqs * seq_tiles; }
@@ -44,6 +63,7 @@ struct AttendParams {
   long long qb, qh, qm, ob, oh, om;  // element strides
   int batch, m, hq, hkv, group;      // group = query heads of a KV head
   int prefix_batch, fan;             // prefixes, and sequences of one (fan = 0: no prefix)
+  Divisor by_m, by_hq, by_hkv, by_group, by_fan;
   int n_prefix;
   int pages;                         // the sequences have own rows
   const int32_t* table;

@@ -78,7 +78,7 @@ struct Segment {
 // The unit's first query sees own rows before this one; from here to the last query's, rows with
 // infinities or NaN in V are marked (at most 256 tokens).
 __device__ __forceinline__ int first_marked(const AttendParams& p, const WideCursor& c) {
-  return c.k.len - c.k.n + (c.k.tile * kWideRows) / p.group + 1;
+  return c.k.len - c.k.n + p.by_group.div(c.k.tile * kWideRows) + 1;
 }
 
 // A position in the ring of K and V tiles, and the parity of the phase that fills it.
@@ -99,7 +99,7 @@ __device__ void producer(const AttendParams& p, WideShared& sh, WideCursor c, in
   bool ok = true;
   while (ok) {
     const Segment g(p, c, count);
-    const int plane = c.k.s < set.prefixes ? c.k.s : p.fan ? (c.k.s - set.prefixes) / p.fan : 0;
+    const int plane = c.k.s < set.prefixes ? c.k.s : p.fan ? p.by_fan.div(c.k.s - set.prefixes) : 0;
     const int32_t* table = p.table + (long long)(c.k.s - set.prefixes) * p.table_stride;
     for (int i = 0; i < g.steps && ok; ++i) {
       const int step = c.step + i;
