@@ -142,20 +142,26 @@ __device__ void producer(const AttendParams& p, WideShared& sh, WideCursor c, in
   for (int i = 0; i < kRing && i < used; ++i) drain_phase(&sh.kv_full[i], ((used - 1 - i) / kRing) & 1, p.err);
 }
 
-// The lock of the MMA warps' turns (bounded, like every wait; the clock is read rarely).
-__device__ __forceinline__ bool take_turn(WideShared& sh, int* err) {
+// Bounds a thread's polling (the clock is read rarely).
+struct Watch {
+  uint32_t polls = 0;
   uint64_t t0 = 0;
-  for (uint32_t spins = 0; atomicCAS(&sh.turn, 0, 1) != 0; ++spins) {
-    if ((spins & 1023) != 1023) continue;
+  __device__ __forceinline__ bool go_on(WideShared& sh, int* err) {
+    if ((++polls & 1023) != 0) return true;
     if (*(volatile int*)&sh.fail) return false;
     const uint64_t t = tc::global_ns();
     if (t0 == 0) t0 = t;
-    if (t - t0 > kWaitLimitNs) {
-      *(volatile int*)&sh.fail = 1;
-      raise_device_error(err, kDevWaitTimeout);
-      return false;
-    }
+    if (t - t0 <= kWaitLimitNs) return true;
+    *(volatile int*)&sh.fail = 1;
+    raise_device_error(err, kDevWaitTimeout);
+    return false;
   }
+};
+// The lock of the MMA warps' turns.
+__device__ __forceinline__ bool take_turn(WideShared& sh, int* err) {
+  Watch watch;
+  while (atomicCAS(&sh.turn, 0, 1) != 0)
+    if (!watch.go_on(sh, err)) return false;
   return true;
 }
 __device__ __forceinline__ void end_turn(WideShared& sh) { atomicExch(&sh.turn, 0); }
@@ -204,7 +210,9 @@ __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, 
   Slot slot;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = wait_phase(bar, parity, &sh.fail, p.err); };
-  auto release = [&](int tiles) {                 // tiles of the other group's steps: this one lets go of them
+  // Tiles of the other group's steps. Both groups let go of every tile: were its user alone to do
+  // it, the other might look for a phase of its barrier that has long been over.
+  auto release = [&](int tiles) {
 #pragma unroll 1
     for (; tiles > 0 && wait(&sh.kv_full[slot.i], slot.parity); --tiles, slot.next()) tc::mbar_arrive(&sh.kv_empty[slot.i]);
   };
@@ -215,42 +223,64 @@ __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, 
     int at = 0;                                   // steps passed
 #pragma unroll 1
     for (int j = 0; j <= jobs && jobs > 0; ++j) {
-      if (j < jobs) {
-        if (g.alt && (j > 0 || w == 1)) {
-          release(2);
-          if (!ok) break;
+      if (j == 0) {
+        if (!wait(&sh.q_full[w], q_parity)) break;
+        q_parity ^= 1;
+      }
+      // What is there first is done first: the weights of the last job (its product with V frees V),
+      // the other group's tiles (let go of), the next K. With both groups on every step the product
+      // and the next S go together, under the lock.
+      bool pv = j > 0, next = j < jobs;
+      int pass = g.alt && next && (j > 0 || w == 1) ? 2 : 0;
+      at += pass / 2;
+      bool locked = false;
+      Watch watch;
+#pragma unroll 1
+      while (pv || next) {
+        if (pass > 0 && tc::mbar_try_wait(&sh.kv_full[slot.i], slot.parity)) {
+          tc::mbar_arrive(&sh.kv_empty[slot.i]);
+          slot.next();
+          --pass;
+          continue;
+        }
+        const bool k_there = next && pass == 0 && tc::mbar_try_wait(&sh.kv_full[slot.i], slot.parity);
+        if (pv && (k_there || !next || !g.two) && tc::mbar_try_wait(&sh.kv_full[v.i], v.parity) &&
+            tc::mbar_try_wait(&sh.p_full[w], p_parity)) {
+          p_parity ^= 1;
+          pv = false;
+          if (g.two && !(locked = take_turn(sh, p.err))) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          issue_pv(o_at, s_at, v_lo + v.i * (kTileBytes >> 4), v_hi, j > 1);
+          if (!next) {
+            if (locked) end_turn(sh);
+            tc::mma_commit(&sh.o_full[w]);
+          }
+          if (!next || !g.two) tc::mma_commit(&sh.kv_empty[v.i]);
+        }
+        if (!pv && k_there) {
+          if (g.two && !locked && !take_turn(sh, p.err)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          issue_qk(s_at, q_lo, k_lo + slot.i * (kTileBytes >> 4), qk_hi);
+          tc::mma_commit(&sh.s_full[w]);
+          if (g.two) end_turn(sh);
+          if (g.two && j > 0) tc::mma_commit(&sh.kv_empty[v.i]);
+          tc::mma_commit(&sh.kv_empty[slot.i]);
+          next = false;
           ++at;
+          slot.next();
+          v = slot;
+          slot.next();
+          break;
         }
-        if (!wait(&sh.kv_full[slot.i], slot.parity)) break;
-        if (j == 0) {
-          if (!wait(&sh.q_full[w], q_parity)) break;
-          q_parity ^= 1;
-        }
+        if ((pv || next) && !(ok = watch.go_on(sh, p.err))) break;
       }
-      if (j > 0) {
-        if (!wait(&sh.kv_full[v.i], v.parity) || !wait(&sh.p_full[w], p_parity)) break;
-        p_parity ^= 1;
-      }
-      if (g.two && !take_turn(sh, p.err)) {
-        ok = false;
-        break;
-      }
-      tc::fence_after_sync();
-      if (j > 0) issue_pv(o_at, s_at, v_lo + v.i * (kTileBytes >> 4), v_hi, j > 1);
-      if (j < jobs) {
-        issue_qk(s_at, q_lo, k_lo + slot.i * (kTileBytes >> 4), qk_hi);
-        tc::mma_commit(&sh.s_full[w]);
-      }
-      if (g.two) end_turn(sh);
-      if (j == jobs) tc::mma_commit(&sh.o_full[w]);
-      if (j > 0) tc::mma_commit(&sh.kv_empty[v.i]);
-      if (j < jobs) {
-        tc::mma_commit(&sh.kv_empty[slot.i]);
-        ++at;
-        slot.next();
-        v = slot;
-        slot.next();
-      }
+      if (!ok) break;
     }
     if (ok) release(2 * (g.steps - at));
     count -= g.steps;
@@ -343,15 +373,22 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
     // A group without a job in this part announces nothing (it could announce twice before the
     // MMA warp has looked once).
     if (g.jobs(w) == 0) return q;
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)q.b * p.qb +
-                                                      (long long)(cu.h * p.group + q.g) * p.qh + (long long)q.t * p.qm);
+    // two rows of the warp at a time, half a warp on each: whole lines of global memory
+    const long long mine = q.real ? (long long)q.b * p.qb + (long long)(cu.h * p.group + q.g) * p.qh + (long long)q.t * p.qm : -1;
+    const int half = (row >> 4) & 1, chunk = row & 15;
     uint4 x[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = q.real ? src[j] : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 16; ++i) {
+      const long long from = __shfl_sync(0xffffffffu, mine, 2 * i + half);
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (from >= 0) x[i] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + from)[chunk];
+    }
+    // row 2 i + half: its chunk's place is that of row `half` moved on, but for the swizzle
+    unsigned char* to = q_mine + 32 * warp * 128 + (chunk >> 3) * (kTileBytes / 2) + half * 128;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      x[j].x ^= flip, x[j].y ^= flip, x[j].z ^= flip, x[j].w ^= flip;
-      *reinterpret_cast<uint4*>(q_mine + tc::sw128_offset(row, j, kTile)) = x[j];
+    for (int i = 0; i < 16; ++i) {
+      x[i].x ^= flip, x[i].y ^= flip, x[i].z ^= flip, x[i].w ^= flip;
+      *reinterpret_cast<uint4*>(to + 2 * i * 128 + (((chunk & 7) ^ ((2 * i + half) & 7)) << 4)) = x[i];
     }
     tc::fence_proxy_async_smem();
     tc::mbar_arrive(&sh.q_full[w]);

@@ -102,6 +102,8 @@ CASES = [
     (2, 8, 2, 300, 0, 1, 128, [300, 1200], None),
     (3, 4, 1, 64, 0, 1, 32, [0, 64, 30], [64, 64, 64]),
     (2, 36, 1, 2, 700, 2, 16, [2, 450], None),
+    (32, 32, 8, 5, 2000, 1, 32, [5 + (b * 97) % 770 for b in range(32)], [(b * 7) % 6 for b in range(32)]),
+    (24, 40, 8, 1, 650, 8, 16, [(b * 131) % 500 for b in range(24)], [(b * 5) % 2 for b in range(24)]),
     (5, 2, 1, 300, 1, 1, 16, None, [300, 0, 1, 129, 128]),
 ]
 
