@@ -40,7 +40,7 @@ namespace {
 
 constexpr int kBoxBytes = kBoxTokens * kHeadDim * 2;       // of K or of V
 
-constexpr int kRows = 16;                         // query rows of a unit
+constexpr int kRows = kFewRows;
 constexpr int kWarps = 12;
 constexpr int kStages = 2;                        // boxes of a warp's ring
 constexpr int kFewSmem = kWarps * kStages * 2 * kBoxBytes + 1024;
@@ -72,14 +72,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_con
   __shared__ FewShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = ((tc::smem_u32(smem_raw) + 1023) & ~1023u) + warp * kStages * 2 * kBoxBytes;
-  const WorkSet& set = p.set;
+  const WorkSet& set = p.few;
   const int blocks = set.blocks();
 
   if (tid < kWarps * kStages) tc::mbar_init(&sh.full[tid / kStages][tid % kStages], 1);
   if (tid == 0) sh.fail = 0;
   if (warp == 1) prefetch_maps(p, set, lane);
   if (!p.late_wait) pdl_wait();
-  const Shares shares = find_shares<kRows, kBoxTokens, kWarps * 32, kWarps>(p, set, sh.scan);
+  const Shares shares = find_shares<kRows, kBoxTokens, kWideRows, kWideTokens, kWarps * 32, kWarps>(p, set, p.wide, sh.scan);
   const int share = blockIdx.x * kWarps + warp;
   if (share < shares.count) {
     int left = shares.begin(share + 1) - shares.begin(share);
@@ -342,7 +342,7 @@ struct Parts {
 __device__ __forceinline__ Parts find_parts(const AttendParams& p, const WorkSet& set, int rows, int e, int h, int r,
                                             int block_rows) {
   const int g0 = set.base[e], steps = p.by_hkv.div(set.base[e + 1] - g0);
-  const Shares shares(set, set.base[set.blocks()]);
+  const Shares shares(set);
   const int g = g0 + h * steps;
   const int c0 = shares.of(g), c1 = shares.of(g + steps - 1);
   return Parts{set.part_ml, set.part_o, e * p.hkv + h + c0, c1 - c0 + 1, rows, r, rows == kWideRows && block_rows <= 128};
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const __gr
         continue;
       }
       const bool wide = part_of == 0 ? p.wide.prefixes > 0 : p.wide.seqs > 0;
-      const WorkSet& set = wide ? p.wide : p.set;
+      const WorkSet& set = wide ? p.wide : p.few;
       const int rows = wide ? kWideRows : kRows, tile = wide ? r / kWideRows : r / kRows;
       const int e = part_of == 0 ? s * set.prefix_tiles + tile : set.prefixes * set.prefix_tiles + s * set.seq_tiles + tile;
       m.add_parts(find_parts(p, set, rows, e, h, r - tile * rows, all - tile * rows), part, kSplit);
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const __gr
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_split_kernel(const __grid_constant__ AttendParams p) {
   pdl_wait();
   const WorkSet& set = p.wide;
-  const Shares shares(set, set.base[set.blocks()]);
+  const Shares shares(set);
   const int c = blockIdx.x + 1;
   if (c >= shares.count) return;
   const int2 at = set.start[c];
@@ -482,7 +482,7 @@ bool encode_boxes(CUtensorMap* tm, const void* base, int rows, int heads, long l
 bool multiple(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Query rows from which the wide kernel takes a unit, and above which a sequence fills one.
-constexpr int kWideFrom = kRows + 1, kJointFrom = 128;
+constexpr int kWideFrom = kRows + 1, kOwnWideFrom = 2 * kRows + 1, kJointFrom = 128;
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -501,7 +501,7 @@ void lay_out(WorkSet& s, int kv_heads, int rows, size_t& off) {
   };
   if (s.blocks() == 0) return;
   const size_t slots = (size_t)s.blocks() * kv_heads + s.max_shares;
-  s.base = reinterpret_cast<int*>(take((size_t)(s.blocks() + 1) * sizeof(int)));
+  s.base = reinterpret_cast<int*>(take((size_t)(s.blocks() + 2) * sizeof(int)));
   s.start = reinterpret_cast<int2*>(take((size_t)s.max_shares * sizeof(int2)));
   s.part_ml = reinterpret_cast<float2*>(take(slots * rows * sizeof(float2)));
   s.part_o = reinterpret_cast<float*>(take(slots * rows * kHeadDim * sizeof(float)));
@@ -520,6 +520,8 @@ constexpr size_t kWorkHead = 256;                 // an error word, for callers 
 // to read.
 constexpr int kFewMinBoxes = 4;
 constexpr int kWideMinSteps = 4;
+// Clocks of an SM for a box (8 KB at an SM's part of HBM) and for a step of 128 rows (with two groups).
+constexpr int kFewCost = 350, kWideCost = 3200;
 
 // Sizes alone decide: lens and n_new are the device's.
 int make_plan(const evict_attention* a, Plan* out) {
@@ -549,7 +551,7 @@ int make_plan(const evict_attention* a, Plan* out) {
     P.wide.seqs = a->batch;
   } else {
     if (pre) (pre_rows >= kWideFrom ? P.wide : P.few).prefixes = a->prefix_batch;
-    if (a->pages) (own_rows >= kWideFrom ? P.wide : P.few).seqs = a->batch;
+    if (a->pages) (own_rows >= kOwnWideFrom ? P.wide : P.few).seqs = a->batch;
   }
   const long long seq_tokens = a->pages ? (long long)a->pages->table_width * a->pages->page_size : 0;
   auto tiles = [&](WorkSet& s, int rows, int tokens) {
@@ -568,10 +570,14 @@ int make_plan(const evict_attention* a, Plan* out) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P.sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e, "looking up the device");
+  P.few.workers = kWarps;
   P.few.max_shares = P.sms * kWarps;
   P.few.min_steps = kFewMinBoxes;
+  P.few.cost = kFewCost;
+  P.wide.workers = 1;
   P.wide.max_shares = P.sms;
   P.wide.min_steps = kWideMinSteps;
+  P.wide.cost = kWideCost;
   size_t off = kWorkHead + round256((size_t)(a->batch + 1) * sizeof(int));
   lay_out(P.few, a->n_kv_heads, kRows, off);
   lay_out(P.wide, a->n_kv_heads, kWideRows, off);
@@ -584,6 +590,7 @@ int check_rows(const evict_rows& x, int heads, const char* name) {
   if (x.heads != heads) return fail(EVICT_EINVAL, "%s has %d heads, not %d", name, x.heads, heads);
   if (!multiple(x.data, 16) || x.stride_b % 8 || x.stride_h % 8 || x.stride_m % 8)
     return fail(EVICT_EINVAL, "%s: addresses and strides must be multiples of 16 bytes", name);
+  if (x.stride_b < 0 || x.stride_h < 0 || x.stride_m < 0) return fail(EVICT_EINVAL, "%s: strides must not be negative", name);
   return EVICT_OK;
 }
 
@@ -689,19 +696,19 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
     }
     return (int)EVICT_OK;
   };
+  P.few = plan.few;
+  P.wide = plan.wide;
+  P.sms = plan.sms;
   cudaStream_t st = static_cast<cudaStream_t>(a->stream);
   cudaError_t e = cudaSuccess;
   const bool few = plan.few.blocks() > 0, wide = plan.wide.blocks() > 0;
   if (wide) {
     if ((rc = encode(true, plan.wide))) return rc;
-    P.set = plan.wide;
     if ((e = prepare_wide()) != cudaSuccess || (e = launch_wide(P, plan.sms, few, st)) != cudaSuccess)
       return cuda_fail(e, "wide attention kernel launch");
     g_launches.fetch_add(1);
     P.late_wait = 1;                              // the few-row kernel needs nothing of the wide one's
   }
-  P.set = plan.few;
-  P.wide = plan.wide;
   if (few) {
     if ((rc = encode(false, plan.few))) return rc;
     e = cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);

@@ -119,11 +119,14 @@ struct Cursor {
 struct Shares {
   int count = 0, each = 0, extra = 0;
   Shares() = default;
-  __device__ __forceinline__ Shares(const WorkSet& set, int total) {
-    count = min(set.max_shares, total / set.min_steps);
-    if (count == 0) count = total > 0 ? 1 : 0;
+  __device__ __forceinline__ Shares(int total, int shares) : count(shares) {
     each = count ? total / count : 0;
     extra = total - each * count;
+  }
+  // as the kernel that took them left it
+  __device__ __forceinline__ explicit Shares(const WorkSet& set) {
+    const int* end = set.base + set.blocks();
+    *this = Shares(end[0], end[1]);
   }
   __device__ __forceinline__ int begin(int i) const { return i * each + min(i, extra); }
   __device__ __forceinline__ int of(int g) const {                 // the share that holds step g
@@ -132,16 +135,26 @@ struct Shares {
   }
 };
 
+// SMs of a kernel with `mine` steps beside one with `other` steps, of sms in all.
+__device__ __forceinline__ int sms_of(const WorkSet& set, int mine, const WorkSet& rest, int other, int sms) {
+  if (other == 0 || mine == 0) return sms;
+  const float a = (float)mine * (float)set.cost, b = (float)other * (float)rest.cost;
+  // the wide kernel's number is computed alike on both sides, and the few-row kernel has what is left
+  const bool wide = set.workers == 1;
+  const float w = wide ? a : b;
+  const int n = min(sms - 1, max(1, (int)((float)sms * (w / (a + b)) + 0.5f)));
+  return wide ? n : sms - n;
+}
+
 constexpr int kMaxWarps = 12;
 struct ScanShared {
-  int a[32];
-  int total;
+  int a[kMaxWarps], b[kMaxWarps];
   int e[kMaxWarps], rest[kMaxWarps];              // where the shares of this CTA begin
 };
 
-// Exclusive sum of `a` over the block's threads, and the total.
+// Exclusive sum of `a` over the block's threads, and the totals of a and b.
 template <int kThreads>
-__device__ __forceinline__ int block_scan(int a, int& total, ScanShared& sh) {
+__device__ __forceinline__ int block_scan(int a, int b, int& total, int& total_b, ScanShared& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = a;
 #pragma unroll
@@ -149,32 +162,36 @@ __device__ __forceinline__ int block_scan(int a, int& total, ScanShared& sh) {
     const int y = __shfl_up_sync(0xffffffffu, x, d);
     if (lane >= d) x += y;
   }
-  if (lane == 31) sh.a[warp] = x;
+  b = __reduce_add_sync(0xffffffffu, b);
+  if (lane == 31) sh.a[warp] = x, sh.b[warp] = b;
   __syncthreads();
-  total = 0;
+  total = total_b = 0;
 #pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) x += sh.a[w];
     total += sh.a[w];
+    total_b += sh.b[w];
   }
   __syncthreads();
   return x - a;
 }
 
 // Where the shares first .. first + kPer - 1 of this CTA begin, found from the lengths on the
-// device (sh.e, sh.rest; all threads call it). CTA 0 leaves the blocks' first steps for the join.
-template <int kRows, int kTokens, int kThreads, int kPer>
-__device__ __forceinline__ Shares find_shares(const AttendParams& p, const WorkSet& set, ScanShared& sh) {
+// device (sh.e, sh.rest; all threads call it). `rest`: the other kernel's work (blocks of kRestRows
+// rows, steps of kRestTokens). CTA 0 leaves the blocks' first steps for the join.
+template <int kRows, int kTokens, int kRestRows, int kRestTokens, int kThreads, int kPer>
+__device__ __forceinline__ Shares find_shares(const AttendParams& p, const WorkSet& set, const WorkSet& rest,
+                                              ScanShared& sh) {
   const int tid = threadIdx.x;
-  int total;
-  if (p.n_new && set.prefixes) {
+  int total, total_rest;
+  if (p.n_new && (set.prefixes || rest.prefixes)) {
     // every CTA writes the same sums, and reads back its own
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
     int a = 0;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) a += sequence(p, b, false).n;
-    a = block_scan<kThreads>(a, total, sh);
+    a = block_scan<kThreads>(a, 0, total, total_rest, sh);
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       p.tok_base[b] = a;
@@ -187,6 +204,12 @@ __device__ __forceinline__ Shares find_shares(const AttendParams& p, const WorkS
   const int per = (blocks + kThreads - 1) / kThreads;
   const int e0 = min(tid * per, blocks), e1 = min(e0 + per, blocks);
   Block k;
+  int other = 0;
+#pragma unroll 1
+  for (int e = tid; e < rest.blocks(); e += kThreads) {
+    load_block<kRestRows, kRestTokens>(p, rest, e, k);
+    other += k.steps * p.hkv;
+  }
   int work = 0, a = 0, lo = 0, hi = 0;
   Shares shares;
   const int first = blockIdx.x * kPer;
@@ -194,8 +217,9 @@ __device__ __forceinline__ Shares find_shares(const AttendParams& p, const WorkS
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     if (pass == 1) {
-      a = block_scan<kThreads>(work, total, sh);
-      shares = Shares(set, total);
+      a = block_scan<kThreads>(work, other, total, total_rest, sh);
+      const int most = sms_of(set, total, rest, total_rest, p.sms) * kPer;
+      shares = Shares(total, total == 0 ? 0 : max(1, min(most, total / set.min_steps)));
       lo = shares.begin(min(first, shares.count));
       hi = shares.begin(min(first + kPer, shares.count));
       if (blockIdx.x != 0 && (a >= hi || a + work <= lo)) break;
@@ -221,7 +245,10 @@ __device__ __forceinline__ Shares find_shares(const AttendParams& p, const WorkS
       a += w;
     }
   }
-  if (blockIdx.x == 0 && tid == 0) set.base[blocks] = total;
+  if (blockIdx.x == 0 && tid == 0) {
+    set.base[blocks] = total;
+    set.base[blocks + 1] = shares.count;
+  }
   __syncthreads();
   return shares;
 }

@@ -11,6 +11,7 @@ namespace evict {
 
 constexpr int kBoxTokens = 16;       // rows of K and V that a warp of the few-row kernel takes at a time
 constexpr int kWideTokens = 128;     // rows that a CTA of the wide kernel takes at a time
+constexpr int kFewRows = 16;         // query rows of a unit of the few-row kernel (one MMA tile)
 constexpr int kWideRows = 256;       // query rows of a unit of the wide kernel (two MMA tiles)
 
 // Quotient by a divisor that the host knows, for dividends below 2^31: a multiplication and a shift.
@@ -37,15 +38,19 @@ struct Divisor {
 // steps of 16 (few-row kernel) or 128 (wide kernel) rows. The steps of all
 // units, in the order of blocks and heads, are laid end to end and cut into
 // equal contiguous shares, one for every warp (few-row kernel) or CTA (wide).
+// Where a call has work for both kernels, they run side by side on different SMs, as many as their
+// work asks for.
 // What a share holds of a unit leaves one partial result, in slot unit +
 // share: from one part to the next either of them goes up, so slots are unique.
 struct WorkSet {
   int prefixes, prefix_tiles;        // streams of prefixes, blocks of one
   int seqs, seq_tiles;               // streams of sequences: 0 or the batch; blocks of one
   int joint;                         // a sequence's stream begins with its prefix
-  int max_shares, min_steps;         // of a share
+  int workers, min_steps;            // shares that a CTA takes (its warps, or itself); steps of a share at least
+  int cost;                          // of a step: clocks of an SM, roughly
+  int max_shares;                    // workers of every SM
   Divisor by_prefix_tiles, by_seq_tiles;
-  int* base;                         // [blocks + 1] first step of every block, then their total
+  int* base;                         // [blocks + 2] first step of every block, their total, the shares' number
   int2* start;                       // [shares] block and step in it where every share begins
   float2* part_ml;                   // [slots][tile rows] running maximum (base 2) and sum
   float* part_o;                     // [slots][tile rows][128]
@@ -55,8 +60,8 @@ struct WorkSet {
 struct AttendParams {
   CUtensorMap tm_pk, tm_pv;          // prefix [prefix_batch][n_kv_heads][n_prefix][128]
   CUtensorMap tm_k, tm_v;            // pages [n_pages][n_kv_heads][page_size][128]
-  WorkSet set;                       // of this launch (the join: of the few-row kernel)
-  WorkSet wide;                      // the join: of the wide kernel
+  WorkSet few, wide;                 // of the two kernels
+  int sms;
   const void* q;
   void* out;
   float* lse;

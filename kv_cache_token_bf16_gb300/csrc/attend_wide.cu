@@ -69,7 +69,7 @@ struct Segment {
     steps = min(c.k.steps - c.step, left);
     pre_steps = (c.k.pre + kWideTokens - 1) / kWideTokens;
     two = c.k.n * p.group - c.k.tile * kWideRows > kTile;
-    alt = !two && !p.set.joint;
+    alt = !two && !p.wide.joint;
   }
   __device__ __forceinline__ bool has(int w, int i) const { return two || (alt ? (i & 1) == w : w == 0); }
   __device__ __forceinline__ int jobs(int w) const { return two ? steps : alt ? (steps + 1 - w) / 2 : w == 0 ? steps : 0; }
@@ -91,7 +91,7 @@ struct Slot {
 };
 
 __device__ void producer(const AttendParams& p, WideShared& sh, WideCursor c, int count, uint32_t ring) {
-  const WorkSet& set = p.set;
+  const WorkSet& set = p.wide;
   const int lane = threadIdx.x & 31, blocks = set.blocks();
   const int box = p.box_rows, boxes = box ? kTile / box : 0;
   Slot slot;
@@ -200,7 +200,7 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pt, uint32_t v, ui
 // by side, both pairs would end together and the tensor cores wait for both groups.
 __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, int count, int w, uint32_t tmem,
                            uint32_t qbuf, uint32_t ring) {
-  const WorkSet& set = p.set;
+  const WorkSet& set = p.wide;
   const int blocks = set.blocks();
   const uint64_t qk = tc::sw128_desc(qbuf + w * kTileBytes), pv = tc::sw128_desc_mn(ring, kTileBytes / 2, 1024);
   const uint32_t q_lo = (uint32_t)qk, k_lo = (uint32_t)tc::sw128_desc(ring), qk_hi = (uint32_t)(qk >> 32);
@@ -359,7 +359,7 @@ __device__ __noinline__ void move_reference(uint32_t s_at, int columns, uint32_t
 // One softmax group: thread `row` of group w.
 __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor c, int count, int w, int row, uint32_t tmem,
                               unsigned char* qbuf, uint32_t ring) {
-  const WorkSet& set = p.set;
+  const WorkSet& set = p.wide;
   const int warp = row >> 5, blocks = set.blocks();
   const uint32_t lanes = (uint32_t)(32 * warp) << 16;
   const uint32_t s_at = tmem + lanes + (uint32_t)(w * kTile), o_at = s_at + 2 * kTile;
@@ -646,7 +646,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attend_wide_kernel(const __gr
     tc::mbar_init(&sh.o_full[w], 1);
     tc::mbar_init(&sh.done[w], 1);
   }
-  if (warp == 3) prefetch_maps(p, p.set, tid & 31);
+  if (warp == 3) prefetch_maps(p, p.wide, tid & 31);
   if (warp > 3) {
     for (int i = tid - 128; i < kBadSets * kBadWords; i += kWideThreads - 128) (&sh.bad[0][0])[i] = 0;
     if (tid == 128) sh.fail = sh.turn = 0;
@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attend_wide_kernel(const __gr
   pdl_wait();
   // what comes next may start on an SM as soon as this kernel leaves it
   if (early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Shares shares = find_shares<kWideRows, kWideTokens, kWideThreads, 1>(p, p.set, sh.scan);
+  const Shares shares = find_shares<kWideRows, kWideTokens, kFewRows, kBoxTokens, kWideThreads, 1>(p, p.wide, p.few, sh.scan);
   const int mine = blockIdx.x;
   const int count = mine < shares.count ? shares.begin(mine + 1) - shares.begin(mine) : 0;
   tc::fence_before_sync();
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) attend_wide_kernel(const __gr
   tc::fence_after_sync();
   const uint32_t tmem = sh.tmem_base;
   if (count > 0) {
-    const WideCursor c = place<kWideRows, kWideTokens>(p, p.set, sh.scan.e[0], sh.scan.rest[0]);
+    const WideCursor c = place<kWideRows, kWideTokens>(p, p.wide, sh.scan.e[0], sh.scan.rest[0]);
     if (warp == kTmaWarp) {
       producer(p, sh, c, count, ring);
     } else if (warp >= kMmaWarp) {
