@@ -4,18 +4,11 @@
 // over the rows a query sees, in one pass over K and V with a running maximum
 // and sum; logits are kept in base 2 (scale * log2 e), so p = 2^(x - m).
 //
-// attend_kernel (units of up to 16 query rows): persistent, one CTA per SM. All
-// the rows of K and V that the batch reads, prefix and pages alike, are laid
-// end to end in boxes of 16 rows, and every warp of the grid takes an equal
-// share of them, whatever the sequences' lengths are: the lengths live on the
-// device, so the shares are found there, by one block scan. A warp works by
-// itself from there on: its own ring of TMA boxes (16 rows of K and of V, 8
-// KB; a box never crosses a page), its own running maximum, sum and output,
-// and no barrier, so that one warp's start or end of a unit hides behind the
-// others' rows. Queries are the rows of m16n8k16 products. Bound: HBM; a warp
-// has one box in flight while it computes on another (96 KB an SM).
-//
-// attend_wide_kernel (attend_wide.cu): units of more query rows.
+// attend_kernel: persistent, one CTA per SM. Units of up to 16 query rows go to
+// CTAs that work as attend_few.cuh says, units of more to CTAs that work as
+// attend_wide.cuh says, side by side. The lengths live on the device, so the
+// SMs that each kind gets, and the shares of its CTAs, are found there: every
+// CTA sums the work of all units, by one block scan.
 //
 // attend_join_kernel: a warp per output row merges the partial results of the
 // row's units, in the order of their slots.
@@ -29,6 +22,8 @@
 #include "api_internal.h"
 #include "attend.h"
 #include "attend.cuh"
+#include "attend_few.cuh"
+#include "attend_wide.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "pipeline.cuh"
@@ -38,294 +33,31 @@
 namespace evict {
 namespace {
 
-constexpr int kBoxBytes = kBoxTokens * kHeadDim * 2;       // of K or of V
+constexpr int kThreads = kWarps * 32;
+constexpr int kSmem = 1024 + (kFewSmem > kWideSmem ? kFewSmem : kWideSmem);
 
-constexpr int kRows = kFewRows;
-constexpr int kWarps = 12;
-constexpr int kStages = 2;                        // boxes of a warp's ring
-constexpr int kFewSmem = kWarps * kStages * 2 * kBoxBytes + 1024;
-
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-// c[16 x 8] += a[16 x 16] b[16 x 8], bf16 in, fp32 sums
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-struct FewShared {
-  uint64_t full[kWarps][kStages];
-  ScanShared scan;
-  int fail;
-};
-
-__global__ void __launch_bounds__(kWarps * 32, 1) attend_kernel(const __grid_constant__ AttendParams p) {
-  using Cur = Cursor<kRows, kBoxTokens>;
+__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ AttendParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ FewShared sh;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t ring = ((tc::smem_u32(smem_raw) + 1023) & ~1023u) + warp * kStages * 2 * kBoxBytes;
-  const WorkSet& set = p.few;
-  const int blocks = set.blocks();
-
-  if (tid < kWarps * kStages) tc::mbar_init(&sh.full[tid / kStages][tid % kStages], 1);
-  if (tid == 0) sh.fail = 0;
-  if (warp == 1) prefetch_maps(p, set, lane);
-  if (!p.late_wait) pdl_wait();
-  const Shares shares = find_shares<kRows, kBoxTokens, kWideRows, kWideTokens, kWarps * 32, kWarps>(p, set, p.wide, sh.scan);
-  const int share = blockIdx.x * kWarps + warp;
-  if (share < shares.count) {
-    int left = shares.begin(share + 1) - shares.begin(share);
-    Cur cur = place<kRows, kBoxTokens>(p, set, sh.scan.e[warp], sh.scan.rest[warp]);
-
-    // --- the ring: boxes are requested in the order in which they are used ---
-    Cur ahead = cur;
-    int ahead_left = left, page = 0;
-    auto look_up = [&] {                          // the page of the next box to request
-      if (lane == 0 && ahead_left > 0 && ahead.k.s >= set.prefixes)
-        page = p.table[(long long)(ahead.k.s - set.prefixes) * p.table_stride + ((ahead.step * kBoxTokens) >> p.page_shift)];
-    };
-    auto request = [&](int stage) {
-      if (lane == 0) {
-        uint64_t* bar = &sh.full[warp][stage];
-        const uint32_t dst = ring + stage * 2 * kBoxBytes;
-        int row = ahead.step * kBoxTokens, plane = ahead.k.s;
-        const bool pre = ahead.k.s < set.prefixes;
-        if (!pre) {
-          if (page < 0 || page >= p.n_pages) {
-            raise_device_error(p.err, kDevBadIndex);
-            page = p.n_pages;                     // outside the pool: the box is zeros
-          }
-          plane = page;
-          row &= (1 << p.page_shift) - 1;
-        }
-        tc::mbar_arrive_expect_tx(bar, 2 * kBoxBytes);
-        tma_load_5d(dst, pre ? &p.tm_pk : &p.tm_k, 0, row, 0, ahead.h, plane, bar);
-        tma_load_5d(dst + kBoxBytes, pre ? &p.tm_pv : &p.tm_v, 0, row, 0, ahead.h, plane, bar);
-      }
-      if (--ahead_left > 0 && ++ahead.step == ahead.k.steps) ahead.next_unit(p, set, blocks);
-      look_up();
-    };
-    look_up();
-    int requested = 0, flying = 0;                // the stage that the next request takes; boxes in the ring
-
-    // addresses of this lane's rows for ldmatrix: 16-byte chunk j of a row sits at j ^ (row % 8), so a
-    // chunk's address is the lane's own xor 16 j (and 2 KB on for the second half)
-    const uint32_t k_at = tc::sw128_offset((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1, kBoxTokens);
-    const uint32_t v_at = kBoxBytes + tc::sw128_offset(lane & 15, lane >> 4, kBoxTokens);
-    int stage = 0;
-    uint32_t parity = 0;
-    bool dead = false;
-
-    while (left > 0) {
-      const int boxes = min(cur.k.steps - cur.step, left);
-      const bool own = cur.k.s >= set.prefixes;
-      // this lane's queries (rows lane / 4 and 8 on) and the last row each sees
-      uint32_t q[8][4];
-      float o[16][4], mx[2], sum[2];
-      int last[2], low = 0;
-
-#pragma unroll 1
-      for (int i = 0; i < boxes; ++i) {
-        __syncwarp();                             // every lane has read the box that the next one replaces
-        const int room = i == 0 ? kStages - 1 : kStages;           // a unit's queries pass through a stage first
-#pragma unroll 1
-        while (flying < room && ahead_left > 0 && !dead) {
-          request(requested);
-          requested = requested == kStages - 1 ? 0 : requested + 1;
-          ++flying;
-        }
-        if (i == 0) {
-          const uint32_t at = ring + requested * 2 * kBoxBytes;
-#pragma unroll 4
-          for (int e = lane; e < kRows * 16; e += 32) {
-            const QueryRow r = query_row<kRows>(p, set, cur.k, e >> 4);
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (r.real)
-              x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)r.b * p.qb +
-                                                 (long long)(cur.h * p.group + r.g) * p.qh + (long long)r.t * p.qm)[e & 15];
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + tc::sw128_offset(e >> 4, e & 15, kRows)),
-                         "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
-          }
-          __syncwarp();
-          const uint32_t q_at = at + tc::sw128_offset(lane & 15, lane >> 4, kRows);
-#pragma unroll
-          for (int s = 0; s < 8; ++s) ldsm4((q_at ^ ((s & 3) * 32)) + (s >> 2) * (kRows * 128), q[s]);
-          tc::fence_proxy_async_smem();           // the stage's next content comes by TMA
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int t = p.by_group.div(cur.k.tile * kRows + (lane >> 2) + 8 * k);
-            last[k] = !own ? cur.k.pre - 1 : t < cur.k.n ? cur.k.len - cur.k.n + t : -1;
-            mx[k] = -INFINITY;
-            sum[k] = 0.f;
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
-          low = __shfl_sync(0xffffffffu, last[0], 0);              // the first row's: the lowest
-        }
-        if (!dead) {
-          const bool ok = wait_phase(&sh.full[warp][stage], parity, &sh.fail, p.err);
-          if (!__all_sync(0xffffffffu, ok)) {
-            // the copies in flight must land before this CTA may end
-            for (int w = 0, s = stage; w < flying; ++w) {
-              drain_phase(&sh.full[warp][s], s >= stage ? parity : parity ^ 1, p.err);
-              s = s == kStages - 1 ? 0 : s + 1;
-            }
-            dead = true;
-          }
-        }
-        const uint32_t kb = ring + stage * 2 * kBoxBytes;
-        if (++stage == kStages) stage = 0, parity ^= 1;
-        --flying;
-        const int row0 = (cur.step + i) * kBoxTokens;
-        if (dead) continue;
-
-        const bool full = row0 + kBoxTokens - 1 <= low;            // every query sees every row
-        float z[2][4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) z[j][k] = 0.f;
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          uint32_t k4[4];
-          ldsm4(((kb + k_at) ^ ((s & 3) * 32)) + (s >> 2) * (kBoxTokens * 128), k4);
-          mma16816(z[0], q[s], k4[0], k4[1]);
-          mma16816(z[1], q[s], k4[2], k4[3]);
-        }
-        float rm[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float v = z[j][k] * p.scale2;
-            if (!full && row0 + 8 * j + 2 * (lane & 3) + (k & 1) > last[k >> 1]) v = -INFINITY;
-            z[j][k] = v;
-            rm[k >> 1] = fmaxf(rm[k >> 1], v);
-          }
-        // the running maximum moves only when a logit passes it
-        if (__any_sync(0xffffffffu, rm[0] > mx[0] || rm[1] > mx[1])) {
-          float f[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            rm[k] = fmaxf(rm[k], __shfl_xor_sync(0xffffffffu, rm[k], 1));
-            rm[k] = fmaxf(rm[k], __shfl_xor_sync(0xffffffffu, rm[k], 2));
-            const float nm = fmaxf(mx[k], rm[k]);
-            f[k] = weight_of(mx[k], nm);
-            mx[k] = nm;
-            sum[k] *= f[k];
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            o[j][0] *= f[0];
-            o[j][1] *= f[0];
-            o[j][2] *= f[1];
-            o[j][3] *= f[1];
-          }
-        }
-        const float m0 = base_of(mx[0]), m1 = base_of(mx[1]);
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) z[j][k] = ex2(z[j][k] - (k < 2 ? m0 : m1));
-          sum[0] += z[j][0] + z[j][1];
-          sum[1] += z[j][2] + z[j][3];
-          // weights as bf16 pairs hi + lo: 16 bits of each, so that their rounding does not add to the
-          // output's own (the tensor cores wait for memory here anyway)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float a = z[j][2 * k], b = z[j][2 * k + 1];
-            const uint32_t h2 = pack_bf16(a, b);
-            hi[2 * j + k] = h2;
-            lo[2 * j + k] = pack_bf16(a - __uint_as_float(h2 << 16), b - __uint_as_float(h2 & 0xffff0000u));
-          }
-        }
-        // V of rows behind the stream's end may hold anything: zeros in its place
-        uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu, bad = 0;
-        if (!full) {
-          const int r0 = row0 + 2 * (lane & 3), end = own ? cur.k.len : cur.k.pre;
-          auto mask = [&](int r) { return (r < end ? 0xffffu : 0u) | (r + 1 < end ? 0xffff0000u : 0u); };
-          keep0 = mask(r0);
-          keep1 = mask(r0 + 8);
-          if (p.m > 1 && own) {
-            // A query that does not see a row gives it weight 0, but 0 * infinity is not 0: the
-            // products leave rows with infinities or NaN out (`bad`), and the queries that see them
-            // take them afterwards.
-#pragma unroll 1
-            for (int j = 0; j < 8; ++j) {
-              uint32_t v4[4];
-              ldsm4_t(((kb + v_at) ^ ((j & 3) * 32)) + (j >> 2) * (kBoxTokens * 128), v4);
-              const uint32_t odd0 = nonfinite2(v4[0] & keep0) | nonfinite2(v4[2] & keep0);
-              const uint32_t odd1 = nonfinite2(v4[1] & keep1) | nonfinite2(v4[3] & keep1);
-              bad |= (odd0 | odd1 << 8) << (2 * (lane & 3));
-            }
-            bad = __reduce_or_sync(0xffffffffu, bad);
-            auto drop = [&](uint32_t two) { return (two & 1u ? 0xffffu : 0u) | (two & 2u ? 0xffff0000u : 0u); };
-            keep0 &= ~drop(bad >> (2 * (lane & 3)));
-            keep1 &= ~drop(bad >> (2 * (lane & 3) + 8));
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          uint32_t v4[4];
-          ldsm4_t(((kb + v_at) ^ ((j & 3) * 32)) + (j >> 2) * (kBoxTokens * 128), v4);
-          if (!full) v4[0] &= keep0, v4[1] &= keep1, v4[2] &= keep0, v4[3] &= keep1;
-          mma16816(o[2 * j], hi, v4[0], v4[1]);
-          mma16816(o[2 * j + 1], hi, v4[2], v4[3]);
-          mma16816(o[2 * j], lo, v4[0], v4[1]);
-          mma16816(o[2 * j + 1], lo, v4[2], v4[3]);
-        }
-#pragma unroll 1
-        for (; bad; bad &= bad - 1) {             // rare
-          const int k = __ffs(bad) - 1, from = (lane & 28) | ((k & 7) >> 1);
-          const float a0 = k & 1 ? z[0][1] : z[0][0], a1 = k & 1 ? z[1][1] : z[1][0];
-          const float b0 = k & 1 ? z[0][3] : z[0][2], b1 = k & 1 ? z[1][3] : z[1][2];
-          const float w0 = __shfl_sync(0xffffffffu, k & 8 ? a1 : a0, from);
-          const float w1 = __shfl_sync(0xffffffffu, k & 8 ? b1 : b0, from);
-          const bool s0 = row0 + k <= last[0], s1 = row0 + k <= last[1];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            uint32_t v;
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v)
-                         : "r"(kb + kBoxBytes + tc::sw128_offset(k, j, kBoxTokens) + 4 * (lane & 3)) : "memory");
-            const float v0 = __uint_as_float(v << 16), v1 = __uint_as_float(v & 0xffff0000u);
-            if (s0) o[j][0] += w0 * v0, o[j][1] += w0 * v1;
-            if (s1) o[j][2] += w1 * v0, o[j][3] += w1 * v1;
-          }
-        }
-      }
-
-      // --- the share leaves the unit: its part of the result ---
-      const size_t slot = (size_t)(cur.unit + share) * kRows;
-      const int rows = min(kRows, cur.k.n * p.group - cur.k.tile * kRows);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float t = sum[k];
-        t += __shfl_xor_sync(0xffffffffu, t, 1);
-        t += __shfl_xor_sync(0xffffffffu, t, 2);
-        const int r = (lane >> 2) + 8 * k;
-        if (r < rows) {
-          if ((lane & 3) == 0) set.part_ml[slot + r] = make_float2(mx[k], t);
-          float2* dst = reinterpret_cast<float2*>(set.part_o + (slot + r) * kHeadDim) + (lane & 3);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) dst[4 * j] = make_float2(o[j][2 * k], o[j][2 * k + 1]);
-        }
-      }
-      left -= boxes;
-      if (left > 0) cur.next_unit(p, set, blocks);
-    }
+  __shared__ FewShared few;
+  __shared__ WideShared wide;
+  __shared__ ScanShared scan;
+  unsigned char* smem = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const bool may_wide = p.wide.blocks() > 0;
+  if (p.few.blocks() > 0) few_setup(few);
+  if (may_wide) wide_setup(wide);
+  if (threadIdx.x >= kThreads - 32) prefetch_maps(p, threadIdx.x & 31);
+  pdl_wait();
+  const Place at = find_place<kThreads, kWarps>(p, scan);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (at.wide) {
+    if (at.first < at.shares.count)
+      wide_rows(p, wide, scan, at.shares.begin(at.first + 1) - at.shares.begin(at.first), smem);
+  } else {
+    few_rows(p, few, scan, at.shares, at.first, tc::smem_u32(smem));
   }
-  if (p.late_wait) pdl_wait();
+  if (may_wide) wide_teardown(wide);
 }
 
 // Partial results of one output row in one unit: `count` slots from `slot` on, row `row` of each;
@@ -397,7 +129,7 @@ struct Merge {
 // (few rows have many parts each, and one warp would wait for memory part after part) and their
 // results meet in shared memory, in the order of the warps.
 template <int kSplit>
-__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 5) attend_join_kernel(const __grid_constant__ AttendParams p) {
   __shared__ float4 acc[kJoinWarps][32];
   __shared__ float2 ml[kJoinWarps];
   pdl_wait();
@@ -520,8 +252,8 @@ constexpr size_t kWorkHead = 256;                 // an error word, for callers 
 // to read.
 constexpr int kFewMinBoxes = 4;
 constexpr int kWideMinSteps = 4;
-// Clocks of an SM for a box (8 KB at an SM's part of HBM) and for a step of 128 rows (with two groups).
-constexpr int kFewCost = 350, kWideCost = 3200;
+// Clocks of an SM for a box of 16 rows and for a step of 128 rows (with two groups), side by side.
+constexpr int kFewCost = 275, kWideCost = 4600;
 
 // Sizes alone decide: lens and n_new are the device's.
 int make_plan(const evict_attention* a, Plan* out) {
@@ -676,22 +408,22 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
     P.page_v = g->v;
     P.page_stride = g->page_stride ? g->page_stride : (long long)g->n_kv_heads * g->page_size * kHeadDim;
   }
-  // The boxes of one of the kernels: 16 whole rows, or up to 128 rows of one half.
-  auto encode = [&](bool wide, const WorkSet& s) {
+  // The two kinds' boxes: 16 whole rows, or up to 128 rows of one half.
+  auto encode = [&](bool wide, const WorkSet& s, CUtensorMap (&pre)[2], CUtensorMap (&own)[2]) {
     if (s.prefixes || (s.joint && P.fan)) {
       // a dimension of extent 1 is never stepped over, but its stride still has to be one the encoder takes
       const long long hs = P.hkv > 1 ? a->prefix_stride_h : (long long)P.n_prefix * kHeadDim;
       const long long bs = P.prefix_batch > 1 ? a->prefix_stride_b : P.hkv * hs;
       for (int v = 0; v < 2; ++v)
-        if (!encode_boxes(v ? &P.tm_pv : &P.tm_pk, v ? a->prefix_v : a->prefix_k, P.n_prefix, P.hkv, hs, P.prefix_batch, bs,
+        if (!encode_boxes(&pre[v], v ? a->prefix_v : a->prefix_k, P.n_prefix, P.hkv, hs, P.prefix_batch, bs,
                           wide ? kWideTokens : kBoxTokens, wide ? 1 : 2))
           return fail(EVICT_EINVAL, "the prefix has sizes or strides beyond a tensor map's");
     }
     if (s.seqs && g) {
       P.box_rows = std::min(g->page_size, kWideTokens);
       for (int v = 0; v < 2; ++v)
-        if (!encode_boxes(v ? &P.tm_v : &P.tm_k, v ? g->v : g->k, g->page_size, P.hkv, (long long)g->page_size * kHeadDim,
-                          g->n_pages, P.page_stride, wide ? P.box_rows : kBoxTokens, wide ? 1 : 2))
+        if (!encode_boxes(&own[v], v ? g->v : g->k, g->page_size, P.hkv, (long long)g->page_size * kHeadDim, g->n_pages,
+                          P.page_stride, wide ? P.box_rows : kBoxTokens, wide ? 1 : 2))
           return fail(EVICT_EINVAL, "the pages have sizes or strides beyond a tensor map's");
     }
     return (int)EVICT_OK;
@@ -699,21 +431,14 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
   P.few = plan.few;
   P.wide = plan.wide;
   P.sms = plan.sms;
+  // a stream is of one kind, so either kind's maps have a place of their own
+  if ((rc = encode(false, P.few, P.few_pre, P.few_own)) || (rc = encode(true, P.wide, P.wide_pre, P.wide_own))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(a->stream);
-  cudaError_t e = cudaSuccess;
-  const bool few = plan.few.blocks() > 0, wide = plan.wide.blocks() > 0;
-  if (wide) {
-    if ((rc = encode(true, plan.wide))) return rc;
-    if ((e = prepare_wide()) != cudaSuccess || (e = launch_wide(P, plan.sms, few, st)) != cudaSuccess)
-      return cuda_fail(e, "wide attention kernel launch");
-    g_launches.fetch_add(1);
-    P.late_wait = 1;                              // the few-row kernel needs nothing of the wide one's
-  }
-  if (few) {
-    if ((rc = encode(false, plan.few))) return rc;
-    e = cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
-    if (e == cudaSuccess) e = launch_pdl(attend_kernel, dim3(plan.sms), dim3(kWarps * 32), kFewSmem, st, nullptr, P);
-    if (e != cudaSuccess) return cuda_fail(e, "attention kernel launch");
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return cuda_fail(e, "attention kernel attribute");
+  if (P.few.blocks() + P.wide.blocks() > 0) {
+    if ((e = launch_pdl(attend_kernel, dim3(plan.sms), dim3(kThreads), kSmem, st, nullptr, P)) != cudaSuccess)
+      return cuda_fail(e, "attention kernel launch");
     g_launches.fetch_add(1);
   }
   if (plan.wide.joint) {

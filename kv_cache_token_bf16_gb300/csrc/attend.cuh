@@ -24,9 +24,11 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const void* tmap, int 
       : "memory");
 }
 // The first lanes of a warp fetch the maps that this launch uses.
-__device__ __forceinline__ void prefetch_maps(const AttendParams& p, const WorkSet& set, int lane) {
-  if (lane < 2 && p.pages && set.seqs) tc::tma_prefetch_desc(lane == 0 ? &p.tm_k : &p.tm_v);
-  if (lane >= 2 && lane < 4 && p.fan && (set.prefixes || set.joint)) tc::tma_prefetch_desc(lane == 2 ? &p.tm_pk : &p.tm_pv);
+__device__ __forceinline__ void prefetch_maps(const AttendParams& p, int lane) {
+  if (lane < 2 && p.few.prefixes) tc::tma_prefetch_desc(&p.few_pre[lane]);
+  if (lane < 2 && p.few.seqs && p.pages) tc::tma_prefetch_desc(&p.few_own[lane]);
+  if (lane < 2 && p.fan && (p.wide.prefixes || p.wide.joint)) tc::tma_prefetch_desc(&p.wide_pre[lane]);
+  if (lane < 2 && p.wide.seqs && p.pages) tc::tma_prefetch_desc(&p.wide_own[lane]);
 }
 // Bit 0: the lower bf16 of the pair is an infinity or NaN; bit 1: the upper.
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t x) {
@@ -135,15 +137,15 @@ struct Shares {
   }
 };
 
-// SMs of a kernel with `mine` steps beside one with `other` steps, of sms in all.
-__device__ __forceinline__ int sms_of(const WorkSet& set, int mine, const WorkSet& rest, int other, int sms) {
-  if (other == 0 || mine == 0) return sms;
-  const float a = (float)mine * (float)set.cost, b = (float)other * (float)rest.cost;
-  // the wide kernel's number is computed alike on both sides, and the few-row kernel has what is left
-  const bool wide = set.workers == 1;
-  const float w = wide ? a : b;
-  const int n = min(sms - 1, max(1, (int)((float)sms * (w / (a + b)) + 0.5f)));
-  return wide ? n : sms - n;
+// SMs of the wide units, with `wide` steps beside the few-row units' `few`: so many that both end
+// together, start + a / w = b / (sms - w) with the two kinds' work a and b and the time by which a
+// wide CTA's start is longer.
+__device__ __forceinline__ int wide_sms(const AttendParams& p, int wide, int few) {
+  if (few == 0 || wide == 0) return wide ? p.sms : 0;
+  const float a = (float)wide * (float)p.wide.cost, b = (float)few * (float)p.few.cost, n = (float)p.sms;
+  const float h = a + b - kWideStart * n;
+  const float w = (sqrtf(h * h + 4.f * kWideStart * a * n) - h) / (2.f * kWideStart);
+  return min(min(p.sms - 1, max(1, wide / p.wide.min_steps)), max(1, (int)(w + 0.5f)));
 }
 
 constexpr int kMaxWarps = 12;
@@ -152,105 +154,125 @@ struct ScanShared {
   int e[kMaxWarps], rest[kMaxWarps];              // where the shares of this CTA begin
 };
 
-// Exclusive sum of `a` over the block's threads, and the totals of a and b.
+// Sums of a and b over the threads before this one, and their totals.
 template <int kThreads>
-__device__ __forceinline__ int block_scan(int a, int b, int& total, int& total_b, ScanShared& sh) {
+__device__ __forceinline__ void block_scan(int& a, int& b, int& total, int& total_b, ScanShared& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = a;
+  int x = a, y = b;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
+    const int u = __shfl_up_sync(0xffffffffu, x, d), v = __shfl_up_sync(0xffffffffu, y, d);
+    if (lane >= d) x += u, y += v;
   }
-  b = __reduce_add_sync(0xffffffffu, b);
-  if (lane == 31) sh.a[warp] = x, sh.b[warp] = b;
+  if (lane == 31) sh.a[warp] = x, sh.b[warp] = y;
   __syncthreads();
   total = total_b = 0;
 #pragma unroll 1
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) x += sh.a[w];
+    if (w < warp) x += sh.a[w], y += sh.b[w];
     total += sh.a[w];
     total_b += sh.b[w];
   }
   __syncthreads();
-  return x - a;
+  a = x - a;
+  b = y - b;
 }
 
-// Where the shares first .. first + kPer - 1 of this CTA begin, found from the lengths on the
-// device (sh.e, sh.rest; all threads call it). `rest`: the other kernel's work (blocks of kRestRows
-// rows, steps of kRestTokens). CTA 0 leaves the blocks' first steps for the join.
-template <int kRows, int kTokens, int kRestRows, int kRestTokens, int kThreads, int kPer>
-__device__ __forceinline__ Shares find_shares(const AttendParams& p, const WorkSet& set, const WorkSet& rest,
-                                              ScanShared& sh) {
+// What a CTA works on: its first share (of one for wide units, of its warps otherwise).
+struct Place {
+  bool wide;
+  int first;
+  Shares shares;
+};
+
+// The blocks e0 .. e1 - 1 of a set, whose steps before are `a`: their first steps for the join (`leave`), and
+// where the CTA's shares begin that begin in them.
+template <int kRows, int kTokens>
+__device__ __forceinline__ void find_starts(const AttendParams& p, const WorkSet& set, const Place& at, int per, int e0,
+                                            int e1, int a, int work, bool leave, ScanShared& sh) {
+  const int lo = at.shares.begin(min(at.first, at.shares.count));
+  const int hi = at.shares.begin(min(at.first + set.workers, at.shares.count));
+  if (!leave && (a >= hi || a + work <= lo)) return;
+#pragma unroll 1
+  for (int e = e0; e < e1; ++e) {
+    int w = work;
+    if (per > 1) {
+      Block k;
+      load_block<kRows, kTokens>(p, set, e, k);
+      w = k.steps * p.hkv;
+    }
+    if (leave) set.base[e] = a;
+#pragma unroll 1
+    for (int i = 0; i < set.workers && at.first + i < at.shares.count; ++i) {
+      const int g = at.shares.begin(at.first + i);
+      if (g >= a && g < a + w) {
+        sh.e[i] = e;
+        sh.rest[i] = g - a;
+        if (set.workers == 1) set.start[at.first] = make_int2(e, g - a);
+      }
+    }
+    a += w;
+  }
+}
+
+// The kind of units and the shares of this CTA, found from the lengths on the device (sh.e, sh.rest;
+// all threads call it). The first CTA of either kind leaves the blocks' first steps for the join.
+template <int kThreads, int kWarps>
+__device__ __forceinline__ Place find_place(const AttendParams& p, ScanShared& sh) {
   const int tid = threadIdx.x;
-  int total, total_rest;
-  if (p.n_new && (set.prefixes || rest.prefixes)) {
+  int total_w, total_f;
+  if (p.n_new && (p.few.prefixes || p.wide.prefixes)) {
     // every CTA writes the same sums, and reads back its own
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, p.batch), b1 = min(b0 + per, p.batch);
-    int a = 0;
+    int a = 0, none = 0;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) a += sequence(p, b, false).n;
-    a = block_scan<kThreads>(a, 0, total, total_rest, sh);
+    block_scan<kThreads>(a, none, total_w, total_f, sh);
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       p.tok_base[b] = a;
       a += sequence(p, b, false).n;
     }
-    if (tid == 0) p.tok_base[p.batch] = total;
+    if (tid == 0) p.tok_base[p.batch] = total_w;
     __syncthreads();
   }
-  const int blocks = set.blocks();
-  const int per = (blocks + kThreads - 1) / kThreads;
-  const int e0 = min(tid * per, blocks), e1 = min(e0 + per, blocks);
-  Block k;
-  int other = 0;
+  const int bw = p.wide.blocks(), bf = p.few.blocks();
+  const int pw = (bw + kThreads - 1) / kThreads, pf = (bf + kThreads - 1) / kThreads;
+  const int w0 = min(tid * pw, bw), w1 = min(w0 + pw, bw), f0 = min(tid * pf, bf), f1 = min(f0 + pf, bf);
+  int work_w = 0, work_f = 0;
 #pragma unroll 1
-  for (int e = tid; e < rest.blocks(); e += kThreads) {
-    load_block<kRestRows, kRestTokens>(p, rest, e, k);
-    other += k.steps * p.hkv;
+  for (int e = w0; e < w1; ++e) {
+    Block k;
+    load_block<kWideRows, kWideTokens>(p, p.wide, e, k, blockIdx.x == 0);
+    work_w += k.steps * p.hkv;
   }
-  int work = 0, a = 0, lo = 0, hi = 0;
-  Shares shares;
-  const int first = blockIdx.x * kPer;
-  // two passes over this thread's blocks: their sum, then (with the sums before) what begins in them
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    if (pass == 1) {
-      a = block_scan<kThreads>(work, other, total, total_rest, sh);
-      const int most = sms_of(set, total, rest, total_rest, p.sms) * kPer;
-      shares = Shares(total, total == 0 ? 0 : max(1, min(most, total / set.min_steps)));
-      lo = shares.begin(min(first, shares.count));
-      hi = shares.begin(min(first + kPer, shares.count));
-      if (blockIdx.x != 0 && (a >= hi || a + work <= lo)) break;
-    }
-#pragma unroll 1
-    for (int e = e0; e < e1; ++e) {
-      if (pass == 0 || per > 1) load_block<kRows, kTokens>(p, set, e, k, blockIdx.x == 0 && pass == 0);
-      const int w = k.steps * p.hkv;
-      if (pass == 0) {
-        work += w;
-        continue;
-      }
-      if (blockIdx.x == 0) set.base[e] = a;
-#pragma unroll 1
-      for (int i = 0; i < kPer && first + i < shares.count; ++i) {
-        const int g = shares.begin(first + i);
-        if (g >= a && g < a + w) {
-          sh.e[i] = e;
-          sh.rest[i] = g - a;
-          if (set.start) set.start[first + i] = make_int2(e, g - a);
-        }
-      }
-      a += w;
-    }
+  for (int e = f0; e < f1; ++e) {
+    Block k;
+    load_block<kFewRows, kBoxTokens>(p, p.few, e, k, blockIdx.x == 0);
+    work_f += k.steps * p.hkv;
   }
-  if (blockIdx.x == 0 && tid == 0) {
-    set.base[blocks] = total;
-    set.base[blocks + 1] = shares.count;
+  int a = work_w, f = work_f;
+  block_scan<kThreads>(a, f, total_w, total_f, sh);
+  const int ctas = wide_sms(p, total_w, total_f);
+  Place at;
+  at.wide = (int)blockIdx.x < ctas;
+  at.first = at.wide ? blockIdx.x : ((int)blockIdx.x - ctas) * kWarps;
+  const int total = at.wide ? total_w : total_f, most = at.wide ? ctas : (p.sms - ctas) * kWarps;
+  const int least = at.wide ? p.wide.min_steps : p.few.min_steps;
+  at.shares = Shares(total, total == 0 ? 0 : max(1, min(most, total / least)));
+  const bool leave = at.first == 0;
+  if (at.wide) find_starts<kWideRows, kWideTokens>(p, p.wide, at, pw, w0, w1, a, work_w, leave, sh);
+  else find_starts<kFewRows, kBoxTokens>(p, p.few, at, pf, f0, f1, f, work_f, leave, sh);
+  if (leave && tid == 0) {
+    const WorkSet& set = at.wide ? p.wide : p.few;
+    set.base[set.blocks()] = total;
+    set.base[set.blocks() + 1] = at.shares.count;
   }
+  if (blockIdx.x == 0 && tid == 0 && total_w == 0 && bw > 0) p.wide.base[bw] = p.wide.base[bw + 1] = 0;
   __syncthreads();
-  return shares;
+  return at;
 }
 
 template <int kRows, int kTokens>

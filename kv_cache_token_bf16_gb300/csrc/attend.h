@@ -12,6 +12,7 @@ namespace evict {
 constexpr int kBoxTokens = 16;       // rows of K and V that a warp of the few-row kernel takes at a time
 constexpr int kWideTokens = 128;     // rows that a CTA of the wide kernel takes at a time
 constexpr int kFewRows = 16;         // query rows of a unit of the few-row kernel (one MMA tile)
+constexpr float kWideStart = 8000.f; // clocks by which the wide kernel's start is longer
 constexpr int kWideRows = 256;       // query rows of a unit of the wide kernel (two MMA tiles)
 
 // Quotient by a divisor that the host knows, for dividends below 2^31: a multiplication and a shift.
@@ -58,8 +59,9 @@ struct WorkSet {
 };
 
 struct AttendParams {
-  CUtensorMap tm_pk, tm_pv;          // prefix [prefix_batch][n_kv_heads][n_prefix][128]
-  CUtensorMap tm_k, tm_v;            // pages [n_pages][n_kv_heads][page_size][128]
+  // K and V: the prefix [prefix_batch][n_kv_heads][n_prefix][128], the pages
+  // [n_pages][n_kv_heads][page_size][128]
+  CUtensorMap few_pre[2], few_own[2], wide_pre[2], wide_own[2];
   WorkSet few, wide;                 // of the two kernels
   int sms;
   const void* q;
@@ -83,11 +85,7 @@ struct AttendParams {
   int out_sectors;                   // every row of out begins on a multiple of 32 bytes
   float scale2;                      // log2(e) * scale
   int* tok_base;                     // [batch + 1] new tokens of the sequences before (with n_new)
-  int late_wait;                     // this kernel may start before its predecessor has ended
   int* err;
 };
-
-cudaError_t prepare_wide();
-cudaError_t launch_wide(const AttendParams& p, int ctas, bool early, cudaStream_t st);
 
 }  // namespace evict

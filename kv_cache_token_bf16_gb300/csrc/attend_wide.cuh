@@ -1,7 +1,7 @@
-// Attention of many query rows over a shared prefix or a sequence's rows
-// (see attend.cu for the operator and the other kernels): tcgen05 tensor cores.
+// Attention of many query rows over a shared prefix or a sequence's rows (see attend.cu): tcgen05
+// tensor cores.
 //
-// attend_wide_kernel: persistent, one CTA of eleven warps per SM. A unit is a
+// A CTA works with eleven of its warps on its share. A unit is a
 // (stream, KV head, tile of 256 query rows); K and V stream through a ring of
 // five 32 KB tiles of 128 rows (TMA). Warps 0-3 and 4-7 are two softmax
 // groups, a thread per query row, each with its own 128 x 128 logits and
@@ -26,15 +26,11 @@
 // output's error grows from one rounding to the root of two.
 //
 // Bound: the tensor cores (2 x 512 clocks a job) with many rows, HBM with few.
+#pragma once
+
 #include <cuda_bf16.h>
-#include <cuda_runtime.h>
 
 #include "attend.cuh"
-#include "attend.h"
-#include "common.cuh"
-#include "launch.h"
-#include "pipeline.cuh"
-#include "tcgen05.cuh"
 
 namespace evict {
 namespace {
@@ -42,8 +38,7 @@ namespace {
 constexpr int kTile = 128;
 constexpr int kTileBytes = kTile * kHeadDim * 2;
 constexpr int kRing = 5;
-constexpr int kWideThreads = 11 * 32;
-constexpr int kWideSmem = (2 + kRing) * kTileBytes + 1024;
+constexpr int kWideSmem = (2 + kRing) * kTileBytes;
 constexpr int kMmaWarp = 8, kTmaWarp = 10;
 constexpr int kBadWords = 9;                      // 257 tokens and more
 constexpr int kBadSets = 16;                      // segments in flight, by far
@@ -55,7 +50,6 @@ struct WideShared {
   uint32_t tmem_base;
   int fail, turn;
   uint32_t bad[kBadSets][kBadWords];              // of the segments in turn: rows of V that were blanked
-  ScanShared scan;
 };
 
 using WideCursor = Cursor<kWideRows, kWideTokens>;
@@ -124,10 +118,10 @@ __device__ void producer(const AttendParams& p, WideShared& sh, WideCursor c, in
         __syncwarp();
         if (pre) {
           if (lane < 2)
-            tma_load_5d(dst + lane * (kTileBytes / 2), kv ? &p.tm_pv : &p.tm_pk, 0, row0, lane, c.h, plane, bar);
+            tma_load_5d(dst + lane * (kTileBytes / 2), &p.wide_pre[kv], 0, row0, lane, c.h, plane, bar);
         } else if (lane < boxes) {
           for (int hf = 0; hf < 2; ++hf)
-            tma_load_5d(dst + hf * (kTileBytes / 2) + lane * box * 128, kv ? &p.tm_v : &p.tm_k, 0,
+            tma_load_5d(dst + hf * (kTileBytes / 2) + lane * box * 128, &p.wide_own[kv], 0,
                         row & ((1 << p.page_shift) - 1), hf, c.h, page, bar);
         }
         slot.next();
@@ -589,12 +583,16 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
         wait32(x[0]);
         load32(s_at + 64 * half + 32, x[1]);
         if (masked) hide(0);
-        got = weights(0);
-        wait32(x[1]);
-        if (masked) hide(1);
-        got += weights(1);
-        // no reference yet, or a sum that says that it has fallen far behind the maximum (NaN as well)
-        if (__any_sync(0xffffffffu, ref == -INFINITY || !(got < kMoveAbove))) {
+#pragma unroll 1
+        for (bool again = false;; again = true) {
+          got = weights(0);
+          if (!again) {
+            wait32(x[1]);
+            if (masked) hide(1);
+          }
+          got += weights(1);
+          // no reference yet, or a sum that says that it has fallen far behind the maximum (NaN as well)
+          if (again || !__any_sync(0xffffffffu, ref == -INFINITY || !(got < kMoveAbove))) break;
           float top = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 32; ++k) top = fmax3(top, x[0][k], x[1][k]);
@@ -603,8 +601,6 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
           sum *= f;
           move_reference(s_at, 32 * half, begun ? o_at : 0, f);
           nb = -base_of(ref);
-          got = weights(0);
-          got += weights(1);
         }
         sum += got;
         // over columns that are in registers by now: half 0 over 0 .. 31, half 1 over 32 .. 63
@@ -627,66 +623,48 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
   }
 }
 
-__global__ void __launch_bounds__(kWideThreads, 1) attend_wide_kernel(const __grid_constant__ AttendParams p, int early) {
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ WideShared sh;
-  const int tid = threadIdx.x, warp = tid >> 5;
-  unsigned char* qbuf = reinterpret_cast<unsigned char*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  const uint32_t q_at = tc::smem_u32(qbuf), ring = q_at + 2 * kTileBytes;
+// Before the totals are known: tensor memory, barriers. The whole CTA.
+__device__ __forceinline__ void wide_setup(WideShared& sh) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == 0) tc::tmem_alloc(&sh.tmem_base, 4 * kTile);
-  if (warp == 1 && (tid & 31) < kRing) {
-    tc::mbar_init(&sh.kv_full[tid & 31], 1);
-    tc::mbar_init(&sh.kv_empty[tid & 31], 2);     // both groups' MMA warps
+  if (warp == 1 && lane < kRing) {
+    tc::mbar_init(&sh.kv_full[lane], 1);
+    tc::mbar_init(&sh.kv_empty[lane], 2);         // both groups' MMA warps
   }
-  if (warp == 2 && (tid & 31) < 2) {
-    const int w = tid & 31;
-    tc::mbar_init(&sh.q_full[w], kTile);
-    tc::mbar_init(&sh.s_full[w], 1);
-    tc::mbar_init(&sh.p_full[w], kTile);
-    tc::mbar_init(&sh.o_full[w], 1);
-    tc::mbar_init(&sh.done[w], 1);
+  if (warp == 2 && lane < 2) {
+    tc::mbar_init(&sh.q_full[lane], kTile);
+    tc::mbar_init(&sh.s_full[lane], 1);
+    tc::mbar_init(&sh.p_full[lane], kTile);
+    tc::mbar_init(&sh.o_full[lane], 1);
+    tc::mbar_init(&sh.done[lane], 1);
   }
-  if (warp == 3) prefetch_maps(p, p.wide, tid & 31);
   if (warp > 3) {
-    for (int i = tid - 128; i < kBadSets * kBadWords; i += kWideThreads - 128) (&sh.bad[0][0])[i] = 0;
+    for (int i = tid - 128; i < kBadSets * kBadWords; i += blockDim.x - 128) (&sh.bad[0][0])[i] = 0;
     if (tid == 128) sh.fail = sh.turn = 0;
   }
-  pdl_wait();
-  // what comes next may start on an SM as soon as this kernel leaves it
-  if (early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Shares shares = find_shares<kWideRows, kWideTokens, kFewRows, kBoxTokens, kWideThreads, 1>(p, p.wide, p.few, sh.scan);
-  const int mine = blockIdx.x;
-  const int count = mine < shares.count ? shares.begin(mine + 1) - shares.begin(mine) : 0;
+}
+__device__ __forceinline__ void wide_teardown(const WideShared& sh) {
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = sh.tmem_base;
-  if (count > 0) {
-    const WideCursor c = place<kWideRows, kWideTokens>(p, p.wide, sh.scan.e[0], sh.scan.rest[0]);
-    if (warp == kTmaWarp) {
-      producer(p, sh, c, count, ring);
-    } else if (warp >= kMmaWarp) {
-      if ((tid & 31) == 0) mma_issuer(p, sh, c, count, warp - kMmaWarp, tmem, q_at, ring);
-      __syncwarp();
-    } else {
-      softmax_group(p, sh, c, count, warp >> 2, tid & (kTile - 1), tmem, qbuf, ring);
-    }
+  if (threadIdx.x < 32) tc::tmem_dealloc(sh.tmem_base, 4 * kTile);
+}
+
+// The wide kernel's part of a CTA: `count` steps from where its share begins.
+__device__ __forceinline__ void wide_rows(const AttendParams& p, WideShared& sh, const ScanShared& scan, int count,
+                                          unsigned char* qbuf) {
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const uint32_t q_at = tc::smem_u32(qbuf), ring = q_at + 2 * kTileBytes, tmem = sh.tmem_base;
+  const WideCursor c = place<kWideRows, kWideTokens>(p, p.wide, scan.e[0], scan.rest[0]);
+  if (warp == kTmaWarp) {
+    producer(p, sh, c, count, ring);
+  } else if (warp >= kMmaWarp && warp < kTmaWarp) {
+    if ((tid & 31) == 0) mma_issuer(p, sh, c, count, warp - kMmaWarp, tmem, q_at, ring);
+    __syncwarp();
+  } else if (warp < kMmaWarp) {
+    softmax_group(p, sh, c, count, warp >> 2, tid & (kTile - 1), tmem, qbuf, ring);
   }
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  if (warp == 0) tc::tmem_dealloc(tmem, 4 * kTile);
 }
 
 }  // namespace
-
-cudaError_t prepare_wide() {
-  return cudaFuncSetAttribute(attend_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
-}
-
-// early: the next kernel in the stream waits for this one by itself (late_wait).
-cudaError_t launch_wide(const AttendParams& p, int ctas, bool early, cudaStream_t st) {
-  return launch_pdl(attend_wide_kernel, dim3(ctas), dim3(kWideThreads), kWideSmem, st, nullptr, p, early ? 1 : 0);
-}
-
 }  // namespace evict
