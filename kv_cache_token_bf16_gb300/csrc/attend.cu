@@ -73,9 +73,9 @@ struct Parts {
 // Row r of block e (its tile, of `rows` rows) and head h.
 __device__ __forceinline__ Parts find_parts(const AttendParams& p, const WorkSet& set, int rows, int e, int h, int r,
                                             int block_rows) {
-  const int g0 = set.base[e], steps = p.by_hkv.div(set.base[e + 1] - g0);
+  const int g0 = set.base[e], per = p.by_hkv.div(set.base[e + 1] - g0), steps = per - set.entry;
   const Shares shares(set);
-  const int g = g0 + h * steps;
+  const int g = g0 + h * per + set.entry;
   const int c0 = shares.of(g), c1 = shares.of(g + steps - 1);
   return Parts{set.part_ml, set.part_o, e * p.hkv + h + c0, c1 - c0 + 1, rows, r, rows == kWideRows && block_rows <= 128};
 }
@@ -187,8 +187,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_split_kernel(cons
   const int2 at = set.start[c];
   Block k;
   load_block<kWideRows, kWideTokens>(p, set, at.x, k);
-  const int h = at.y / k.steps, r = at.y - h * k.steps;
-  if (r == 0) return;                             // the share begins with the unit
+  const int per = k.steps + set.entry, h = at.y / per, r = at.y - h * per - set.entry;
+  if (r <= 0) return;                             // the share begins with the unit
   const int first = shares.begin(c) - r;          // the unit's first step
   if (c > 1 && shares.begin(c - 1) > first) return;
   const int c1 = shares.of(first + k.steps - 1), row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
@@ -254,6 +254,8 @@ constexpr int kFewMinBoxes = 4;
 constexpr int kWideMinSteps = 4;
 // Clocks of an SM for a box of 16 rows and for a step of 128 rows (with two groups), side by side.
 constexpr int kFewCost = 275, kWideCost = 4600;
+// What a unit's start costs beside: a warp or CTA fetches its queries and leaves the last unit's results.
+constexpr int kFewEntry = 1, kWideEntry = 3;
 
 // Sizes alone decide: lens and n_new are the device's.
 int make_plan(const evict_attention* a, Plan* out) {
@@ -293,7 +295,7 @@ int make_plan(const evict_attention* a, Plan* out) {
     s.by_seq_tiles = Divisor(s.seq_tiles);
     const long long pre_steps = (a->n_prefix + tokens - 1) / tokens, seq_steps = (seq_tokens + tokens - 1) / tokens + 1;
     const long long work = ((long long)s.prefixes * s.prefix_tiles * pre_steps +
-                            (long long)s.seqs * s.seq_tiles * (seq_steps + (s.joint ? pre_steps : 0))) * a->n_kv_heads;
+                            (long long)s.seqs * s.seq_tiles * (seq_steps + (s.joint ? pre_steps : 0)) + 4ll * s.blocks()) * a->n_kv_heads;
     return work < (1ll << 31) && ((long long)s.blocks() + 1) * a->n_kv_heads < (1ll << 30);
   };
   if (!tiles(P.few, kRows, kBoxTokens) || !tiles(P.wide, kWideRows, kWideTokens))
@@ -306,10 +308,12 @@ int make_plan(const evict_attention* a, Plan* out) {
   P.few.max_shares = P.sms * kWarps;
   P.few.min_steps = kFewMinBoxes;
   P.few.cost = kFewCost;
+  P.few.entry = kFewEntry;
   P.wide.workers = 1;
   P.wide.max_shares = P.sms;
   P.wide.min_steps = kWideMinSteps;
   P.wide.cost = kWideCost;
+  P.wide.entry = kWideEntry;
   size_t off = kWorkHead + round256((size_t)(a->batch + 1) * sizeof(int));
   lay_out(P.few, a->n_kv_heads, kRows, off);
   lay_out(P.wide, a->n_kv_heads, kWideRows, off);

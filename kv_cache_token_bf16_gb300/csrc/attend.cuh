@@ -96,14 +96,26 @@ __device__ __forceinline__ void load_block(const AttendParams& p, const WorkSet&
   }
 }
 
+// Steps of a block's units, entries included.
+__device__ __forceinline__ int work_of(const AttendParams& p, const WorkSet& set, const Block& k) {
+  return k.steps ? (k.steps + set.entry) * p.hkv : 0;
+}
+
 // A position in the line of steps.
 template <int kRows, int kTokens>
 struct Cursor {
-  int e, h, step, unit;
+  int e, h, step, unit;              // step < 0: in the unit's entry
   Block k;
+  // past the entry, as far as the share's `left` steps reach
+  __device__ __forceinline__ void settle(int& left) {
+    if (step >= 0) return;
+    const int pay = min(left, -step);
+    step += pay;
+    left -= pay;
+  }
   // on to the next unit
   __device__ __forceinline__ void next_unit(const AttendParams& p, const WorkSet& set, int blocks) {
-    step = 0;
+    step = -set.entry;
     ++unit;
     if (++h < p.hkv) return;
     h = 0;
@@ -199,7 +211,7 @@ __device__ __forceinline__ void find_starts(const AttendParams& p, const WorkSet
     if (per > 1) {
       Block k;
       load_block<kRows, kTokens>(p, set, e, k);
-      w = k.steps * p.hkv;
+      w = work_of(p, set, k);
     }
     if (leave) set.base[e] = a;
 #pragma unroll 1
@@ -245,13 +257,13 @@ __device__ __forceinline__ Place find_place(const AttendParams& p, ScanShared& s
   for (int e = w0; e < w1; ++e) {
     Block k;
     load_block<kWideRows, kWideTokens>(p, p.wide, e, k, blockIdx.x == 0);
-    work_w += k.steps * p.hkv;
+    work_w += work_of(p, p.wide, k);
   }
 #pragma unroll 1
   for (int e = f0; e < f1; ++e) {
     Block k;
     load_block<kFewRows, kBoxTokens>(p, p.few, e, k, blockIdx.x == 0);
-    work_f += k.steps * p.hkv;
+    work_f += work_of(p, p.few, k);
   }
   int a = work_w, f = work_f;
   block_scan<kThreads>(a, f, total_w, total_f, sh);
@@ -280,8 +292,8 @@ __device__ __forceinline__ Cursor<kRows, kTokens> place(const AttendParams& p, c
   Cursor<kRows, kTokens> c;
   c.e = e;
   load_block<kRows, kTokens>(p, set, e, c.k);
-  c.h = rest / c.k.steps;
-  c.step = rest - c.h * c.k.steps;
+  c.h = rest / (c.k.steps + set.entry);
+  c.step = rest - c.h * (c.k.steps + set.entry) - set.entry;
   c.unit = e * p.hkv + c.h;
   return c;
 }

@@ -36,9 +36,10 @@ struct Divisor {
 // streams are the prefixes (all query rows of their sequences), then the
 // sequences (their own pages; `joint`: behind the prefix as well). A unit is a
 // block and a KV head, and its work the rows of K and V that the tile sees, in
-// steps of 16 (few-row kernel) or 128 (wide kernel) rows. The steps of all
-// units, in the order of blocks and heads, are laid end to end and cut into
-// equal contiguous shares, one for every warp (few-row kernel) or CTA (wide).
+// steps of 16 (few-row kernel) or 128 (wide kernel) rows, behind `entry` more
+// for its start. The steps of all units, in the order of blocks and heads, are
+// laid end to end and cut into equal contiguous shares, one for every warp
+// (few-row kernel) or CTA (wide).
 // Where a call has work for both kernels, they run side by side on different SMs, as many as their
 // work asks for.
 // What a share holds of a unit leaves one partial result, in slot unit +
@@ -48,6 +49,7 @@ struct WorkSet {
   int seqs, seq_tiles;               // streams of sequences: 0 or the batch; blocks of one
   int joint;                         // a sequence's stream begins with its prefix
   int workers, min_steps;            // shares that a CTA takes (its warps, or itself); steps of a share at least
+  int entry;                         // steps that the start of a unit counts as
   int cost;                          // of a step: clocks of an SM, roughly
   int max_shares;                    // workers of every SM
   Divisor by_prefix_tiles, by_seq_tiles;

@@ -60,6 +60,7 @@ __device__ __forceinline__ void few_rows(const AttendParams& p, FewShared& sh, c
   if (share < shares.count) {
     int left = shares.begin(share + 1) - shares.begin(share);
     Cur cur = place<kRows, kBoxTokens>(p, set, scan.e[warp], scan.rest[warp]);
+    cur.settle(left);
 
     // --- the ring: boxes are requested in the order in which they are used ---
     Cur ahead = cur;
@@ -86,7 +87,10 @@ __device__ __forceinline__ void few_rows(const AttendParams& p, FewShared& sh, c
         tma_load_5d(dst, pre ? &p.few_pre[0] : &p.few_own[0], 0, row, 0, ahead.h, plane, bar);
         tma_load_5d(dst + kBoxBytes, pre ? &p.few_pre[1] : &p.few_own[1], 0, row, 0, ahead.h, plane, bar);
       }
-      if (--ahead_left > 0 && ++ahead.step == ahead.k.steps) ahead.next_unit(p, set, blocks);
+      if (--ahead_left > 0 && ++ahead.step == ahead.k.steps) {
+        ahead.next_unit(p, set, blocks);
+        ahead.settle(ahead_left);
+      }
       look_up();
     };
     look_up();
@@ -298,7 +302,10 @@ __device__ __forceinline__ void few_rows(const AttendParams& p, FewShared& sh, c
         }
       }
       left -= boxes;
-      if (left > 0) cur.next_unit(p, set, blocks);
+      if (left > 0) {
+        cur.next_unit(p, set, blocks);
+        cur.settle(left);
+      }
     }
   }
 }

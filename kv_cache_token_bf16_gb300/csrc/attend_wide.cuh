@@ -91,7 +91,7 @@ __device__ void producer(const AttendParams& p, WideShared& sh, WideCursor c, in
   Slot slot;
   int used = 0;
   bool ok = true;
-  while (ok) {
+  while (ok && count > 0) {
     const Segment g(p, c, count);
     const int plane = c.k.s < set.prefixes ? c.k.s : p.fan ? p.by_fan.div(c.k.s - set.prefixes) : 0;
     const int32_t* table = p.table + (long long)(c.k.s - set.prefixes) * p.table_stride;
@@ -131,6 +131,7 @@ __device__ void producer(const AttendParams& p, WideShared& sh, WideCursor c, in
     count -= g.steps;
     if (count == 0) break;
     c.next_unit(p, set, blocks);
+    c.settle(count);
   }
   // every copy issued must land before the CTA may release its shared memory
   for (int i = 0; i < kRing && i < used; ++i) drain_phase(&sh.kv_full[i], ((used - 1 - i) / kRing) & 1, p.err);
@@ -210,7 +211,7 @@ __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, 
 #pragma unroll 1
     for (; tiles > 0 && wait(&sh.kv_full[slot.i], slot.parity); --tiles, slot.next()) tc::mbar_arrive(&sh.kv_empty[slot.i]);
   };
-  while (ok) {
+  while (ok && count > 0) {
     const Segment g(p, c, count);
     const int jobs = g.jobs(w);
     Slot v;
@@ -280,6 +281,7 @@ __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, 
     count -= g.steps;
     if (count == 0 || !ok) break;
     c.next_unit(p, set, blocks);
+    c.settle(count);
   }
   // every MMA must finish before tensor and shared memory are released
   tc::mma_commit(&sh.done[w]);
@@ -433,13 +435,16 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
     const WideCursor at = c;
     const Segment part = g;
     const QueryRow mine = q;
-    const bool more = segment < 0 || count > part.steps;
-    if (segment >= 0) count -= part.steps;
-    if (more) {
-      if (segment >= 0) {
+    if (segment >= 0) {
+      count -= part.steps;
+      if (count > 0) {
         c.next_unit(p, set, blocks);
-        g = Segment(p, c, count);
+        c.settle(count);
       }
+    }
+    const bool more = count > 0;
+    if (more) {
+      g = Segment(p, c, count);
       q = load_query(c, g);
     }
     if (segment >= 0) {
@@ -655,7 +660,8 @@ __device__ __forceinline__ void wide_rows(const AttendParams& p, WideShared& sh,
                                           unsigned char* qbuf) {
   const int tid = threadIdx.x, warp = tid >> 5;
   const uint32_t q_at = tc::smem_u32(qbuf), ring = q_at + 2 * kTileBytes, tmem = sh.tmem_base;
-  const WideCursor c = place<kWideRows, kWideTokens>(p, p.wide, scan.e[0], scan.rest[0]);
+  WideCursor c = place<kWideRows, kWideTokens>(p, p.wide, scan.e[0], scan.rest[0]);
+  c.settle(count);
   if (warp == kTmaWarp) {
     producer(p, sh, c, count, ring);
   } else if (warp >= kMmaWarp && warp < kTmaWarp) {
