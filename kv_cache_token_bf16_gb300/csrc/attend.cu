@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     if (at.first < at.shares.count)
       wide_rows(p, wide, scan, at.shares.begin(at.first + 1) - at.shares.begin(at.first), smem);
   } else {
-    few_rows(p, few, scan, at.shares, at.first, tc::smem_u32(smem));
+    few_rows(p, few, scan, at, tc::smem_u32(smem));
   }
   if (may_wide) wide_teardown(wide);
 }
@@ -129,7 +129,7 @@ struct Merge {
 // (few rows have many parts each, and one warp would wait for memory part after part) and their
 // results meet in shared memory, in the order of the warps.
 template <int kSplit>
-__global__ void __launch_bounds__(kJoinWarps * 32, 5) attend_join_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) attend_join_kernel(const __grid_constant__ AttendParams p) {
   __shared__ float4 acc[kJoinWarps][32];
   __shared__ float2 ml[kJoinWarps];
   pdl_wait();
@@ -252,10 +252,11 @@ constexpr size_t kWorkHead = 256;                 // an error word, for callers 
 // to read.
 constexpr int kFewMinBoxes = 4;
 constexpr int kWideMinSteps = 4;
-// Clocks of an SM for a box of 16 rows and for a step of 128 rows (with two groups), side by side.
-constexpr int kFewCost = 275, kWideCost = 4600;
+// Clocks of an SM, side by side, for a box of 16 rows, and for a step of 128 rows with two groups of
+// query rows at it, or with the groups taking turns.
+constexpr int kFewCost = 262, kWideCostTwo = 4600, kWideCostAlt = 2800;
 // What a unit's start costs beside: a warp or CTA fetches its queries and leaves the last unit's results.
-constexpr int kFewEntry = 1, kWideEntry = 3;
+constexpr int kFewEntry = 2, kWideEntry = 3;
 
 // Sizes alone decide: lens and n_new are the device's.
 int make_plan(const evict_attention* a, Plan* out) {
@@ -312,7 +313,7 @@ int make_plan(const evict_attention* a, Plan* out) {
   P.wide.workers = 1;
   P.wide.max_shares = P.sms;
   P.wide.min_steps = kWideMinSteps;
-  P.wide.cost = kWideCost;
+  P.wide.cost = (P.wide.prefixes ? pre_rows : own_rows) > 128 ? kWideCostTwo : kWideCostAlt;
   P.wide.entry = kWideEntry;
   size_t off = kWorkHead + round256((size_t)(a->batch + 1) * sizeof(int));
   lay_out(P.few, a->n_kv_heads, kRows, off);

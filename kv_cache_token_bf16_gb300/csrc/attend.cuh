@@ -190,10 +190,11 @@ __device__ __forceinline__ void block_scan(int& a, int& b, int& total, int& tota
   b = y - b;
 }
 
-// What a CTA works on: its first share (of one for wide units, of its warps otherwise).
+// What a CTA works on: for wide units one share, otherwise one for each of its warps, `stride` apart
+// (where there are fewer shares than warps, every SM has some).
 struct Place {
   bool wide;
-  int first;
+  int first, stride;
   Shares shares;
 };
 
@@ -202,9 +203,6 @@ struct Place {
 template <int kRows, int kTokens>
 __device__ __forceinline__ void find_starts(const AttendParams& p, const WorkSet& set, const Place& at, int per, int e0,
                                             int e1, int a, int work, bool leave, ScanShared& sh) {
-  const int lo = at.shares.begin(min(at.first, at.shares.count));
-  const int hi = at.shares.begin(min(at.first + set.workers, at.shares.count));
-  if (!leave && (a >= hi || a + work <= lo)) return;
 #pragma unroll 1
   for (int e = e0; e < e1; ++e) {
     int w = work;
@@ -215,8 +213,10 @@ __device__ __forceinline__ void find_starts(const AttendParams& p, const WorkSet
     }
     if (leave) set.base[e] = a;
 #pragma unroll 1
-    for (int i = 0; i < set.workers && at.first + i < at.shares.count; ++i) {
-      const int g = at.shares.begin(at.first + i);
+    for (int i = 0; i < set.workers && w > 0; ++i) {
+      const int share = at.first + i * at.stride;
+      if (share >= at.shares.count) break;
+      const int g = at.shares.begin(share);
       if (g >= a && g < a + w) {
         sh.e[i] = e;
         sh.rest[i] = g - a;
@@ -270,7 +270,8 @@ __device__ __forceinline__ Place find_place(const AttendParams& p, ScanShared& s
   const int ctas = wide_sms(p, total_w, total_f);
   Place at;
   at.wide = (int)blockIdx.x < ctas;
-  at.first = at.wide ? blockIdx.x : ((int)blockIdx.x - ctas) * kWarps;
+  at.first = at.wide ? blockIdx.x : blockIdx.x - ctas;
+  at.stride = p.sms - ctas;
   const int total = at.wide ? total_w : total_f, most = at.wide ? ctas : (p.sms - ctas) * kWarps;
   const int least = at.wide ? p.wide.min_steps : p.few.min_steps;
   at.shares = Shares(total, total == 0 ? 0 : max(1, min(most, total / least)));

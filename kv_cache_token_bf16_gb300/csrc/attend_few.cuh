@@ -48,15 +48,16 @@ __device__ __forceinline__ void few_setup(FewShared& sh) {
   if (tid == 0) sh.fail = 0;
 }
 
-// The few-row kernel's part of a CTA whose shares begin at `first`; ring0: 1024-byte aligned.
-__device__ __forceinline__ void few_rows(const AttendParams& p, FewShared& sh, const ScanShared& scan, const Shares& shares,
-                                         int first, uint32_t ring0) {
+// The few-row kernel's part of a CTA: a share for each of its warps; ring0: 1024-byte aligned.
+__device__ __forceinline__ void few_rows(const AttendParams& p, FewShared& sh, const ScanShared& scan, const Place& at,
+                                         uint32_t ring0) {
   using Cur = Cursor<kRows, kBoxTokens>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t ring = ring0 + warp * kStages * 2 * kBoxBytes;
   const WorkSet& set = p.few;
   const int blocks = set.blocks();
-  const int share = first + warp;
+  const Shares& shares = at.shares;
+  const int share = at.first + warp * at.stride;
   if (share < shares.count) {
     int left = shares.begin(share + 1) - shares.begin(share);
     Cur cur = place<kRows, kBoxTokens>(p, set, scan.e[warp], scan.rest[warp]);
