@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -219,7 +220,7 @@ constexpr int kWideFrom = kRows + 1, kOwnWideFrom = 2 * kRows + 1, kJointFrom = 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Plan {
-  int sms;
+  int dev, sms;
   WorkSet few, wide;        // counts, and offsets into the workspace in place of pointers
   size_t bytes;
 };
@@ -250,8 +251,8 @@ void rebase(WorkSet& s, char* base) {
 constexpr size_t kWorkHead = 256;                 // an error word, for callers without one
 // Boxes (steps) that a share has at least: fewer would leave more partial results to merge than rows
 // to read.
-constexpr int kFewMinBoxes = 4;
-constexpr int kWideMinSteps = 4;
+constexpr int kFewMinBoxes = 2;
+constexpr int kWideMinSteps = 3;
 // Clocks of an SM, side by side, for a box of 16 rows, and for a step of 128 rows with two groups of
 // query rows at it, or with the groups taking turns.
 constexpr int kFewCost = 262, kWideCostTwo = 4600, kWideCostAlt = 2800;
@@ -301,9 +302,8 @@ int make_plan(const evict_attention* a, Plan* out) {
   };
   if (!tiles(P.few, kRows, kBoxTokens) || !tiles(P.wide, kWideRows, kWideTokens))
     return fail(EVICT_ELIMIT, "the batch's heads and rows (to the tables' width) are too many for one call");
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P.sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = cudaGetDevice(&P.dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P.sms, cudaDevAttrMultiProcessorCount, P.dev);
   if (e != cudaSuccess) return cuda_fail(e, "looking up the device");
   P.few.workers = kWarps;
   P.few.max_shares = P.sms * kWarps;
@@ -329,6 +329,16 @@ int check_rows(const evict_rows& x, int heads, const char* name) {
     return fail(EVICT_EINVAL, "%s: addresses and strides must be multiples of 16 bytes", name);
   if (x.stride_b < 0 || x.stride_h < 0 || x.stride_m < 0) return fail(EVICT_EINVAL, "%s: strides must not be negative", name);
   return EVICT_OK;
+}
+
+// The kernel's dynamic shared memory, allowed once for each device.
+cudaError_t allow_smem(int dev) {
+  static std::atomic<uint64_t> done{0};
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e == cudaSuccess) done.fetch_or(bit);
+  return e;
 }
 
 }  // namespace
@@ -439,7 +449,7 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
   // a stream is of one kind, so either kind's maps have a place of their own
   if ((rc = encode(false, P.few, P.few_pre, P.few_own)) || (rc = encode(true, P.wide, P.wide_pre, P.wide_own))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(a->stream);
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = allow_smem(plan.dev);
   if (e != cudaSuccess) return cuda_fail(e, "attention kernel attribute");
   if (P.few.blocks() + P.wide.blocks() > 0) {
     if ((e = launch_pdl(attend_kernel, dim3(plan.sms), dim3(kThreads), kSmem, st, nullptr, P)) != cudaSuccess)

@@ -25,72 +25,109 @@ Work goes on the current stream of the tensors' device; nothing is synchronised.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 from . import binding
 from .binding import EVICT_BF16, EVICT_FP32, HEAD_DIM, EvictAttention, EvictPages, EvictRotaryConfig, EvictRows
 
 PAGE_SIZES = (16, 32, 64, 128, 256)
 
+# A decode step calls these functions for every layer, in tens of microseconds in all: the argument
+# structs are packed in one call each instead of field by field (evict_rows; evict_attention).
+_ROWS = struct.Struct("=Qqqqi4x")
+_ATTENTION = struct.Struct("=4i Qqqqi4x Qqqqi4x Q f4x QQ qq ii 6Q")
+assert _ROWS.size == ctypes.sizeof(EvictRows) and _ATTENTION.size == ctypes.sizeof(EvictAttention)
 
-def _torch():
+_torch = None
+_calls = None
+
+
+def _load():
+    """torch, and the library's calls with packed structs as arguments."""
+    global _torch, _calls
     import torch
-    return torch
+    lib = binding.load()
+    calls = ctypes.CDLL(lib._name)               # function objects of their own: other argument types
+    p, i, q = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+    packed = ctypes.c_char_p
+    for name, args in (("evict_rotate", [p, i, i, i, p, q, i, packed, packed, i, p]),
+                       ("evict_paged_append", [p, i, i, p, p, p, q, packed, packed, packed, packed, p]),
+                       ("evict_shared_attention", [packed])):
+        fn = getattr(calls, name)
+        fn.restype, fn.argtypes = i, args
+    _torch, _calls = torch, calls
 
 
 def _dtype(t):
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
+    if t is _torch.bfloat16:
         return EVICT_BF16
-    if t.dtype == torch.float32:
+    if t is _torch.float32:
         return EVICT_FP32
-    raise ValueError(f"bf16 or fp32 tensors only, not {t.dtype}")
+    raise ValueError(f"bf16 or fp32 tensors only, not {t}")
 
 
-def _rows(t, name, batch=None, m=None):
-    """EvictRows of a tensor [batch, heads, m, 128]."""
-    if t.dim() != 4 or t.shape[3] != HEAD_DIM:
-        raise ValueError(f"{name} must be [batch, heads, m, {HEAD_DIM}], not {tuple(t.shape)}")
-    if (batch is not None and t.shape[0] != batch) or (m is not None and t.shape[2] != m):
-        raise ValueError(f"{name} is {tuple(t.shape)}: batch or m differ from the other tensors")
+def _device(t):
+    """Index of a CUDA tensor's device."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    return index
+
+
+def _rows(t, name, index, dtype, batch=None, m=None, heads=None):
+    """The fields of a tensor's evict_rows [batch, heads, m, 128]."""
+    shape = t.shape
+    if len(shape) != 4 or shape[3] != HEAD_DIM:
+        raise ValueError(f"{name} must be [batch, heads, m, {HEAD_DIM}], not {tuple(shape)}")
+    if shape[0] != batch or shape[2] != m or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} is {tuple(shape)}: batch, m or heads differ from the other tensors")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} is {t.dtype}, not {dtype}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on CUDA device {index}")
     sb, sh, sm, se = t.stride()
     if se != 1:
         raise ValueError(f"{name}: the 128 elements of a row must be adjacent")
-    return EvictRows(t.data_ptr(), sb, sh, sm, t.shape[1])
+    return t.data_ptr(), sb, sh, sm, shape[1]
 
 
-def _like(t, name, shape, dtype, device):
-    """An int32 or fp32 side tensor: dense, of this shape, on this device. Its pointer."""
+def _like(t, name, shape, dtype, index):
+    """An int32 or fp32 side tensor: dense, of this shape, on this device. Its pointer (0 for None)."""
     if t is None:
-        return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}")
+        return 0
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on CUDA device {index}")
     return t.data_ptr()
 
 
-def _same_device(first, *others):
-    if not first.is_cuda:
-        raise ValueError("tensors must be on a CUDA device")
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
-    return first.device
+def _stream(index):
+    """The current stream of a device (as an integer)."""
+    raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw else _torch.cuda.current_stream(index).cuda_stream
 
 
 class _on:
-    """Makes a device current for the call (nothing to do where it already is)."""
+    """Makes a device current for a call."""
 
-    def __init__(self, device):
-        torch = _torch()
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    def __init__(self, index):
+        self.guard = _torch.cuda.device(index)
 
     def __enter__(self):
-        if self.guard:
-            self.guard.__enter__()
-        return _torch().cuda.current_stream().cuda_stream
+        self.guard.__enter__()
 
     def __exit__(self, *e):
-        if self.guard:
-            self.guard.__exit__(*e)
+        self.guard.__exit__(*e)
+
+
+def _call(index, fn, *args):
+    """fn(*args) with the device current; raises the library's error."""
+    if _torch.cuda.current_device() == index:
+        code = fn(*args)
+    else:
+        with _on(index):
+            code = fn(*args)
+    if code:
+        binding.check(code)
 
 
 class Rotary:
@@ -141,37 +178,51 @@ def rotate(rotary: Rotary, x, pos=None, pos_base: int = 0, out=None, transpose: 
 
     pos [n_axes, batch, m] int32 (with one axis also [batch, m]), or None: token t of every
     sequence is at pos_base + t. ``out`` (a tensor or pair; x itself rotates in place) defaults to
-    new dense tensors. ``transpose`` turns by the negative angle: the gradient of the rotation,
-    and with scale 1 its inverse.
+    new tensors with x's strides where they are dense. ``transpose`` turns by the negative angle:
+    the gradient of the rotation, and with scale 1 its inverse.
     """
-    torch = _torch()
-    one = torch.is_tensor(x)
+    if _torch is None:
+        _load()
+    one = isinstance(x, _torch.Tensor)
     xs = (x,) if one else tuple(x)
     if out is None:
-        outs = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in xs)
+        outs = tuple([_torch.empty_like(t) for t in xs])
     else:
-        outs = (out,) if torch.is_tensor(out) else tuple(out)
-    if len(outs) != len(xs) or not 1 <= len(xs) <= 2:
+        outs = (out,) if isinstance(out, _torch.Tensor) else tuple(out)
+    n = len(xs)
+    if len(outs) != n or not 1 <= n <= 2:
         raise ValueError("one or two tensors, and as many outputs")
-    device = _same_device(xs[0], *xs[1:], *outs)
-    batch, m = xs[0].shape[0], xs[0].shape[2]
-    for t, o in zip(xs, outs):
-        if t.dtype != xs[0].dtype or o.dtype != t.dtype or o.shape != t.shape:
-            raise ValueError("all tensors need one dtype, and outputs their input's shape")
-    ins = (EvictRows * len(xs))(*[_rows(t, "x", batch, m) for t in xs])
-    ous = (EvictRows * len(xs))(*[_rows(t, "out", batch, m) for t in outs])
-    with _on(device) as stream:
-        binding.evict_rotate(rotary.handle, _dtype(xs[0]), batch, m, _pos(pos, rotary, batch, m, device), pos_base,
-                             int(transpose), ins, ous, len(xs), stream)
+    first = xs[0]
+    index, dtype, shape = _device(first), first.dtype, first.shape
+    if len(shape) != 4:
+        raise ValueError(f"x must be [batch, heads, m, {HEAD_DIM}], not {tuple(shape)}")
+    batch, m = shape[0], shape[2]
+    ins = b"".join([_ROWS.pack(*_rows(t, "x", index, dtype, batch, m)) for t in xs])
+    ous = b"".join([_ROWS.pack(*_rows(o, "out", index, dtype, batch, m, t.shape[1])) for t, o in zip(xs, outs)])
+    _call(index, _calls.evict_rotate, rotary.handle, _dtype(dtype), batch, m, _pos(pos, rotary, batch, m, index), pos_base,
+          1 if transpose else 0, ins, ous, n, _stream(index))
     return outs[0] if one else outs
 
 
-def _pos(pos, rotary, batch, m, device):
+def _pos(pos, rotary, batch, m, index):
     if pos is None:
         return None
     n_axes = rotary.n_axes if rotary is not None else 1
-    shape = (batch, m) if pos.dim() == 2 and n_axes == 1 else (n_axes, batch, m)
-    return _like(pos, "pos", shape, _torch().int32, device)
+    shape = (batch, m) if n_axes == 1 and pos.dim() == 2 else (n_axes, batch, m)
+    return _like(pos, "pos", shape, _torch.int32, index)
+
+
+# Workspace bytes of a call's sizes, on a device (the sizes alone decide).
+_workspace = {}
+
+
+def _workspace_bytes(key, args):
+    if len(_workspace) >= 4096:
+        _workspace.clear()
+    with _on(key[0]):
+        n = binding.evict_shared_attention_workspace(EvictAttention.from_buffer_copy(args))
+    _workspace[key] = n
+    return n
 
 
 def shared_attention(q, prefix=None, pages: "PagedCache | None" = None, n_new=None, scale=None, out=None, lse=None):
@@ -183,52 +234,55 @@ def shared_attention(q, prefix=None, pages: "PagedCache | None" = None, n_new=No
     their own. Padding queries (t >= n_new[b]) leave their rows of ``out`` and ``lse`` as they are;
     a new ``out`` has zeros there. lse: fp32 [batch, n_q_heads, m] for the log-sum-exp. Returns out.
     """
-    torch = _torch()
-    device = _same_device(q, out, lse, n_new)
-    if q.dtype != torch.bfloat16:
-        raise ValueError(f"q must be bf16, not {q.dtype}")
-    batch, hq, m = q.shape[0], q.shape[1], q.shape[2] if q.dim() == 4 else 0
+    if _torch is None:
+        _load()
+    index, shape = _device(q), q.shape
+    if len(shape) != 4:
+        raise ValueError(f"q must be [batch, heads, m, {HEAD_DIM}], not {tuple(shape)}")
+    batch, hq, m, _ = shape
+    bf16 = _torch.bfloat16
     if out is None:
-        out = (torch.empty if n_new is None else torch.zeros)(q.shape, dtype=q.dtype, device=device)
-    elif out.dtype != q.dtype or out.shape != q.shape:
-        raise ValueError("out must have q's shape and dtype")
-    a = EvictAttention(batch=batch, m=m, n_q_heads=hq, q=_rows(q, "q"), out=_rows(out, "out"),
-                       lse=_like(lse, "lse", (batch, hq, m), torch.float32, device),
-                       n_new=_like(n_new, "n_new", (batch,), torch.int32, device))
-    if scale is not None:
-        if scale == 0:
-            raise ValueError("scale must not be 0")
-        a.scale = scale
+        out = _torch.empty_like(q) if n_new is None else _torch.zeros_like(q)
+    qr, outr = _rows(q, "q", index, bf16, batch, m), _rows(out, "out", index, bf16, batch, m, hq)
+    if scale is None:
+        scale = 0.0
+    elif scale == 0:
+        raise ValueError("scale must not be 0")
+    hkv = pages_at = error = width = page = 0
     if pages is not None:
-        if pages.batch != batch or pages.device != device:
+        if pages.batch != batch or pages.index != index:
             raise ValueError(f"the pages are for {pages.batch} sequences on {pages.device}")
-        a.pages = ctypes.pointer(pages.struct)
-        a.error = pages.error.data_ptr()
-        a.n_kv_heads = pages.n_kv_heads
+        hkv, pages_at, error, width, page = pages.n_kv_heads, pages.address, pages.error_at, pages.width, pages.page_size
+    pk = pv = sb = sh = n = groups = 0
     if prefix is not None:
         k, v = prefix
-        if k.dtype != q.dtype or v.dtype != q.dtype or k.shape != v.shape or k.dim() != 4 or k.shape[3] != HEAD_DIM:
+        ks = k.shape
+        if k.dtype is not bf16 or v.dtype is not bf16 or len(ks) != 4 or ks[3] != HEAD_DIM or ks != v.shape:
             raise ValueError(f"the prefix must be two bf16 tensors [prefix_batch, n_kv_heads, n, {HEAD_DIM}]")
-        _same_device(q, k, v)
-        if k.shape[2] > 0:
-            if pages is not None and k.shape[1] != pages.n_kv_heads:
-                raise ValueError(f"the prefix has {k.shape[1]} KV heads, the pages {pages.n_kv_heads}")
-            sb, sh, sn, se = k.stride()
-            if (v.stride(0), v.stride(1)) != (sb, sh) or se != 1 or v.stride(3) != 1 or \
-                    (k.shape[2] > 1 and (sn != HEAD_DIM or v.stride(2) != HEAD_DIM)):
+        if k.get_device() != index or v.get_device() != index:
+            raise ValueError(f"the prefix is not on CUDA device {index}")
+        if hkv and ks[1] != hkv:
+            raise ValueError(f"the prefix has {ks[1]} KV heads, the pages {hkv}")
+        hkv = ks[1]
+        if ks[2] > 0:
+            groups, n = ks[0], ks[2]
+            strides = k.stride()
+            sb, sh, sn, se = strides
+            if v.stride() != strides or se != 1 or (sn != HEAD_DIM and n > 1):
                 raise ValueError("the prefix's rows must be adjacent, K and V with the same strides")
-            a.prefix_k, a.prefix_v, a.prefix_stride_b, a.prefix_stride_h = k.data_ptr(), v.data_ptr(), sb, sh
-            a.n_prefix, a.prefix_batch = k.shape[2], k.shape[0]
-        a.n_kv_heads = k.shape[1]
-    if a.n_kv_heads == 0:
+            pk, pv = k.data_ptr(), v.data_ptr()
+    if hkv == 0:
         raise ValueError("neither a prefix nor pages: nothing to attend to")
-    with _on(device) as stream:
-        a.stream = stream
-        bytes_ = binding.evict_shared_attention_workspace(a)
-        # from torch's allocator: reused in stream order, private to a graph that is being captured
-        ws = torch.empty(bytes_, dtype=torch.uint8, device=device)
-        a.workspace, a.workspace_bytes = ws.data_ptr(), bytes_
-        binding.evict_shared_attention(a)
+    lse_at = _like(lse, "lse", (batch, hq, m), _torch.float32, index)
+    new_at = _like(n_new, "n_new", (batch,), _torch.int32, index)
+    head = (batch, m, hq, hkv, *qr, *outr, lse_at, scale, pk, pv, sb, sh, n, groups, pages_at, new_at)
+    key = (index, batch, m, hq, hkv, n, groups, width, page)
+    size = _workspace.get(key)
+    if size is None:
+        size = _workspace_bytes(key, _ATTENTION.pack(*head, 0, 0, 0, 0))
+    # from torch's allocator: reused in stream order, private to a graph that is being captured
+    work = _torch.empty(size, dtype=_torch.uint8, device=q.device)
+    _call(index, _calls.evict_shared_attention, _ATTENTION.pack(*head, work.data_ptr(), size, error, _stream(index)))
     return out
 
 
@@ -246,7 +300,9 @@ class PagedCache:
     def __init__(self, n_pages: int | None = None, page_size: int | None = None, n_kv_heads: int | None = None,
                  batch: int | None = None, max_rows: int | None = None, dtype: str = "bf16", device=None,
                  k_pages=None, v_pages=None, table=None, lens=None):
-        torch = _torch()
+        if _torch is None:
+            _load()
+        torch = _torch
         given = [x is not None for x in (k_pages, v_pages, table, lens)]
         if any(given) and not all(given):
             raise ValueError("k_pages, v_pages, table and lens go together")
@@ -264,7 +320,9 @@ class PagedCache:
             lens = torch.zeros(batch, dtype=torch.int32, device=device)
             self._free = list(range(n_pages - 1, -1, -1))
             self._rows, self._pages = [0] * batch, [[] for _ in range(batch)]
-        self.device = _same_device(k_pages, v_pages, table, lens)
+        self.index, self.device = _device(k_pages), k_pages.device
+        if v_pages.device != self.device or table.device != self.device:
+            raise ValueError("pages, table and lens must be on one device")
         if k_pages.dim() != 4 or k_pages.shape[3] != HEAD_DIM or v_pages.shape != k_pages.shape or \
                 v_pages.dtype != k_pages.dtype or v_pages.stride() != k_pages.stride():
             raise ValueError(f"pages must be two tensors [n_pages, n_kv_heads, page_size, {HEAD_DIM}] alike")
@@ -274,14 +332,15 @@ class PagedCache:
             raise ValueError("the rows of a page must be dense")
         if table.dim() != 2 or table.dtype != torch.int32 or table.stride(1) != 1:
             raise ValueError("table must be int32 [batch, width] with adjacent entries")
-        self.batch = table.shape[0]
-        _like(lens, "lens", (self.batch,), torch.int32, self.device)
+        self.batch, self.width = table.shape
+        _like(lens, "lens", (self.batch,), torch.int32, self.index)
         self.k_pages, self.v_pages, self.table, self.lens = k_pages, v_pages, table, lens
         self.error = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.struct = EvictPages(k=k_pages.data_ptr(), v=v_pages.data_ptr(), page_stride=sp, n_pages=self.n_pages,
-                                 page_size=self.page_size, n_kv_heads=self.n_kv_heads, dtype=_dtype(k_pages),
+                                 page_size=self.page_size, n_kv_heads=self.n_kv_heads, dtype=_dtype(k_pages.dtype),
                                  table=table.data_ptr(), table_stride=table.stride(0), table_width=table.shape[1],
                                  lens=lens.data_ptr(), error=self.error.data_ptr())
+        self.address, self.error_at = ctypes.addressof(self.struct), self.error.data_ptr()
 
     # --- pages ------------------------------------------------------------------------------
     def _managed(self):
@@ -290,8 +349,8 @@ class PagedCache:
 
     def _upload(self, rows):
         """Table rows and all lens to the device, in stream order."""
-        torch = _torch()
-        with _on(self.device):
+        torch = _torch
+        with _on(self.index):
             self.lens.copy_(torch.tensor(self._rows, dtype=torch.int32))
             for b in rows:
                 if self._pages[b]:
@@ -334,25 +393,21 @@ class PagedCache:
         index in the sequence; values are copied. q [batch, n_q_heads, m, 128] is rotated alike
         in the same launch, into q_out (q itself: in place; None: a new tensor). Returns q_out.
         """
-        torch = _torch()
-        device = _same_device(self.k_pages, k, v, q, q_out)
-        batch, m = self.batch, k.shape[2] if k.dim() == 4 else 0
-        if k.dtype != self.k_pages.dtype or v.dtype != k.dtype:
-            raise ValueError(f"k and v must be {self.k_pages.dtype}, as the pages")
-        kr, vr = _rows(k, "k", batch, m), _rows(v, "v", batch, m)
+        index, dtype, batch = self.index, self.k_pages.dtype, self.batch
+        shape = k.shape
+        m = shape[2] if len(shape) == 4 else -1
+        kr, vr = _ROWS.pack(*_rows(k, "k", index, dtype, batch, m)), _ROWS.pack(*_rows(v, "v", index, dtype, batch, m))
         qr = qo = None
         if q is not None:
             if q_out is None:
-                q_out = (torch.empty if n_new is None else torch.zeros)(q.shape, dtype=q.dtype, device=device)
-            if q.dtype != k.dtype or q_out.dtype != k.dtype or q_out.shape != q.shape:
-                raise ValueError("q and q_out must have one shape and the pages' dtype")
-            qr, qo = _rows(q, "q", batch, m), _rows(q_out, "q_out", batch, m)
+                q_out = _torch.empty_like(q) if n_new is None else _torch.zeros_like(q)
+            qr = _ROWS.pack(*_rows(q, "q", index, dtype, batch, m))
+            qo = _ROWS.pack(*_rows(q_out, "q_out", index, dtype, batch, m, q.shape[1]))
         elif q_out is not None:
             raise ValueError("q_out without q")
-        with _on(device) as stream:
-            binding.evict_paged_append(self.struct, batch, m, _like(n_new, "n_new", (batch,), torch.int32, device),
-                                       rotary.handle if rotary is not None else None,
-                                       _pos(pos, rotary, batch, m, device), pos_base, kr, vr, qr, qo, stream)
+        _call(index, _calls.evict_paged_append, self.address, batch, m, _like(n_new, "n_new", (batch,), _torch.int32, index) or None,
+              rotary.handle if rotary is not None else None, _pos(pos, rotary, batch, m, index), pos_base, kr, vr, qr, qo,
+              _stream(index))
         return q_out
 
     def attend(self, q, prefix=None, n_new=None, scale=None, out=None, lse=None):
@@ -362,5 +417,5 @@ class PagedCache:
     def sync(self):
         """Synchronise the current stream; raises EvictError(EVICT_EDEVICE) if a call's kernel has
         reported an error (a table entry outside the pool, rows outside the table) since the last."""
-        with _on(self.device) as stream:
-            binding.evict_pages_status(self.error.data_ptr(), stream)
+        with _on(self.index):
+            binding.evict_pages_status(self.error_at, _stream(self.index))
