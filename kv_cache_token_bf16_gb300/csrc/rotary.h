@@ -8,8 +8,8 @@
 namespace evict {
 
 struct RotaryTable {
-  uint64_t freq[EVICT_HEAD_DIM / 2];   // turns per position, as a fraction of 2^64
-  uint8_t axis[EVICT_HEAD_DIM / 2];
+  alignas(16) uint64_t freq[EVICT_HEAD_DIM / 2];   // turns per position, as a fraction of 2^64
+  alignas(8) uint8_t axis[EVICT_HEAD_DIM / 2];
   int half;                            // pairs that turn
   int adjacent;
   int n_axes;

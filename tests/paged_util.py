@@ -36,10 +36,12 @@ def rotate64(x, pos, freq, axis, pairs="half", transpose=False, scale=1.0):
 
 
 def rotate_bound(x, ref, rotary_dim, pairs, dtype, scale=1.0):
-    """|error| of a rotated element. The angle in half turns is truncated to 2^-31 and rounded to
+    """|error| of a rotated element. fp32: the angle in half turns is truncated to 2^-31 and rounded to
     fp32 (2^-25): pi * (2^-31 + 2^-25) < 1.6 U32 of an angle; sincospif is within one step (2 U32 of
     1); scaling it, two products and a sum round once each (4 U32). Under 8 U32 of |x| + |y|, and
-    the output's rounding."""
+    the output's rounding. bf16: the angle of up to pi rounds twice (2 pi U32 < 6.3 U32) and __sinf and
+    __cosf are within 2^-21.19 < 7.1 U32 on [-pi, pi], with the other 4 under 18 U32."""
+    units = 8 if dtype is torch.float32 else 18
     a = x.double().cpu().abs()
     t = torch.zeros_like(a)
     r = rotary_dim
@@ -47,7 +49,7 @@ def rotate_bound(x, ref, rotary_dim, pairs, dtype, scale=1.0):
         t[..., :r // 2] = t[..., r // 2:r] = a[..., :r // 2] + a[..., r // 2:r]
     else:
         t[..., 0:r:2] = t[..., 1:r:2] = a[..., 0:r:2] + a[..., 1:r:2]
-    return 8 * U32 * abs(scale) * t + HALF[dtype] * ref.abs() + 1e-38
+    return units * U32 * abs(scale) * t + HALF[dtype] * ref.abs() + 1e-38
 
 
 def attend64(q, prefix, own, n_new=None, scale=None):
