@@ -15,9 +15,9 @@
 // step; a smaller one gives both the same rows and every other step each (two
 // partial results).
 //
-// The exponent's reference is a row's maximum over the first 64 columns that it
+// The exponent's reference is a row's maximum over the first 32 columns that it
 // sees, and stays there: later columns are taken against it without a maximum
-// of their own while the sum of 64 of their weights is below 2^12, and it moves
+// of their own while the sum of 32 of their weights is below 2^12, and it moves
 // to the running maximum (with a read and write of O in tensor memory) where
 // that is passed. Weights, sums and O are relative to it and floating, so the
 // result does not depend on where it stands. Weights enter the product
@@ -42,7 +42,7 @@ constexpr int kWideSmem = (2 + kRing) * kTileBytes;
 constexpr int kMmaWarp = 8, kTmaWarp = 10;
 constexpr int kBadWords = 9;                      // 257 tokens and more
 constexpr int kBadSets = 16;                      // segments in flight, by far
-constexpr float kMoveAbove = 4096.f;              // sum of 64 weights that makes the reference move
+constexpr float kMoveAbove = 4096.f;              // sum of 32 weights that makes the reference move
 
 struct WideShared {
   uint64_t kv_full[kRing], kv_empty[kRing];
@@ -291,24 +291,15 @@ __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, 
 // 32 columns of this thread's row. The load runs on; nothing may use the registers before wait32,
 // which has them as operands to that end.
 __device__ __forceinline__ void load32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr) : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void wait32(float* v) {
+__device__ __forceinline__ void wait32(float (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
                :: "memory");
-}
-__device__ __forceinline__ void store32(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
 }
 __device__ __forceinline__ void store16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
@@ -555,62 +546,55 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
       const int own0 = (c.step + i - g.pre_steps) * kWideTokens;
       const int seen = own0 < 0 ? c.k.pre - 1 - (c.step + i) * kWideTokens : limit - own0;   // columns 0 .. seen
       const bool masked = __any_sync(0xffffffffu, seen < kTile - 1);
-      // 64 columns at a time, in two loads of 32: each is on its way while the one before is at work
+      // 32 columns at a time; the next ones are on their way while these are at work
       float x[2][32];
       load32(s_at, x[0]);
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
+      auto chunk = [&](int ch, float(&y)[32], float(&next)[32], bool last) {
+        wait32(y);
+        if (!last) load32(s_at + 32 * (ch + 1), next);
+        if (masked) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (32 * ch + k > seen) y[k] = -INFINITY;
+        }
         const uint64_t sc2 = pack_f32x2(scale, scale);
-        float nb = -base_of(ref);
-        uint32_t pk[32];
+        uint32_t pk[16];
         float got;
-        // weights of the columns against the reference, packed, and their sum
-        auto weights = [&](int k0) {
+#pragma unroll 1
+        for (bool again = false;; again = true) {
+          // weights against the reference, packed, and their sum
+          const float nb = -base_of(ref);
           const uint64_t nb2 = pack_f32x2(nb, nb);
           uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
-            const uint64_t e = ex2_f32x2(fma_f32x2(pack_f32x2(x[k0][k], x[k0][k + 1]), sc2, nb2));
+            const uint64_t e = ex2_f32x2(fma_f32x2(pack_f32x2(y[k], y[k + 1]), sc2, nb2));
             acc[(k >> 1) & 1] = add_f32x2(acc[(k >> 1) & 1], e);
-            float a, b;
-            split_f32x2(e, a, b);
-            pk[16 * k0 + (k >> 1)] = pack_bf16(a, b);
+            float e0, e1;
+            split_f32x2(e, e0, e1);
+            pk[k >> 1] = pack_bf16(e0, e1);
           }
           float a0, a1;
           split_f32x2(add_f32x2(acc[0], acc[1]), a0, a1);
-          return a0 + a1;
-        };
-        auto hide = [&](int k0) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (64 * half + 32 * k0 + k > seen) x[k0][k] = -INFINITY;
-        };
-        wait32(x[0]);
-        load32(s_at + 64 * half + 32, x[1]);
-        if (masked) hide(0);
-#pragma unroll 1
-        for (bool again = false;; again = true) {
-          got = weights(0);
-          if (!again) {
-            wait32(x[1]);
-            if (masked) hide(1);
-          }
-          got += weights(1);
+          got = a0 + a1;
           // no reference yet, or a sum that says that it has fallen far behind the maximum (NaN as well)
           if (again || !__any_sync(0xffffffffu, ref == -INFINITY || !(got < kMoveAbove))) break;
+          if (!last) wait32(next);                // no call while a load is on its way to registers
           float top = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) top = fmax3(top, x[0][k], x[1][k]);
+          for (int k = 0; k < 32; k += 2) top = fmax3(top, y[k], y[k + 1]);
           const float to = fmaxf(ref, top * scale), f = weight_of(ref, to);
           ref = to;
           sum *= f;
-          move_reference(s_at, 32 * half, begun ? o_at : 0, f);
-          nb = -base_of(ref);
+          move_reference(s_at, 16 * ch, begun ? o_at : 0, f);
         }
         sum += got;
-        // over columns that are in registers by now: half 0 over 0 .. 31, half 1 over 32 .. 63
-        store32(s_at + 32 * half, pk);
-        if (half == 0) load32(s_at + 64, x[0]);
+        store16(s_at + 16 * ch, pk);              // over columns that are in registers by now
+      };
+#pragma unroll 1
+      for (int ch = 0; ch < kTile / 32; ch += 2) {
+        chunk(ch, x[0], x[1], false);
+        chunk(ch + 1, x[1], x[0], ch + 2 == kTile / 32);
       }
       begun = true;
       if (own0 >= 0 && (own0 + kTile - 1 > c.k.reach || own0 + kTile > first)) {
