@@ -35,7 +35,7 @@
 namespace evict {
 namespace {
 
-constexpr int kTile = 128;
+constexpr int kTile = 128, kHalf = 64;
 constexpr int kTileBytes = kTile * kHeadDim * 2;
 constexpr int kRing = 5;
 constexpr int kWideSmem = (2 + kRing) * kTileBytes;
@@ -46,9 +46,9 @@ constexpr float kMoveAbove = 4096.f;              // sum of 32 weights that make
 
 struct WideShared {
   uint64_t kv_full[kRing], kv_empty[kRing];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done[2];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2], done[2];   // group, half of the step
   uint32_t tmem_base;
-  int fail, turn;
+  int fail;
   uint32_t bad[kBadSets][kBadWords];              // of the segments in turn: rows of V that were blanked
 };
 
@@ -152,33 +152,24 @@ struct Watch {
     return false;
   }
 };
-// The lock of the MMA warps' turns.
-__device__ __forceinline__ bool take_turn(WideShared& sh, int* err) {
-  Watch watch;
-  while (atomicCAS(&sh.turn, 0, 1) != 0)
-    if (!watch.go_on(sh, err)) return false;
-  return true;
-}
-__device__ __forceinline__ void end_turn(WideShared& sh) { atomicExch(&sh.turn, 0); }
-
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return (uint64_t)lo | ((uint64_t)hi << 32); }
 
-// S = Q K^T, both K-major; q and k: the tiles' descriptors' low words (their steps differ in the
-// start address alone, which does not carry over).
+// Half a step's S = Q K^T, both K-major; q and k: the tiles' descriptors' low words (their steps
+// differ in the start address alone, which does not carry over).
 __device__ __forceinline__ void issue_qk(uint32_t d, uint32_t q, uint32_t k, uint32_t hi) {
-  constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile);
+  constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, kHalf);
 #pragma unroll
   for (int s = 0; s < 8; ++s) {
     const uint32_t off = (uint32_t)((s >> 2) * kTile * 128 + (s & 3) * 32) >> 4;
     tc::mma_bf16(d, desc_of(q + off, hi), desc_of(k + off, hi), idesc, s > 0 ? 1u : 0u);
   }
 }
-// O (+)= P V: P in tensor memory (two weights a column), V with its rows as the product's
-// depth (MN-major). 16 rows of V are 2048 bytes of each half.
+// O (+)= P V of half a step: P in tensor memory (two weights a column), V with its rows as the
+// product's depth (MN-major). 16 rows of V are 2048 bytes of each half of its columns.
 __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pt, uint32_t v, uint32_t hi, bool accumulate) {
   constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile) | (1u << 16);
 #pragma unroll
-  for (int s = 0; s < 8; ++s) {
+  for (int s = 0; s < kHalf / 16; ++s) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
@@ -188,11 +179,9 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pt, uint32_t v, ui
   }
 }
 
-// The MMAs of group w, issued by one warp of its own: the product with V of a job and S = Q K^T of
-// the group's next one right behind it (S goes where the weights lay, and MMAs run in order). Where
-// both groups work on every step they take turns at this pair, under a lock: the tensor cores then
-// finish one group's pair and that group exponentiates while they work on the other's; issued side
-// by side, both pairs would end together and the tensor cores wait for both groups.
+// The MMAs of group w, issued by one warp of its own. S of half step j + 2 goes where the weights of
+// half step j lay: behind their product with V, MMAs run in order. What is there first is done first:
+// the next K, the weights of the next product, the other group's tiles (let go of).
 __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, int count, int w, uint32_t tmem,
                            uint32_t qbuf, uint32_t ring) {
   const WorkSet& set = p.wide;
@@ -213,69 +202,57 @@ __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, 
   };
   while (ok && count > 0) {
     const Segment g(p, c, count);
-    const int jobs = g.jobs(w);
-    Slot v;
-    int at = 0;                                   // steps passed
+    const int n = 2 * g.jobs(w);                  // half steps
+    if (n > 0) {
+      if (!wait(&sh.q_full[w], q_parity)) break;
+      q_parity ^= 1;
+    }
+    Slot v, v_next;                               // V of the product's step, of the last S's
+    int jq = 0, jp = 0;                           // half steps whose S, whose product were issued
+    int pass = g.alt && w == 1 && n > 0 ? 2 : 0;  // tiles of the other group before the next K
+    int at = pass / 2;                            // steps passed
+    Watch watch;
 #pragma unroll 1
-    for (int j = 0; j <= jobs && jobs > 0; ++j) {
-      if (j == 0) {
-        if (!wait(&sh.q_full[w], q_parity)) break;
-        q_parity ^= 1;
-      }
-      // What is there first is done first: the weights of the last job (its product with V frees V),
-      // the other group's tiles (let go of), the next K. With both groups on every step the product
-      // and the next S go together, under the lock.
-      bool pv = j > 0, next = j < jobs;
-      int pass = g.alt && next && (j > 0 || w == 1) ? 2 : 0;
-      at += pass / 2;
-      bool locked = false;
-      Watch watch;
-#pragma unroll 1
-      while (pv || next) {
-        if (pass > 0 && tc::mbar_try_wait(&sh.kv_full[slot.i], slot.parity)) {
+    while (jp < n) {
+      if (pass > 0) {
+        if (tc::mbar_try_wait(&sh.kv_full[slot.i], slot.parity)) {
           tc::mbar_arrive(&sh.kv_empty[slot.i]);
           slot.next();
           --pass;
-          continue;
         }
-        const bool k_there = next && pass == 0 && tc::mbar_try_wait(&sh.kv_full[slot.i], slot.parity);
-        if (pv && (k_there || !next || !g.two) && tc::mbar_try_wait(&sh.kv_full[v.i], v.parity) &&
-            tc::mbar_try_wait(&sh.p_full[w], p_parity)) {
-          p_parity ^= 1;
-          pv = false;
-          if (g.two && !(locked = take_turn(sh, p.err))) {
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
-          issue_pv(o_at, s_at, v_lo + v.i * (kTileBytes >> 4), v_hi, j > 1);
-          if (!next) {
-            if (locked) end_turn(sh);
-            tc::mma_commit(&sh.o_full[w]);
-          }
-          if (!next || !g.two) tc::mma_commit(&sh.kv_empty[v.i]);
-        }
-        if (!pv && k_there) {
-          if (g.two && !locked && !take_turn(sh, p.err)) {
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
-          issue_qk(s_at, q_lo, k_lo + slot.i * (kTileBytes >> 4), qk_hi);
-          tc::mma_commit(&sh.s_full[w]);
-          if (g.two) end_turn(sh);
-          if (g.two && j > 0) tc::mma_commit(&sh.kv_empty[v.i]);
+      } else if (jq < n && jq < jp + 2 && tc::mbar_try_wait(&sh.kv_full[slot.i], slot.parity)) {
+        const int h = jq & 1;
+        tc::fence_after_sync();
+        issue_qk(s_at + h * kHalf, q_lo, k_lo + ((slot.i * kTileBytes + h * (kHalf * 128)) >> 4), qk_hi);
+        tc::mma_commit(&sh.s_full[w][h]);
+        if (h == 0) {
+          v_next = slot;
+          v_next.next();
+        } else {
           tc::mma_commit(&sh.kv_empty[slot.i]);
-          next = false;
+          slot.next();
+          slot.next();
           ++at;
-          slot.next();
-          v = slot;
-          slot.next();
-          break;
+          if (g.alt && jq + 1 < n) pass = 2, ++at;
         }
-        if ((pv || next) && !(ok = watch.go_on(sh, p.err))) break;
+        ++jq;
       }
-      if (!ok) break;
+      if (jp < jq) {
+        const int h = jp & 1;
+        if (h == 0) v = v_next;
+        if (tc::mbar_try_wait(&sh.p_full[w][h], p_parity) && tc::mbar_try_wait(&sh.kv_full[v.i], v.parity)) {
+          tc::fence_after_sync();
+          issue_pv(o_at, s_at + h * kHalf, v_lo + ((v.i * kTileBytes + h * (kHalf * 128)) >> 4), v_hi, jp > 0);
+          tc::mma_commit(&sh.o_full[w][h]);
+          if (h) {
+            tc::mma_commit(&sh.kv_empty[v.i]);
+            p_parity ^= 1;
+          }
+          ++jp;
+          watch = Watch();
+        }
+      }
+      if (!(ok = watch.go_on(sh, p.err))) break;
     }
     if (ok) release(2 * (g.steps - at));
     count -= g.steps;
@@ -378,7 +355,8 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
       *reinterpret_cast<uint4*>(to + 2 * i * 128 + (((chunk & 7) ^ ((2 * i + half) & 7)) << 4)) = x[i];
     }
     tc::fence_proxy_async_smem();
-    tc::mbar_arrive(&sh.q_full[w]);
+    __syncwarp();
+    if ((row & 31) == 0) tc::mbar_arrive(&sh.q_full[w]);
     return q;
   };
 
@@ -413,8 +391,20 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
     }
   };
 
-  uint32_t s_parity = 0, o_parity = 0;
+  uint32_t s_parity = 0;                          // of the step at hand
   bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool there = wait_phase(bar, parity, &sh.fail, p.err);
+    ok = __all_sync(0xffffffffu, there) && ok;
+    tc::fence_after_sync();
+    return ok;
+  };
+  // The products with V before half h of this step. (Two are in flight at most: one barrier for both could be
+  // a phase further than the one that is waited for.)
+  auto wait_products = [&](int h) {
+    wait(&sh.o_full[w][0], h == 0 ? s_parity ^ 1 : s_parity);
+    wait(&sh.o_full[w][1], s_parity ^ 1);
+  };
   Segment g(p, c, count);
   QueryRow q = {};
   int limit = -1;                                 // last own row that this query sees
@@ -440,13 +430,8 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
     }
     if (segment >= 0) {
       const int jobs = part.jobs(w);
-      if (jobs > 0) {
-        ok = wait_phase(&sh.o_full[w], o_parity, &sh.fail, p.err);
-        ok = __all_sync(0xffffffffu, ok);
-        o_parity ^= 1;
-      }
+      if (jobs > 0) wait_products(0);
       if (!ok) break;
-      tc::fence_after_sync();
       const bool whole = set.joint && part.steps == at.k.steps;     // no other part, no other unit for these rows
       const bool write = mine.real && (part.two || part.alt || w == 0);
       const size_t prow = (size_t)(at.unit + blockIdx.x) * kWideRows + w * kTile + row;
@@ -538,24 +523,18 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
       const uint32_t v_parity = slot.parity;
       slot.next();
       if (!g.has(w, i)) continue;
-      ok = wait_phase(&sh.s_full[w], s_parity, &sh.fail, p.err);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      s_parity ^= 1;
-      tc::fence_after_sync();
       const int own0 = (c.step + i - g.pre_steps) * kWideTokens;
       const int seen = own0 < 0 ? c.k.pre - 1 - (c.step + i) * kWideTokens : limit - own0;   // columns 0 .. seen
       const bool masked = __any_sync(0xffffffffu, seen < kTile - 1);
-      // 32 columns at a time; the next ones are on their way while these are at work
+      // 32 columns at a time; the next ones of the half step are on their way while these are at work
       float x[2][32];
-      load32(s_at, x[0]);
-      auto chunk = [&](int ch, float(&y)[32], float(&next)[32], bool last) {
+      auto chunk = [&](uint32_t at, int ch, int from, float(&y)[32], float(&next)[32]) {
         wait32(y);
-        if (!last) load32(s_at + 32 * (ch + 1), next);
+        if (ch == 0) load32(at + 32, next);
         if (masked) {
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            if (32 * ch + k > seen) y[k] = -INFINITY;
+            if (from + k > seen) y[k] = -INFINITY;
         }
         const uint64_t sc2 = pack_f32x2(scale, scale);
         uint32_t pk[16];
@@ -579,34 +558,40 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
           got = a0 + a1;
           // no reference yet, or a sum that says that it has fallen far behind the maximum (NaN as well)
           if (again || !__any_sync(0xffffffffu, ref == -INFINITY || !(got < kMoveAbove))) break;
-          if (!last) wait32(next);                // no call while a load is on its way to registers
+          if (ch == 0) wait32(next);              // no call while a load is on its way to registers
           float top = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 32; k += 2) top = fmax3(top, y[k], y[k + 1]);
           const float to = fmaxf(ref, top * scale), f = weight_of(ref, to);
           ref = to;
           sum *= f;
-          move_reference(s_at, 16 * ch, begun ? o_at : 0, f);
+          // O follows once the products before this half step are through
+          if (begun) wait_products(from / kHalf);
+          move_reference(at, 16 * ch, begun ? o_at : 0, f);
         }
         sum += got;
-        store16(s_at + 16 * ch, pk);              // over columns that are in registers by now
+        store16(at + 16 * ch, pk);                // over columns that are in registers by now
       };
 #pragma unroll 1
-      for (int ch = 0; ch < kTile / 32; ch += 2) {
-        chunk(ch, x[0], x[1], false);
-        chunk(ch + 1, x[1], x[0], ch + 2 == kTile / 32);
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t at = s_at + h * kHalf;
+        if (!wait(&sh.s_full[w][h], s_parity)) break;
+        load32(at, x[0]);
+        chunk(at, 0, h * kHalf, x[0], x[1]);
+        chunk(at, 1, h * kHalf + 32, x[1], x[0]);
+        if (h == 0 && own0 >= 0 && (own0 + kTile - 1 > c.k.reach || own0 + kTile > first)) {
+          if (!wait(&sh.kv_full[v_slot], v_parity)) break;
+          blank_rows(v_slot, own0, first, bad);
+          marks = marks || own0 + kTile > first;
+        }
+        wait_stores();
+        tc::fence_before_sync();
+        __syncwarp();
+        if ((row & 31) == 0) tc::mbar_arrive(&sh.p_full[w][h]);   // a warp's 32 arrivals would go one by one
+        begun = true;
       }
-      begun = true;
-      if (own0 >= 0 && (own0 + kTile - 1 > c.k.reach || own0 + kTile > first)) {
-        ok = wait_phase(&sh.kv_full[v_slot], v_parity, &sh.fail, p.err);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        blank_rows(v_slot, own0, first, bad);
-        marks = marks || own0 + kTile > first;
-      }
-      wait_stores();
-      tc::fence_before_sync();
-      tc::mbar_arrive(&sh.p_full[w]);
+      if (!ok) break;
+      s_parity ^= 1;
     }
     if (!ok) break;
   }
@@ -621,15 +606,17 @@ __device__ __forceinline__ void wide_setup(WideShared& sh) {
     tc::mbar_init(&sh.kv_empty[lane], 2);         // both groups' MMA warps
   }
   if (warp == 2 && lane < 2) {
-    tc::mbar_init(&sh.q_full[lane], kTile);
-    tc::mbar_init(&sh.s_full[lane], 1);
-    tc::mbar_init(&sh.p_full[lane], kTile);
-    tc::mbar_init(&sh.o_full[lane], 1);
+    tc::mbar_init(&sh.q_full[lane], kTile / 32);
+    for (int h = 0; h < 2; ++h) {
+      tc::mbar_init(&sh.s_full[lane][h], 1);
+      tc::mbar_init(&sh.p_full[lane][h], kTile / 32);
+      tc::mbar_init(&sh.o_full[lane][h], 1);
+    }
     tc::mbar_init(&sh.done[lane], 1);
   }
   if (warp > 3) {
     for (int i = tid - 128; i < kBadSets * kBadWords; i += blockDim.x - 128) (&sh.bad[0][0])[i] = 0;
-    if (tid == 128) sh.fail = sh.turn = 0;
+    if (tid == 128) sh.fail = 0;
   }
 }
 __device__ __forceinline__ void wide_teardown(const WideShared& sh) {
