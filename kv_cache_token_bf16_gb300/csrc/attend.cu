@@ -254,8 +254,10 @@ constexpr size_t kWorkHead = 256;                 // an error word, for callers 
 constexpr int kFewMinBoxes = 2;
 constexpr int kWideMinSteps = 3;
 // Clocks of an SM, side by side, for a box of 16 rows, and for a step of 128 rows with two groups of
-// query rows at it, or with the groups taking turns.
-constexpr int kFewCost = 262, kWideCostTwo = 4600, kWideCostAlt = 2800;
+// query rows at it, or with the groups taking turns. Fitted to when the two kinds end: with 262, 4600
+// and 2800 the wide CTAs of 128 sequences behind 16,384 rows ended 10 of 73 us before the others, and
+// 32 sequences' draft tokens behind 8,192 rows took 52 us instead of 47.
+constexpr int kFewCost = 300, kWideCostTwo = 4000, kWideCostAlt = 2600;
 // What a unit's start costs beside: a warp or CTA fetches its queries and leaves the last unit's results.
 constexpr int kFewEntry = 2, kWideEntry = 3;
 
