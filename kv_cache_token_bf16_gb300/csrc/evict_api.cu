@@ -565,7 +565,13 @@ int evict_sync(evict_handle* h) {
 
 void evict_destroy(evict_handle* h) {
   if (!h) return;
-  cudaStreamSynchronize(h->stream);
+  // A garbage collector may call this while any stream captures a graph: waiting and freeing would end
+  // the capture with an error unless this thread says that they are no part of it.
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(h->stream, &capturing) == cudaSuccess && capturing == cudaStreamCaptureStatusNone)
+    cudaStreamSynchronize(h->stream);
   for (auto& r : h->pending) {
     cudaEventDestroy(r.start);
     cudaEventDestroy(r.stop);
@@ -579,6 +585,7 @@ void evict_destroy(evict_handle* h) {
   }
   cudaFree(h->arena);
   curdkv_release(h);
+  cudaThreadExchangeStreamCaptureMode(&mode);
   delete h;
 }
 
