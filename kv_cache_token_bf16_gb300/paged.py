@@ -55,7 +55,8 @@ def _load():
                        ("evict_shared_attention", [packed])):
         fn = getattr(calls, name)
         fn.restype, fn.argtypes = i, args
-    _torch, _calls = torch, calls
+    _calls = calls                               # before _torch, which other threads take as the sign
+    _torch = torch
 
 
 def _dtype(t):

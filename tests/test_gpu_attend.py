@@ -142,6 +142,17 @@ def test_rising_logits(hq):
     check(s, *attend(s))
 
 
+@pytest.mark.parametrize("hq,m", [(8, 1), (40, 1), (100, 2), (260, 1), (400, 2)])
+def test_spikes_anywhere(hq, m):
+    # a maximum that jumps at some columns, for some rows: in any part of a step, first or last
+    s = make(124, 4, hq, 2, m, 1500, 1, 16, [m, 100, 300, 17])
+    k = s["prefix"][0]
+    g = torch.Generator().manual_seed(125)
+    for j in [31, 32, 63, 64, 127, 128, 191, 192, 1472, 1499] + torch.randint(0, 1500, (24,), generator=g).tolist():
+        k[:, :, j] *= 20
+    check(s, *attend(s))
+
+
 @pytest.mark.parametrize("hq", [8, 100, 260], ids=["few", "wide", "joint"])
 def test_results_are_the_same_every_time(hq):
     s = make(123, 7, hq, 2, 3, 3000, 1, 16, [3 + 100 * b for b in range(7)])
@@ -207,6 +218,30 @@ def test_empty_everything():
     out = paged.shared_attention(q, prefix=(k, k), out=torch.full_like(q, 5.0), lse=lse)
     assert not bool(out.any())
     assert paged.shared_attention(q[:, :, :0], prefix=(k, k)).shape == (2, 4, 0, D)
+
+
+@pytest.mark.parametrize("hq", [4, 40, 400], ids=["few", "wide", "joint"])
+def test_only_padding(hq):
+    s = make(144, 3, hq, 2, 4, 200, 1, 16, [0, 3, 70], [0, 0, 0])
+    out, lse = attend(s, out=torch.full_like(s["q"], 5.0))
+    assert bool((out == 5).all()) and bool((lse == 7).all())
+
+
+def test_the_largest_batch():
+    n = 4096
+    s = make(145, n, 4, 2, 2, 130, 4, 16, [b * 7 % 41 for b in range(n)], [min(2, b * 7 % 41) for b in range(n)])
+    out, lse = attend(s, out=torch.zeros_like(s["q"]))
+    # the definition for some of them, each group's first and last among them
+    at = [0, 1, 1023, 1024, 2047, 2048, 3000, 3071, 4095]
+    few = dict(q=s["q"][at], new=s["new"][at], own=[s["own"][b] for b in at], prefix=None)
+    for i, b in enumerate(at):
+        one = dict(q=few["q"][i:i + 1], new=few["new"][i:i + 1], own=[few["own"][i]],
+                   prefix=tuple(x[b // 1024][None] for x in s["prefix"]))
+        check(one, out[b:b + 1], lse[b:b + 1])
+    with pytest.raises(binding.EvictError, match="4096") as e:
+        paged.shared_attention(torch.zeros(n + 1, 4, 1, D, dtype=torch.bfloat16, device="cuda"),
+                               prefix=tuple(x[:1] for x in s["prefix"]))
+    assert e.value.code == binding.EVICT_ELIMIT
 
 
 def test_bad_tables_and_lengths_are_reported():
@@ -295,6 +330,30 @@ def test_two_streams_and_two_graphs_at_once(m):
                 g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_two_host_threads():
+    import threading
+    cases = [make(152 + i, 8, 8, 2, m, 600, 1, 16, [m + 9 * b for b in range(8)]) for i, m in enumerate((1, 40))]
+    want = [attend(s)[0].clone() for s in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(50):
+                out = cases[i]["cache"].attend(cases[i]["q"], prefix=cases[i]["prefix"])
+            st.synchronize()
+            if not torch.equal(out, want[i]):
+                bad.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
 
 
 def test_a_captured_step_follows_the_lengths():
