@@ -214,8 +214,24 @@ bool encode_boxes(CUtensorMap* tm, const void* base, int rows, int heads, long l
 
 bool multiple(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// Query rows from which the wide kernel takes a unit, and above which a sequence fills one.
-constexpr int kWideFrom = kRows + 1, kOwnWideFrom = 2 * kRows + 1, kJointFrom = 128;
+// Which kernel takes which units. Times are of whole calls with 32 query and 8 KV heads.
+//
+// A prefix is the few-row kernel's where its queries fill at most two tiles of 16 rows and reading it
+// for each tile is little work: then the start counts, and the wide kernel's is longer. One tile (16
+// rows) over 1,024 / 2,048 / 4,096 / 16,384 rows: 15.1 / 16.9 / 20.7 / 33.0 us, wide 16.1 / 16.9 /
+// 17.3 / 25.4; two tiles (32 rows) over 512 / 1,024 / 2,048: 14.4 / 15.9 / 18.3, wide 16.3 / 16.4 / 17.1.
+constexpr int kFewTiles = 2, kFewPrefix = 2048;
+// Own rows are the few-row kernel's up to two tiles: 32 sequences of 1,024 rows with 20 / 32 query
+// rows each 52 / 55 us, wide 50 / 53, but behind a shared prefix the SMs split between the kinds (the
+// 20 rows of five drafts each behind 8,192 rows: 47 us, wide 53). With 40 / 64 rows 67 / 95 us, wide
+// 54 / 57.
+constexpr int kOwnWideFrom = kFewTiles * kRows + 1;
+// Sequences of more query rows than these take the prefix along in units of their own (joint: no
+// partial results to merge) where the prefix is short or they fill tiles of 256 rows by three
+// quarters; otherwise the sequences' rows share the prefix's tiles. 16 sequences behind 1,024 rows,
+// 160 / 320 rows each: joint 46 / 74 us, else 50 / 101; behind 16,384 rows, 160 / 208 / 320 / 512
+// rows each: joint 223 / 229 / 423 / 431, else 180 / 250 / 346 / 601.
+constexpr int kJointFrom = 128, kJointPrefix = 2048;
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -249,8 +265,9 @@ void rebase(WorkSet& s, char* base) {
 }
 
 constexpr size_t kWorkHead = 256;                 // an error word, for callers without one
-// Boxes (steps) that a share has at least: fewer would leave more partial results to merge than rows
-// to read.
+// Boxes (steps) that a share has at least: fewer would leave more partial results to merge than rows to
+// read. A step of 4 sequences behind 1,024 rows 14.7 us with two boxes, 14.9 with one, 16.3 with four;
+// 16 sequences behind 2,048 rows 17.9 us with three steps, 20.3 with one and 20.7 with six.
 constexpr int kFewMinBoxes = 2;
 constexpr int kWideMinSteps = 3;
 // Clocks of an SM, side by side, for a box of 16 rows, and for a step of 128 rows with two groups of
@@ -259,6 +276,8 @@ constexpr int kWideMinSteps = 3;
 // 32 sequences' draft tokens behind 8,192 rows took 52 us instead of 47.
 constexpr int kFewCost = 300, kWideCostTwo = 4000, kWideCostAlt = 2600;
 // What a unit's start costs beside: a warp or CTA fetches its queries and leaves the last unit's results.
+// (Counted as nothing: 16 sequences behind 2,048 rows 20.2 us instead of 17.9, 256 new rows of each of
+// eight sequences 61.7 instead of 58.3.)
 constexpr int kFewEntry = 2, kWideEntry = 3;
 
 // Sizes alone decide: lens and n_new are the device's.
@@ -280,15 +299,15 @@ int make_plan(const evict_attention* a, Plan* out) {
   const int group = a->n_q_heads / a->n_kv_heads;
   const bool pre = a->n_prefix > 0;
 
-  // Which kernel takes a unit goes by its query rows, the wide one from kWideFrom on. Sequences of
-  // more than kJointFrom rows fill a wide unit by themselves: their units take the prefix along
-  // (no partial results to merge); below that, rows of several sequences share the prefix's units.
   const int own_rows = a->m * group, pre_rows = pre ? own_rows * (a->batch / a->prefix_batch) : 0;
-  if (own_rows > kJointFrom && (pre || a->pages)) {
+  const int wide_tiles = (own_rows + kWideRows - 1) / kWideRows, few_tiles = (pre_rows + kRows - 1) / kRows;
+  if (own_rows > kJointFrom && (pre || a->pages) &&
+      (a->n_prefix <= kJointPrefix || 4ll * own_rows > 3ll * kWideRows * wide_tiles)) {
     P.wide.joint = 1;
     P.wide.seqs = a->batch;
   } else {
-    if (pre) (pre_rows >= kWideFrom ? P.wide : P.few).prefixes = a->prefix_batch;
+    const bool few = few_tiles <= kFewTiles && (long long)few_tiles * a->n_prefix * a->prefix_batch <= kFewPrefix;
+    if (pre) (few ? P.few : P.wide).prefixes = a->prefix_batch;
     if (a->pages) (own_rows >= kOwnWideFrom ? P.wide : P.few).seqs = a->batch;
   }
   const long long seq_tokens = a->pages ? (long long)a->pages->table_width * a->pages->page_size : 0;
@@ -462,7 +481,8 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
     if (plan.sms > 1)
       e = launch_pdl(attend_join_split_kernel, dim3(plan.sms - 1, kWideRows / kJoinWarps), dim3(kJoinWarps * 32), 0, st, nullptr, P);
   } else {
-    // four warps a row while the rows are few
+    // four warps a row while the rows are few (4 sequences x 12 heads 14.7 us, with one 18.0; 48 x 32 heads
+    // 36.6 us with one, with four 41.1)
     const int rows = a->batch * a->n_q_heads * a->m, split = rows <= plan.sms * kJoinWarps ? 4 : 1;
     const dim3 grid((rows * split + kJoinWarps - 1) / kJoinWarps), block(kJoinWarps * 32);
     e = split == 4 ? launch_pdl(attend_join_kernel<4>, grid, block, 0, st, nullptr, P)

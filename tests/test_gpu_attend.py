@@ -105,6 +105,11 @@ CASES = [
     (32, 32, 8, 5, 2000, 1, 32, [5 + (b * 97) % 770 for b in range(32)], [(b * 7) % 6 for b in range(32)]),
     (24, 40, 8, 1, 650, 8, 16, [(b * 131) % 500 for b in range(24)], [(b * 5) % 2 for b in range(24)]),
     (5, 2, 1, 300, 1, 1, 16, None, [300, 0, 1, 129, 128]),
+    # long prefixes: few rows in the wide kernel, sequences of more than 128 rows in tiles that they share
+    (2, 8, 4, 1, 4200, 1, 16, [1, 40], None),
+    (3, 8, 2, 40, 2100, 1, 16, [40, 170, 300], None),
+    (3, 8, 2, 40, 2100, 1, 16, [40, 170, 300], [40, 33, 0]),
+    (4, 12, 2, 50, 2300, 2, 64, [50, 51, 260, 0], [50, 1, 50, 0]),
 ]
 
 
@@ -176,11 +181,11 @@ def test_kept_rows_of_a_cache():
     cache.close()
 
 
-@pytest.mark.parametrize("hq", [4, 40, 400], ids=["few", "wide", "joint"])
-def test_masked_rows_may_hold_anything(hq):
+@pytest.mark.parametrize("hq,n_prefix", [(4, 60), (40, 60), (400, 60), (50, 2100)], ids=["few", "wide", "joint", "shared"])
+def test_masked_rows_may_hold_anything(hq, n_prefix):
     # new rows with infinities and NaN: queries before them are untouched, queries from them on see them
     m, lens = 6, [6, 50]
-    s = make(140, 2, hq, 2, m, 60, 1, 16, lens)
+    s = make(140, 2, hq, 2, m, n_prefix, 1, 16, lens)
     clean, _ = attend(s)
     page = 16
     for b, j, val in ((0, 4, math.nan), (1, 47, math.inf), (1, 49, math.nan)):
