@@ -251,6 +251,7 @@ int evict_set_stream(evict_handle* h, void* stream);
  * (the flag is cleared). */
 int evict_sync(evict_handle* h);
 
+/* May be called while another stream captures a graph (a garbage collector's call): the capture goes on. */
 void evict_destroy(evict_handle* h);
 
 /* One-time Q-Filters calibration ("Q-Filters", §Calibrated — the paper's
@@ -426,7 +427,7 @@ int evict_pages_status(int32_t* error, void* stream);
  * anything but the arguments (no order of atomics). */
 typedef struct evict_attention {
   int batch, m, n_q_heads, n_kv_heads;
-  evict_rows q;              /* bf16; addresses and strides multiples of 16 bytes */
+  evict_rows q;              /* bf16; addresses and strides multiples of 16 bytes, strides not negative */
   evict_rows out;            /* bf16, likewise; must not overlap any input */
   float* lse;                /* device [batch, n_q_heads, m], or NULL */
   float scale;               /* 0 = 1 / sqrt(128) */
@@ -449,8 +450,9 @@ typedef struct evict_attention {
 int evict_shared_attention_workspace(const evict_attention* a, size_t* bytes);
 
 /* EVICT_EINVAL: NULL or misaligned pointers, bad sizes or strides, head counts that do not divide,
- * pages that are not bf16, a workspace that is too small; EVICT_ELIMIT: batch above
- * EVICT_MAX_ATTEND_BATCH, or batch * n_q_heads * m of 2^30 or more, or rows of tables beyond 2^31 steps of 16 in all. batch or m of 0 is a no-op.
+ * pages that are not bf16, a workspace that is too small. EVICT_ELIMIT: batch above
+ * EVICT_MAX_ATTEND_BATCH, batch * n_q_heads * m of 2^30 or more, or 2^31 or more steps of 16 rows in
+ * all, by the tables' width. batch or m of 0 is a no-op.
  * Device errors (a table entry outside the pool, read as zeros; lens beyond the table, cut to it;
  * n_new outside [0, m], taken as the nearest of these; a bounded wait that gave up) are reported
  * through `error`. */
