@@ -166,7 +166,7 @@ struct ScanShared {
   int e[kMaxWarps], rest[kMaxWarps];              // where the shares of this CTA begin
 };
 
-// Sums of a and b over the threads before this one, and their totals.
+// Sums of a and b over the threads before this one, and their totals. Between two calls is a barrier.
 template <int kThreads>
 __device__ __forceinline__ void block_scan(int& a, int& b, int& total, int& total_b, ScanShared& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -178,16 +178,19 @@ __device__ __forceinline__ void block_scan(int& a, int& b, int& total, int& tota
   }
   if (lane == 31) sh.a[warp] = x, sh.b[warp] = y;
   __syncthreads();
-  total = total_b = 0;
-#pragma unroll 1
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) x += sh.a[w], y += sh.b[w];
-    total += sh.a[w];
-    total_b += sh.b[w];
+  // every warp scans the warps' sums
+  constexpr int kCount = kThreads / 32;
+  int u = lane < kCount ? sh.a[lane] : 0, v = lane < kCount ? sh.b[lane] : 0;
+#pragma unroll
+  for (int d = 1; d < kCount; d <<= 1) {
+    const int s = __shfl_up_sync(0xffffffffu, u, d), t = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) u += s, v += t;
   }
-  __syncthreads();
-  a = x - a;
-  b = y - b;
+  total = __shfl_sync(0xffffffffu, u, kCount - 1);
+  total_b = __shfl_sync(0xffffffffu, v, kCount - 1);
+  const int before = __shfl_sync(0xffffffffu, u, max(warp - 1, 0)), before_b = __shfl_sync(0xffffffffu, v, max(warp - 1, 0));
+  a = x - a + (warp ? before : 0);
+  b = y - b + (warp ? before_b : 0);
 }
 
 // What a CTA works on: for wide units one share, otherwise one for each of its warps, `stride` apart

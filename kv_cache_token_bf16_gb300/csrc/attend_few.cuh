@@ -130,16 +130,22 @@ __device__ __forceinline__ void few_rows(const AttendParams& p, FewShared& sh, c
         }
         if (i == 0) {
           const uint32_t at = ring + requested * 2 * kBoxBytes;
-#pragma unroll 4
-          for (int e = lane; e < kRows * 16; e += 32) {
-            const QueryRow r = query_row<kRows>(p, set, cur.k, e >> 4);
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (r.real)
-              x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + (long long)r.b * p.qb +
-                                                 (long long)(cur.h * p.group + r.g) * p.qh + (long long)r.t * p.qm)[e & 15];
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + tc::sw128_offset(e >> 4, e & 15, kRows)),
-                         "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+          // two rows at a time, half a warp on each; lanes l and l + 16 know where row l is
+          const QueryRow r = query_row<kRows>(p, set, cur.k, lane & 15);
+          const long long mine =
+              r.real ? (long long)r.b * p.qb + (long long)(cur.h * p.group + r.g) * p.qh + (long long)r.t * p.qm : -1;
+          uint4 x[kRows / 2];
+#pragma unroll
+          for (int e = 0; e < kRows / 2; ++e) {
+            const long long from = __shfl_sync(0xffffffffu, mine, 2 * e + (lane >> 4));
+            x[e] = make_uint4(0, 0, 0, 0);
+            if (from >= 0) x[e] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + from)[lane & 15];
           }
+#pragma unroll
+          for (int e = 0; e < kRows / 2; ++e)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                         ::"r"(at + tc::sw128_offset(2 * e + (lane >> 4), lane & 15, kRows)),
+                         "r"(x[e].x), "r"(x[e].y), "r"(x[e].z), "r"(x[e].w) : "memory");
           __syncwarp();
           const uint32_t q_at = at + tc::sw128_offset(lane & 15, lane >> 4, kRows);
 #pragma unroll
