@@ -121,14 +121,16 @@ __device__ __forceinline__ void few_rows(const AttendParams& p, FewShared& sh, c
 #pragma unroll 1
       for (int i = 0; i < boxes; ++i) {
         __syncwarp();                             // every lane has read the box that the next one replaces
-        const int room = i == 0 ? kStages - 1 : kStages;           // a unit's queries pass through a stage first
+        // a unit's queries pass through a stage before the last box is requested
 #pragma unroll 1
-        while (flying < room && ahead_left > 0 && !dead) {
-          request(requested);
-          requested = requested == kStages - 1 ? 0 : requested + 1;
-          ++flying;
-        }
-        if (i == 0) {
+        for (int room = i == 0 ? kStages - 1 : kStages; room <= kStages; ++room) {
+#pragma unroll 1
+          while (flying < room && ahead_left > 0 && !dead) {
+            request(requested);
+            requested = requested == kStages - 1 ? 0 : requested + 1;
+            ++flying;
+          }
+          if (room == kStages) break;
           const uint32_t at = ring + requested * 2 * kBoxBytes;
           // two rows at a time, half a warp on each; lanes l and l + 16 know where row l is
           const QueryRow r = query_row<kRows>(p, set, cur.k, lane & 15);
@@ -163,6 +165,7 @@ __device__ __forceinline__ void few_rows(const AttendParams& p, FewShared& sh, c
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[j][k] = 0.f;
           low = __shfl_sync(0xffffffffu, last[0], 0);              // the first row's: the lowest
+          __syncwarp();
         }
         if (!dead) {
           const bool ok = wait_phase(&sh.full[warp][stage], parity, &sh.fail, p.err);
