@@ -218,19 +218,17 @@ bool multiple(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) 
 //
 // A prefix is the few-row kernel's where its queries fill at most two tiles of 16 rows and reading it
 // for each tile is little work: then the start counts, and the wide kernel's is longer. One tile (16
-// rows) over 1,024 / 2,048 / 4,096 / 16,384 rows: 15.1 / 16.9 / 20.7 / 33.0 us, wide 16.1 / 16.9 /
-// 17.3 / 25.4; two tiles (32 rows) over 512 / 1,024 / 2,048: 14.4 / 15.9 / 18.3, wide 16.3 / 16.4 / 17.1.
+// rows) over 1,024 / 2,048 / 4,096 / 16,384 rows: 12.1 / 14.0 / 17.6 / 28.3 us, wide 15.2 / 15.8 /
+// 16.2 / 22.0; two tiles (32 rows) over 512 / 1,024 / 2,048: 11.5 / 12.8 / 15.3, wide 15.3 / 15.4 / 16.2.
 constexpr int kFewTiles = 2, kFewPrefix = 2048;
 // Own rows are the few-row kernel's up to two tiles: 32 sequences of 1,024 rows with 20 / 32 query
-// rows each 52 / 55 us, wide 50 / 53, but behind a shared prefix the SMs split between the kinds (the
-// 20 rows of five drafts each behind 8,192 rows: 47 us, wide 53). With 40 / 64 rows 67 / 95 us, wide
-// 54 / 57.
+// rows each 42 / 45 us, wide 50 / 52; with 40 / 64 rows 56 / 89 us, wide 54 / 57.
 constexpr int kOwnWideFrom = kFewTiles * kRows + 1;
 // Sequences of more query rows than these take the prefix along in units of their own (joint: no
 // partial results to merge) where the prefix is short or they fill tiles of 256 rows by three
 // quarters; otherwise the sequences' rows share the prefix's tiles. 16 sequences behind 1,024 rows,
-// 160 / 320 rows each: joint 46 / 74 us, else 50 / 101; behind 16,384 rows, 160 / 208 / 320 / 512
-// rows each: joint 223 / 229 / 423 / 431, else 180 / 250 / 346 / 601.
+// 160 / 320 rows each: joint 46 / 73 us, else 49 / 102; behind 16,384 rows, 160 / 208 / 320 / 512
+// rows each: joint 227 / 232 / 431 / 439, else 183 / 248 / 352 / 598.
 constexpr int kJointFrom = 128, kJointPrefix = 2048;
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
@@ -266,18 +264,19 @@ void rebase(WorkSet& s, char* base) {
 
 constexpr size_t kWorkHead = 256;                 // an error word, for callers without one
 // Boxes (steps) that a share has at least: fewer would leave more partial results to merge than rows to
-// read. A step of 4 sequences behind 1,024 rows 14.7 us with two boxes, 14.9 with one, 16.3 with four;
-// 16 sequences behind 2,048 rows 17.9 us with three steps, 20.3 with one and 20.7 with six.
+// read. A step of 4 sequences behind 1,024 rows 11.8 us with two boxes, 12.2 with one, 13.4 with four;
+// 16 sequences behind 2,048 rows 16.8 us with three steps, 18.1 with one and 19.9 with six.
 constexpr int kFewMinBoxes = 2;
 constexpr int kWideMinSteps = 3;
 // Clocks of an SM, side by side, for a box of 16 rows, and for a step of 128 rows with two groups of
-// query rows at it, or with the groups taking turns. Fitted to when the two kinds end: with 262, 4600
-// and 2800 the wide CTAs of 128 sequences behind 16,384 rows ended 10 of 73 us before the others, and
-// 32 sequences' draft tokens behind 8,192 rows took 52 us instead of 47.
-constexpr int kFewCost = 300, kWideCostTwo = 4000, kWideCostAlt = 2600;
+// query rows at it, or with the groups taking turns. Fitted to when the two kinds end: 128 sequences
+// behind 16,384 rows take 75 us (with kWideCostTwo 4,000 80, with 4,700 79), 32 sequences' draft tokens
+// behind 8,192 rows 41 (43, 42); four answers to each of eight prompts 32 (with kWideCostAlt 2,400 37,
+// with 2,800 35), a decode step of 32 sequences 27 (27, 26).
+constexpr int kFewCost = 300, kWideCostTwo = 4400, kWideCostAlt = 2600;
 // What a unit's start costs beside: a warp or CTA fetches its queries and leaves the last unit's results.
-// (Counted as nothing: 16 sequences behind 2,048 rows 20.2 us instead of 17.9, 256 new rows of each of
-// eight sequences 61.7 instead of 58.3.)
+// (Counted as nothing: 16 sequences behind 2,048 rows 19.4 us instead of 16.8, 256 new rows of each of
+// eight sequences 60.7 instead of 57.3.)
 constexpr int kFewEntry = 2, kWideEntry = 3;
 
 // Sizes alone decide: lens and n_new are the device's.
@@ -481,8 +480,8 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
     if (plan.sms > 1)
       e = launch_pdl(attend_join_split_kernel, dim3(plan.sms - 1, kWideRows / kJoinWarps), dim3(kJoinWarps * 32), 0, st, nullptr, P);
   } else {
-    // four warps a row while the rows are few (4 sequences x 12 heads 14.7 us, with one 18.0; 48 x 32 heads
-    // 36.6 us with one, with four 41.1)
+    // four warps a row while the rows are few (4 sequences x 12 heads 11.8 us, with one 15.3; 48 x 32 heads
+    // 34.5 us with one, with four 39.1)
     const int rows = a->batch * a->n_q_heads * a->m, split = rows <= plan.sms * kJoinWarps ? 4 : 1;
     const dim3 grid((rows * split + kJoinWarps - 1) / kJoinWarps), block(kJoinWarps * 32);
     e = split == 4 ? launch_pdl(attend_join_kernel<4>, grid, block, 0, st, nullptr, P)

@@ -7,8 +7,8 @@
 // start or end of a unit hides behind the others' rows. Queries are the products' rows. Bound: HBM;
 // a warp has one box in flight while it computes on another (96 KB an SM).
 //
-// Measured: 16 sequences of 16,384 own rows with 4 query rows a KV head (1.07 GB) 180 us, 6.0 TB/s;
-// 32 sequences of 4,096 rows 100 us, 5.4; of 1,024 rows 38 us, 3.5: 14 us of a call are its start and
+// Measured: 16 sequences of 16,384 own rows with 4 query rows a KV head (1.07 GB) 174 us, 6.2 TB/s;
+// 32 sequences of 4,096 rows 95 us, 5.7; of 1,024 rows 33 us, 4.0: 11 us of a call are its start and
 // the join. The split of the weights into hi + lo costs no time there and keeps the output's error
 // that of one rounding.
 #pragma once
