@@ -75,9 +75,14 @@ def _device(t):
     return index
 
 
-def _rows(t, name, index, dtype, batch=None, m=None, heads=None):
+def _rows(t, name, index, dtype, batch, m, heads=None):
     """The fields of a tensor's evict_rows [batch, heads, m, 128]."""
-    shape = t.shape
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 4 and strides[3] == 1:
+        b, h, n, d = shape
+        if d == HEAD_DIM and b == batch and n == m and t.dtype is dtype and t.get_device() == index and (
+                heads is None or h == heads):
+            return t.data_ptr(), strides[0], strides[1], strides[2], h
     if len(shape) != 4 or shape[3] != HEAD_DIM:
         raise ValueError(f"{name} must be [batch, heads, m, {HEAD_DIM}], not {tuple(shape)}")
     if shape[0] != batch or shape[2] != m or (heads is not None and shape[1] != heads):
@@ -86,10 +91,15 @@ def _rows(t, name, index, dtype, batch=None, m=None, heads=None):
         raise ValueError(f"{name} is {t.dtype}, not {dtype}")
     if t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, not on CUDA device {index}")
+    raise ValueError(f"{name}: the 128 elements of a row must be adjacent")
+
+
+def _new_rows(t):
+    """The same of a tensor made here like one that was checked."""
     sb, sh, sm, se = t.stride()
     if se != 1:
-        raise ValueError(f"{name}: the 128 elements of a row must be adjacent")
-    return t.data_ptr(), sb, sh, sm, shape[1]
+        raise ValueError("no output can be made like this input: give one")
+    return t.data_ptr(), sb, sh, sm, t.shape[1]
 
 
 def _like(t, name, shape, dtype, index):
@@ -186,12 +196,9 @@ def rotate(rotary: Rotary, x, pos=None, pos_base: int = 0, out=None, transpose: 
         _load()
     one = isinstance(x, _torch.Tensor)
     xs = (x,) if one else tuple(x)
-    if out is None:
-        outs = tuple([_torch.empty_like(t) for t in xs])
-    else:
-        outs = (out,) if isinstance(out, _torch.Tensor) else tuple(out)
+    outs = None if out is None else (out,) if isinstance(out, _torch.Tensor) else tuple(out)
     n = len(xs)
-    if len(outs) != n or not 1 <= n <= 2:
+    if not 1 <= n <= 2 or (outs is not None and len(outs) != n):
         raise ValueError("one or two tensors, and as many outputs")
     first = xs[0]
     index, dtype, shape = _device(first), first.dtype, first.shape
@@ -199,7 +206,11 @@ def rotate(rotary: Rotary, x, pos=None, pos_base: int = 0, out=None, transpose: 
         raise ValueError(f"x must be [batch, heads, m, {HEAD_DIM}], not {tuple(shape)}")
     batch, m = shape[0], shape[2]
     ins = b"".join([_ROWS.pack(*_rows(t, "x", index, dtype, batch, m)) for t in xs])
-    ous = b"".join([_ROWS.pack(*_rows(o, "out", index, dtype, batch, m, t.shape[1])) for t, o in zip(xs, outs)])
+    if outs is None:
+        outs = tuple([_torch.empty_like(t) for t in xs])
+        ous = b"".join([_ROWS.pack(*_new_rows(o)) for o in outs])
+    else:
+        ous = b"".join([_ROWS.pack(*_rows(o, "out", index, dtype, batch, m, t.shape[1])) for t, o in zip(xs, outs)])
     _call(index, _calls.evict_rotate, rotary.handle, _dtype(dtype), batch, m, _pos(pos, rotary, batch, m, index), pos_base,
           1 if transpose else 0, ins, ous, n, _stream(index))
     return outs[0] if one else outs
@@ -242,9 +253,12 @@ def shared_attention(q, prefix=None, pages: "PagedCache | None" = None, n_new=No
         raise ValueError(f"q must be [batch, heads, m, {HEAD_DIM}], not {tuple(shape)}")
     batch, hq, m, _ = shape
     bf16 = _torch.bfloat16
+    qr = _rows(q, "q", index, bf16, batch, m)
     if out is None:
         out = _torch.empty_like(q) if n_new is None else _torch.zeros_like(q)
-    qr, outr = _rows(q, "q", index, bf16, batch, m), _rows(out, "out", index, bf16, batch, m, hq)
+        outr = _new_rows(out)
+    else:
+        outr = _rows(out, "out", index, bf16, batch, m, hq)
     if scale is None:
         scale = 0.0
     elif scale == 0:
@@ -400,9 +414,9 @@ class PagedCache:
         kr, vr = _ROWS.pack(*_rows(k, "k", index, dtype, batch, m)), _ROWS.pack(*_rows(v, "v", index, dtype, batch, m))
         qr = qo = None
         if q is not None:
+            qr = _ROWS.pack(*_rows(q, "q", index, dtype, batch, m))
             if q_out is None:
                 q_out = _torch.empty_like(q) if n_new is None else _torch.zeros_like(q)
-            qr = _ROWS.pack(*_rows(q, "q", index, dtype, batch, m))
             qo = _ROWS.pack(*_rows(q_out, "q_out", index, dtype, batch, m, q.shape[1]))
         elif q_out is not None:
             raise ValueError("q_out without q")

@@ -292,3 +292,20 @@ def test_bad_append_tensors_are_refused():
                   ((k, k), dict(q=rows(1, 3, 4, 2))), ((k, k), dict(n_new=torch.zeros(2, dtype=torch.int32).cuda()))):
         with pytest.raises(ValueError):
             c.append(*a, **kw)
+
+
+@pytest.mark.parametrize("shared", [0, 1, 2])
+def test_outputs_like_an_expanded_input(shared):
+    # an input that repeats itself along an axis gets an output that does not
+    shape = [3, 4, 5, D]
+    small = list(shape)
+    small[shared] = 1
+    g = torch.Generator().manual_seed(77)
+    x = torch.randn(*small, generator=g).cuda().expand(*shape)
+    rot = paged.Rotary()
+    out = paged.rotate(rot, x, pos_base=9)
+    assert torch.equal(out, paged.rotate(rot, x.contiguous(), pos_base=9))
+    q = x.to(torch.bfloat16)[:, :, :, :].contiguous()[:, :1].expand(*shape)
+    k = torch.randn(1, 2, 40, D, generator=g).to(torch.bfloat16).cuda()
+    got = paged.shared_attention(q, prefix=(k, k))
+    assert torch.equal(got, paged.shared_attention(q.contiguous(), prefix=(k, k)))
