@@ -20,11 +20,12 @@
 // packed fp32 pairs. The first heads' loads leave before the angles and the
 // page table are looked at: the rows' addresses need neither.
 //
-// Measured: 8,192 tokens of 32 bf16 heads 22.9 us (134 MB, 5.9 TB/s); 4 x 1,023
-// tokens of 40 fp32 heads 27.0 us (168 MB, 6.2 TB/s); prompts of up to 2,048
-// tokens of 48 heads, 219 MB, into pages 43.9 us (5.0 TB/s). With 256 threads
-// and 4 tokens a block: 24.3, 28.0 and 45.8; with the loads after the angles
-// and eight threads of an fp32 row: 28, 50 and 50.
+// Measured: 8,192 tokens of 32 bf16 heads 22.8 us (134 MB, 5.9 TB/s); 4 x 1,023
+// tokens of 40 fp32 heads 27.1 us (168 MB, 6.2 TB/s); prompts of up to 2,048
+// tokens of 48 heads, 219 MB, into pages 37.9 us (5.8 TB/s; 43.9 where blocks of
+// padding made their angles, too, and pages were looked up behind them). With
+// 256 threads and 4 tokens a block the first two took 24.3 and 28.0, with the
+// loads after the angles and eight threads of an fp32 row 28 and 50.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(kRowThreads, 8) rows_kernel(const __grid_const
   constexpr int kUnit = 16 / (int)sizeof(T);       // pairs of a thread
   constexpr int kLanes = kHeadDim / 2 / kUnit;     // threads of a row
   constexpr int kRows = kRowThreads / kLanes;      // rows that a block works on at a time
-  constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;   // heads of a thread in flight
+  constexpr int kAhead = sizeof(T) == 4 ? 2 : kPaged ? 3 : 4;   // heads of a thread in flight
   __shared__ __align__(16) float cosine[kTokens][kHeadDim / 2], sine[kTokens][kHeadDim / 2];
   pdl_wait();
   const int half = p.rot.half;
@@ -146,16 +147,20 @@ __global__ void __launch_bounds__(kRowThreads, 8) rows_kernel(const __grid_const
   const int own = threadIdx.x / kLanes / groups, group = threadIdx.x / kLanes - own * groups;   // token, row of its heads
   const unsigned tok = blockIdx.x * p.per_block + own;
   const int b = (int)(tok / (unsigned)p.m), t = (int)(tok - (unsigned)b * p.m);
-  int n = p.m;
-  bool odd = false;
+  int n = p.m, len = 0;
   if constexpr (kPaged) {
-    if (p.n_new && tok < p.tokens) {
-      n = p.n_new[b];
-      odd = n < 0 || n > p.m;
-      n = n < 0 ? 0 : n > p.m ? p.m : n;
+    if (tok < p.tokens) {
+      len = p.lens[b];
+      if (p.n_new) {
+        n = p.n_new[b];
+        if ((n < 0 || n > p.m) && u == 0 && group == 0 && t == 0 && p.err) raise_device_error(p.err, kDevBadIndex);
+        n = n < 0 ? 0 : n > p.m ? p.m : n;
+      }
     }
   }
   const bool live = tok < p.tokens && t < n;
+  if constexpr (kPaged)
+    if (p.n_new && !__syncthreads_or(live)) return;            // padding
 
   const bool turns = kUnit * u < half;             // kVec: all of its pairs turn, or none
   // this thread's elements: at `ea` and `eb`, kUnit each
@@ -180,6 +185,17 @@ __global__ void __launch_bounds__(kRowThreads, 8) rows_kernel(const __grid_const
   };
   if constexpr (kVec)
     if (live) pull(group);
+  // The token's page, its row there: looked up while the angles are made. (fp32's take sincospif's
+  // registers: 12.7 us behind them, 13.6 before, for 59 MB.)
+  int page = -1, row = 0;
+  if constexpr (kPaged && sizeof(T) == 2) {
+    if (live) {
+      const int j = len - n + t;
+      row = j & ((1 << p.page_shift) - 1);
+      if (j >= 0 && (j >> p.page_shift) < p.table_width)
+        page = p.table[(long long)b * p.table_stride + (j >> p.page_shift)];
+    }
+  }
 
   // the angles
   if ((int)threadIdx.x < p.per_block * (kHeadDim / 2)) {
@@ -203,18 +219,21 @@ __global__ void __launch_bounds__(kRowThreads, 8) rows_kernel(const __grid_const
     cosine[i][f] = c;
     sine[i][f] = s;
   }
+  if constexpr (kPaged && sizeof(T) == 4) {
+    if (live) {
+      const int j = len - n + t;
+      row = j & ((1 << p.page_shift) - 1);
+      if (j >= 0 && (j >> p.page_shift) < p.table_width)
+        page = p.table[(long long)b * p.table_stride + (j >> p.page_shift)];
+    }
+  }
   bool stored = true;                              // the token's page row exists
   long long at = 0;                                // its element offset in the pool (head 0)
   if constexpr (kPaged) {
-    if (odd && u == 0 && group == 0 && t == 0 && p.err) raise_device_error(p.err, kDevBadIndex);
     if (live) {
-      const int j = p.lens[b] - n + t;
-      int page = -1;
-      if (j >= 0 && (j >> p.page_shift) < p.table_width)
-        page = p.table[(long long)b * p.table_stride + (j >> p.page_shift)];
       stored = page >= 0 && page < p.n_pages;
       if (!stored && u == 0 && group == 0 && p.err) raise_device_error(p.err, kDevBadIndex);
-      if (stored) at = (long long)page * p.page_stride + (long long)(j & ((1 << p.page_shift) - 1)) * kHeadDim;
+      if (stored) at = (long long)page * p.page_stride + (long long)row * kHeadDim;
     }
   }
   auto target = [&](int h) -> T* {                 // null: nowhere
@@ -343,7 +362,7 @@ int run_rows(RowsParams& P, bool vec, bool paged, int dtype, cudaStream_t st) {
   if (tokens * P.heads >= (1ll << 31))
     return fail(EVICT_ELIMIT, "batch * m * heads = %lld rows are 2^31 or more", tokens * P.heads);
   P.tokens = (unsigned)tokens;
-  // A block a token while that is no more than two blocks an SM: a decode step of 32 sequences takes 3.4 us so, and
+  // A block a token while that is no more than two blocks an SM: a decode step of 32 sequences takes 3.2 us so, and
   // 4.8 with kTokens. With many tokens the other way round: 8,192 tokens 26.0 us with one and 22.8 with kTokens.
   P.per_block = tokens <= 2 * 152 ? 1 : kTokens;
   const dim3 grid((P.tokens + P.per_block - 1) / P.per_block);
