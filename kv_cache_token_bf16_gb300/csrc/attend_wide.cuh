@@ -50,7 +50,7 @@ constexpr int kRing = 5;
 constexpr int kWideSmem = (2 + kRing) * kTileBytes;
 constexpr int kMmaWarp = 8, kTmaWarp = 10;
 constexpr int kBadWords = 9;                      // 257 tokens and more
-constexpr int kBadSets = 16;                      // segments in flight, by far
+constexpr int kBadSets = 4;                       // of a group's segments in turn (see softmax_group)
 constexpr float kMoveAbove = 4096.f;              // sum of 32 weights that makes the reference move
 
 struct WideShared {
@@ -58,7 +58,8 @@ struct WideShared {
   uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2], done[2];   // group, half of the step
   uint32_t tmem_base;
   int fail;
-  uint32_t bad[kBadSets][kBadWords];              // of the segments in turn: rows of V that were blanked
+  uint32_t bad[2][kBadSets][kBadWords];           // of either group: rows of V that it found blanked
+  uint32_t blanked[kRing][kTile / 32];            // of the tile of V in a slot: rows that either group blanked
 };
 
 using WideCursor = Cursor<kWideRows, kWideTokens>;
@@ -123,6 +124,9 @@ __device__ void producer(const AttendParams& p, WideShared& sh, WideCursor c, in
         if (!ok) break;
         uint64_t* bar = &sh.kv_full[slot.i];
         const uint32_t dst = ring + slot.i * kTileBytes;
+        // both groups are done with the slot's last tile, and see these zeros once they see the next
+        if (kv && lane < kTile / 32) sh.blanked[slot.i][lane] = 0;
+        __syncwarp();
         if (lane == 0) tc::mbar_arrive_expect_tx(bar, kTileBytes);
         __syncwarp();
         if (pre) {
@@ -372,8 +376,10 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
   // A step's rows of V that no query of the unit sees may hold anything, and so may rows that some
   // queries do not see: both meet weights of 0, but 0 * infinity is not 0. This thread looks at the
   // tile's row `row` and writes zeros over it in the first case and, where it holds infinities or
-  // NaN, in the second, with a mark for the queries that do see it. Both groups may do so; the mark
-  // is there before the zeros are, so a group that finds zeros finds the mark, too.
+  // NaN, in the second, with a mark for the group's queries that do see it. Both groups may do so with
+  // the same tile, and each writes all of a row's zeros itself before its own product. A group may
+  // find a row that the other one has begun to clear, finite by then: the row's bit in `blanked` is
+  // there before the zeros are, so who reads a zero of the other's reads its bit afterwards.
   auto blank_rows = [&](int slot, int own0, int first, uint32_t* bad) {
     const uint32_t at = ring + slot * kTileBytes + row * 128;
     const int tok = own0 + row;
@@ -386,7 +392,12 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
                      : "r"(at + (j >> 3) * (kTileBytes / 2) + ((j + row) & 7) * 16) : "memory");
         blank = nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w);
       }
+      const uint32_t bit = 1u << (row & 31);
+      uint32_t* const blanked = &sh.blanked[slot][row >> 5];
+      __threadfence_block();
+      if (!blank) blank = *(volatile uint32_t*)blanked & bit;
       if (blank) {
+        atomicOr(blanked, bit);
         atomicOr(&bad[(tok - first) >> 5], 1u << ((tok - first) & 31));
         __threadfence_block();
       }
@@ -419,6 +430,11 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
   int limit = -1;                                 // last own row that this query sees
   float ref = -INFINITY, sum = 0.f;
   bool marks = false;                             // the segment holds rows that may have been marked
+  // The segments in which this group has a job, counted: segment i's marks are in set i % kBadSets. Its
+  // first warp clears the set of segment i + 2 as it begins segment i. It has then seen the products of
+  // segment i - 1, so every warp has left segment i - 2 and its marks, which lay there; and none marks
+  // in segment i + 2 before all four warps have announced its queries.
+  int turn = -1;
   Slot slot;                                      // of the segment's first tile
   for (int segment = -1;; ++segment) {            // -1: only the first unit's queries
     // The next unit's queries: this group's last S is in registers, so its tile is free.
@@ -449,7 +465,7 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
       const float inv = sees ? 1.f / sum : 0.f;
       uint32_t any_bad = 0;
       const int first = first_marked(p, at);
-      const uint32_t* bad = sh.bad[segment & (kBadSets - 1)];
+      const uint32_t* bad = sh.bad[w][turn & (kBadSets - 1)];   // (marks: the group had a job)
       if (marks)
         for (int k = 0; k < kBadWords; ++k) any_bad |= bad[k];
 #pragma unroll 1
@@ -523,8 +539,11 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
     marks = false;
     bool begun = false;
     const int first = p.m > 1 && c.k.reach >= 0 ? first_marked(p, c) : 1 << 30;
-    uint32_t* bad = sh.bad[(segment + 1) & (kBadSets - 1)];
-    if (w == 0 && row < kBadWords) sh.bad[(segment + 1 + kBadSets / 2) & (kBadSets - 1)][row] = 0;
+    if (g.jobs(w) > 0) {
+      ++turn;
+      if (row < kBadWords) sh.bad[w][(turn + 2) & (kBadSets - 1)][row] = 0;
+    }
+    uint32_t* bad = sh.bad[w][turn & (kBadSets - 1)];
 #pragma unroll 1
     for (int i = 0; i < g.steps; ++i) {
       slot.next();                                // the step's V
@@ -624,7 +643,7 @@ __device__ __forceinline__ void wide_setup(WideShared& sh) {
     tc::mbar_init(&sh.done[lane], 1);
   }
   if (warp > 3) {
-    for (int i = tid - 128; i < kBadSets * kBadWords; i += blockDim.x - 128) (&sh.bad[0][0])[i] = 0;
+    for (int i = tid - 128; i < 2 * kBadSets * kBadWords; i += blockDim.x - 128) (&sh.bad[0][0][0])[i] = 0;
     if (tid == 128) sh.fail = 0;
   }
 }
