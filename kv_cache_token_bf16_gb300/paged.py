@@ -301,15 +301,29 @@ def shared_attention(q, prefix=None, pages: "PagedCache | None" = None, n_new=No
     return out
 
 
+def _page_strides(k_pages, table):
+    """Elements between pages, and between the table's rows, for evict_pages (0: dense, which is what a
+    single page or row is given as). Pages or rows of the table on top of each other are refused."""
+    n_pages, heads, page, _ = k_pages.shape
+    batch, width = table.shape
+    ps, ts = k_pages.stride(0) if n_pages > 1 else 0, table.stride(0) if batch > 1 else 0
+    if n_pages > 1 and ps < heads * page * HEAD_DIM:
+        raise ValueError(f"pages of {heads * page * HEAD_DIM} elements are {ps} apart: they would lie on top of each other")
+    if batch > 1 and ts < width:
+        raise ValueError(f"the table's rows of {width} entries are {ts} apart: give every sequence a row of its own")
+    return ps, ts
+
+
 class PagedCache:
     """Own rows of a batch of sequences, in pages of a pool.
 
     Either ``PagedCache(n_pages=, page_size=, n_kv_heads=, batch=, max_rows=, dtype=)`` makes the
     tensors (zeros, no rows), and ``grow`` / ``release`` hand out the pages; or the caller brings
     ``k_pages``, ``v_pages`` [n_pages, n_kv_heads, page_size, 128] (a page's rows dense, pages any
-    stride apart), ``table`` [batch, width] int32 and ``lens`` [batch] int32, and keeps the last
-    two up to date: row j of sequence b is row j % page_size of page table[b, j // page_size], and
-    lens counts a call's new rows before the call.
+    stride apart), ``table`` [batch, width] int32 (a row of its own for every sequence, also where
+    they name the same pages) and ``lens`` [batch] int32, and keeps the last two up to date: row j of
+    sequence b is row j % page_size of page table[b, j // page_size], and lens counts a call's new
+    rows before the call.
     """
 
     def __init__(self, n_pages: int | None = None, page_size: int | None = None, n_kv_heads: int | None = None,
@@ -342,18 +356,19 @@ class PagedCache:
                 v_pages.dtype != k_pages.dtype or v_pages.stride() != k_pages.stride():
             raise ValueError(f"pages must be two tensors [n_pages, n_kv_heads, page_size, {HEAD_DIM}] alike")
         self.n_pages, self.n_kv_heads, self.page_size, _ = k_pages.shape
-        sp, sh, sr, se = k_pages.stride()
+        _, sh, sr, se = k_pages.stride()
         if (sh, sr, se) != (self.page_size * HEAD_DIM, HEAD_DIM, 1) and self.n_pages * self.n_kv_heads > 0:
             raise ValueError("the rows of a page must be dense")
         if table.dim() != 2 or table.dtype != torch.int32 or table.stride(1) != 1:
             raise ValueError("table must be int32 [batch, width] with adjacent entries")
         self.batch, self.width = table.shape
+        page_stride, table_stride = _page_strides(k_pages, table)
         _like(lens, "lens", (self.batch,), torch.int32, self.index)
         self.k_pages, self.v_pages, self.table, self.lens = k_pages, v_pages, table, lens
         self.error = torch.zeros(1, dtype=torch.int32, device=self.device)
-        self.struct = EvictPages(k=k_pages.data_ptr(), v=v_pages.data_ptr(), page_stride=sp, n_pages=self.n_pages,
+        self.struct = EvictPages(k=k_pages.data_ptr(), v=v_pages.data_ptr(), page_stride=page_stride, n_pages=self.n_pages,
                                  page_size=self.page_size, n_kv_heads=self.n_kv_heads, dtype=_dtype(k_pages.dtype),
-                                 table=table.data_ptr(), table_stride=table.stride(0), table_width=table.shape[1],
+                                 table=table.data_ptr(), table_stride=table_stride, table_width=self.width,
                                  lens=lens.data_ptr(), error=self.error.data_ptr())
         self.address, self.error_at = ctypes.addressof(self.struct), self.error.data_ptr()
 

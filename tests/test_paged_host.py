@@ -217,3 +217,23 @@ def test_host_tensors_are_refused(lib):
         paged.rotate(paged.Rotary(), x)
     with pytest.raises(ValueError, match="CUDA"):
         paged.shared_attention(x.bfloat16(), prefix=(x, x))
+
+
+# --- strides that the C structs cannot say -------------------------------------------------------
+def test_shared_table_rows_and_pages_on_top_of_each_other_are_refused():
+    torch = pytest.importorskip("torch")
+    pool = torch.zeros(6, 2, 16, 128, dtype=torch.bfloat16)
+    table = torch.zeros(3, 4, dtype=torch.int32)
+    assert paged._page_strides(pool, table) == (2 * 16 * 128, 4)
+    assert paged._page_strides(pool[::2], table[:, :3]) == (2 * 2 * 16 * 128, 4)
+    # a stride of 0 is what the structs hold for "dense": it must never come from a tensor
+    with pytest.raises(ValueError, match="table"):
+        paged._page_strides(pool, table[:1].expand(3, 4))
+    with pytest.raises(ValueError, match="table"):
+        paged._page_strides(pool, torch.zeros(12, dtype=torch.int32).as_strided((3, 4), (2, 1)))
+    with pytest.raises(ValueError, match="pages"):
+        paged._page_strides(pool[:1].expand(6, 2, 16, 128), table)
+    with pytest.raises(ValueError, match="pages"):
+        paged._page_strides(pool.flatten().as_strided((3, 2, 16, 128), (2048, 2048, 128, 1)), table)
+    # one page, one sequence: nothing is stepped over, whatever the strides say
+    assert paged._page_strides(pool[:1].as_strided((1, 2, 16, 128), (8, 2048, 128, 1)), table[:1].as_strided((1, 4), (1, 1))) == (0, 0)
