@@ -246,6 +246,10 @@ int evict_reset(evict_handle* h);
 /* Change the stream of subsequent work. */
 int evict_set_stream(evict_handle* h, void* stream);
 
+/* The stream of subsequent work: who reads a view on another stream has to order that stream behind
+ * this one, and this one's next update behind the reading. EVICT_EINVAL: NULL arguments. */
+int evict_get_stream(const evict_handle* h, void** stream);
+
 /* Synchronise the handle's stream and check the device error word:
  * EVICT_ECUDA on a CUDA error, EVICT_EDEVICE if a kernel flagged one
  * (the flag is cleared). */

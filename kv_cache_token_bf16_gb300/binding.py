@@ -100,6 +100,7 @@ _SIGNATURES = {
     "evict_set_state": (_I, [_P, _P, _P, _P, _P, _I, ctypes.c_int64]),
     "evict_reset": (_I, [_P]),
     "evict_set_stream": (_I, [_P, _P]),
+    "evict_get_stream": (_I, [_P, ctypes.POINTER(_P)]),
     "evict_sync": (_I, [_P]),
     "evict_destroy": (None, [_P]),
     "evict_qfilters_calibrate": (_I, [_P, _I, _I, _I, _I, _I, _P, _P]),
@@ -203,6 +204,12 @@ def evict_reset(h):
 
 def evict_set_stream(h, stream):
     check(load().evict_set_stream(h, stream))
+
+
+def evict_get_stream(h) -> int:
+    s = _P()
+    check(load().evict_get_stream(h, ctypes.byref(s)))
+    return s.value or 0
 
 
 def evict_sync(h):
@@ -388,12 +395,36 @@ class EvictCache:
     def attend(self, q, n_new=None, scale=None, out=None, lse=None):
         """Attention of the queries q [batch, n_q_heads, m, 128] (bf16, rotated) over this cache's
         kept rows, all of which every query sees: paged.shared_attention without pages. A batch
-        that is a multiple of the cache's gives every kept prefix to that many sequences."""
+        that is a multiple of the cache's gives every kept prefix to that many sequences.
+
+        Work goes on the current stream. Where that is not the cache's, it is ordered behind the
+        cache's last update, and the cache's next one behind it. A graph that another stream captures
+        cannot hold that order: it reads the rows kept when it is replayed, and the replay has to be
+        ordered like any other reader. (A capture of the cache's own stream needs attend under it.)"""
+        import torch
         from . import paged
+        here, own = torch.cuda.current_stream(), evict_get_stream(self.handle)
+        if here.cuda_stream == own:
+            own = None
+        else:
+            own = torch.cuda.ExternalStream(own) if own else torch.cuda.default_stream()
+            captures = torch.cuda.is_current_stream_capturing()
+            with torch.cuda.stream(own):
+                if torch.cuda.is_current_stream_capturing() and not captures:
+                    raise ValueError("the cache's stream is being captured: attend under it")
+            if captures:
+                own = None
+            else:
+                here.wait_stream(own)
         k, v, _, _ = self.view()
-        return paged.shared_attention(q, prefix=(k, v), n_new=n_new, scale=scale, out=out, lse=lse)
+        got = paged.shared_attention(q, prefix=(k, v), n_new=n_new, scale=scale, out=out, lse=lse)
+        if own is not None:
+            own.wait_stream(here)
+        return got
 
     def view(self):
+        """Tensors over the kept rows, without a copy: what the cache's stream has left there, until its
+        next update. (A reader on another stream orders itself: evict_get_stream.)"""
         return view_tensors(evict_get_view(self.handle), self.batch, self.heads, self.dtype)
 
     def set_state(self, k, v, pos, score=None, offset=None):

@@ -546,6 +546,12 @@ int evict_set_stream(evict_handle* h, void* stream) {
   return EVICT_OK;
 }
 
+int evict_get_stream(const evict_handle* h, void** stream) {
+  if (!h || !stream) return fail(EVICT_EINVAL, "handle and stream must not be NULL");
+  *stream = h->stream;
+  return EVICT_OK;
+}
+
 int evict_sync(evict_handle* h) {
   if (!h) return fail(EVICT_EINVAL, "handle is NULL");
   cudaError_t e = cudaStreamSynchronize(h->stream);

@@ -4,7 +4,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from kv_cache_token_bf16_gb300 import paged  # noqa: E402
+from kv_cache_token_bf16_gb300 import binding, paged  # noqa: E402
 from tests.paged_util import D, gather  # noqa: E402
 from tests.test_gpu_attend import _built, attend, check, make, randn  # noqa: E402,F401
 
@@ -26,3 +26,64 @@ def test_a_table_shared_by_all_sequences_has_to_be_repeated():
         one = dict(s, q=s["q"][b:b + 1], own=s["own"][b:b + 1])
         one["cache"] = paged.PagedCache(k_pages=kp, v_pages=vp, table=row.as_strided((1, 2), (0, 1)), lens=lens[b:b + 1])
         check(one, *attend(one))
+
+
+WAIT = 40_000_000                   # clocks: some 20 ms
+
+
+@pytest.mark.parametrize("default", [True, False], ids=["default", "own"])
+def test_kept_rows_attended_to_on_another_stream(default):
+    # the cache's stream is late: the attention waits for it; and then the other way round
+    B, H, n = 2, 2, 64
+    mine, other = torch.cuda.Stream(), torch.cuda.Stream()
+    made = torch.cuda.current_stream() if default else mine
+    k, v, q = randn(500, B, H, 4 * n, D), randn(501, B, H, 4 * n, D), randn(502, B, 8, 2, D)
+    block = [(k[:, :, i * n:(i + 1) * n].contiguous(), v[:, :, i * n:(i + 1) * n].contiguous()) for i in range(4)]
+    with torch.cuda.stream(made):
+        cache = binding.EvictCache("knorm", B, H, budget=4 * n, max_block=n, n_sink=4, recent=8)
+    assert binding.evict_get_stream(cache.handle) == made.cuda_stream
+    torch.cuda.synchronize()
+    for i in (0, 2):
+        lse = [torch.full((B, 8, 2), 7.0, device="cuda") for _ in range(2)]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(made):
+            torch.cuda._sleep(WAIT)
+            cache.update_and_fetch(*block[i])
+        with torch.cuda.stream(other):
+            first = cache.attend(q, lse=lse[0])              # behind the update
+            torch.cuda._sleep(WAIT)
+            second = cache.attend(q, lse=lse[1])             # before the next one
+        with torch.cuda.stream(made):
+            cache.update_and_fetch(*block[i + 1])
+            # the rows read above are overwritten: the cache starts again
+            cache.set_state(k[:, :, 4 * n - 8:].contiguous(), v[:, :, 4 * n - 8:].contiguous(),
+                            torch.arange(8, dtype=torch.int32, device="cuda").expand(B, H, 8).contiguous())
+            cache.set_state(k[:, :, :(i + 2) * n].contiguous(), v[:, :, :(i + 2) * n].contiguous(),
+                            torch.arange((i + 2) * n, dtype=torch.int32, device="cuda").expand(B, H, (i + 2) * n).contiguous())
+        torch.cuda.synchronize()
+        s = {"q": q, "prefix": (k[:, :, :(i + 1) * n], v[:, :, :(i + 1) * n]), "new": None}
+        check(s, first, lse[0])
+        check(s, second, lse[1])
+    cache.sync()
+    cache.close()
+
+
+def test_kept_rows_attended_to_in_a_captured_graph():
+    # captured on another stream than the cache's: a replay reads what is kept then
+    k, v, q = randn(510, 1, 2, 128, D), randn(511, 1, 2, 128, D), randn(512, 3, 4, 1, D)
+    cache = binding.EvictCache("knorm", 1, 2, budget=128, max_block=128, n_sink=4, recent=8)
+    cache.update_and_fetch(k, v)
+    out = torch.zeros_like(q)
+    lse = torch.full((3, 4, 1), 7.0, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.attend(q, out=out, lse=lse)
+    for seed in (513, 514):
+        k2 = randn(seed, 1, 2, 128, D)
+        cache.set_state(k2, v, torch.arange(128, dtype=torch.int32, device="cuda").expand(1, 2, 128).contiguous())
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        check({"q": q, "prefix": (k2, v), "new": None}, out, lse)
+    cache.close()

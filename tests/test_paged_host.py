@@ -237,3 +237,8 @@ def test_shared_table_rows_and_pages_on_top_of_each_other_are_refused():
         paged._page_strides(pool.flatten().as_strided((3, 2, 16, 128), (2048, 2048, 128, 1)), table)
     # one page, one sequence: nothing is stepped over, whatever the strides say
     assert paged._page_strides(pool[:1].as_strided((1, 2, 16, 128), (8, 2048, 128, 1)), table[:1].as_strided((1, 4), (1, 1))) == (0, 0)
+
+
+def test_a_handles_stream_needs_a_handle(lib):
+    out = ctypes.c_void_p(7)
+    assert lib.evict_get_stream(None, ctypes.byref(out)) == EVICT_EINVAL and out.value == 7
