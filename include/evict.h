@@ -255,7 +255,9 @@ int evict_get_stream(const evict_handle* h, void** stream);
  * (the flag is cleared). */
 int evict_sync(evict_handle* h);
 
-/* May be called while another stream captures a graph (a garbage collector's call): the capture goes on. */
+/* May be called while any stream captures a graph (a garbage collector's call): the capture goes on,
+ * unless it holds work of this very handle, whose memory is gone with it: that capture ends with an
+ * error (cudaErrorStreamCaptureInvalidated). A graph captured before must not be replayed afterwards. */
 void evict_destroy(evict_handle* h);
 
 /* One-time Q-Filters calibration ("Q-Filters", §Calibrated — the paper's

@@ -51,6 +51,7 @@ struct evict_handle {
   bool fallback = false;      // Q-Filters without calibrated filters: key-SVD fallback
   bool frozen = false;        // fallback: the per-(b, h) filters have been estimated
   cudaStream_t stream = nullptr;
+  unsigned long long captured = 0;   // the last capture that holds work of this handle (0: none)
 
   void* arena = nullptr;      // one device allocation, carved below
   size_t arena_bytes = 0;
@@ -99,6 +100,10 @@ extern std::atomic<long long> g_launches;
 
 int fail(int code, const char* fmt, ...);
 int cuda_fail(cudaError_t e, const char* what);
+// The capture that a stream is part of: 0 for none, kUnknownCapture where the runtime does not say (the
+// legacy stream while another one captures). Leaves no error behind.
+constexpr unsigned long long kUnknownCapture = ~0ull;
+unsigned long long capture_of(cudaStream_t st);
 cudaEvent_t take_event(evict_handle* h);
 void fold_events(evict_handle* h);
 

@@ -39,6 +39,16 @@ int cuda_fail(cudaError_t e, const char* what) {
   return fail(EVICT_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+unsigned long long capture_of(cudaStream_t st) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  if (cudaStreamGetCaptureInfo(st, &status, &id) != cudaSuccess) {
+    cudaGetLastError();
+    return kUnknownCapture;
+  }
+  return status == cudaStreamCaptureStatusNone ? 0 : status == cudaStreamCaptureStatusActive ? id : kUnknownCapture;
+}
+
 const char* const kKernelNames[kKidCount] = {
     "score", "score_append", "select", "compact", "calib_gram", "calib_eig",
     "curdkv_lse", "curdkv_lse_merge", "curdkv_colsum", "curdkv_colsum_merge", "curdkv_gram", "curdkv_eig", "curdkv_leverage",
@@ -310,6 +320,12 @@ int per_token_update(evict_handle* h, const void* k, const void* v, const int32_
 
 // `device`: k, v (and pos) are read by the kernels directly, so they must be
 // aligned for 16-byte vector and TMA loads (4 bytes for positions).
+// Work of these handles (of one stream) is about to be enqueued: remember the capture that takes it in.
+void note_capture(evict_handle* const* hs, int n) {
+  if (const unsigned long long id = capture_of(hs[0]->stream))
+    for (int l = 0; l < n; ++l) hs[l]->captured = id;
+}
+
 int check_update_args(const evict_handle* h, const void* k, const void* v, const int32_t* pos, int m, bool device) {
   if (!h) return fail(EVICT_EINVAL, "handle is NULL");
   if (m < 0) return fail(EVICT_EINVAL, "m must be >= 0 (got %d)", m);
@@ -394,6 +410,7 @@ int evict_update_and_fetch(evict_handle* h, const void* k, const void* v, const 
   int rc = check_update_args(h, k, v, pos, m, true);
   if (rc) return rc;
   if (m > 0) {
+    note_capture(&h, 1);
     if (attention_family(h->cfg.method)) {
       rc = h->cfg.per_token && m > 1 ? per_token_update(h, k, v, pos, m) : curdkv_update(h, k, v, pos, m);
     } else {
@@ -420,6 +437,7 @@ int evict_update_and_fetch_group(evict_handle* const* hs, int n_layers, const vo
   }
   if (attention_family(hs[0]->cfg.method)) return fail(EVICT_EINVAL, "grouped update supports KNorm and Q-Filters");
   if (m > 0) {
+    note_capture(hs, n_layers);
     int rc = run_intrinsic(hs, n_layers, k, v, pos, m);
     if (rc) return rc;
   }
@@ -509,6 +527,7 @@ int evict_set_state(evict_handle* h, const void* k, const void* v, const int32_t
   const size_t row = kHeadDim * h->elem;
   cudaError_t e;
   if (n > 0) {
+    note_capture(&h, 1);
     if ((e = cudaMemcpy2DAsync(h->kst, h->cap * row, k, n * row, n * row, bh, cudaMemcpyDeviceToDevice,
                                h->stream)) != cudaSuccess)
       return cuda_fail(e, "loading k");
@@ -572,19 +591,22 @@ int evict_sync(evict_handle* h) {
 void evict_destroy(evict_handle* h) {
   if (!h) return;
   // A garbage collector may call this while any stream captures a graph: waiting and freeing would end
-  // the capture with an error unless this thread says that they are no part of it.
+  // the capture with an error unless this thread says that they are no part of it. Waiting for a stream
+  // that captures ends its capture all the same, which is done where the graph holds this handle's work.
+  // (Otherwise freeing waits for what the stream was given before.)
   cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
   cudaThreadExchangeStreamCaptureMode(&mode);
-  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(h->stream, &capturing) == cudaSuccess && capturing == cudaStreamCaptureStatusNone)
-    cudaStreamSynchronize(h->stream);
+  const unsigned long long capture = capture_of(h->stream);
+  if (capture == 0 || (capture == h->captured && capture != kUnknownCapture)) {
+    if (cudaStreamSynchronize(h->stream) != cudaSuccess && capture) cudaGetLastError();
+  }
   for (auto& r : h->pending) {
     cudaEventDestroy(r.start);
     cudaEventDestroy(r.stop);
   }
   for (auto ev : h->event_pool) cudaEventDestroy(ev);
   if (h->copy_stream) {
-    cudaStreamSynchronize(h->copy_stream);
+    if (cudaStreamSynchronize(h->copy_stream) != cudaSuccess && capture) cudaGetLastError();
     cudaEventDestroy(h->stage_ready);
     cudaEventDestroy(h->stage_free);
     cudaStreamDestroy(h->copy_stream);
@@ -661,6 +683,7 @@ int evict_qfilters_filters(evict_handle* h, float* out_host, int* n_rows) {
 int evict_curdkv_scores(evict_handle* h, float* attn, float* leverage, int* n_rows) {
   if (!h || !n_rows) return fail(EVICT_EINVAL, "handle and n_rows must not be NULL");
   if (!attention_family(h->cfg.method)) return fail(EVICT_EINVAL, "not a CurDKV or H2O cache");
+  note_capture(&h, 1);
   return curdkv_last_scores(h, attn, leverage, n_rows);
 }
 
