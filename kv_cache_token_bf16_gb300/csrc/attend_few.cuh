@@ -235,14 +235,17 @@ __device__ __forceinline__ void few_rows(const AttendParams& p, FewShared& sh, c
           for (int k = 0; k < 4; ++k) z[j][k] = ex2(z[j][k] - (k < 2 ? m0 : m1));
           sum[0] += z[j][0] + z[j][1];
           sum[1] += z[j][2] + z[j][3];
-          // weights as bf16 pairs hi + lo: 16 bits of each, so that their rounding does not add to the
-          // output's own (the tensor cores wait for memory here anyway)
+          // weights as bf16 pairs hi + lo, within 2^-15 of each, so that their rounding does not add to the
+          // output's own (the tensor cores wait for memory here anyway). Both meet a V that may be infinite:
+          // hi is cut off, not rounded, so that lo is not negative, and lo is 0 only where the weight is
+          // (otherwise 2^-133 at least, bf16's least).
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float a = z[j][2 * k], b = z[j][2 * k + 1];
-            const uint32_t h2 = pack_bf16(a, b);
+            const uint32_t h2 = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
             hi[2 * j + k] = h2;
-            lo[2 * j + k] = pack_bf16(a - __uint_as_float(h2 << 16), b - __uint_as_float(h2 & 0xffff0000u));
+            lo[2 * j + k] = __vmaxu2(pack_bf16(a - __uint_as_float(h2 << 16), b - __uint_as_float(h2 & 0xffff0000u)),
+                                     __vminu2(h2, 0x00010001u));
           }
         }
         // V of rows behind the stream's end may hold anything: zeros in its place

@@ -1,4 +1,6 @@
 """Calls around pages and attention that a user may make and that the ordinary cases leave out."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -87,3 +89,30 @@ def test_kept_rows_attended_to_in_a_captured_graph():
         torch.cuda.synchronize()
         check({"q": q, "prefix": (k2, v), "new": None}, out, lse)
     cache.close()
+
+
+@pytest.mark.parametrize("hq,m,n_prefix", [(4, 1, 60), (4, 3, 60), (40, 3, 60), (400, 3, 60), (50, 3, 2100)],
+                         ids=["few-1", "few", "wide", "joint", "shared"])
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
+def test_values_that_every_query_sees_may_be_infinite(hq, m, n_prefix, value):
+    # in the prefix and in own rows, of the largest weight, small ones and one in between: the result is
+    # that infinity, wherever the row lies in its box or tile, and finite columns are untouched
+    lens = [m, 90, 40]
+    s = make(520, 3, hq, 2, m, n_prefix, 1, 16, lens)
+    k, v = s["prefix"]
+    k[0, :, 5] = s["q"][0, 0, 0]                           # a large logit for some, a small one for others
+    want, _ = attend(s)
+    cols = {}
+    for i, row in enumerate((0, 5, 17, n_prefix - 1)):
+        v[0, :, row, 3 * i] = value
+        cols[3 * i] = (0, 1, 2)
+    for i, (b, row) in enumerate(((1, 0), (1, 33), (2, 3))):
+        s["vp"][int(s["table"][b, row // 16]), :, row % 16, 50 + i] = value
+        cols[50 + i] = (b,)
+    got, _ = attend(s)
+    hit = torch.zeros(3, D, dtype=torch.bool, device="cuda")
+    for c, bs in cols.items():
+        hit[list(bs), c] = True
+    hit = hit[:, None, None].expand_as(got)
+    assert bool((got[hit] == value).all() if value == value else got[hit].isnan().all())
+    assert torch.equal(got[~hit], want[~hit])
