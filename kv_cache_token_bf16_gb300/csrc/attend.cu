@@ -279,8 +279,7 @@ constexpr int kFewCost = 300, kWideCostTwo = 4400, kWideCostAlt = 2600;
 // eight sequences 60.7 instead of 57.3.)
 constexpr int kFewEntry = 2, kWideEntry = 3;
 
-// Sizes alone decide: lens and n_new are the device's.
-int make_plan(const evict_attention* a, Plan* out) {
+int check_sizes(const evict_attention* a) {
   if (!a) return fail(EVICT_EINVAL, "the arguments are NULL");
   if (a->batch < 0 || a->m < 0) return fail(EVICT_EINVAL, "batch and m must be >= 0 (got %d, %d)", a->batch, a->m);
   if (a->n_q_heads < 1 || a->n_kv_heads < 1 || a->n_q_heads % a->n_kv_heads)
@@ -292,6 +291,12 @@ int make_plan(const evict_attention* a, Plan* out) {
   if (a->n_prefix < 0 || a->n_prefix > (1 << 30)) return fail(EVICT_EINVAL, "n_prefix must be in [0, 2^30]");
   if (a->n_prefix > 0 && (a->prefix_batch < 1 || a->batch % a->prefix_batch))
     return fail(EVICT_EINVAL, "prefix_batch (%d) must divide batch (%d)", a->prefix_batch, a->batch);
+  return EVICT_OK;
+}
+
+// Sizes alone decide: lens and n_new are the device's.
+int make_plan(const evict_attention* a, Plan* out) {
+  if (const int rc = check_sizes(a)) return rc;
   Plan& P = *out;
   P = Plan();
   if (a->batch == 0 || a->m == 0) return EVICT_OK;
@@ -395,6 +400,11 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
   }
   if (a->batch > 0 && a->m > 0)
     if ((rc = check_rows(a->q, a->n_q_heads, "q")) || (rc = check_rows(a->out, a->n_q_heads, "out"))) return rc;
+  if ((rc = check_sizes(a))) return rc;
+  if (a->batch > 0 && a->m > 0) {
+    if (a->out.data == a->q.data) return fail(EVICT_EINVAL, "out must not be q: queries are read while results are written");
+    if (rows_overlap(a->out, a->batch, a->m)) return fail(EVICT_EINVAL, "out: rows lie on top of each other");
+  }
   Plan plan;
   if ((rc = make_plan(a, &plan))) return rc;
   if (a->batch == 0 || a->m == 0) return EVICT_OK;

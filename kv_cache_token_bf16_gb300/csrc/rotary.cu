@@ -338,6 +338,14 @@ int check_tensor(const evict_rows* x, int elem, const char* name) {
   return EVICT_OK;
 }
 
+int check_output(const evict_rows* x, const evict_rows* in, int elem, const char* name) {
+  if (const int rc = check_tensor(x, elem, name)) return rc;
+  if (x->heads != in->heads) return fail(EVICT_EINVAL, "%s has %d heads, its input %d", name, x->heads, in->heads);
+  if (x->data == in->data && (x->stride_b != in->stride_b || x->stride_h != in->stride_h || x->stride_m != in->stride_m))
+    return fail(EVICT_EINVAL, "an output in place must have its input's strides");
+  return EVICT_OK;
+}
+
 int check_common(int dtype, int batch, int m, const int32_t* pos) {
   if (dtype != EVICT_BF16 && dtype != EVICT_FP32) return fail(EVICT_EINVAL, "unknown dtype %d", dtype);
   if (batch < 0 || m < 0) return fail(EVICT_EINVAL, "batch and m must be >= 0 (got %d, %d)", batch, m);
@@ -357,10 +365,14 @@ void set_tensor(RowsParams& P, const evict_rows& x, const evict_rows* out, bool 
   t.rotate = rotate;
 }
 
+int check_size(const RowsParams& P) {
+  const long long rows = (long long)P.batch * P.m * P.heads;
+  if (rows >= (1ll << 31)) return fail(EVICT_ELIMIT, "batch * m * heads = %lld rows are 2^31 or more", rows);
+  return EVICT_OK;
+}
+
 int run_rows(RowsParams& P, bool vec, bool paged, int dtype, cudaStream_t st) {
   const long long tokens = (long long)P.batch * P.m;
-  if (tokens * P.heads >= (1ll << 31))
-    return fail(EVICT_ELIMIT, "batch * m * heads = %lld rows are 2^31 or more", tokens * P.heads);
   P.tokens = (unsigned)tokens;
   // A block a token while that is no more than two blocks an SM: a decode step of 32 sequences takes 3.2 us so, and
   // 4.8 with kTokens. With many tokens the other way round: 8,192 tokens 26.0 us with one and 22.8 with kTokens.
@@ -380,6 +392,41 @@ int run_rows(RowsParams& P, bool vec, bool paged, int dtype, cudaStream_t st) {
 }
 
 }  // namespace
+
+bool rows_overlap(const evict_rows& x, int batch, int m) {
+  struct Dim {
+    long long n, s;
+  };
+  Dim d[3];
+  int dims = 0;
+  for (const Dim& e : {Dim{batch, x.stride_b}, Dim{x.heads, x.stride_h}, Dim{m, x.stride_m}}) {
+    if (e.n <= 1) continue;
+    if (e.s == 0) return true;
+    d[dims++] = e;
+  }
+  auto size = [](long long v) { return v < 0 ? -(__int128)v : (__int128)v; };
+  // ordinary layouts: each stride steps over all that the smaller ones reach
+  std::sort(d, d + dims, [&](const Dim& a, const Dim& b) { return size(a.s) < size(b.s); });
+  __int128 reach = kHeadDim;
+  bool nested = true;
+  for (int i = 0; i < dims; ++i) {
+    nested = nested && size(d[i].s) >= reach;
+    reach += size(d[i].s) * (d[i].n - 1);
+  }
+  if (nested) return false;
+  // others: two rows lie i, j, k steps apart, with less than a row between them. i and j go through the
+  // shorter axes (at most some 2^20 pairs), k is what brings the third nearest.
+  for (int i = dims; i < 3; ++i) d[i] = Dim{1, 1};
+  std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.n < b.n; });
+  for (long long i = 0; i < d[0].n; ++i)
+    for (long long j = i ? 1 - d[1].n : 0; j < d[1].n; ++j) {
+      const __int128 at = (__int128)i * d[0].s + (__int128)j * d[1].s;
+      const __int128 near = -at / d[2].s;
+      for (__int128 k = near - 1; k <= near + 1; ++k)
+        if (size((long long)k) < d[2].n && (i || j || k) && at + k * d[2].s < kHeadDim && at + k * d[2].s > -kHeadDim) return true;
+    }
+  return false;
+}
 
 int check_pages(const evict_pages* g) {
   if (!g) return fail(EVICT_EINVAL, "pages is NULL");
@@ -457,17 +504,15 @@ extern "C" int evict_rotate(const evict_rotary* r, int dtype, int batch, int m, 
   P.rot = r->t;
   bool vec = r->t.half % 8 == 0;
   for (int i = 0; i < n_tensors; ++i) {
-    if ((rc = check_tensor(&x[i], elem, "x")) || (rc = check_tensor(&out[i], elem, "out"))) return rc;
-    if (x[i].heads != out[i].heads)
-      return fail(EVICT_EINVAL, "tensor %d has %d heads and its output %d", i, x[i].heads, out[i].heads);
-    if (x[i].data == out[i].data && (x[i].stride_b != out[i].stride_b || x[i].stride_h != out[i].stride_h ||
-                                     x[i].stride_m != out[i].stride_m))
-      return fail(EVICT_EINVAL, "an output in place must have its input's strides");
+    if ((rc = check_tensor(&x[i], elem, "x")) || (rc = check_output(&out[i], &x[i], elem, "out"))) return rc;
     vec = vec && rows_aligned(x[i], elem, 16) && rows_aligned(out[i], elem, 16);
     set_tensor(P, x[i], &out[i], true);
   }
   P.batch = batch;
   P.m = m;
+  if ((rc = check_size(P))) return rc;
+  for (int i = 0; i < n_tensors; ++i)
+    if (rows_overlap(out[i], batch, m)) return fail(EVICT_EINVAL, "out: rows lie on top of each other");
   P.pos = pos;
   P.pos_base = pos_base;
   P.transpose = transpose;
@@ -494,16 +539,14 @@ extern "C" int evict_paged_append(const evict_pages* g, int batch, int m, const 
   set_tensor(P, *k, nullptr, r != nullptr);
   set_tensor(P, *v, nullptr, false);
   if (q) {
-    if ((rc = check_tensor(q, elem, "q")) || (rc = check_tensor(q_out, elem, "q_out"))) return rc;
-    if (q->heads != q_out->heads) return fail(EVICT_EINVAL, "q has %d heads and q_out %d", q->heads, q_out->heads);
-    if (q->data == q_out->data &&
-        (q->stride_b != q_out->stride_b || q->stride_h != q_out->stride_h || q->stride_m != q_out->stride_m))
-      return fail(EVICT_EINVAL, "an output in place must have its input's strides");
+    if ((rc = check_tensor(q, elem, "q")) || (rc = check_output(q_out, q, elem, "q_out"))) return rc;
     vec = vec && rows_aligned(*q, elem, 16) && rows_aligned(*q_out, elem, 16);
     set_tensor(P, *q, q_out, r != nullptr);
   }
   P.batch = batch;
   P.m = m;
+  if ((rc = check_size(P))) return rc;
+  if (q && rows_overlap(*q_out, batch, m)) return fail(EVICT_EINVAL, "q_out: rows lie on top of each other");
   P.pos = pos;
   P.pos_base = pos_base;
   P.pages[0] = static_cast<char*>(g->k);

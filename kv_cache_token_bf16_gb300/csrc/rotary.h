@@ -17,6 +17,8 @@ struct RotaryTable {
 };
 
 int check_pages(const evict_pages* pages);
+// Two of a tensor's batch x heads x m rows share an element: no output may have that.
+bool rows_overlap(const evict_rows& x, int batch, int m);
 
 }  // namespace evict
 

@@ -242,3 +242,57 @@ def test_shared_table_rows_and_pages_on_top_of_each_other_are_refused():
 def test_a_handles_stream_needs_a_handle(lib):
     out = ctypes.c_void_p(7)
     assert lib.evict_get_stream(None, ctypes.byref(out)) == EVICT_EINVAL and out.value == 7
+
+
+def sized(heads, b, h, m, data=2 * A):
+    return EvictRows(data, b, h, m, heads)
+
+
+OVERLAPPING = [sized(4, 4096, 0, 128), sized(4, 0, 1024, 128), sized(4, 4096, 1024, 0), sized(4, 4096, 1024, 64),
+               sized(4, 4096, 512, 128), sized(4, 2048, 1024, 128), sized(4, -4096, 1024, -64), sized(4, 1024, 4096, 512),
+               sized(2, 128, 256, 384)]
+# as [2, heads, 8, 128]: token-major, heads within a wider tensor, backwards, and two interleaved by hand
+APART = [sized(4, 4096, 1024, 128), sized(4, 4096, 128, 512), sized(4, 8 * 7 * 128, 128, 7 * 128), sized(4, -4096, -1024, -128),
+         sized(2, 128, 2048, 256), sized(3, 384, 3072, 1 << 40), sized(1, 128, 0, 256), sized(1, 128, 7, 256)]
+
+
+@pytest.mark.parametrize("x", OVERLAPPING + APART, ids=lambda x: f"{x.heads}-{x.stride_b}-{x.stride_h}-{x.stride_m}")
+def test_overlapping_layouts_are_told_from_others(x):
+    # what the refusals below go by, against the addresses themselves
+    seen = set()
+    for b in range(2):
+        for h in range(x.heads):
+            for t in range(8):
+                at = b * x.stride_b + h * x.stride_h + t * x.stride_m
+                seen.add(at)
+    rows_at = sorted(seen)
+    overlap = len(rows_at) < 16 * x.heads or any(b - a < 128 for a, b in zip(rows_at, rows_at[1:]))
+    assert overlap == (x in OVERLAPPING)
+
+
+@pytest.mark.parametrize("out", OVERLAPPING, ids=lambda x: f"{x.heads}-{x.stride_b}-{x.stride_h}-{x.stride_m}")
+def test_outputs_on_top_of_each_other_are_refused(rot, out):
+    n = out.heads
+    refused(EVICT_EINVAL, "on top", binding.evict_rotate, rot.handle, EVICT_BF16, 2, 8, None, 0, 0, rows(heads=n), out, 1, None)
+    same = EvictRows(A, out.stride_b, out.stride_h, out.stride_m, n)      # in place
+    refused(EVICT_EINVAL, "on top", binding.evict_rotate, rot.handle, EVICT_FP32, 2, 8, None, 0, 0, same, same, 1, None)
+    refused(EVICT_EINVAL, "on top", binding.evict_paged_append, pages(), 2, 8, None, rot.handle, None, 0, rows(5 * A),
+            rows(6 * A), rows(heads=n), out, None)
+    if min(out.stride_b, out.stride_h, out.stride_m) >= 0:
+        refused(EVICT_EINVAL, "on top", binding.evict_shared_attention,
+                attention(batch=2, m=8, n_q_heads=n, n_kv_heads=n // 2, q=rows(heads=n), out=out))
+
+
+@pytest.mark.parametrize("out", APART, ids=lambda x: f"{x.heads}-{x.stride_b}-{x.stride_h}-{x.stride_m}")
+def test_other_outputs_get_further(rot, out):
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses would reach a GPU")
+    with pytest.raises(binding.EvictError) as e:
+        binding.evict_rotate(rot.handle, EVICT_BF16, 2, 8, None, 0, 0, rows(heads=out.heads), out, 1, None)
+    assert e.value.code == binding.EVICT_ECUDA                            # there is no GPU to launch on
+
+
+def test_results_on_top_of_the_queries_are_refused(lib):
+    q = rows(A, heads=8, stride_b=8192)
+    refused(EVICT_EINVAL, "must not be q", binding.evict_shared_attention, attention(q=q, out=q))
