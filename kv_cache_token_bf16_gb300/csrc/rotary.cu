@@ -365,9 +365,11 @@ void set_tensor(RowsParams& P, const evict_rows& x, const evict_rows* out, bool 
   t.rotate = rotate;
 }
 
-int check_size(const RowsParams& P) {
-  const long long rows = (long long)P.batch * P.m * P.heads;
-  if (rows >= (1ll << 31)) return fail(EVICT_ELIMIT, "batch * m * heads = %lld rows are 2^31 or more", rows);
+// Rows of all tensors, whose heads have been checked one by one: no product or sum here passes 2^63.
+int check_size(int batch, int m, const evict_rows& a, const evict_rows* b, const evict_rows* c) {
+  const long long tokens = (long long)batch * m, heads = (long long)a.heads + (b ? b->heads : 0) + (c ? c->heads : 0);
+  if (tokens >= (1ll << 31) || heads >= (1ll << 31) || tokens * heads >= (1ll << 31))
+    return fail(EVICT_ELIMIT, "batch * m * heads (%lld tokens of %lld heads): 2^31 rows or more", tokens, heads);
   return EVICT_OK;
 }
 
@@ -499,20 +501,20 @@ extern "C" int evict_rotate(const evict_rotary* r, int dtype, int batch, int m, 
   if (n_tensors < 1 || n_tensors > 2 || !x || !out) return fail(EVICT_EINVAL, "need 1 or 2 tensors (got %d)", n_tensors);
   if (batch == 0 || m == 0) return EVICT_OK;
   const int elem = dtype == EVICT_BF16 ? 2 : 4;
+  for (int i = 0; i < n_tensors; ++i)
+    if ((rc = check_tensor(&x[i], elem, "x")) || (rc = check_output(&out[i], &x[i], elem, "out"))) return rc;
+  if ((rc = check_size(batch, m, x[0], n_tensors > 1 ? &x[1] : nullptr, nullptr))) return rc;
   RowsParams P;
   memset(&P, 0, sizeof(P));
   P.rot = r->t;
   bool vec = r->t.half % 8 == 0;
   for (int i = 0; i < n_tensors; ++i) {
-    if ((rc = check_tensor(&x[i], elem, "x")) || (rc = check_output(&out[i], &x[i], elem, "out"))) return rc;
+    if (rows_overlap(out[i], batch, m)) return fail(EVICT_EINVAL, "out: rows lie on top of each other");
     vec = vec && rows_aligned(x[i], elem, 16) && rows_aligned(out[i], elem, 16);
     set_tensor(P, x[i], &out[i], true);
   }
   P.batch = batch;
   P.m = m;
-  if ((rc = check_size(P))) return rc;
-  for (int i = 0; i < n_tensors; ++i)
-    if (rows_overlap(out[i], batch, m)) return fail(EVICT_EINVAL, "out: rows lie on top of each other");
   P.pos = pos;
   P.pos_base = pos_base;
   P.transpose = transpose;
@@ -532,6 +534,11 @@ extern "C" int evict_paged_append(const evict_pages* g, int batch, int m, const 
   if ((rc = check_tensor(k, elem, "k")) || (rc = check_tensor(v, elem, "v"))) return rc;
   if (k->heads != g->n_kv_heads || v->heads != g->n_kv_heads)
     return fail(EVICT_EINVAL, "k and v have %d and %d heads, the pages %d", k->heads, v->heads, g->n_kv_heads);
+  if (q) {
+    if ((rc = check_tensor(q, elem, "q")) || (rc = check_output(q_out, q, elem, "q_out"))) return rc;
+  }
+  if ((rc = check_size(batch, m, *k, v, q))) return rc;
+  if (q && rows_overlap(*q_out, batch, m)) return fail(EVICT_EINVAL, "q_out: rows lie on top of each other");
   RowsParams P;
   memset(&P, 0, sizeof(P));
   if (r) P.rot = r->t;
@@ -539,14 +546,11 @@ extern "C" int evict_paged_append(const evict_pages* g, int batch, int m, const 
   set_tensor(P, *k, nullptr, r != nullptr);
   set_tensor(P, *v, nullptr, false);
   if (q) {
-    if ((rc = check_tensor(q, elem, "q")) || (rc = check_output(q_out, q, elem, "q_out"))) return rc;
     vec = vec && rows_aligned(*q, elem, 16) && rows_aligned(*q_out, elem, 16);
     set_tensor(P, *q, q_out, r != nullptr);
   }
   P.batch = batch;
   P.m = m;
-  if ((rc = check_size(P))) return rc;
-  if (q && rows_overlap(*q_out, batch, m)) return fail(EVICT_EINVAL, "q_out: rows lie on top of each other");
   P.pos = pos;
   P.pos_base = pos_base;
   P.pages[0] = static_cast<char*>(g->k);

@@ -296,3 +296,17 @@ def test_other_outputs_get_further(rot, out):
 def test_results_on_top_of_the_queries_are_refused(lib):
     q = rows(A, heads=8, stride_b=8192)
     refused(EVICT_EINVAL, "must not be q", binding.evict_shared_attention, attention(q=q, out=q))
+
+
+BIG = 0x7fffffff
+
+
+@pytest.mark.parametrize("batch,m,heads,n", [(BIG, BIG, 4, 1), (1 << 16, 1 << 15, 1, 1), (1 << 30, 1 << 30, 16, 1),
+                                             (1, 1, BIG, 2), (2, 1, 1 << 30, 1), (1, 1, 1 << 30, 2)])
+def test_sizes_whose_product_wraps_are_refused(rot, batch, m, heads, n):
+    x = (EvictRows * 2)(*[EvictRows(A, 0, 0, 0, heads)] * 2)
+    out = (EvictRows * 2)(*[EvictRows(2 * A, 128, 128, 128, heads)] * 2)
+    refused(EVICT_ELIMIT, "2\\^31", binding.evict_rotate, rot.handle, EVICT_BF16, batch, m, None, 0, 0, x, out, n, None)
+    one, q = EvictRows(A, 0, 0, 0, 4), EvictRows(A, 0, 0, 0, heads if n == 1 else BIG - 7)
+    refused(EVICT_ELIMIT, "2\\^31", binding.evict_paged_append, pages(), batch, m, None, rot.handle, None, 0, one, one, q,
+            EvictRows(2 * A, 0, 128, 0, q.heads), None)
