@@ -399,16 +399,18 @@ bool rows_overlap(const evict_rows& x, int batch, int m) {
   struct Dim {
     long long n, s;
   };
+  const Dim axes[3] = {{batch, x.stride_b}, {x.heads, x.stride_h}, {m, x.stride_m}};
+  auto size = [](long long v) { return v < 0 ? -(__int128)v : (__int128)v; };
   Dim d[3];
   int dims = 0;
-  for (const Dim& e : {Dim{batch, x.stride_b}, Dim{x.heads, x.stride_h}, Dim{m, x.stride_m}}) {
+  for (const Dim& e : axes) {                     // axes to step over, by the size of their strides
     if (e.n <= 1) continue;
     if (e.s == 0) return true;
-    d[dims++] = e;
+    int at = dims++;
+    for (; at > 0 && size(e.s) < size(d[at - 1].s); --at) d[at] = d[at - 1];
+    d[at] = e;
   }
-  auto size = [](long long v) { return v < 0 ? -(__int128)v : (__int128)v; };
   // ordinary layouts: each stride steps over all that the smaller ones reach
-  std::sort(d, d + dims, [&](const Dim& a, const Dim& b) { return size(a.s) < size(b.s); });
   __int128 reach = kHeadDim;
   bool nested = true;
   for (int i = 0; i < dims; ++i) {

@@ -20,7 +20,9 @@ A decode step behind a shared prompt that an ``EvictCache`` of batch 1 has absor
 
 Work goes on the current stream of the tensors' device; nothing is synchronised. Tensors are
 [batch, heads, m, 128] with any strides whose innermost is 1, so a projection's
-[batch, m, heads, 128] is passed as ``x.transpose(1, 2)``.
+[batch, m, heads, 128] is passed as ``x.transpose(1, 2)``. The calls are not part of autograd:
+tensors that require a gradient are refused while gradients are recorded (the gradient of ``rotate``
+is ``rotate(..., transpose=True)``).
 """
 from __future__ import annotations
 
@@ -40,12 +42,14 @@ assert _ROWS.size == ctypes.sizeof(EvictRows) and _ATTENTION.size == ctypes.size
 
 _torch = None
 _calls = None
+_recording = None                                # torch.is_grad_enabled
 
 
 def _load():
     """torch, and the library's calls with packed structs as arguments."""
-    global _torch, _calls
+    global _torch, _calls, _recording
     import torch
+    _recording = torch.is_grad_enabled
     lib = binding.load()
     calls = ctypes.CDLL(lib._name)               # function objects of their own: other argument types
     p, i, q = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
@@ -73,6 +77,11 @@ def _device(t):
     if index < 0:
         raise ValueError("tensors must be on a CUDA device")
     return index
+
+
+def _no_history():
+    """Of tensors that require a gradient, which would be lost without a word."""
+    raise ValueError("no gradient is recorded for this call: make it under torch.no_grad(), or of detached tensors")
 
 
 def _rows(t, name, index, dtype, batch, m, heads=None):
@@ -200,6 +209,10 @@ def rotate(rotary: Rotary, x, pos=None, pos_base: int = 0, out=None, transpose: 
     n = len(xs)
     if not 1 <= n <= 2 or (outs is not None and len(outs) != n):
         raise ValueError("one or two tensors, and as many outputs")
+    if _recording():
+        for t in xs + outs if outs else xs:
+            if t.requires_grad:
+                _no_history()
     first = xs[0]
     index, dtype, shape = _device(first), first.dtype, first.shape
     if len(shape) != 4:
@@ -249,6 +262,10 @@ def shared_attention(q, prefix=None, pages: "PagedCache | None" = None, n_new=No
     """
     if _torch is None:
         _load()
+    k, v = prefix if prefix is not None else (None, None)
+    if _recording() and (q.requires_grad or (out is not None and out.requires_grad) or
+                         (k is not None and (k.requires_grad or v.requires_grad))):
+        _no_history()
     index, shape = _device(q), q.shape
     if len(shape) != 4:
         raise ValueError(f"q must be [batch, heads, m, {HEAD_DIM}], not {tuple(shape)}")
@@ -271,7 +288,6 @@ def shared_attention(q, prefix=None, pages: "PagedCache | None" = None, n_new=No
         hkv, pages_at, error, width, page = pages.n_kv_heads, pages.address, pages.error_at, pages.width, pages.page_size
     pk = pv = sb = sh = n = groups = 0
     if prefix is not None:
-        k, v = prefix
         ks = k.shape
         if k.dtype is not bf16 or v.dtype is not bf16 or len(ks) != 4 or ks[3] != HEAD_DIM or ks != v.shape:
             raise ValueError(f"the prefix must be two bf16 tensors [prefix_batch, n_kv_heads, n, {HEAD_DIM}]")
@@ -336,6 +352,8 @@ class PagedCache:
         given = [x is not None for x in (k_pages, v_pages, table, lens)]
         if any(given) and not all(given):
             raise ValueError("k_pages, v_pages, table and lens go together")
+        if _recording() and any(given) and (k_pages.requires_grad or v_pages.requires_grad):
+            _no_history()
         self._free = self._rows = None
         if not any(given):
             if min(n_pages or 0, page_size or 0, n_kv_heads or 0, batch or 0, max_rows or 0) < 1:
@@ -424,6 +442,9 @@ class PagedCache:
         index in the sequence; values are copied. q [batch, n_q_heads, m, 128] is rotated alike
         in the same launch, into q_out (q itself: in place; None: a new tensor). Returns q_out.
         """
+        if _recording() and (k.requires_grad or v.requires_grad or (q is not None and q.requires_grad) or
+                             (q_out is not None and q_out.requires_grad)):
+            _no_history()
         index, dtype, batch = self.index, self.k_pages.dtype, self.batch
         shape = k.shape
         m = shape[2] if len(shape) == 4 else -1

@@ -310,3 +310,24 @@ def test_sizes_whose_product_wraps_are_refused(rot, batch, m, heads, n):
     one, q = EvictRows(A, 0, 0, 0, 4), EvictRows(A, 0, 0, 0, heads if n == 1 else BIG - 7)
     refused(EVICT_ELIMIT, "2\\^31", binding.evict_paged_append, pages(), batch, m, None, rot.handle, None, 0, one, one, q,
             EvictRows(2 * A, 0, 128, 0, q.heads), None)
+
+
+def test_tensors_that_require_a_gradient_are_refused(lib):
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(1, 2, 3, 128)
+    w = x.clone().requires_grad_()
+    rot, h = paged.Rotary(), w.bfloat16()
+    cache = paged.PagedCache.__new__(paged.PagedCache)      # refused before anything of it is looked at
+    for call in (lambda a, b: paged.rotate(rot, a), lambda a, b: paged.rotate(rot, (b, a)),
+                 lambda a, b: paged.rotate(rot, b, out=a), lambda a, b: paged.shared_attention(a, prefix=(b, b)),
+                 lambda a, b: paged.shared_attention(b, prefix=(b, a)), lambda a, b: paged.shared_attention(b, prefix=(b, b), out=a),
+                 lambda a, b: cache.append(a, b), lambda a, b: cache.append(b, a), lambda a, b: cache.append(b, b, q=a),
+                 lambda a, b: cache.append(b, b, q=b, q_out=a),
+                 lambda a, b: paged.PagedCache(k_pages=a, v_pages=b, table=b, lens=b)):
+        for a, b in ((w, x), (h, x.bfloat16())):
+            with pytest.raises(ValueError, match="gradient"):
+                call(a, b)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        paged.rotate(rot, w)
+    with pytest.raises(ValueError, match="CUDA"):
+        paged.rotate(rot, w.detach())
