@@ -396,19 +396,27 @@ class PagedCache:
         if self._free is None:
             raise ValueError("the caller keeps this cache's table and lens")
 
-    def _upload(self, rows):
-        """Table rows and all lens to the device, in stream order."""
+    def _changes(self):
+        """Before grow and release: a graph would replay today's lengths and pages for ever."""
+        self._managed()
+        with _on(self.index):
+            if _torch.cuda.is_current_stream_capturing():
+                raise ValueError("grow and release belong between replays: they cannot be captured")
+
+    def _upload(self, taken):
+        """All lens, and the pages `taken` [(place in the table, page)], to the device in stream order.
+        From pinned memory, which torch hands out again once the copies are through: no wait."""
         torch = _torch
         with _on(self.index):
-            self.lens.copy_(torch.tensor(self._rows, dtype=torch.int32))
-            for b in rows:
-                if self._pages[b]:
-                    self.table[b, :len(self._pages[b])].copy_(torch.tensor(self._pages[b], dtype=torch.int32))
+            self.lens.copy_(torch.tensor(self._rows, dtype=torch.int32, pin_memory=True), non_blocking=True)
+            if taken:
+                places, pages = torch.tensor(taken, dtype=torch.int64, pin_memory=True).to(self.device, non_blocking=True).T
+                self.table.view(-1).scatter_(0, places, pages.to(torch.int32))
 
     def grow(self, n_new):
         """Count n_new (a number, or one for every sequence) new rows in, taking pages for them.
         Raises ValueError, with nothing changed, where the pool or the table has no room."""
-        self._managed()
+        self._changes()
         new = [int(n_new)] * self.batch if isinstance(n_new, int) else [int(n) for n in n_new]
         if len(new) != self.batch or min(new, default=0) < 0:
             raise ValueError("n_new must be one number >= 0 for every sequence")
@@ -417,14 +425,17 @@ class PagedCache:
             raise ValueError(f"a sequence would have more than {self.table.shape[1]} pages")
         if sum(need) > len(self._free):
             raise ValueError(f"{sum(need)} pages needed, {len(self._free)} free")
+        taken = []
         for b, x in enumerate(need):
-            self._pages[b] += [self._free.pop() for _ in range(x)]
+            for _ in range(x):
+                taken.append((b * self.width + len(self._pages[b]), self._free[-1]))
+                self._pages[b].append(self._free.pop())
             self._rows[b] += new[b]
-        self._upload([b for b, x in enumerate(need) if x])
+        self._upload(taken)
 
     def release(self, b: int):
         """Sequence b ends: its pages are free and it has no rows."""
-        self._managed()
+        self._changes()
         self._free += reversed(self._pages[b])
         self._pages[b], self._rows[b] = [], 0
         self._upload([])

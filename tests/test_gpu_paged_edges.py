@@ -116,3 +116,55 @@ def test_values_that_every_query_sees_may_be_infinite(hq, m, n_prefix, value):
     hit = hit[:, None, None].expand_as(got)
     assert bool((got[hit] == value).all() if value == value else got[hit].isnan().all())
     assert torch.equal(got[~hit], want[~hit])
+
+
+def test_growing_waits_for_nothing():
+    # fifty steps of growing and releasing, enqueued behind work that is still running: each takes
+    # effect in its place
+    B, page, width = 6, 16, 5
+    c = paged.PagedCache(n_pages=B * width, page_size=page, n_kv_heads=1, batch=B, max_rows=page * width)
+    stream = torch.cuda.Stream()
+
+    def steps():
+        want, got = [], []
+        for i in range(50):
+            for b in range(B):
+                if c.rows()[b] > page * (width - 2):
+                    c.release(b)
+            c.grow([(i * 7 + b * 5) % 20 for b in range(B)])
+            want.append((c.rows(), [list(p) for p in c._pages]))
+            got.append((c.lens.clone(), c.table.clone()))
+        return want, got
+
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(WAIT)
+        steps()                                     # torch's pinned memory for so many copies at once
+        stream.synchronize()
+        torch.cuda._sleep(40 * WAIT)
+        want, got = steps()
+        assert not stream.query()                   # still asleep: nothing above has waited
+    torch.cuda.synchronize()
+    for (rows, pages), (lens, table) in zip(want, got):
+        assert lens.tolist() == rows
+        for b in range(B):
+            assert table[b, :len(pages[b])].tolist() == pages[b]
+            assert len(pages[b]) == -(-rows[b] // page)
+        used = [p for q in pages for p in q]
+        assert len(used) == len(set(used))
+
+
+def test_growing_cannot_be_captured():
+    c = paged.PagedCache(n_pages=4, page_size=16, n_kv_heads=1, batch=2, max_rows=32)
+    c.grow([3, 17])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    x = torch.zeros(4, device="cuda")
+    with torch.cuda.graph(g):
+        x += 1
+        for call in (lambda: c.grow(1), lambda: c.release(1)):
+            with pytest.raises(ValueError, match="captured"):
+                call()
+    assert c.rows() == [3, 17]
+    g.replay()
+    c.grow(1)
+    assert c.lens.tolist() == c.rows() == [4, 18]
