@@ -331,6 +331,14 @@ def _page_strides(k_pages, table):
     return ps, ts
 
 
+def _kept(i):
+    """A property: one of a cache's tensors."""
+    def same(self, value):
+        if value is not self._tensors[i]:
+            raise AttributeError("the cache holds this tensor's address: write to it in place")
+    return property(lambda self: self._tensors[i], same)
+
+
 class PagedCache:
     """Own rows of a batch of sequences, in pages of a pool.
 
@@ -338,9 +346,9 @@ class PagedCache:
     tensors (zeros, no rows), and ``grow`` / ``release`` hand out the pages; or the caller brings
     ``k_pages``, ``v_pages`` [n_pages, n_kv_heads, page_size, 128] (a page's rows dense, pages any
     stride apart), ``table`` [batch, width] int32 (a row of its own for every sequence, also where
-    they name the same pages) and ``lens`` [batch] int32, and keeps the last two up to date: row j of
-    sequence b is row j % page_size of page table[b, j // page_size], and lens counts a call's new
-    rows before the call.
+    they name the same pages) and ``lens`` [batch] int32, and keeps the last two up to date in place:
+    row j of sequence b is row j % page_size of page table[b, j // page_size], and lens counts a
+    call's new rows before the call.
     """
 
     def __init__(self, n_pages: int | None = None, page_size: int | None = None, n_kv_heads: int | None = None,
@@ -383,13 +391,16 @@ class PagedCache:
         self.batch, self.width = table.shape
         page_stride, table_stride = _page_strides(k_pages, table)
         _like(lens, "lens", (self.batch,), torch.int32, self.index)
-        self.k_pages, self.v_pages, self.table, self.lens = k_pages, v_pages, table, lens
+        self._tensors = k_pages, v_pages, table, lens
         self.error = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.struct = EvictPages(k=k_pages.data_ptr(), v=v_pages.data_ptr(), page_stride=page_stride, n_pages=self.n_pages,
                                  page_size=self.page_size, n_kv_heads=self.n_kv_heads, dtype=_dtype(k_pages.dtype),
                                  table=table.data_ptr(), table_stride=table_stride, table_width=self.width,
                                  lens=lens.data_ptr(), error=self.error.data_ptr())
         self.address, self.error_at = ctypes.addressof(self.struct), self.error.data_ptr()
+
+    # The calls hold these tensors' addresses: they can be written to (``cache.lens += 1``), not replaced.
+    k_pages, v_pages, table, lens = (_kept(i) for i in range(4))
 
     # --- pages ------------------------------------------------------------------------------
     def _managed(self):

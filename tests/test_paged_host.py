@@ -331,3 +331,17 @@ def test_tensors_that_require_a_gradient_are_refused(lib):
         paged.rotate(rot, w)
     with pytest.raises(ValueError, match="CUDA"):
         paged.rotate(rot, w.detach())
+
+
+@pytest.mark.parametrize("name", ["k_pages", "v_pages", "table", "lens"])
+def test_a_caches_tensors_are_written_to_and_not_replaced(name):
+    # the calls go by the addresses of the tensors that the cache was made of
+    torch = pytest.importorskip("torch")
+    cache = paged.PagedCache.__new__(paged.PagedCache)
+    cache._tensors = tuple(torch.zeros(3, dtype=torch.int32) for _ in range(4))
+    before = getattr(cache, name)
+    with pytest.raises(AttributeError, match="in place"):
+        setattr(cache, name, before + 1)
+    cache.lens += 1
+    cache.table[1] = 5
+    assert getattr(cache, name) is before and cache.lens.tolist() == [1, 1, 1] and cache.table.tolist() == [0, 5, 0]
