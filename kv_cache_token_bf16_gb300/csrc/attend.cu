@@ -61,24 +61,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   if (may_wide) wide_teardown(wide);
 }
 
-// Partial results of one output row in one unit: `count` slots from `slot` on, row `row` of each;
-// `twice`: rows row and row + 128 (the wide kernel's two groups took turns).
+// Partial results of one output row in one unit: `count` of them, the first at row `first`, the others
+// `step` rows apart behind it, and all but the first `back` rows before that. `twice`: each is two, half a
+// slot apart (the wide kernel's two groups took turns).
 struct Parts {
   const float2* ml;
   const float* o;
-  int slot, count, rows, row, twice;
-  __device__ size_t at(int k) const { return (size_t)(slot + (k >> twice)) * rows + row + (twice ? (k & 1) * 128 : 0); }
+  long long first;
+  int count, step, back, twice;
+  __device__ size_t at(int k) const {
+    const int i = k >> twice;
+    return first + (long long)i * step - (i ? back : 0) + (twice ? (k & 1) * (step >> 1) : 0);
+  }
   __device__ int parts() const { return count << twice; }
 };
 
-// Row r of block e (its tile, of `rows` rows) and head h.
-__device__ __forceinline__ Parts find_parts(const AttendParams& p, const WorkSet& set, int rows, int e, int h, int r,
-                                            int block_rows) {
+// Row r of block e and head h; twice: see Parts.
+__device__ __forceinline__ Parts find_parts(const AttendParams& p, const WorkSet& set, int e, int h, int r, int twice) {
   const int g0 = set.base[e], per = p.by_hkv.div(set.base[e + 1] - g0), steps = per - set.entry;
   const Shares shares(set);
   const int g = g0 + h * per + set.entry;
-  const int c0 = shares.of(g), c1 = shares.of(g + steps - 1);
-  return Parts{set.part_ml, set.part_o, e * p.hkv + h + c0, c1 - c0 + 1, rows, r, rows == kWideRows && block_rows <= 128};
+  const int c0 = shares.of(g), c1 = shares.of(g + steps - 1), unit = e * p.hkv + h;
+  return Parts{set.part_ml, set.part_o, set.slot_row(unit, c0) + r, c1 - c0 + 1, set.rows_of(unit), 0, twice};
 }
 
 constexpr int kJoinWarps = 8;
@@ -160,7 +164,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) attend_join_kernel(const _
       const WorkSet& set = wide ? p.wide : p.few;
       const int rows = wide ? kWideRows : kRows, tile = wide ? r / kWideRows : r / kRows;
       const int e = part_of == 0 ? s * set.prefix_tiles + tile : set.prefixes * set.prefix_tiles + s * set.seq_tiles + tile;
-      m.add_parts(find_parts(p, set, rows, e, h, r - tile * rows, all - tile * rows), part, kSplit);
+      m.add_parts(find_parts(p, set, e, h, r - tile * rows, wide && all - tile * rows <= kWideRows / 2), part, kSplit);
       sees = true;
     }
   }
@@ -196,7 +200,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_split_kernel(cons
   const QueryRow q = query_row<kWideRows>(p, set, k, row);
   if (!q.real) return;
   Merge m;
-  m.add_parts(Parts{set.part_ml, set.part_o, at.x * p.hkv + h + c - 1, c1 - (c - 1) + 1, kWideRows, row, 0}, 0, 1);
+  m.add_parts(Parts{set.part_ml, set.part_o, (long long)(2 * (c - 1) + 1) * kWideRows + row, c1 - (c - 1) + 1, 2 * kWideRows,
+                    kWideRows, 0}, 0, 1);
   m.write(p, q.b, q.t, h * p.group + q.g, k.pre > 0 || k.len - k.n + q.t >= 0);
 }
 
@@ -239,19 +244,34 @@ struct Plan {
   size_t bytes;
 };
 
-// Room for a kernel's blocks and partial results; sets the set's pointers (from a null base).
-void lay_out(WorkSet& s, int kv_heads, int rows, size_t& off) {
+// Room for a kernel's blocks and partial results of units of up to pre_rows and own_rows rows; sets the
+// set's pointers (from a null base). Wide units of up to half a tile's rows are two groups' that take
+// turns, and leave two rows for each of theirs.
+void lay_out(WorkSet& s, bool wide, int kv_heads, int pre_rows, int own_rows, size_t& off) {
   auto take = [&](size_t bytes) {
     const size_t at = off;
     off += round256(bytes);
     return at;
   };
   if (s.blocks() == 0) return;
-  const size_t slots = (size_t)s.blocks() * kv_heads + s.max_shares;
+  auto rows_of = [&](int rows) {
+    return !wide ? std::min(rows, kFewRows) : rows > kWideRows / 2 ? kWideRows : 2 * rows;
+  };
+  s.pre_units = s.prefixes * s.prefix_tiles * kv_heads;
+  s.pre_rows = rows_of(pre_rows);
+  s.own_rows = rows_of(own_rows);
+  size_t rows = 0;                                // of all slots
+  if (s.joint) {
+    rows = 2 * (size_t)s.max_shares * kWideRows;
+  } else {
+    if (s.prefixes) rows = ((size_t)s.pre_units + s.max_shares) * s.pre_rows;
+    s.own_at = (long long)rows;
+    if (s.seqs) rows += ((size_t)s.seqs * s.seq_tiles * kv_heads + s.max_shares) * s.own_rows;
+  }
   s.base = reinterpret_cast<int*>(take((size_t)(s.blocks() + 2) * sizeof(int)));
   s.start = reinterpret_cast<int2*>(take((size_t)s.max_shares * sizeof(int2)));
-  s.part_ml = reinterpret_cast<float2*>(take(slots * rows * sizeof(float2)));
-  s.part_o = reinterpret_cast<float*>(take(slots * rows * kHeadDim * sizeof(float)));
+  s.part_ml = reinterpret_cast<float2*>(take(rows * sizeof(float2)));
+  s.part_o = reinterpret_cast<float*>(take(rows * kHeadDim * sizeof(float)));
 }
 template <typename T>
 void rebase(T*& x, char* base) { x = reinterpret_cast<T*>(base + reinterpret_cast<size_t>(x)); }
@@ -341,8 +361,8 @@ int make_plan(const evict_attention* a, Plan* out) {
   P.wide.cost = (P.wide.prefixes ? pre_rows : own_rows) > 128 ? kWideCostTwo : kWideCostAlt;
   P.wide.entry = kWideEntry;
   size_t off = kWorkHead + round256((size_t)(a->batch + 1) * sizeof(int));
-  lay_out(P.few, a->n_kv_heads, kRows, off);
-  lay_out(P.wide, a->n_kv_heads, kWideRows, off);
+  lay_out(P.few, false, a->n_kv_heads, pre_rows, own_rows, off);
+  lay_out(P.wide, true, a->n_kv_heads, pre_rows, own_rows, off);
   P.bytes = off;
   return EVICT_OK;
 }

@@ -44,6 +44,10 @@ struct Divisor {
 // work asks for.
 // What a share holds of a unit leaves one partial result, in slot unit +
 // share: from one part to the next either of them goes up, so slots are unique.
+// A slot has the rows that the largest unit of its kind fills; prefixes' slots
+// come first, then the sequences' own, counted anew. Joint units leave one only
+// where a share ends or begins inside a unit: slot 2 share for the part of a unit
+// that began before, 2 share + 1 for one that begins there.
 struct WorkSet {
   int prefixes, prefix_tiles;        // streams of prefixes, blocks of one
   int seqs, seq_tiles;               // streams of sequences: 0 or the batch; blocks of one
@@ -55,9 +59,18 @@ struct WorkSet {
   Divisor by_prefix_tiles, by_seq_tiles;
   int* base;                         // [blocks + 2] first step of every block, their total, the shares' number
   int2* start;                       // [shares] block and step in it where every share begins
-  float2* part_ml;                   // [slots][tile rows] running maximum (base 2) and sum
-  float* part_o;                     // [slots][tile rows][128]
+  int pre_units, pre_rows, own_rows; // units of prefixes; rows of their slots, and of the others'
+  long long own_at;                  // first row of the others' slots
+  float2* part_ml;                   // [rows of all slots] running maximum (base 2) and sum
+  float* part_o;                     // [rows of all slots][128]
   __host__ __device__ int blocks() const { return prefixes * prefix_tiles + seqs * seq_tiles; }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int rows_of(int unit) const { return unit < pre_units ? pre_rows : own_rows; }
+  // First row of the slot of what `share` holds of a unit (not joint).
+  __device__ __forceinline__ long long slot_row(int unit, int share) const {
+    return unit < pre_units ? (long long)(unit + share) * pre_rows : own_at + (long long)(unit - pre_units + share) * own_rows;
+  }
+#endif
 };
 
 struct AttendParams {

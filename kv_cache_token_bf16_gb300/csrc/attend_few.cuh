@@ -304,7 +304,7 @@ __device__ __forceinline__ void few_rows(const AttendParams& p, FewShared& sh, c
       }
 
       // --- the share leaves the unit: its part of the result ---
-      const size_t slot = (size_t)(cur.unit + share) * kRows;
+      const size_t slot = set.slot_row(cur.unit, share);
       const int rows = min(kRows, cur.k.n * p.group - cur.k.tile * kRows);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {

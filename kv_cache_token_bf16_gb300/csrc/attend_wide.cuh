@@ -459,7 +459,9 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
       if (!ok) break;
       const bool whole = set.joint && part.steps == at.k.steps;     // no other part, no other unit for these rows
       const bool write = mine.real && (part.two || part.alt || w == 0);
-      const size_t prow = (size_t)(at.unit + blockIdx.x) * kWideRows + w * kTile + row;
+      // groups that take turns leave a row each, half a slot apart (kTile where both have all steps)
+      const size_t prow = set.joint ? (size_t)(2 * blockIdx.x + (at.step == 0 ? 1 : 0)) * kWideRows + w * kTile + row
+                                    : set.slot_row(at.unit, blockIdx.x) + w * (set.rows_of(at.unit) >> 1) + row;
       const bool sees = at.k.pre > 0 || limit >= 0;
       const int hq = at.h * p.group + mine.g;
       const float inv = sees ? 1.f / sum : 0.f;

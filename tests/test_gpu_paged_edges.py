@@ -1,4 +1,5 @@
 """Calls around pages and attention that a user may make and that the ordinary cases leave out."""
+import ctypes
 import math
 
 import pytest
@@ -168,3 +169,34 @@ def test_growing_cannot_be_captured():
     g.replay()
     c.grow(1)
     assert c.lens.tolist() == c.rows() == [4, 18]
+
+
+def workspace(batch, m, hq, h, n_prefix=0, groups=1, rows=0):
+    a = binding.EvictAttention(batch=batch, m=m, n_q_heads=hq, n_kv_heads=h, n_prefix=n_prefix, prefix_batch=groups)
+    if rows:
+        g = binding.EvictPages(page_size=16, table_width=-(-rows // 16))
+        a.pages = ctypes.pointer(g)
+    return binding.evict_shared_attention_workspace(a)
+
+
+def test_workspace_is_no_more_than_partial_results_need():
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    row = (D + 2) * 4                               # a row of a partial result
+    # long blocks: at most two parts of 256 rows for each SM, however many tokens there are
+    for args in ((8, 8192, 32, 8, 0, 1, 8192), (128, 512, 32, 8, 1024, 2, 600), (1, 8192, 32, 8), (1, 300, 8, 8, 0, 1, 300)):
+        assert workspace(*args) <= 2 * sms * 256 * row + (1 << 20), args
+    # units of 36 rows: two groups' rows of each, not a whole tile
+    assert workspace(4096, 9, 32, 8, 4096, 4096, 64) <= 2 * (4096 * 8 + sms) * 2 * 36 * row + (1 << 20)
+    # one token of each of 4,096 sequences: four rows of each of their 8 heads
+    assert workspace(4096, 1, 32, 8, 0, 1, 4096) <= (4096 * 8 + 12 * sms) * 4 * row + (1 << 20)
+
+
+@pytest.mark.parametrize("hq,h,m,n_prefix,groups", [(36, 4, 4, 2300, 2), (36, 4, 4, 30, 8), (20, 4, 7, 2500, 4), (8, 8, 30, 2300, 1),
+                                                    (8, 2, 32, 2600, 8), (8, 2, 33, 2600, 8), (6, 2, 1, 40, 1), (6, 2, 5, 0, 1)])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_partial_results_of_any_number_of_rows(hq, h, m, n_prefix, groups, ragged):
+    B = 8
+    lens = [m + (b * 211) % 900 for b in range(B)]
+    new = [m if b % 3 == 0 else (b * 5) % (m + 1) for b in range(B)] if ragged else None
+    s = make(530, B, hq, h, m, n_prefix, groups, 32, lens, new)
+    check(s, *attend(s, out=torch.zeros_like(s["q"])))
