@@ -9,8 +9,9 @@
 // F_i = frac(w_i / 2 pi) * 2^64 instead, so the low 64 bits of pos * F_i are
 // the angle's fraction of a turn, off by at most |pos| / 2 units of 2^-64
 // turns; whole turns fall off the top of the integer. Its upper 32 bits, read
-// as a signed number, times 2^-31 are the angle in half turns in [-1, 1),
-// which sincospif takes without a range reduction of its own.
+// as a signed number, times 2^-31 are the angle in half turns in [-1, 1). In fp32
+// whole quarters are taken off before it is rounded: within 0.42 steps of 2^-24
+// radians of the angle (1.6 without).
 //
 // Bound: HBM, every row read once and written once. A block of 128 threads
 // owns two tokens (one where they are few): each thread makes the sine and
@@ -98,7 +99,15 @@ __device__ __forceinline__ void sine_cosine(int32_t turn, float& s, float& c) {
     s = __sinf(a);
     c = __cosf(a);
   } else {
-    sincospif((float)turn * 0x1p-31f, &s, &c);
+    // off to the nearest quarter turn in integers first: what is left has at most 30 bits, of which fp32
+    // drops five in place of seven
+    const uint32_t quarters = ((uint32_t)turn + (1u << 29)) >> 30;
+    float rs, rc;
+    sincospif((float)(int32_t)((uint32_t)turn - (quarters << 30)) * 0x1p-31f, &rs, &rc);
+    s = quarters & 1 ? rc : rs;
+    c = quarters & 1 ? rs : rc;
+    if (quarters & 2) s = -s;
+    if (quarters + 1 & 2) c = -c;
   }
 }
 

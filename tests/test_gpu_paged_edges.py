@@ -200,3 +200,25 @@ def test_partial_results_of_any_number_of_rows(hq, h, m, n_prefix, groups, ragge
     new = [m if b % 3 == 0 else (b * 5) % (m + 1) for b in range(B)] if ragged else None
     s = make(530, B, hq, h, m, n_prefix, groups, 32, lens, new)
     check(s, *attend(s, out=torch.zeros_like(s["q"])))
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_fp32_angles_keep_their_bits_all_around(transpose):
+    """Rows (1, 0) give cosine and sine themselves. The angle's fraction of a turn is cut to 2^-32 (2 pi
+    2^-32 < 0.03 U32 radians) and, less whole quarters, rounded to fp32: at most 2^-27 half turns (pi
+    2^-27 < 0.4 U32). sincospif is within one step of its value, 2 U32 of it at most. The products
+    with 1 and 0 are exact."""
+    u = 2.0 ** -24
+    n = 4096
+    rot = paged.Rotary(2, inv_freq=[1.0])
+    x = torch.zeros(1, 1, n, D, device="cuda")
+    x[..., 0] = 1
+    g = torch.Generator().manual_seed(540)
+    for hi in (1 << 12, 1 << 30):
+        pos = torch.randint(-hi, hi, (1, n), generator=g, dtype=torch.int64).to(torch.int32)
+        got = paged.rotate(rot, x, pos=pos.cuda(), transpose=transpose)[0, 0].double().cpu()
+        a = pos[0].double()
+        c, s = a.cos(), (-a if transpose else a).sin()
+        for v, ref, slope in ((got[:, 0], c, s), (got[:, 1], s, c)):
+            err = (v - ref).abs()
+            assert bool((err <= 0.43 * u * slope.abs() + 2 * u * ref.abs() + 1e-13).all()), float(err.max() / u)
