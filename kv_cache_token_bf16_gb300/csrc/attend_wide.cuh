@@ -16,11 +16,10 @@
 // both the same rows and every other step each (two partial results).
 //
 // The exponent's reference is a row's maximum over the first 32 columns that it
-// sees, rounded up to a whole number, and stays there: later columns are taken
-// against it without a maximum of their own while the sum of 32 of their weights
-// is below 2^12, and it moves to the running maximum (with a read and write of O
-// in tensor memory) where that is passed. It moves by whole numbers, so weights
-// that are bf16 already are not rounded again. Weights, sums and O are relative to it and floating, so the
+// sees, and stays there: later columns are taken against it without a maximum
+// of their own while the sum of 32 of their weights is below 2^12, and it moves
+// to the running maximum (with a read and write of O in tensor memory) where
+// that is passed. Weights, sums and O are relative to it and floating, so the
 // result does not depend on where it stands. Weights enter the product
 // with V as bf16 (half a step: 2^-8 of a weight at most), at twice the rate of
 // the split that the few-row kernel uses; their roundings are independent, so
@@ -593,7 +592,7 @@ __device__ void softmax_group(const AttendParams& p, WideShared& sh, WideCursor 
           float top = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 32; k += 2) top = fmax3(top, y[k], y[k + 1]);
-          const float to = fmaxf(ref, ceilf(top * scale)), f = weight_of(ref, to);
+          const float to = fmaxf(ref, top * scale), f = weight_of(ref, to);
           ref = to;
           sum *= f;
           // O follows once the products before this half step are through

@@ -222,29 +222,3 @@ def test_fp32_angles_keep_their_bits_all_around(transpose):
         for v, ref, slope in ((got[:, 0], c, s), (got[:, 1], s, c)):
             err = (v - ref).abs()
             assert bool((err <= 0.43 * u * slope.abs() + 2 * u * ref.abs() + 1e-13).all()), float(err.max() / u)
-
-
-def test_weights_round_once_where_the_maximum_moves():
-    """Wide kernel: the logits of a tile's first 32 columns are weighed before a far larger one is seen in
-    the next, and their bf16 weights move along. Query n's logits are a, b, c at rows 0, 1, 32 (few bits,
-    so exact) and far lower elsewhere; row 1 alone has a 1 in its column of V. The result is off by the
-    one rounding of its weight, whose bits are those of e^b, by the output's own, and by 2^-16 for the
-    fp32 rest (the logit times log2 e: 2^-24 of up to 29, ex2 2^-22, sums of 64)."""
-    n = 1024
-    g = torch.Generator().manual_seed(550)
-    a, b, c = [(lo + (hi - lo) * torch.rand(n, generator=g)).bfloat16() for lo, hi in ((4, 5), (2, 4), (14, 20))]
-    q = torch.zeros(n, 1, 1, D, dtype=torch.bfloat16)
-    q[:, 0, 0, 0], q[:, 0, 0, 1], q[:, 0, 0, 2], q[:, 0, 0, 3] = a, b, c, 1
-    k = torch.zeros(1, 1, 64, D, dtype=torch.bfloat16)
-    v = torch.zeros_like(k)
-    k[..., 3] = -60
-    for row, e in ((0, 0), (1, 1), (32, 2)):
-        k[0, 0, row] = 0
-        k[0, 0, row, e] = 1
-    v[0, 0, 1, 5] = 1
-    out = paged.shared_attention(q.cuda(), prefix=(k.cuda(), v.cuda()), scale=1.0)[:, 0, 0, 5].double().cpu()
-    a, b, c = a.double(), b.double(), c.double()
-    ref = b.exp() / (a.exp() + b.exp() + c.exp())
-    half = lambda x: 2.0 ** (torch.floor(torch.log2(x)) - 8)
-    bound = half(b.exp()) / b.exp() * ref * (1 + 2.0 ** -7) + half(ref) * (1 + 2.0 ** -7) + 2.0 ** -16 * ref
-    assert bool(((out - ref).abs() <= bound).all()), float(((out - ref).abs() / bound).max())
