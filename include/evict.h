@@ -430,7 +430,13 @@ int evict_pages_status(int32_t* error, void* stream);
  * are padding: their rows of out and lse are left as they were.
  * Either part may be absent: pages = NULL (attention over kept rows only;
  * n_new still marks padding) or n_prefix = 0. Logits, softmax statistics and
- * sums are fp32; the result is rounded once to bf16. Results do not depend on
+ * sums are fp32, and the result is rounded to bf16. The weights that multiply
+ * the values (not those that are summed) have fewer bits: they are within 2^-15
+ * of themselves where a KV head has few query rows, and rounded to bf16, within
+ * 2^-8, where it has many: more than 32 of a sequence for its own rows; for a
+ * prefix more than 32 of all its sequences, or n_prefix * prefix_batch above
+ * 2,048 (above 1,024 with more than 16 query rows). The latter is an error of
+ * 1.2 to 1.4 times that of the result's own rounding. Results do not depend on
  * anything but the arguments (no order of atomics). */
 typedef struct evict_attention {
   int batch, m, n_q_heads, n_kv_heads;
