@@ -359,9 +359,10 @@ void evict_rotary_destroy(evict_rotary* r);
  * one launch: out[i] <- rotation of x[i]. pos [n_axes, batch, m] device int32,
  * or NULL (then every axis has pos_base + t at token t). transpose = 1 turns
  * by the negative angle, with the same scale: the rotation's gradient, and
- * (scale 1) its inverse. Angles are exact to fp32 for every int32 position:
- * they are held as 64-bit fractions of a turn. Arithmetic is fp32, rounded
- * once to `dtype`.
+ * (scale 1) its inverse. Far positions lose nothing: angles are
+ * held as 64-bit fractions of a turn, exact for every int32 position, and meet
+ * sine and cosine within 2^-25 radians (fp32; 2^-21 and their results as well
+ * for bf16). Arithmetic is fp32, rounded once to `dtype`.
  * out[i] may be x[i] itself (same data and strides); otherwise they must not
  * overlap. The rows of one output must not share elements (refused), those of
  * an input may. Rows whose addresses and strides are multiples of 16 bytes, with
@@ -402,7 +403,7 @@ typedef struct evict_pages {
  * prompt: pos_base = the prompt's offset). Values are copied. r = NULL copies
  * the keys, too. q (with q_out; both may be NULL) are the step's queries
  * [batch, q->heads, m, 128], rotated alike in the same launch.
- * Two rows of one call that fall on the same page row leave either of them.
+ * Two rows of one call that fall on the same page row leave elements of either.
  * A table entry outside the pool, or a row outside the table, is skipped and
  * reported through pages->error as kind "index" (EVICT_EDEVICE of
  * evict_pages_status); so are n_new[b] outside [0, m], taken as the nearest
@@ -413,7 +414,9 @@ int evict_paged_append(const evict_pages* pages, int batch, int m, const int32_t
                        const evict_rows* q, const evict_rows* q_out, void* stream);
 
 /* Synchronise `stream`, read `error` (a device word as in evict_pages) and
- * clear it: EVICT_OK, or EVICT_EDEVICE if a kernel has reported an error. */
+ * clear it: EVICT_OK, or EVICT_EDEVICE if a kernel has reported an error. The
+ * word holds the first of them; reports of kernels on other streams that come
+ * while this call clears it count with that one. */
 int evict_pages_status(int32_t* error, void* stream);
 
 /* Attention of a batch over a shared prefix and its own pages (bf16). Query t

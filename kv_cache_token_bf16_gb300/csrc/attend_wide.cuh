@@ -30,7 +30,7 @@
 // the output's error grows from one rounding to the root of two.
 //
 // Measured: 8 sequences of up to 509 questions behind 4,096 rows (32 query
-// heads, 141 GFLOP) 162 us, 0.87 PFLOP/s; a step of 256 query rows takes 3,400
+// heads, 141 GFLOP) 160 us, 0.88 PFLOP/s; a step of 256 query rows takes 3,400
 // clocks, 2,048 of them the products' at the tensor cores' rate. What bounds
 // it there: the first product reads Q from shared memory, 64 clocks for an
 // instruction whatever its width, so halves of 64 columns cost it twice, 3,072

@@ -18,7 +18,8 @@ A decode step behind a shared prompt that an ``EvictCache`` of batch 1 has absor
     own.append(k, v, rotary=rotary, pos_base=prompt.stats()["offset"], q=q, q_out=q)
     out = own.attend(q, prefix=prompt.view()[:2])
 
-Work goes on the current stream of the tensors' device; nothing is synchronised. Tensors are
+Work goes on the current stream of the tensors' device; nothing but ``PagedCache.sync`` waits for it
+(``grow`` and ``release`` copy from pinned memory, which torch has to make the first times). Tensors are
 [batch, heads, m, 128] with any strides whose innermost is 1, so a projection's
 [batch, m, heads, 128] is passed as ``x.transpose(1, 2)``. The calls are not part of autograd:
 tensors that require a gradient are refused while gradients are recorded (the gradient of ``rotate``
