@@ -398,9 +398,9 @@ class EvictCache:
         that is a multiple of the cache's gives every kept prefix to that many sequences.
 
         Work goes on the current stream. Where that is not the cache's, it is ordered behind the
-        cache's last update, and the cache's next one behind it. A graph that another stream captures
-        cannot hold that order: it reads the rows kept when it is replayed, and the replay has to be
-        ordered like any other reader. (A capture of the cache's own stream needs attend under it.)"""
+        cache's last update, and the cache's next one behind it, also inside one graph that captures
+        both streams. A graph that captures the current stream alone cannot hold that order: it reads
+        the rows kept when it is replayed, and the replay has to be ordered like any other reader."""
         import torch
         from . import paged
         here, own = torch.cuda.current_stream(), evict_get_stream(self.handle)
@@ -410,9 +410,10 @@ class EvictCache:
             own = torch.cuda.ExternalStream(own) if own else torch.cuda.default_stream()
             captures = torch.cuda.is_current_stream_capturing()
             with torch.cuda.stream(own):
-                if torch.cuda.is_current_stream_capturing() and not captures:
-                    raise ValueError("the cache's stream is being captured: attend under it")
-            if captures:
+                own_captures = torch.cuda.is_current_stream_capturing()
+            if own_captures and not captures:
+                raise ValueError("the cache's stream is being captured: attend under it")
+            if captures and not own_captures:
                 own = None
             else:
                 here.wait_stream(own)

@@ -92,6 +92,35 @@ def test_kept_rows_attended_to_in_a_captured_graph():
     cache.close()
 
 
+def test_update_and_attention_on_two_streams_of_one_graph():
+    # the cache's stream joins the capture: its update comes before the attention in every replay
+    origin, mine = torch.cuda.Stream(), torch.cuda.Stream()
+    k, v, q = randn(515, 1, 2, 64, D), randn(516, 1, 2, 64, D), randn(517, 3, 4, 1, D)
+    with torch.cuda.stream(mine):
+        cache = binding.EvictCache("knorm", 1, 2, budget=64, max_block=64, n_sink=4, recent=8)
+    out, lse = torch.zeros_like(q), torch.full((3, 4, 1), 7.0, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=origin):
+        mine.wait_stream(origin)
+        with torch.cuda.stream(mine):
+            torch.cuda._sleep(WAIT // 4)
+            cache.update_and_fetch(k, v)
+        cache.attend(q, out=out, lse=lse)
+        with pytest.raises(ValueError, match="under it"):
+            with torch.cuda.stream(torch.cuda.Stream()):
+                cache.attend(q, out=out)                # a third stream, outside the capture
+    for seed in (518, 519):
+        k.copy_(randn(seed, 1, 2, 64, D))
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        check({"q": q, "prefix": (k, v), "new": None}, out, lse)
+    cache.sync()
+    del g
+    cache.close()
+
+
 @pytest.mark.parametrize("hq,m,n_prefix", [(4, 1, 60), (4, 3, 60), (40, 3, 60), (400, 3, 60), (50, 3, 2100)],
                          ids=["few-1", "few", "wide", "joint", "shared"])
 @pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan])
