@@ -359,18 +359,18 @@ void evict_rotary_destroy(evict_rotary* r);
  * one launch: out[i] <- rotation of x[i]. pos [n_axes, batch, m] device int32,
  * or NULL (then every axis has pos_base + t at token t). transpose = 1 turns
  * by the negative angle, with the same scale: the rotation's gradient, and
- * (scale 1) its inverse. Far positions lose nothing: angles are
- * held as 64-bit fractions of a turn, exact for every int32 position, and meet
- * sine and cosine within 2^-25 radians (fp32; 2^-21 and their results as well
- * for bf16). Arithmetic is fp32, rounded once to `dtype`.
+ * (scale 1) its inverse. Far positions lose nothing: angles are held as 64-bit
+ * fractions of a turn, exact for every int32 position, and reach sine and cosine
+ * within 2^-25 radians (bf16: they and their sines within 2^-20). Arithmetic is
+ * fp32, rounded once to `dtype`.
  * out[i] may be x[i] itself (same data and strides); otherwise they must not
  * overlap. The rows of one output must not share elements (refused), those of
  * an input may. Rows whose addresses and strides are multiples of 16 bytes, with
  * rotary_dim a multiple of 16, move in 16-byte pieces; any other layout is
  * taken an element at a time.
  * EVICT_EINVAL: NULL or misaligned pointers, bad sizes, out[i].heads !=
- * x[i].heads, an output's rows on top of each other. EVICT_ELIMIT: batch * m * heads of 2^31 or more. batch or m of
- * 0 is a no-op. */
+ * x[i].heads, an output's rows on top of each other. EVICT_ELIMIT: batch * m *
+ * heads of 2^31 or more. batch or m of 0 is a no-op. */
 int evict_rotate(const evict_rotary* r, int dtype, int batch, int m, const int32_t* pos, int64_t pos_base,
                  int transpose, const evict_rows* x, const evict_rows* out, int n_tensors, void* stream);
 
@@ -466,9 +466,9 @@ typedef struct evict_attention {
 int evict_shared_attention_workspace(const evict_attention* a, size_t* bytes);
 
 /* EVICT_EINVAL: NULL or misaligned pointers, bad sizes or strides, out's rows on top of each other or
- * its data that of q, head counts that do not divide, pages that are not bf16, a workspace that is too small. EVICT_ELIMIT: batch above
- * EVICT_MAX_ATTEND_BATCH, batch * n_q_heads * m of 2^30 or more, or 2^31 or more steps of 16 rows in
- * all, by the tables' width. batch or m of 0 is a no-op.
+ * its data that of q, head counts that do not divide, pages that are not bf16, a workspace that is too
+ * small. EVICT_ELIMIT: batch above EVICT_MAX_ATTEND_BATCH, batch * n_q_heads * m of 2^30 or more, or
+ * 2^31 or more steps of 16 rows in all, by the tables' width. batch or m of 0 is a no-op.
  * Device errors (a table entry outside the pool, read as zeros; lens beyond the table, cut to it;
  * n_new outside [0, m], taken as the nearest of these; a bounded wait that gave up) are reported
  * through `error`. */

@@ -107,7 +107,7 @@ __device__ __forceinline__ void sine_cosine(int32_t turn, float& s, float& c) {
     s = quarters & 1 ? rc : rs;
     c = quarters & 1 ? rs : rc;
     if (quarters & 2) s = -s;
-    if (quarters + 1 & 2) c = -c;
+    if ((quarters + 1) & 2) c = -c;
   }
 }
 
@@ -428,7 +428,7 @@ bool rows_overlap(const evict_rows& x, int batch, int m) {
   }
   if (nested) return false;
   // others: two rows lie i, j, k steps apart, with less than a row between them. i and j go through the
-  // shorter axes (at most some 2^20 pairs), k is what brings the third nearest.
+  // shorter axes (of 2^31 rows at most some 2^21 pairs), k is what brings the third nearest.
   for (int i = dims; i < 3; ++i) d[i] = Dim{1, 1};
   std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.n < b.n; });
   for (long long i = 0; i < d[0].n; ++i)
@@ -436,7 +436,8 @@ bool rows_overlap(const evict_rows& x, int batch, int m) {
       const __int128 at = (__int128)i * d[0].s + (__int128)j * d[1].s;
       const __int128 near = -at / d[2].s;
       for (__int128 k = near - 1; k <= near + 1; ++k)
-        if (size((long long)k) < d[2].n && (i || j || k) && at + k * d[2].s < kHeadDim && at + k * d[2].s > -kHeadDim) return true;
+        if (k < d[2].n && -k < d[2].n && (i || j || k) && at + k * d[2].s < kHeadDim && at + k * d[2].s > -kHeadDim)
+          return true;
     }
   return false;
 }
