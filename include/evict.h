@@ -449,7 +449,7 @@ typedef struct evict_attention {
   float scale;               /* 0 = 1 / sqrt(128) */
   const void* prefix_k;      /* device bf16 [prefix_batch, n_kv_heads, n_prefix, 128], rows 128 apart */
   const void* prefix_v;
-  int64_t prefix_stride_b;   /* elements, multiples of 8 */
+  int64_t prefix_stride_b;   /* elements, multiples of 8, not 0 where there are several */
   int64_t prefix_stride_h;
   int n_prefix;
   int prefix_batch;          /* divides batch */

@@ -417,6 +417,8 @@ extern "C" int evict_shared_attention(const evict_attention* a) {
     if (!multiple(a->prefix_k, 16) || !multiple(a->prefix_v, 16) || a->prefix_stride_b % 8 || a->prefix_stride_h % 8 ||
         a->prefix_stride_b < 0 || a->prefix_stride_h < 0)
       return fail(EVICT_EINVAL, "the prefix must be 16-byte aligned, with strides that are multiples of 8");
+    if ((a->prefix_batch > 1 && a->prefix_stride_b == 0) || (a->n_kv_heads > 1 && a->prefix_stride_h == 0))
+      return fail(EVICT_EINVAL, "prefixes or KV heads in one place (stride 0): say prefix_batch or n_kv_heads 1");
   }
   if (a->batch > 0 && a->m > 0)
     if ((rc = check_rows(a->q, a->n_q_heads, "q")) || (rc = check_rows(a->out, a->n_q_heads, "out"))) return rc;

@@ -255,9 +255,9 @@ def shared_attention(q, prefix=None, pages: "PagedCache | None" = None, n_new=No
     """Attention of q [batch, n_q_heads, m, 128] (bf16) over a shared prefix and own pages.
 
     prefix: (K, V) [prefix_batch, n_kv_heads, n, 128], e.g. ``EvictCache.view()[:2]``; prefix p
-    serves the batch / prefix_batch sequences from p * (batch / prefix_batch) on. pages: a
-    PagedCache whose lens count the m (or n_new[b]) query tokens' own rows, which they see up to
-    their own. ``out`` must not overlap an input (not even q). Padding queries (t >= n_new[b]) leave
+    serves the batch / prefix_batch sequences from p * (batch / prefix_batch) on (one that is expanded
+    over its first axis is read once for all). pages: a PagedCache whose lens count the m (or n_new[b])
+    query tokens' own rows, which they see up to their own. ``out`` must not overlap an input (not even q). Padding queries (t >= n_new[b]) leave
     their rows of ``out`` and ``lse`` as they are; a new ``out`` has zeros there. lse: fp32
     [batch, n_q_heads, m] for the log-sum-exp. Returns out.
     """
@@ -303,6 +303,12 @@ def shared_attention(q, prefix=None, pages: "PagedCache | None" = None, n_new=No
             sb, sh, sn, se = strides
             if v.stride() != strides or se != 1 or (sn != HEAD_DIM and n > 1):
                 raise ValueError("the prefix's rows must be adjacent, K and V with the same strides")
+            if sb == 0 and batch % groups == 0:  # expanded: one prefix for all, read once
+                groups = 1
+            if sh == 0 and hkv > 1:              # expanded: one KV head for all query heads
+                if pages is not None:
+                    raise ValueError("the prefix's heads lie in one place, the pages' do not: repeat them")
+                hkv, sh = 1, n * HEAD_DIM
             pk, pv = k.data_ptr(), v.data_ptr()
     if hkv == 0:
         raise ValueError("neither a prefix nor pages: nothing to attend to")

@@ -251,3 +251,26 @@ def test_fp32_angles_keep_their_bits_all_around(transpose):
         for v, ref, slope in ((got[:, 0], c, s), (got[:, 1], s, c)):
             err = (v - ref).abs()
             assert bool((err <= 0.43 * u * slope.abs() + 2 * u * ref.abs() + 1e-13).all()), float(err.max() / u)
+
+
+@pytest.mark.parametrize("own", [True, False])
+@pytest.mark.parametrize("hq,m", [(4, 1), (40, 1), (300, 2)], ids=["few", "wide", "joint"])
+def test_prefixes_and_heads_expanded_over_an_axis(hq, m, own):
+    # one prefix for every sequence, one head for every KV head, as torch's expand gives them
+    B, h, n = 3, 2, 170
+    s = make(560, B, hq, h, m, n, B, 16, [m + 3, m, m + 40] if own else None)
+    k, v = s["prefix"]
+    for over_b, over_h in ((True, False), (False, True), (True, True)):
+        kk, vv = ((x[:1 if over_b else B, :1 if over_h else h]).expand(B, h, -1, -1) for x in (k, v))
+        s["prefix"] = kk, vv
+        if over_h and own:
+            with pytest.raises(ValueError, match="repeat"):
+                attend(s)
+            continue
+        got, lse = attend(s)
+        s["prefix"] = kk.contiguous(), vv.contiguous()
+        check(s, got, lse)
+        if over_b and not over_h:                   # the very work of one prefix that is given as such
+            s["prefix"] = k[:1], v[:1]
+            want, wl = attend(s)
+            assert torch.equal(got, want) and torch.equal(lse, wl)

@@ -345,3 +345,8 @@ def test_a_caches_tensors_are_written_to_and_not_replaced(name):
     cache.lens += 1
     cache.table[1] = 5
     assert getattr(cache, name) is before and cache.lens.tolist() == [1, 1, 1] and cache.table.tolist() == [0, 5, 0]
+
+
+@pytest.mark.parametrize("kw", [dict(prefix_stride_b=0), dict(prefix_stride_h=0)])
+def test_prefixes_in_one_place_are_refused(lib, kw):
+    refused(EVICT_EINVAL, "in one place", binding.evict_shared_attention, attention(**kw))
