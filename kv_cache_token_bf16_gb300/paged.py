@@ -257,9 +257,9 @@ def shared_attention(q, prefix=None, pages: "PagedCache | None" = None, n_new=No
     prefix: (K, V) [prefix_batch, n_kv_heads, n, 128], e.g. ``EvictCache.view()[:2]``; prefix p
     serves the batch / prefix_batch sequences from p * (batch / prefix_batch) on (one that is expanded
     over its first axis is read once for all). pages: a PagedCache whose lens count the m (or n_new[b])
-    query tokens' own rows, which they see up to their own. ``out`` must not overlap an input (not even q). Padding queries (t >= n_new[b]) leave
-    their rows of ``out`` and ``lse`` as they are; a new ``out`` has zeros there. lse: fp32
-    [batch, n_q_heads, m] for the log-sum-exp. Returns out.
+    query tokens' own rows, which they see up to their own. ``out`` must not overlap an input (not even
+    q). Padding queries (t >= n_new[b]) leave their rows of ``out`` and ``lse`` as they are; a new
+    ``out`` has zeros there. lse: fp32 [batch, n_q_heads, m] for the log-sum-exp. Returns out.
     """
     if _torch is None:
         _load()
