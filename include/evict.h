@@ -48,18 +48,24 @@ typedef enum evict_method {
   EVICT_KNORM = 0,     /* "L2Norm — Intrinsic Key-Norm Eviction", §How it works */
   EVICT_QFILTERS = 1,  /* "Q-Filters — Query-Agnostic Projection Eviction", §How it works */
   EVICT_CURDKV = 2,    /* "CurDKV-adapted — Value-Aware Leverage-Score Eviction", §How it works */
-  EVICT_H2O = 3        /* H2O-adapted: cumulative proxy-attention mass, the softmax of CurDKV's
+  EVICT_H2O = 3,       /* H2O-adapted: cumulative proxy-attention mass, the softmax of CurDKV's
                           step 1 ("CurDKV-adapted", §How it works step 1; a new token starts
                           from exactly 0, §The honesty crux item 4). Per block: query t (the
                           incoming key k+t) attends rows i <= k+t with scale 1/sqrt(D); row i
                           gains the weights of the queries after it (a new row not its own
                           query's weight); kept rows add this to their cumulative score, new
                           rows start from it; the budget highest are kept. bf16 only. */
+  EVICT_ATTENTION = 4  /* accumulated attention weight, of the queries themselves and not of a proxy:
+                          the score of a row is the sum of the softmax weights that queries put
+                          on it. Rows bring a start (evict_update_scored; 0 by default), e.g.
+                          from evict_prompt_weights, and evict_weigh adds a step's weights; the
+                          budget highest are kept. A new row is the lightest at first: `recent`
+                          keeps it until queries have seen it. bf16 only. */
 } evict_method;
 
 typedef enum evict_dtype {
   EVICT_BF16 = 0,
-  EVICT_FP32 = 1       /* KNorm and Q-Filters only (CurDKV and H2O store bf16) */
+  EVICT_FP32 = 1       /* KNorm and Q-Filters only (the others store bf16) */
 } evict_dtype;
 
 /* Compiled bounds (EVICT_ELIMIT above them). */
@@ -116,7 +122,8 @@ typedef struct evict_config {
  * [batch, n_kv_heads, capacity]; rows [0, n_kept) of every (b,h) are valid,
  * in temporal order. pos holds absolute token positions, never renumbered
  * ("Q-Filters", §Adaptation notes). score is the stored fp32 score (KNorm
- * norm, Q-Filters projection, CurDKV cumulative leverage). */
+ * norm, Q-Filters projection, CurDKV cumulative leverage, H2O cumulative mass, accumulated
+ * attention weight). */
 typedef struct evict_view {
   void* k;
   void* v;
@@ -162,6 +169,12 @@ int evict_init(const evict_config* cfg, evict_handle** out);
  * eviction. `out` may be NULL. */
 int evict_update_and_fetch(evict_handle* h, const void* k, const void* v, const int32_t* pos,
                            int m, evict_view* out);
+
+/* The same for a cache of EVICT_ATTENTION whose new rows start from score
+ * [B, H, m] (device fp32, 4-byte aligned; NULL: from 0, as the call above
+ * does). NaN counts as the lowest score. EVICT_EINVAL for other methods. */
+int evict_update_scored(evict_handle* h, const void* k, const void* v, const int32_t* pos,
+                        const float* score, int m, evict_view* out);
 
 /* Grouped update of n_layers (1..32) caches that share every configuration
  * field, their kept-row count, offset and stream — e.g. the layers of one
@@ -474,6 +487,86 @@ int evict_shared_attention_workspace(const evict_attention* a, size_t* bytes);
  * through `error`. */
 int evict_shared_attention(const evict_attention* a);
 #define EVICT_MAX_ATTEND_BATCH 4096
+
+/* --------------------------------------------------------------------------
+ * Prompts, and the weights that attention puts on rows
+ * --------------------------------------------------------------------------
+ * Whole prompts before any cache, and the scores of EVICT_ATTENTION: the
+ * attention leaves every query's log-sum-exp, with which the weights that a
+ * key got are summed afterwards. The calls keep the conventions of the calls
+ * above: a stream each, no allocation, no wait, nothing kept between calls.
+ *
+ * Tokens are the rows of [batch, heads, m, 128] tensors. With `starts` NULL a
+ * sequence is a batch row's m tokens. Otherwise batch is 1 and sequence i the
+ * tokens starts[i] .. starts[i + 1] - 1, one behind the other (some may be
+ * empty); tokens before the first and behind the last are
+ * neither read as numbers nor written. Query t of a sequence and query head g
+ * sees the keys j <= t of its own sequence, with KV head g / (n_q_heads /
+ * n_kv_heads). Rows that a query does not see do not reach its result,
+ * whatever they hold (infinities and NaN included). */
+typedef struct evict_prompt {
+  int batch, m;
+  evict_rows q;              /* bf16; addresses and strides multiples of 16 bytes, strides not negative */
+  evict_rows k;              /* and, where there is more than one row, head or batch row, not 0 */
+  evict_rows v;              /* attention only: heads as k's */
+  evict_rows out;            /* attention only: heads as q's; must not overlap any input */
+  float* lse;                /* device [batch, n_q_heads, m]: written by the attention (or NULL), read by the weights */
+  float* weights;            /* device [batch, n_kv_heads, m]: written by the weights */
+  const int32_t* starts;     /* device [n_seqs + 1], or NULL */
+  int n_seqs;
+  int last;                  /* weights: only the last `last` queries of every sequence count (0 = all) */
+  float scale;               /* 0 = 1 / sqrt(128) */
+  void* workspace;           /* device, 256-byte aligned; in use until the call's work is done */
+  size_t workspace_bytes;    /* at least that of the call's _workspace function */
+  int32_t* error;            /* device word as in evict_pages, or NULL */
+  void* stream;
+} evict_prompt;
+
+#define EVICT_MAX_PROMPT_GROUP 128
+#define EVICT_MAX_PROMPT_SEQS 65536
+
+/* Bytes of workspace that a call with these sizes needs on the current device, whatever `starts` holds:
+ * reads batch, m, the heads of q and k, starts (as NULL or not) and n_seqs. */
+int evict_prompt_attention_workspace(const evict_prompt* a, size_t* bytes);
+int evict_prompt_weights_workspace(const evict_prompt* a, size_t* bytes);
+
+/* out = softmax(scale * q . k) v over the keys that a query sees, lse = the
+ * natural logarithm of the sum of exp(scale * q . k). Logits, softmax
+ * statistics and sums are fp32, the result is rounded to bf16; the weights
+ * that multiply the values (not those that are summed) are rounded to bf16,
+ * within 2^-8. Results depend on nothing but the arguments.
+ * EVICT_EINVAL: NULL or misaligned pointers, bad sizes or strides, heads that
+ * do not divide, out's rows on top of each other or its data that of an input,
+ * a workspace that is too small. EVICT_ELIMIT: more than EVICT_MAX_PROMPT_GROUP
+ * query heads for a KV head or EVICT_MAX_PROMPT_SEQS sequences, batch *
+ * n_q_heads * m of 2^30 or more, or 2^31 or more steps of 128 keys in all.
+ * batch, m or n_seqs of 0 is a no-op. Device errors, reported through `error`:
+ * starts that fall, or leave [0, m] (kind "index": then nothing is written);
+ * a bounded wait that gave up. */
+int evict_prompt_attention(const evict_prompt* a);
+
+/* weights[j] = the sum of exp(scale * q . k[j] - lse) over the KV head's query
+ * heads and the queries that see key j and count (`last`), in fp32. With the
+ * attention's own lse that is the softmax weight that key j got. A query whose
+ * lse is -inf (it saw nothing) has no weights. v and out are not looked at.
+ * Errors as evict_prompt_attention's; last < 0 is EVICT_EINVAL. */
+int evict_prompt_weights(const evict_prompt* a);
+
+/* Add to the scores of a cache of EVICT_ATTENTION the weights that queries put
+ * on its kept rows: score[j] += the sum of exp(scale * q . k[j] - lse) over the
+ * KV head's query heads of the m (or n_new[b]) tokens of the sequences that the
+ * row serves (batch row p of the cache serves the batch / B sequences from
+ * p * (batch / B) on). q [batch, n_q_heads, m, 128] bf16, as in evict_attention
+ * but for strides, which may be any multiples of 16 bytes; lse [batch,
+ * n_q_heads, m] device fp32, as evict_shared_attention leaves it, over whatever
+ * rows the queries saw; n_new [batch] device int32 or NULL. A query whose lse is
+ * -inf has no weights. On `stream`, which the caller orders behind the handle's
+ * last update and before its next one. n_new outside [0, m] counts as the
+ * nearest of these and is reported by evict_sync (EVICT_EDEVICE). EVICT_EINVAL:
+ * another method, NULL or misaligned pointers, bad sizes; EVICT_ELIMIT: batch *
+ * n_q_heads * m of 2^30 or more. No rows or no queries is a no-op. */
+int evict_weigh(evict_handle* h, const evict_rows* q, int batch, int m, const float* lse, const int32_t* n_new,
+                float scale, void* stream);
 
 /* Process-wide count of kernels this library has launched. */
 int64_t evict_launch_count(void);

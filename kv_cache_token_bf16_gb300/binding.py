@@ -17,11 +17,12 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libevict.so")
 
 EVICT_OK, EVICT_EINVAL, EVICT_ELIMIT, EVICT_ECUDA, EVICT_EDEVICE, EVICT_ENUM = range(6)
-EVICT_KNORM, EVICT_QFILTERS, EVICT_CURDKV, EVICT_H2O = range(4)
+EVICT_KNORM, EVICT_QFILTERS, EVICT_CURDKV, EVICT_H2O, EVICT_ATTENTION = range(5)
 EVICT_BF16, EVICT_FP32 = range(2)
 HEAD_DIM = 128
 MAX_GROUP = 32
-METHODS = {"knorm": EVICT_KNORM, "qfilters": EVICT_QFILTERS, "curdkv": EVICT_CURDKV, "h2o": EVICT_H2O}
+METHODS = {"knorm": EVICT_KNORM, "qfilters": EVICT_QFILTERS, "curdkv": EVICT_CURDKV, "h2o": EVICT_H2O,
+           "attention": EVICT_ATTENTION}
 DTYPES = {"bf16": EVICT_BF16, "fp32": EVICT_FP32}
 
 
@@ -79,6 +80,14 @@ class EvictAttention(ctypes.Structure):
                 ("error", ctypes.c_void_p), ("stream", ctypes.c_void_p)]
 
 
+class EvictPrompt(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("m", ctypes.c_int), ("q", EvictRows), ("k", EvictRows), ("v", EvictRows),
+                ("out", EvictRows), ("lse", ctypes.c_void_p), ("weights", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int), ("last", ctypes.c_int), ("scale", ctypes.c_float),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("error", ctypes.c_void_p),
+                ("stream", ctypes.c_void_p)]
+
+
 class EvictError(RuntimeError):
     def __init__(self, code, msg):
         super().__init__(f"libevict error {code}: {msg}")
@@ -92,6 +101,7 @@ _I = ctypes.c_int
 _SIGNATURES = {
     "evict_init": (_I, [ctypes.POINTER(EvictConfig), ctypes.POINTER(_P)]),
     "evict_update_and_fetch": (_I, [_P, _P, _P, _P, _I, ctypes.POINTER(EvictView)]),
+    "evict_update_scored": (_I, [_P, _P, _P, _P, _P, _I, ctypes.POINTER(EvictView)]),
     "evict_update_and_fetch_group": (_I, [ctypes.POINTER(_P), _I, ctypes.POINTER(_P), ctypes.POINTER(_P),
                                           ctypes.POINTER(_P), _I, ctypes.POINTER(EvictView)]),
     "evict_update_and_fetch_host": (_I, [_P, _P, _P, _P, _I, ctypes.POINTER(EvictView)]),
@@ -121,6 +131,11 @@ _SIGNATURES = {
     "evict_pages_status": (_I, [_P, _P]),
     "evict_shared_attention_workspace": (_I, [ctypes.POINTER(EvictAttention), ctypes.POINTER(ctypes.c_size_t)]),
     "evict_shared_attention": (_I, [ctypes.POINTER(EvictAttention)]),
+    "evict_prompt_attention_workspace": (_I, [ctypes.POINTER(EvictPrompt), ctypes.POINTER(ctypes.c_size_t)]),
+    "evict_prompt_weights_workspace": (_I, [ctypes.POINTER(EvictPrompt), ctypes.POINTER(ctypes.c_size_t)]),
+    "evict_prompt_attention": (_I, [ctypes.POINTER(EvictPrompt)]),
+    "evict_prompt_weights": (_I, [ctypes.POINTER(EvictPrompt)]),
+    "evict_weigh": (_I, [_P, ctypes.POINTER(EvictRows), _I, _I, _P, _P, ctypes.c_float, _P]),
     "evict_launch_count": (ctypes.c_int64, []),
     "evict_last_error": (ctypes.c_char_p, []),
 }
@@ -164,6 +179,12 @@ def evict_init(cfg: EvictConfig) -> int:
 def evict_update_and_fetch(h, k_ptr, v_ptr, pos_ptr, m) -> EvictView:
     view = EvictView()
     check(load().evict_update_and_fetch(h, k_ptr, v_ptr, pos_ptr, m, ctypes.byref(view)))
+    return view
+
+
+def evict_update_scored(h, k_ptr, v_ptr, pos_ptr, score_ptr, m) -> EvictView:
+    view = EvictView()
+    check(load().evict_update_scored(h, k_ptr, v_ptr, pos_ptr, score_ptr, m, ctypes.byref(view)))
     return view
 
 
@@ -307,6 +328,30 @@ def evict_shared_attention(a: EvictAttention):
     check(load().evict_shared_attention(a))
 
 
+def evict_prompt_attention_workspace(a: EvictPrompt) -> int:
+    n = ctypes.c_size_t()
+    check(load().evict_prompt_attention_workspace(a, n))
+    return n.value
+
+
+def evict_prompt_weights_workspace(a: EvictPrompt) -> int:
+    n = ctypes.c_size_t()
+    check(load().evict_prompt_weights_workspace(a, n))
+    return n.value
+
+
+def evict_prompt_attention(a: EvictPrompt):
+    check(load().evict_prompt_attention(a))
+
+
+def evict_prompt_weights(a: EvictPrompt):
+    check(load().evict_prompt_weights(a))
+
+
+def evict_weigh(h, q: EvictRows, batch, m, lse_ptr, n_new_ptr, scale, stream):
+    check(load().evict_weigh(h, q, batch, m, lse_ptr, n_new_ptr, scale, stream))
+
+
 def evict_launch_count() -> int:
     return load().evict_launch_count()
 
@@ -342,6 +387,34 @@ def view_tensors(view: EvictView, batch: int, heads: int, dtype: str):
     pos = wrap(view.pos, (batch, heads, n), "<i4", row_strides)
     score = wrap(view.score, (batch, heads, n), "<f4", row_strides)
     return k, v, pos, score
+
+
+class _Ordered:
+    """Orders work on the current stream behind a cache's last update, and its next one behind the work."""
+
+    def __init__(self, handle):
+        import torch
+        self.here, own = torch.cuda.current_stream(), evict_get_stream(handle)
+        if self.here.cuda_stream == own:
+            own = None
+        else:
+            own = torch.cuda.ExternalStream(own) if own else torch.cuda.default_stream()
+            captures = torch.cuda.is_current_stream_capturing()
+            with torch.cuda.stream(own):
+                own_captures = torch.cuda.is_current_stream_capturing()
+            if own_captures and not captures:
+                raise ValueError("the cache's stream is being captured: attend under it")
+            if captures and not own_captures:
+                own = None
+        self.own = own
+
+    def __enter__(self):
+        if self.own is not None:
+            self.here.wait_stream(self.own)
+
+    def __exit__(self, failed, *_):
+        if self.own is not None and failed is None:
+            self.own.wait_stream(self.here)
 
 
 class EvictCache:
@@ -383,45 +456,57 @@ class EvictCache:
         except Exception:
             pass
 
-    def update_and_fetch(self, k, v, pos=None):
+    def update_and_fetch(self, k, v, pos=None, score=None):
+        """Absorb one block. ``score`` (method "attention"): fp32 [B, H, m], what the new rows' accumulated
+        weights start from, e.g. ``prompt.weights`` of them (None: 0)."""
         m = k.shape[2]
         for t in (k, v):
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError("k and v must be contiguous CUDA tensors [B, H, m, 128]")
         pos_ptr = pos.data_ptr() if pos is not None else None
-        view = evict_update_and_fetch(self.handle, k.data_ptr(), v.data_ptr(), pos_ptr, m)
+        if score is None:
+            view = evict_update_and_fetch(self.handle, k.data_ptr(), v.data_ptr(), pos_ptr, m)
+        else:
+            import torch
+            if score.dtype is not torch.float32 or score.shape != k.shape[:3] or not score.is_contiguous() or \
+                    score.device != k.device:
+                raise ValueError("score must be contiguous fp32 [B, H, m] on k's device")
+            view = evict_update_scored(self.handle, k.data_ptr(), v.data_ptr(), pos_ptr, score.data_ptr(), m)
         return view_tensors(view, self.batch, self.heads, self.dtype)
 
-    def attend(self, q, n_new=None, scale=None, out=None, lse=None):
+    def attend(self, q, n_new=None, scale=None, out=None, lse=None, weigh=False):
         """Attention of the queries q [batch, n_q_heads, m, 128] (bf16, rotated) over this cache's
         kept rows, all of which every query sees: paged.shared_attention without pages. A batch
         that is a multiple of the cache's gives every kept prefix to that many sequences.
+        ``weigh`` (method "attention"): and ``weigh`` of the same queries.
 
         Work goes on the current stream. Where that is not the cache's, it is ordered behind the
         cache's last update, and the cache's next one behind it, also inside one graph that captures
         both streams. A graph that captures the current stream alone cannot hold that order: it reads
         the rows kept when it is replayed, and the replay has to be ordered like any other reader."""
-        import torch
         from . import paged
-        here, own = torch.cuda.current_stream(), evict_get_stream(self.handle)
-        if here.cuda_stream == own:
-            own = None
-        else:
-            own = torch.cuda.ExternalStream(own) if own else torch.cuda.default_stream()
-            captures = torch.cuda.is_current_stream_capturing()
-            with torch.cuda.stream(own):
-                own_captures = torch.cuda.is_current_stream_capturing()
-            if own_captures and not captures:
-                raise ValueError("the cache's stream is being captured: attend under it")
-            if captures and not own_captures:
-                own = None
-            else:
-                here.wait_stream(own)
-        k, v, _, _ = self.view()
-        got = paged.shared_attention(q, prefix=(k, v), n_new=n_new, scale=scale, out=out, lse=lse)
-        if own is not None:
-            own.wait_stream(here)
-        return got
+        if weigh:
+            import torch
+            if self.method != "attention":
+                raise ValueError('only a cache of method "attention" accumulates weights')
+            if lse is None:
+                lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        with _Ordered(self.handle):
+            k, v, _, _ = self.view()
+            out = paged.shared_attention(q, prefix=(k, v), n_new=n_new, scale=scale, out=out, lse=lse)
+            if weigh:
+                paged.weigh_rows(self, q, lse, n_new=n_new, scale=scale)
+        return out
+
+    def weigh(self, q, lse, n_new=None, scale=None):
+        """Add to the kept rows' scores the attention weights exp(scale * q . k - lse) that the queries
+        q [batch, n_q_heads, m, 128] (bf16, rotated) put on them. lse: fp32 [batch, n_q_heads, m] of the
+        attention that they made, over these rows alone or together with others (``attend`` and
+        ``paged.PagedCache.attend`` fill it). Method "attention" only; batch, streams and captures as for
+        ``attend``."""
+        from . import paged
+        with _Ordered(self.handle):
+            paged.weigh_rows(self, q, lse, n_new=n_new, scale=scale)
 
     def view(self):
         """Tensors over the kept rows, without a copy: what the cache's stream has left there, until its

@@ -44,9 +44,12 @@
 #include <cuda_bf16.h>
 
 #include "attend.cuh"
+#include "tmem.cuh"
 
 namespace evict {
 namespace {
+
+using namespace tm;
 
 constexpr int kTile = 128, kHalf = 64;
 constexpr int kTileBytes = kTile * kHeadDim * 2;
@@ -169,7 +172,6 @@ struct Watch {
     return false;
   }
 };
-__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return (uint64_t)lo | ((uint64_t)hi << 32); }
 
 // Half a step's S = Q K^T, both K-major; q and k: the tiles' descriptors' low words (their steps
 // differ in the start address alone, which does not carry over).
@@ -187,12 +189,7 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t pt, uint32_t v, ui
   constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile) | (1u << 16);
 #pragma unroll
   for (int s = 0; s < kHalf / 16; ++s) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-        "r"(pt + s * 8), "l"(desc_of(v + s * 128, hi)), "r"(idesc), "r"(accumulate || s > 0 ? 1u : 0u)
-        : "memory");
+    mma_bf16_ts(d, pt + s * 8, desc_of(v + s * 128, hi), idesc, accumulate || s > 0 ? 1u : 0u);
   }
 }
 
@@ -281,40 +278,6 @@ __device__ void mma_issuer(const AttendParams& p, WideShared& sh, WideCursor c, 
   tc::mma_commit(&sh.done[w]);
   drain_phase(&sh.done[w], 0, p.err);
 }
-
-// 32 columns of this thread's row. The load runs on; nothing may use the registers before wait32,
-// which has them as operands to that end.
-__device__ __forceinline__ void load32(uint32_t taddr, float (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-      : "r"(taddr) : "memory");
-}
-__device__ __forceinline__ void wait32(float (&v)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
-               :: "memory");
-}
-__device__ __forceinline__ void store16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-// 32 bytes to global memory, 32-byte aligned: a whole sector from each thread
-__device__ __forceinline__ void store_sector(void* dst, const uint32_t* r) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
-}
-// 16 columns, complete on return
-__device__ __forceinline__ void load16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr) : "memory");
-}
-__device__ __forceinline__ void wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // The reference of a row's exponents moved: its O (where there is one) and the step's weights so
 // far (`columns` of them) follow by the factor f. Whole warp; rare after a unit's first step.

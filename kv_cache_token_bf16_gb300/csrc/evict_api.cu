@@ -134,10 +134,10 @@ int fallback_tokens(const evict_config* c) { return c->calib_tokens > 0 ? c->cal
 
 int validate(const evict_config* c) {
   if (!c) return fail(EVICT_EINVAL, "config is NULL");
-  if (c->method < EVICT_KNORM || c->method > EVICT_H2O) return fail(EVICT_EINVAL, "unknown method %d", c->method);
+  if (c->method < EVICT_KNORM || c->method > EVICT_ATTENTION) return fail(EVICT_EINVAL, "unknown method %d", c->method);
   if (c->dtype != EVICT_BF16 && c->dtype != EVICT_FP32) return fail(EVICT_EINVAL, "unknown dtype %d", c->dtype);
-  if (attention_family(c->method) && c->dtype != EVICT_BF16)
-    return fail(EVICT_EINVAL, "CurDKV and H2O store bf16 keys and values only");
+  if ((attention_family(c->method) || c->method == EVICT_ATTENTION) && c->dtype != EVICT_BF16)
+    return fail(EVICT_EINVAL, "CurDKV, H2O and attention weights store bf16 keys and values only");
   if (c->batch < 1 || c->n_kv_heads < 1) return fail(EVICT_EINVAL, "batch and n_kv_heads must be >= 1");
   if (c->head_dim != EVICT_HEAD_DIM) return fail(EVICT_EINVAL, "head_dim must be %d (got %d)", EVICT_HEAD_DIM, c->head_dim);
   if (c->budget < 1) return fail(EVICT_EINVAL, "budget must be >= 1");
@@ -240,12 +240,18 @@ bool same_shape(const evict_handle* a, const evict_handle* b) {
          a->n_kept == b->n_kept && a->offset == b->offset && a->stream == b->stream;
 }
 
-// Enqueue the update of n_layers same-shaped caches (KNorm / Q-Filters).
+// Enqueue the update of n_layers same-shaped caches (KNorm / Q-Filters), or of one by attention weights,
+// whose rows' starts are `score` (EVICT_ATTENTION writes nothing to new_score: its zeros are the default).
 int run_intrinsic(evict_handle* const* hs, int n_layers, const void* const* k, const void* const* v,
-                  const int32_t* const* pos, int m) {
+                  const int32_t* const* pos, int m, const float* score = nullptr) {
   evict_handle* h = hs[0];
+  const bool given = h->cfg.method == EVICT_ATTENTION;
   GroupParams P = make_group_params(h, m, n_layers);
   for (int l = 0; l < n_layers; ++l) P.L[l] = make_layer_ptrs(hs[l], k[l], v[l], pos ? pos[l] : nullptr);
+  if (score) {
+    P.L[0].new_score = const_cast<float*>(score);   // read only
+    P.s.new_stride = m;
+  }
   const long long n = (long long)h->n_kept + m;
   cudaError_t e;
   if (h->fallback && !h->frozen) {
@@ -281,8 +287,10 @@ int run_intrinsic(evict_handle* const* hs, int n_layers, const void* const* k, c
       hs[l]->last_evicted = true;
     }
   } else {
-    e = timed_launch(h, kKidScore, [&] { return launch_score(P, h->elem, h->stream); });
-    if (e != cudaSuccess) return cuda_fail(e, "score kernel launch");
+    if (!given) {
+      e = timed_launch(h, kKidScore, [&] { return launch_score(P, h->elem, h->stream); });
+      if (e != cudaSuccess) return cuda_fail(e, "score kernel launch");
+    }
     e = timed_launch(h, kKidSelect, [&] { return launch_select(P, h->stream); });
     if (e != cudaSuccess) return cuda_fail(e, "select kernel launch");
     e = timed_launch(h, kKidCompact, [&] { return launch_compact(P, h->elem, h->stream); });
@@ -334,6 +342,22 @@ int check_update_args(const evict_handle* h, const void* k, const void* v, const
   if (device && ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15))
     return fail(EVICT_EINVAL, "k and v must be 16-byte aligned");
   if (device && (reinterpret_cast<uintptr_t>(pos) & 3)) return fail(EVICT_EINVAL, "pos must be 4-byte aligned");
+  return EVICT_OK;
+}
+
+int update(evict_handle* h, const void* k, const void* v, const int32_t* pos, const float* score, int m, evict_view* out) {
+  int rc = check_update_args(h, k, v, pos, m, true);
+  if (rc) return rc;
+  if (m > 0) {
+    note_capture(&h, 1);
+    if (attention_family(h->cfg.method)) {
+      rc = h->cfg.per_token && m > 1 ? per_token_update(h, k, v, pos, m) : curdkv_update(h, k, v, pos, m);
+    } else {
+      rc = run_intrinsic(&h, 1, &k, &v, &pos, m, score);
+    }
+    if (rc) return rc;
+  }
+  fill_view(h, out);
   return EVICT_OK;
 }
 
@@ -407,19 +431,15 @@ int evict_init(const evict_config* cfg, evict_handle** out) {
 
 int evict_update_and_fetch(evict_handle* h, const void* k, const void* v, const int32_t* pos, int m,
                            evict_view* out) {
-  int rc = check_update_args(h, k, v, pos, m, true);
-  if (rc) return rc;
-  if (m > 0) {
-    note_capture(&h, 1);
-    if (attention_family(h->cfg.method)) {
-      rc = h->cfg.per_token && m > 1 ? per_token_update(h, k, v, pos, m) : curdkv_update(h, k, v, pos, m);
-    } else {
-      rc = run_intrinsic(&h, 1, &k, &v, &pos, m);
-    }
-    if (rc) return rc;
-  }
-  fill_view(h, out);
-  return EVICT_OK;
+  return update(h, k, v, pos, nullptr, m, out);
+}
+
+int evict_update_scored(evict_handle* h, const void* k, const void* v, const int32_t* pos, const float* score, int m,
+                        evict_view* out) {
+  if (!h) return fail(EVICT_EINVAL, "handle is NULL");
+  if (h->cfg.method != EVICT_ATTENTION) return fail(EVICT_EINVAL, "this cache's method makes its rows' scores itself");
+  if (reinterpret_cast<uintptr_t>(score) & 3) return fail(EVICT_EINVAL, "score must be 4-byte aligned");
+  return update(h, k, v, pos, score, m, out);
 }
 
 int evict_update_and_fetch_group(evict_handle* const* hs, int n_layers, const void* const* k,
@@ -435,7 +455,8 @@ int evict_update_and_fetch_group(evict_handle* const* hs, int n_layers, const vo
     for (int j = 0; j < l; ++j)
       if (hs[j] == hs[l]) return fail(EVICT_EINVAL, "handle %d appears twice", l);
   }
-  if (attention_family(hs[0]->cfg.method)) return fail(EVICT_EINVAL, "grouped update supports KNorm and Q-Filters");
+  if (attention_family(hs[0]->cfg.method) || hs[0]->cfg.method == EVICT_ATTENTION)
+    return fail(EVICT_EINVAL, "grouped update supports KNorm and Q-Filters");
   if (m > 0) {
     note_capture(hs, n_layers);
     int rc = run_intrinsic(hs, n_layers, k, v, pos, m);

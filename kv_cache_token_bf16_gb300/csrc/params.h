@@ -9,7 +9,7 @@ namespace evict {
 // Up to this many layer caches can be updated by one set of launches.
 constexpr int kMaxGroup = 32;
 
-enum Method : int { kKNorm = 0, kQFilters = 1, kCurDKV = 2 };
+enum Method : int { kKNorm = 0, kQFilters = 1, kCurDKV = 2 };   // kCurDKV and above: scores in new_score
 
 // Per-layer device pointers of one grouped update.
 struct LayerPtrs {
@@ -22,7 +22,7 @@ struct LayerPtrs {
   float* score_st;         // [B, H, cap]
   float* filters;          // Q-Filters: [H, D] calibrated, or [B, H, D] frozen by the key-SVD
                            // fallback (written only by the freeze kernel)
-  float* new_score;        // [B, H, new_stride] scores of incoming rows
+  float* new_score;        // [B, H, new_stride] scores of incoming rows (attention weights: the caller's)
   int32_t* src_map;        // [B, H, cap] source row of each kept destination
   int2* meta;              // [B, H] {first moved destination, old survivors}
   int* flags;              // [B, H, flag_stride] compaction read-done flags, then the chunk counter

@@ -1,0 +1,770 @@
+// Attention of whole prompts with themselves, causal, query heads in groups, sequences packed behind
+// each other or in a batch.
+//
+//   o_t = sum_{j <= t} p_j v_j / sum_{j <= t} p_j,  p_j = exp(scale q_t.k_j - max)
+// in one pass over K and V; logits are kept in base 2 (scale * log2 e), so p = 2^(x - ref).
+//
+// A unit is a (sequence, KV head, tile of tokens): the tokens' query rows of the whole group, token by
+// token, fill two tiles of 128 rows, so that K and V are read once for all of the group's heads and few
+// rows at the diagonal go unseen. Warps 0-3 and 4-7 are two softmax groups, a thread per query row, each
+// with its own 128 x 128 logits and 128 x 128 output accumulator in tensor memory (512 columns in all).
+// Warp 8 issues the tensor cores' work of both in turn:
+//     S = Q K^T -> P = 2^(S scale - ref) as bf16 over S (softmax group) -> O += P V,
+// the product with V in halves of 64 rows, so that it begins while the second half is exponentiated; one
+// group's products run while the other exponentiates. Warp 9 fetches (TMA): K and V through a ring of five
+// 32 KB tiles of 128 rows, the queries of the next unit as soon as the last product that reads a tile is
+// through. Warp 10 clears rows of V that only some of the unit's queries see, or none (see scrub).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstring>
+
+#include "api_internal.h"
+#include "common.cuh"
+#include "launch.h"
+#include "prompt.cuh"
+#include "prompt.h"
+#include "rotary.h"
+#include "tmem.cuh"
+
+namespace evict {
+namespace {
+
+constexpr int kTile = 128, kHalf = 64;
+constexpr int kTileBytes = kTile * kHeadDim * 2;
+constexpr int kRows = 2 * kTile;                  // query rows of a unit
+constexpr int kRing = 5;
+constexpr int kSmem = 1024 + (2 + kRing) * kTileBytes;
+constexpr int kMmaWarp = 8, kTmaWarp = 9, kThreads = 352;   // warp 10 scrubs
+constexpr int kBadWords = kRows / 32;             // rows of V behind the unit's first token, a bit each
+constexpr int kBadSets = 8;                       // of a CTA's units in turn
+constexpr int kPartly = 4;                        // barriers of tiles to scrub, in turn: the ring holds at most three
+constexpr float kMoveAbove = 4096.f;              // sum of 32 weights that makes the reference move
+constexpr int kEntry = 1, kMinSteps = 4;
+constexpr int kWholeRows = 1024;
+
+struct AttentionShared {
+  uint64_t q_full[2], q_empty[2], kv_full[kRing], kv_empty[kRing], partly_full[kPartly], scrubbed[kPartly];
+  uint64_t s_full[2], p_full[2][2], first_half[2], o_full[2], done;
+  uint32_t tmem_base;
+  int fail;
+  uint32_t bad[kBadSets][kBadWords];
+  PromptScan scan;
+};
+
+struct Steps {
+  int tile;
+  __device__ __forceinline__ int operator()(int tok0, int len) const { return (min(tok0 + tile, len) + kTile - 1) / kTile; }
+};
+
+// A unit's part, as every role sees it.
+struct Part {
+  int tok0, reach;                                // first token; last one
+  int n[2];                                       // steps of the two groups (from c.from on); n[1] >= n[0] or 0
+  __device__ __forceinline__ Part(const PromptParams& p, const PromptCursor& c) {
+    tok0 = c.k.tile * p.work.tile;
+    reach = min(tok0 + p.work.tile, c.k.at.len) - 1;
+    const int first_reach = min(tok0 + p.half - 1, reach);        // of the first group's tokens
+    n[0] = min(c.to, first_reach / kTile + 1) - c.from;
+    n[0] = max(n[0], 0);
+    n[1] = first_reach < reach ? c.to - c.from : 0;
+  }
+  __device__ __forceinline__ int steps() const { return max(n[0], n[1]); }
+  // the step's rows of V hold some that not every query of the unit sees
+  __device__ __forceinline__ bool partly(int step) const { return step * kTile + kTile - 1 > tok0; }
+};
+
+struct Slot {
+  int i = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == kRing) i = 0, parity ^= 1;
+  }
+};
+
+__device__ void producer(const PromptParams& p, AttentionShared& sh, PromptCursor c, uint32_t qbuf, uint32_t ring) {
+  const Steps steps{p.work.tile};
+  Slot slot;
+  int used = 0, turns[2] = {0, 0}, partly = 0;
+  bool ok = true;
+  // a tile to be scrubbed lands on a barrier of the scrubbing warp's, and its slot counts as full at once
+  auto load_kv = [&](const CUtensorMap* map, int step, bool to_scrub) {
+    if (!(ok = wait_phase(&sh.kv_empty[slot.i], slot.parity ^ 1, &sh.fail, p.work.err))) return;
+    uint64_t* bar = &sh.kv_full[slot.i];
+    if (to_scrub) {
+      tc::mbar_arrive(bar);
+      bar = &sh.partly_full[partly++ % kPartly];
+    }
+    const uint32_t dst = ring + slot.i * kTileBytes;
+    tc::mbar_arrive_expect_tx(bar, kTileBytes);
+    for (int hf = 0; hf < 2; ++hf)
+      tma_load_4d(dst + hf * (kTileBytes / 2), map, hf * 64, c.k.at.row0 + step * kTile, c.h, c.k.at.plane, bar);
+    slot.next();
+    ++used;
+  };
+  do {
+    const Part part(p, c);
+    const int n = part.steps();
+    load_kv(&p.k_map, c.from, false);
+    for (int w = 0; w < 2 && ok; ++w) {
+      if (part.n[w] == 0) continue;
+      if (!(ok = wait_phase(&sh.q_empty[w], (turns[w] & 1) ^ 1, &sh.fail, p.work.err))) break;
+      ++turns[w];
+      tc::mbar_arrive_expect_tx(&sh.q_full[w], 2 * p.half * p.group * 128);
+      for (int hf = 0; hf < 2; ++hf)
+        tma_load_4d(qbuf + w * kTileBytes + hf * (kTileBytes / 2), &p.q_map, hf * 64, c.h * p.group,
+                    c.k.at.row0 + part.tok0 + w * p.half, c.k.at.plane, &sh.q_full[w]);
+    }
+    if (ok) load_kv(&p.v_map, c.from, part.partly(c.from));
+    for (int i = 1; i < n && ok; ++i) {
+      load_kv(&p.k_map, c.from + i, false);
+      if (ok) load_kv(&p.v_map, c.from + i, part.partly(c.from + i));
+    }
+  } while (ok && next_unit(p.work, c, steps));
+  // every copy issued must land before the CTA may release its shared memory
+  for (int i = 0; i < kRing && i < used; ++i) drain_phase(&sh.kv_full[i], ((used - 1 - i) / kRing) & 1, p.work.err);
+  for (int i = 0; i < kPartly && i < partly; ++i) drain_phase(&sh.partly_full[i], ((partly - 1 - i) / kPartly) & 1, p.work.err);
+  for (int w = 0; w < 2; ++w)
+    if (turns[w]) drain_phase(&sh.q_full[w], (turns[w] - 1) & 1, p.work.err);
+}
+
+// Rows of V that a query does not see meet a weight of 0, but 0 * infinity is not 0. Rows behind the unit's
+// last token (another sequence's, or none) are cleared; rows between its first and last token are cleared
+// where they hold infinities or NaN, and marked: the queries that do see them add them at the unit's end.
+__device__ void scrub(const PromptParams& p, AttentionShared& sh, PromptCursor c, uint32_t ring) {
+  const Steps steps{p.work.tile};
+  const int lane = threadIdx.x & 31;
+  Slot slot;
+  uint32_t count = 0, unit = 0;
+  bool ok = true;
+  do {
+    const Part part(p, c);
+    uint32_t* bad = sh.bad[unit++ % kBadSets];
+    if (lane < kBadWords) bad[lane] = 0;
+    __syncwarp();
+    for (int i = 0; i < part.steps() && ok; ++i) {
+      slot.next();                                // the step's V
+      const int own0 = (c.from + i) * kTile;
+      if (part.partly(c.from + i)) {
+        ok = wait_phase(&sh.partly_full[count % kPartly], (count / kPartly) & 1, &sh.fail, p.work.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+#pragma unroll 1
+        for (int r = lane; r < kTile; r += 32) {
+          const uint32_t at = ring + slot.i * kTileBytes + r * 128;
+          const int tok = own0 + r;
+          bool blank = tok > part.reach;
+          if (!blank && tok > part.tok0) {
+            uint32_t seen = 0;                    // x * 0 is 0, or NaN where x is not finite
+#pragma unroll 4
+            for (int j = 0; j < 16; ++j) {
+              uint4 x;
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                           : "r"(at + (j >> 3) * (kTileBytes / 2) + ((j + r) & 7) * 16) : "memory");
+              asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(seen) : "r"(x.x), "r"(0u));
+              asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(seen) : "r"(x.y), "r"(0u));
+              asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(seen) : "r"(x.z), "r"(0u));
+              asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(seen) : "r"(x.w), "r"(0u));
+            }
+            blank = nonfinite2(seen) != 0;
+            if (blank) atomicOr(&bad[(tok - part.tok0 - 1) >> 5], 1u << ((tok - part.tok0 - 1) & 31));
+          }
+          if (blank) {
+#pragma unroll 1
+            for (int j = 0; j < 16; ++j)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};"
+                           ::"r"(at + (j >> 3) * (kTileBytes / 2) + ((j + r) & 7) * 16), "r"(0u) : "memory");
+            tc::fence_proxy_async_smem();
+          }
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh.scrubbed[count % kPartly]);
+        ++count;
+      }
+      slot.next();
+    }
+  } while (ok && next_unit(p.work, c, steps));
+}
+
+// S = Q K^T of a step; O (+)= P V of half a step (see tmem.cuh). q, k, v: low words of the tiles' descriptors.
+struct Issuer {
+  uint32_t qk_hi, v_hi, q_lo, k_lo, v_lo, tmem;
+  __device__ __forceinline__ void logits(int w, int slot) const {
+    constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile);
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const uint32_t off = (uint32_t)((s >> 2) * kTile * 128 + (s & 3) * 32) >> 4;
+      tc::mma_bf16(tmem + w * kTile, tm::desc_of(q_lo + (w * kTileBytes >> 4) + off, qk_hi),
+                   tm::desc_of(k_lo + (slot * kTileBytes >> 4) + off, qk_hi), idesc, s > 0 ? 1u : 0u);
+    }
+  }
+  __device__ __forceinline__ void product(int w, int slot, int h, bool accumulate) const {
+    constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile) | (1u << 16);
+#pragma unroll
+    for (int s = 0; s < kHalf / 16; ++s)          // 16 rows of V are 2048 bytes of each half of its columns
+      tm::mma_bf16_ts(tmem + (2 + w) * kTile, tmem + w * kTile + h * (kHalf / 2) + s * 8,
+                      tm::desc_of(v_lo + ((slot * kTileBytes + h * (kHalf * 128)) >> 4) + s * 128, v_hi), idesc,
+                      accumulate || s > 0 ? 1u : 0u);
+  }
+};
+
+// The tensor cores' work of both groups, by one thread. They take it in order, so a step's S may be issued
+// over the weights of the product before it.
+__device__ void mma_issuer(const PromptParams& p, AttentionShared& sh, PromptCursor c, uint32_t tmem, uint32_t qbuf,
+                           uint32_t ring) {
+  const Steps steps{p.work.tile};
+  const uint64_t qd = tc::sw128_desc(qbuf), kd = tc::sw128_desc(ring), vd = tc::sw128_desc_mn(ring, kTileBytes / 2, 1024);
+  const Issuer issue{(uint32_t)(qd >> 32), (uint32_t)(vd >> 32), (uint32_t)qd, (uint32_t)kd, (uint32_t)vd, tmem};
+  uint32_t q_turn[2] = {0, 0}, p_turn[2] = {0, 0}, scrubs = 0;
+  Slot k_slot;                                    // K of the next step; V of the step at hand is behind its K
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && wait_phase(bar, parity, &sh.fail, p.work.err); };
+  Part part(p, c);
+  bool begun[2] = {false, false};                 // the unit's first logits are issued
+  // the first logits of a part; with `try_only` where their operands are there
+  auto first_logits = [&](const Part& x, int w, bool try_only) {
+    if (x.n[w] == 0 || begun[w]) return;
+    if (try_only && !(test_phase(&sh.q_full[w], q_turn[w] & 1) && test_phase(&sh.kv_full[k_slot.i], k_slot.parity)))
+      return;
+    if (!wait(&sh.q_full[w], q_turn[w] & 1) || !wait(&sh.kv_full[k_slot.i], k_slot.parity)) return;
+    ++q_turn[w];
+    tc::fence_after_sync();
+    issue.logits(w, k_slot.i);
+    tc::mma_commit(&sh.s_full[w]);
+    if (x.n[w] == 1) tc::mma_commit(&sh.q_empty[w]);
+    begun[w] = true;
+  };
+  bool more = true;
+  while (ok && more) {
+    first_logits(part, 0, false);
+    first_logits(part, 1, false);
+    if (!ok) break;
+    tc::mma_commit(&sh.kv_empty[k_slot.i]);
+    begun[0] = begun[1] = false;
+    const int n = part.steps(), from = c.from;
+    Part next = part;
+#pragma unroll 1
+    for (int i = 0; i < n && ok; ++i) {
+      Slot v_slot = k_slot;
+      v_slot.next();
+      k_slot = v_slot;
+      k_slot.next();
+      const bool last_step = i + 1 == n;
+      if (last_step) {
+        more = next_unit(p.work, c, steps);
+        if (more) next = Part(p, c);
+      }
+      if (!wait(&sh.kv_full[v_slot.i], v_slot.parity)) break;
+      if (part.partly(from + i)) {
+        if (!wait(&sh.scrubbed[scrubs % kPartly], (scrubs / kPartly) & 1)) break;
+        ++scrubs;
+      }
+#pragma unroll 1
+      for (int w = 0; w < 2 && ok; ++w) {
+        if (i < part.n[w]) {
+          for (int h = 0; h < 2; ++h) {
+            if (!wait(&sh.p_full[w][h], p_turn[w] & 1)) break;
+            tc::fence_after_sync();
+            issue.product(w, v_slot.i, h, i > 0 || h > 0);
+            if (h == 0) tc::mma_commit(&sh.first_half[w]);
+          }
+          if (!ok) break;
+          ++p_turn[w];
+          if (i + 1 == part.n[w]) tc::mma_commit(&sh.o_full[w]);
+          if (i + 1 < part.n[w]) {
+            if (!wait(&sh.kv_full[k_slot.i], k_slot.parity)) break;
+            tc::fence_after_sync();
+            issue.logits(w, k_slot.i);
+            tc::mma_commit(&sh.s_full[w]);
+            if (i + 2 == part.n[w]) tc::mma_commit(&sh.q_empty[w]);
+          }
+        }
+        // the next unit's first logits where they would not make the other group wait
+        if (last_step && more && w == 0) first_logits(next, 0, true);
+      }
+      if (!ok) break;
+      tc::mma_commit(&sh.kv_empty[v_slot.i]);
+      if (!last_step) tc::mma_commit(&sh.kv_empty[k_slot.i]);
+    }
+    part = next;
+  }
+  // every MMA must finish before tensor and shared memory are released
+  tc::mma_commit(&sh.done);
+  drain_phase(&sh.done, 0, p.work.err);
+}
+
+// The reference of a row's exponents moved: its O (where there is one) and the half step's weights so far
+// (`columns` of them) follow by the factor f. Whole warp; rare after a unit's first step.
+__device__ __noinline__ void move_reference(uint32_t p_at, int columns, uint32_t o_at, float f) {
+  tm::wait_stores();
+  uint32_t x[16];
+  for (int c = 0; c < columns; c += 16) {
+    tm::load16(p_at + c, x);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = pack_bf16(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xffff0000u) * f);
+    tm::store16(p_at + c, x);
+  }
+  if (o_at) {
+    for (int c = 0; c < kHeadDim; c += 16) {
+      tm::load16(o_at + c, x);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+      tm::store16(o_at + c, x);
+    }
+  }
+}
+
+// One softmax group: thread `row` of group w.
+__device__ void softmax_group(const PromptParams& p, AttentionShared& sh, PromptCursor c, int w, int row, uint32_t tmem) {
+  const Steps steps{p.work.tile};
+  const uint32_t lanes = (uint32_t)(row & ~31) << 16;
+  const uint32_t s_at = tmem + lanes + (uint32_t)(w * kTile), o_at = s_at + 2 * kTile;
+  const float scale = p.scale2, hidden = scale < 0.f ? INFINITY : -INFINITY;   // a logit that gives -infinity
+  const int tl = p.by_group.div(row), g = row - tl * p.group;     // token of the tile, head of the group
+  uint32_t turn = 0, o_turn = 0, unit = 0;        // steps so far, units with a step so far, units so far
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool there = wait_phase(bar, parity, &sh.fail, p.work.err);
+    ok = __all_sync(0xffffffffu, there) && ok;
+    tc::fence_after_sync();
+    return ok;
+  };
+  do {
+    const Part part(p, c);
+    const int n = part.n[w], token = part.tok0 + w * p.half + tl;
+    const bool real = tl < p.half && token <= part.reach;
+    float ref = real ? -INFINITY : 0.f;           // rows without a query never wait for a maximum
+    float sum = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i, ++turn) {
+      const int own0 = (c.from + i) * kTile;
+      const int seen = token - own0;              // columns 0 .. seen
+      const bool masked = __any_sync(0xffffffffu, real && seen < kTile - 1);
+      if (!wait(&sh.s_full[w], turn & 1)) break;
+      // 32 columns at a time; the next ones are on their way while these are at work
+      float x[2][32];
+      auto chunk = [&](int ch, float(&y)[32], float(&next)[32]) {
+        tm::wait32(y);
+        if (ch < 3) tm::load32(s_at + 32 * (ch + 1), next);
+        if (masked) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (32 * ch + k > seen) y[k] = hidden;
+        }
+        const uint64_t sc2 = pack_f32x2(scale, scale);
+        uint32_t pk[16];
+        float got;
+#pragma unroll 1
+        for (bool again = false;; again = true) {
+          // weights against the reference, packed, and their sum
+          const float nb = -base_of(ref);
+          const uint64_t nb2 = pack_f32x2(nb, nb);
+          uint64_t acc[2] = {0ull, 0ull};
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const uint64_t e = ex2_f32x2(fma_f32x2(pack_f32x2(y[k], y[k + 1]), sc2, nb2));
+            acc[(k >> 1) & 1] = add_f32x2(acc[(k >> 1) & 1], e);
+            float e0, e1;
+            split_f32x2(e, e0, e1);
+            pk[k >> 1] = pack_bf16(e0, e1);
+          }
+          float a0, a1;
+          split_f32x2(add_f32x2(acc[0], acc[1]), a0, a1);
+          got = a0 + a1;
+          // no reference yet, or a sum that says that it has fallen far behind the maximum (NaN as well)
+          if (again || !__any_sync(0xffffffffu, real && (ref == -INFINITY || !(got < kMoveAbove)))) break;
+          if (ch < 3) tm::wait32(next);           // no call while a load is on its way to registers
+          float top = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) top = fmax3(top, y[k] * scale, y[k + 1] * scale);
+          const float to = real ? fmaxf(ref, top) : ref, f = weight_of(ref, to);
+          ref = to;
+          sum *= f;
+          // O as the products so far left it: those of earlier steps were through before this step's logits
+          const bool half_in = ch >= 2;
+          if (half_in) wait(&sh.first_half[w], turn & 1);
+          move_reference(s_at + (half_in ? kHalf / 2 : 0), 16 * (ch & 1), i > 0 || half_in ? o_at : 0, f);
+        }
+        sum += got;
+        tm::store16(s_at + 16 * ch, pk);          // over columns that are in registers by now
+      };
+      auto announce = [&](int h) {
+        tm::wait_stores();
+        tc::fence_before_sync();
+        __syncwarp();
+        if ((row & 31) == 0) tc::mbar_arrive(&sh.p_full[w][h]);   // a warp's 32 arrivals would go one by one
+      };
+      tm::load32(s_at, x[0]);
+      chunk(0, x[0], x[1]);
+      chunk(1, x[1], x[0]);
+      announce(0);
+      chunk(2, x[0], x[1]);
+      chunk(3, x[1], x[0]);
+      announce(1);
+    }
+    if (!ok) break;
+    if (n > 0 && !wait(&sh.o_full[w], o_turn++ & 1)) break;
+    const uint32_t* bad = sh.bad[unit++ % kBadSets];
+    uint32_t any_bad = 0;
+    if (n > 0 && part.partly(c.to - 1))
+      for (int k = 0; k < kBadWords; ++k) any_bad |= bad[k];
+    const bool whole = c.to - c.from == c.k.steps;
+    const bool write = real && (whole ? n > 0 : true);
+    const size_t part_row = (size_t)(2 * blockIdx.x + (c.from == 0 ? 1 : 0)) * kRows + w * kTile + row;
+    const float inv = 1.f / sum;
+    const long long out_row = (long long)c.k.at.row0 + token;
+    const int hq = c.h * p.group + g;
+#pragma unroll 1
+    for (int h = 0; h < 4; ++h) {
+      float o[32];
+      if (n > 0) {
+        tc::tmem_ld32(o_at + 32 * h, o);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = 0.f;
+      }
+      if (any_bad && write) {
+        // rare: the rows that were cleared, for the queries that see them, where this part's steps hold them
+#pragma unroll 1
+        for (int k = 0; k < kRows; ++k) {
+          const int tok = part.tok0 + 1 + k;
+          if (!((bad[k >> 5] >> (k & 31)) & 1) || tok > token) continue;
+          const int step = tok / kTile - c.from;
+          if (step < 0 || step >= n) continue;
+          const long long at = (long long)c.k.at.row0 + tok;
+          const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(p.k) + c.k.at.plane * p.kb + c.h * p.kh + at * p.km;
+          const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.v) + c.k.at.plane * p.vb + c.h * p.vh + at * p.vm + 32 * h;
+          const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q) + c.k.at.plane * p.qb + hq * p.qh + out_row * p.qm;
+          float z = 0.f;
+#pragma unroll 1
+          for (int d = 0; d < kHeadDim; ++d) z += __bfloat162float(qr[d]) * __bfloat162float(kr[d]);
+          const float wt = ex2(z * scale - base_of(ref));
+#pragma unroll
+          for (int d = 0; d < 32; ++d) o[d] += wt * __bfloat162float(vr[d]);
+        }
+      }
+      if (!write) continue;
+      if (whole) {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + c.k.at.plane * p.ob + hq * p.oh + out_row * p.om + 32 * h;
+        uint32_t y[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) y[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
+        if (p.out_sectors) {
+          tm::store_sector(dst, y);
+          tm::store_sector(dst + 16, y + 8);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            reinterpret_cast<uint4*>(dst)[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+        }
+      } else {
+        float* dst = p.part + part_row * kHeadDim + 32 * h;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tm::store_sector(dst + 8 * k, reinterpret_cast<const uint32_t*>(o) + 8 * k);
+      }
+    }
+    if (write) {
+      if (!whole) {
+        p.part_ml[part_row] = make_float2(ref, sum);
+      } else if (p.lse) {
+        p.lse[((long long)c.k.at.plane * p.hq + hq) * p.work.m + out_row] = (ref + log2f(sum)) * 0.6931471805599453f;
+      }
+    }
+    tc::fence_before_sync();                      // O is read: the next unit's first product follows our weights
+  } while (next_unit(p.work, c, steps));
+}
+
+__global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __grid_constant__ PromptParams p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ AttentionShared sh;
+  const uint32_t smem = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == 0) tc::tmem_alloc(&sh.tmem_base, 4 * kTile);
+  if (tid == 32) {
+    for (int w = 0; w < 2; ++w) {
+      tc::mbar_init(&sh.q_full[w], 1);
+      tc::mbar_init(&sh.q_empty[w], 1);
+      tc::mbar_init(&sh.s_full[w], 1);
+      tc::mbar_init(&sh.first_half[w], 1);
+      tc::mbar_init(&sh.o_full[w], 1);
+      for (int h = 0; h < 2; ++h) tc::mbar_init(&sh.p_full[w][h], kTile / 32);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      tc::mbar_init(&sh.kv_full[i], 1);
+      tc::mbar_init(&sh.kv_empty[i], 1);
+    }
+    for (int i = 0; i < kPartly; ++i) {
+      tc::mbar_init(&sh.partly_full[i], 1);
+      tc::mbar_init(&sh.scrubbed[i], 1);
+    }
+    tc::mbar_init(&sh.done, 1);
+    sh.fail = 0;
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    tc::tma_prefetch_desc(&p.q_map);
+    tc::tma_prefetch_desc(&p.k_map);
+    tc::tma_prefetch_desc(&p.v_map);
+  }
+  pdl_wait();
+  PromptCursor c;
+  const bool any = first_unit<kThreads>(p.work, sh.scan, c, Steps{p.work.tile});
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = sh.tmem_base, ring = smem + 2 * kTileBytes;
+  if (any) {
+    if (warp < kMmaWarp) {
+      softmax_group(p, sh, c, warp >> 2, tid & (kTile - 1), tmem);
+    } else if (warp == kMmaWarp) {
+      if (lane == 0) mma_issuer(p, sh, c, tmem, smem, ring);
+      __syncwarp();
+    } else if (warp == kTmaWarp) {
+      if (lane == 0) producer(p, sh, c, smem, ring);
+      __syncwarp();
+    } else {
+      scrub(p, sh, c, ring);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 0) tc::tmem_dealloc(tmem, 4 * kTile);
+}
+
+// Rows of units that two or more CTAs share: a warp merges a row's parts, in the shares' order.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(const __grid_constant__ PromptParams p) {
+  pdl_wait();
+  SplitUnit u;
+  if (!split_unit(p.work, blockIdx.x + 1, u, Steps{p.work.tile})) return;
+  const int lane = threadIdx.x & 31, row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  const int w = row / kTile, tl = p.by_group.div(row - w * kTile), g = row - w * kTile - tl * p.group;
+  const int token = u.k.tile * p.work.tile + w * p.half + tl;
+  if (tl >= p.half || token >= u.k.at.len) return;
+  float top = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int i = u.c0; i <= u.c1; ++i) {
+    const size_t at = (size_t)(2 * i + (i == u.c0 ? 1 : 0)) * kRows + row;
+    const float2 ml = p.part_ml[at];
+    const float4 v = reinterpret_cast<const float4*>(p.part + at * kHeadDim)[lane];
+    const float to = fmaxf(top, ml.x), f = weight_of(top, to), wt = weight_of(ml.x, to);
+    top = to;
+    sum = sum * f + ml.y * wt;
+    acc.x = acc.x * f + v.x * wt;
+    acc.y = acc.y * f + v.y * wt;
+    acc.z = acc.z * f + v.z * wt;
+    acc.w = acc.w * f + v.w * wt;
+  }
+  const float inv = 1.f / sum;
+  const int hq = u.h * p.group + g;
+  const long long out_row = (long long)u.k.at.row0 + token;
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + u.k.at.plane * p.ob + hq * p.oh + out_row * p.om + 4 * lane) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (p.lse && lane == 0)
+    p.lse[((long long)u.k.at.plane * p.hq + hq) * p.work.m + out_row] = (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+bool multiple(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+int check_tensor(const evict_rows& x, int batch, int m, int heads, bool output, const char* name) {
+  if (!x.data) return fail(EVICT_EINVAL, "%s must not be NULL", name);
+  if (x.heads != heads) return fail(EVICT_EINVAL, "%s has %d heads, not %d", name, x.heads, heads);
+  if (!multiple(x.data, 16) || x.stride_b % 8 || x.stride_h % 8 || x.stride_m % 8)
+    return fail(EVICT_EINVAL, "%s: addresses and strides must be multiples of 16 bytes", name);
+  if (x.stride_b < 0 || x.stride_h < 0 || x.stride_m < 0) return fail(EVICT_EINVAL, "%s: strides must not be negative", name);
+  if ((batch > 1 && !x.stride_b) || (heads > 1 && !x.stride_h) || (m > 1 && !x.stride_m))
+    return fail(EVICT_EINVAL, "%s is expanded (a stride of 0): give every row a place of its own", name);
+  if (output && rows_overlap(x, batch, m)) return fail(EVICT_EINVAL, "%s: rows lie on top of each other", name);
+  return EVICT_OK;
+}
+
+// The kernel's dynamic shared memory, allowed once for each device.
+cudaError_t allow_smem(int dev) {
+  static std::atomic<uint64_t> done{0};
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(prompt_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e == cudaSuccess) done.fetch_or(bit);
+  return e;
+}
+
+int make_plan(const evict_prompt* a, PromptPlan* plan) {
+  const int group = a->q.heads / a->k.heads, half = kTile / group, tile = 2 * half;
+  const int rc = plan_prompt(a, tile, ((long long)a->m + kTile - 1) / kTile, kEntry, kMinSteps, kWholeRows,
+                             2 * kRows * sizeof(float2), 2 * (size_t)kRows * kHeadDim * sizeof(float), plan);
+  plan->p.half = half;
+  return rc;
+}
+
+}  // namespace
+
+int check_prompt_sizes(const evict_prompt* a) {
+  if (!a) return fail(EVICT_EINVAL, "the arguments are NULL");
+  if (a->batch < 0 || a->m < 0) return fail(EVICT_EINVAL, "batch and m must be >= 0 (got %d, %d)", a->batch, a->m);
+  if (a->q.heads < 1 || a->k.heads < 1 || a->q.heads % a->k.heads)
+    return fail(EVICT_EINVAL, "q's heads (%d) must be a multiple of k's (%d)", a->q.heads, a->k.heads);
+  if (a->q.heads / a->k.heads > EVICT_MAX_PROMPT_GROUP)
+    return fail(EVICT_ELIMIT, "%d query heads for a KV head are more than %d", a->q.heads / a->k.heads, EVICT_MAX_PROMPT_GROUP);
+  if (a->starts && (a->batch != 1 || a->n_seqs < 0))
+    return fail(EVICT_EINVAL, "packed sequences lie in a batch of 1 (got %d), and n_seqs must be >= 0 (got %d)", a->batch, a->n_seqs);
+  if (a->starts && a->n_seqs > EVICT_MAX_PROMPT_SEQS)
+    return fail(EVICT_ELIMIT, "%d sequences are more than %d", a->n_seqs, EVICT_MAX_PROMPT_SEQS);
+  if ((long long)a->batch * a->m >= (1ll << 30) || (long long)a->batch * a->m * a->q.heads >= (1ll << 30))
+    return fail(EVICT_ELIMIT, "batch * heads * m is 2^30 or more");
+  return EVICT_OK;
+}
+
+int check_prompt(const evict_prompt* a, bool attention) {
+  if (const int rc = check_prompt_sizes(a)) return rc;
+  if (!std::isfinite(a->scale)) return fail(EVICT_EINVAL, "scale must be finite");
+  if (!multiple(a->starts, 4) || !multiple(a->lse, 4) || !multiple(a->weights, 4) || !multiple(a->error, 4))
+    return fail(EVICT_EINVAL, "starts, lse, weights and error must be 4-byte aligned");
+  if (a->batch == 0 || a->m == 0) return EVICT_OK;
+  int rc;
+  if ((rc = check_tensor(a->q, a->batch, a->m, a->q.heads, false, "q")) ||
+      (rc = check_tensor(a->k, a->batch, a->m, a->k.heads, false, "k")))
+    return rc;
+  if (!attention) {
+    if (!a->lse || !a->weights) return fail(EVICT_EINVAL, "lse and weights must not be NULL");
+    if (a->last < 0) return fail(EVICT_EINVAL, "last must be >= 0 (got %d)", a->last);
+    return EVICT_OK;
+  }
+  if ((rc = check_tensor(a->v, a->batch, a->m, a->k.heads, false, "v")) ||
+      (rc = check_tensor(a->out, a->batch, a->m, a->q.heads, true, "out")))
+    return rc;
+  if (a->out.data == a->q.data || a->out.data == a->k.data || a->out.data == a->v.data)
+    return fail(EVICT_EINVAL, "out must not be q, k or v: they are read while results are written");
+  return EVICT_OK;
+}
+
+// Sizes alone decide: the sequences' lengths are the device's.
+int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry, int min_steps, int whole_rows,
+                size_t part_ml, size_t part, PromptPlan* out) {
+  PromptPlan& P = *out;
+  P = PromptPlan();
+  PromptParams& p = P.p;
+  PromptWork& w = p.work;
+  p.hq = a->q.heads;
+  p.group = a->q.heads / a->k.heads;
+  p.by_group = Divisor(p.group);
+  w.starts = a->starts;
+  w.seqs = a->starts ? a->n_seqs : a->batch;
+  w.m = a->m;
+  w.hkv = a->k.heads;
+  w.tile = tile;
+  w.entry = entry;
+  w.min_steps = min_steps;
+  w.whole = a->m <= whole_rows;
+  const int seq_blocks = (a->m + tile - 1) / tile;
+  const long long blocks = a->starts ? (long long)a->m / tile + a->n_seqs : (long long)a->batch * seq_blocks;
+  if (blocks * w.hkv >= (1ll << 30) || (double)blocks * w.hkv * (double)(most_steps + entry) >= 2147483648.0)
+    return fail(EVICT_ELIMIT, "the sequences are too many or too long for one call");
+  w.blocks = (int)blocks;
+  w.by_hkv = Divisor(w.hkv);
+  w.by_tile = Divisor(tile);
+  w.by_seq_blocks = Divisor(seq_blocks);
+  int dev;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P.sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "looking up the device");
+  P.dev = dev;
+  size_t off = 256;                               // an error word, for callers without one
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += round256(bytes);
+    return at;
+  };
+  w.total = reinterpret_cast<int*>(take(2 * sizeof(int)));
+  w.begin = reinterpret_cast<int2*>(take(P.sms * sizeof(int2)));
+  w.block_base = reinterpret_cast<int*>(take(((size_t)w.seqs + 1) * sizeof(int)));
+  p.part_ml = reinterpret_cast<float2*>(take(w.whole ? 0 : P.sms * part_ml));
+  p.part = reinterpret_cast<float*>(take(w.whole ? 0 : P.sms * part));
+  P.bytes = off;
+  return EVICT_OK;
+}
+
+int bind_prompt(const evict_prompt* a, PromptPlan* plan) {
+  if (!a->workspace || !multiple(a->workspace, 256)) return fail(EVICT_EINVAL, "workspace must be 256-byte aligned");
+  if (a->workspace_bytes < plan->bytes)
+    return fail(EVICT_EINVAL, "workspace has %zu bytes, the call needs %zu", a->workspace_bytes, plan->bytes);
+  if (!encode_tiled()) return fail(EVICT_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  char* base = static_cast<char*>(a->workspace);
+  PromptParams& p = plan->p;
+  auto rebase = [&](auto*& x) { x = reinterpret_cast<std::remove_reference_t<decltype(x)>>(base + reinterpret_cast<size_t>(x)); };
+  rebase(p.work.total);
+  rebase(p.work.begin);
+  rebase(p.work.block_base);
+  rebase(p.part_ml);
+  rebase(p.part);
+  p.work.err = a->error ? a->error : reinterpret_cast<int*>(base);
+  p.lse = a->lse;
+  p.weights = a->weights;
+  p.scale2 = (a->scale == 0.f ? 0.08838834764831845f : a->scale) * kLog2e;
+  return EVICT_OK;
+}
+
+int encode_heads(CUtensorMap* map, const evict_rows& x, int batch, int m, int heads_box, int rows_box, bool heads_first,
+                 const char* name) {
+  // a dimension of extent 1 is never stepped over, but its stride still has to be one the encoder takes
+  const cuuint64_t hs = (x.heads > 1 ? x.stride_h : kHeadDim) * 2, ms = (m > 1 ? x.stride_m : kHeadDim) * 2,
+                   bs = (batch > 1 ? x.stride_b : kHeadDim) * 2;
+  const cuuint64_t hn = (cuuint64_t)x.heads, mn = (cuuint64_t)m;
+  const cuuint64_t dims[4] = {kHeadDim, heads_first ? hn : mn, heads_first ? mn : hn, (cuuint64_t)batch};
+  const cuuint64_t strides[3] = {heads_first ? hs : ms, heads_first ? ms : hs, bs};
+  const cuuint32_t hb = (cuuint32_t)heads_box, mb = (cuuint32_t)rows_box;
+  const cuuint32_t box[4] = {64, heads_first ? hb : mb, heads_first ? mb : hb, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  if (encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, x.data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return fail(EVICT_EINVAL, "%s has sizes or strides beyond a tensor map's", name);
+  return EVICT_OK;
+}
+
+}  // namespace evict
+
+using namespace evict;
+
+extern "C" int evict_prompt_attention_workspace(const evict_prompt* a, size_t* bytes) {
+  if (!bytes) return fail(EVICT_EINVAL, "bytes is NULL");
+  PromptPlan plan;
+  int rc;
+  if ((rc = check_prompt_sizes(a)) || (rc = make_plan(a, &plan))) return rc;
+  *bytes = plan.bytes;
+  return EVICT_OK;
+}
+
+extern "C" int evict_prompt_attention(const evict_prompt* a) {
+  int rc;
+  if ((rc = check_prompt(a, true))) return rc;
+  if (a->batch == 0 || a->m == 0 || (a->starts && a->n_seqs == 0)) return EVICT_OK;
+  PromptPlan plan;
+  if ((rc = make_plan(a, &plan)) || (rc = bind_prompt(a, &plan))) return rc;
+  PromptParams& p = plan.p;
+  p.q = a->q.data, p.qb = a->q.stride_b, p.qh = a->q.stride_h, p.qm = a->q.stride_m;
+  p.k = a->k.data, p.kb = a->k.stride_b, p.kh = a->k.stride_h, p.km = a->k.stride_m;
+  p.v = a->v.data, p.vb = a->v.stride_b, p.vh = a->v.stride_h, p.vm = a->v.stride_m;
+  p.out = a->out.data, p.ob = a->out.stride_b, p.oh = a->out.stride_h, p.om = a->out.stride_m;
+  p.out_sectors = multiple(a->out.data, 32) && a->out.stride_b % 16 == 0 && a->out.stride_h % 16 == 0 && a->out.stride_m % 16 == 0;
+  if ((rc = encode_heads(&p.q_map, a->q, a->batch, a->m, p.group, p.half, true, "q")) ||
+      (rc = encode_heads(&p.k_map, a->k, a->batch, a->m, 1, kTile, false, "k")) ||
+      (rc = encode_heads(&p.v_map, a->v, a->batch, a->m, 1, kTile, false, "v")))
+    return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(a->stream);
+  cudaError_t e = allow_smem(plan.dev);
+  if (e != cudaSuccess) return cuda_fail(e, "prompt attention kernel attribute");
+  const int ctas = p.work.whole ? std::min(plan.sms, p.work.blocks * p.work.hkv) : plan.sms;
+  if ((e = launch_pdl(prompt_attention_kernel, dim3(ctas), dim3(kThreads), kSmem, st, nullptr, p)) != cudaSuccess)
+    return cuda_fail(e, "prompt attention kernel launch");
+  g_launches.fetch_add(1);
+  if (!p.work.whole && ctas > 1) {
+    if ((e = launch_pdl(prompt_join_kernel, dim3(ctas - 1, kRows / kJoinWarps), dim3(kJoinWarps * 32), 0, st, nullptr, p)) != cudaSuccess)
+      return cuda_fail(e, "prompt join kernel launch");
+    g_launches.fetch_add(1);
+  }
+  return EVICT_OK;
+}

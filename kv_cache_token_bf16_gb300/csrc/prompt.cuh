@@ -1,0 +1,256 @@
+// Device side of the prompts' schedule: blocks, units, steps and the share of
+// them that a CTA takes (see prompt.h). The sequences' lengths are the device's.
+// Counts of steps fit 31 bits (the host refuses calls that might pass them).
+#pragma once
+
+#include "attend.cuh"
+#include "common.cuh"
+#include "pipeline.cuh"
+#include "prompt.h"
+#include "tcgen05.cuh"
+
+namespace evict {
+
+// Tokens of a sequence: rows row0 .. row0 + len - 1 of a plane.
+struct Span {
+  int plane, row0, len;
+};
+__device__ __forceinline__ Span span_of(const PromptWork& w, int s) {
+  if (!w.starts) return {s, 0, w.m};
+  const int a = w.starts[s];
+  return {0, a, w.starts[s + 1] - a};
+}
+
+struct PromptBlock {
+  int s, tile;                       // sequence, block of it
+  Span at;
+  int steps;                         // of each of its units
+};
+
+// Block e (below the blocks' number), where sequences are packed the last that begins at or before it.
+// Steps(work, first token, length) are the kernel's.
+template <typename Steps>
+__device__ __forceinline__ PromptBlock block_of(const PromptWork& w, int e, Steps steps) {
+  PromptBlock k;
+  if (!w.starts) {
+    k.s = w.by_seq_blocks.div(e);
+    k.tile = e - k.s * (int)w.by_seq_blocks.by;
+  } else {
+    int lo = 0, hi = w.seqs;
+#pragma unroll 1
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (w.block_base[mid] <= e) lo = mid;
+      else hi = mid;
+    }
+    k.s = lo;
+    k.tile = e - w.block_base[lo];
+  }
+  k.at = span_of(w, k.s);
+  k.steps = steps(k.tile * w.tile, k.at.len);
+  return k;
+}
+
+constexpr int kMaxPromptWarps = 20;
+struct PromptScan {
+  int sum[kMaxPromptWarps];
+  int blocks, e, rest;
+};
+
+// Sum of x over the threads before this one; its total. Between two calls is a barrier.
+template <int kThreads>
+__device__ __forceinline__ int prompt_scan(int x, int& total, PromptScan& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int y = x;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, y, d);
+    if (lane >= d) y += u;
+  }
+  if (lane == 31) sh.sum[warp] = y;
+  __syncthreads();
+  constexpr int kCount = kThreads / 32;
+  int u = lane < kCount ? sh.sum[lane] : 0;
+#pragma unroll
+  for (int d = 1; d < kCount; d <<= 1) {
+    const int s = __shfl_up_sync(0xffffffffu, u, d);
+    if (lane >= d) u += s;
+  }
+  total = __shfl_sync(0xffffffffu, u, kCount - 1);
+  return y - x + (warp ? __shfl_sync(0xffffffffu, u, warp - 1) : 0);
+}
+
+// The blocks' number, 0 where the sequences are not one behind the other inside the plane: then the call
+// writes nothing but the error. All threads. Every CTA leaves the same block_base, and reads back its own.
+template <int kThreads>
+__device__ __forceinline__ int count_blocks(const PromptWork& w, PromptScan& sh) {
+  if (!w.starts) return w.blocks;
+  const int tid = threadIdx.x, per = (w.seqs + kThreads - 1) / kThreads;
+  const int s0 = min(tid * per, w.seqs), s1 = min(s0 + per, w.seqs);
+  int bad = 0, mine = 0;
+#pragma unroll 1
+  for (int s = s0; s < s1; ++s) {
+    const int a = w.starts[s], b = w.starts[s + 1];
+    if (a < 0 || b < a || b > w.m) bad = 1;
+    else mine += w.by_tile.div(b - a + w.tile - 1);
+  }
+  if (__syncthreads_or(bad)) {
+    if (blockIdx.x == 0 && tid == 0) raise_device_error(w.err, kDevBadIndex);
+    return 0;
+  }
+  int total, base = prompt_scan<kThreads>(mine, total, sh);
+#pragma unroll 1
+  for (int s = s0; s < s1; ++s) {
+    w.block_base[s] = base;
+    base += w.by_tile.div(w.starts[s + 1] - w.starts[s] + w.tile - 1);
+  }
+  __syncthreads();
+  return total;
+}
+
+// A CTA's way through its units.
+struct PromptCursor {
+  PromptBlock k;
+  int blocks;
+  int e, h;
+  int from, to;                      // steps of the unit that are this CTA's
+  int left;                          // of the share, from `from` on; whole: of the units
+};
+
+// The steps of the unit at hand behind `step` (negative: in its entry); false where the share ends before.
+__device__ __forceinline__ bool settle(PromptCursor& c, int step) {
+  if (step < 0) {
+    const int pay = min(c.left, -step);
+    step += pay;
+    c.left -= pay;
+  }
+  if (c.left <= 0) return false;
+  c.from = step;
+  c.to = min(c.k.steps, step + c.left);
+  return true;
+}
+
+// On to the next unit; false at the share's end.
+template <typename Steps>
+__device__ __forceinline__ bool next_unit(const PromptWork& w, PromptCursor& c, Steps steps) {
+  if (w.whole) {
+    c.left -= gridDim.x;
+    if (c.left <= 0) return false;
+    c.h += gridDim.x;
+    if (c.h >= w.hkv) {
+      const int up = w.by_hkv.div(c.h);
+      c.e += up;
+      c.h -= up * w.hkv;
+      c.k = block_of(w, c.e, steps);
+    }
+    c.from = 0;
+    c.to = c.k.steps;
+    return true;
+  }
+  c.left -= c.to - c.from;
+  if (c.left <= 0) return false;
+  if (++c.h == w.hkv) {
+    c.h = 0;
+    c.k = block_of(w, ++c.e, steps);
+  }
+  return settle(c, -w.entry);
+}
+
+// Where this CTA's share begins; false where it has none. All threads call it, and again nothing of `sh`
+// is written after it. The shares are left for the join.
+template <int kThreads, typename Steps>
+__device__ __forceinline__ bool first_unit(const PromptWork& w, PromptScan& sh, PromptCursor& c, Steps steps) {
+  c.blocks = count_blocks<kThreads>(w, sh);
+  if (w.whole) {
+    const int units = c.blocks * w.hkv;
+    if ((int)blockIdx.x >= units) return false;
+    c.left = units - blockIdx.x;
+    c.e = w.by_hkv.div(blockIdx.x);
+    c.h = blockIdx.x - c.e * w.hkv;
+    c.k = block_of(w, c.e, steps);
+    c.from = 0;
+    c.to = c.k.steps;
+    return true;
+  }
+  const int tid = threadIdx.x, per = (c.blocks + kThreads - 1) / kThreads;
+  const int e0 = min(tid * per, c.blocks), e1 = min(e0 + per, c.blocks);
+  int mine = 0;
+#pragma unroll 1
+  for (int e = e0; e < e1; ++e) mine += (block_of(w, e, steps).steps + w.entry) * w.hkv;
+  int total, base = prompt_scan<kThreads>(mine, total, sh);
+  const Shares shares(total, total ? max(1, min((int)gridDim.x, total / w.min_steps)) : 0);
+  const bool has = (int)blockIdx.x < shares.count;
+  const int g0 = has ? shares.begin(blockIdx.x) : 0;
+  if (blockIdx.x == 0 && tid == 0) {
+    w.total[0] = total;
+    w.total[1] = shares.count;
+  }
+  if (!has) return false;                         // the whole CTA
+  if (g0 >= base && g0 < base + mine) {
+#pragma unroll 1
+    for (int e = e0; e < e1; ++e) {
+      const int of_block = (block_of(w, e, steps).steps + w.entry) * w.hkv;
+      if (g0 < base + of_block) {
+        sh.e = e;
+        sh.rest = g0 - base;
+        w.begin[blockIdx.x] = make_int2(e, g0 - base);
+        break;
+      }
+      base += of_block;
+    }
+  }
+  __syncthreads();
+  c.e = sh.e;
+  c.k = block_of(w, c.e, steps);
+  const int unit = c.k.steps + w.entry;
+  c.h = sh.rest / unit;
+  c.left = shares.begin(blockIdx.x + 1) - g0;
+  c.from = c.to = 0;
+  if (settle(c, sh.rest - c.h * unit - w.entry)) return true;
+  return false;                                   // the share lies in one unit's entry
+}
+
+// A unit that two or more CTAs share, found where a share begins inside it: the first such share's
+// block does the work. Its parts: slot 2 c0 + 1, then 2 c of the following shares up to c1.
+struct SplitUnit {
+  PromptBlock k;
+  int h, c0, c1;
+};
+template <typename Steps>
+__device__ __forceinline__ bool split_unit(const PromptWork& w, int c, SplitUnit& u, Steps steps) {
+  const Shares shares(w.total[0], w.total[1]);
+  if (c >= shares.count) return false;
+  const int2 at = w.begin[c];
+  u.k = block_of(w, at.x, steps);
+  const int per = u.k.steps + w.entry;
+  u.h = at.y / per;
+  const int step = at.y - u.h * per - w.entry;
+  if (step <= 0) return false;                    // the share begins with the unit, or in its entry
+  const int first = shares.begin(c) - step;
+  u.c0 = shares.of(first);
+  u.c1 = shares.of(first + u.k.steps - 1);
+  return u.c0 == c - 1;
+}
+
+// Whether a phase is over, without a wait.
+__device__ __forceinline__ bool test_phase(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+
+}  // namespace evict

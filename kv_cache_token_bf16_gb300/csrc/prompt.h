@@ -1,0 +1,72 @@
+// Launch parameters of the prompts' kernels: attention (prompt.cu), weights of keys (weights.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/evict.h"
+#include "attend.h"
+
+namespace evict {
+
+// The work of one call. A block is `tile` tokens of one sequence; a unit is a
+// block and a KV head, and its work a number of steps that the kernel knows,
+// behind `entry` more for its start. The blocks' units, in the order of blocks
+// and heads, are laid end to end and cut into equal contiguous shares, one for
+// a CTA. `whole`: units are not cut; CTA i takes units i, i + CTAs, ...
+struct PromptWork {
+  const int32_t* starts;             // [seqs + 1] first rows of the sequences of one plane; or NULL: a plane each
+  int seqs, m;                       // sequences; rows of a plane
+  int hkv;
+  int tile;                          // tokens of a block
+  int blocks;                        // at most
+  int entry, min_steps;              // steps that a unit's start counts as; of a share at least
+  int whole;
+  Divisor by_hkv, by_tile, by_seq_blocks;
+  int* block_base;                   // [seqs + 1] blocks of the sequences before (packed)
+  int2* begin;                       // [CTAs] block and rest in it where a share begins
+  int* total;                        // [2] steps of all units, the shares' number
+  int* err;
+};
+
+struct PromptParams {
+  CUtensorMap q_map, k_map, v_map;
+  PromptWork work;
+  const void* q;                     // (the attention's rare path)
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;
+  float* weights;
+  long long qb, qh, qm, kb, kh, km, vb, vh, vm, ob, oh, om;   // element strides
+  int hq, group;                     // group = query heads of a KV head
+  Divisor by_group;
+  int half;                          // attention: tokens of a tile of 128 query rows
+  int out_sectors;                   // every row of out begins on a multiple of 32 bytes
+  int last;                          // weights: the last queries of a sequence that count
+  float scale2;                      // log2(e) * scale
+  float2* part_ml;                   // attention: [2 CTAs][256] maximum (base 2) and sum
+  float* part;                       // attention: [2 CTAs][256][128] outputs; weights: [2 CTAs][256] sums
+};
+
+// The checks of a call's sizes, and of its pointers as well (prompt.cu).
+int check_prompt_sizes(const evict_prompt* a);
+int check_prompt(const evict_prompt* a, bool attention);
+// The schedule and the workspace, with offsets in place of pointers until bind_prompt.
+struct PromptPlan {
+  int dev, sms;
+  PromptParams p;
+  size_t bytes;
+};
+// tile, entry, min_steps: as above; most_steps: of a unit; whole_rows: planes of so many rows are not cut; part_ml, part:
+// bytes of a CTA's partial results.
+int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry, int min_steps, int whole_rows,
+                size_t part_ml, size_t part, PromptPlan* out);
+int bind_prompt(const evict_prompt* a, PromptPlan* plan);
+// Boxes of heads_box heads of rows_box rows of 64 elements, 128-byte swizzle: a row's heads one behind the other
+// (heads_first; coordinates element, head, row, plane), or a head's rows (element, row, head, plane).
+int encode_heads(CUtensorMap* map, const evict_rows& x, int batch, int m, int heads_box, int rows_box, bool heads_first,
+                 const char* name);
+
+}  // namespace evict

@@ -57,7 +57,8 @@ def _load():
     packed = ctypes.c_char_p
     for name, args in (("evict_rotate", [p, i, i, i, p, q, i, packed, packed, i, p]),
                        ("evict_paged_append", [p, i, i, p, p, p, q, packed, packed, packed, packed, p]),
-                       ("evict_shared_attention", [packed])):
+                       ("evict_shared_attention", [packed]),
+                       ("evict_weigh", [p, packed, i, i, p, p, ctypes.c_float, p])):
         fn = getattr(calls, name)
         fn.restype, fn.argtypes = i, args
     _calls = calls                               # before _torch, which other threads take as the sign
@@ -323,6 +324,27 @@ def shared_attention(q, prefix=None, pages: "PagedCache | None" = None, n_new=No
     work = _torch.empty(size, dtype=_torch.uint8, device=q.device)
     _call(index, _calls.evict_shared_attention, _ATTENTION.pack(*head, work.data_ptr(), size, error, _stream(index)))
     return out
+
+
+def weigh_rows(cache, q, lse, n_new=None, scale=None):
+    """``EvictCache.weigh`` without its order between streams."""
+    if _torch is None:
+        _load()
+    if _recording() and (q.requires_grad or lse.requires_grad):
+        _no_history()
+    index, shape = _device(q), q.shape
+    if len(shape) != 4:
+        raise ValueError(f"q must be [batch, heads, m, {HEAD_DIM}], not {tuple(shape)}")
+    batch, hq, m, _ = shape
+    qr = _ROWS.pack(*_rows(q, "q", index, _torch.bfloat16, batch, m))
+    if scale is None:
+        scale = 0.0
+    elif scale == 0:
+        raise ValueError("scale must not be 0")
+    if lse is None:
+        raise ValueError("lse must be given")
+    _call(index, _calls.evict_weigh, cache.handle, qr, batch, m, _like(lse, "lse", (batch, hq, m), _torch.float32, index),
+          _like(n_new, "n_new", (batch,), _torch.int32, index) or None, scale, _stream(index))
 
 
 def _page_strides(k_pages, table):

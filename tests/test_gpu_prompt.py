@@ -1,0 +1,274 @@
+"""Attention of whole prompts and the weights of their keys, against plain 64-bit forms."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from kv_cache_token_bf16_gb300 import binding, prompt  # noqa: E402
+from tests.paged_util import D  # noqa: E402
+from tests.prompt_util import SCALE, check_prompt, check_weights, spans_of, weights64  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built(lib):
+    pass
+
+
+def rows(seed, batch, heads, m, layout="token", std=1.0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    if layout == "token":
+        return torch.randn(batch, m, heads, D, device="cuda", generator=g).mul_(std).bfloat16().transpose(1, 2)
+    if layout == "wide":                             # rows apart from each other, heads among other tensors'
+        x = torch.randn(batch, m + 1, heads + 3, 2 * D, device="cuda", generator=g).mul_(std).bfloat16()
+        return x[:, :m, 1:heads + 1, D:].transpose(1, 2)
+    return torch.randn(batch, heads, m, D, device="cuda", generator=g).mul_(std).bfloat16()
+
+
+def starts_of(lens, lead=0):
+    got = [lead]
+    for l in lens:
+        got.append(got[-1] + l)
+    return got
+
+
+def run(q, k, v, starts=None, last=0, scale=None, layout="token"):
+    """Both calls, checked."""
+    B, hq, m, _ = q.shape
+    pk = prompt.Packing(torch.tensor(starts, dtype=torch.int32).cuda()) if starts is not None else None
+    out = torch.full((B, m, hq, D), 5.0, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+    if layout == "head":
+        out = out.contiguous()
+    lse = torch.full((B, hq, m), 7.0, device="cuda")
+    assert prompt.attention(q, k, v, pk, scale=scale, out=out, lse=lse) is out
+    w = torch.full((B, k.shape[1], m), 3.0, device="cuda")
+    assert prompt.weights(q, k, lse, pk, last=last, scale=scale, out=w) is w
+    torch.cuda.synchronize()
+    if pk is not None:
+        pk.sync()
+    spans = spans_of(starts, B, m)
+    at = SCALE if scale is None else scale
+    check_prompt(q, k, v, spans, out, lse, at, 5.0, 7.0)
+    check_weights(w, *weights64(q, k, lse, spans, last, at), 3.0)
+    return out, lse, w
+
+
+@pytest.mark.parametrize("hq,hkv,lens,last", [
+    (1, 1, [1], 0), (8, 2, [1, 1, 1], 1), (8, 8, [5], 3), (3, 1, [33, 64], 0), (12, 4, [1, 45, 20, 7], 0),
+    (4, 4, [127, 128, 129], 0), (4, 4, [255, 256, 257], 5), (32, 8, [63, 64, 65, 31, 32, 33], 16),
+    (28, 4, [17, 18, 19, 36, 37, 300], 0), (40, 8, [25, 50, 51, 401], 64), (24, 1, [200, 5], 7),
+    (128, 1, [3, 130], 0), (100, 1, [140], 0), (65, 1, [70], 0),
+    (8, 2, [300, 0, 1, 77, 513], 0), (8, 2, [0, 0, 40, 0], 32), (16, 2, [500, 524], 513),
+    (8, 2, [1024], 0), (8, 2, [1025], 0), (8, 2, [900, 200], 1), (4, 4, [2049, 3], 0), (28, 4, [1500, 700], 64),
+    (3, 1, [2048, 3, 1100], 0), (32, 8, [1] * 300, 0), (8, 8, [7] * 200, 4), (2, 2, [6000], 0), (2, 1, [4097, 4096], 4000)])
+def test_packed_prompts(hq, hkv, lens, last):
+    starts = starts_of(lens, 3)
+    m = starts[-1] + 11
+    q, k, v = rows(1, 1, hq, m, std=1.5), rows(2, 1, hkv, m), rows(3, 1, hkv, m)
+    run(q, k, v, starts, last)
+
+
+@pytest.mark.parametrize("layout", ["token", "head", "wide"])
+@pytest.mark.parametrize("batch,m,hq,hkv,last,scale", [
+    (1, 1, 4, 4, 0, None), (3, 100, 8, 2, 0, 0.11), (2, 257, 3, 1, 1, None), (2, 1100, 16, 2, 0, -0.07), (3, 1300, 10, 2, 100, None)])
+def test_batches(layout, batch, m, hq, hkv, last, scale):
+    q, k, v = rows(4, batch, hq, m, layout, 1.5), rows(5, batch, hkv, m, layout), rows(6, batch, hkv, m, layout)
+    run(q, k, v, None, last, scale, layout)
+
+
+def test_no_tokens():
+    for m, starts in ((0, None), (0, [0]), (0, [0, 0]), (6, [2]), (6, [4, 4, 4])):
+        q, k, v = rows(7, 1, 4, m), rows(8, 1, 2, m), rows(9, 1, 2, m)
+        run(q, k, v, starts)
+    assert prompt.attention(rows(7, 0, 4, 5), rows(8, 0, 2, 5), rows(9, 0, 2, 5)).shape == (0, 4, 5, D)
+    # new outputs: zeros where there is no sequence
+    pk = prompt.Packing(torch.tensor([1, 3], dtype=torch.int32).cuda())
+    q, k, v = rows(7, 1, 4, 6), rows(8, 1, 2, 6), rows(9, 1, 2, 6)
+    lse = torch.zeros(1, 4, 6, device="cuda")
+    out = prompt.attention(q, k, v, pk, lse=lse)
+    w = prompt.weights(q, k, lse, pk)
+    assert not out[:, :, [0, 3, 4, 5]].any() and out[:, :, 1:3].any(3).all()
+    assert not w[:, :, [0, 3, 4, 5]].any() and (w[:, :, 1:3] > 0).all()
+
+
+@pytest.mark.parametrize("rising", [True, False])
+def test_logits_that_rise_and_fall(rising):
+    # the reference of the exponents has to follow: each key's logit tops the last ones' by far, in a step and over steps
+    m, hq, hkv = 1200, 4, 2
+    q, k, v = rows(10, 1, hq, m, std=0.05), rows(11, 1, hkv, m, std=0.3), rows(12, 1, hkv, m)
+    size = torch.linspace(0.0, 60.0, m, device="cuda")
+    if not rising:
+        size = size.flip(0)
+    q[..., 0] = 8.0
+    k[..., 0] = size.bfloat16()
+    run(q, k, v, [0, 1100, 1200])
+    k[..., 0] = (size * torch.where(torch.arange(m, device="cuda") % 97 == 5, 2.0, 0.1)).bfloat16()   # a few tower
+    run(q, k, v, [0, 1100, 1200])
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 4), (8, 2)])
+def test_what_a_query_does_not_see_may_hold_anything(hq, hkv):
+    lens = [40, 300, 130, 1, 600, 90]
+    starts = starts_of(lens, 5)
+    m = starts[-1] + 9
+    q, k, v = rows(13, 1, hq, m, std=1.5), rows(14, 1, hkv, m), rows(15, 1, hkv, m)
+    spans = spans_of(starts, 1, m)
+    clean = [x.clone() for x in (q, k, v)]
+    was = run(q, k, v, starts)
+    # tokens of no sequence, and a whole sequence between others
+    for x in (q, k, v):
+        for a, e, bad in ((0, 5, math.nan), (starts[-1], m, math.inf), (starts[2], starts[3], -math.inf), (starts[2] + 7, starts[2] + 8, math.nan)):
+            x[:, :, a:e] = bad
+    pk = prompt.Packing(torch.tensor(starts, dtype=torch.int32).cuda())
+    lse = torch.full((1, hq, m), 7.0, device="cuda")
+    got = prompt.attention(q, k, v, pk, lse=lse)
+    w = prompt.weights(q, k, lse, pk)
+    pk.sync()
+    for i, (_, a, l) in enumerate(spans):
+        if i == 2:
+            continue
+        for x, y in zip((got, lse, w), was):
+            assert torch.equal(x[:, :, a:a + l], y[:, :, a:a + l]), i
+    # rows of V that later queries of the same tile see, and earlier ones do not
+    q, k, v = clean
+    for row, bad in ((starts[1] + 150, math.inf), (starts[1] + 151, math.nan), (starts[4] + 599, -math.inf), (starts[4] + 1, math.nan),
+                     (starts[3], math.inf)):
+        v[:, 0, row, 7] = bad
+    got = prompt.attention(q, k, v, pk, lse=lse)
+    pk.sync()
+    check_prompt(q, k, v, spans, got, lse)
+
+
+def test_infinite_rows_in_long_prompts_and_parts_of_units():
+    m, hq, hkv = 3000, 4, 2
+    q, k, v = rows(16, 1, hq, m, std=0.3), rows(17, 1, hkv, m, std=0.3), rows(18, 1, hkv, m)
+    for row in (0, 100, 127, 128, 1000, 1500, 2047, 2048, 2500, 2998, 2999):
+        v[:, row % 2, row, row % 128] = math.inf if row % 3 else -math.inf
+    lse = torch.zeros(1, hq, m, device="cuda")
+    got = prompt.attention(q, k, v, lse=lse)
+    torch.cuda.synchronize()
+    check_prompt(q, k, v, [(0, 0, m)], got, lse)
+
+
+def test_keys_and_queries_of_infinities_and_nan():
+    # a key that is NaN reaches the queries that see it; so does one whose logit is +infinity; one of -infinity has no weight
+    m = 200
+    q, k, v = rows(19, 1, 2, m).abs(), rows(20, 1, 2, m), rows(21, 1, 2, m)
+    k[0, 0, 50] = math.nan
+    k[0, 1, 60, 3] = -math.inf
+    lse = torch.zeros(1, 2, m, device="cuda")
+    got = prompt.attention(q, k, v, lse=lse)
+    assert torch.isnan(got[0, 0, 50:]).all() and torch.isfinite(got[0, 0, :50]).all()
+    assert torch.isnan(lse[0, 0, 50:]).all() and torch.isfinite(lse[0, 0, :50]).all()
+    check_prompt(q[:, 1:], k[:, 1:], v[:, 1:], [(0, 0, m)], got[:, 1:], lse[:, 1:])
+    q[0, 1, 100] = math.nan
+    got = prompt.attention(q, k, v, lse=lse)
+    assert torch.isnan(got[0, 1, 100]).all() and torch.isfinite(got[0, 1, [99, 101]]).all()
+    w = prompt.weights(q, k, lse)
+    assert torch.isnan(w[0, 1, :101]).sum() == 101 and torch.isfinite(w[0, 1, 101:]).all()
+    # a first key of -infinity: the query that sees it alone has no weights that add up
+    k[0, 1, 0, 3] = -math.inf
+    got = prompt.attention(q, k, v, lse=lse)
+    assert lse[0, 1, 0] == -math.inf and torch.isfinite(lse[0, 1, 1:100]).all()
+    w = prompt.weights(q, k, lse)
+    assert torch.isnan(w[0, 1, 0])                  # of query 100 alone: query 0 has no weights
+
+
+def test_weights_of_queries_that_saw_nothing():
+    m = 300
+    q, k = rows(22, 1, 4, m), rows(23, 1, 2, m)
+    lse = torch.randn(1, 4, m, device="cuda", generator=torch.Generator("cuda").manual_seed(24)) + 5
+    lse[0, :, 17] = lse[0, 2, 200:] = -math.inf
+    lse[0, 1, 40] = math.inf
+    check_weights(prompt.weights(q, k, lse), *weights64(q, k, lse, [(0, 0, m)]))
+
+
+@pytest.mark.parametrize("lens", [[300, 1, 77], [1700, 900]])
+def test_the_same_bits_every_time(lens):
+    starts = starts_of(lens)
+    m = starts[-1]
+    q, k, v = rows(25, 1, 8, m, std=1.5), rows(26, 1, 2, m), rows(27, 1, 2, m)
+    pk = prompt.Packing(torch.tensor(starts, dtype=torch.int32).cuda())
+    got = []
+    for _ in range(4):
+        lse = torch.zeros(1, 8, m, device="cuda")
+        out = prompt.attention(q, k, v, pk, lse=lse)
+        got.append((out, lse, prompt.weights(q, k, lse, pk)))
+    pk.sync()
+    for x in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(x, got[0]))
+
+
+@pytest.mark.parametrize("starts", [[0, 50, 40, 100], [-1, 50, 100], [0, 50, 2001], [5, 3]])
+@pytest.mark.parametrize("m", [900, 2000])
+def test_starts_that_fall_or_leave_the_tensors_write_nothing(starts, m):
+    if m == 900 and 2001 in starts:
+        starts = [0, 50, 901]
+    q, k, v = rows(28, 1, 4, m), rows(29, 1, 2, m), rows(30, 1, 2, m)
+    pk = prompt.Packing(torch.tensor(starts, dtype=torch.int32).cuda())
+    out, lse, w = torch.full_like(q, 5.0), torch.full((1, 4, m), 7.0, device="cuda"), torch.full((1, 2, m), 3.0, device="cuda")
+    for call in (lambda: prompt.attention(q, k, v, pk, out=out, lse=lse), lambda: prompt.weights(q, k, lse, pk, out=w)):
+        call()
+        with pytest.raises(binding.EvictError, match="index") as e:
+            pk.sync()
+        assert e.value.code == binding.EVICT_EDEVICE
+        pk.sync()
+    assert (out == 5).all() and (lse == 7).all() and (w == 3).all()
+    pk.starts.copy_(torch.linspace(0, m, len(starts)).int())     # put right in place
+    prompt.attention(q, k, v, pk, out=out, lse=lse)
+    pk.sync()
+    check_prompt(q, k, v, spans_of(pk.starts.tolist(), 1, m), out, lse)
+
+
+def test_captured_calls_follow_the_starts():
+    m = 1400
+    q, k, v = rows(31, 1, 8, m), rows(32, 1, 2, m), rows(33, 1, 2, m)
+    pk = prompt.Packing(torch.tensor([0, 10, 1400], dtype=torch.int32).cuda())
+    out, lse, w = torch.zeros_like(q), torch.zeros(1, 8, m, device="cuda"), torch.zeros(1, 2, m, device="cuda")
+
+    def both():
+        prompt.attention(q, k, v, pk, out=out, lse=lse)
+        prompt.weights(q, k, lse, pk, last=40, out=w)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        both()
+    torch.cuda.current_stream().wait_stream(s)
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    for g in (g1, g2):
+        with torch.cuda.graph(g):
+            both()
+    for g, starts in ((g1, [0, 10, 1400]), (g2, [3, 700, 701]), (g1, [0, 0, 1399]), (g2, [100, 200, 1300])):
+        pk.starts.copy_(torch.tensor(starts, dtype=torch.int32))
+        q.copy_(rows(40 + starts[1], 1, 8, m))
+        out.fill_(5.0)
+        lse.fill_(7.0)
+        w.fill_(3.0)
+        g.replay()
+        pk.sync()
+        spans = spans_of(starts, 1, m)
+        check_prompt(q, k, v, spans, out, lse, out_was=5.0, lse_was=7.0)
+        check_weights(w, *weights64(q, k, lse, spans, 40), 3.0)
+
+
+def test_two_streams_at_once():
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    args = []
+    for i in range(2):
+        m = 1500 + 200 * i
+        args.append((rows(50 + i, 1, 8, m), rows(60 + i, 1, 2, m), rows(70 + i, 1, 2, m), torch.zeros(1, 8, m, device="cuda")))
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            q, k, v, lse = args[i]
+            with torch.cuda.stream(s):
+                out = prompt.attention(q, k, v, lse=lse)
+                got[i] = (out, prompt.weights(q, k, lse))
+    torch.cuda.synchronize()
+    for (q, k, v, lse), (out, w) in zip(args, got):
+        spans = [(0, 0, q.shape[2])]
+        check_prompt(q, k, v, spans, out, lse)
+        check_weights(w, *weights64(q, k, lse, spans))
