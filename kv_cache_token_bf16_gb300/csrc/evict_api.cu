@@ -272,7 +272,7 @@ int run_intrinsic(evict_handle* const* hs, int n_layers, const void* const* k, c
     P.s.zero_scores = 0;
   }
   if (n <= h->cfg.budget) {
-    e = timed_launch(h, kKidAppend, [&] { return launch_append(P, h->elem, h->stream); });
+    e = timed_launch(h, kKidAppend, [&] { return given ? launch_append_given(P, h->stream) : launch_append(P, h->elem, h->stream); });
     if (e != cudaSuccess) return cuda_fail(e, "append kernel launch");
     for (int l = 0; l < n_layers; ++l) {
       hs[l]->n_kept = (int)n;

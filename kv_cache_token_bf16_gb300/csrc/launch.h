@@ -38,6 +38,8 @@ int compact_flag_slots(int rows, int dtype_bytes);
 
 cudaError_t launch_score(const GroupParams& P, int dtype_bytes, cudaStream_t st);
 cudaError_t launch_append(const GroupParams& P, int dtype_bytes, cudaStream_t st);
+// The append of rows whose scores are in new_score (attention weights; bf16).
+cudaError_t launch_append_given(const GroupParams& P, cudaStream_t st);
 // Raise the select kernel's dynamic shared memory limit (current device) to
 // hold EVICT_MAX_SELECT_ROWS keys.
 cudaError_t prepare_select();

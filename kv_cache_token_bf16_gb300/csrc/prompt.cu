@@ -7,13 +7,13 @@
 // A unit is a (sequence, KV head, tile of tokens): the tokens' query rows of the whole group, token by
 // token, fill two tiles of 128 rows, so that K and V are read once for all of the group's heads and few
 // rows at the diagonal go unseen. Warps 0-3 and 4-7 are two softmax groups, a thread per query row, each
-// with its own 128 x 128 logits and 128 x 128 output accumulator in tensor memory (512 columns in all).
-// Warp 8 issues the tensor cores' work of both in turn:
-//     S = Q K^T -> P = 2^(S scale - ref) as bf16 over S (softmax group) -> O += P V,
-// the product with V in halves of 64 rows, so that it begins while the second half is exponentiated; one
-// group's products run while the other exponentiates. Warp 9 fetches (TMA): K and V through a ring of five
-// 32 KB tiles of 128 rows, the queries of the next unit as soon as the last product that reads a tile is
-// through. Warp 10 clears rows of V that only some of the unit's queries see, or none (see scrub).
+// with its own 128 x 128 logits and 128 x 128 output accumulator in tensor memory (512 columns in all);
+// warps 8 and 9 issue the tensor cores' work of one group each, in halves of 64 rows of K and V:
+//     S = Q K^T -> P = 2^(S scale - ref) as bf16 over S (softmax group) -> O += P V.
+// While the group exponentiates one half, the logits of the other are made, of the next unit as well.
+// Warp 10 fetches (TMA): K and V through a ring of five 32 KB tiles of 128 rows, the queries of the next
+// unit as soon as the last product that reads a tile is through. Warp 11 clears rows of V that only some
+// of the unit's queries see, or none (see scrub).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -38,17 +38,17 @@ constexpr int kTileBytes = kTile * kHeadDim * 2;
 constexpr int kRows = 2 * kTile;                  // query rows of a unit
 constexpr int kRing = 5;
 constexpr int kSmem = 1024 + (2 + kRing) * kTileBytes;
-constexpr int kMmaWarp = 8, kTmaWarp = 9, kThreads = 352;   // warp 10 scrubs
+constexpr int kMmaWarp = 8, kTmaWarp = 10, kThreads = 384;   // warp 11 scrubs
 constexpr int kBadWords = kRows / 32;             // rows of V behind the unit's first token, a bit each
 constexpr int kBadSets = 8;                       // of a CTA's units in turn
 constexpr int kPartly = 4;                        // barriers of tiles to scrub, in turn: the ring holds at most three
 constexpr float kMoveAbove = 4096.f;              // sum of 32 weights that makes the reference move
-constexpr int kEntry = 1, kMinSteps = 4;
+constexpr int kEntry = 2, kMinSteps = 4;
 constexpr int kWholeRows = 1024;
 
 struct AttentionShared {
   uint64_t q_full[2], q_empty[2], kv_full[kRing], kv_empty[kRing], partly_full[kPartly], scrubbed[kPartly];
-  uint64_t s_full[2], p_full[2][2], first_half[2], o_full[2], done;
+  uint64_t s_full[2][2], p_full[2][2], o_full[2][2], done[2];   // group, half of the step
   uint32_t tmem_base;
   int fail;
   uint32_t bad[kBadSets][kBadWords];
@@ -63,16 +63,16 @@ struct Steps {
 // A unit's part, as every role sees it.
 struct Part {
   int tok0, reach;                                // first token; last one
-  int n[2];                                       // steps of the two groups (from c.from on); n[1] >= n[0] or 0
+  int n0, n1;                                     // steps of the two groups (from c.from on); n1 >= n0 or 0
   __device__ __forceinline__ Part(const PromptParams& p, const PromptCursor& c) {
     tok0 = c.k.tile * p.work.tile;
     reach = min(tok0 + p.work.tile, c.k.at.len) - 1;
     const int first_reach = min(tok0 + p.half - 1, reach);        // of the first group's tokens
-    n[0] = min(c.to, first_reach / kTile + 1) - c.from;
-    n[0] = max(n[0], 0);
-    n[1] = first_reach < reach ? c.to - c.from : 0;
+    n0 = max(min(c.to, first_reach / kTile + 1) - c.from, 0);
+    n1 = first_reach < reach ? c.to - c.from : 0;
   }
-  __device__ __forceinline__ int steps() const { return max(n[0], n[1]); }
+  __device__ __forceinline__ int n(int w) const { return w ? n1 : n0; }
+  __device__ __forceinline__ int steps() const { return max(n0, n1); }
   // the step's rows of V hold some that not every query of the unit sees
   __device__ __forceinline__ bool partly(int step) const { return step * kTile + kTile - 1 > tok0; }
 };
@@ -85,10 +85,26 @@ struct Slot {
   }
 };
 
+// Bounds a warp's polling (the clock is read rarely).
+struct Watch {
+  uint32_t polls = 0;
+  uint64_t t0 = 0;
+  __device__ __forceinline__ bool go_on(AttentionShared& sh, int* err) {
+    if ((++polls & 1023) != 0) return true;
+    if (*(volatile int*)&sh.fail) return false;
+    const uint64_t t = tc::global_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 <= kWaitLimitNs) return true;
+    *(volatile int*)&sh.fail = 1;
+    raise_device_error(err, kDevWaitTimeout);
+    return false;
+  }
+};
+
 __device__ void producer(const PromptParams& p, AttentionShared& sh, PromptCursor c, uint32_t qbuf, uint32_t ring) {
   const Steps steps{p.work.tile};
   Slot slot;
-  int used = 0, turns[2] = {0, 0}, partly = 0;
+  int used = 0, turns0 = 0, turns1 = 0, partly = 0;
   bool ok = true;
   // a tile to be scrubbed lands on a barrier of the scrubbing warp's, and its slot counts as full at once
   auto load_kv = [&](const CUtensorMap* map, int step, bool to_scrub) {
@@ -110,9 +126,9 @@ __device__ void producer(const PromptParams& p, AttentionShared& sh, PromptCurso
     const int n = part.steps();
     load_kv(&p.k_map, c.from, false);
     for (int w = 0; w < 2 && ok; ++w) {
-      if (part.n[w] == 0) continue;
-      if (!(ok = wait_phase(&sh.q_empty[w], (turns[w] & 1) ^ 1, &sh.fail, p.work.err))) break;
-      ++turns[w];
+      if (part.n(w) == 0) continue;
+      const int turn = w ? turns1++ : turns0++;
+      if (!(ok = wait_phase(&sh.q_empty[w], (turn & 1) ^ 1, &sh.fail, p.work.err))) break;
       tc::mbar_arrive_expect_tx(&sh.q_full[w], 2 * p.half * p.group * 128);
       for (int hf = 0; hf < 2; ++hf)
         tma_load_4d(qbuf + w * kTileBytes + hf * (kTileBytes / 2), &p.q_map, hf * 64, c.h * p.group,
@@ -127,8 +143,8 @@ __device__ void producer(const PromptParams& p, AttentionShared& sh, PromptCurso
   // every copy issued must land before the CTA may release its shared memory
   for (int i = 0; i < kRing && i < used; ++i) drain_phase(&sh.kv_full[i], ((used - 1 - i) / kRing) & 1, p.work.err);
   for (int i = 0; i < kPartly && i < partly; ++i) drain_phase(&sh.partly_full[i], ((partly - 1 - i) / kPartly) & 1, p.work.err);
-  for (int w = 0; w < 2; ++w)
-    if (turns[w]) drain_phase(&sh.q_full[w], (turns[w] - 1) & 1, p.work.err);
+  if (ok && turns0) drain_phase(&sh.q_full[0], (turns0 - 1) & 1, p.work.err);
+  if (ok && turns1) drain_phase(&sh.q_full[1], (turns1 - 1) & 1, p.work.err);
 }
 
 // Rows of V that a query does not see meet a weight of 0, but 0 * infinity is not 0. Rows behind the unit's
@@ -189,111 +205,138 @@ __device__ void scrub(const PromptParams& p, AttentionShared& sh, PromptCursor c
   } while (ok && next_unit(p.work, c, steps));
 }
 
-// S = Q K^T of a step; O (+)= P V of half a step (see tmem.cuh). q, k, v: low words of the tiles' descriptors.
-struct Issuer {
-  uint32_t qk_hi, v_hi, q_lo, k_lo, v_lo, tmem;
-  __device__ __forceinline__ void logits(int w, int slot) const {
-    constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile);
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const uint32_t off = (uint32_t)((s >> 2) * kTile * 128 + (s & 3) * 32) >> 4;
-      tc::mma_bf16(tmem + w * kTile, tm::desc_of(q_lo + (w * kTileBytes >> 4) + off, qk_hi),
-                   tm::desc_of(k_lo + (slot * kTileBytes >> 4) + off, qk_hi), idesc, s > 0 ? 1u : 0u);
-    }
+// A place in the order of a group's half steps.
+struct Side {
+  PromptCursor c;
+  Part part;
+  int n, j;                                       // half steps of the part; the one at hand
+  Slot slot;                                      // K of its step
+  bool live;
+  __device__ __forceinline__ Side(const PromptParams& p, const PromptCursor& from, int w) : c(from), part(p, from), live(true) {
+    n = 2 * part.n(w);
+    j = 0;
   }
-  __device__ __forceinline__ void product(int w, int slot, int h, bool accumulate) const {
-    constexpr uint32_t idesc = tc::idesc_bf16_f32(kTile, kTile) | (1u << 16);
-#pragma unroll
-    for (int s = 0; s < kHalf / 16; ++s)          // 16 rows of V are 2048 bytes of each half of its columns
-      tm::mma_bf16_ts(tmem + (2 + w) * kTile, tmem + w * kTile + h * (kHalf / 2) + s * 8,
-                      tm::desc_of(v_lo + ((slot * kTileBytes + h * (kHalf * 128)) >> 4) + s * 128, v_hi), idesc,
-                      accumulate || s > 0 ? 1u : 0u);
+  __device__ __forceinline__ void next_step() {
+    slot.next();
+    slot.next();
   }
 };
 
-// The tensor cores' work of both groups, by one thread. They take it in order, so a step's S may be issued
-// over the weights of the product before it.
-__device__ void mma_issuer(const PromptParams& p, AttentionShared& sh, PromptCursor c, uint32_t tmem, uint32_t qbuf,
-                           uint32_t ring) {
+// The tensor cores' work of group w, by a converged warp of its own. They take it in order, so the logits
+// of half step j + 2 may be issued over the weights of half step j behind their product with V.
+__device__ void mma_issuer(const PromptParams& p, AttentionShared& sh, const PromptCursor& first, int w, uint32_t tmem,
+                           uint32_t qbuf, uint32_t ring) {
   const Steps steps{p.work.tile};
-  const uint64_t qd = tc::sw128_desc(qbuf), kd = tc::sw128_desc(ring), vd = tc::sw128_desc_mn(ring, kTileBytes / 2, 1024);
-  const Issuer issue{(uint32_t)(qd >> 32), (uint32_t)(vd >> 32), (uint32_t)qd, (uint32_t)kd, (uint32_t)vd, tmem};
-  uint32_t q_turn[2] = {0, 0}, p_turn[2] = {0, 0}, scrubs = 0;
-  Slot k_slot;                                    // K of the next step; V of the step at hand is behind its K
+  const uint64_t qd = tc::sw128_desc(qbuf + w * kTileBytes), vd = tc::sw128_desc_mn(ring, kTileBytes / 2, 1024);
+  const uint32_t q_lo = (uint32_t)qd, k_lo = (uint32_t)tc::sw128_desc(ring), v_lo = (uint32_t)vd;
+  const uint32_t qk_hi = (uint32_t)(qd >> 32), v_hi = (uint32_t)(vd >> 32);
+  const uint32_t s_at = tmem + w * kTile, o_at = s_at + 2 * kTile;
+  constexpr uint32_t s_idesc = tc::idesc_bf16_f32(kTile, kHalf), o_idesc = tc::idesc_bf16_f32(kTile, kTile) | (1u << 16);
+  Side s(p, first, w), o(p, first, w);            // of the logits, of the products with V
+  uint32_t q_parity = 0, p_parity = 0, scrubs = 0;
+  int ahead = 0;                                  // half steps whose logits are issued and whose product is not
   bool ok = true;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && wait_phase(bar, parity, &sh.fail, p.work.err); };
-  Part part(p, c);
-  bool begun[2] = {false, false};                 // the unit's first logits are issued
-  // the first logits of a part; with `try_only` where their operands are there
-  auto first_logits = [&](const Part& x, int w, bool try_only) {
-    if (x.n[w] == 0 || begun[w]) return;
-    if (try_only && !(test_phase(&sh.q_full[w], q_turn[w] & 1) && test_phase(&sh.kv_full[k_slot.i], k_slot.parity)))
-      return;
-    if (!wait(&sh.q_full[w], q_turn[w] & 1) || !wait(&sh.kv_full[k_slot.i], k_slot.parity)) return;
-    ++q_turn[w];
-    tc::fence_after_sync();
-    issue.logits(w, k_slot.i);
-    tc::mma_commit(&sh.s_full[w]);
-    if (x.n[w] == 1) tc::mma_commit(&sh.q_empty[w]);
-    begun[w] = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return ok = __all_sync(0xffffffffu, wait_phase(bar, parity, &sh.fail, p.work.err));
   };
-  bool more = true;
-  while (ok && more) {
-    first_logits(part, 0, false);
-    first_logits(part, 1, false);
-    if (!ok) break;
-    tc::mma_commit(&sh.kv_empty[k_slot.i]);
-    begun[0] = begun[1] = false;
-    const int n = part.steps(), from = c.from;
-    Part next = part;
+  auto test = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, test_phase(bar, parity)) != 0; };
+  // both groups let go of every tile, of those that they have no use for as well
+  auto skip = [&]() {
 #pragma unroll 1
-    for (int i = 0; i < n && ok; ++i) {
-      Slot v_slot = k_slot;
-      v_slot.next();
-      k_slot = v_slot;
-      k_slot.next();
-      const bool last_step = i + 1 == n;
-      if (last_step) {
-        more = next_unit(p.work, c, steps);
-        if (more) next = Part(p, c);
+    for (int i = o.n / 2; i < o.part.steps() && ok; ++i) {
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv, o.slot.next()) {
+        if (!wait(&sh.kv_full[o.slot.i], o.slot.parity)) return;
+        if (kv && o.part.partly(o.c.from + i)) {
+          if (!wait(&sh.scrubbed[scrubs % kPartly], (scrubs / kPartly) & 1)) return;
+          ++scrubs;
+        }
+        if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&sh.kv_empty[o.slot.i]);
       }
-      if (!wait(&sh.kv_full[v_slot.i], v_slot.parity)) break;
-      if (part.partly(from + i)) {
+    }
+  };
+  // on to the next unit in which the group has a part; the logits' side only looks, the products' lets go
+  auto next = [&](Side& x, bool let_go) {
+    while (x.live && x.j == x.n && ok) {
+      if (let_go) {
+        skip();
+      } else {
+        for (int i = x.n / 2; i < x.part.steps(); ++i) x.next_step();
+      }
+      x.live = next_unit(p.work, x.c, steps);
+      if (!x.live) break;
+      x.part = Part(p, x.c);
+      x.n = 2 * x.part.n(w);
+      x.j = 0;
+    }
+  };
+  next(s, false);
+  next(o, true);
+  Watch watch;
+#pragma unroll 1
+  while (ok && (s.live || ahead > 0)) {
+    if (s.live && ahead < 2) {
+      uint64_t* const k_full = &sh.kv_full[s.slot.i];
+      const bool there = test(k_full, s.slot.parity) && (s.j > 0 || test(&sh.q_full[w], q_parity));
+      if (there || ahead == 0) {
+        if (!there && (!wait(k_full, s.slot.parity) || (s.j == 0 && !wait(&sh.q_full[w], q_parity)))) break;
+        if (s.j == 0) q_parity ^= 1;
+        const int h = s.j & 1;
+        tc::fence_after_sync();
+        const uint32_t k_half = k_lo + ((s.slot.i * kTileBytes + h * (kHalf * 128)) >> 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t off = (uint32_t)((i >> 2) * kTile * 128 + (i & 3) * 32) >> 4;
+          tm::warp_mma_ss(s_at + h * kHalf, tm::desc_of(q_lo + off, qk_hi), tm::desc_of(k_half + off, qk_hi), s_idesc, i > 0 ? 1u : 0u);
+        }
+        tm::warp_mma_commit(&sh.s_full[w][h]);
+        ++ahead;
+        if (h) {
+          tm::warp_mma_commit(&sh.kv_empty[s.slot.i]);
+          s.next_step();
+        }
+        if (++s.j == s.n) {
+          tm::warp_mma_commit(&sh.q_empty[w]);
+          next(s, false);
+        }
+        continue;
+      }
+      // the product where its weights are there, or the logits' operands, whichever come first
+      if (!test(&sh.p_full[w][o.j & 1], p_parity)) {
+        ok = __all_sync(0xffffffffu, watch.go_on(sh, p.work.err));
+        continue;
+      }
+    }
+    const int h = o.j & 1;
+    Slot v = o.slot;
+    v.next();
+    if (!wait(&sh.p_full[w][h], p_parity)) break;
+    if (h == 0) {
+      if (!wait(&sh.kv_full[v.i], v.parity)) break;
+      if (o.part.partly(o.c.from + o.j / 2)) {
         if (!wait(&sh.scrubbed[scrubs % kPartly], (scrubs / kPartly) & 1)) break;
         ++scrubs;
       }
-#pragma unroll 1
-      for (int w = 0; w < 2 && ok; ++w) {
-        if (i < part.n[w]) {
-          for (int h = 0; h < 2; ++h) {
-            if (!wait(&sh.p_full[w][h], p_turn[w] & 1)) break;
-            tc::fence_after_sync();
-            issue.product(w, v_slot.i, h, i > 0 || h > 0);
-            if (h == 0) tc::mma_commit(&sh.first_half[w]);
-          }
-          if (!ok) break;
-          ++p_turn[w];
-          if (i + 1 == part.n[w]) tc::mma_commit(&sh.o_full[w]);
-          if (i + 1 < part.n[w]) {
-            if (!wait(&sh.kv_full[k_slot.i], k_slot.parity)) break;
-            tc::fence_after_sync();
-            issue.logits(w, k_slot.i);
-            tc::mma_commit(&sh.s_full[w]);
-            if (i + 2 == part.n[w]) tc::mma_commit(&sh.q_empty[w]);
-          }
-        }
-        // the next unit's first logits where they would not make the other group wait
-        if (last_step && more && w == 0) first_logits(next, 0, true);
-      }
-      if (!ok) break;
-      tc::mma_commit(&sh.kv_empty[v_slot.i]);
-      if (!last_step) tc::mma_commit(&sh.kv_empty[k_slot.i]);
     }
-    part = next;
+    tc::fence_after_sync();
+#pragma unroll
+    for (int i = 0; i < kHalf / 16; ++i)          // 16 rows of V are 2048 bytes of each half of its columns
+      tm::warp_mma_ts(o_at, s_at + h * kHalf + i * 8,
+                      tm::desc_of(v_lo + ((v.i * kTileBytes + h * (kHalf * 128)) >> 4) + i * 128, v_hi), o_idesc,
+                      o.j > 0 || i > 0 ? 1u : 0u);
+    tm::warp_mma_commit(&sh.o_full[w][h]);
+    --ahead;
+    if (h) {
+      tm::warp_mma_commit(&sh.kv_empty[v.i]);
+      p_parity ^= 1;
+      o.next_step();
+    }
+    watch = Watch();
+    if (++o.j == o.n) next(o, true);
   }
   // every MMA must finish before tensor and shared memory are released
-  tc::mma_commit(&sh.done);
-  drain_phase(&sh.done, 0, p.work.err);
+  tm::warp_mma_commit(&sh.done[w]);
+  drain_phase(&sh.done[w], 0, p.work.err);
 }
 
 // The reference of a row's exponents moved: its O (where there is one) and the half step's weights so far
@@ -324,7 +367,7 @@ __device__ void softmax_group(const PromptParams& p, AttentionShared& sh, Prompt
   const uint32_t s_at = tmem + lanes + (uint32_t)(w * kTile), o_at = s_at + 2 * kTile;
   const float scale = p.scale2, hidden = scale < 0.f ? INFINITY : -INFINITY;   // a logit that gives -infinity
   const int tl = p.by_group.div(row), g = row - tl * p.group;     // token of the tile, head of the group
-  uint32_t turn = 0, o_turn = 0, unit = 0;        // steps so far, units with a step so far, units so far
+  uint32_t turn = 0, unit = 0;                    // steps so far, units so far
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     const bool there = wait_phase(bar, parity, &sh.fail, p.work.err);
@@ -332,27 +375,30 @@ __device__ void softmax_group(const PromptParams& p, AttentionShared& sh, Prompt
     tc::fence_after_sync();
     return ok;
   };
+  // The products with V before half h of this step.
+  auto wait_products = [&](int h) {
+    wait(&sh.o_full[w][0], (h == 0 ? turn + 1 : turn) & 1);
+    wait(&sh.o_full[w][1], (turn + 1) & 1);
+  };
   do {
     const Part part(p, c);
-    const int n = part.n[w], token = part.tok0 + w * p.half + tl;
+    const int n = part.n(w), token = part.tok0 + w * p.half + tl;
     const bool real = tl < p.half && token <= part.reach;
     float ref = real ? -INFINITY : 0.f;           // rows without a query never wait for a maximum
     float sum = 0.f;
 #pragma unroll 1
     for (int i = 0; i < n; ++i, ++turn) {
-      const int own0 = (c.from + i) * kTile;
-      const int seen = token - own0;              // columns 0 .. seen
+      const int seen = token - (c.from + i) * kTile;   // columns 0 .. seen
       const bool masked = __any_sync(0xffffffffu, real && seen < kTile - 1);
-      if (!wait(&sh.s_full[w], turn & 1)) break;
-      // 32 columns at a time; the next ones are on their way while these are at work
+      // 32 columns at a time; the next ones of the half step are on their way while these are at work
       float x[2][32];
-      auto chunk = [&](int ch, float(&y)[32], float(&next)[32]) {
+      auto chunk = [&](uint32_t at, int ch, int from, float(&y)[32], float(&next)[32]) {
         tm::wait32(y);
-        if (ch < 3) tm::load32(s_at + 32 * (ch + 1), next);
+        if (ch == 0) tm::load32(at + 32, next);
         if (masked) {
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            if (32 * ch + k > seen) y[k] = hidden;
+            if (from + k > seen) y[k] = hidden;
         }
         const uint64_t sc2 = pack_f32x2(scale, scale);
         uint32_t pk[16];
@@ -376,37 +422,38 @@ __device__ void softmax_group(const PromptParams& p, AttentionShared& sh, Prompt
           got = a0 + a1;
           // no reference yet, or a sum that says that it has fallen far behind the maximum (NaN as well)
           if (again || !__any_sync(0xffffffffu, real && (ref == -INFINITY || !(got < kMoveAbove)))) break;
-          if (ch < 3) tm::wait32(next);           // no call while a load is on its way to registers
+          if (ch == 0) tm::wait32(next);          // no call while a load is on its way to registers
           float top = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 32; k += 2) top = fmax3(top, y[k] * scale, y[k + 1] * scale);
           const float to = real ? fmaxf(ref, top) : ref, f = weight_of(ref, to);
           ref = to;
           sum *= f;
-          // O as the products so far left it: those of earlier steps were through before this step's logits
-          const bool half_in = ch >= 2;
-          if (half_in) wait(&sh.first_half[w], turn & 1);
-          move_reference(s_at + (half_in ? kHalf / 2 : 0), 16 * (ch & 1), i > 0 || half_in ? o_at : 0, f);
+          // O follows once the products before this half step are through
+          const bool begun = i > 0 || from >= kHalf;
+          if (begun) wait_products(from / kHalf);
+          move_reference(at, 16 * ch, begun ? o_at : 0, f);
         }
         sum += got;
-        tm::store16(s_at + 16 * ch, pk);          // over columns that are in registers by now
+        tm::store16(at + 16 * ch, pk);            // over columns that are in registers by now
       };
-      auto announce = [&](int h) {
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t at = s_at + h * kHalf;
+        if (!wait(&sh.s_full[w][h], turn & 1)) break;
+        tm::load32(at, x[0]);
+        chunk(at, 0, h * kHalf, x[0], x[1]);
+        chunk(at, 1, h * kHalf + 32, x[1], x[0]);
         tm::wait_stores();
         tc::fence_before_sync();
         __syncwarp();
         if ((row & 31) == 0) tc::mbar_arrive(&sh.p_full[w][h]);   // a warp's 32 arrivals would go one by one
-      };
-      tm::load32(s_at, x[0]);
-      chunk(0, x[0], x[1]);
-      chunk(1, x[1], x[0]);
-      announce(0);
-      chunk(2, x[0], x[1]);
-      chunk(3, x[1], x[0]);
-      announce(1);
+      }
+      if (!ok) break;
     }
     if (!ok) break;
-    if (n > 0 && !wait(&sh.o_full[w], o_turn++ & 1)) break;
+    if (n > 0) wait_products(0);
+    if (!ok) break;
     const uint32_t* bad = sh.bad[unit++ % kBadSets];
     uint32_t any_bad = 0;
     if (n > 0 && part.partly(c.to - 1))
@@ -481,26 +528,27 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ AttentionShared sh;
   const uint32_t smem = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (warp == 0) tc::tmem_alloc(&sh.tmem_base, 4 * kTile);
   if (tid == 32) {
     for (int w = 0; w < 2; ++w) {
       tc::mbar_init(&sh.q_full[w], 1);
       tc::mbar_init(&sh.q_empty[w], 1);
-      tc::mbar_init(&sh.s_full[w], 1);
-      tc::mbar_init(&sh.first_half[w], 1);
-      tc::mbar_init(&sh.o_full[w], 1);
-      for (int h = 0; h < 2; ++h) tc::mbar_init(&sh.p_full[w][h], kTile / 32);
+      for (int h = 0; h < 2; ++h) {
+        tc::mbar_init(&sh.s_full[w][h], 1);
+        tc::mbar_init(&sh.p_full[w][h], kTile / 32);
+        tc::mbar_init(&sh.o_full[w][h], 1);
+      }
+      tc::mbar_init(&sh.done[w], 1);
     }
     for (int i = 0; i < kRing; ++i) {
       tc::mbar_init(&sh.kv_full[i], 1);
-      tc::mbar_init(&sh.kv_empty[i], 1);
+      tc::mbar_init(&sh.kv_empty[i], 2);          // both groups' issuers
     }
     for (int i = 0; i < kPartly; ++i) {
       tc::mbar_init(&sh.partly_full[i], 1);
       tc::mbar_init(&sh.scrubbed[i], 1);
     }
-    tc::mbar_init(&sh.done, 1);
     sh.fail = 0;
   }
   if (warp == kTmaWarp && lane == 0) {
@@ -514,13 +562,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = sh.tmem_base, ring = smem + 2 * kTileBytes;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_base, 0), ring = smem + 2 * kTileBytes;
   if (any) {
     if (warp < kMmaWarp) {
       softmax_group(p, sh, c, warp >> 2, tid & (kTile - 1), tmem);
-    } else if (warp == kMmaWarp) {
-      if (lane == 0) mma_issuer(p, sh, c, tmem, smem, ring);
-      __syncwarp();
+    } else if (warp < kTmaWarp) {
+      mma_issuer(p, sh, c, warp - kMmaWarp, tmem, smem, ring);
     } else if (warp == kTmaWarp) {
       if (lane == 0) producer(p, sh, c, smem, ring);
       __syncwarp();

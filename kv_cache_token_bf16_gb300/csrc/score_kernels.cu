@@ -58,8 +58,7 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(const __grid_const
 
 // ---------------------------------------------------------------------------
 // Score + append (the concatenation stays within budget): copies each
-// incoming K/V row to storage row k + t, with its score and position (the
-// kCurDKV variant takes the scores from new_score).
+// incoming K/V row to storage row k + t, with its score and position.
 // grid = (ceil(m / 64), n_layers * B * H)
 // ---------------------------------------------------------------------------
 template <bool kBf16, int kMethod>
@@ -93,9 +92,7 @@ __global__ void __launch_bounds__(kScoreThreads) append_kernel(const __grid_cons
     }
     float x[8];
     kr.widen(x);
-    float sigma;
-    if constexpr (kMethod == kCurDKV) sigma = t < s.m ? L.new_score[(size_t)bh * s.new_stride + t] : 0.f;
-    else sigma = canonical_score<kMethod>(x, f, s.sign);
+    const float sigma = canonical_score<kMethod>(x, f, s.sign);
     if (t < s.m) {
       // kLaneBytes = 16 (bf16) or 32 (fp32) bytes per lane, contiguous per lane
       uint4* kd = reinterpret_cast<uint4*>(kout + (size_t)t * kRowBytes + kLaneBytes * c);
@@ -136,8 +133,6 @@ cudaError_t launch_append(const GroupParams& P, int dtype_bytes, cudaStream_t st
   const bool bf = dtype_bytes == 2;
   if (P.s.method == kKNorm)
     return launch(bf ? append_kernel<true, kKNorm> : append_kernel<false, kKNorm>, grid, kScoreThreads, 0, st, P);
-  if (P.s.method >= kCurDKV)          // attention weights: scores given, bf16 storage
-    return launch(append_kernel<true, kCurDKV>, grid, kScoreThreads, 0, st, P);
   return launch(bf ? append_kernel<true, kQFilters> : append_kernel<false, kQFilters>, grid, kScoreThreads, 0, st, P);
 }
 
@@ -158,9 +153,8 @@ namespace {
 // works step 5) the smallest index among them. Every row after it moves down
 // by one. One CTA per (layer, b, h):
 //   1. score the m incoming rows (same canonical order as score_kernel); the
-//      kCurDKV variant takes the scores in new_score instead, which the
-//      attention pipeline of CurDKV and H2O left there, or the caller's own
-//      (attention weights);
+//      kCurDKV variant (CurDKV and H2O per-token steps) takes the scores the
+//      attention pipeline left in new_score instead;
 //   2. block-wide max of (~key << 32 | tag) over the unprotected rows, the
 //      tag being the index (or its complement with tie_low);
 //   3. destinations [min(e, k), n - 1) take row d below e and row d + 1 from
@@ -376,7 +370,7 @@ cudaError_t launch_evict1(const GroupParams& P, int dtype_bytes, cudaStream_t st
   const bool bf = dtype_bytes == 2;
   if (P.s.method == kKNorm)
     return launch(bf ? evict1_kernel<true, kKNorm> : evict1_kernel<false, kKNorm>, grid, kE1Threads, kE1Smem, st, P);
-  if (P.s.method >= kCurDKV)          // scores already in new_score, bf16 storage
+  if (P.s.method >= kCurDKV)          // CurDKV and H2O: scores already in new_score, bf16 storage
     return launch(evict1_kernel<true, kCurDKV>, grid, kE1Threads, kE1Smem, st, P);
   return launch(bf ? evict1_kernel<true, kQFilters> : evict1_kernel<false, kQFilters>, grid, kE1Threads, kE1Smem, st,
                 P);

@@ -127,9 +127,35 @@ __global__ void __launch_bounds__(kWarps * 32, 2) weigh_kernel(const __grid_cons
     }
 }
 
+// The rows of a block behind the kept ones, with their positions and given scores: a warp per row.
+constexpr int kAppendWarps = 8;
+__global__ void __launch_bounds__(kAppendWarps * 32) append_given_kernel(const __grid_constant__ GroupParams P) {
+  pdl_wait();
+  const Shape& s = P.s;
+  const LayerPtrs& L = P.L[0];
+  const int t = blockIdx.x * kAppendWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31, bh = blockIdx.y;
+  if (t >= s.m) return;
+  const size_t from = (size_t)bh * s.m + t, to = (size_t)bh * s.cap + s.k + t;
+  constexpr int kPieces = kHeadDim * 2 / 16;      // of K, and of V
+  const bool value = lane >= kPieces;
+  const uint4* src = static_cast<const uint4*>(value ? L.v_in : L.k_in) + from * kPieces;
+  uint4* dst = static_cast<uint4*>(value ? L.vst : L.kst) + to * kPieces;
+  dst[lane & (kPieces - 1)] = src[lane & (kPieces - 1)];
+  if (lane == 0) {
+    L.score_st[to] = L.new_score[(size_t)bh * s.new_stride + t];
+    L.pos_st[to] = L.pos_in ? L.pos_in[(size_t)(bh / s.heads) * s.m + t] : (int32_t)(s.offset + t);
+  }
+}
+
 bool multiple(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
+
+cudaError_t launch_append_given(const GroupParams& P, cudaStream_t st) {
+  return launch_pdl(append_given_kernel, dim3((P.s.m + kAppendWarps - 1) / kAppendWarps, P.s.batch * P.s.heads),
+                    dim3(kAppendWarps * 32), 0, st, nullptr, P);
+}
+
 }  // namespace evict
 
 using namespace evict;

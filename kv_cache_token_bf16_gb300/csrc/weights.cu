@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "api_internal.h"
 #include "common.cuh"
@@ -67,11 +68,20 @@ struct Unit {
   }
 };
 struct Step {
-  int g, tok0, n;
-  __device__ __forceinline__ Step(const Unit& u, const PromptCursor& c, int step) {
-    g = step / u.tiles;
-    tok0 = u.first + (step - g * u.tiles) * kTile;
+  int g, tile;                                    // head of the group, tile of 128 queries
+  int tok0, n;
+  __device__ __forceinline__ Step(const Unit& u, const PromptCursor& c) {
+    g = c.from / u.tiles;
+    tile = c.from - g * u.tiles;
+    place(u, c);
+  }
+  __device__ __forceinline__ void place(const Unit& u, const PromptCursor& c) {
+    tok0 = u.first + tile * kTile;
     n = min(kTile, c.k.at.len - tok0);
+  }
+  __device__ __forceinline__ void next(const Unit& u, const PromptCursor& c) {
+    if (++tile == u.tiles) tile = 0, ++g;
+    place(u, c);
   }
   // some query of the step sees a key of tile kt
   __device__ __forceinline__ bool sees(const Unit& u, int kt) const {
@@ -104,8 +114,8 @@ __device__ void producer(const PromptParams& p, WeightsShared& sh, PromptCursor 
                   c.k.at.row0 + u.key0 + (j >> 1) * kTile, c.h, c.k.at.plane, &sh.k_full[k.i]);
     k.next();
     ++used_k;
-    for (int i = c.from; i < c.to; ++i) {
-      const Step s(u, c, i);
+    Step s(u, c);
+    for (int i = c.from; i < c.to; ++i, s.next(u, c)) {
       if (!(ok = wait_phase(&sh.q_empty[q.i], q.parity ^ 1, &sh.fail, p.work.err))) break;
       tc::mbar_arrive_expect_tx(&sh.q_full[q.i], kTileBytes);
       for (int hf = 0; hf < 2; ++hf)
@@ -128,8 +138,8 @@ __device__ void lse_loader(const PromptParams& p, WeightsShared& sh, PromptCurso
   bool ok = true;
   do {
     const Unit u(p, c);
-    for (int i = c.from; i < c.to; ++i) {
-      const Step s(u, c, i);
+    Step s(u, c);
+    for (int i = c.from; i < c.to; ++i, s.next(u, c)) {
       const float* from = p.lse + ((long long)c.k.at.plane * p.hq + c.h * p.group + s.g) * p.work.m + c.k.at.row0 + s.tok0;
       float x[4];
 #pragma unroll
@@ -158,12 +168,14 @@ __device__ void mma_issuer(const PromptParams& p, WeightsShared& sh, PromptCurso
   Ring<2> k, s_buf;
   Ring<kRing> q;
   bool ok = true;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = wait_phase(bar, parity, &sh.fail, p.work.err); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return ok = __all_sync(0xffffffffu, wait_phase(bar, parity, &sh.fail, p.work.err));
+  };
   do {
     const Unit u(p, c);
     if (!wait(&sh.k_full[k.i], k.parity)) break;
-    for (int i = c.from; i < c.to; ++i) {
-      const Step s(u, c, i);
+    Step s(u, c);
+    for (int i = c.from; i < c.to; ++i, s.next(u, c)) {
       if (!wait(&sh.q_full[q.i], q.parity) || !wait(&sh.s_empty[s_buf.i], s_buf.parity ^ 1)) break;
       tc::fence_after_sync();
       const uint32_t idesc = tc::idesc_bf16_f32(kTile, (s.n + 15) & ~15);
@@ -173,21 +185,21 @@ __device__ void mma_issuer(const PromptParams& p, WeightsShared& sh, PromptCurso
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const uint32_t off = (uint32_t)((j >> 2) * kTile * 128 + (j & 3) * 32) >> 4;
-          tc::mma_bf16(tmem + (2 * s_buf.i + kt) * kTile, tm::desc_of(k_lo + (((2 * k.i + kt) * kTileBytes) >> 4) + off, hi),
+          tm::warp_mma_ss(tmem + (2 * s_buf.i + kt) * kTile, tm::desc_of(k_lo + (((2 * k.i + kt) * kTileBytes) >> 4) + off, hi),
                        tm::desc_of(q_lo + ((q.i * kTileBytes) >> 4) + off, hi), idesc, j > 0 ? 1u : 0u);
         }
       }
-      tc::mma_commit(&sh.s_full[s_buf.i]);
-      tc::mma_commit(&sh.q_empty[q.i]);
+      tm::warp_mma_commit(&sh.s_full[s_buf.i]);
+      tm::warp_mma_commit(&sh.q_empty[q.i]);
       q.next();
       s_buf.next();
     }
     if (!ok) break;
-    tc::mma_commit(&sh.k_empty[k.i]);
+    tm::warp_mma_commit(&sh.k_empty[k.i]);
     k.next();
   } while (next_unit(p.work, c, steps));
   // every MMA must finish before tensor and shared memory are released
-  tc::mma_commit(&sh.done);
+  tm::warp_mma_commit(&sh.done);
   drain_phase(&sh.done, 0, p.work.err);
 }
 
@@ -222,10 +234,10 @@ __device__ void sum_warp(const PromptParams& p, WeightsShared& sh, PromptCursor 
   };
   do {
     const Unit u(p, c);
+    Step s(u, c);
     float sum = 0.f;
 #pragma unroll 1
-    for (int i = c.from; i < c.to; ++i) {
-      const Step s(u, c, i);
+    for (int i = c.from; i < c.to; ++i, s.next(u, c)) {
       if (!wait(&sh.lse_full[r.i], r.parity) || !wait(&sh.s_full[s_buf.i], s_buf.parity)) break;
       tc::fence_after_sync();
       const int columns = s.sees(u, kt) ? s.n - 64 * half : 0;   // of this warp's 64
@@ -234,38 +246,34 @@ __device__ void sum_warp(const PromptParams& p, WeightsShared& sh, PromptCursor 
         const int before = u.key0 + key - s.tok0 - 64 * half;    // columns that do not see this key
         const bool masked = columns < 64 || __any_sync(0xffffffffu, before > 0);
         const float4* l2 = reinterpret_cast<const float4*>(&sh.neg_lse2[r.i][64 * half]);
-        float x[2][32];
-        uint64_t acc[2] = {0ull, 0ull};
-        auto chunk = [&](int ch, float(&y)[32]) {
+        float x[64];
+        tm::load64(at, x);
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sh.s_empty[s_buf.i]);
+        auto add = [&](auto with_mask) {
+          uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 l = l2[8 * ch + j / 4];
-            uint64_t e0 = ex2_f32x2(fma_f32x2(pack_f32x2(y[j], y[j + 1]), sc2, pack_f32x2(l.x, l.y)));
-            uint64_t e1 = ex2_f32x2(fma_f32x2(pack_f32x2(y[j + 2], y[j + 3]), sc2, pack_f32x2(l.z, l.w)));
-            if (masked) {
+          for (int j = 0; j < 64; j += 4) {
+            const float4 l = l2[j / 4];
+            uint64_t e0 = ex2_f32x2(fma_f32x2(pack_f32x2(x[j], x[j + 1]), sc2, pack_f32x2(l.x, l.y)));
+            uint64_t e1 = ex2_f32x2(fma_f32x2(pack_f32x2(x[j + 2], x[j + 3]), sc2, pack_f32x2(l.z, l.w)));
+            if constexpr (decltype(with_mask)::value) {
               float a, b;
-              const int t = 32 * ch + j;
               split_f32x2(e0, a, b);
-              e0 = pack_f32x2(t >= before && t < columns ? a : 0.f, t + 1 >= before && t + 1 < columns ? b : 0.f);
+              e0 = pack_f32x2(j >= before && j < columns ? a : 0.f, j + 1 >= before && j + 1 < columns ? b : 0.f);
               split_f32x2(e1, a, b);
-              e1 = pack_f32x2(t + 2 >= before && t + 2 < columns ? a : 0.f, t + 3 >= before && t + 3 < columns ? b : 0.f);
+              e1 = pack_f32x2(j + 2 >= before && j + 2 < columns ? a : 0.f, j + 3 >= before && j + 3 < columns ? b : 0.f);
             }
             acc[0] = add_f32x2(acc[0], e0);
             acc[1] = add_f32x2(acc[1], e1);
           }
+          float a, b;
+          split_f32x2(add_f32x2(acc[0], acc[1]), a, b);
+          sum += a + b;
         };
-        tm::load32(at, x[0]);
-        if (columns > 32) tm::load32(at + 32, x[1]);
-        tm::wait32(x[0]);
-        if (columns > 32) tm::wait32(x[1]);
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sh.s_empty[s_buf.i]);
-        chunk(0, x[0]);
-        if (columns > 32) chunk(1, x[1]);
-        float a, b;
-        split_f32x2(add_f32x2(acc[0], acc[1]), a, b);
-        sum += a + b;
+        if (masked) add(std::true_type{});
+        else add(std::false_type{});
         __syncwarp();
       } else if (lane == 0) {
         tc::mbar_arrive(&sh.s_empty[s_buf.i]);
@@ -298,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_weights_kernel(const __gri
     if (threadIdx.x == 0) raise_device_error(p.work.err, kDevBadIndex);
     return;
   }
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (warp == 0) tc::tmem_alloc(&sh.tmem_base, 4 * kTile);
   if (tid == 32) {
     for (int i = 0; i < 2; ++i) {
@@ -328,13 +336,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_weights_kernel(const __gri
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = sh.tmem_base, ring = smem + 4 * kTileBytes;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_base, 0), ring = smem + 4 * kTileBytes;
   if (any) {
     if (warp < kSumWarps) {
       sum_warp(p, sh, c, tmem);
     } else if (warp == kMmaWarp) {
-      if (lane == 0) mma_issuer(p, sh, c, tmem, smem, ring);
-      __syncwarp();
+      mma_issuer(p, sh, c, tmem, smem, ring);
     } else if (warp == kTmaWarp) {
       if (lane == 0) producer(p, sh, c, smem, ring);
       __syncwarp();
