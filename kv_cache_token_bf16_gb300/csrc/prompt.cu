@@ -39,42 +39,44 @@ constexpr int kRows = 2 * kTile;                  // query rows of a unit
 constexpr int kRing = 5;
 constexpr int kSmem = 1024 + (2 + kRing) * kTileBytes;
 constexpr int kMmaWarp = 8, kTmaWarp = 10, kThreads = 384;   // warp 11 scrubs
+constexpr int kUnits = 8;                         // units that warps are apart at most
+constexpr int kReaders = 11;                      // warps that read a unit: softmax, issuers, scrubbing
 constexpr int kBadWords = kRows / 32;             // rows of V behind the unit's first token, a bit each
-constexpr int kBadSets = 8;                       // of a CTA's units in turn
 constexpr int kPartly = 4;                        // barriers of tiles to scrub, in turn: the ring holds at most three
 constexpr float kMoveAbove = 4096.f;              // sum of 32 weights that makes the reference move
+constexpr uint32_t kPolls = 100000;               // of a wait, each of up to 20 us
 constexpr int kEntry = 2, kMinSteps = 4;
 constexpr int kWholeRows = 1024;
-
-struct AttentionShared {
-  uint64_t q_full[2], q_empty[2], kv_full[kRing], kv_empty[kRing], partly_full[kPartly], scrubbed[kPartly];
-  uint64_t s_full[2][2], p_full[2][2], o_full[2][2], done[2];   // group, half of the step
-  uint32_t tmem_base;
-  int fail;
-  uint32_t bad[kBadSets][kBadWords];
-  PromptScan scan;
-};
 
 struct Steps {
   int tile;
   __device__ __forceinline__ int operator()(int tok0, int len) const { return (min(tok0 + tile, len) + kTile - 1) / kTile; }
 };
 
-// A unit's part, as every role sees it.
-struct Part {
+// A CTA's part of a unit, as every warp sees it. (The fetching warp alone goes through the schedule: one
+// warp's code for it, and nothing of it between a product and the next.)
+struct alignas(16) Unit {
+  int plane, row0, h;                             // the sequence's plane and first row; KV head
   int tok0, reach;                                // first token; last one
-  int n0, n1;                                     // steps of the two groups (from c.from on); n1 >= n0 or 0
-  __device__ __forceinline__ Part(const PromptParams& p, const PromptCursor& c) {
-    tok0 = c.k.tile * p.work.tile;
-    reach = min(tok0 + p.work.tile, c.k.at.len) - 1;
-    const int first_reach = min(tok0 + p.half - 1, reach);        // of the first group's tokens
-    n0 = max(min(c.to, first_reach / kTile + 1) - c.from, 0);
-    n1 = first_reach < reach ? c.to - c.from : 0;
-  }
+  int from;                                       // first step of the part
+  int n0, n1;                                     // steps of the two groups, from there on: n1 >= n0, or 0
+  int kind;                                       // 0: there is none
   __device__ __forceinline__ int n(int w) const { return w ? n1 : n0; }
   __device__ __forceinline__ int steps() const { return max(n0, n1); }
   // the step's rows of V hold some that not every query of the unit sees
   __device__ __forceinline__ bool partly(int step) const { return step * kTile + kTile - 1 > tok0; }
+};
+constexpr int kPart = 1, kWhole = 2;              // kinds
+
+struct AttentionShared {
+  uint64_t unit_full[kUnits], unit_empty[kUnits];
+  uint64_t q_full[2], q_empty[2], kv_full[kRing], kv_empty[kRing], partly_full[kPartly], scrubbed[kPartly];
+  uint64_t s_full[2][2], p_full[2][2], o_full[2][2], done[2];   // group, half of the step
+  uint32_t tmem_base;
+  int fail;
+  Unit units[kUnits];
+  uint32_t bad[kUnits][kBadWords];                // rows of V that were cleared
+  PromptScan scan;
 };
 
 struct Slot {
@@ -83,97 +85,143 @@ struct Slot {
   __device__ __forceinline__ void next() {
     if (++i == kRing) i = 0, parity ^= 1;
   }
-};
-
-// Bounds a warp's polling (the clock is read rarely).
-struct Watch {
-  uint32_t polls = 0;
-  uint64_t t0 = 0;
-  __device__ __forceinline__ bool go_on(AttentionShared& sh, int* err) {
-    if ((++polls & 1023) != 0) return true;
-    if (*(volatile int*)&sh.fail) return false;
-    const uint64_t t = tc::global_ns();
-    if (t0 == 0) t0 = t;
-    if (t - t0 <= kWaitLimitNs) return true;
-    *(volatile int*)&sh.fail = 1;
-    raise_device_error(err, kDevWaitTimeout);
-    return false;
+  __device__ __forceinline__ void step() {
+    next();
+    next();
   }
 };
 
+// Waits at many places, so little code: polls that sleep in hardware, a bounded number of them. The kernel's end
+// reports one that gave up.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, AttentionShared& sh) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+  for (uint32_t polls = 0; !tc::mbar_try_wait_sleep(bar, parity, kWaitSleepNs);)
+    if (++polls == kPolls || *(volatile int*)&sh.fail) {
+      *(volatile int*)&sh.fail = 1;
+      return false;
+    }
+  return true;
+}
+// A warp's wait; the same for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, AttentionShared& sh) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, sh));
+}
+// One lane's value for the warp, which the compiler then knows to be the same: what follows from it stays in uniform
+// registers, where products take their operands from. (A lone thread's, or what might differ, is moved there one by
+// one: 128 x 64 x 16 products then take 65 clocks instead of 48; a document of 8192 tokens 395 us instead of 369.)
+__device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+// The i-th unit of the CTA, by a whole warp; kind 0 behind the last one, and where a wait gave up.
+__device__ __forceinline__ Unit read_unit(AttentionShared& sh, int i) {
+  Unit u = {};
+  if (warp_wait(&sh.unit_full[i % kUnits], (i / kUnits) & 1, sh)) u = sh.units[i % kUnits];
+  u.plane = uni(u.plane), u.row0 = uni(u.row0), u.h = uni(u.h);
+  u.tok0 = uni(u.tok0), u.reach = uni(u.reach), u.from = uni(u.from);
+  u.n0 = uni(u.n0), u.n1 = uni(u.n1), u.kind = uni(u.kind);
+  return u;
+}
+__device__ __forceinline__ void let_go(AttentionShared& sh, int i) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&sh.unit_empty[i % kUnits]);
+}
+
+// The schedule and the copies, by one thread.
 __device__ void producer(const PromptParams& p, AttentionShared& sh, PromptCursor c, uint32_t qbuf, uint32_t ring) {
   const Steps steps{p.work.tile};
   Slot slot;
-  int used = 0, turns0 = 0, turns1 = 0, partly = 0;
-  bool ok = true;
-  // a tile to be scrubbed lands on a barrier of the scrubbing warp's, and its slot counts as full at once
-  auto load_kv = [&](const CUtensorMap* map, int step, bool to_scrub) {
-    if (!(ok = wait_phase(&sh.kv_empty[slot.i], slot.parity ^ 1, &sh.fail, p.work.err))) return;
-    uint64_t* bar = &sh.kv_full[slot.i];
-    if (to_scrub) {
-      tc::mbar_arrive(bar);
-      bar = &sh.partly_full[partly++ % kPartly];
+  int used = 0, turns0 = 0, turns1 = 0, partly = 0, unit = 0;
+  bool ok = true, any = true;                     // any: there is a unit at hand
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = wait_for(bar, parity, sh); };
+  for (;; ++unit) {
+    if (!wait(&sh.unit_empty[unit % kUnits], ((unit / kUnits) & 1) ^ 1)) break;
+    Unit u = {};
+    if (any) {
+      u.plane = c.k.at.plane;
+      u.row0 = c.k.at.row0;
+      u.h = c.h;
+      u.tok0 = c.k.tile * p.work.tile;
+      u.reach = min(u.tok0 + p.work.tile, c.k.at.len) - 1;
+      u.from = c.from;
+      const int first_reach = min(u.tok0 + p.half - 1, u.reach);  // of the first group's tokens
+      u.n0 = max(min(c.to, first_reach / kTile + 1) - c.from, 0);
+      u.n1 = first_reach < u.reach ? c.to - c.from : 0;
+      u.kind = c.to - c.from == c.k.steps ? kWhole : kPart;
     }
-    const uint32_t dst = ring + slot.i * kTileBytes;
-    tc::mbar_arrive_expect_tx(bar, kTileBytes);
-    for (int hf = 0; hf < 2; ++hf)
-      tma_load_4d(dst + hf * (kTileBytes / 2), map, hf * 64, c.k.at.row0 + step * kTile, c.h, c.k.at.plane, bar);
-    slot.next();
-    ++used;
-  };
-  do {
-    const Part part(p, c);
-    const int n = part.steps();
-    load_kv(&p.k_map, c.from, false);
-    for (int w = 0; w < 2 && ok; ++w) {
-      if (part.n(w) == 0) continue;
-      const int turn = w ? turns1++ : turns0++;
-      if (!(ok = wait_phase(&sh.q_empty[w], (turn & 1) ^ 1, &sh.fail, p.work.err))) break;
-      tc::mbar_arrive_expect_tx(&sh.q_full[w], 2 * p.half * p.group * 128);
+    sh.units[unit % kUnits] = u;
+    tc::mbar_arrive(&sh.unit_full[unit % kUnits]);
+    if (!any) break;
+#pragma unroll 1
+    for (int j = 0; j < 2 * u.steps(); ++j) {     // K and V of a step; the queries behind the first K
+      if (j == 1) {
+#pragma unroll 1
+        for (int w = 0; w < 2; ++w) {
+          if (u.n(w) == 0) continue;
+          const int turn = w ? turns1 : turns0;
+          if (!wait(&sh.q_empty[w], (turn & 1) ^ 1)) break;
+          if (w) ++turns1;
+          else ++turns0;
+          tc::mbar_arrive_expect_tx(&sh.q_full[w], 2 * p.half * p.group * 128);
+          for (int hf = 0; hf < 2; ++hf)
+            tma_load_4d(qbuf + w * kTileBytes + hf * (kTileBytes / 2), &p.q_map, hf * 64, u.h * p.group,
+                        u.row0 + u.tok0 + w * p.half, u.plane, &sh.q_full[w]);
+        }
+        if (!ok) break;
+      }
+      if (!wait(&sh.kv_empty[slot.i], slot.parity ^ 1)) break;
+      const int step = u.from + j / 2;
+      uint64_t* bar = &sh.kv_full[slot.i];
+      if ((j & 1) && u.partly(step)) {
+        // a tile to be scrubbed lands on a barrier of the scrubbing warp's, and its slot counts as full at once
+        tc::mbar_arrive(bar);
+        bar = &sh.partly_full[partly++ % kPartly];
+      }
+      tc::mbar_arrive_expect_tx(bar, kTileBytes);
       for (int hf = 0; hf < 2; ++hf)
-        tma_load_4d(qbuf + w * kTileBytes + hf * (kTileBytes / 2), &p.q_map, hf * 64, c.h * p.group,
-                    c.k.at.row0 + part.tok0 + w * p.half, c.k.at.plane, &sh.q_full[w]);
+        tma_load_4d(ring + slot.i * kTileBytes + hf * (kTileBytes / 2), j & 1 ? &p.v_map : &p.k_map, hf * 64,
+                    u.row0 + step * kTile, u.h, u.plane, bar);
+      slot.next();
+      ++used;
     }
-    if (ok) load_kv(&p.v_map, c.from, part.partly(c.from));
-    for (int i = 1; i < n && ok; ++i) {
-      load_kv(&p.k_map, c.from + i, false);
-      if (ok) load_kv(&p.v_map, c.from + i, part.partly(c.from + i));
-    }
-  } while (ok && next_unit(p.work, c, steps));
+    if (!ok) break;
+    any = next_unit(p.work, c, steps);
+  }
   // every copy issued must land before the CTA may release its shared memory
+#pragma unroll 1
   for (int i = 0; i < kRing && i < used; ++i) drain_phase(&sh.kv_full[i], ((used - 1 - i) / kRing) & 1, p.work.err);
+#pragma unroll 1
   for (int i = 0; i < kPartly && i < partly; ++i) drain_phase(&sh.partly_full[i], ((partly - 1 - i) / kPartly) & 1, p.work.err);
-  if (ok && turns0) drain_phase(&sh.q_full[0], (turns0 - 1) & 1, p.work.err);
-  if (ok && turns1) drain_phase(&sh.q_full[1], (turns1 - 1) & 1, p.work.err);
+#pragma unroll 1
+  for (int w = 0; w < 2; ++w) {
+    const int turns = w ? turns1 : turns0;
+    if (turns) drain_phase(&sh.q_full[w], (turns - 1) & 1, p.work.err);
+  }
 }
 
 // Rows of V that a query does not see meet a weight of 0, but 0 * infinity is not 0. Rows behind the unit's
 // last token (another sequence's, or none) are cleared; rows between its first and last token are cleared
 // where they hold infinities or NaN, and marked: the queries that do see them add them at the unit's end.
-__device__ void scrub(const PromptParams& p, AttentionShared& sh, PromptCursor c, uint32_t ring) {
-  const Steps steps{p.work.tile};
+__device__ void scrub(const PromptParams& p, AttentionShared& sh, uint32_t ring) {
   const int lane = threadIdx.x & 31;
   Slot slot;
-  uint32_t count = 0, unit = 0;
-  bool ok = true;
-  do {
-    const Part part(p, c);
-    uint32_t* bad = sh.bad[unit++ % kBadSets];
+  uint32_t count = 0;
+#pragma unroll 1
+  for (int unit = 0;; ++unit) {
+    const Unit u = read_unit(sh, unit);
+    if (!u.kind) return;
+    uint32_t* bad = sh.bad[unit % kUnits];
     if (lane < kBadWords) bad[lane] = 0;
     __syncwarp();
-    for (int i = 0; i < part.steps() && ok; ++i) {
+#pragma unroll 1
+    for (int step = u.from; step < u.from + u.steps(); ++step) {
       slot.next();                                // the step's V
-      const int own0 = (c.from + i) * kTile;
-      if (part.partly(c.from + i)) {
-        ok = wait_phase(&sh.partly_full[count % kPartly], (count / kPartly) & 1, &sh.fail, p.work.err);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+      if (u.partly(step)) {
+        if (!warp_wait(&sh.partly_full[count % kPartly], (count / kPartly) & 1, sh)) return;
 #pragma unroll 1
         for (int r = lane; r < kTile; r += 32) {
           const uint32_t at = ring + slot.i * kTileBytes + r * 128;
-          const int tok = own0 + r;
-          bool blank = tok > part.reach;
-          if (!blank && tok > part.tok0) {
+          const int tok = step * kTile + r;
+          bool blank = tok > u.reach;
+          if (!blank && tok > u.tok0) {
             uint32_t seen = 0;                    // x * 0 is 0, or NaN where x is not finite
 #pragma unroll 4
             for (int j = 0; j < 16; ++j) {
@@ -186,7 +234,7 @@ __device__ void scrub(const PromptParams& p, AttentionShared& sh, PromptCursor c
               asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(seen) : "r"(x.w), "r"(0u));
             }
             blank = nonfinite2(seen) != 0;
-            if (blank) atomicOr(&bad[(tok - part.tok0 - 1) >> 5], 1u << ((tok - part.tok0 - 1) & 31));
+            if (blank) atomicOr(&bad[(tok - u.tok0 - 1) >> 5], 1u << ((tok - u.tok0 - 1) & 31));
           }
           if (blank) {
 #pragma unroll 1
@@ -202,137 +250,110 @@ __device__ void scrub(const PromptParams& p, AttentionShared& sh, PromptCursor c
       }
       slot.next();
     }
-  } while (ok && next_unit(p.work, c, steps));
+    let_go(sh, unit);
+  }
 }
-
-// A place in the order of a group's half steps.
-struct Side {
-  PromptCursor c;
-  Part part;
-  int n, j;                                       // half steps of the part; the one at hand
-  Slot slot;                                      // K of its step
-  bool live;
-  __device__ __forceinline__ Side(const PromptParams& p, const PromptCursor& from, int w) : c(from), part(p, from), live(true) {
-    n = 2 * part.n(w);
-    j = 0;
-  }
-  __device__ __forceinline__ void next_step() {
-    slot.next();
-    slot.next();
-  }
-};
 
 // The tensor cores' work of group w, by a converged warp of its own. They take it in order, so the logits
 // of half step j + 2 may be issued over the weights of half step j behind their product with V.
-__device__ void mma_issuer(const PromptParams& p, AttentionShared& sh, const PromptCursor& first, int w, uint32_t tmem,
-                           uint32_t qbuf, uint32_t ring) {
-  const Steps steps{p.work.tile};
+__device__ void mma_issuer(const PromptParams& p, AttentionShared& sh, int w, uint32_t tmem, uint32_t qbuf, uint32_t ring) {
   const uint64_t qd = tc::sw128_desc(qbuf + w * kTileBytes), vd = tc::sw128_desc_mn(ring, kTileBytes / 2, 1024);
   const uint32_t q_lo = (uint32_t)qd, k_lo = (uint32_t)tc::sw128_desc(ring), v_lo = (uint32_t)vd;
   const uint32_t qk_hi = (uint32_t)(qd >> 32), v_hi = (uint32_t)(vd >> 32);
   const uint32_t s_at = tmem + w * kTile, o_at = s_at + 2 * kTile;
   constexpr uint32_t s_idesc = tc::idesc_bf16_f32(kTile, kHalf), o_idesc = tc::idesc_bf16_f32(kTile, kTile) | (1u << 16);
-  Side s(p, first, w), o(p, first, w);            // of the logits, of the products with V
   uint32_t q_parity = 0, p_parity = 0, scrubs = 0;
-  int ahead = 0;                                  // half steps whose logits are issued and whose product is not
   bool ok = true;
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return ok = __all_sync(0xffffffffu, wait_phase(bar, parity, &sh.fail, p.work.err));
-  };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && warp_wait(bar, parity, sh); };
   auto test = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, test_phase(bar, parity)) != 0; };
-  // both groups let go of every tile, of those that they have no use for as well
-  auto skip = [&]() {
+  // The logits of half step j of n, K in `slot`.
+  auto logits = [&](const Slot& slot, int j, int n) {
+    const int h = j & 1;
+    tc::fence_after_sync();
+    const uint32_t k_half = k_lo + ((slot.i * kTileBytes + h * (kHalf * 128)) >> 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t off = (uint32_t)((i >> 2) * kTile * 128 + (i & 3) * 32) >> 4;
+      tm::warp_mma_ss(s_at + h * kHalf, tm::desc_of(q_lo + off, qk_hi), tm::desc_of(k_half + off, qk_hi), s_idesc, i > 0 ? 1u : 0u);
+    }
+    tm::warp_mma_commit(&sh.s_full[w][h]);
+    if (h) tm::warp_mma_commit(&sh.kv_empty[slot.i]);
+    if (j + 1 == n) tm::warp_mma_commit(&sh.q_empty[w]);
+  };
+  Slot k;                                         // K of the step whose logits come next (in the unit at hand)
+  Unit u = read_unit(sh, 0);
+  int lead = 0;                                   // half steps of the unit whose logits are issued beforehand
 #pragma unroll 1
-    for (int i = o.n / 2; i < o.part.steps() && ok; ++i) {
+  for (int unit = 0; u.kind && ok; ++unit) {
+    const int n = 2 * u.n(w);
+    Slot v = k, first = k;                        // V's step; the next unit's first K
 #pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv, o.slot.next()) {
-        if (!wait(&sh.kv_full[o.slot.i], o.slot.parity)) return;
-        if (kv && o.part.partly(o.c.from + i)) {
-          if (!wait(&sh.scrubbed[scrubs % kPartly], (scrubs / kPartly) & 1)) return;
+    for (int i = 0; i < u.steps(); ++i) first.step();
+    Unit next = {};
+    bool known = false;                           // the next unit
+    int ahead = 0;                                // half steps of it whose logits are issued
+#pragma unroll 1
+    for (int j = lead; j < 2 && j < n && ok; ++j) {
+      if (j == 0 && wait(&sh.q_full[w], q_parity)) q_parity ^= 1;
+      if (wait(&sh.kv_full[k.i], k.parity)) logits(k, j, n);
+    }
+    if (n > 0) k.step();
+#pragma unroll 1
+    for (int j = 0; j < n && ok; ++j) {
+      const int h = j & 1;
+      if (h == 0) {
+        v.next();
+        if (!wait(&sh.kv_full[v.i], v.parity)) break;
+        if (u.partly(u.from + j / 2)) {
+          if (!wait(&sh.scrubbed[scrubs % kPartly], (scrubs / kPartly) & 1)) break;
           ++scrubs;
         }
-        if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&sh.kv_empty[o.slot.i]);
       }
-    }
-  };
-  // on to the next unit in which the group has a part; the logits' side only looks, the products' lets go
-  auto next = [&](Side& x, bool let_go) {
-    while (x.live && x.j == x.n && ok) {
-      if (let_go) {
-        skip();
-      } else {
-        for (int i = x.n / 2; i < x.part.steps(); ++i) x.next_step();
-      }
-      x.live = next_unit(p.work, x.c, steps);
-      if (!x.live) break;
-      x.part = Part(p, x.c);
-      x.n = 2 * x.part.n(w);
-      x.j = 0;
-    }
-  };
-  next(s, false);
-  next(o, true);
-  Watch watch;
-#pragma unroll 1
-  while (ok && (s.live || ahead > 0)) {
-    if (s.live && ahead < 2) {
-      uint64_t* const k_full = &sh.kv_full[s.slot.i];
-      const bool there = test(k_full, s.slot.parity) && (s.j > 0 || test(&sh.q_full[w], q_parity));
-      if (there || ahead == 0) {
-        if (!there && (!wait(k_full, s.slot.parity) || (s.j == 0 && !wait(&sh.q_full[w], q_parity)))) break;
-        if (s.j == 0) q_parity ^= 1;
-        const int h = s.j & 1;
-        tc::fence_after_sync();
-        const uint32_t k_half = k_lo + ((s.slot.i * kTileBytes + h * (kHalf * 128)) >> 4);
+      if (!wait(&sh.p_full[w][h], p_parity)) break;
+      tc::fence_after_sync();
+      const uint32_t v_half = v_lo + ((v.i * kTileBytes + h * (kHalf * 128)) >> 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t off = (uint32_t)((i >> 2) * kTile * 128 + (i & 3) * 32) >> 4;
-          tm::warp_mma_ss(s_at + h * kHalf, tm::desc_of(q_lo + off, qk_hi), tm::desc_of(k_half + off, qk_hi), s_idesc, i > 0 ? 1u : 0u);
-        }
-        tm::warp_mma_commit(&sh.s_full[w][h]);
-        ++ahead;
-        if (h) {
-          tm::warp_mma_commit(&sh.kv_empty[s.slot.i]);
-          s.next_step();
-        }
-        if (++s.j == s.n) {
-          tm::warp_mma_commit(&sh.q_empty[w]);
-          next(s, false);
-        }
-        continue;
+      for (int i = 0; i < kHalf / 16; ++i)        // 16 rows of V are 2048 bytes of each half of its columns
+        tm::warp_mma_ts(o_at, s_at + h * kHalf + i * 8, tm::desc_of(v_half + i * 128, v_hi), o_idesc, j > 0 || i > 0 ? 1u : 0u);
+      tm::warp_mma_commit(&sh.o_full[w][h]);
+      if (h) {
+        tm::warp_mma_commit(&sh.kv_empty[v.i]);
+        p_parity ^= 1;
+        v.next();
       }
-      // the product where its weights are there, or the logits' operands, whichever come first
-      if (!test(&sh.p_full[w][o.j & 1], p_parity)) {
-        ok = __all_sync(0xffffffffu, watch.go_on(sh, p.work.err));
-        continue;
+      if (j + 2 < n) {
+        if (!wait(&sh.kv_full[k.i], k.parity)) break;
+        logits(k, j + 2, n);
+        if (h) k.step();
+      } else {
+        // the next unit's first logits, where that is no wait for the products to come
+        if (!known && test(&sh.unit_full[(unit + 1) % kUnits], ((unit + 1) / kUnits) & 1)) {
+          next = read_unit(sh, unit + 1);
+          known = true;
+        }
+        if (known && next.n(w) > 0 && ahead == j + 2 - n && test(&sh.kv_full[first.i], first.parity) &&
+            (ahead > 0 || test(&sh.q_full[w], q_parity))) {
+          if (ahead == 0) q_parity ^= 1;
+          logits(first, ahead++, 2 * next.n(w));
+        }
       }
     }
-    const int h = o.j & 1;
-    Slot v = o.slot;
-    v.next();
-    if (!wait(&sh.p_full[w][h], p_parity)) break;
-    if (h == 0) {
-      if (!wait(&sh.kv_full[v.i], v.parity)) break;
-      if (o.part.partly(o.c.from + o.j / 2)) {
-        if (!wait(&sh.scrubbed[scrubs % kPartly], (scrubs / kPartly) & 1)) break;
+    // both groups let go of every tile, of those of steps as well that the other group alone has
+    Slot rest = v;
+#pragma unroll 1
+    for (int i = n; i < 2 * u.steps() && ok; ++i, rest.next()) {
+      wait(&sh.kv_full[rest.i], rest.parity);
+      if ((i & 1) && u.partly(u.from + i / 2)) {
+        wait(&sh.scrubbed[scrubs % kPartly], (scrubs / kPartly) & 1);
         ++scrubs;
       }
+      if (ok && (threadIdx.x & 31) == 0) tc::mbar_arrive(&sh.kv_empty[rest.i]);
     }
-    tc::fence_after_sync();
-#pragma unroll
-    for (int i = 0; i < kHalf / 16; ++i)          // 16 rows of V are 2048 bytes of each half of its columns
-      tm::warp_mma_ts(o_at, s_at + h * kHalf + i * 8,
-                      tm::desc_of(v_lo + ((v.i * kTileBytes + h * (kHalf * 128)) >> 4) + i * 128, v_hi), o_idesc,
-                      o.j > 0 || i > 0 ? 1u : 0u);
-    tm::warp_mma_commit(&sh.o_full[w][h]);
-    --ahead;
-    if (h) {
-      tm::warp_mma_commit(&sh.kv_empty[v.i]);
-      p_parity ^= 1;
-      o.next_step();
-    }
-    watch = Watch();
-    if (++o.j == o.n) next(o, true);
+    if (!ok) break;
+    let_go(sh, unit);
+    u = known ? next : read_unit(sh, unit + 1);
+    lead = ahead;
+    k = first;
   }
   // every MMA must finish before tensor and shared memory are released
   tm::warp_mma_commit(&sh.done[w]);
@@ -344,34 +365,109 @@ __device__ void mma_issuer(const PromptParams& p, AttentionShared& sh, const Pro
 __device__ __noinline__ void move_reference(uint32_t p_at, int columns, uint32_t o_at, float f) {
   tm::wait_stores();
   uint32_t x[16];
+#pragma unroll 1
   for (int c = 0; c < columns; c += 16) {
     tm::load16(p_at + c, x);
 #pragma unroll
     for (int k = 0; k < 16; ++k) x[k] = pack_bf16(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xffff0000u) * f);
     tm::store16(p_at + c, x);
   }
-  if (o_at) {
-    for (int c = 0; c < kHeadDim; c += 16) {
-      tm::load16(o_at + c, x);
+#pragma unroll 1
+  for (int c = 0; o_at && c < kHeadDim; c += 16) {
+    tm::load16(o_at + c, x);
 #pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
-      tm::store16(o_at + c, x);
+    for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+    tm::store16(o_at + c, x);
+  }
+}
+
+// A row's result of one part of a unit, and where it goes.
+struct RowResult {
+  Unit u;
+  int n, unit;                                    // steps of this row's group; units before
+  float ref, sum;
+};
+
+// Thread `row` of group w leaves its row of O, as it is when the group's products are through.
+__device__ __forceinline__ void leave_row(const PromptParams& p, AttentionShared& sh, const RowResult& r, int w, int row, uint32_t o_at) {
+  const int tl = p.by_group.div(row), token = r.u.tok0 + w * p.half + tl, hq = r.u.h * p.group + row - tl * p.group;
+  const bool real = tl < p.half && token <= r.u.reach;
+  const uint32_t* bad = sh.bad[r.unit % kUnits];
+  uint32_t any_bad = 0;
+  if (r.n > 0 && r.u.partly(r.u.from + r.n - 1))
+    for (int k = 0; k < kBadWords; ++k) any_bad |= bad[k];
+  const bool whole = r.u.kind == kWhole;
+  const size_t part_row = (size_t)(2 * blockIdx.x + (r.u.from == 0 ? 1 : 0)) * kRows + w * kTile + row;
+  const float inv = 1.f / r.sum;
+  const long long out_row = (long long)r.u.row0 + token;
+#pragma unroll 1
+  for (int h = 0; h < 4; ++h) {
+    float o[32];
+    if (r.n > 0) {
+      tc::tmem_ld32(o_at + 32 * h, o);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = 0.f;
     }
+    if (any_bad && real) {
+      // rare: the rows that were cleared, for the queries that see them, where this part's steps hold them
+#pragma unroll 1
+      for (int k = 0; k < kRows; ++k) {
+        const int tok = r.u.tok0 + 1 + k;
+        if (!((bad[k >> 5] >> (k & 31)) & 1) || tok > token) continue;
+        const int step = tok / kTile - r.u.from;
+        if (step < 0 || step >= r.n) continue;
+        const long long at = (long long)r.u.row0 + tok;
+        const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(p.k) + r.u.plane * p.kb + r.u.h * p.kh + at * p.km;
+        const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.v) + r.u.plane * p.vb + r.u.h * p.vh + at * p.vm + 32 * h;
+        const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q) + r.u.plane * p.qb + hq * p.qh + out_row * p.qm;
+        float z = 0.f;
+#pragma unroll 1
+        for (int d = 0; d < kHeadDim; ++d) z += __bfloat162float(qr[d]) * __bfloat162float(kr[d]);
+        const float wt = ex2(z * p.scale2 - base_of(r.ref));
+#pragma unroll
+        for (int d = 0; d < 32; ++d) o[d] += wt * __bfloat162float(vr[d]);
+      }
+    }
+    if (!real) continue;
+    if (whole) {
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + r.u.plane * p.ob + hq * p.oh + out_row * p.om + 32 * h;
+      uint32_t y[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) y[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
+      if (p.out_sectors) {
+        tm::store_sector(dst, y);
+        tm::store_sector(dst + 16, y + 8);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          reinterpret_cast<uint4*>(dst)[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+      }
+    } else {
+      float* dst = p.part + part_row * kHeadDim + 32 * h;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tm::store_sector(dst + 8 * k, reinterpret_cast<const uint32_t*>(o) + 8 * k);
+    }
+  }
+  if (!real) return;
+  if (!whole) {
+    p.part_ml[part_row] = make_float2(r.ref, r.sum);
+  } else if (p.lse) {
+    p.lse[((long long)r.u.plane * p.hq + hq) * p.work.m + out_row] = (r.ref + log2f(r.sum)) * 0.6931471805599453f;
   }
 }
 
 // One softmax group: thread `row` of group w.
-__device__ void softmax_group(const PromptParams& p, AttentionShared& sh, PromptCursor c, int w, int row, uint32_t tmem) {
-  const Steps steps{p.work.tile};
+__device__ void softmax_group(const PromptParams& p, AttentionShared& sh, int w, int row, uint32_t tmem) {
   const uint32_t lanes = (uint32_t)(row & ~31) << 16;
   const uint32_t s_at = tmem + lanes + (uint32_t)(w * kTile), o_at = s_at + 2 * kTile;
   const float scale = p.scale2, hidden = scale < 0.f ? INFINITY : -INFINITY;   // a logit that gives -infinity
-  const int tl = p.by_group.div(row), g = row - tl * p.group;     // token of the tile, head of the group
-  uint32_t turn = 0, unit = 0;                    // steps so far, units so far
+  const int tl = p.by_group.div(row) + w * p.half;                // the row's token in the unit
+  const bool has = tl < (w + 1) * p.half;
+  uint32_t turn = 0;                              // steps so far
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    const bool there = wait_phase(bar, parity, &sh.fail, p.work.err);
-    ok = __all_sync(0xffffffffu, there) && ok;
+    ok = warp_wait(bar, parity, sh) && ok;
     tc::fence_after_sync();
     return ok;
   };
@@ -380,25 +476,30 @@ __device__ void softmax_group(const PromptParams& p, AttentionShared& sh, Prompt
     wait(&sh.o_full[w][0], (h == 0 ? turn + 1 : turn) & 1);
     wait(&sh.o_full[w][1], (turn + 1) & 1);
   };
-  do {
-    const Part part(p, c);
-    const int n = part.n(w), token = part.tok0 + w * p.half + tl;
-    const bool real = tl < p.half && token <= part.reach;
+#pragma unroll 1
+  for (int unit = 0;; ++unit) {
+    const Unit u = read_unit(sh, unit);
+    if (!u.kind) break;
+    const int n = u.n(w), token = u.tok0 + tl;
+    const bool real = has && token <= u.reach;
     float ref = real ? -INFINITY : 0.f;           // rows without a query never wait for a maximum
     float sum = 0.f;
 #pragma unroll 1
-    for (int i = 0; i < n; ++i, ++turn) {
-      const int seen = token - (c.from + i) * kTile;   // columns 0 .. seen
-      const bool masked = __any_sync(0xffffffffu, real && seen < kTile - 1);
-      // 32 columns at a time; the next ones of the half step are on their way while these are at work
+    for (int j = 0; j < 2 * n; ++j) {
+      const int h = j & 1;
+      const uint32_t at = s_at + h * kHalf;
+      const int seen = token - u.from * kTile - j * kHalf;        // columns 0 .. seen
+      const bool masked = __any_sync(0xffffffffu, real && seen < kHalf - 1);
+      if (!wait(&sh.s_full[w][h], turn & 1)) break;
+      // 32 columns at a time; the next ones are on their way while these are at work
       float x[2][32];
-      auto chunk = [&](uint32_t at, int ch, int from, float(&y)[32], float(&next)[32]) {
+      auto chunk = [&](int ch, float(&y)[32], float(&next)[32]) {
         tm::wait32(y);
         if (ch == 0) tm::load32(at + 32, next);
         if (masked) {
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            if (from + k > seen) y[k] = hidden;
+            if (32 * ch + k > seen) y[k] = hidden;
         }
         const uint64_t sc2 = pack_f32x2(scale, scale);
         uint32_t pk[16];
@@ -429,99 +530,27 @@ __device__ void softmax_group(const PromptParams& p, AttentionShared& sh, Prompt
           const float to = real ? fmaxf(ref, top) : ref, f = weight_of(ref, to);
           ref = to;
           sum *= f;
-          // O follows once the products before this half step are through
-          const bool begun = i > 0 || from >= kHalf;
-          if (begun) wait_products(from / kHalf);
-          move_reference(at, 16 * ch, begun ? o_at : 0, f);
+          if (j > 0) wait_products(h);            // O follows once the products before this half step are through
+          move_reference(at, 16 * ch, j > 0 ? o_at : 0, f);
         }
         sum += got;
         tm::store16(at + 16 * ch, pk);            // over columns that are in registers by now
       };
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t at = s_at + h * kHalf;
-        if (!wait(&sh.s_full[w][h], turn & 1)) break;
-        tm::load32(at, x[0]);
-        chunk(at, 0, h * kHalf, x[0], x[1]);
-        chunk(at, 1, h * kHalf + 32, x[1], x[0]);
-        tm::wait_stores();
-        tc::fence_before_sync();
-        __syncwarp();
-        if ((row & 31) == 0) tc::mbar_arrive(&sh.p_full[w][h]);   // a warp's 32 arrivals would go one by one
-      }
-      if (!ok) break;
+      tm::load32(at, x[0]);
+      chunk(0, x[0], x[1]);
+      chunk(1, x[1], x[0]);
+      tm::wait_stores();
+      tc::fence_before_sync();
+      __syncwarp();
+      if ((row & 31) == 0) tc::mbar_arrive(&sh.p_full[w][h]);     // a warp's 32 arrivals would go one by one
+      turn += h;
     }
-    if (!ok) break;
     if (n > 0) wait_products(0);
     if (!ok) break;
-    const uint32_t* bad = sh.bad[unit++ % kBadSets];
-    uint32_t any_bad = 0;
-    if (n > 0 && part.partly(c.to - 1))
-      for (int k = 0; k < kBadWords; ++k) any_bad |= bad[k];
-    const bool whole = c.to - c.from == c.k.steps;
-    const bool write = real && (whole ? n > 0 : true);
-    const size_t part_row = (size_t)(2 * blockIdx.x + (c.from == 0 ? 1 : 0)) * kRows + w * kTile + row;
-    const float inv = 1.f / sum;
-    const long long out_row = (long long)c.k.at.row0 + token;
-    const int hq = c.h * p.group + g;
-#pragma unroll 1
-    for (int h = 0; h < 4; ++h) {
-      float o[32];
-      if (n > 0) {
-        tc::tmem_ld32(o_at + 32 * h, o);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = 0.f;
-      }
-      if (any_bad && write) {
-        // rare: the rows that were cleared, for the queries that see them, where this part's steps hold them
-#pragma unroll 1
-        for (int k = 0; k < kRows; ++k) {
-          const int tok = part.tok0 + 1 + k;
-          if (!((bad[k >> 5] >> (k & 31)) & 1) || tok > token) continue;
-          const int step = tok / kTile - c.from;
-          if (step < 0 || step >= n) continue;
-          const long long at = (long long)c.k.at.row0 + tok;
-          const __nv_bfloat16* kr = static_cast<const __nv_bfloat16*>(p.k) + c.k.at.plane * p.kb + c.h * p.kh + at * p.km;
-          const __nv_bfloat16* vr = static_cast<const __nv_bfloat16*>(p.v) + c.k.at.plane * p.vb + c.h * p.vh + at * p.vm + 32 * h;
-          const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q) + c.k.at.plane * p.qb + hq * p.qh + out_row * p.qm;
-          float z = 0.f;
-#pragma unroll 1
-          for (int d = 0; d < kHeadDim; ++d) z += __bfloat162float(qr[d]) * __bfloat162float(kr[d]);
-          const float wt = ex2(z * scale - base_of(ref));
-#pragma unroll
-          for (int d = 0; d < 32; ++d) o[d] += wt * __bfloat162float(vr[d]);
-        }
-      }
-      if (!write) continue;
-      if (whole) {
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + c.k.at.plane * p.ob + hq * p.oh + out_row * p.om + 32 * h;
-        uint32_t y[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) y[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
-        if (p.out_sectors) {
-          tm::store_sector(dst, y);
-          tm::store_sector(dst + 16, y + 8);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            reinterpret_cast<uint4*>(dst)[k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
-        }
-      } else {
-        float* dst = p.part + part_row * kHeadDim + 32 * h;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tm::store_sector(dst + 8 * k, reinterpret_cast<const uint32_t*>(o) + 8 * k);
-      }
-    }
-    if (write) {
-      if (!whole) {
-        p.part_ml[part_row] = make_float2(ref, sum);
-      } else if (p.lse) {
-        p.lse[((long long)c.k.at.plane * p.hq + hq) * p.work.m + out_row] = (ref + log2f(sum)) * 0.6931471805599453f;
-      }
-    }
+    leave_row(p, sh, RowResult{u, n, unit, ref, sum}, w, row, o_at);
+    let_go(sh, unit);
     tc::fence_before_sync();                      // O is read: the next unit's first product follows our weights
-  } while (next_unit(p.work, c, steps));
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __grid_constant__ PromptParams p) {
@@ -549,6 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
       tc::mbar_init(&sh.partly_full[i], 1);
       tc::mbar_init(&sh.scrubbed[i], 1);
     }
+    for (int i = 0; i < kUnits; ++i) {
+      tc::mbar_init(&sh.unit_full[i], 1);
+      tc::mbar_init(&sh.unit_empty[i], kReaders);
+    }
     sh.fail = 0;
   }
   if (warp == kTmaWarp && lane == 0) {
@@ -565,20 +598,21 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
   const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem_base, 0), ring = smem + 2 * kTileBytes;
   if (any) {
     if (warp < kMmaWarp) {
-      softmax_group(p, sh, c, warp >> 2, tid & (kTile - 1), tmem);
+      softmax_group(p, sh, warp >> 2, tid & (kTile - 1), tmem);
     } else if (warp < kTmaWarp) {
-      mma_issuer(p, sh, c, warp - kMmaWarp, tmem, smem, ring);
+      mma_issuer(p, sh, warp - kMmaWarp, tmem, smem, ring);
     } else if (warp == kTmaWarp) {
       if (lane == 0) producer(p, sh, c, smem, ring);
       __syncwarp();
     } else {
-      scrub(p, sh, c, ring);
+      scrub(p, sh, ring);
     }
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   if (warp == 0) tc::tmem_dealloc(tmem, 4 * kTile);
+  if (tid == 0 && sh.fail) raise_device_error(p.work.err, kDevWaitTimeout);
 }
 
 // Rows of units that two or more CTAs share: a warp merges a row's parts, in the shares' order.
