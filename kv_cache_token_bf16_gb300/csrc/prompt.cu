@@ -258,7 +258,7 @@ __device__ void scrub(const PromptParams& p, AttentionShared& sh, uint32_t ring)
 // of half step j + 2 may be issued over the weights of half step j behind their product with V.
 __device__ void mma_issuer(const PromptParams& p, AttentionShared& sh, int w, uint32_t tmem, uint32_t qbuf, uint32_t ring) {
   const uint64_t qd = tc::sw128_desc(qbuf + w * kTileBytes), vd = tc::sw128_desc_mn(ring, kTileBytes / 2, 1024);
-  const uint32_t q_lo = (uint32_t)qd, k_lo = (uint32_t)tc::sw128_desc(ring), v_lo = (uint32_t)vd;
+  const uint32_t k_lo = (uint32_t)tc::sw128_desc(ring), v_lo = (uint32_t)vd;
   const uint32_t qk_hi = (uint32_t)(qd >> 32), v_hi = (uint32_t)(vd >> 32);
   const uint32_t s_at = tmem + w * kTile, o_at = s_at + 2 * kTile;
   constexpr uint32_t s_idesc = tc::idesc_bf16_f32(kTile, kHalf), o_idesc = tc::idesc_bf16_f32(kTile, kTile) | (1u << 16);
@@ -270,12 +270,7 @@ __device__ void mma_issuer(const PromptParams& p, AttentionShared& sh, int w, ui
   auto logits = [&](const Slot& slot, int j, int n) {
     const int h = j & 1;
     tc::fence_after_sync();
-    const uint32_t k_half = k_lo + ((slot.i * kTileBytes + h * (kHalf * 128)) >> 4);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t off = (uint32_t)((i >> 2) * kTile * 128 + (i & 3) * 32) >> 4;
-      tm::warp_mma_ss(s_at + h * kHalf, tm::desc_of(q_lo + off, qk_hi), tm::desc_of(k_half + off, qk_hi), s_idesc, i > 0 ? 1u : 0u);
-    }
+    tm::warp_mma_rows(s_at + h * kHalf, qd, tm::desc_of(k_lo + ((slot.i * kTileBytes + h * (kHalf * 128)) >> 4), qk_hi), s_idesc);
     tm::warp_mma_commit(&sh.s_full[w][h]);
     if (h) tm::warp_mma_commit(&sh.kv_empty[slot.i]);
     if (j + 1 == n) tm::warp_mma_commit(&sh.q_empty[w]);
@@ -311,10 +306,8 @@ __device__ void mma_issuer(const PromptParams& p, AttentionShared& sh, int w, ui
       }
       if (!wait(&sh.p_full[w][h], p_parity)) break;
       tc::fence_after_sync();
-      const uint32_t v_half = v_lo + ((v.i * kTileBytes + h * (kHalf * 128)) >> 4);
-#pragma unroll
-      for (int i = 0; i < kHalf / 16; ++i)        // 16 rows of V are 2048 bytes of each half of its columns
-        tm::warp_mma_ts(o_at, s_at + h * kHalf + i * 8, tm::desc_of(v_half + i * 128, v_hi), o_idesc, j > 0 || i > 0 ? 1u : 0u);
+      tm::warp_mma_weights(o_at, s_at + h * kHalf, tm::desc_of(v_lo + ((v.i * kTileBytes + h * (kHalf * 128)) >> 4), v_hi), o_idesc,
+                           j > 0 ? 1u : 0u);
       tm::warp_mma_commit(&sh.o_full[w][h]);
       if (h) {
         tm::warp_mma_commit(&sh.kv_empty[v.i]);
@@ -465,11 +458,11 @@ __device__ void softmax_group(const PromptParams& p, AttentionShared& sh, int w,
   const int tl = p.by_group.div(row) + w * p.half;                // the row's token in the unit
   const bool has = tl < (w + 1) * p.half;
   uint32_t turn = 0;                              // steps so far
-  bool ok = true;
+  // (no vote: a wait that gives up leaves `fail`, which is looked at once a unit)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    ok = warp_wait(bar, parity, sh) && ok;
+    wait_for(bar, parity, sh);
+    __syncwarp();
     tc::fence_after_sync();
-    return ok;
   };
   // The products with V before half h of this step.
   auto wait_products = [&](int h) {
@@ -489,8 +482,8 @@ __device__ void softmax_group(const PromptParams& p, AttentionShared& sh, int w,
       const int h = j & 1;
       const uint32_t at = s_at + h * kHalf;
       const int seen = token - u.from * kTile - j * kHalf;        // columns 0 .. seen
-      const bool masked = __any_sync(0xffffffffu, real && seen < kHalf - 1);
-      if (!wait(&sh.s_full[w][h], turn & 1)) break;
+      const bool masked = u.from * kTile + j * kHalf + kHalf - 1 > u.tok0 + w * p.half;   // some row does not see them all
+      wait(&sh.s_full[w][h], turn & 1);
       // 32 columns at a time; the next ones are on their way while these are at work
       float x[2][32];
       auto chunk = [&](int ch, float(&y)[32], float(&next)[32]) {
@@ -546,7 +539,7 @@ __device__ void softmax_group(const PromptParams& p, AttentionShared& sh, int w,
       turn += h;
     }
     if (n > 0) wait_products(0);
-    if (!ok) break;
+    if (__any_sync(0xffffffffu, *(volatile int*)&sh.fail)) break;
     leave_row(p, sh, RowResult{u, n, unit, ref, sum}, w, row, o_at);
     let_go(sh, unit);
     tc::fence_before_sync();                      // O is read: the next unit's first product follows our weights
@@ -616,15 +609,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
 }
 
 // Rows of units that two or more CTAs share: a warp merges a row's parts, in the shares' order.
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 8, kJoinSplit = 4;
 __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(const __grid_constant__ PromptParams p) {
   pdl_wait();
   SplitUnit u;
   if (!split_unit(p.work, blockIdx.x + 1, u, Steps{p.work.tile})) return;
-  const int lane = threadIdx.x & 31, row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); row < kRows; row += kJoinWarps * kJoinSplit) {
   const int w = row / kTile, tl = p.by_group.div(row - w * kTile), g = row - w * kTile - tl * p.group;
   const int token = u.k.tile * p.work.tile + w * p.half + tl;
-  if (tl >= p.half || token >= u.k.at.len) return;
+  if (tl >= p.half || token >= u.k.at.len) continue;
   float top = -INFINITY, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
@@ -647,6 +642,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(const __gr
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   if (p.lse && lane == 0)
     p.lse[((long long)u.k.at.plane * p.hq + hq) * p.work.m + out_row] = (top + log2f(sum)) * 0.6931471805599453f;
+  }
 }
 
 bool multiple(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -843,7 +839,7 @@ extern "C" int evict_prompt_attention(const evict_prompt* a) {
     return cuda_fail(e, "prompt attention kernel launch");
   g_launches.fetch_add(1);
   if (!p.work.whole && ctas > 1) {
-    if ((e = launch_pdl(prompt_join_kernel, dim3(ctas - 1, kRows / kJoinWarps), dim3(kJoinWarps * 32), 0, st, nullptr, p)) != cudaSuccess)
+    if ((e = launch_pdl(prompt_join_kernel, dim3(ctas - 1, kJoinSplit), dim3(kJoinWarps * 32), 0, st, nullptr, p)) != cudaSuccess)
       return cuda_fail(e, "prompt join kernel launch");
     g_launches.fetch_add(1);
   }

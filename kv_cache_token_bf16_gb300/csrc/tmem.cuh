@@ -11,24 +11,51 @@ namespace tm {
 // A shared-memory descriptor of two words; the low one holds the start address.
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return (uint64_t)lo | ((uint64_t)hi << 32); }
 
-// The same products, issued by one lane of a converged warp: what the whole warp computes alike the compiler keeps
-// in the uniform registers that these instructions take their operands from. (A lone thread's operands are moved
-// there one by one: 128 x 64 x 16 products then take 65 clocks instead of 48.)
-__device__ __forceinline__ void warp_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Products issued by one lane of a converged warp: what the whole warp computes alike the compiler keeps in the
+// uniform registers that these instructions take their operands from. (A lone thread's operands are moved there one
+// by one: 128 x 64 x 16 products then take 65 clocks instead of 48.) The lane is elected once for all of them.
+// D[tmem] = A B^T, both K-major tiles of 128 rows of 128 elements (B's descriptor may begin further down): eight
+// steps of 16 elements, 32 bytes further in a half of the row.
+__device__ __forceinline__ void warp_mma_rows(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p, one;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred one, first, more;\n\t.reg .b64 a, b;\n\t"
       "elect.sync _|one, 0xffffffff;\n\t"
-      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.u32 first, 0, 0;\n\t"
+      "setp.eq.u32 more, 0, 0;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, first;\n\t"
+      "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, more;\n\t"
+      "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, more;\n\t"
+      "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, more;\n\t"
+      "add.s64 a, %1, 1024;\n\tadd.s64 b, %2, 1024;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, more;\n\t"
+      "add.s64 a, %1, 1026;\n\tadd.s64 b, %2, 1026;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, more;\n\t"
+      "add.s64 a, %1, 1028;\n\tadd.s64 b, %2, 1028;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, more;\n\t"
+      "add.s64 a, %1, 1030;\n\tadd.s64 b, %2, 1030;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, more;\n\t"
+      "}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc)
       : "memory");
 }
-__device__ __forceinline__ void warp_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] B over 64 rows of B, MN-major with 16 rows in 2048 bytes; A has two elements a column.
+__device__ __forceinline__ void warp_mma_weights(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, one;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred one, first, more;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
       "elect.sync _|one, 0xffffffff;\n\t"
-      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "setp.ne.u32 first, %4, 0;\n\t"
+      "setp.eq.u32 more, 0, 0;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, first;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
+      "}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }

@@ -182,12 +182,8 @@ __device__ void mma_issuer(const PromptParams& p, WeightsShared& sh, PromptCurso
 #pragma unroll 1
       for (int kt = 0; kt < 2; ++kt) {
         if (!s.sees(u, kt)) continue;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t off = (uint32_t)((j >> 2) * kTile * 128 + (j & 3) * 32) >> 4;
-          tm::warp_mma_ss(tmem + (2 * s_buf.i + kt) * kTile, tm::desc_of(k_lo + (((2 * k.i + kt) * kTileBytes) >> 4) + off, hi),
-                          tm::desc_of(q_lo + ((q.i * kTileBytes) >> 4) + off, hi), idesc, j > 0 ? 1u : 0u);
-        }
+        tm::warp_mma_rows(tmem + (2 * s_buf.i + kt) * kTile, tm::desc_of(k_lo + (((2 * k.i + kt) * kTileBytes) >> 4), hi),
+                          tm::desc_of(q_lo + ((q.i * kTileBytes) >> 4), hi), idesc);
       }
       tm::warp_mma_commit(&sh.s_full[s_buf.i]);
       tm::warp_mma_commit(&sh.q_empty[q.i]);
