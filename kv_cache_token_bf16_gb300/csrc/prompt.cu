@@ -44,7 +44,6 @@ constexpr int kReaders = 11;                      // warps that read a unit: sof
 constexpr int kBadWords = kRows / 32;             // rows of V behind the unit's first token, a bit each
 constexpr int kPartly = 4;                        // barriers of tiles to scrub, in turn: the ring holds at most three
 constexpr float kMoveAbove = 4096.f;              // sum of 32 weights that makes the reference move
-constexpr uint32_t kPolls = 100000;               // of a wait, each of up to 20 us
 constexpr int kEntry = 2, kMinSteps = 4;
 constexpr int kWholeRows = 1024;
 
@@ -91,30 +90,10 @@ struct Slot {
   }
 };
 
-// Waits at many places, so little code: polls that sleep in hardware, a bounded number of them. The kernel's end
-// reports one that gave up.
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, AttentionShared& sh) {
-  if (tc::mbar_try_wait(bar, parity)) return true;
-#pragma unroll 1
-  for (uint32_t polls = 0; !tc::mbar_try_wait_sleep(bar, parity, kWaitSleepNs);)
-    if (++polls == kPolls || *(volatile int*)&sh.fail) {
-      *(volatile int*)&sh.fail = 1;
-      return false;
-    }
-  return true;
-}
-// A warp's wait; the same for all its lanes.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, AttentionShared& sh) {
-  return __all_sync(0xffffffffu, wait_for(bar, parity, sh));
-}
-// One lane's value for the warp, which the compiler then knows to be the same: what follows from it stays in uniform
-// registers, where products take their operands from. (A lone thread's, or what might differ, is moved there one by
-// one: 128 x 64 x 16 products then take 65 clocks instead of 48; a document of 8192 tokens 395 us instead of 369.)
-__device__ __forceinline__ int uni(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 // The i-th unit of the CTA, by a whole warp; kind 0 behind the last one, and where a wait gave up.
 __device__ __forceinline__ Unit read_unit(AttentionShared& sh, int i) {
   Unit u = {};
-  if (warp_wait(&sh.unit_full[i % kUnits], (i / kUnits) & 1, sh)) u = sh.units[i % kUnits];
+  if (warp_wait(&sh.unit_full[i % kUnits], (i / kUnits) & 1, &sh.fail)) u = sh.units[i % kUnits];
   u.plane = uni(u.plane), u.row0 = uni(u.row0), u.h = uni(u.h);
   u.tok0 = uni(u.tok0), u.reach = uni(u.reach), u.from = uni(u.from);
   u.n0 = uni(u.n0), u.n1 = uni(u.n1), u.kind = uni(u.kind);
@@ -131,7 +110,7 @@ __device__ void producer(const PromptParams& p, AttentionShared& sh, PromptCurso
   Slot slot;
   int used = 0, turns0 = 0, turns1 = 0, partly = 0, unit = 0;
   bool ok = true, any = true;                     // any: there is a unit at hand
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = wait_for(bar, parity, sh); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = wait_for(bar, parity, &sh.fail); };
   for (;; ++unit) {
     if (!wait(&sh.unit_empty[unit % kUnits], ((unit / kUnits) & 1) ^ 1)) break;
     Unit u = {};
@@ -215,7 +194,7 @@ __device__ void scrub(const PromptParams& p, AttentionShared& sh, uint32_t ring)
     for (int step = u.from; step < u.from + u.steps(); ++step) {
       slot.next();                                // the step's V
       if (u.partly(step)) {
-        if (!warp_wait(&sh.partly_full[count % kPartly], (count / kPartly) & 1, sh)) return;
+        if (!warp_wait(&sh.partly_full[count % kPartly], (count / kPartly) & 1, &sh.fail)) return;
 #pragma unroll 1
         for (int r = lane; r < kTile; r += 32) {
           const uint32_t at = ring + slot.i * kTileBytes + r * 128;
@@ -264,7 +243,7 @@ __device__ void mma_issuer(const PromptParams& p, AttentionShared& sh, int w, ui
   constexpr uint32_t s_idesc = tc::idesc_bf16_f32(kTile, kHalf), o_idesc = tc::idesc_bf16_f32(kTile, kTile) | (1u << 16);
   uint32_t q_parity = 0, p_parity = 0, scrubs = 0;
   bool ok = true;
-  auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && warp_wait(bar, parity, sh); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && warp_wait(bar, parity, &sh.fail); };
   auto test = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, test_phase(bar, parity)) != 0; };
   // The logits of half step j of n, K in `slot`.
   auto logits = [&](const Slot& slot, int j, int n) {
@@ -460,7 +439,7 @@ __device__ void softmax_group(const PromptParams& p, AttentionShared& sh, int w,
   uint32_t turn = 0;                              // steps so far
   // (no vote: a wait that gives up leaves `fail`, which is looked at once a unit)
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    wait_for(bar, parity, sh);
+    wait_for(bar, parity, &sh.fail);
     __syncwarp();
     tc::fence_after_sync();
   };

@@ -42,9 +42,11 @@ struct PromptParams {
   long long qb, qh, qm, kb, kh, km, vb, vh, vm, ob, oh, om;   // element strides
   int hq, group;                     // group = query heads of a KV head
   Divisor by_group;
-  int half;                          // attention: tokens of a tile of 128 query rows
+  int half;                          // attention: tokens of a tile of 128 query rows; weights: tokens of a step
   int out_sectors;                   // every row of out begins on a multiple of 32 bytes
   int last;                          // weights: the last queries of a sequence that count
+  int half_shift;                    // weights: log2 half
+  int step_heads, head_steps;        // weights: heads of a step, steps that the group's heads take
   float scale2;                      // log2(e) * scale
   float2* part_ml;                   // attention: [2 CTAs][256] maximum (base 2) and sum
   float* part;                       // attention: [2 CTAs][256][128] outputs; weights: [2 CTAs][256] sums
