@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
   }
   pdl_wait();
   PromptCursor c;
-  const bool any = first_unit<kThreads>(p.work, sh.scan, c, Steps{p.work.tile});
+  const bool any = first_unit<kThreads>(p.work, sh.scan, reinterpret_cast<int*>(smem_raw + (smem - tc::smem_u32(smem_raw))), c, Steps{p.work.tile});
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();

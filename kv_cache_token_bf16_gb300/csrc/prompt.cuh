@@ -15,11 +15,6 @@ namespace evict {
 struct Span {
   int plane, row0, len;
 };
-__device__ __forceinline__ Span span_of(const PromptWork& w, int s) {
-  if (!w.starts) return {s, 0, w.m};
-  const int a = w.starts[s];
-  return {0, a, w.starts[s + 1] - a};
-}
 
 struct PromptBlock {
   int s, tile;                       // sequence, block of it
@@ -27,26 +22,34 @@ struct PromptBlock {
   int steps;                         // of each of its units
 };
 
+// Where packed sequences begin, and the blocks of those before each: in memory, or in shared memory.
+struct Tables {
+  const int32_t* starts;
+  const int* base;
+};
+
 // Block e (below the blocks' number), where sequences are packed the last that begins at or before it.
-// Steps(work, first token, length) are the kernel's.
+// Steps(first token, length) are the kernel's.
 template <typename Steps>
-__device__ __forceinline__ PromptBlock block_of(const PromptWork& w, int e, Steps steps) {
+__device__ __forceinline__ PromptBlock block_of(const PromptWork& w, const Tables& t, int e, Steps steps) {
   PromptBlock k;
   if (!w.starts) {
     k.s = w.by_seq_blocks.div(e);
     k.tile = e - k.s * (int)w.by_seq_blocks.by;
+    k.at = {k.s, 0, w.m};
   } else {
     int lo = 0, hi = w.seqs;
 #pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (w.block_base[mid] <= e) lo = mid;
+      if (t.base[mid] <= e) lo = mid;
       else hi = mid;
     }
     k.s = lo;
-    k.tile = e - w.block_base[lo];
+    k.tile = e - t.base[lo];
+    const int row0 = t.starts[lo];
+    k.at = {0, row0, t.starts[lo + 1] - row0};
   }
-  k.at = span_of(w, k.s);
   k.steps = steps(k.tile * w.tile, k.at.len);
   return k;
 }
@@ -54,7 +57,8 @@ __device__ __forceinline__ PromptBlock block_of(const PromptWork& w, int e, Step
 constexpr int kMaxPromptWarps = 20;
 struct PromptScan {
   int sum[kMaxPromptWarps];
-  int blocks, e, rest;
+  int e, rest;
+  PromptBlock k;
 };
 
 // Sum of x over the threads before this one; its total. Between two calls is a barrier.
@@ -80,17 +84,29 @@ __device__ __forceinline__ int prompt_scan(int x, int& total, PromptScan& sh) {
   return y - x + (warp ? __shfl_sync(0xffffffffu, u, warp - 1) : 0);
 }
 
+// Sequences whose tables fit the shared memory that the tiles have not come to yet.
+constexpr int kScratchSeqs = 4096;
+
 // The blocks' number, 0 where the sequences are not one behind the other inside the plane: then the call
 // writes nothing but the error. All threads. Every CTA leaves the same block_base, and reads back its own.
 template <int kThreads>
-__device__ __forceinline__ int count_blocks(const PromptWork& w, PromptScan& sh) {
+__device__ __forceinline__ int count_blocks(const PromptWork& w, PromptScan& sh, int* scratch, Tables& t) {
+  t = {w.starts, w.block_base};
   if (!w.starts) return w.blocks;
   const int tid = threadIdx.x, per = (w.seqs + kThreads - 1) / kThreads;
   const int s0 = min(tid * per, w.seqs), s1 = min(s0 + per, w.seqs);
+  int* bases = nullptr;
+  if (w.seqs <= kScratchSeqs) {                   // the searches below are in them
+#pragma unroll 1
+    for (int s = tid; s <= w.seqs; s += kThreads) scratch[s] = w.starts[s];
+    bases = scratch + kScratchSeqs + 1;
+    t = {scratch, bases};
+    __syncthreads();
+  }
   int bad = 0, mine = 0;
 #pragma unroll 1
   for (int s = s0; s < s1; ++s) {
-    const int a = w.starts[s], b = w.starts[s + 1];
+    const int a = t.starts[s], b = t.starts[s + 1];
     if (a < 0 || b < a || b > w.m) bad = 1;
     else mine += w.by_tile.div(b - a + w.tile - 1);
   }
@@ -102,7 +118,8 @@ __device__ __forceinline__ int count_blocks(const PromptWork& w, PromptScan& sh)
 #pragma unroll 1
   for (int s = s0; s < s1; ++s) {
     w.block_base[s] = base;
-    base += w.by_tile.div(w.starts[s + 1] - w.starts[s] + w.tile - 1);
+    if (bases) bases[s] = base;
+    base += w.by_tile.div(t.starts[s + 1] - t.starts[s] + w.tile - 1);
   }
   __syncthreads();
   return total;
@@ -130,84 +147,82 @@ __device__ __forceinline__ bool settle(PromptCursor& c, int step) {
   return true;
 }
 
-// On to the next unit; false at the share's end.
+// On to the next unit; false at the share's end. (This and first_unit look a block up in one place each: at a
+// kernel's start its code comes from memory, some 6,000 clocks for 25 KB of it.)
 template <typename Steps>
 __device__ __forceinline__ bool next_unit(const PromptWork& w, PromptCursor& c, Steps steps) {
-  if (w.whole) {
-    c.left -= gridDim.x;
-    if (c.left <= 0) return false;
-    c.h += gridDim.x;
-    if (c.h >= w.hkv) {
-      const int up = w.by_hkv.div(c.h);
-      c.e += up;
-      c.h -= up * w.hkv;
-      c.k = block_of(w, c.e, steps);
-    }
-    c.from = 0;
-    c.to = c.k.steps;
-    return true;
-  }
-  c.left -= c.to - c.from;
+  const int by = w.whole ? (int)gridDim.x : 1;
+  c.left -= w.whole ? by : c.to - c.from;
   if (c.left <= 0) return false;
-  if (++c.h == w.hkv) {
-    c.h = 0;
-    c.k = block_of(w, ++c.e, steps);
+  c.h += by;
+  if (c.h >= w.hkv) {
+    const int up = w.by_hkv.div(c.h);
+    c.e += up;
+    c.h -= up * w.hkv;
+    c.k = block_of(w, Tables{w.starts, w.block_base}, c.e, steps);
   }
-  return settle(c, -w.entry);
+  if (!w.whole) return settle(c, -w.entry);
+  c.from = 0;
+  c.to = c.k.steps;
+  return true;
 }
 
-// Where this CTA's share begins; false where it has none. All threads call it, and again nothing of `sh`
-// is written after it. The shares are left for the join.
+// Where this CTA's share begins; false where it has none. All threads call it, and a barrier comes before the first
+// copy to `scratch` (2 kScratchSeqs + 1 words). The shares are left for the join.
 template <int kThreads, typename Steps>
-__device__ __forceinline__ bool first_unit(const PromptWork& w, PromptScan& sh, PromptCursor& c, Steps steps) {
-  c.blocks = count_blocks<kThreads>(w, sh);
-  if (w.whole) {
-    const int units = c.blocks * w.hkv;
-    if ((int)blockIdx.x >= units) return false;
-    c.left = units - blockIdx.x;
-    c.e = w.by_hkv.div(blockIdx.x);
-    c.h = blockIdx.x - c.e * w.hkv;
-    c.k = block_of(w, c.e, steps);
-    c.from = 0;
-    c.to = c.k.steps;
-    return true;
-  }
-  const int tid = threadIdx.x, per = (c.blocks + kThreads - 1) / kThreads;
+__device__ __forceinline__ bool first_unit(const PromptWork& w, PromptScan& sh, int* scratch, PromptCursor& c, Steps steps) {
+  Tables t;
+  c.blocks = count_blocks<kThreads>(w, sh, scratch, t);
+  tc::fence_proxy_async_smem();                   // of `scratch`, for the copies to come
+  const int tid = threadIdx.x, per = (c.blocks + kThreads - 1) / kThreads, units = c.blocks * w.hkv;
   const int e0 = min(tid * per, c.blocks), e1 = min(e0 + per, c.blocks);
-  int mine = 0;
+  Shares shares;
+  int base = 0, g0 = 0;
+  // the sums of the steps, unless units are not cut; then the block where the share begins
 #pragma unroll 1
-  for (int e = e0; e < e1; ++e) mine += (block_of(w, e, steps).steps + w.entry) * w.hkv;
-  int total, base = prompt_scan<kThreads>(mine, total, sh);
-  const Shares shares(total, total ? max(1, min((int)gridDim.x, total / w.min_steps)) : 0);
-  const bool has = (int)blockIdx.x < shares.count;
-  const int g0 = has ? shares.begin(blockIdx.x) : 0;
-  if (blockIdx.x == 0 && tid == 0) {
-    w.total[0] = total;
-    w.total[1] = shares.count;
-  }
-  if (!has) return false;                         // the whole CTA
-  if (g0 >= base && g0 < base + mine) {
+  for (int find = w.whole; find < 2; ++find) {
+    if (find) {
+      if (!w.whole && (int)blockIdx.x >= shares.count) return false;   // the whole CTA, here and below
+      if (w.whole && (int)blockIdx.x >= units) return false;
+      g0 = w.whole ? 0 : shares.begin(blockIdx.x);
+    }
+    int at = base;
 #pragma unroll 1
     for (int e = e0; e < e1; ++e) {
-      const int of_block = (block_of(w, e, steps).steps + w.entry) * w.hkv;
-      if (g0 < base + of_block) {
+      const PromptBlock k = block_of(w, t, e, steps);
+      const int of_block = (k.steps + w.entry) * w.hkv;
+      if (find && (w.whole ? e == w.by_hkv.div(blockIdx.x) : g0 >= at && g0 < at + of_block)) {
         sh.e = e;
-        sh.rest = g0 - base;
-        w.begin[blockIdx.x] = make_int2(e, g0 - base);
-        break;
+        sh.rest = g0 - at;
+        sh.k = k;
+        if (!w.whole) w.begin[blockIdx.x] = make_int2(e, g0 - at);
       }
-      base += of_block;
+      at += of_block;
+    }
+    if (!find) {
+      int total;
+      base = prompt_scan<kThreads>(at, total, sh);
+      shares = Shares(total, total ? max(1, min((int)gridDim.x, total / w.min_steps)) : 0);
+      if (blockIdx.x == 0 && tid == 0) {
+        w.total[0] = total;
+        w.total[1] = shares.count;
+      }
     }
   }
   __syncthreads();
   c.e = sh.e;
-  c.k = block_of(w, c.e, steps);
+  c.k = sh.k;
+  if (w.whole) {
+    c.left = units - blockIdx.x;
+    c.h = blockIdx.x - c.e * w.hkv;
+    c.from = 0;
+    c.to = c.k.steps;
+    return true;
+  }
   const int unit = c.k.steps + w.entry;
   c.h = sh.rest / unit;
   c.left = shares.begin(blockIdx.x + 1) - g0;
-  c.from = c.to = 0;
-  if (settle(c, sh.rest - c.h * unit - w.entry)) return true;
-  return false;                                   // the share lies in one unit's entry
+  return settle(c, sh.rest - c.h * unit - w.entry);   // false: the share lies in one unit's entry
 }
 
 // A unit that two or more CTAs share, found where a share begins inside it: the first such share's
@@ -221,7 +236,7 @@ __device__ __forceinline__ bool split_unit(const PromptWork& w, int c, SplitUnit
   const Shares shares(w.total[0], w.total[1]);
   if (c >= shares.count) return false;
   const int2 at = w.begin[c];
-  u.k = block_of(w, at.x, steps);
+  u.k = block_of(w, Tables{w.starts, w.block_base}, at.x, steps);
   const int per = u.k.steps + w.entry;
   u.h = at.y / per;
   const int step = at.y - u.h * per - w.entry;

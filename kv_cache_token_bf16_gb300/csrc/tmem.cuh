@@ -41,6 +41,32 @@ __device__ __forceinline__ void warp_mma_rows(uint32_t d, uint64_t a, uint64_t b
       "l"(a), "l"(b), "r"(idesc)
       : "memory");
 }
+// D[tmem] = A[tmem] B^T, 128 elements deep: A has two elements a column, B as above.
+__device__ __forceinline__ void warp_mma_rows_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred one, first, more;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
+      "elect.sync _|one, 0xffffffff;\n\t"
+      "setp.ne.u32 first, 0, 0;\n\t"
+      "setp.eq.u32 more, 0, 0;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, first;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.s64 b, %2, 2;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.s64 b, %2, 4;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.s64 b, %2, 6;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
+      "add.u32 a, %1, 32;\n\tadd.s64 b, %2, 1024;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
+      "add.u32 a, %1, 40;\n\tadd.s64 b, %2, 1026;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
+      "add.u32 a, %1, 48;\n\tadd.s64 b, %2, 1028;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
+      "add.u32 a, %1, 56;\n\tadd.s64 b, %2, 1030;\n\t"
+      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
+      "}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc)
+      : "memory");
+}
 // D[tmem] (+)= A[tmem] B over 64 rows of B, MN-major with 16 rows in 2048 bytes; A has two elements a column.
 __device__ __forceinline__ void warp_mma_weights(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(

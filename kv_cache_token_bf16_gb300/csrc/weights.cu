@@ -90,8 +90,14 @@ struct Step {
     n = min(p.half, u.len - tok0);
   }
   __device__ __forceinline__ void next(const PromptParams& p, const Unit& u) {
-    if (++tile == u.tiles) tile = 0, ++hs;
-    place(p, u);
+    tok0 += p.half;
+    if (++tile == u.tiles) {
+      tile = 0;
+      ++hs;
+      g0 += p.step_heads;
+      tok0 = u.first;
+    }
+    n = min(p.half, u.len - tok0);
   }
   // some query of the step sees a key of tile kt
   __device__ __forceinline__ bool sees(const Unit& u, int kt) const {
@@ -301,35 +307,35 @@ __device__ void sum_warp(const PromptParams& p, WeightsShared& sh, uint32_t tmem
         const bool masked = !s.full(p) || u.key0 + kt * kTile + kTile - 1 > s.tok0;
         uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll 1
-        for (int c0 = 0; c0 < columns; c0 += 64) {
+        for (int c0 = 0; c0 < columns; c0 += 32) {
           const float4* l2 = reinterpret_cast<const float4*>(&sh.neg_lse2[r.i][c0]);
-          float x[64];
-          tm::load64(s_at + c0, x);
-          if (c0 + 64 >= columns) {
+          float x[32];
+          tm::load32(s_at + c0, x);
+          tm::wait32(x);
+          if (c0 + 32 >= columns) {
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&sh.s_empty[buf][kt]);
           }
           if (!masked) {
 #pragma unroll
-            for (int j = 0; j < 64; j += 4) {
+            for (int j = 0; j < 32; j += 4) {
               const float4 l = l2[j / 4];
               acc[0] = add_f32x2(acc[0], ex2_f32x2(fma_f32x2(pack_f32x2(x[j], x[j + 1]), sc2, pack_f32x2(l.x, l.y))));
               acc[1] = add_f32x2(acc[1], ex2_f32x2(fma_f32x2(pack_f32x2(x[j + 2], x[j + 3]), sc2, pack_f32x2(l.z, l.w))));
             }
           } else {
             // (a step's log-sum-exps of columns that do not count are -infinity, but their logits may be anything)
-            const uint32_t bits[2] = {seen_columns(p, s, c0, columns, before), seen_columns(p, s, c0 + 32, columns, before)};
+            const uint32_t m = seen_columns(p, s, c0, columns, before);
 #pragma unroll
-            for (int j = 0; j < 64; j += 4) {
+            for (int j = 0; j < 32; j += 4) {
               const float4 l = l2[j / 4];
-              const uint32_t m = bits[j / 32];
               float e[4];
               split_f32x2(ex2_f32x2(fma_f32x2(pack_f32x2(x[j], x[j + 1]), sc2, pack_f32x2(l.x, l.y))), e[0], e[1]);
               split_f32x2(ex2_f32x2(fma_f32x2(pack_f32x2(x[j + 2], x[j + 3]), sc2, pack_f32x2(l.z, l.w))), e[2], e[3]);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                if (!(m & (1u << ((j + k) & 31)))) e[k] = 0.f;
+                if (!(m & (1u << (j + k)))) e[k] = 0.f;
               acc[0] = add_f32x2(acc[0], pack_f32x2(e[0], e[1]));
               acc[1] = add_f32x2(acc[1], pack_f32x2(e[2], e[3]));
             }
@@ -400,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_weights_kernel(const __gri
   }
   pdl_wait();
   PromptCursor c;
-  const bool any = first_unit<kThreads>(p.work, sh.scan, c, Steps(p));
+  const bool any = first_unit<kThreads>(p.work, sh.scan, reinterpret_cast<int*>(smem_raw), c, Steps(p));
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
