@@ -362,13 +362,15 @@ def evict_launch_count() -> int:
 class _CudaArray:
     """Exposes a device pointer to torch.as_tensor via __cuda_array_interface__."""
 
-    def __init__(self, ptr, shape, typestr, strides=None):
+    def __init__(self, ptr, shape, typestr, strides=None, owner=None):
+        self.owner = owner          # what keeps the memory: as long as a tensor over it is held, so is this
         self.__cuda_array_interface__ = {"shape": tuple(shape), "typestr": typestr, "data": (ptr, False),
                                          "version": 3, "strides": strides}
 
 
-def view_tensors(view: EvictView, batch: int, heads: int, dtype: str):
-    """Zero-copy torch tensors over a view: k, v [B,H,n,D], pos, score [B,H,n]."""
+def view_tensors(view: EvictView, batch: int, heads: int, dtype: str, owner=None):
+    """Zero-copy torch tensors over a view: k, v [B,H,n,D], pos, score [B,H,n]. They hold ``owner``, if one is
+    given; without, whoever holds the handle keeps it for as long as they are read."""
     import torch
     cap, n = view.capacity, view.n_kept
     esz = 2 if dtype == "bf16" else 4
@@ -378,7 +380,7 @@ def view_tensors(view: EvictView, batch: int, heads: int, dtype: str):
     shp = (batch, heads, n, HEAD_DIM)
 
     def wrap(ptr, shape, ts, strides):
-        return torch.as_tensor(_CudaArray(ptr, shape, ts, strides), device="cuda")
+        return torch.as_tensor(_CudaArray(ptr, shape, ts, strides, owner), device="cuda")
 
     k = wrap(view.k, shp, tstr, kv_strides)
     v = wrap(view.v, shp, tstr, kv_strides)
@@ -389,15 +391,34 @@ def view_tensors(view: EvictView, batch: int, heads: int, dtype: str):
     return k, v, pos, score
 
 
+class _Handle:
+    """A library handle, destroyed with the last of the cache and the tensors over its rows."""
+
+    def __init__(self, value):
+        self.value = value
+
+    def close(self):
+        value, self.value = self.value, None
+        if value:
+            evict_destroy(value)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
 class _Ordered:
     """Orders work on the current stream behind a cache's last update, and its next one behind the work."""
 
     def __init__(self, handle):
         import torch
-        self.here, own = torch.cuda.current_stream(), evict_get_stream(handle)
-        if self.here.cuda_stream == own:
+        own = evict_get_stream(handle)
+        if torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) == own:
             own = None
         else:
+            self.here = torch.cuda.current_stream()
             own = torch.cuda.ExternalStream(own) if own else torch.cuda.default_stream()
             captures = torch.cuda.is_current_stream_capturing()
             with torch.cuda.stream(own):
@@ -443,18 +464,15 @@ class EvictCache:
             cfg.filters = f.data_ptr()
             cfg.n_filter_heads = f.shape[0]
         self.handle = evict_init(cfg)
+        self._held = _Handle(self.handle)
+        self._rows = None           # tensors over all rows that there is room for
         self._filters = None        # the library copied them
 
     def close(self):
+        """Frees the rows now, also under tensors that are still held (without it they go with the last of those)."""
         if self.handle:
-            evict_destroy(self.handle)
-            self.handle = None
-
-    def __del__(self):
-        try:
-            self.close()
-        except Exception:
-            pass
+            self.handle = self._rows = None
+            self._held.close()
 
     def update_and_fetch(self, k, v, pos=None, score=None):
         """Absorb one block. ``score`` (method "attention"): fp32 [B, H, m], what the new rows' accumulated
@@ -472,7 +490,7 @@ class EvictCache:
                     score.device != k.device:
                 raise ValueError("score must be contiguous fp32 [B, H, m] on k's device")
             view = evict_update_scored(self.handle, k.data_ptr(), v.data_ptr(), pos_ptr, score.data_ptr(), m)
-        return view_tensors(view, self.batch, self.heads, self.dtype)
+        return self._kept(view)
 
     def attend(self, q, n_new=None, scale=None, out=None, lse=None, weigh=False):
         """Attention of the queries q [batch, n_q_heads, m, 128] (bf16, rotated) over this cache's
@@ -511,7 +529,17 @@ class EvictCache:
     def view(self):
         """Tensors over the kept rows, without a copy: what the cache's stream has left there, until its
         next update. (A reader on another stream orders itself: evict_get_stream.)"""
-        return view_tensors(evict_get_view(self.handle), self.batch, self.heads, self.dtype)
+        return self._kept(evict_get_view(self.handle))
+
+    def _kept(self, view):
+        """view_tensors of a view, which lies where the handle's rows have lain from the start."""
+        if self._rows is None:
+            every = EvictView(view.k, view.v, view.pos, view.score, view.capacity, view.capacity)
+            import torch
+            with torch.inference_mode(False):       # tensors for any mode, whichever asks first
+                self._rows = view_tensors(every, self.batch, self.heads, self.dtype, self._held)
+        n, (k, v, pos, score) = view.n_kept, self._rows
+        return k.narrow(2, 0, n), v.narrow(2, 0, n), pos.narrow(2, 0, n), score.narrow(2, 0, n)
 
     def set_state(self, k, v, pos, score=None, offset=None):
         n = k.shape[2]

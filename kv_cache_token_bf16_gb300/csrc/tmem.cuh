@@ -41,32 +41,6 @@ __device__ __forceinline__ void warp_mma_rows(uint32_t d, uint64_t a, uint64_t b
       "l"(a), "l"(b), "r"(idesc)
       : "memory");
 }
-// D[tmem] = A[tmem] B^T, 128 elements deep: A has two elements a column, B as above.
-__device__ __forceinline__ void warp_mma_rows_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
-  asm volatile(
-      "{\n\t.reg .pred one, first, more;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
-      "elect.sync _|one, 0xffffffff;\n\t"
-      "setp.ne.u32 first, 0, 0;\n\t"
-      "setp.eq.u32 more, 0, 0;\n\t"
-      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, first;\n\t"
-      "add.u32 a, %1, 8;\n\tadd.s64 b, %2, 2;\n\t"
-      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
-      "add.u32 a, %1, 16;\n\tadd.s64 b, %2, 4;\n\t"
-      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
-      "add.u32 a, %1, 24;\n\tadd.s64 b, %2, 6;\n\t"
-      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
-      "add.u32 a, %1, 32;\n\tadd.s64 b, %2, 1024;\n\t"
-      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
-      "add.u32 a, %1, 40;\n\tadd.s64 b, %2, 1026;\n\t"
-      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
-      "add.u32 a, %1, 48;\n\tadd.s64 b, %2, 1028;\n\t"
-      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
-      "add.u32 a, %1, 56;\n\tadd.s64 b, %2, 1030;\n\t"
-      "@one tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, more;\n\t"
-      "}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc)
-      : "memory");
-}
 // D[tmem] (+)= A[tmem] B over 64 rows of B, MN-major with 16 rows in 2048 bytes; A has two elements a column.
 __device__ __forceinline__ void warp_mma_weights(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -137,12 +111,6 @@ __device__ __forceinline__ void load64(uint32_t taddr, float (&v)[64]) {
   for (int c = 0; c < 64; ++c) v[c] = __uint_as_float(r[c]);
 }
 
-__device__ __forceinline__ void store32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 // 32 bytes to global memory, 32-byte aligned: a whole sector from each thread
 __device__ __forceinline__ void store_sector(void* dst, const uint32_t* r) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]),

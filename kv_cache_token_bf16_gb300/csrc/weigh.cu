@@ -23,6 +23,7 @@ namespace evict {
 namespace {
 
 constexpr int kWarps = 8, kKeys = 32, kQueries = 8;
+constexpr int kScan = kWarps * 32;                // query rows that are looked through at once
 
 struct WeighParams {
   const void* k;                     // [batch][heads][cap][128]
@@ -47,52 +48,88 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// A tile's queries as a lane holds them: its pieces of one row, and the row's log-sum-exp (base 2, negative;
+// -inf: the query does not count).
+struct Queries {
+  uint4 x[4];
+  float neg;
+};
+
 __global__ void __launch_bounds__(kWarps * 32, 2) weigh_kernel(const __grid_constant__ WeighParams p) {
   __shared__ float sums[kWarps][kKeys];
+  __shared__ long long at[kScan];                 // of the queries that count: where their rows lie in q,
+  __shared__ int lse_at[kScan];                   // and their log-sum-exps
+  __shared__ int counts[kWarps];
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % p.split;
   const int unit = blockIdx.y, b = p.by_heads.div(unit), h = unit - b * p.heads;
   const int row0 = (blockIdx.x * (kWarps / p.split) + warp / p.split) * kKeys;
   const int n = lane >> 2, t = lane & 3;          // row of a fragment, and which pieces of it
   const __nv_bfloat16* keys = static_cast<const __nv_bfloat16*>(p.k) + (long long)unit * p.cap * kHeadDim;
+  uint4 a[4][4];                                  // key n + 8 i, elements 32 j + 8 t ..
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + n + 8 * i;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      a[i][j] = row < p.rows ? reinterpret_cast<const uint4*>(keys + (long long)row * kHeadDim)[4 * j + t]
+                             : make_uint4(0, 0, 0, 0);
+  }
   float sum[4] = {0.f, 0.f, 0.f, 0.f};            // of keys row0 + n + 8 i
-  if (row0 < p.rows) {
-    uint4 a[4][4];                                // key n + 8 i, elements 32 j + 8 t ..
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = row0 + n + 8 * i;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        a[i][j] = row < p.rows ? reinterpret_cast<const uint4*>(keys + (long long)row * kHeadDim)[4 * j + t]
-                               : make_uint4(0, 0, 0, 0);
-    }
 #pragma unroll 1
-    for (int r0 = part * kQueries; r0 < p.queries; r0 += p.split * kQueries) {
-      // this lane's query row: sequence, token, head of the group
-      const int r = r0 + n, f = p.by_per.div(r), in = r - f * p.m * p.group, tok = p.by_group.div(in);
-      const int seq = b * p.fan + f, hq = h * p.group + in - tok * p.group;
-      float nl = -INFINITY;                       // a query that does not count
-      uint4 x[4];
+  for (int c0 = 0; c0 < p.queries; c0 += kScan) {
+    // a thread's query row: sequence, token, head of the group
+    const int c = c0 + threadIdx.x, f = p.by_per.div(c), in = c - f * p.m * p.group, tok = p.by_group.div(in);
+    const int seq = b * p.fan + f, hq = h * p.group + in - tok * p.group;
+    const bool counts_here = c < p.queries && (!p.n_new || tok < p.n_new[seq]);
+    const uint32_t mine = __ballot_sync(0xffffffffu, counts_here);
+    if (c0) __syncthreads();                      // the last ones are worked off
+    if (lane == 0) counts[warp] = __popc(mine);
+    __syncthreads();
+    int before = 0, total = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[j] = make_uint4(0, 0, 0, 0);
-      if (r < p.queries && (!p.n_new || tok < p.n_new[seq])) {
-        const float l = p.lse[((long long)seq * p.hq + hq) * p.m + tok];
-        nl = l == -INFINITY ? l : -l * kLog2e;
-        const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(p.q) + seq * p.qb + hq * p.qh + tok * p.qm;
+    for (int i = 0; i < kWarps; ++i) {
+      if (i == warp) before = total;
+      total += counts[i];
+    }
+    if (counts_here) {
+      const int i = before + __popc(mine & ((1u << lane) - 1));
+      at[i] = seq * p.qb + hq * p.qh + tok * p.qm;
+      lse_at[i] = (seq * p.hq + hq) * p.m + tok;
+    }
+    __syncthreads();
+    if (row0 >= p.rows) continue;
+    auto load = [&](int r0) {
+      Queries q;
+      const int r = r0 + n;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = reinterpret_cast<const uint4*>(row)[4 * j + t];
+      for (int j = 0; j < 4; ++j) q.x[j] = make_uint4(0, 0, 0, 0);
+      q.neg = -INFINITY;
+      if (r < total) {
+        const float l = p.lse[lse_at[r]];
+        const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at[r]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q.x[j] = row[4 * j + t];
+        q.neg = l == -INFINITY ? l : -l * kLog2e;
       }
+      return q;
+    };
+    Queries next = load(part * kQueries);
+#pragma unroll 1
+    for (int r0 = part * kQueries; r0 < total; r0 += p.split * kQueries) {
+      const Queries q = next;
+      next = load(r0 + p.split * kQueries);
       float d[2][4] = {};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint4 &u = a[2 * i][j], &v = a[2 * i + 1][j];
-          mma(d[i], u.x, v.x, u.y, v.y, x[j].x, x[j].y);
-          mma(d[i], u.z, v.z, u.w, v.w, x[j].z, x[j].w);
+          mma(d[i], u.x, v.x, u.y, v.y, q.x[j].x, q.x[j].y);
+          mma(d[i], u.z, v.z, u.w, v.w, q.x[j].z, q.x[j].w);
         }
       // columns 2 t and 2 t + 1 are the queries of lanes 8 t and 8 t + 4
-      const float n0 = __shfl_sync(0xffffffffu, nl, 8 * t), n1 = __shfl_sync(0xffffffffu, nl, 8 * t + 4);
+      const float n0 = __shfl_sync(0xffffffffu, q.neg, 8 * t), n1 = __shfl_sync(0xffffffffu, q.neg, 8 * t + 4);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -102,11 +139,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) weigh_kernel(const __grid_cons
           sum[2 * i + k] += w0 + w1;
         }
     }
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
-      sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-    }
+  for (int i = 0; i < 4; ++i) {
+    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
   }
   if (t == 0) {
 #pragma unroll

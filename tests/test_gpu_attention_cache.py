@@ -313,3 +313,49 @@ def test_a_captured_decode_step():
     torch.cuda.synchronize()
     cache.sync()
     eager.sync()
+
+
+def test_tensors_over_the_rows_outlive_the_cache():
+    def views():
+        cache = binding.EvictCache("attention", 1, 2, budget=40, n_sink=0, max_block=50)
+        cache.weigh(rows(71, 1, 4, 1), torch.zeros(1, 4, 1, device="cuda"))         # of no rows
+        fetched = cache.update_and_fetch(*block(72, 1, 2, 30))
+        cache.weigh(rows(74, 1, 4, 1), torch.full((1, 4, 1), 3.0, device="cuda"))
+        cache.sync()
+        assert cache.view()[3].shape == (1, 2, 30) and cache.view()[3].data_ptr() == fetched[3].data_ptr()
+        return fetched, cache.view()
+
+    fetched, view = views()                         # the cache itself is gone
+    other = [torch.full((1 << 20,), 7.0, device="cuda") for _ in range(8)]
+    k, v = block(72, 1, 2, 30)
+    for x in (fetched, view):
+        assert torch.equal(x[0], k) and torch.equal(x[1], v) and torch.equal(x[3], view[3])
+        assert torch.equal(x[2], torch.arange(30, device="cuda").int().expand(1, 2, 30)) and (x[3] > 0).all()
+    del other
+
+
+def test_views_of_any_mode():
+    cache = binding.EvictCache("attention", 1, 1, budget=8, n_sink=0, max_block=8)
+    with torch.inference_mode():
+        cache.update_and_fetch(*block(75, 1, 1, 8))
+        cache.view()
+    cache.view()[3].add_(1.0)                       # the user's own start
+    cache.sync()
+    assert (cache.view()[3] == 1).all()
+    cache.close()
+
+
+@pytest.mark.parametrize("fan,m,n,hq,hkv", [(40, 3, 70, 8, 2), (3, 100, 33, 16, 2), (513, 1, 300, 4, 4), (1, 257, 40, 1, 1)])
+def test_weights_of_more_queries_than_are_looked_through_at_once(fan, m, n, hq, hkv):
+    test_weights_of_a_step(1, fan, m, n, hq, hkv, True, "token", None)
+    k, v = block(76, 2, hkv, n)
+    cache = binding.EvictCache("attention", 2, hkv, budget=n, n_sink=0, max_block=n)
+    cache.update_and_fetch(k, v)
+    q, lse = rows(78, 2 * fan, hq, m), torch.full((2 * fan, hq, m), 5.0, device="cuda")
+    n_new = torch.zeros(2 * fan, dtype=torch.int32)
+    n_new[-1] = m                                   # all sequences of the first row, and most of the second, have none
+    cache.weigh(q, lse, n_new=n_new.cuda())
+    cache.sync()
+    assert (cache.view()[3][0] == 0).all()
+    check_weights(cache.view()[3], *weigh64(torch.zeros(2, hkv, n, device="cuda"), k, q, lse, n_new.tolist(), SCALE))
+    cache.close()
