@@ -415,7 +415,7 @@ class _Ordered:
     def __init__(self, handle):
         import torch
         own = evict_get_stream(handle)
-        if torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) == own:
+        if torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) == own:
             own = None
         else:
             self.here = torch.cuda.current_stream()
@@ -465,29 +465,31 @@ class EvictCache:
             cfg.n_filter_heads = f.shape[0]
         self.handle = evict_init(cfg)
         self._held = _Handle(self.handle)
-        self._rows = None           # tensors over all rows that there is room for
+        self._rows = None           # tensors over all rows that there is room for,
+        self._views = (-1, None)    # and over as many as were asked for last
         self._filters = None        # the library copied them
 
     def close(self):
         """Frees the rows now, also under tensors that are still held (without it they go with the last of those)."""
         if self.handle:
             self.handle = self._rows = None
+            self._views = (-1, None)
             self._held.close()
 
     def update_and_fetch(self, k, v, pos=None, score=None):
         """Absorb one block. ``score`` (method "attention"): fp32 [B, H, m], what the new rows' accumulated
         weights start from, e.g. ``prompt.weights`` of them (None: 0)."""
-        m = k.shape[2]
-        for t in (k, v):
-            if not t.is_cuda or not t.is_contiguous():
-                raise ValueError("k and v must be contiguous CUDA tensors [B, H, m, 128]")
+        shape = k.shape
+        m = shape[2]
+        if not (k.is_cuda and v.is_cuda and k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("k and v must be contiguous CUDA tensors [B, H, m, 128]")
         pos_ptr = pos.data_ptr() if pos is not None else None
         if score is None:
             view = evict_update_and_fetch(self.handle, k.data_ptr(), v.data_ptr(), pos_ptr, m)
         else:
             import torch
-            if score.dtype is not torch.float32 or score.shape != k.shape[:3] or not score.is_contiguous() or \
-                    score.device != k.device:
+            if score.dtype is not torch.float32 or score.shape != shape[:3] or not score.is_contiguous() or \
+                    score.get_device() != k.get_device():
                 raise ValueError("score must be contiguous fp32 [B, H, m] on k's device")
             view = evict_update_scored(self.handle, k.data_ptr(), v.data_ptr(), pos_ptr, score.data_ptr(), m)
         return self._kept(view)
@@ -533,13 +535,17 @@ class EvictCache:
 
     def _kept(self, view):
         """view_tensors of a view, which lies where the handle's rows have lain from the start."""
+        if view.n_kept == self._views[0]:           # a cache that is full keeps as many after every step
+            return self._views[1]
+        import torch
         if self._rows is None:
             every = EvictView(view.k, view.v, view.pos, view.score, view.capacity, view.capacity)
-            import torch
             with torch.inference_mode(False):       # tensors for any mode, whichever asks first
                 self._rows = view_tensors(every, self.batch, self.heads, self.dtype, self._held)
-        n, (k, v, pos, score) = view.n_kept, self._rows
-        return k.narrow(2, 0, n), v.narrow(2, 0, n), pos.narrow(2, 0, n), score.narrow(2, 0, n)
+        n = view.n_kept
+        with torch.inference_mode(False):
+            self._views = n, tuple(x.narrow(2, 0, n) for x in self._rows)
+        return self._views[1]
 
     def set_state(self, k, v, pos, score=None, offset=None):
         n = k.shape[2]

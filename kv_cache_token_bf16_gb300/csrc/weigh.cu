@@ -2,15 +2,21 @@
 //   score_j += sum over the sequences of a kept prefix, their tokens and the group's query heads of
 //              exp(scale q.k_j - lse).
 //
-// A warp takes 32 keys, straight from memory to the registers of m16n8k16 products (their rows; a lane's
-// 16-byte pieces of a row stand for the product's columns in another order, the same for the queries), and
-// goes through the queries eight at a time, which come from L1 and L2. A key's sum lies in four lanes.
-// Keys are read once: what bounds few queries is HBM or L2, many queries the products. Where there are
-// fewer warps of keys than the GPU has room for, the queries are dealt out to up to eight warps for the same keys.
+// Few queries (weigh_kernel): a warp takes 32 keys, straight from memory to the registers of m16n8k16 products (their
+// rows; a lane's 16-byte pieces of a row stand for the product's columns in another order, the same for the queries),
+// and goes through the queries eight at a time, which come from L1 and L2. A key's sum lies in four lanes. Keys are
+// read once: what bounds it is HBM, 4.2 of 6.8 TB/s for one token of 32 caches of 512 rows (32 / 8 heads; 7.9 us).
+// Where there are fewer warps of keys than the GPU has room for, the queries are dealt out to up to eight warps for
+// the same keys. 320 queries over 16384 rows were bound by these products (65 us).
+// Many (weigh_wide_kernel): the large products of the tensor cores, bound by HBM up to about a hundred queries and by
+// the exponentials behind that: 8 heads' 16384 rows by 64 queries 10.9 us, by 320 23.4, by 1024 54.5 (a third, a half
+// and two thirds of what their bytes and exponentials, at 32 a clock and SM, would allow; the rest is the launch and
+// the laying out of the queries, once a chunk).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "api_internal.h"
@@ -18,6 +24,9 @@
 #include "common.cuh"
 #include "launch.h"
 #include "pipeline.cuh"
+#include "prompt.cuh"
+#include "prompt.h"
+#include "tmem.cuh"
 
 namespace evict {
 namespace {
@@ -33,7 +42,7 @@ struct WeighParams {
   long long qb, qh, qm;              // element strides
   const float* lse;                  // [sequences][hq][m]
   const int32_t* n_new;
-  int fan, m, hq, group;             // sequences of a cache's batch row
+  int fan, m, hq, group, seqs;       // fan: sequences of a cache's batch row
   int queries;                       // fan * m * group
   int split;                         // warps that share the queries of the same keys
   Divisor by_heads, by_per, by_group;   // per = m * group: query rows of a sequence
@@ -164,6 +173,260 @@ __global__ void __launch_bounds__(kWarps * 32, 2) weigh_kernel(const __grid_cons
     }
 }
 
+// Many queries: the tensor cores' large products, in 128 keys by 128 queries, D[key, query] in tensor memory. A CTA
+// takes an equal share of the key tiles. Of a unit's queries it lays up to kChunk that count into shared memory
+// once, behind each other, and goes through its tiles of the unit by them; a warp sums 32 keys over 32 queries of
+// each product.
+constexpr int kTile = 128, kTileBytes = kTile * kHeadDim * 2;
+constexpr int kChunk = 256, kKeyRing = 4, kBuffers = 4;
+constexpr int kSumWarps = 16, kIssueWarp = 16, kCopyWarp = 17, kWideThreads = 576;
+
+struct WideShared {
+  uint64_t k_full[kKeyRing], k_empty[kKeyRing], s_full[kBuffers], s_empty[kBuffers], done;
+  uint64_t sums_full[4][2], sums_empty[4][2];     // of a quarter of the keys, of a tile
+  uint32_t tmem_base;
+  int fail, next;                                 // next: first query row behind the chunk's
+  int counts[kSumWarps];
+  long long at[kChunk];                           // where the chunk's query rows lie in q,
+  alignas(16) float neg[kChunk];                  // and their log-sum-exps, base 2, negative
+  float sums[2][3][kTile];
+};
+constexpr int kWideSmem = (kKeyRing + kChunk / kTile) * kTileBytes + (int)sizeof(WideShared);
+static_assert(kWideSmem <= 227 * 1024);
+
+struct WideParams {
+  WeighParams w;
+  CUtensorMap k_map;
+  int tiles;                                      // of a unit
+  long long all;                                  // of all
+  Divisor by_tiles;
+};
+
+// The next query rows from c0 on that count, at most kChunk, to shared memory; their number. By all threads.
+__device__ int lay_queries(const WeighParams& p, WideShared& sh, unsigned char* rows, int b, int h, int c0) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = c0 + tid;
+  bool counts_here = false;
+  long long at = 0;
+  float l = 0.f;
+  if (warp < kSumWarps && c < p.queries) {
+    const int f = p.by_per.div(c), in = c - f * p.m * p.group, tok = p.by_group.div(in);
+    const int seq = b * p.fan + f, hq = h * p.group + in - tok * p.group;
+    if (!p.n_new || tok < p.n_new[seq]) {
+      l = p.lse[((long long)seq * p.hq + hq) * p.m + tok];
+      counts_here = fabsf(l) != INFINITY;         // no weights of a query that saw nothing, or with all elsewhere
+      at = seq * p.qb + hq * p.qh + tok * p.qm;
+    }
+  }
+  const uint32_t mine = __ballot_sync(0xffffffffu, counts_here);
+  if (lane == 0 && warp < kSumWarps) sh.counts[warp] = __popc(mine);
+  if (tid == 0) sh.next = c0 + kSumWarps * 32;
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < kSumWarps; ++i) {
+    if (i == warp) before = total;
+    total += sh.counts[i];
+  }
+  if (counts_here) {
+    const int i = before + __popc(mine & ((1u << lane) - 1));
+    if (i < kChunk) {
+      sh.at[i] = at;
+      sh.neg[i] = -l * kLog2e;
+      if (i == kChunk - 1) sh.next = c + 1;
+    }
+  }
+  // (none once a wait has given up: no thread is between these barriers and a wait)
+  total = *(volatile int*)&sh.fail ? 0 : min(total, kChunk);
+  __syncthreads();
+  // 128-byte halves of the rows, their 16-byte pieces in the order of a 128-byte swizzle
+#pragma unroll 4
+  for (int i = tid; i < total * 16; i += kWideThreads) {
+    const int r = i >> 4, piece = i & 15;
+    const uint4 x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + sh.at[r])[piece];
+    *reinterpret_cast<uint4*>(rows + (r / kTile) * kTileBytes + (piece >> 3) * (kTileBytes / 2) + (r % kTile) * 128 +
+                              (((piece & 7) ^ (r & 7)) << 4)) = x;
+  }
+  tc::fence_proxy_async_smem();
+  __syncthreads();
+  return total;
+}
+
+// Tiles first .. last - 1 of the unit's keys into the ring, by one thread. `used` counts the ring's tiles.
+__device__ __forceinline__ bool copy_tiles(const WideParams& p, WideShared& sh, uint32_t ring, int b, int h, int first, int last,
+                                           int& used) {
+#pragma unroll 1
+  for (int t = first; t < last; ++t, ++used) {
+    const int i = used % kKeyRing;
+    if (!wait_for(&sh.k_empty[i], ((used / kKeyRing) & 1) ^ 1, &sh.fail)) return false;
+    tc::mbar_arrive_expect_tx(&sh.k_full[i], kTileBytes);
+    for (int j = 0; j < 2; ++j)
+      tma_load_4d(ring + i * kTileBytes + j * (kTileBytes / 2), &p.k_map, j * 64, t * kTile, h, b, &sh.k_full[i]);
+  }
+  return true;
+}
+
+__global__ void __launch_bounds__(kWideThreads, 1) weigh_wide_kernel(const __grid_constant__ WideParams p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  const uint32_t smem = tc::smem_u32(smem_raw), queries = smem + kKeyRing * kTileBytes;
+  WideShared& sh = *reinterpret_cast<WideShared*>(smem_raw + (kKeyRing + kChunk / kTile) * kTileBytes);
+  const WeighParams& w = p.w;
+  if (smem & 1023) {                              // not as declared: no tile could be right
+    if (threadIdx.x == 0) raise_device_error(w.err, kDevBadIndex);
+    return;
+  }
+  const int tid = threadIdx.x, warp = uni(tid >> 5), lane = tid & 31;
+  if (warp == 0) tc::tmem_alloc(&sh.tmem_base, kBuffers * kTile);
+  if (tid == 32) {
+    for (int i = 0; i < kKeyRing; ++i) {
+      tc::mbar_init(&sh.k_full[i], 1);
+      tc::mbar_init(&sh.k_empty[i], 1);
+    }
+    for (int i = 0; i < kBuffers; ++i) {
+      tc::mbar_init(&sh.s_full[i], 1);
+      tc::mbar_init(&sh.s_empty[i], kSumWarps);
+    }
+    for (int i = 0; i < 8; ++i) {
+      tc::mbar_init(&sh.sums_full[i >> 1][i & 1], 3);
+      tc::mbar_init(&sh.sums_empty[i >> 1][i & 1], 1);
+    }
+    tc::mbar_init(&sh.done, 1);
+    sh.fail = 0;
+  }
+  if (warp == kCopyWarp && lane == 0) tc::tma_prefetch_desc(&p.k_map);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = uni(sh.tmem_base);
+  pdl_wait();
+  const uint64_t kd = tc::sw128_desc(smem), qd = tc::sw128_desc(queries);
+  const uint32_t hi = (uint32_t)(kd >> 32), k_lo = (uint32_t)kd, q_lo = (uint32_t)qd;
+  const int quarter = warp & 3, group = warp >> 2;
+  const int end = (int)(p.all * (blockIdx.x + 1) / gridDim.x);
+  int tiles = 0, steps = 0;                       // done by this warp's role: places in the rings
+  bool ok = true;
+#pragma unroll 1
+  for (int t0 = (int)(p.all * blockIdx.x / gridDim.x); t0 < end;) {
+    const int unit = uni(p.by_tiles.div(t0)), b = uni(w.by_heads.div(unit)), h = unit - b * w.heads;
+    const int first = t0 - unit * p.tiles, last = min(p.tiles, end - unit * p.tiles);
+    t0 = unit * p.tiles + last;
+#pragma unroll 1
+    for (int c0 = 0; c0 < w.queries;) {
+      // keys on their way meanwhile
+      const int ahead = min(first + kKeyRing, last);
+      if (warp == kCopyWarp && lane == 0 && ok) ok = copy_tiles(p, sh, smem, b, h, first, ahead, tiles);
+      __syncwarp();
+      const int total = uni(lay_queries(w, sh, smem_raw + kKeyRing * kTileBytes, b, h, c0));
+      c0 = uni(sh.next);
+      const int blocks = (total + kTile - 1) / kTile;
+      if (total == 0) {                           // no use for them
+        if (warp == kIssueWarp)
+          for (int t = first; ok && t < ahead; ++t, ++tiles) {
+            if (!(ok = warp_wait(&sh.k_full[tiles % kKeyRing], (tiles / kKeyRing) & 1, &sh.fail))) break;
+            if (lane == 0) tc::mbar_arrive(&sh.k_empty[tiles % kKeyRing]);
+          }
+      } else if (warp == kCopyWarp) {
+        if (lane == 0 && ok) ok = copy_tiles(p, sh, smem, b, h, ahead, last, tiles);
+        __syncwarp();
+      } else if (warp == kIssueWarp) {
+#pragma unroll 1
+        for (int t = first; ok && t < last; ++t, ++tiles) {
+          const int i = uni(tiles % kKeyRing);
+          if (!(ok = warp_wait(&sh.k_full[i], (tiles / kKeyRing) & 1, &sh.fail))) break;
+#pragma unroll 1
+          for (int j = 0; j < blocks; ++j, ++steps) {
+            const int buf = uni(steps % kBuffers);
+            if (!(ok = warp_wait(&sh.s_empty[buf], ((steps / kBuffers) & 1) ^ 1, &sh.fail))) break;
+            tc::fence_after_sync();
+            tm::warp_mma_rows(tmem + buf * kTile, tm::desc_of(k_lo + ((i * kTileBytes) >> 4), hi),
+                              tm::desc_of(q_lo + ((j * kTileBytes) >> 4), hi),
+                              tc::idesc_bf16_f32(kTile, (min(kTile, total - j * kTile) + 15) & ~15));
+            tm::warp_mma_commit(&sh.s_full[buf]);
+          }
+          if (!ok) break;
+          tm::warp_mma_commit(&sh.k_empty[i]);
+        }
+      } else {
+        const int key = quarter * 32 + lane;
+        const uint64_t sc2 = pack_f32x2(w.scale2, w.scale2);
+#pragma unroll 1
+        for (int t = first; t < last; ++t, ++tiles) {
+          const int row = t * kTile + key;
+          float* to = w.score + (long long)unit * w.cap + row;
+          float was = 0.f, sum = 0.f;
+          if (group == 0 && row < w.rows) was = *to;
+#pragma unroll 1
+          for (int j = 0; j < blocks; ++j, ++steps) {
+            const int buf = steps % kBuffers, columns = total - j * kTile - group * 32;
+            // (a wait that gives up leaves `fail`)
+            wait_for(&sh.s_full[buf], (steps / kBuffers) & 1, &sh.fail);
+            __syncwarp();
+            tc::fence_after_sync();
+            float x[32];
+            if (columns > 0) {
+              tm::load32(tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTile + group * 32, x);
+              tm::wait32(x);
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.s_empty[buf]);
+            const float4* neg = reinterpret_cast<const float4*>(&sh.neg[j * kTile + group * 32]);
+            uint64_t acc[2] = {0ull, 0ull};
+            if (columns >= 32) {
+#pragma unroll
+              for (int q = 0; q < 32; q += 4) {
+                const float4 n = neg[q / 4];
+                acc[0] = add_f32x2(acc[0], ex2_f32x2(fma_f32x2(pack_f32x2(x[q], x[q + 1]), sc2, pack_f32x2(n.x, n.y))));
+                acc[1] = add_f32x2(acc[1], ex2_f32x2(fma_f32x2(pack_f32x2(x[q + 2], x[q + 3]), sc2, pack_f32x2(n.z, n.w))));
+              }
+            } else if (columns > 0) {             // (what lies behind them may be anything)
+#pragma unroll
+              for (int q = 0; q < 32; q += 2) {
+                const float e = ex2(fmaf(x[q], w.scale2, sh.neg[j * kTile + group * 32 + q]));
+                const float f = ex2(fmaf(x[q + 1], w.scale2, sh.neg[j * kTile + group * 32 + q + 1]));
+                acc[0] = add_f32x2(acc[0], pack_f32x2(q < columns ? e : 0.f, q + 1 < columns ? f : 0.f));
+              }
+            }
+            float lo, up;
+            split_f32x2(add_f32x2(acc[0], acc[1]), lo, up);
+            sum += lo + up;
+          }
+          // a key's four sums meet in the first warp of its quarter
+          const int slot = tiles & 1, parity = (tiles >> 1) & 1;
+          if (group) {
+            wait_for(&sh.sums_empty[quarter][slot], parity ^ 1, &sh.fail);
+            sh.sums[slot][group - 1][key] = sum;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.sums_full[quarter][slot]);
+          } else {
+            wait_for(&sh.sums_full[quarter][slot], parity, &sh.fail);
+            for (int g = 0; g < 3; ++g) sum += sh.sums[slot][g][key];
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&sh.sums_empty[quarter][slot]);
+            if (row < w.rows && !*(volatile int*)&sh.fail) *to = was + sum;
+          }
+        }
+      }
+      __syncthreads();                            // the queries' rows are read
+    }
+  }
+  // every product and copy issued must end before tensor and shared memory are released
+  if (warp == kIssueWarp) {
+    tm::warp_mma_commit(&sh.done);
+    drain_phase(&sh.done, 0, w.err);
+  } else if (warp == kCopyWarp && lane == 0) {
+#pragma unroll 1
+    for (int i = 0; i < kKeyRing && i < tiles; ++i) drain_phase(&sh.k_full[i], ((tiles - 1 - i) / kKeyRing) & 1, w.err);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 0) tc::tmem_dealloc(tmem, kBuffers * kTile);
+  if (tid == 0 && sh.fail) raise_device_error(w.err, kDevWaitTimeout);
+  if (w.n_new && w.err && blockIdx.x == 0)
+    for (int f = tid; f < w.seqs; f += kWideThreads)
+      if (w.n_new[f] < 0 || w.n_new[f] > w.m) raise_device_error(w.err, kDevBadIndex);
+}
+
 // The rows of a block behind the kept ones, with their positions and given scores: a warp per row.
 constexpr int kAppendWarps = 8;
 __global__ void __launch_bounds__(kAppendWarps * 32) append_given_kernel(const __grid_constant__ GroupParams P) {
@@ -182,6 +445,16 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_given_kernel(const _
     L.score_st[to] = L.new_score[(size_t)bh * s.new_stride + t];
     L.pos_st[to] = L.pos_in ? L.pos_in[(size_t)(bh / s.heads) * s.m + t] : (int32_t)(s.offset + t);
   }
+}
+
+// The wide kernel's dynamic shared memory, allowed once for each device.
+cudaError_t allow_smem(int dev) {
+  static std::atomic<uint64_t> done{0};
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(weigh_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
+  if (e == cudaSuccess) done.fetch_or(bit);
+  return e;
 }
 
 bool multiple(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -224,6 +497,7 @@ extern "C" int evict_weigh(evict_handle* h, const evict_rows* q, int batch, int 
   p.lse = lse;
   p.n_new = n_new;
   p.fan = batch / h->cfg.batch;
+  p.seqs = batch;
   p.m = m;
   p.hq = q->heads;
   p.group = q->heads / p.heads;
@@ -237,13 +511,35 @@ extern "C" int evict_weigh(evict_handle* h, const evict_rows* q, int batch, int 
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e, "looking up the device");
-  // warps for the same keys: as many as there is room for, while each has a tile of queries
   const int units = h->cfg.batch * p.heads;
+  if (const unsigned long long id = capture_of(static_cast<cudaStream_t>(stream))) h->captured = id;
+  // Key tiles for every SM and enough products for the wide kernel's start to pay (8 heads; us, narrow and wide):
+  // 1024 tiles by 16 queries 9.0 and 10.0, by 32 11.5 and 10.1; 512 by 32 7.4 and 8.3, by 64 9.9 and 9.1; 2048 by 16
+  // 20.3 and 19.8; but 16 tiles by 3584 queries 31 and 64, which the narrow kernel deals out.
+  const int key_tiles = (p.rows + kTile - 1) / kTile;
+  const long long tiles = (long long)units * key_tiles;
+  if (tiles >= sms && p.queries >= 16 && tiles * p.queries >= 32768) {
+    WideParams wide = {};
+    wide.w = p;
+    wide.tiles = key_tiles;
+    wide.all = tiles;
+    wide.by_tiles = Divisor(wide.tiles);
+    const evict_rows keys = {h->kst, (int64_t)p.heads * p.cap * kHeadDim, (int64_t)p.cap * kHeadDim, kHeadDim, p.heads};
+    if (!encode_tiled()) return fail(EVICT_ECUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const int rc = encode_heads(&wide.k_map, keys, h->cfg.batch, p.rows, 1, kTile, false, "the kept rows");
+    if (rc) return rc;
+    if ((e = allow_smem(dev)) != cudaSuccess) return cuda_fail(e, "the weigh kernel's shared memory");
+    e = launch_pdl(weigh_wide_kernel, dim3(sms), dim3(kWideThreads), kWideSmem,
+                   static_cast<cudaStream_t>(stream), nullptr, wide);
+    if (e != cudaSuccess) return cuda_fail(e, "weigh kernel launch");
+    g_launches.fetch_add(1);
+    return EVICT_OK;
+  }
+  // warps for the same keys: as many as there is room for, while each has a tile of queries
   const long long key_warps = (long long)units * ((p.rows + kKeys - 1) / kKeys);
   p.split = 1;
   while (p.split < kWarps && key_warps * p.split < 2ll * kWarps * sms && p.split * kQueries < p.queries) p.split *= 2;
   const int keys_cta = kKeys * (kWarps / p.split);
-  if (const unsigned long long id = capture_of(static_cast<cudaStream_t>(stream))) h->captured = id;
   e = launch_pdl(weigh_kernel, dim3((p.rows + keys_cta - 1) / keys_cta, units), dim3(kWarps * 32), 0,
                  static_cast<cudaStream_t>(stream), nullptr, p);
   if (e != cudaSuccess) return cuda_fail(e, "weigh kernel launch");

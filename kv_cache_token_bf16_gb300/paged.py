@@ -143,7 +143,7 @@ class _on:
 
 def _call(index, fn, *args):
     """fn(*args) with the device current; raises the library's error."""
-    if _torch.cuda.current_device() == index:
+    if _torch._C._cuda_getDevice() == index:
         code = fn(*args)
     else:
         with _on(index):

@@ -74,23 +74,21 @@ class Packing:
             binding.evict_pages_status(self.error_at, paged._stream(self.index))
 
 
-# Workspace bytes of a call's sizes, on a device (the sizes alone decide).
+# Workspace bytes of a call (0: attention, 1: weights) and its sizes on a device (which alone decide).
 _workspace = {}
 
 
-def _run(name, key, fields, device):
-    """Ask for the workspace of these sizes (once), and make the call."""
-    index = key[0]
-    size = _workspace.get((name, key))
+def _work(name, key, fields, device):
+    """The workspace of a call of these sizes: (tensor, bytes)."""
+    size = _workspace.get(key)
     if size is None:
         if len(_workspace) >= 4096:
             _workspace.clear()
-        with paged._on(index):
+        with paged._on(key[1]):
             size = getattr(binding, name + "_workspace")(EvictPrompt.from_buffer_copy(_PROMPT.pack(*fields, 0, 0, 0, 0)))
-        _workspace[name, key] = size
+        _workspace[key] = size
     # from torch's allocator: reused in stream order, private to a graph that is being captured
-    work = paged._torch.empty(size, dtype=paged._torch.uint8, device=device)
-    return work, size
+    return paged._torch.empty(size, dtype=paged._torch.uint8, device=device), size
 
 
 def _sizes(q, k, packing, scale):
@@ -135,7 +133,7 @@ def attention(q, k, v, packing: Packing | None = None, scale=None, out=None, lse
     lse_at = paged._like(lse, "lse", (batch, hq, m), torch.float32, index)
     starts, n, error = (packing.at, packing.n, packing.error_at) if packing is not None else (0, 0, 0)
     fields = (batch, m, *qr, *kr, *vr, *outr, lse_at, 0, starts, n, 0, scale)
-    work, size = _run("evict_prompt_attention", (index, batch, hq, hkv, m, n, packing is None), fields, q.device)
+    work, size = _work("evict_prompt_attention", (0, index, batch, hq, hkv, m, n, packing is None), fields, q.device)
     paged._call(index, _calls.evict_prompt_attention,
                 _PROMPT.pack(*fields, work.data_ptr(), size, error, paged._stream(index)))
     return out
@@ -166,7 +164,7 @@ def weights(q, k, lse, packing: Packing | None = None, last: int = 0, scale=None
     out_at = paged._like(out, "out", (batch, hkv, m), torch.float32, index)
     starts, n, error = (packing.at, packing.n, packing.error_at) if packing is not None else (0, 0, 0)
     fields = (batch, m, *qr, *kr, *_NO_ROWS, *_NO_ROWS, lse_at, out_at, starts, n, min(last, m), scale)
-    work, size = _run("evict_prompt_weights", (index, batch, hq, hkv, m, n, packing is None), fields, q.device)
+    work, size = _work("evict_prompt_weights", (1, index, batch, hq, hkv, m, n, packing is None), fields, q.device)
     paged._call(index, _calls.evict_prompt_weights,
                 _PROMPT.pack(*fields, work.data_ptr(), size, error, paged._stream(index)))
     return out

@@ -359,3 +359,83 @@ def test_weights_of_more_queries_than_are_looked_through_at_once(fan, m, n, hq, 
     assert (cache.view()[3][0] == 0).all()
     check_weights(cache.view()[3], *weigh64(torch.zeros(2, hkv, n, device="cuda"), k, q, lse, n_new.tolist(), SCALE))
     cache.close()
+
+
+# sizes that take the large products (every SM has a tile of 128 keys, 32768 tile-by-query pairs): a tile of one key, chunks
+# of 256 queries that are full, a chunk of which nothing counts before one that does, units that begin inside a share
+@pytest.mark.parametrize("B,fan,m,n,hq,hkv,ragged,layout", [
+    (1, 16, 5, 2433, 32, 8, True, "token"), (3, 4, 32, 6528, 6, 2, False, "wide"), (24, 1, 9, 900, 40, 8, True, "head"),
+    (1, 300, 1, 19457, 8, 1, True, "token")])
+def test_weights_of_many_queries_on_many_rows(B, fan, m, n, hq, hkv, ragged, layout):
+    assert -(-n // 128) * B * hkv >= 152 and -(-n // 128) * B * fan * m * hq >= 32768
+    test_weights_of_a_step(B, fan, m, n, hq, hkv, ragged, layout, None)
+
+
+def test_many_padded_queries_and_keys_of_infinities():
+    n, fan, m = 20000, 64, 3
+    k, v = block(80, 1, 2, n)
+    k[0, 0, 5], k[0, 1, n - 1, 3] = math.inf, math.nan
+    cache = binding.EvictCache("attention", 1, 2, budget=n, n_sink=0, max_block=n)
+    cache.update_and_fetch(k, v)
+    q, lse = rows(82, fan, 16, m), torch.full((fan, 16, m), 5.0, device="cuda")
+    lse[50, 3], lse[60, 3], lse[60, 12], lse[61, 0, 1] = -math.inf, math.inf, math.nan, 9.0
+    n_new = torch.zeros(fan, dtype=torch.int32)
+    n_new[48:] = torch.tensor([3, 0, 3, 1] * 4)     # nothing in the first 1152 query rows of a head
+    n_new[60] = 0                                   # which has the NaN
+    cache.weigh(q, lse, n_new=n_new.cuda())
+    cache.sync()
+    zero = torch.zeros(1, 2, n, device="cuda")
+    got, (w, bound) = cache.view()[3], weigh64(zero, k, q, lse, n_new.tolist(), SCALE)
+    other = torch.ones(1, 2, n, dtype=torch.bool)
+    other[0, 0, 5] = other[0, 1, n - 1] = False
+    check_weights(got[other.cuda()], w[other.cuda()], bound[other.cuda()])
+    assert torch.isnan(got[~other.cuda()]).all()
+    cache.close()
+    none = binding.EvictCache("attention", 1, 2, budget=n, n_sink=0, max_block=n)
+    none.update_and_fetch(k, v)
+    none.weigh(q, lse, n_new=torch.zeros(fan, dtype=torch.int32).cuda())
+    none.sync()
+    assert (none.view()[3] == 0).all()
+    none.close()
+
+
+def test_many_queries_with_counts_out_of_range():
+    n = 10000
+    k, v = block(84, 1, 2, n)
+    cache = binding.EvictCache("attention", 1, 2, budget=n, max_block=n)
+    cache.update_and_fetch(k, v)
+    q, lse = rows(86, 64, 8, 3), torch.full((64, 8, 3), 4.0, device="cuda")
+    n_new = torch.full((64,), 2, dtype=torch.int32)
+    n_new[7], n_new[40] = -5, 99
+    cache.weigh(q, lse, n_new=n_new.cuda())
+    with pytest.raises(binding.EvictError, match="index"):
+        cache.sync()
+    check_weights(cache.view()[3], *weigh64(torch.zeros(1, 2, n, device="cuda"), k, q, lse, n_new.clamp(0, 3).tolist(), SCALE))
+    cache.close()
+
+
+def test_a_captured_step_of_many_queries():
+    n, fan = 4000, 24
+    k, v = block(88, 1, 8, n)
+    stream = torch.cuda.Stream()
+    q, lse = rows(90, fan, 32, 4), torch.full((fan, 32, 4), 6.0, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        cache = binding.EvictCache("attention", 1, 8, budget=n, n_sink=0, max_block=n)
+        cache.update_and_fetch(k, v)
+        cache.weigh(q, lse)
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            cache.weigh(q, lse)
+        q.mul_(0.5)
+        graph.replay()
+        graph.replay()
+        stream.synchronize()
+    cache.sync()
+    got = cache.view()[3]
+    zero = torch.zeros(1, 8, n, device="cuda")
+    w1, b1 = weigh64(zero, k, q.double() * 2, lse, None, SCALE)
+    w2, b2 = weigh64(zero, k, q, lse, None, SCALE)
+    check_weights(got, w1 + 2 * w2, b1 + 2 * b2 + 6 * U32 * (w1 + 2 * w2))
+    cache.close()
