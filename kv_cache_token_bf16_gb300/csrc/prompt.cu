@@ -760,10 +760,7 @@ int bind_prompt(const evict_prompt* a, PromptPlan* plan) {
   p.work.err = a->error ? a->error : reinterpret_cast<int*>(base);
   p.lse = a->lse;
   p.weights = a->weights;
-  // (The tensor cores cut each of a logit's eight partial sums toward zero: logits of 10 .. 20 of random rows lost
-  // 0.9e-7 of themselves in the mean, of a row with itself 1.4e-7 .. 2.3e-7, which sums of weights add up: those of
-  // 8192 tokens with 28 heads were 2.8e-6 off, an fp32 product's 1.3e-6. The scale makes up for 2^-23 of it.)
-  p.scale2 = (float)((a->scale == 0.f ? 0.08838834764831845 : (double)a->scale) * 1.4426950408889634 * (1.0 + 0x1p-23));
+  p.scale2 = scale_base2(a->scale);
   return EVICT_OK;
 }
 

@@ -505,7 +505,7 @@ extern "C" int evict_weigh(evict_handle* h, const evict_rows* q, int batch, int 
   p.by_heads = Divisor(p.heads);
   p.by_per = Divisor(m * p.group);
   p.by_group = Divisor(p.group);
-  p.scale2 = (scale == 0.f ? 0.08838834764831845f : scale) * kLog2e;
+  p.scale2 = scale_base2(scale);
   p.err = h->err;
   int dev, sms;
   cudaError_t e = cudaGetDevice(&dev);

@@ -30,17 +30,20 @@ _PROMPT = struct.Struct("=2i Qqqqi4x Qqqqi4x Qqqqi4x Qqqqi4x QQQ iif4x QQ QQ")
 assert _PROMPT.size == ctypes.sizeof(EvictPrompt)
 _NO_ROWS = (0, 0, 0, 0, 0)
 
-_calls = None
+_calls = _alloc = _free = None
 
 
 def _load():
     """The library's calls with packed structs as arguments."""
-    global _calls
+    global _calls, _alloc, _free
     if paged._torch is None:
         paged._load()
-    calls = ctypes.CDLL(binding.load()._name)    # function objects of their own: other argument types
+    _alloc = paged._torch._C._cuda_cudaCachingAllocator_raw_alloc
+    _free = paged._torch._C._cuda_cudaCachingAllocator_raw_delete
+    lib = ctypes.CDLL(binding.load()._name)      # function objects of their own: other argument types
+    calls = {}
     for name in ("evict_prompt_attention", "evict_prompt_weights"):
-        fn = getattr(calls, name)
+        calls[name] = fn = getattr(lib, name)
         fn.restype, fn.argtypes = ctypes.c_int, [ctypes.c_char_p]
     _calls = calls
 
@@ -61,6 +64,7 @@ class Packing:
         self._starts, self.at = starts, starts.data_ptr()
         self.error = torch.zeros(1, dtype=torch.int32, device=starts.device)
         self.error_at = self.error.data_ptr()
+        self._call = self.at, self.n, self.error_at
 
     @property
     def starts(self):
@@ -74,21 +78,31 @@ class Packing:
             binding.evict_pages_status(self.error_at, paged._stream(self.index))
 
 
-# Workspace bytes of a call (0: attention, 1: weights) and its sizes on a device (which alone decide).
+# Workspace bytes of a call (0: attention, 1: weights) and its sizes on a device, which alone decide.
 _workspace = {}
 
 
-def _work(name, key, fields, device):
-    """The workspace of a call of these sizes: (tensor, bytes)."""
+def _run(name, key, fields, error):
+    """Make a call of these sizes with its workspace, which comes from torch's allocator: reused in stream order,
+    private to a graph that is being captured. (Not as a tensor: making and dropping one takes 3 us, this 0.6.)"""
+    index = key[1]
+    if paged._torch._C._cuda_getDevice() != index:
+        with paged._on(index):
+            return _run(name, key, fields, error)
     size = _workspace.get(key)
     if size is None:
         if len(_workspace) >= 4096:
             _workspace.clear()
-        with paged._on(key[1]):
-            size = getattr(binding, name + "_workspace")(EvictPrompt.from_buffer_copy(_PROMPT.pack(*fields, 0, 0, 0, 0)))
+        size = getattr(binding, name + "_workspace")(EvictPrompt.from_buffer_copy(_PROMPT.pack(*fields, 0, 0, 0, 0)))
         _workspace[key] = size
-    # from torch's allocator: reused in stream order, private to a graph that is being captured
-    return paged._torch.empty(size, dtype=paged._torch.uint8, device=device), size
+    stream = paged._stream(index)
+    at = _alloc(size, stream)
+    try:
+        code = _calls[name](_PROMPT.pack(*fields, at, size, error, stream))
+    finally:
+        _free(at)
+    if code:
+        binding.check(code)
 
 
 def _sizes(q, k, packing, scale):
@@ -131,11 +145,9 @@ def attention(q, k, v, packing: Packing | None = None, scale=None, out=None, lse
     else:
         outr = paged._rows(out, "out", index, bf16, batch, m, hq)
     lse_at = paged._like(lse, "lse", (batch, hq, m), torch.float32, index)
-    starts, n, error = (packing.at, packing.n, packing.error_at) if packing is not None else (0, 0, 0)
+    starts, n, error = packing._call if packing is not None else (0, 0, 0)
     fields = (batch, m, *qr, *kr, *vr, *outr, lse_at, 0, starts, n, 0, scale)
-    work, size = _work("evict_prompt_attention", (0, index, batch, hq, hkv, m, n, packing is None), fields, q.device)
-    paged._call(index, _calls.evict_prompt_attention,
-                _PROMPT.pack(*fields, work.data_ptr(), size, error, paged._stream(index)))
+    _run("evict_prompt_attention", (0, index, batch, hq, hkv, m, n, packing is None), fields, error)
     return out
 
 
@@ -162,9 +174,7 @@ def weights(q, k, lse, packing: Packing | None = None, last: int = 0, scale=None
         make = torch.empty if packing is None else torch.zeros
         out = make(batch, hkv, m, dtype=torch.float32, device=q.device)
     out_at = paged._like(out, "out", (batch, hkv, m), torch.float32, index)
-    starts, n, error = (packing.at, packing.n, packing.error_at) if packing is not None else (0, 0, 0)
+    starts, n, error = packing._call if packing is not None else (0, 0, 0)
     fields = (batch, m, *qr, *kr, *_NO_ROWS, *_NO_ROWS, lse_at, out_at, starts, n, min(last, m), scale)
-    work, size = _work("evict_prompt_weights", (1, index, batch, hq, hkv, m, n, packing is None), fields, q.device)
-    paged._call(index, _calls.evict_prompt_weights,
-                _PROMPT.pack(*fields, work.data_ptr(), size, error, paged._stream(index)))
+    _run("evict_prompt_weights", (1, index, batch, hq, hkv, m, n, packing is None), fields, error)
     return out
