@@ -272,3 +272,53 @@ def test_two_streams_at_once():
         spans = [(0, 0, q.shape[2])]
         check_prompt(q, k, v, spans, out, lse)
         check_weights(w, *weights64(q, k, lse, spans))
+
+
+# steps of 64, 32 or 16 tokens by several heads, whose number does not divide the group's; the window longer than the
+# sequence, as long, and shorter; one key tile and two
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (3, 1), (7, 1), (24, 1), (9, 1), (16, 2)])
+@pytest.mark.parametrize("last", [1, 16, 17, 32, 33, 64, 65])
+def test_windows_of_few_tokens(hq, hkv, last):
+    q, k = rows(80, 1, hq, 1700, std=1.5), rows(81, 1, hkv, 1700)
+    lse = torch.randn(1, hq, 1700, device="cuda", generator=torch.Generator("cuda").manual_seed(82)) + 4.0
+    for starts in ([0, 1400, 1416, 1417, 1480, 1700], [3, 130, 300]):
+        pk = prompt.Packing(torch.tensor(starts, dtype=torch.int32).cuda())
+        m = starts[-1] + 4 if starts[0] else 1700
+        args = q[:, :, :m], k[:, :, :m], lse[:, :, :m].contiguous()
+        w = torch.full((1, hkv, m), 3.0, device="cuda")
+        prompt.weights(*args, pk, last=last, out=w)
+        pk.sync()
+        check_weights(w, *weights64(*args, spans_of(starts, 1, m), last), 3.0)
+
+
+# more sequences than the schedule's tables in shared memory hold, most of them empty
+@pytest.mark.parametrize("m", [1000, 2500])
+@pytest.mark.parametrize("n", [4095, 4096, 4097, 20000])
+def test_very_many_sequences(m, n):
+    lens = [0] * n
+    g = torch.Generator().manual_seed(n)
+    for i in torch.randint(0, n, (m // 9,), generator=g).tolist():
+        lens[i] = 1 + i % 7
+    lens[n // 2] = 300
+    starts = starts_of(lens)
+    assert starts[-1] <= m
+    q, k, v = rows(83, 1, 8, m, std=1.5), rows(84, 1, 2, m), rows(85, 1, 2, m)
+    run(q, k, v, starts)
+
+
+def test_calls_between_others_of_torchs_allocator():
+    # workspaces go back to the allocator when the call returns: what takes their place comes behind the work
+    q, k, v = rows(86, 1, 8, 3000), rows(87, 1, 2, 3000), rows(88, 1, 2, 3000)
+    outs = []
+    for i in range(6):
+        lse = torch.empty(1, 8, 3000, device="cuda")
+        out = prompt.attention(q, k, v, lse=lse)
+        junk = [torch.full((1 << s,), float("nan"), device="cuda") for s in range(10, 26, 3)]
+        w = prompt.weights(q, k, lse)
+        del junk
+        outs.append((out, lse, w))
+    for got in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got, outs[0]))
+    spans = [(0, 0, 3000)]
+    check_prompt(q, k, v, spans, outs[0][0], outs[0][1])
+    check_weights(outs[0][2], *weights64(q, k, outs[0][1], spans))
