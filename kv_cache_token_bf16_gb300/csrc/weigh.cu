@@ -203,7 +203,7 @@ struct WideParams {
 };
 
 // The next query rows from c0 on that count, at most kChunk, to shared memory; their number. By all threads.
-__device__ int lay_queries(const WeighParams& p, WideShared& sh, unsigned char* rows, int b, int h, int c0) {
+__device__ int lay_queries(const WeighParams& p, WideShared& sh, uint32_t rows, int b, int h, int c0) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = c0 + tid;
   bool counts_here = false;
   long long at = 0;
@@ -211,11 +211,11 @@ __device__ int lay_queries(const WeighParams& p, WideShared& sh, unsigned char* 
   if (warp < kSumWarps && c < p.queries) {
     const int f = p.by_per.div(c), in = c - f * p.m * p.group, tok = p.by_group.div(in);
     const int seq = b * p.fan + f, hq = h * p.group + in - tok * p.group;
-    if (!p.n_new || tok < p.n_new[seq]) {
-      l = p.lse[((long long)seq * p.hq + hq) * p.m + tok];
-      counts_here = fabsf(l) != INFINITY;         // no weights of a query that saw nothing, or with all elsewhere
-      at = seq * p.qb + hq * p.qh + tok * p.qm;
-    }
+    const int news = p.n_new ? p.n_new[seq] : p.m;
+    l = p.lse[((long long)seq * p.hq + hq) * p.m + tok];
+    // (no weights of a query that saw nothing, or with all of them elsewhere)
+    counts_here = tok < news && fabsf(l) != INFINITY;
+    at = seq * p.qb + hq * p.qh + tok * p.qm;
   }
   const uint32_t mine = __ballot_sync(0xffffffffu, counts_here);
   if (lane == 0 && warp < kSumWarps) sh.counts[warp] = __popc(mine);
@@ -242,10 +242,12 @@ __device__ int lay_queries(const WeighParams& p, WideShared& sh, unsigned char* 
 #pragma unroll 4
   for (int i = tid; i < total * 16; i += kWideThreads) {
     const int r = i >> 4, piece = i & 15;
-    const uint4 x = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + sh.at[r])[piece];
-    *reinterpret_cast<uint4*>(rows + (r / kTile) * kTileBytes + (piece >> 3) * (kTileBytes / 2) + (r % kTile) * 128 +
-                              (((piece & 7) ^ (r & 7)) << 4)) = x;
+    const uint32_t to = rows + (r / kTile) * kTileBytes + (piece >> 3) * (kTileBytes / 2) + (r % kTile) * 128 +
+                        (((piece & 7) ^ (r & 7)) << 4);
+    const void* from = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + sh.at[r]) + piece;
+    tc::cp_async16(to, from, 16);
   }
+  tc::cp_async_wait_all();
   tc::fence_proxy_async_smem();
   __syncthreads();
   return total;
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) weigh_wide_kernel(const __gri
       const int ahead = min(first + kKeyRing, last);
       if (warp == kCopyWarp && lane == 0 && ok) ok = copy_tiles(p, sh, smem, b, h, first, ahead, tiles);
       __syncwarp();
-      const int total = uni(lay_queries(w, sh, smem_raw + kKeyRing * kTileBytes, b, h, c0));
+      const int total = uni(lay_queries(w, sh, queries, b, h, c0));
       c0 = uni(sh.next);
       const int blocks = (total + kTile - 1) / kTile;
       if (total == 0) {                           // no use for them
