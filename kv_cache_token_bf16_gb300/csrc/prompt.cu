@@ -45,7 +45,7 @@ constexpr int kBadWords = kRows / 32;             // rows of V behind the unit's
 constexpr int kPartly = 4;                        // barriers of tiles to scrub, in turn: the ring holds at most three
 constexpr float kMoveAbove = 4096.f;              // sum of 32 weights that makes the reference move
 constexpr int kEntry = 2, kMinSteps = 4;
-constexpr int kWholeRows = 1024;
+constexpr int kWholeRows = 1024, kWholeRounds = 5;
 
 struct Steps {
   int tile;
@@ -587,40 +587,55 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
   if (tid == 0 && sh.fail) raise_device_error(p.work.err, kDevWaitTimeout);
 }
 
-// Rows of units that two or more CTAs share: a warp merges a row's parts, in the shares' order.
-constexpr int kJoinWarps = 8, kJoinSplit = 4;
+// Rows of units that two or more CTAs share: a warp merges its rows' parts, in the shares' order, four rows at a
+// time, whose loads are on their way together.
+constexpr int kJoinWarps = 8, kJoinSplit = 4, kJoinRows = 4;
+static_assert(kRows % (kJoinRows * kJoinWarps * kJoinSplit) == 0);
 __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(const __grid_constant__ PromptParams p) {
   pdl_wait();
   SplitUnit u;
-  if (!split_unit(p.work, blockIdx.x + 1, u, Steps{p.work.tile})) return;
-  const int lane = threadIdx.x & 31;
+  if (!split_unit(p.work, blockIdx.x + 1, u)) return;
+  const int lane = threadIdx.x & 31, warp = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
 #pragma unroll 1
-  for (int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); row < kRows; row += kJoinWarps * kJoinSplit) {
-  const int w = row / kTile, tl = p.by_group.div(row - w * kTile), g = row - w * kTile - tl * p.group;
-  const int token = u.k.tile * p.work.tile + w * p.half + tl;
-  if (tl >= p.half || token >= u.k.at.len) continue;
-  float top = -INFINITY, sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int i = u.c0; i <= u.c1; ++i) {
-    const size_t at = (size_t)(2 * i + (i == u.c0 ? 1 : 0)) * kRows + row;
-    const float2 ml = p.part_ml[at];
-    const float4 v = reinterpret_cast<const float4*>(p.part + at * kHeadDim)[lane];
-    const float to = fmaxf(top, ml.x), f = weight_of(top, to), wt = weight_of(ml.x, to);
-    top = to;
-    sum = sum * f + ml.y * wt;
-    acc.x = acc.x * f + v.x * wt;
-    acc.y = acc.y * f + v.y * wt;
-    acc.z = acc.z * f + v.z * wt;
-    acc.w = acc.w * f + v.w * wt;
-  }
-  const float inv = 1.f / sum;
-  const int hq = u.h * p.group + g;
-  const long long out_row = (long long)u.k.at.row0 + token;
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + u.k.at.plane * p.ob + hq * p.oh + out_row * p.om + 4 * lane) =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (p.lse && lane == 0)
-    p.lse[((long long)u.k.at.plane * p.hq + hq) * p.work.m + out_row] = (top + log2f(sum)) * 0.6931471805599453f;
+  for (int row0 = warp * kJoinRows; row0 < kRows; row0 += kJoinWarps * kJoinSplit * kJoinRows) {
+    float top[kJoinRows], sum[kJoinRows];
+    float4 acc[kJoinRows];
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) top[r] = -INFINITY, sum[r] = 0.f, acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int i = u.c0; i <= u.c1; ++i) {
+      const size_t at = (size_t)(2 * i + (i == u.c0 ? 1 : 0)) * kRows + row0;
+      float2 ml[kJoinRows];
+      float4 v[kJoinRows];
+#pragma unroll
+      for (int r = 0; r < kJoinRows; ++r) {       // (of rows without a query whatever lies there)
+        ml[r] = p.part_ml[at + r];
+        v[r] = reinterpret_cast<const float4*>(p.part + (at + r) * kHeadDim)[lane];
+      }
+#pragma unroll
+      for (int r = 0; r < kJoinRows; ++r) {
+        const float to = fmaxf(top[r], ml[r].x), f = weight_of(top[r], to), wt = weight_of(ml[r].x, to);
+        top[r] = to;
+        sum[r] = sum[r] * f + ml[r].y * wt;
+        acc[r].x = acc[r].x * f + v[r].x * wt;
+        acc[r].y = acc[r].y * f + v[r].y * wt;
+        acc[r].z = acc[r].z * f + v[r].z * wt;
+        acc[r].w = acc[r].w * f + v[r].w * wt;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) {
+      const int row = row0 + r, w = row / kTile, tl = p.by_group.div(row - w * kTile), g = row - w * kTile - tl * p.group;
+      const int token = u.tile * p.work.tile + w * p.half + tl;
+      if (tl >= p.half || token >= u.at.len) continue;
+      const float inv = 1.f / sum[r];
+      const int hq = u.h * p.group + g;
+      const long long out_row = (long long)u.at.row0 + token;
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + u.at.plane * p.ob + hq * p.oh + out_row * p.om + 4 * lane) =
+          make_uint2(pack_bf16(acc[r].x * inv, acc[r].y * inv), pack_bf16(acc[r].z * inv, acc[r].w * inv));
+      if (p.lse && lane == 0)
+        p.lse[((long long)u.at.plane * p.hq + hq) * p.work.m + out_row] = (top[r] + log2f(sum[r])) * 0.6931471805599453f;
+    }
   }
 }
 
@@ -652,7 +667,7 @@ cudaError_t allow_smem(int dev) {
 int make_plan(const evict_prompt* a, PromptPlan* plan) {
   const int group = a->q.heads / a->k.heads, half = kTile / group, tile = 2 * half;
   const int rc = plan_prompt(a, tile, ((long long)a->m + kTile - 1) / kTile, kEntry, kMinSteps, kWholeRows,
-                             2 * kRows * sizeof(float2), 2 * (size_t)kRows * kHeadDim * sizeof(float), plan);
+                             kWholeRounds, 2 * kRows * sizeof(float2), 2 * (size_t)kRows * kHeadDim * sizeof(float), true, plan);
   plan->p.half = half;
   return rc;
 }
@@ -699,8 +714,8 @@ int check_prompt(const evict_prompt* a, bool attention) {
 }
 
 // Sizes alone decide: the sequences' lengths are the device's.
-int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry, int min_steps, int whole_rows,
-                size_t part_ml, size_t part, PromptPlan* out) {
+int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry, int min_steps, int whole_rows, int whole_rounds,
+                size_t part_ml, size_t part, bool longest_last, PromptPlan* out) {
   PromptPlan& P = *out;
   P = PromptPlan();
   PromptParams& p = P.p;
@@ -715,7 +730,7 @@ int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry
   w.tile = tile;
   w.entry = entry;
   w.min_steps = min_steps;
-  w.whole = a->m <= whole_rows;
+  w.longest_last = longest_last;
   const int seq_blocks = (a->m + tile - 1) / tile;
   const long long blocks = a->starts ? (long long)a->m / tile + a->n_seqs : (long long)a->batch * seq_blocks;
   if (blocks * w.hkv >= (1ll << 30) || (double)blocks * w.hkv * (double)(most_steps + entry) >= 2147483648.0)
@@ -729,6 +744,7 @@ int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P.sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e, "looking up the device");
   P.dev = dev;
+  w.whole = a->m <= whole_rows || blocks * w.hkv >= (long long)whole_rounds * P.sms;
   size_t off = 256;                               // an error word, for callers without one
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -736,7 +752,7 @@ int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry
     return at;
   };
   w.total = reinterpret_cast<int*>(take(2 * sizeof(int)));
-  w.begin = reinterpret_cast<int2*>(take(P.sms * sizeof(int2)));
+  w.begin = reinterpret_cast<PromptBegin*>(take(P.sms * sizeof(PromptBegin)));
   w.block_base = reinterpret_cast<int*>(take(((size_t)w.seqs + 1) * sizeof(int)));
   p.part_ml = reinterpret_cast<float2*>(take(w.whole ? 0 : P.sms * part_ml));
   p.part = reinterpret_cast<float*>(take(w.whole ? 0 : P.sms * part));

@@ -131,8 +131,16 @@ struct PromptCursor {
   int blocks;
   int e, h;
   int from, to;                      // steps of the unit that are this CTA's
-  int left;                          // of the share, from `from` on; whole: of the units
+  int left;                          // of the share, from `from` on
+  int round;                         // whole: units before
 };
+
+// Whole units: the CTA's unit of this round; negative where there is none. The longest units come first, and every
+// other round goes the other way round the CTAs, so that their sums are nearly equal.
+__device__ __forceinline__ int whole_unit(const PromptWork& w, int units, int round) {
+  const int rank = round * (int)gridDim.x + (round & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+  return rank >= units ? -1 : w.longest_last ? units - 1 - rank : rank;
+}
 
 // The steps of the unit at hand behind `step` (negative: in its entry); false where the share ends before.
 __device__ __forceinline__ bool settle(PromptCursor& c, int step) {
@@ -151,15 +159,20 @@ __device__ __forceinline__ bool settle(PromptCursor& c, int step) {
 // kernel's start its code comes from memory, some 6,000 clocks for 25 KB of it.)
 template <typename Steps>
 __device__ __forceinline__ bool next_unit(const PromptWork& w, PromptCursor& c, Steps steps) {
-  const int by = w.whole ? (int)gridDim.x : 1;
-  c.left -= w.whole ? by : c.to - c.from;
-  if (c.left <= 0) return false;
-  c.h += by;
-  if (c.h >= w.hkv) {
-    const int up = w.by_hkv.div(c.h);
-    c.e += up;
-    c.h -= up * w.hkv;
-    c.k = block_of(w, Tables{w.starts, w.block_base}, c.e, steps);
+  int e = c.e;
+  if (w.whole) {
+    const int unit = whole_unit(w, c.blocks * w.hkv, ++c.round);
+    if (unit < 0) return false;
+    e = w.by_hkv.div(unit);
+    c.h = unit - e * w.hkv;
+  } else {
+    c.left -= c.to - c.from;
+    if (c.left <= 0) return false;
+    if (++c.h == w.hkv) c.h = 0, ++e;
+  }
+  if (e != c.e) {
+    c.e = e;
+    c.k = block_of(w, Tables{w.starts, w.block_base}, e, steps);
   }
   if (!w.whole) return settle(c, -w.entry);
   c.from = 0;
@@ -177,13 +190,14 @@ __device__ __forceinline__ bool first_unit(const PromptWork& w, PromptScan& sh, 
   const int tid = threadIdx.x, per = (c.blocks + kThreads - 1) / kThreads, units = c.blocks * w.hkv;
   const int e0 = min(tid * per, c.blocks), e1 = min(e0 + per, c.blocks);
   Shares shares;
+  const int first = w.whole ? whole_unit(w, units, 0) : 0, at_block = w.by_hkv.div(max(first, 0));
   int base = 0, g0 = 0;
   // the sums of the steps, unless units are not cut; then the block where the share begins
 #pragma unroll 1
   for (int find = w.whole; find < 2; ++find) {
     if (find) {
       if (!w.whole && (int)blockIdx.x >= shares.count) return false;   // the whole CTA, here and below
-      if (w.whole && (int)blockIdx.x >= units) return false;
+      if (first < 0) return false;
       g0 = w.whole ? 0 : shares.begin(blockIdx.x);
     }
     int at = base;
@@ -191,11 +205,10 @@ __device__ __forceinline__ bool first_unit(const PromptWork& w, PromptScan& sh, 
     for (int e = e0; e < e1; ++e) {
       const PromptBlock k = block_of(w, t, e, steps);
       const int of_block = (k.steps + w.entry) * w.hkv;
-      if (find && (w.whole ? e == w.by_hkv.div(blockIdx.x) : g0 >= at && g0 < at + of_block)) {
+      if (find && (w.whole ? e == at_block : g0 >= at && g0 < at + of_block)) {
         sh.e = e;
         sh.rest = g0 - at;
         sh.k = k;
-        if (!w.whole) w.begin[blockIdx.x] = make_int2(e, g0 - at);
       }
       at += of_block;
     }
@@ -213,8 +226,8 @@ __device__ __forceinline__ bool first_unit(const PromptWork& w, PromptScan& sh, 
   c.e = sh.e;
   c.k = sh.k;
   if (w.whole) {
-    c.left = units - blockIdx.x;
-    c.h = blockIdx.x - c.e * w.hkv;
+    c.round = 0;
+    c.h = first - c.e * w.hkv;
     c.from = 0;
     c.to = c.k.steps;
     return true;
@@ -222,28 +235,33 @@ __device__ __forceinline__ bool first_unit(const PromptWork& w, PromptScan& sh, 
   const int unit = c.k.steps + w.entry;
   c.h = sh.rest / unit;
   c.left = shares.begin(blockIdx.x + 1) - g0;
-  return settle(c, sh.rest - c.h * unit - w.entry);   // false: the share lies in one unit's entry
+  const int step = sh.rest - c.h * unit - w.entry;
+  if (tid == 0) {                                 // what the join needs to know
+    int4* at = reinterpret_cast<int4*>(w.begin + blockIdx.x);
+    at[0] = make_int4(c.k.at.plane, c.k.at.row0, c.k.at.len, c.k.tile);
+    at[1] = make_int4(c.h, step, c.k.steps, 0);
+  }
+  return settle(c, step);            // false: the share lies in one unit's entry
 }
 
 // A unit that two or more CTAs share, found where a share begins inside it: the first such share's
 // block does the work. Its parts: slot 2 c0 + 1, then 2 c of the following shares up to c1.
 struct SplitUnit {
-  PromptBlock k;
-  int h, c0, c1;
+  Span at;
+  int tile, h, c0, c1;
 };
-template <typename Steps>
-__device__ __forceinline__ bool split_unit(const PromptWork& w, int c, SplitUnit& u, Steps steps) {
+__device__ __forceinline__ bool split_unit(const PromptWork& w, int c, SplitUnit& u) {
+  const int4* from = reinterpret_cast<const int4*>(w.begin + c);
+  const int4 a = from[0], b = from[1];            // beside the next, whether there is such a share or not
   const Shares shares(w.total[0], w.total[1]);
   if (c >= shares.count) return false;
-  const int2 at = w.begin[c];
-  u.k = block_of(w, Tables{w.starts, w.block_base}, at.x, steps);
-  const int per = u.k.steps + w.entry;
-  u.h = at.y / per;
-  const int step = at.y - u.h * per - w.entry;
-  if (step <= 0) return false;                    // the share begins with the unit, or in its entry
-  const int first = shares.begin(c) - step;
+  if (b.y <= 0) return false;                     // the share begins with the unit, or in its entry
+  const int first = shares.begin(c) - b.y;
+  u.at = {a.x, a.y, a.z};
+  u.tile = a.w;
+  u.h = b.x;
   u.c0 = shares.of(first);
-  u.c1 = shares.of(first + u.k.steps - 1);
+  u.c1 = shares.of(first + b.z - 1);
   return u.c0 == c - 1;
 }
 

@@ -10,11 +10,16 @@
 
 namespace evict {
 
+// Where a share begins: the block's plane, its sequence's first row and length, the block; KV head, step, steps.
+struct alignas(16) PromptBegin {
+  int of[8];
+};
+
 // The work of one call. A block is `tile` tokens of one sequence; a unit is a
 // block and a KV head, and its work a number of steps that the kernel knows,
 // behind `entry` more for its start. The blocks' units, in the order of blocks
 // and heads, are laid end to end and cut into equal contiguous shares, one for
-// a CTA. `whole`: units are not cut; CTA i takes units i, i + CTAs, ...
+// a CTA. `whole`: units are not cut, but dealt out to the CTAs.
 struct PromptWork {
   const int32_t* starts;             // [seqs + 1] first rows of the sequences of one plane; or NULL: a plane each
   int seqs, m;                       // sequences; rows of a plane
@@ -22,10 +27,10 @@ struct PromptWork {
   int tile;                          // tokens of a block
   int blocks;                        // at most
   int entry, min_steps;              // steps that a unit's start counts as; of a share at least
-  int whole;
+  int whole, longest_last;           // longest_last: of a sequence's blocks the last has the most steps
   Divisor by_hkv, by_tile, by_seq_blocks;
   int* block_base;                   // [seqs + 1] blocks of the sequences before (packed)
-  int2* begin;                       // [CTAs] block and rest in it where a share begins
+  PromptBegin* begin;                // [CTAs]
   int* total;                        // [2] steps of all units, the shares' number
   int* err;
 };
@@ -69,10 +74,10 @@ struct PromptPlan {
   PromptParams p;
   size_t bytes;
 };
-// tile, entry, min_steps: as above; most_steps: of a unit; whole_rows: planes of so many rows are not cut; part_ml, part:
-// bytes of a CTA's partial results.
-int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry, int min_steps, int whole_rows,
-                size_t part_ml, size_t part, PromptPlan* out);
+// tile, entry, min_steps, longest_last: as above; most_steps: of a unit; whole_rows, whole_rounds: units of planes of
+// so many rows, or of as many for every SM, are not cut; part_ml, part: bytes of a CTA's partial results.
+int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry, int min_steps, int whole_rows, int whole_rounds,
+                size_t part_ml, size_t part, bool longest_last, PromptPlan* out);
 int bind_prompt(const evict_prompt* a, PromptPlan* plan);
 // Boxes of heads_box heads of rows_box rows of 64 elements, 128-byte swizzle: a row's heads one behind the other
 // (heads_first; coordinates element, head, row, plane), or a head's rows (element, row, head, plane).

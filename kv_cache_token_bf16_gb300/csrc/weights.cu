@@ -36,7 +36,7 @@ constexpr int kSumWarps = 16;
 constexpr int kReaders = kSumWarps + 3;           // warps that read a unit: summing, issuing, loading log-sum-exps
 constexpr int kMmaWarp = 16, kTmaWarp = 18, kThreads = 640;
 constexpr int kEntry = 3, kMinSteps = 8;
-constexpr int kWholeRows = 1024;
+constexpr int kWholeRows = 1024, kWholeRounds = 5;
 
 // The first query that counts for the keys from key0 on.
 __device__ __forceinline__ int first_query(int last, int key0, int len) { return max(key0, last ? len - last : 0); }
@@ -63,12 +63,15 @@ constexpr int kPart = 1, kWhole = 2;              // kinds
 struct WeightsShared {
   uint64_t unit_full[kUnits], unit_empty[kUnits], k_full[2], k_empty[2], q_full[kRing], q_empty[kRing];
   uint64_t s_full[2][2], s_empty[2][2], lse_full[kRing], lse_empty[kRing], done[2];   // buffer, key tile
+  uint64_t turn[2];                               // of the issuing warps
   uint32_t tmem_base;
   int fail;
   Unit units[kUnits];
-  alignas(16) float neg_lse2[kRing][kTile];
+  union {
+    alignas(16) float neg_lse2[kRing][kTile];
+    PromptScan scan;                              // before the first of them
+  };
   float sums[kKeys];
-  PromptScan scan;
 };
 // All of it is dynamic: seven tiles and this fill the 227 KB.
 constexpr int kSmem = (4 + kRing) * kTileBytes + (int)sizeof(WeightsShared);
@@ -223,6 +226,7 @@ __device__ void mma_issuer(const PromptParams& p, WeightsShared& sh, int kt, uin
   const uint64_t kd = tc::sw128_desc(kbuf), qd = tc::sw128_desc(ring);
   const uint32_t hi = (uint32_t)(kd >> 32), k_lo = (uint32_t)kd, q_lo = (uint32_t)qd;
   Ring<2> k, s_buf;
+  uint32_t turns = 0;
   Ring<kRing> q;
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return ok = ok && warp_wait(bar, parity, &sh.fail); };
@@ -234,10 +238,14 @@ __device__ void mma_issuer(const PromptParams& p, WeightsShared& sh, int kt, uin
 #pragma unroll 1
     for (int i = u.from; i < u.to; ++i, s.next(p, u)) {
       if (!wait(&sh.q_full[q.i], q.parity) || !wait(&sh.lse_full[q.i], q.parity) || !wait(&sh.s_empty[s_buf.i][kt], s_buf.parity ^ 1)) break;
+      // the two take turns, each with its waits behind it: the tensor cores have the one's products while the other waits
+      if ((kt || turns) && !wait(&sh.turn[kt], (turns - 1 + kt) & 1)) break;
+      ++turns;
       tc::fence_after_sync();
       if (s.sees(u, kt))
         tm::warp_mma_rows(tmem + (2 * s_buf.i + kt) * kTile, tm::desc_of(k_lo + (((2 * k.i + kt) * kTileBytes) >> 4), hi),
                           tm::desc_of(q_lo + ((q.i * kTileBytes) >> 4), hi), tc::idesc_bf16_f32(kTile, (s.columns(p) + 15) & ~15));
+      if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&sh.turn[kt ^ 1]);
       tm::warp_mma_commit(&sh.s_full[s_buf.i][kt]);
       tm::warp_mma_commit(&sh.q_empty[q.i]);
       q.next();
@@ -383,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_weights_kernel(const __gri
       tc::mbar_init(&sh.k_full[i], 1);
       tc::mbar_init(&sh.k_empty[i], 2);           // both issuers
       tc::mbar_init(&sh.done[i], 1);
+      tc::mbar_init(&sh.turn[i], 1);
       for (int kt = 0; kt < 2; ++kt) {
         tc::mbar_init(&sh.s_full[i][kt], 1);
         tc::mbar_init(&sh.s_empty[i][kt], kSumWarps / 4);
@@ -434,13 +443,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_weights_kernel(const __gri
 __global__ void __launch_bounds__(kKeys) prompt_weights_join_kernel(const __grid_constant__ PromptParams p) {
   pdl_wait();
   SplitUnit u;
-  if (!split_unit(p.work, blockIdx.x + 1, u, Steps(p))) return;
-  const int key = threadIdx.x, at = u.k.tile * kKeys + key;
-  if (at >= u.k.at.len) return;
+  if (!split_unit(p.work, blockIdx.x + 1, u)) return;
+  const int key = threadIdx.x, at = u.tile * kKeys + key;
+  if (at >= u.at.len) return;
   float sum = 0.f;
 #pragma unroll 4
   for (int i = u.c0; i <= u.c1; ++i) sum += p.part[(size_t)(2 * i + (i == u.c0 ? 1 : 0)) * kKeys + key];
-  p.weights[((long long)u.k.at.plane * p.work.hkv + u.h) * p.work.m + u.k.at.row0 + at] = sum;
+  p.weights[((long long)u.at.plane * p.work.hkv + u.h) * p.work.m + u.at.row0 + at] = sum;
 }
 
 // The kernel's dynamic shared memory, allowed once for each device.
@@ -465,7 +474,7 @@ int step_tokens(const evict_prompt* a) {
 int make_plan(const evict_prompt* a, PromptPlan* plan) {
   const int group = a->q.heads / a->k.heads, tokens = step_tokens(a), heads = kTile / tokens, head_steps = (group + heads - 1) / heads;
   const long long most = (long long)head_steps * (((long long)a->m + tokens - 1) / tokens);
-  const int rc = plan_prompt(a, kKeys, most, kEntry, kMinSteps, kWholeRows, 0, 2 * kKeys * sizeof(float), plan);
+  const int rc = plan_prompt(a, kKeys, most, kEntry, kMinSteps, kWholeRows, kWholeRounds, 0, 2 * kKeys * sizeof(float), false, plan);
   PromptParams& p = plan->p;
   p.last = a->last;
   p.half = tokens;
