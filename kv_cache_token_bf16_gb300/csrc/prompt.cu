@@ -45,7 +45,10 @@ constexpr int kBadWords = kRows / 32;             // rows of V behind the unit's
 constexpr int kPartly = 4;                        // barriers of tiles to scrub, in turn: the ring holds at most three
 constexpr float kMoveAbove = 4096.f;              // sum of 32 weights that makes the reference move
 constexpr int kEntry = 2, kMinSteps = 4;
-constexpr int kWholeRows = 1024, kWholeRounds = 5;
+// Units go uncut in planes of this many rows (too short to share), and where every SM has this many: then nothing is
+// joined. (us, uncut and cut: 24 sequences of up to 1021 tokens, 32 / 8 heads, 12 units an SM, 129 and 135; 8192 tokens,
+// 28 / 4 heads, 6 an SM, 333 and 352; 4096 tokens, 3 an SM, 100 and 112; 4 x 2048, 40 / 8 heads, 9 an SM, 170 and 168.)
+constexpr int kWholeRows = 1024, kWholeRounds = 3;
 
 struct Steps {
   int tile;
@@ -754,8 +757,10 @@ int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry
   w.total = reinterpret_cast<int*>(take(2 * sizeof(int)));
   w.begin = reinterpret_cast<PromptBegin*>(take(P.sms * sizeof(PromptBegin)));
   w.block_base = reinterpret_cast<int*>(take(((size_t)w.seqs + 1) * sizeof(int)));
-  p.part_ml = reinterpret_cast<float2*>(take(w.whole ? 0 : P.sms * part_ml));
-  p.part = reinterpret_cast<float*>(take(w.whole ? 0 : P.sms * part));
+  // (`last` may decide whether the weights' units are cut, but not the bytes)
+  const bool parts = a->m > whole_rows && !(longest_last && w.whole);
+  p.part_ml = reinterpret_cast<float2*>(take(parts ? P.sms * part_ml : 0));
+  p.part = reinterpret_cast<float*>(take(parts ? P.sms * part : 0));
   P.bytes = off;
   return EVICT_OK;
 }

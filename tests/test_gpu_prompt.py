@@ -6,7 +6,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from kv_cache_token_bf16_gb300 import binding, prompt  # noqa: E402
+from kv_cache_token_bf16_gb300 import binding, paged, prompt  # noqa: E402
 from tests.paged_util import D  # noqa: E402
 from tests.prompt_util import SCALE, check_prompt, check_weights, spans_of, weights64  # noqa: E402
 
@@ -322,3 +322,31 @@ def test_calls_between_others_of_torchs_allocator():
     spans = [(0, 0, 3000)]
     check_prompt(q, k, v, spans, outs[0][0], outs[0][1])
     check_weights(outs[0][2], *weights64(q, k, outs[0][1], spans))
+
+
+# units that go uncut beyond 1024 rows: three or more for every SM, dealt out the longest first
+@pytest.mark.parametrize("lens", [[3700], [700, 1, 0, 1300, 64, 513, 1022, 400], [129] * 40, [0, 0, 4100, 3, 0]])
+def test_uncut_units_of_long_planes(lens):
+    starts = starts_of(lens, 2)
+    m = starts[-1] + 5
+    q, k, v = rows(90, 1, 32, m, std=1.5), rows(91, 1, 8, m), rows(92, 1, 8, m)
+    v[0, :, starts[-1] - 3, 17], v[0, 2, 700, 5] = math.inf, -math.inf
+    run(q, k, v, starts)
+
+
+def test_uncut_units_of_windows_take_the_workspace_of_any_window():
+    B, m, h = 6, 4100, 8
+    q, k = rows(93, B, h, m, std=1.5), rows(94, B, h, m)
+    lse = torch.randn(B, h, m, device="cuda", generator=torch.Generator("cuda").manual_seed(95)) + 6.0
+    starts = torch.tensor([0, 1500, 4100], dtype=torch.int32).cuda()
+    for last in (0, 64, 300, 0, 1):
+        w = prompt.weights(q, k, lse, last=last)
+        check_weights(w, *weights64(q, k, lse, spans_of(None, B, m), last))
+        one = prompt.weights(q[:1], k[:1], lse[:1], prompt.Packing(starts), last=last)
+        check_weights(one, *weights64(q[:1], k[:1], lse[:1], spans_of([0, 1500, 4100], 1, m), last))
+    sizes = set()
+    for last in (0, 1, 64, 300, 5000):
+        fields = (B, m, *paged._rows(q, "q", 0, q.dtype, B, m), *paged._rows(k, "k", 0, k.dtype, B, m), *prompt._NO_ROWS * 2,
+                  lse.data_ptr(), 0, 0, 0, last, 0.0, 0, 0, 0, 0)
+        sizes.add(binding.evict_prompt_weights_workspace(binding.EvictPrompt.from_buffer_copy(prompt._PROMPT.pack(*fields))))
+    assert len(sizes) == 1
