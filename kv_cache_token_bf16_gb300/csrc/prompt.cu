@@ -45,10 +45,13 @@ constexpr int kBadWords = kRows / 32;             // rows of V behind the unit's
 constexpr int kPartly = 4;                        // barriers of tiles to scrub, in turn: the ring holds at most three
 constexpr float kMoveAbove = 4096.f;              // sum of 32 weights that makes the reference move
 constexpr int kEntry = 2, kMinSteps = 4;
+// Units that go uncut are taken as CTAs come to them where every SM has more than two (a kernel of its own sets their
+// count to 0): dealt out by their number, 24 sequences of up to 1021 tokens took 130 us instead of 117, 4 x 2048 171
+// instead of 150, 3 sequences of up to 2000 71 instead of 56.
 // Units go uncut in planes of this many rows (too short to share), and where every SM has this many: then nothing is
-// joined. (us, uncut and cut: 24 sequences of up to 1021 tokens, 32 / 8 heads, 12 units an SM, 129 and 135; 8192 tokens,
-// 28 / 4 heads, 6 an SM, 333 and 352; 4096 tokens, 3 an SM, 100 and 112; 4 x 2048, 40 / 8 heads, 9 an SM, 170 and 168.)
-constexpr int kWholeRows = 1024, kWholeRounds = 3;
+// joined. (us, uncut and cut: 24 sequences of up to 1021 tokens, 32 / 8 heads, 12 units an SM, 117 and 135; 8192 tokens,
+// 28 / 4 heads, 6 an SM, 343 and 352; 4096 tokens, 3 an SM, 102 and 112; 4 x 2048, 40 / 8 heads, 9 an SM, 150 and 168.)
+constexpr int kWholeRows = 1024, kWholeRounds = 3, kTakenRounds = 2;
 
 struct Steps {
   int tile;
@@ -590,6 +593,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_attention_kernel(const __g
   if (tid == 0 && sh.fail) raise_device_error(p.work.err, kDevWaitTimeout);
 }
 
+__global__ void prompt_begin_kernel(int* taken) {
+  pdl_wait();
+  if (threadIdx.x == 0) *taken = 0;
+}
+
 // Rows of units that two or more CTAs share: a warp merges its rows' parts, in the shares' order, four rows at a
 // time, whose loads are on their way together.
 constexpr int kJoinWarps = 8, kJoinSplit = 4, kJoinRows = 4;
@@ -754,13 +762,12 @@ int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry
     off += round256(bytes);
     return at;
   };
-  w.total = reinterpret_cast<int*>(take(2 * sizeof(int)));
+  w.total = reinterpret_cast<int*>(take(3 * sizeof(int)));
+  w.taken = w.whole && blocks * w.hkv > kTakenRounds * P.sms ? w.total + 2 : nullptr;
   w.begin = reinterpret_cast<PromptBegin*>(take(P.sms * sizeof(PromptBegin)));
   w.block_base = reinterpret_cast<int*>(take(((size_t)w.seqs + 1) * sizeof(int)));
-  // (`last` may decide whether the weights' units are cut, but not the bytes)
-  const bool parts = a->m > whole_rows && !(longest_last && w.whole);
-  p.part_ml = reinterpret_cast<float2*>(take(parts ? P.sms * part_ml : 0));
-  p.part = reinterpret_cast<float*>(take(parts ? P.sms * part : 0));
+  p.part_ml = reinterpret_cast<float2*>(take(w.whole ? 0 : P.sms * part_ml));
+  p.part = reinterpret_cast<float*>(take(w.whole ? 0 : P.sms * part));
   P.bytes = off;
   return EVICT_OK;
 }
@@ -775,6 +782,7 @@ int bind_prompt(const evict_prompt* a, PromptPlan* plan) {
   auto rebase = [&](auto*& x) { x = reinterpret_cast<std::remove_reference_t<decltype(x)>>(base + reinterpret_cast<size_t>(x)); };
   rebase(p.work.total);
   rebase(p.work.begin);
+  if (p.work.taken) p.work.taken = p.work.total + 2;
   rebase(p.work.block_base);
   rebase(p.part_ml);
   rebase(p.part);
@@ -782,6 +790,14 @@ int bind_prompt(const evict_prompt* a, PromptPlan* plan) {
   p.lse = a->lse;
   p.weights = a->weights;
   p.scale2 = scale_base2(a->scale);
+  return EVICT_OK;
+}
+
+int begin_prompt(const PromptWork& w, cudaStream_t st) {
+  if (!w.taken) return EVICT_OK;
+  const cudaError_t e = launch_pdl(prompt_begin_kernel, dim3(1), dim3(32), 0, st, nullptr, w.taken);
+  if (e != cudaSuccess) return cuda_fail(e, "prompt begin kernel launch");
+  g_launches.fetch_add(1);
   return EVICT_OK;
 }
 
@@ -835,6 +851,7 @@ extern "C" int evict_prompt_attention(const evict_prompt* a) {
   cudaError_t e = allow_smem(plan.dev);
   if (e != cudaSuccess) return cuda_fail(e, "prompt attention kernel attribute");
   const int ctas = p.work.whole ? std::min(plan.sms, p.work.blocks * p.work.hkv) : plan.sms;
+  if ((rc = begin_prompt(p.work, st))) return rc;
   if ((e = launch_pdl(prompt_attention_kernel, dim3(ctas), dim3(kThreads), kSmem, st, nullptr, p)) != cudaSuccess)
     return cuda_fail(e, "prompt attention kernel launch");
   g_launches.fetch_add(1);

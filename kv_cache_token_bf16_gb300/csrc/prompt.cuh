@@ -135,10 +135,12 @@ struct PromptCursor {
   int round;                         // whole: units before
 };
 
-// Whole units: the CTA's unit of this round; negative where there is none. The longest units come first, and every
-// other round goes the other way round the CTAs, so that their sums are nearly equal.
+// Whole units: the CTA's unit of this round; negative where there is none. The longest units come first. Either a CTA
+// takes the next one when it comes to it (who takes which changes no result), or every other round goes the other way
+// round the CTAs, so that their sums are nearly equal.
 __device__ __forceinline__ int whole_unit(const PromptWork& w, int units, int round) {
-  const int rank = round * (int)gridDim.x + (round & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+  int rank = round * (int)gridDim.x + (round & 1 ? (int)gridDim.x - 1 - (int)blockIdx.x : (int)blockIdx.x);
+  if (w.taken && round > 0) rank = (int)gridDim.x + atomicAdd(w.taken, 1);
   return rank >= units ? -1 : w.longest_last ? units - 1 - rank : rank;
 }
 

@@ -19,7 +19,7 @@ struct alignas(16) PromptBegin {
 // block and a KV head, and its work a number of steps that the kernel knows,
 // behind `entry` more for its start. The blocks' units, in the order of blocks
 // and heads, are laid end to end and cut into equal contiguous shares, one for
-// a CTA. `whole`: units are not cut, but dealt out to the CTAs.
+// a CTA. `whole`: units are not cut, but dealt out to the CTAs, or taken as CTAs come to them.
 struct PromptWork {
   const int32_t* starts;             // [seqs + 1] first rows of the sequences of one plane; or NULL: a plane each
   int seqs, m;                       // sequences; rows of a plane
@@ -31,7 +31,8 @@ struct PromptWork {
   Divisor by_hkv, by_tile, by_seq_blocks;
   int* block_base;                   // [seqs + 1] blocks of the sequences before (packed)
   PromptBegin* begin;                // [CTAs]
-  int* total;                        // [2] steps of all units, the shares' number
+  int* total;                        // [3] steps of all units, the shares' number; units taken
+  int* taken;                        // whole: units taken beyond the CTAs' first ones; or NULL
   int* err;
 };
 
@@ -79,6 +80,8 @@ struct PromptPlan {
 int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry, int min_steps, int whole_rows, int whole_rounds,
                 size_t part_ml, size_t part, bool longest_last, PromptPlan* out);
 int bind_prompt(const evict_prompt* a, PromptPlan* plan);
+// No units taken yet, before the kernel that takes them.
+int begin_prompt(const PromptWork& w, cudaStream_t st);
 // Boxes of heads_box heads of rows_box rows of 64 elements, 128-byte swizzle: a row's heads one behind the other
 // (heads_first; coordinates element, head, row, plane), or a head's rows (element, row, head, plane).
 int encode_heads(CUtensorMap* map, const evict_rows& x, int batch, int m, int heads_box, int rows_box, bool heads_first,

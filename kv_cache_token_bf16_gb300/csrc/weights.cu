@@ -36,11 +36,11 @@ constexpr int kSumWarps = 16;
 constexpr int kReaders = kSumWarps + 3;           // warps that read a unit: summing, issuing, loading log-sum-exps
 constexpr int kMmaWarp = 16, kTmaWarp = 18, kThreads = 640;
 constexpr int kEntry = 3, kMinSteps = 8;
-// Units go uncut in planes of this many rows (too short to share), and where they have this few steps, as those of short
-// windows, and every SM has this many: then nothing is joined. (us, uncut and cut: a window of 64 tokens, 8 x 8192, 32 / 8
-// heads, 40.7 and 46.3; of 200 tokens, 20 sequences of up to 2000, 51.7 and 62.2. Long units that differ are better cut:
-// 64 sequences of up to 1021 tokens, 14 units an SM, 152 and 144.)
-constexpr int kWholeRows = 1024, kWholeRounds = 5, kWholeSteps = 16;
+// Units go uncut in planes of this many rows (too short to share), and where every SM has this many: then nothing is
+// joined, and CTAs take units as they come to them. (us, uncut and cut: a window of 64 tokens, 8 x 8192, 32 / 8 heads, 13
+// units an SM, 41 and 46; 64 sequences of up to 1021 tokens, 14 an SM, 135 and 145; 24, 32 / 16 heads, 7 an SM, 72 and 80;
+// 32 / 8 heads, 3.5 an SM, 77 and 75.)
+constexpr int kWholeRows = 1024, kWholeRounds = 5;
 
 // The first query that counts for the keys from key0 on.
 __device__ __forceinline__ int first_query(int last, int key0, int len) { return max(key0, last ? len - last : 0); }
@@ -478,7 +478,7 @@ int step_tokens(const evict_prompt* a) {
 int make_plan(const evict_prompt* a, PromptPlan* plan) {
   const int group = a->q.heads / a->k.heads, tokens = step_tokens(a), heads = kTile / tokens, head_steps = (group + heads - 1) / heads;
   const long long most = (long long)head_steps * (((long long)(a->last > 0 ? std::min(a->last, a->m) : a->m) + tokens - 1) / tokens);
-  const int rc = plan_prompt(a, kKeys, most, kEntry, kMinSteps, kWholeRows, most <= kWholeSteps ? kWholeRounds : 1 << 30, 0, 2 * kKeys * sizeof(float), false, plan);
+  const int rc = plan_prompt(a, kKeys, most, kEntry, kMinSteps, kWholeRows, kWholeRounds, 0, 2 * kKeys * sizeof(float), false, plan);
   PromptParams& p = plan->p;
   p.last = a->last;
   p.half = tokens;
@@ -516,6 +516,7 @@ extern "C" int evict_prompt_weights(const evict_prompt* a) {
   cudaError_t e = allow_smem(plan.dev);
   if (e != cudaSuccess) return cuda_fail(e, "prompt weights kernel attribute");
   const int ctas = p.work.whole ? std::min(plan.sms, p.work.blocks * p.work.hkv) : plan.sms;
+  if ((rc = begin_prompt(p.work, st))) return rc;
   if ((e = launch_pdl(prompt_weights_kernel, dim3(ctas), dim3(kThreads), kSmem, st, nullptr, p)) != cudaSuccess)
     return cuda_fail(e, "prompt weights kernel launch");
   g_launches.fetch_add(1);
