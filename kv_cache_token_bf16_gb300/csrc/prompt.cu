@@ -48,10 +48,12 @@ constexpr int kEntry = 2, kMinSteps = 4;
 // Units that go uncut are taken as CTAs come to them where every SM has more than two (a kernel of its own sets their
 // count to 0): dealt out by their number, 24 sequences of up to 1021 tokens took 130 us instead of 117, 4 x 2048 171
 // instead of 150, 3 sequences of up to 2000 71 instead of 56.
-// Units go uncut in planes of this many rows (too short to share), and where every SM has this many: then nothing is
-// joined. (us, uncut and cut: 24 sequences of up to 1021 tokens, 32 / 8 heads, 12 units an SM, 117 and 135; 8192 tokens,
-// 28 / 4 heads, 6 an SM, 343 and 352; 4096 tokens, 3 an SM, 102 and 112; 4 x 2048, 40 / 8 heads, 9 an SM, 150 and 168.)
-constexpr int kWholeRows = 1024, kWholeRounds = 3, kTakenRounds = 2;
+// Units go uncut in planes of this many rows (too short to share), and where there is one for every SM: then nothing is
+// joined. (us, uncut and cut, of one sequence: 1021 tokens, 16 / 2 heads, 20 and 26; 1500, 26 and
+// 30; 2000, 8 / 1 heads, 33 and 29; 4000, 8 / 1 heads, 0.8 units an SM,
+// 57 and 46; 2900, 16 / 2 heads, 1.2 an SM, 44 and 51; 2000, 28 / 4 heads, 1.5 an SM, 34 and 48; 8192, 28 / 4 heads, 6 an
+// SM, 343 and 352. 24 of up to 1021 tokens, 32 / 8 heads, 12 an SM, 117 and 135; 4 x 2048, 40 / 8 heads, 150 and 168.)
+constexpr int kWholeRows = 1536, kWholeRounds = 1, kTakenRounds = 2;
 
 struct Steps {
   int tile;
@@ -677,8 +679,8 @@ cudaError_t allow_smem(int dev) {
 
 int make_plan(const evict_prompt* a, PromptPlan* plan) {
   const int group = a->q.heads / a->k.heads, half = kTile / group, tile = 2 * half;
-  const int rc = plan_prompt(a, tile, ((long long)a->m + kTile - 1) / kTile, kEntry, kMinSteps, kWholeRows,
-                             kWholeRounds, 2 * kRows * sizeof(float2), 2 * (size_t)kRows * kHeadDim * sizeof(float), true, plan);
+  const int rc = plan_prompt(a, tile, ((long long)a->m + kTile - 1) / kTile, kEntry, kMinSteps,
+                             a->m <= kWholeRows ? 0 : kWholeRounds, 2 * kRows * sizeof(float2), 2 * (size_t)kRows * kHeadDim * sizeof(float), true, plan);
   plan->p.half = half;
   return rc;
 }
@@ -725,7 +727,7 @@ int check_prompt(const evict_prompt* a, bool attention) {
 }
 
 // Sizes alone decide: the sequences' lengths are the device's.
-int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry, int min_steps, int whole_rows, int whole_rounds,
+int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry, int min_steps, int whole_rounds,
                 size_t part_ml, size_t part, bool longest_last, PromptPlan* out) {
   PromptPlan& P = *out;
   P = PromptPlan();
@@ -755,7 +757,7 @@ int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&P.sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e, "looking up the device");
   P.dev = dev;
-  w.whole = a->m <= whole_rows || blocks * w.hkv >= (long long)whole_rounds * P.sms;
+  w.whole = blocks * w.hkv >= (long long)whole_rounds * P.sms;
   size_t off = 256;                               // an error word, for callers without one
   auto take = [&](size_t bytes) {
     const size_t at = off;

@@ -75,9 +75,9 @@ struct PromptPlan {
   PromptParams p;
   size_t bytes;
 };
-// tile, entry, min_steps, longest_last: as above; most_steps: of a unit; whole_rows, whole_rounds: units of planes of
-// so many rows, or of as many for every SM, are not cut; part_ml, part: bytes of a CTA's partial results.
-int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry, int min_steps, int whole_rows, int whole_rounds,
+// tile, entry, min_steps, longest_last: as above; most_steps: of a unit; whole_rounds: where there are so many units for
+// every SM, they are not cut; part_ml, part: bytes of a CTA's partial results.
+int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry, int min_steps, int whole_rounds,
                 size_t part_ml, size_t part, bool longest_last, PromptPlan* out);
 int bind_prompt(const evict_prompt* a, PromptPlan* plan);
 // No units taken yet, before the kernel that takes them.

@@ -50,6 +50,16 @@ struct WeighParams {
   int* err;
 };
 
+// -lse in base 2, and what its rounding left out as a factor of the weights: 2^(x + neg) rest. (A large weight's relative
+// error is the exponent's, and a log-sum-exp of 11 has 2^-20 of one in base 2: a step's few queries add up no others.)
+struct Lse {
+  float neg, rest;
+};
+__device__ __forceinline__ Lse base2(float l) {
+  const float neg = -l * kLog2e, lo = fmaf(-l, kLog2e, -neg) - l * 1.92596299e-8f;   // log2 e - kLog2e
+  return {neg, fabsf(lo) < 1e-3f ? fmaf(lo, 0.69314718f, 1.f) : 1.f};
+}
+
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -61,7 +71,7 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
 // -inf: the query does not count).
 struct Queries {
   uint4 x[4];
-  float neg;
+  Lse lse;
 };
 
 __global__ void __launch_bounds__(kWarps * 32, 2) weigh_kernel(const __grid_constant__ WeighParams p) {
@@ -113,13 +123,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) weigh_kernel(const __grid_cons
       const int r = r0 + n;
 #pragma unroll
       for (int j = 0; j < 4; ++j) q.x[j] = make_uint4(0, 0, 0, 0);
-      q.neg = -INFINITY;
+      q.lse = {-INFINITY, 1.f};
       if (r < total) {
         const float l = p.lse[lse_at[r]];
         const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at[r]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) q.x[j] = row[4 * j + t];
-        q.neg = l == -INFINITY ? l : -l * kLog2e;
+        q.lse = base2(l);
+        if (l == -INFINITY) q.lse.neg = l;
       }
       return q;
     };
@@ -138,14 +149,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) weigh_kernel(const __grid_cons
           mma(d[i], u.z, v.z, u.w, v.w, q.x[j].z, q.x[j].w);
         }
       // columns 2 t and 2 t + 1 are the queries of lanes 8 t and 8 t + 4
-      const float n0 = __shfl_sync(0xffffffffu, q.neg, 8 * t), n1 = __shfl_sync(0xffffffffu, q.neg, 8 * t + 4);
+      const float n0 = __shfl_sync(0xffffffffu, q.lse.neg, 8 * t), n1 = __shfl_sync(0xffffffffu, q.lse.neg, 8 * t + 4);
+      const float f0 = __shfl_sync(0xffffffffu, q.lse.rest, 8 * t), f1 = __shfl_sync(0xffffffffu, q.lse.rest, 8 * t + 4);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float w0 = n0 == -INFINITY ? 0.f : ex2(fmaf(d[i][2 * k], p.scale2, n0));
           const float w1 = n1 == -INFINITY ? 0.f : ex2(fmaf(d[i][2 * k + 1], p.scale2, n1));
-          sum[2 * i + k] += w0 + w1;
+          sum[2 * i + k] += fmaf(w0, f0, w1 * f1);
         }
     }
   }
@@ -188,7 +200,7 @@ struct WideShared {
   int fail, next;                                 // next: first query row behind the chunk's
   int counts[kSumWarps];
   long long at[kChunk];                           // where the chunk's query rows lie in q,
-  alignas(16) float neg[kChunk];                  // and their log-sum-exps, base 2, negative
+  alignas(16) float neg[kChunk], rest[kChunk];    // and their log-sum-exps
   float sums[2][3][kTile];
 };
 constexpr int kWideSmem = (kKeyRing + kChunk / kTile) * kTileBytes + (int)sizeof(WideShared);
@@ -231,7 +243,9 @@ __device__ int lay_queries(const WeighParams& p, WideShared& sh, uint32_t rows, 
     const int i = before + __popc(mine & ((1u << lane) - 1));
     if (i < kChunk) {
       sh.at[i] = at;
-      sh.neg[i] = -l * kLog2e;
+      const Lse x = base2(l);
+      sh.neg[i] = x.neg;
+      sh.rest[i] = x.rest;
       if (i == kChunk - 1) sh.next = c + 1;
     }
   }
@@ -371,20 +385,21 @@ __global__ void __launch_bounds__(kWideThreads, 1) weigh_wide_kernel(const __gri
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&sh.s_empty[buf]);
-            const float4* neg = reinterpret_cast<const float4*>(&sh.neg[j * kTile + group * 32]);
+            const int c0 = j * kTile + group * 32;
+            const float4 *neg = reinterpret_cast<const float4*>(&sh.neg[c0]), *rest = reinterpret_cast<const float4*>(&sh.rest[c0]);
             uint64_t acc[2] = {0ull, 0ull};
             if (columns >= 32) {
 #pragma unroll
               for (int q = 0; q < 32; q += 4) {
-                const float4 n = neg[q / 4];
-                acc[0] = add_f32x2(acc[0], ex2_f32x2(fma_f32x2(pack_f32x2(x[q], x[q + 1]), sc2, pack_f32x2(n.x, n.y))));
-                acc[1] = add_f32x2(acc[1], ex2_f32x2(fma_f32x2(pack_f32x2(x[q + 2], x[q + 3]), sc2, pack_f32x2(n.z, n.w))));
+                const float4 n = neg[q / 4], f = rest[q / 4];
+                acc[0] = fma_f32x2(ex2_f32x2(fma_f32x2(pack_f32x2(x[q], x[q + 1]), sc2, pack_f32x2(n.x, n.y))), pack_f32x2(f.x, f.y), acc[0]);
+                acc[1] = fma_f32x2(ex2_f32x2(fma_f32x2(pack_f32x2(x[q + 2], x[q + 3]), sc2, pack_f32x2(n.z, n.w))), pack_f32x2(f.z, f.w), acc[1]);
               }
             } else if (columns > 0) {             // (what lies behind them may be anything)
 #pragma unroll
               for (int q = 0; q < 32; q += 2) {
-                const float e = ex2(fmaf(x[q], w.scale2, sh.neg[j * kTile + group * 32 + q]));
-                const float f = ex2(fmaf(x[q + 1], w.scale2, sh.neg[j * kTile + group * 32 + q + 1]));
+                const float e = ex2(fmaf(x[q], w.scale2, sh.neg[c0 + q])) * sh.rest[c0 + q];
+                const float f = ex2(fmaf(x[q + 1], w.scale2, sh.neg[c0 + q + 1])) * sh.rest[c0 + q + 1];
                 acc[0] = add_f32x2(acc[0], pack_f32x2(q < columns ? e : 0.f, q + 1 < columns ? f : 0.f));
               }
             }

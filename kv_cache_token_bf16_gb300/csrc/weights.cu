@@ -35,12 +35,13 @@ constexpr int kRing = 3, kUnits = 2;
 constexpr int kSumWarps = 16;
 constexpr int kReaders = kSumWarps + 3;           // warps that read a unit: summing, issuing, loading log-sum-exps
 constexpr int kMmaWarp = 16, kTmaWarp = 18, kThreads = 640;
-constexpr int kEntry = 3, kMinSteps = 8;
-// Units go uncut in planes of this many rows (too short to share), and where every SM has this many: then nothing is
-// joined, and CTAs take units as they come to them. (us, uncut and cut: a window of 64 tokens, 8 x 8192, 32 / 8 heads, 13
-// units an SM, 41 and 46; 64 sequences of up to 1021 tokens, 14 an SM, 135 and 145; 24, 32 / 16 heads, 7 an SM, 72 and 80;
-// 32 / 8 heads, 3.5 an SM, 77 and 75.)
-constexpr int kWholeRows = 1024, kWholeRounds = 5;
+constexpr int kEntry = 3, kMinSteps = 4;
+// Units of few steps go uncut (too short to share), and all where every SM has this many: then nothing is joined, and
+// CTAs take units as they come to them. (us, uncut and cut: windows of 64 tokens, 8192, 28 / 4 heads, 10 and 13; of 256,
+// 4000, 32 / 8 heads, 14 and 18; units of 32 steps, 446 tokens, 16 / 2 heads, 35 and 13. Of many steps, 64 sequences of
+// up to 1021 tokens, 32 / 8 heads, 14 units an SM, 135 and 145; 24, 32 / 16 heads, 7 an SM, 72 and 80; 32 / 8 heads, 3.5
+// an SM, 77 and 75.)
+constexpr int kWholeSteps = 8, kWholeRounds = 5;
 
 // The first query that counts for the keys from key0 on.
 __device__ __forceinline__ int first_query(int last, int key0, int len) { return max(key0, last ? len - last : 0); }
@@ -478,7 +479,7 @@ int step_tokens(const evict_prompt* a) {
 int make_plan(const evict_prompt* a, PromptPlan* plan) {
   const int group = a->q.heads / a->k.heads, tokens = step_tokens(a), heads = kTile / tokens, head_steps = (group + heads - 1) / heads;
   const long long most = (long long)head_steps * (((long long)(a->last > 0 ? std::min(a->last, a->m) : a->m) + tokens - 1) / tokens);
-  const int rc = plan_prompt(a, kKeys, most, kEntry, kMinSteps, kWholeRows, kWholeRounds, 0, 2 * kKeys * sizeof(float), false, plan);
+  const int rc = plan_prompt(a, kKeys, most, kEntry, kMinSteps, most <= kWholeSteps ? 0 : kWholeRounds, 0, 2 * kKeys * sizeof(float), false, plan);
   PromptParams& p = plan->p;
   p.last = a->last;
   p.half = tokens;
@@ -497,7 +498,10 @@ extern "C" int evict_prompt_weights_workspace(const evict_prompt* a, size_t* byt
   if (!bytes) return fail(EVICT_EINVAL, "bytes is NULL");
   PromptPlan plan;
   int rc;
-  if ((rc = check_prompt_sizes(a)) || (rc = make_plan(a, &plan))) return rc;
+  if ((rc = check_prompt_sizes(a))) return rc;
+  evict_prompt all = *a;                          // a window needs no more
+  all.last = 0;
+  if ((rc = make_plan(&all, &plan))) return rc;
   *bytes = plan.bytes;
   return EVICT_OK;
 }

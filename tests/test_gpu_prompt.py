@@ -350,3 +350,47 @@ def test_uncut_units_of_windows_take_the_workspace_of_any_window():
                   lse.data_ptr(), 0, 0, 0, last, 0.0, 0, 0, 0, 0)
         sizes.add(binding.evict_prompt_weights_workspace(binding.EvictPrompt.from_buffer_copy(prompt._PROMPT.pack(*fields))))
     assert len(sizes) == 1
+
+
+def test_units_that_ctas_take_as_they_come():
+    # which CTA takes which unit changes from run to run: no result does, nor those of a graph or of two calls at once
+    lens = [700, 1, 0, 1300, 64, 513, 1022, 400, 900, 77]
+    starts = starts_of(lens)
+    m = starts[-1]
+    pk = prompt.Packing(torch.tensor(starts, dtype=torch.int32).cuda())
+    args = [(rows(96 + i, 1, 32, m, std=1.5), rows(98 + i, 1, 8, m), rows(100 + i, 1, 8, m)) for i in range(2)]
+
+    def call(i, out=None, lse=None, w=None):
+        q, k, v = args[i]
+        lse = torch.empty(1, 32, m, device="cuda") if lse is None else lse
+        out = prompt.attention(q, k, v, pk, out=out, lse=lse)
+        return out, lse, prompt.weights(q, k, lse, pk, out=w)
+
+    ref = [call(i) for i in range(2)]
+    for i, (q, k, v) in enumerate(args):
+        spans = spans_of(starts, 1, m)
+        check_prompt(q, k, v, spans, *ref[i][:2])
+        check_weights(ref[i][2], *weights64(q, k, ref[i][1], spans))
+    same = lambda a, b: all(torch.equal(x, y) for x, y in zip(a, b))  # noqa: E731
+    for _ in range(4):
+        assert same(call(0), ref[0])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((i, call(i)))
+    torch.cuda.synchronize()
+    assert all(same(x, ref[i]) for i, x in got)
+    del got
+    held = [torch.zeros_like(x) for x in ref[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(0, *held)
+    for _ in range(3):
+        for x in held:
+            x.zero_()
+        graph.replay()
+        assert same(held, ref[0])
+    pk.sync()
