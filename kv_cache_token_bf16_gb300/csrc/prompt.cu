@@ -14,6 +14,15 @@
 // Warp 10 fetches (TMA): K and V through a ring of five 32 KB tiles of 128 rows, the queries of the next
 // unit as soon as the last product that reads a tile is through. Warp 11 clears rows of V that only some
 // of the unit's queries see, or none (see scrub).
+//
+// What bounds it: a half step of both groups is 1,280 clocks of the tensor cores (logits in halves of 64 columns take
+// 48 clocks a product instead of 32) and takes 1,450; beginning and leaving a unit takes 5,300, of which 3,000 are the
+// stores of its 64 KB. 8192 tokens with 28 / 4 heads 340 us (1.41 PFLOP/s of 1.90); 4 x 2048 with 40 / 8 149 us (1.15);
+// 24 sequences of up to 1021 tokens with 32 / 8 117 us (0.76), 45 tokens 8.6 us.
+// Tried and taken back: logits of 128 columns at once (518 us for the 8192 tokens, with a lone thread issuing), masked
+// and unmasked exponentials apart (10-20 % more on short prompts: instruction cache), the second group a step behind
+// the first (no gain), rows stored 128 bytes by four lanes (packed 124 instead of 129 at the time, but short prompts
+// 9.0 instead of 8.7 and the batch as before), a ring of four tiles (3-6 % more).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -49,10 +58,10 @@ constexpr int kEntry = 2, kMinSteps = 4;
 // count to 0): dealt out by their number, 24 sequences of up to 1021 tokens took 130 us instead of 117, 4 x 2048 171
 // instead of 150, 3 sequences of up to 2000 71 instead of 56.
 // Units go uncut in planes of this many rows (too short to share), and where there is one for every SM: then nothing is
-// joined. (us, uncut and cut, of one sequence: 1021 tokens, 16 / 2 heads, 20 and 26; 1500, 26 and
-// 30; 2000, 8 / 1 heads, 33 and 29; 4000, 8 / 1 heads, 0.8 units an SM,
-// 57 and 46; 2900, 16 / 2 heads, 1.2 an SM, 44 and 51; 2000, 28 / 4 heads, 1.5 an SM, 34 and 48; 8192, 28 / 4 heads, 6 an
-// SM, 343 and 352. 24 of up to 1021 tokens, 32 / 8 heads, 12 an SM, 117 and 135; 4 x 2048, 40 / 8 heads, 150 and 168.)
+// joined. (us, uncut and cut, of one sequence: 1021 tokens, 16 / 2 heads, 20 and 26; 1500, 26 and 30; 2000, 8 / 1 heads,
+// 33 and 29; 4000, 8 / 1 heads, 0.8 units an SM, 57 and 46; 2900, 16 / 2 heads, 1.2 an SM, 44 and 51; 2000, 28 / 4 heads,
+// 1.5 an SM, 34 and 48; 8192, 28 / 4 heads, 6 an SM, 343 and 352. 24 of up to 1021 tokens, 32 / 8 heads, 12 an SM, 117
+// and 135; 4 x 2048, 40 / 8 heads, 9 an SM, 150 and 168.)
 constexpr int kWholeRows = 1536, kWholeRounds = 1, kTakenRounds = 2;
 
 struct Steps {

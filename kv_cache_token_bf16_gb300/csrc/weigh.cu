@@ -9,9 +9,9 @@
 // Where there are fewer warps of keys than the GPU has room for, the queries are dealt out to up to eight warps for
 // the same keys. 320 queries over 16384 rows were bound by these products (65 us).
 // Many (weigh_wide_kernel): the large products of the tensor cores, bound by HBM up to about a hundred queries and by
-// the exponentials behind that: 8 heads' 16384 rows by 64 queries 10.9 us, by 320 23.4, by 1024 54.5 (a third, a half
-// and two thirds of what their bytes and exponentials, at 32 a clock and SM, would allow; the rest is the launch and
-// the laying out of the queries, once a chunk).
+// the exponentials behind that: 8 heads' 16384 rows by 64 queries 10.9 us (3.1 TB/s), by 320 22.4, by 1024 52.6 (0.65
+// PFLOP/s; their exponentials, at 32 a clock and SM, are 14 us). The rest is the launch and the laying out of the
+// queries, some 3 us once a chunk, in which nothing else runs.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

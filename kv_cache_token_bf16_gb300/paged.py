@@ -330,6 +330,8 @@ def weigh_rows(cache, q, lse, n_new=None, scale=None):
     """``EvictCache.weigh`` without its order between streams."""
     if _torch is None:
         _load()
+    if lse is None:
+        raise ValueError("lse must be given")
     if _recording() and (q.requires_grad or lse.requires_grad):
         _no_history()
     index, shape = _device(q), q.shape
@@ -341,8 +343,6 @@ def weigh_rows(cache, q, lse, n_new=None, scale=None):
         scale = 0.0
     elif scale == 0:
         raise ValueError("scale must not be 0")
-    if lse is None:
-        raise ValueError("lse must be given")
     _call(index, _calls.evict_weigh, cache.handle, qr, batch, m, _like(lse, "lse", (batch, hq, m), _torch.float32, index),
           _like(n_new, "n_new", (batch,), _torch.int32, index) or None, scale, _stream(index))
 

@@ -159,6 +159,8 @@ def weights(q, k, lse, packing: Packing | None = None, last: int = 0, scale=None
     if _calls is None:
         _load()
     torch = paged._torch
+    if lse is None:
+        raise ValueError("lse must be given")
     if paged._recording() and (q.requires_grad or k.requires_grad or lse.requires_grad or
                                (out is not None and out.requires_grad)):
         paged._no_history()
@@ -167,8 +169,6 @@ def weights(q, k, lse, packing: Packing | None = None, last: int = 0, scale=None
         raise ValueError(f"last must be >= 0, not {last}")
     qr = paged._rows(q, "q", index, torch.bfloat16, batch, m)
     kr = paged._rows(k, "k", index, torch.bfloat16, batch, m)
-    if lse is None:
-        raise ValueError("lse must be given")
     lse_at = paged._like(lse, "lse", (batch, hq, m), torch.float32, index)
     if out is None:
         make = torch.empty if packing is None else torch.zeros

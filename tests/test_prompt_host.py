@@ -118,3 +118,13 @@ def test_tensors_of_the_cpu_or_with_a_gradient_are_refused(lib):
         prompt.Packing(torch.zeros(3))
     with pytest.raises(ValueError, match="CUDA"):
         prompt.Packing(torch.zeros(3, dtype=torch.int32))
+
+
+def test_weights_want_log_sum_exps(lib):
+    torch = pytest.importorskip("torch")
+    from kv_cache_token_bf16_gb300 import paged, prompt
+    x = torch.zeros(1, 1, 1, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="lse must be given"):
+        prompt.weights(x, x, None)
+    with pytest.raises(ValueError, match="lse must be given"):
+        paged.weigh_rows(None, x, None)
