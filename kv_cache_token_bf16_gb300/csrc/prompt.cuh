@@ -157,8 +157,8 @@ __device__ __forceinline__ bool settle(PromptCursor& c, int step) {
   return true;
 }
 
-// On to the next unit; false at the share's end. (This and first_unit look a block up in one place each: at a
-// kernel's start its code comes from memory, some 6,000 clocks for 25 KB of it.)
+// On to the next unit; false at the share's end. (Blocks are looked up at few places, and uncut units without the search
+// for a share: at a kernel's start its code comes from memory, some 6,000 clocks for 25 KB of it.)
 template <typename Steps>
 __device__ __forceinline__ bool next_unit(const PromptWork& w, PromptCursor& c, Steps steps) {
   int e = c.e;
@@ -189,25 +189,34 @@ __device__ __forceinline__ bool first_unit(const PromptWork& w, PromptScan& sh, 
   Tables t;
   c.blocks = count_blocks<kThreads>(w, sh, scratch, t);
   tc::fence_proxy_async_smem();                   // of `scratch`, for the copies to come
-  const int tid = threadIdx.x, per = (c.blocks + kThreads - 1) / kThreads, units = c.blocks * w.hkv;
+  if (w.whole) {
+    const int unit = whole_unit(w, c.blocks * w.hkv, 0);
+    if (unit < 0) return false;                   // the whole CTA, here and below
+    c.round = 0;
+    c.e = w.by_hkv.div(unit);
+    c.h = unit - c.e * w.hkv;
+    c.k = block_of(w, t, c.e, steps);
+    c.from = 0;
+    c.to = c.k.steps;
+    return true;
+  }
+  const int tid = threadIdx.x, per = (c.blocks + kThreads - 1) / kThreads;
   const int e0 = min(tid * per, c.blocks), e1 = min(e0 + per, c.blocks);
   Shares shares;
-  const int first = w.whole ? whole_unit(w, units, 0) : 0, at_block = w.by_hkv.div(max(first, 0));
   int base = 0, g0 = 0;
-  // the sums of the steps, unless units are not cut; then the block where the share begins
+  // the sums of the steps; then the block where the share begins
 #pragma unroll 1
-  for (int find = w.whole; find < 2; ++find) {
+  for (int find = 0; find < 2; ++find) {
     if (find) {
-      if (!w.whole && (int)blockIdx.x >= shares.count) return false;   // the whole CTA, here and below
-      if (first < 0) return false;
-      g0 = w.whole ? 0 : shares.begin(blockIdx.x);
+      if ((int)blockIdx.x >= shares.count) return false;
+      g0 = shares.begin(blockIdx.x);
     }
     int at = base;
 #pragma unroll 1
     for (int e = e0; e < e1; ++e) {
       const PromptBlock k = block_of(w, t, e, steps);
       const int of_block = (k.steps + w.entry) * w.hkv;
-      if (find && (w.whole ? e == at_block : g0 >= at && g0 < at + of_block)) {
+      if (find && g0 >= at && g0 < at + of_block) {
         sh.e = e;
         sh.rest = g0 - at;
         sh.k = k;
@@ -227,13 +236,6 @@ __device__ __forceinline__ bool first_unit(const PromptWork& w, PromptScan& sh, 
   __syncthreads();
   c.e = sh.e;
   c.k = sh.k;
-  if (w.whole) {
-    c.round = 0;
-    c.h = first - c.e * w.hkv;
-    c.from = 0;
-    c.to = c.k.steps;
-    return true;
-  }
   const int unit = c.k.steps + w.entry;
   c.h = sh.rest / unit;
   c.left = shares.begin(blockIdx.x + 1) - g0;
