@@ -17,8 +17,8 @@
 //
 // What bounds it: a half step of both groups is 1,280 clocks of the tensor cores (logits in halves of 64 columns take
 // 48 clocks a product instead of 32) and takes 1,450; beginning and leaving a unit takes 5,300, of which 3,000 are the
-// stores of its 64 KB. 8192 tokens with 28 / 4 heads 340 us (1.41 PFLOP/s of 1.90); 4 x 2048 with 40 / 8 149 us (1.15);
-// 24 sequences of up to 1021 tokens with 32 / 8 117 us (0.76), 45 tokens 8.6 us.
+// stores of its 64 KB. 8192 tokens with 28 / 4 heads 340 us (1.41 PFLOP/s of 1.90); 4 x 2048 with 40 / 8 148 us (1.16);
+// 24 sequences of up to 1021 tokens with 32 / 8 116 us (0.77), 45 tokens 8.2 us.
 // Tried and taken back: logits of 128 columns at once (518 us for the 8192 tokens, with a lone thread issuing), masked
 // and unmasked exponentials apart (10-20 % more on short prompts: instruction cache), the second group a step behind
 // the first (no gain), rows stored 128 bytes by four lanes (packed 124 instead of 129 at the time, but short prompts
@@ -63,6 +63,8 @@ constexpr int kEntry = 2, kMinSteps = 4;
 // 1.5 an SM, 34 and 48; 8192, 28 / 4 heads, 6 an SM, 343 and 352. 24 of up to 1021 tokens, 32 / 8 heads, 12 an SM, 117
 // and 135; 4 x 2048, 40 / 8 heads, 9 an SM, 150 and 168.)
 constexpr int kWholeRows = 1536, kWholeRounds = 1, kTakenRounds = 2;
+// Weights' units of so many sequences are put in order: each block looks through all of them.
+constexpr int kOrderedSeqs = 256;
 
 struct Steps {
   int tile;
@@ -777,6 +779,10 @@ int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry
   w.taken = w.whole && blocks * w.hkv > kTakenRounds * P.sms ? w.total + 2 : nullptr;
   w.begin = reinterpret_cast<PromptBegin*>(take(P.sms * sizeof(PromptBegin)));
   w.block_base = reinterpret_cast<int*>(take(((size_t)w.seqs + 1) * sizeof(int)));
+  if (w.starts && w.seqs <= kOrderedSeqs && !longest_last) {
+    int* order = reinterpret_cast<int*>(take(blocks * sizeof(int)));   // (taken or not: `last` does not change the bytes)
+    if (w.taken) w.order = order;
+  }
   p.part_ml = reinterpret_cast<float2*>(take(w.whole ? 0 : P.sms * part_ml));
   p.part = reinterpret_cast<float*>(take(w.whole ? 0 : P.sms * part));
   P.bytes = off;
@@ -795,6 +801,7 @@ int bind_prompt(const evict_prompt* a, PromptPlan* plan) {
   rebase(p.work.begin);
   if (p.work.taken) p.work.taken = p.work.total + 2;
   rebase(p.work.block_base);
+  if (p.work.order) rebase(p.work.order);
   rebase(p.part_ml);
   rebase(p.part);
   p.work.err = a->error ? a->error : reinterpret_cast<int*>(base);

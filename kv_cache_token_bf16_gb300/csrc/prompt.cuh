@@ -157,6 +157,32 @@ __device__ __forceinline__ bool settle(PromptCursor& c, int step) {
   return true;
 }
 
+// Block of a whole unit.
+__device__ __forceinline__ int whole_block(const PromptWork& w, int unit) {
+  const int e = w.by_hkv.div(unit);
+  return w.order ? w.order[e] : e;
+}
+
+// Blocks by their number in their sequence, all sequences' first ones first: where a sequence's first blocks have the
+// most steps, long units then come early and the last ones taken are short. All threads.
+template <int kThreads, typename Steps>
+__device__ __forceinline__ void order_blocks(const PromptWork& w, const Tables& t, int blocks, Steps steps) {
+#pragma unroll 1
+  for (int e = threadIdx.x; e < blocks; e += kThreads) {
+    const PromptBlock k = block_of(w, t, e, steps);
+    int at = 0;                                   // blocks before: of lower number, and of the same one
+    int base = 0;
+#pragma unroll 4
+    for (int s = 0; s < w.seqs; ++s) {
+      const int next = s + 1 < w.seqs ? t.base[s + 1] : blocks, n = next - base;
+      at += min(n, k.tile) + (s < k.s && n > k.tile);
+      base = next;
+    }
+    w.order[at] = e;
+  }
+  __syncthreads();
+}
+
 // On to the next unit; false at the share's end. (Blocks are looked up at few places, and uncut units without the search
 // for a share: at a kernel's start its code comes from memory, some 6,000 clocks for 25 KB of it.)
 template <typename Steps>
@@ -165,8 +191,8 @@ __device__ __forceinline__ bool next_unit(const PromptWork& w, PromptCursor& c, 
   if (w.whole) {
     const int unit = whole_unit(w, c.blocks * w.hkv, ++c.round);
     if (unit < 0) return false;
-    e = w.by_hkv.div(unit);
-    c.h = unit - e * w.hkv;
+    e = whole_block(w, unit);
+    c.h = unit - w.by_hkv.div(unit) * w.hkv;
   } else {
     c.left -= c.to - c.from;
     if (c.left <= 0) return false;
@@ -190,11 +216,12 @@ __device__ __forceinline__ bool first_unit(const PromptWork& w, PromptScan& sh, 
   c.blocks = count_blocks<kThreads>(w, sh, scratch, t);
   tc::fence_proxy_async_smem();                   // of `scratch`, for the copies to come
   if (w.whole) {
+    if (w.order) order_blocks<kThreads>(w, t, c.blocks, steps);
     const int unit = whole_unit(w, c.blocks * w.hkv, 0);
     if (unit < 0) return false;                   // the whole CTA, here and below
     c.round = 0;
-    c.e = w.by_hkv.div(unit);
-    c.h = unit - c.e * w.hkv;
+    c.e = whole_block(w, unit);
+    c.h = unit - w.by_hkv.div(unit) * w.hkv;
     c.k = block_of(w, t, c.e, steps);
     c.from = 0;
     c.to = c.k.steps;

@@ -33,6 +33,7 @@ struct PromptWork {
   PromptBegin* begin;                // [CTAs]
   int* total;                        // [3] steps of all units, the shares' number; units taken
   int* taken;                        // whole: units taken beyond the CTAs' first ones; or NULL
+  int* order;                        // [blocks] whole: the blocks in the order in which units are taken; or NULL
   int* err;
 };
 

@@ -16,7 +16,7 @@
 // What bounds it: a step is 1,024 clocks of the tensor cores and as many of exponentials (at 32 a clock and SM) and
 // takes some 1,750: tensor memory holds no more than the four accumulators, whose products come one after the other,
 // 512 clocks each. 8192 tokens with 28 / 4 heads 183 us (1.31 PFLOP/s of 1.90); 24 sequences of up to 1021 tokens with
-// 32 / 8 heads 75 us, of which 23 would be the products of what queries see: tiles at the diagonal, and their masks;
+// 32 / 8 heads 68 us, of which 23 would be the products of what queries see: tiles at the diagonal, and their masks;
 // windows of 64 tokens of 8 x 8192 41 us, 3.3 TB/s.
 // Tried and taken back: K in tensor memory (214 us), 64 columns at a time (190 -> 196), chunks of a masked step that no
 // query or every one sees left out or unmasked (packed no gain, 8192 tokens 200).
@@ -46,11 +46,12 @@ constexpr int kReaders = kSumWarps + 3;           // warps that read a unit: sum
 constexpr int kMmaWarp = 16, kTmaWarp = 18, kThreads = 640;
 constexpr int kEntry = 3, kMinSteps = 4;
 // Units of few steps go uncut (too short to share), and all where every SM has this many: then nothing is joined, and
-// CTAs take units as they come to them. (us, uncut and cut: windows of 64 tokens, 8192, 28 / 4 heads, 10 and 13; of 256,
-// 4000, 32 / 8 heads, 14 and 18; units of 32 steps, 446 tokens, 16 / 2 heads, 35 and 13. Of many steps, 64 sequences of
-// up to 1021 tokens, 32 / 8 heads, 14 units an SM, 135 and 145; 24, 32 / 16 heads, 7 an SM, 72 and 80; 32 / 8 heads, 3.5
-// an SM, 77 and 75.)
-constexpr int kWholeSteps = 8, kWholeRounds = 5;
+// CTAs take units as they come to them, in an order in which the long ones are early. (us, uncut and cut: windows of 64
+// tokens, 8192, 28 / 4 heads, 10 and 13; of 256, 4000, 32 / 8 heads, 14 and 18; units of 32 steps, 446 tokens, 16 / 2
+// heads, 35 and 13. Of many steps, 64 sequences of up to 1021 tokens, 32 / 8 heads, 14 units an SM, 131 and 145; 24,
+// 32 / 16 heads, 7 an SM, 69 and 80; 32 / 8 heads, 3.5 an SM, 68 and 75, in the sequences' order 77; 8 of up to 4000,
+// 2.5 an SM, 99 and 93.)
+constexpr int kWholeSteps = 8, kWholeRounds = 3;
 
 // The first query that counts for the keys from key0 on.
 __device__ __forceinline__ int first_query(int last, int key0, int len) { return max(key0, last ? len - last : 0); }

@@ -394,3 +394,21 @@ def test_units_that_ctas_take_as_they_come():
         graph.replay()
         assert same(held, ref[0])
     pk.sync()
+
+
+# weights' units that go uncut, in the order of the blocks' numbers (up to 256 sequences) and in the sequences'
+@pytest.mark.parametrize("lens", [[700, 1, 0, 1300, 64, 513, 1022, 400, 900, 77], [30, 0, 257] * 100, [1500, 1400, 0, 0, 1300, 800]])
+def test_weights_units_that_ctas_take_as_they_come(lens):
+    starts = starts_of(lens, 1)
+    m = starts[-1] + 3
+    pk = prompt.Packing(torch.tensor(starts, dtype=torch.int32).cuda())
+    q, k = rows(110, 1, 16, m, std=1.5), rows(111, 1, 16, m)
+    lse = torch.randn(1, 16, m, device="cuda", generator=torch.Generator("cuda").manual_seed(112)) + 5.0
+    w = torch.full((1, 16, m), 3.0, device="cuda")
+    prompt.weights(q, k, lse, pk, out=w)
+    pk.sync()
+    check_weights(w, *weights64(q, k, lse, spans_of(starts, 1, m)), 3.0)
+    for _ in range(4):
+        again = torch.full_like(w, 3.0)
+        prompt.weights(q, k, lse, pk, out=again)
+        assert torch.equal(again, w)
