@@ -9,7 +9,7 @@
 // Where there are fewer warps of keys than the GPU has room for, the queries are dealt out to up to eight warps for
 // the same keys. 320 queries over 16384 rows were bound by these products (65 us).
 // Many (weigh_wide_kernel): the large products of the tensor cores, bound by HBM up to about a hundred queries and by
-// the exponentials behind that: 8 heads' 16384 rows by 64 queries 10.9 us (3.1 TB/s), by 320 22.4, by 1024 52.6 (0.65
+// the exponentials behind that: 8 heads' 16384 rows by 64 queries 10.9 us (3.1 TB/s), by 320 22.2, by 1024 52 (0.66
 // PFLOP/s; their exponentials, at 32 a clock and SM, are 14 us). The rest is the launch and the laying out of the
 // queries, some 3 us once a chunk, in which nothing else runs.
 #include <cuda_bf16.h>
@@ -187,21 +187,22 @@ __global__ void __launch_bounds__(kWarps * 32, 2) weigh_kernel(const __grid_cons
 
 // Many queries: the tensor cores' large products, in 128 keys by 128 queries, D[key, query] in tensor memory. A CTA
 // takes an equal share of the key tiles. Of a unit's queries it lays up to kChunk that count into shared memory
-// once, behind each other, and goes through its tiles of the unit by them; a warp sums 32 keys over 32 queries of
-// each product.
+// once, behind each other, and goes through its tiles of the unit by them; a warp sums 32 keys of every other tile over
+// 64 queries of each product. (Of every tile over 32, so that what it does once a product counts twice: 14.6 us instead
+// of 13.4 for some 190 queries over 8 heads' 16384 rows.)
 constexpr int kTile = 128, kTileBytes = kTile * kHeadDim * 2;
 constexpr int kChunk = 256, kKeyRing = 4, kBuffers = 4;
 constexpr int kSumWarps = 16, kIssueWarp = 16, kCopyWarp = 17, kWideThreads = 576;
 
 struct WideShared {
   uint64_t k_full[kKeyRing], k_empty[kKeyRing], s_full[kBuffers], s_empty[kBuffers], done;
-  uint64_t sums_full[4][2], sums_empty[4][2];     // of a quarter of the keys, of a tile
+  uint64_t sums_full[4][2], sums_empty[4][2];     // of a quarter of the keys, of every other tile
   uint32_t tmem_base;
   int fail, next;                                 // next: first query row behind the chunk's
   int counts[kSumWarps];
   long long at[kChunk];                           // where the chunk's query rows lie in q,
   alignas(16) float neg[kChunk], rest[kChunk];    // and their log-sum-exps
-  float sums[2][3][kTile];
+  float sums[2][kTile];
 };
 constexpr int kWideSmem = (kKeyRing + kChunk / kTile) * kTileBytes + (int)sizeof(WideShared);
 static_assert(kWideSmem <= 227 * 1024);
@@ -299,10 +300,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) weigh_wide_kernel(const __gri
     }
     for (int i = 0; i < kBuffers; ++i) {
       tc::mbar_init(&sh.s_full[i], 1);
-      tc::mbar_init(&sh.s_empty[i], kSumWarps);
+      tc::mbar_init(&sh.s_empty[i], kSumWarps / 2);
     }
     for (int i = 0; i < 8; ++i) {
-      tc::mbar_init(&sh.sums_full[i >> 1][i & 1], 3);
+      tc::mbar_init(&sh.sums_full[i >> 1][i & 1], 1);
       tc::mbar_init(&sh.sums_empty[i >> 1][i & 1], 1);
     }
     tc::mbar_init(&sh.done, 1);
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) weigh_wide_kernel(const __gri
   pdl_wait();
   const uint64_t kd = tc::sw128_desc(smem), qd = tc::sw128_desc(queries);
   const uint32_t hi = (uint32_t)(kd >> 32), k_lo = (uint32_t)kd, q_lo = (uint32_t)qd;
-  const int quarter = warp & 3, group = warp >> 2;
+  const int quarter = warp & 3, half = (warp >> 2) & 1, set = warp >> 3;
   const int end = (int)(p.all * (blockIdx.x + 1) / gridDim.x);
   int tiles = 0, steps = 0;                       // done by this warp's role: places in the rings
   bool ok = true;
@@ -366,59 +367,69 @@ __global__ void __launch_bounds__(kWideThreads, 1) weigh_wide_kernel(const __gri
         const uint64_t sc2 = pack_f32x2(w.scale2, w.scale2);
 #pragma unroll 1
         for (int t = first; t < last; ++t, ++tiles) {
+          if ((tiles & 1) != set) {
+            steps += blocks;
+            continue;
+          }
           const int row = t * kTile + key;
           float* to = w.score + (long long)unit * w.cap + row;
-          float was = 0.f, sum = 0.f;
-          if (group == 0 && row < w.rows) was = *to;
+          float was = 0.f;
+          if (half == 0 && row < w.rows) was = *to;
+          uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll 1
           for (int j = 0; j < blocks; ++j, ++steps) {
-            const int buf = steps % kBuffers, columns = total - j * kTile - group * 32;
+            const int buf = steps % kBuffers, columns = total - j * kTile - half * 64;
             // (a wait that gives up leaves `fail`)
             wait_for(&sh.s_full[buf], (steps / kBuffers) & 1, &sh.fail);
             __syncwarp();
             tc::fence_after_sync();
-            float x[32];
-            if (columns > 0) {
-              tm::load32(tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTile + group * 32, x);
-              tm::wait32(x);
-            }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sh.s_empty[buf]);
-            const int c0 = j * kTile + group * 32;
-            const float4 *neg = reinterpret_cast<const float4*>(&sh.neg[c0]), *rest = reinterpret_cast<const float4*>(&sh.rest[c0]);
-            uint64_t acc[2] = {0ull, 0ull};
-            if (columns >= 32) {
-#pragma unroll
-              for (int q = 0; q < 32; q += 4) {
-                const float4 n = neg[q / 4], f = rest[q / 4];
-                acc[0] = fma_f32x2(ex2_f32x2(fma_f32x2(pack_f32x2(x[q], x[q + 1]), sc2, pack_f32x2(n.x, n.y))), pack_f32x2(f.x, f.y), acc[0]);
-                acc[1] = fma_f32x2(ex2_f32x2(fma_f32x2(pack_f32x2(x[q + 2], x[q + 3]), sc2, pack_f32x2(n.z, n.w))), pack_f32x2(f.z, f.w), acc[1]);
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 32) {
+              float x[32];
+              if (columns > c) {
+                tm::load32(tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTile + half * 64 + c, x);
+                tm::wait32(x);
               }
-            } else if (columns > 0) {             // (what lies behind them may be anything)
-#pragma unroll
-              for (int q = 0; q < 32; q += 2) {
-                const float e = ex2(fmaf(x[q], w.scale2, sh.neg[c0 + q])) * sh.rest[c0 + q];
-                const float f = ex2(fmaf(x[q + 1], w.scale2, sh.neg[c0 + q + 1])) * sh.rest[c0 + q + 1];
-                acc[0] = add_f32x2(acc[0], pack_f32x2(q < columns ? e : 0.f, q + 1 < columns ? f : 0.f));
+              if (c || columns <= 32) {           // the last that is read
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&sh.s_empty[buf]);
               }
+              const int c0 = j * kTile + half * 64 + c;
+              const float4 *neg = reinterpret_cast<const float4*>(&sh.neg[c0]), *rest = reinterpret_cast<const float4*>(&sh.rest[c0]);
+              if (columns >= c + 32) {
+#pragma unroll
+                for (int q = 0; q < 32; q += 4) {
+                  const float4 n = neg[q / 4], f = rest[q / 4];
+                  acc[0] = fma_f32x2(ex2_f32x2(fma_f32x2(pack_f32x2(x[q], x[q + 1]), sc2, pack_f32x2(n.x, n.y))), pack_f32x2(f.x, f.y), acc[0]);
+                  acc[1] = fma_f32x2(ex2_f32x2(fma_f32x2(pack_f32x2(x[q + 2], x[q + 3]), sc2, pack_f32x2(n.z, n.w))), pack_f32x2(f.z, f.w), acc[1]);
+                }
+              } else if (columns > c) {           // (what lies behind them may be anything)
+#pragma unroll
+                for (int q = 0; q < 32; q += 2) {
+                  const float e = ex2(fmaf(x[q], w.scale2, sh.neg[c0 + q])) * sh.rest[c0 + q];
+                  const float f = ex2(fmaf(x[q + 1], w.scale2, sh.neg[c0 + q + 1])) * sh.rest[c0 + q + 1];
+                  acc[0] = add_f32x2(acc[0], pack_f32x2(c + q < columns ? e : 0.f, c + q + 1 < columns ? f : 0.f));
+                }
+              }
+              if (columns <= 32) break;
             }
-            float lo, up;
-            split_f32x2(add_f32x2(acc[0], acc[1]), lo, up);
-            sum += lo + up;
           }
-          // a key's four sums meet in the first warp of its quarter
-          const int slot = tiles & 1, parity = (tiles >> 1) & 1;
-          if (group) {
-            wait_for(&sh.sums_empty[quarter][slot], parity ^ 1, &sh.fail);
-            sh.sums[slot][group - 1][key] = sum;
+          float lo, up;
+          split_f32x2(add_f32x2(acc[0], acc[1]), lo, up);
+          float sum = lo + up;
+          // a key's two sums meet in the warp of the first half
+          const int parity = (tiles >> 1) & 1;
+          if (half) {
+            wait_for(&sh.sums_empty[quarter][set], parity ^ 1, &sh.fail);
+            sh.sums[set][key] = sum;
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sh.sums_full[quarter][slot]);
+            if (lane == 0) tc::mbar_arrive(&sh.sums_full[quarter][set]);
           } else {
-            wait_for(&sh.sums_full[quarter][slot], parity, &sh.fail);
-            for (int g = 0; g < 3; ++g) sum += sh.sums[slot][g][key];
+            wait_for(&sh.sums_full[quarter][set], parity, &sh.fail);
+            sum += sh.sums[set][key];
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&sh.sums_empty[quarter][slot]);
+            if (lane == 0) tc::mbar_arrive(&sh.sums_empty[quarter][set]);
             if (row < w.rows && !*(volatile int*)&sh.fail) *to = was + sum;
           }
         }
