@@ -22,7 +22,9 @@
 // Tried and taken back: logits of 128 columns at once (518 us for the 8192 tokens, with a lone thread issuing), masked
 // and unmasked exponentials apart (10-20 % more on short prompts: instruction cache), the second group a step behind
 // the first (no gain), rows stored 128 bytes by four lanes (packed 124 instead of 129 at the time, but short prompts
-// 9.0 instead of 8.7 and the batch as before), a ring of four tiles (3-6 % more).
+// 9.0 instead of 8.7 and the batch as before), results stored by a warpgroup of its own while the groups go on (8192
+// tokens 333 instead of 337, packed 120 instead of 116, 64 sequences of up to 512 100 instead of 91), a ring of four
+// tiles (3-6 % more).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

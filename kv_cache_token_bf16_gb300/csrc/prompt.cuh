@@ -135,7 +135,7 @@ struct PromptCursor {
   int round;                         // whole: units before
 };
 
-// Whole units: the CTA's unit of this round; negative where there is none. The longest units come first. Either a CTA
+// Whole units: the CTA's unit of this turn; negative where there is none. The longest units come first. Either a CTA
 // takes the next one when it comes to it (who takes which changes no result), or every other round goes the other way
 // round the CTAs, so that their sums are nearly equal.
 __device__ __forceinline__ int whole_unit(const PromptWork& w, int units, int round) {
