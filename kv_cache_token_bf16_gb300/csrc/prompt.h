@@ -37,6 +37,8 @@ struct PromptWork {
   int* err;
 };
 
+constexpr float kLog2eRest = 1.92596299e-8f;       // log2 e beyond its fp32 value
+
 // scale * log2 e (0: 1 / sqrt(128)), a little more. The tensor cores cut each of a logit's eight partial sums toward
 // zero: logits of 10 .. 20 of random rows lost 0.9e-7 of themselves in the mean, of a row with itself 1.4e-7 .. 2.3e-7,
 // and sums of weights add that up. 2^-23 makes up for it: a prompt's weights of keys (8192 tokens, 28 heads) were

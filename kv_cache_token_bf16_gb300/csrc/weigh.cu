@@ -56,7 +56,7 @@ struct Lse {
   float neg, rest;
 };
 __device__ __forceinline__ Lse base2(float l) {
-  const float neg = -l * kLog2e, lo = fmaf(-l, kLog2e, -neg) - l * 1.92596299e-8f;   // log2 e - kLog2e
+  const float neg = -l * kLog2e, lo = fmaf(-l, kLog2e, -neg) - l * kLog2eRest;
   return {neg, fabsf(lo) < 1e-3f ? fmaf(lo, 0.69314718f, 1.f) : 1.f};
 }
 
