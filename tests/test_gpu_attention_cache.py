@@ -439,3 +439,22 @@ def test_a_captured_step_of_many_queries():
     w2, b2 = weigh64(zero, k, q, lse, None, SCALE)
     check_weights(got, w1 + 2 * w2, b1 + 2 * b2 + 6 * U32 * (w1 + 2 * w2))
     cache.close()
+
+
+@pytest.mark.parametrize("m", [1, 8])
+def test_offsets_past_32_bits(m):
+    # 2.3e9 elements of kept keys, by few queries (the register products) and by more; the last caches' rows
+    B, H, hq, n = 64, 8, 32, 35001
+    assert B * H * n * D > 2 ** 31
+    g = torch.Generator("cuda").manual_seed(130)
+    k = torch.randn(B, H, n, D, device="cuda", generator=g, dtype=torch.bfloat16)
+    cache = binding.EvictCache("attention", B, H, budget=n, n_sink=0, max_block=1)
+    cache.set_state(k, k, torch.arange(n, device="cuda").int().expand(B, H, n).contiguous(), torch.zeros(B, H, n, device="cuda"))
+    q = rows(131, B, hq, m)
+    lse = torch.randn(B, hq, m, device="cuda", generator=g) + 10.0
+    cache.weigh(q, lse)
+    cache.sync()
+    for b in (0, 60, 63):
+        zero = torch.zeros(1, H, n, device="cuda")
+        check_weights(cache.view()[3][b:b + 1], *weigh64(zero, k[b:b + 1], q[b:b + 1], lse[b:b + 1], None, SCALE))
+    cache.close()

@@ -412,3 +412,24 @@ def test_weights_units_that_ctas_take_as_they_come(lens):
         again = torch.full_like(w, 3.0)
         prompt.weights(q, k, lse, pk, out=again)
         assert torch.equal(again, w)
+
+
+def test_offsets_past_32_bits():
+    # 2.5e9 elements of q and out; the last sequences against calls of their own
+    lens = [1000] * 610 + [333, 1, 777]
+    starts = starts_of(lens)
+    m = starts[-1]
+    assert m * 32 * D > 2 ** 31
+    g = torch.Generator("cuda").manual_seed(120)
+    q = torch.randn(1, m, 32, D, device="cuda", generator=g, dtype=torch.bfloat16).transpose(1, 2)
+    k, v = (torch.randn(1, m, 8, D, device="cuda", generator=g, dtype=torch.bfloat16).transpose(1, 2) for _ in range(2))
+    pk = prompt.Packing(torch.tensor(starts, dtype=torch.int32).cuda())
+    lse = torch.empty(1, 32, m, device="cuda")
+    out = prompt.attention(q, k, v, pk, lse=lse)
+    w = prompt.weights(q, k, lse, pk)
+    pk.sync()
+    for i in (0, 500, 609, 610, 611, 612):
+        a, b = starts[i], starts[i + 1]
+        x = [t[:, :, a:b].contiguous() for t in (q, k, v, out, lse)]
+        check_prompt(*x[:3], [(0, 0, b - a)], *x[3:])
+        check_weights(w[:, :, a:b], *weights64(x[0], x[1], x[4], [(0, 0, b - a)]))
