@@ -458,3 +458,36 @@ def test_offsets_past_32_bits(m):
         zero = torch.zeros(1, H, n, device="cuda")
         check_weights(cache.view()[3][b:b + 1], *weigh64(zero, k[b:b + 1], q[b:b + 1], lse[b:b + 1], None, SCALE))
     cache.close()
+
+
+def test_weighing_beside_prompts_on_other_streams():
+    # three kernels at once that each take all of an SM's tensor memory
+    n = 6000
+    k, v = block(140, 1, 8, n)
+    cache = binding.EvictCache("attention", 1, 8, budget=n, n_sink=0, max_block=n)
+    cache.update_and_fetch(k, v)
+    q, lse = rows(142, 16, 32, 3), torch.full((16, 32, 3), 6.0, device="cuda")
+    qp, kp, vp = rows(143, 1, 32, 2500), rows(144, 1, 8, 2500), rows(145, 1, 8, 2500)
+    lp = torch.empty(1, 32, 2500, device="cuda")
+    ref_out, ref_lse = prompt.attention(qp, kp, vp, lse=lp), lp.clone()
+    ref_w = prompt.weights(qp, kp, ref_lse)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(6):
+        cache.weigh(q, lse)
+        with torch.cuda.stream(a):
+            l = torch.empty(1, 32, 2500, device="cuda")
+            got.append((prompt.attention(qp, kp, vp, lse=l), l))
+        with torch.cuda.stream(b):
+            got.append(prompt.weights(qp, kp, ref_lse))
+    torch.cuda.synchronize()
+    cache.sync()
+    for x in got:
+        if isinstance(x, tuple):
+            assert torch.equal(x[0], ref_out) and torch.equal(x[1], ref_lse)
+        else:
+            assert torch.equal(x, ref_w)
+    w, bound = weigh64(torch.zeros(1, 8, n, device="cuda"), k, q, lse, None, SCALE)
+    check_weights(cache.view()[3], 6 * w, 6 * bound + 8 * U32 * 6 * w)
+    cache.close()
