@@ -316,8 +316,10 @@ __device__ void sum_warp(const PromptParams& p, WeightsShared& sh, uint32_t tmem
   Ring<kRing> r;
 #pragma unroll 1
   for (int unit = 0;; ++unit) {
+    // Warps w and w + 8 meet at a unit's end, so they go on, or leave, together: where a wait has given up somewhere, one
+    // of them may have come before the unit was there, the other after. (And the sums of the unit before are read.)
     const Unit u = read_unit(sh, unit);
-    if (!u.kind) break;
+    if (!named_and(1 + (warp & 7), 64, u.kind != 0)) break;
     Step s(p, u);
     float sum = 0.f;
 #pragma unroll 1
@@ -378,7 +380,7 @@ __device__ void sum_warp(const PromptParams& p, WeightsShared& sh, uint32_t tmem
       s_buf.next();
       r.next();
     }
-    // a key's two sums meet: warp w + 8's go to warp w. Both leave together where either has given up.
+    // a key's two sums meet: warp w + 8's go to warp w
     if (buf) sh.sums[key] = sum;
     if (!named_and(1 + (warp & 7), 64, !*(volatile int*)&sh.fail)) break;
     if (!buf) {
@@ -389,7 +391,6 @@ __device__ void sum_warp(const PromptParams& p, WeightsShared& sh, uint32_t tmem
         p.part[(size_t)(2 * blockIdx.x + (u.from == 0 ? 1 : 0)) * kKeys + key] = sum;
       }
     }
-    tc::named_sync(1 + (warp & 7), 64);
   }
 }
 

@@ -1,0 +1,30 @@
+"""Prompts' attention, weights of keys and of steps: rarer calls' refusals, and what reading alone can show (no GPU needed)."""
+import os
+import re
+
+from kv_cache_token_bf16_gb300 import binding
+
+CSRC = os.path.join(os.path.dirname(os.path.abspath(binding.__file__)), "csrc")
+
+
+def body(file, head):
+    """The text of the function that begins with `head`."""
+    text = open(os.path.join(CSRC, file)).read()
+    at = text.index("{", text.index(head))
+    depth = 0
+    for i in range(at, len(text)):
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        if depth == 0:
+            return re.sub(r"//[^\n]*", "", text[at:i + 1])
+    raise AssertionError(head)
+
+
+def test_warps_that_meet_at_a_barrier_leave_it_together():
+    # warps w and w + 8 sum halves of the same keys and meet at a barrier that nothing bounds. A warp that left the loop
+    # on its own (a wait that gave up makes read_unit's answer differ between the two) would leave the other there for
+    # good: every way out has to be a decision of both.
+    text = body("weights.cu", "void sum_warp(")
+    exits = [line.strip() for line in text.splitlines() if re.search(r"\b(break|return|goto)\b", line)]
+    assert len(exits) == 2
+    for line in exits:
+        assert re.fullmatch(r"if \(!named_and\(1 \+ \(warp & 7\), 64, .+\)\) break;", line), line
