@@ -511,7 +511,7 @@ typedef struct evict_prompt {
   evict_rows v;              /* attention only: heads as k's */
   evict_rows out;            /* attention only: heads as q's; must not overlap any input */
   float* lse;                /* device [batch, n_q_heads, m]: written by the attention (or NULL), read by the weights */
-  float* weights;            /* device [batch, n_kv_heads, m]: written by the weights */
+  float* weights;            /* device [batch, n_kv_heads, m]: written by the weights; must not overlap any input */
   const int32_t* starts;     /* device [n_seqs + 1], or NULL */
   int n_seqs;
   int last;                  /* weights: only the last `last` queries of every sequence count (0 = all) */
@@ -551,7 +551,8 @@ int evict_prompt_attention(const evict_prompt* a);
  * heads and the queries that see key j and count (`last`), in fp32. With the
  * attention's own lse that is the softmax weight that key j got. A query whose
  * lse is -inf (it saw nothing) has no weights. v and out are not looked at.
- * Errors as evict_prompt_attention's; last < 0 is EVICT_EINVAL. */
+ * Errors as evict_prompt_attention's; last < 0 and weights that overlap lse, or
+ * begin where q or k do, are EVICT_EINVAL. */
 int evict_prompt_weights(const evict_prompt* a);
 
 /* Add to the scores of a cache of EVICT_ATTENTION the weights that queries put

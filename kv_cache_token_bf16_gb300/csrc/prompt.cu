@@ -667,6 +667,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(const __gr
 
 bool multiple(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
 
 int check_tensor(const evict_rows& x, int batch, int m, int heads, bool output, const char* name) {
   if (!x.data) return fail(EVICT_EINVAL, "%s must not be NULL", name);
@@ -729,6 +733,11 @@ int check_prompt(const evict_prompt* a, bool attention) {
   if (!attention) {
     if (!a->lse || !a->weights) return fail(EVICT_EINVAL, "lse and weights must not be NULL");
     if (a->last < 0) return fail(EVICT_EINVAL, "last must be >= 0 (got %d)", a->last);
+    const size_t tokens = (size_t)a->batch * a->m;
+    if (overlap(a->weights, tokens * a->k.heads * 4, a->lse, tokens * a->q.heads * 4))
+      return fail(EVICT_EINVAL, "weights must not overlap lse: it is read while results are written");
+    if (a->weights == a->q.data || a->weights == a->k.data)
+      return fail(EVICT_EINVAL, "weights must not be q or k: they are read while results are written");
     return EVICT_OK;
   }
   if ((rc = check_tensor(a->v, a->batch, a->m, a->k.heads, false, "v")) ||

@@ -154,8 +154,8 @@ def attention(q, k, v, packing: Packing | None = None, scale=None, out=None, lse
 def weights(q, k, lse, packing: Packing | None = None, last: int = 0, scale=None, out=None):
     """The weights that a prompt's queries put on each key: fp32 [batch, n_kv_heads, m], the sums of
     exp(scale * q . k - lse) over the KV head's query heads and the queries that see the key, or of them
-    the ``last`` ones of every sequence (0: all). lse: as ``attention`` leaves it. Tokens of no sequence
-    keep their values of ``out``, and have zeros in a new one. Returns out."""
+    the ``last`` ones of every sequence (0: all). lse: as ``attention`` leaves it. ``out`` must not overlap
+    an input; tokens of no sequence keep their values of it, and have zeros in a new one. Returns out."""
     if _calls is None:
         _load()
     torch = paged._torch

@@ -2,7 +2,11 @@
 import os
 import re
 
+import pytest
+
 from kv_cache_token_bf16_gb300 import binding
+from kv_cache_token_bf16_gb300.binding import EVICT_EINVAL
+from tests.test_prompt_host import A, call, refused, rows
 
 CSRC = os.path.join(os.path.dirname(os.path.abspath(binding.__file__)), "csrc")
 
@@ -28,3 +32,19 @@ def test_warps_that_meet_at_a_barrier_leave_it_together():
     assert len(exits) == 2
     for line in exits:
         assert re.fullmatch(r"if \(!named_and\(1 \+ \(warp & 7\), 64, .+\)\) break;", line), line
+
+
+# 8 query heads and as many KV heads, 100 tokens: log-sum-exps and weights are 3200 bytes each
+@pytest.mark.parametrize("match,kw", [
+    ("overlap lse", dict(weights=A)), ("overlap lse", dict(weights=A + 3196)), ("overlap lse", dict(weights=A - 3196)),
+    ("be q or k", dict(weights=A << 3)), ("be q or k", dict(weights=A << 4))])
+def test_weights_over_what_they_are_made_of_are_refused(lib, match, kw):
+    base = dict(hkv=8, q=rows(8, 100, A << 3), k=rows(8, 100, A << 4), lse=A)
+    refused(EVICT_EINVAL, match, binding.evict_prompt_weights, call(**dict(base, **kw)))
+
+
+def test_weights_beside_their_log_sum_exps_are_not_refused(lib):
+    for at in (A + 3200, A - 3200):
+        with pytest.raises(binding.EvictError) as e:             # the workspace, or no GPU here
+            binding.evict_prompt_weights(call(hkv=8, lse=A, weights=at))
+        assert "overlap" not in str(e.value)
