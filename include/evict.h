@@ -566,8 +566,9 @@ int evict_prompt_weights(const evict_prompt* a);
  * -inf has no weights. On `stream`, which the caller orders behind the handle's
  * last update and before its next one. n_new outside [0, m] counts as the
  * nearest of these and is reported by evict_sync (EVICT_EDEVICE). EVICT_EINVAL:
- * another method, NULL or misaligned pointers, bad sizes; EVICT_ELIMIT: batch *
- * n_q_heads * m of 2^30 or more. No rows or no queries is a no-op. */
+ * another method, NULL or misaligned pointers, bad sizes, another device than the
+ * handle's being current; EVICT_ELIMIT: batch * n_q_heads * m of 2^30 or more. No
+ * rows or no queries is a no-op. */
 int evict_weigh(evict_handle* h, const evict_rows* q, int batch, int m, const float* lse, const int32_t* n_new,
                 float scale, void* stream);
 

@@ -463,6 +463,7 @@ class EvictCache:
             self._filters = f
             cfg.filters = f.data_ptr()
             cfg.n_filter_heads = f.shape[0]
+        self.device_index = torch.cuda.current_device()     # where the rows lie
         self.handle = evict_init(cfg)
         self._held = _Handle(self.handle)
         self._rows = None           # tensors over all rows that there is room for,

@@ -50,6 +50,7 @@ struct evict_handle {
   int new_stride = 0;         // row stride of new_score (= max_block)
   bool fallback = false;      // Q-Filters without calibrated filters: key-SVD fallback
   bool frozen = false;        // fallback: the per-(b, h) filters have been estimated
+  int dev = 0;                // device of the arena
   cudaStream_t stream = nullptr;
   unsigned long long captured = 0;   // the last capture that holds work of this handle (0: none)
 

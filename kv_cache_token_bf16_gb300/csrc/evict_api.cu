@@ -384,7 +384,8 @@ int evict_init(const evict_config* cfg, evict_handle** out) {
   h->flag_stride = compact_flag_slots(h->cap, h->elem);
   h->stream = static_cast<cudaStream_t>(cfg->stream);
   const size_t bytes = arena_layout(h, nullptr);
-  cudaError_t e = cudaMalloc(&h->arena, bytes);
+  cudaError_t e = cudaGetDevice(&h->dev);
+  if (e == cudaSuccess) e = cudaMalloc(&h->arena, bytes);
   if (e != cudaSuccess) {
     delete h;
     return cuda_fail(e, "device allocation of the cache");

@@ -539,6 +539,7 @@ extern "C" int evict_weigh(evict_handle* h, const evict_rows* q, int batch, int 
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e, "looking up the device");
+  if (dev != h->dev) return fail(EVICT_EINVAL, "the cache is on device %d, the current device is %d", h->dev, dev);
   const int units = h->cfg.batch * p.heads;
   if (const unsigned long long id = capture_of(static_cast<cudaStream_t>(stream))) h->captured = id;
   // Key tiles for every SM and enough products for the wide kernel's start to pay (8 heads; us, narrow and wide):

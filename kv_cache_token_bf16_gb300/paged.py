@@ -335,6 +335,8 @@ def weigh_rows(cache, q, lse, n_new=None, scale=None):
     if _recording() and (q.requires_grad or lse.requires_grad):
         _no_history()
     index, shape = _device(q), q.shape
+    if index != cache.device_index:
+        raise ValueError(f"the cache is on CUDA device {cache.device_index}, q on {index}")
     if len(shape) != 4:
         raise ValueError(f"q must be [batch, heads, m, {HEAD_DIM}], not {tuple(shape)}")
     batch, hq, m, _ = shape

@@ -1,6 +1,7 @@
 """Prompts' attention, weights of keys and of steps: rarer calls' refusals, and what reading alone can show (no GPU needed)."""
 import os
 import re
+from types import SimpleNamespace
 
 import pytest
 
@@ -48,3 +49,13 @@ def test_weights_beside_their_log_sum_exps_are_not_refused(lib):
         with pytest.raises(binding.EvictError) as e:             # the workspace, or no GPU here
             binding.evict_prompt_weights(call(hkv=8, lse=A, weights=at))
         assert "overlap" not in str(e.value)
+
+
+def test_queries_on_another_device_than_the_caches_are_refused(lib):
+    # (tensors and a cache that say where they are: two devices are more than there may be)
+    pytest.importorskip("torch")
+    from kv_cache_token_bf16_gb300 import paged
+    q = SimpleNamespace(shape=(1, 4, 1, 128), requires_grad=False, get_device=lambda: 1, device="cuda:1")
+    lse = SimpleNamespace(requires_grad=False)
+    with pytest.raises(ValueError, match="cache is on CUDA device 0, q on 1"):
+        paged.weigh_rows(SimpleNamespace(device_index=0, handle=None), q, lse)
