@@ -410,19 +410,21 @@ class _Handle:
 
 
 class _Ordered:
-    """Orders work on the current stream behind a cache's last update, and its next one behind the work."""
+    """Orders work on the current stream of a cache's device behind the cache's last update, and its next one behind
+    the work."""
 
-    def __init__(self, handle):
+    def __init__(self, handle, index):
         import torch
         own = evict_get_stream(handle)
-        if torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) == own:
+        if torch._C._cuda_getCurrentRawStream(index) == own:
             own = None
         else:
-            self.here = torch.cuda.current_stream()
-            own = torch.cuda.ExternalStream(own) if own else torch.cuda.default_stream()
-            captures = torch.cuda.is_current_stream_capturing()
-            with torch.cuda.stream(own):
-                own_captures = torch.cuda.is_current_stream_capturing()
+            self.here = torch.cuda.current_stream(index)
+            own = torch.cuda.ExternalStream(own, device=index) if own else torch.cuda.default_stream(index)
+            with torch.cuda.device(index):
+                captures = torch.cuda.is_current_stream_capturing()
+                with torch.cuda.stream(own):
+                    own_captures = torch.cuda.is_current_stream_capturing()
             if own_captures and not captures:
                 raise ValueError("the cache's stream is being captured: attend under it")
             if captures and not own_captures:
@@ -501,9 +503,9 @@ class EvictCache:
         that is a multiple of the cache's gives every kept prefix to that many sequences.
         ``weigh`` (method "attention"): and ``weigh`` of the same queries.
 
-        Work goes on the current stream. Where that is not the cache's, it is ordered behind the
-        cache's last update, and the cache's next one behind it, also inside one graph that captures
-        both streams. A graph that captures the current stream alone cannot hold that order: it reads
+        Work goes on the current stream of the cache's device. Where that is not the cache's own, it is
+        ordered behind the cache's last update, and the cache's next one behind it, also inside one graph
+        that captures both streams. A graph that captures the current stream alone cannot hold that order: it reads
         the rows kept when it is replayed, and the replay has to be ordered like any other reader."""
         from . import paged
         if weigh:
@@ -512,7 +514,7 @@ class EvictCache:
                 raise ValueError('only a cache of method "attention" accumulates weights')
             if lse is None:
                 lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
-        with _Ordered(self.handle):
+        with _Ordered(self.handle, self.device_index):
             k, v, _, _ = self.view()
             out = paged.shared_attention(q, prefix=(k, v), n_new=n_new, scale=scale, out=out, lse=lse)
             if weigh:
@@ -526,7 +528,7 @@ class EvictCache:
         ``paged.PagedCache.attend`` fill it). Method "attention" only; batch, streams and captures as for
         ``attend``."""
         from . import paged
-        with _Ordered(self.handle):
+        with _Ordered(self.handle, self.device_index):
             paged.weigh_rows(self, q, lse, n_new=n_new, scale=scale)
 
     def view(self):

@@ -59,3 +59,39 @@ def test_queries_on_another_device_than_the_caches_are_refused(lib):
     lse = SimpleNamespace(requires_grad=False)
     with pytest.raises(ValueError, match="cache is on CUDA device 0, q on 1"):
         paged.weigh_rows(SimpleNamespace(device_index=0, handle=None), q, lse)
+
+
+def test_streams_are_ordered_on_the_caches_device(lib, monkeypatch):
+    # the cache is on device 1, and device 0 current, whose current stream has the number of the cache's
+    torch = pytest.importorskip("torch")
+    log = []
+
+    class Stream:
+        def __init__(self, number, device=None):
+            self.at = device, number
+
+        def wait_stream(self, other):
+            log.append((self.at, other.at))
+
+    class Context:
+        def __init__(self, *_):
+            pass
+
+        def __enter__(self):
+            pass
+
+        __exit__ = __init__
+
+    monkeypatch.setattr(binding, "evict_get_stream", lambda handle: 77)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: (77, 5)[index], raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index=0: Stream((77, 5)[index], index))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    for name, fake in (("ExternalStream", Stream), ("stream", Context), ("device", Context)):
+        monkeypatch.setattr(torch.cuda, name, fake)
+    cache = binding.EvictCache.__new__(binding.EvictCache)
+    cache.handle, cache.device_index, cache.method = None, 1, "attention"
+    from kv_cache_token_bf16_gb300 import paged
+    monkeypatch.setattr(paged, "weigh_rows", lambda *a, **kw: log.append("weigh"))
+    cache.weigh(None, None)
+    assert log == [((1, 5), (1, 77)), "weigh", ((1, 77), (1, 5))]
