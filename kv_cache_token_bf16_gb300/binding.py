@@ -368,9 +368,10 @@ class _CudaArray:
                                          "version": 3, "strides": strides}
 
 
-def view_tensors(view: EvictView, batch: int, heads: int, dtype: str, owner=None):
+def view_tensors(view: EvictView, batch: int, heads: int, dtype: str, owner=None, device="cuda"):
     """Zero-copy torch tensors over a view: k, v [B,H,n,D], pos, score [B,H,n]. They hold ``owner``, if one is
-    given; without, whoever holds the handle keeps it for as long as they are read."""
+    given; without, whoever holds the handle keeps it for as long as they are read. ``device``: where the rows
+    lie (the current device by default; torch would copy them from another one)."""
     import torch
     cap, n = view.capacity, view.n_kept
     esz = 2 if dtype == "bf16" else 4
@@ -380,7 +381,7 @@ def view_tensors(view: EvictView, batch: int, heads: int, dtype: str, owner=None
     shp = (batch, heads, n, HEAD_DIM)
 
     def wrap(ptr, shape, ts, strides):
-        return torch.as_tensor(_CudaArray(ptr, shape, ts, strides, owner), device="cuda")
+        return torch.as_tensor(_CudaArray(ptr, shape, ts, strides, owner), device=device)
 
     k = wrap(view.k, shp, tstr, kv_strides)
     v = wrap(view.v, shp, tstr, kv_strides)
@@ -544,7 +545,8 @@ class EvictCache:
         if self._rows is None:
             every = EvictView(view.k, view.v, view.pos, view.score, view.capacity, view.capacity)
             with torch.inference_mode(False):       # tensors for any mode, whichever asks first
-                self._rows = view_tensors(every, self.batch, self.heads, self.dtype, self._held)
+                self._rows = view_tensors(every, self.batch, self.heads, self.dtype, self._held,
+                                          f"cuda:{self.device_index}")
         n = view.n_kept
         with torch.inference_mode(False):
             self._views = n, tuple(x.narrow(2, 0, n) for x in self._rows)

@@ -95,3 +95,26 @@ def test_streams_are_ordered_on_the_caches_device(lib, monkeypatch):
     monkeypatch.setattr(paged, "weigh_rows", lambda *a, **kw: log.append("weigh"))
     cache.weigh(None, None)
     assert log == [((1, 5), (1, 77)), "weigh", ((1, 77), (1, 5))]
+
+
+def fake_rows(monkeypatch, device_index):
+    """A cache of 2 KV heads with room for 8 rows, and the devices that tensors over them are asked for on."""
+    torch = pytest.importorskip("torch")
+    asked = []
+
+    def as_tensor(x, device=None):
+        asked.append(str(device))
+        at = x.__cuda_array_interface__
+        return torch.zeros(at["shape"], dtype={"<i2": torch.int16, "<f4": torch.float32, "<i4": torch.int32}[at["typestr"]])
+
+    monkeypatch.setattr(torch, "as_tensor", as_tensor)
+    cache = binding.EvictCache.__new__(binding.EvictCache)
+    cache.handle, cache.device_index, cache.batch, cache.heads, cache.dtype = None, device_index, 1, 2, "bf16"
+    cache._held, cache._rows, cache._views = None, None, (-1, None)
+    return cache, asked
+
+
+def test_views_are_made_on_the_caches_device(lib, monkeypatch):
+    cache, asked = fake_rows(monkeypatch, 3)
+    cache._kept(binding.EvictView(A, A, A, A, 5, 8))
+    assert asked == ["cuda:3"] * 4
