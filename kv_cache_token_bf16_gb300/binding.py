@@ -539,18 +539,18 @@ class EvictCache:
 
     def _kept(self, view):
         """view_tensors of a view, which lies where the handle's rows have lain from the start."""
-        if view.n_kept == self._views[0]:           # a cache that is full keeps as many after every step
-            return self._views[1]
-        import torch
-        if self._rows is None:
-            every = EvictView(view.k, view.v, view.pos, view.score, view.capacity, view.capacity)
-            with torch.inference_mode(False):       # tensors for any mode, whichever asks first
-                self._rows = view_tensors(every, self.batch, self.heads, self.dtype, self._held,
-                                          f"cuda:{self.device_index}")
         n = view.n_kept
-        with torch.inference_mode(False):
-            self._views = n, tuple(x.narrow(2, 0, n) for x in self._rows)
-        return self._views[1]
+        if n != self._views[0]:                     # a cache that is full keeps as many after every step
+            import torch
+            with torch.inference_mode(False):       # tensors for any mode, whichever asks first
+                if self._rows is None:
+                    every = EvictView(view.k, view.v, view.pos, view.score, view.capacity, view.capacity)
+                    self._rows = view_tensors(every, self.batch, self.heads, self.dtype, self._held,
+                                              f"cuda:{self.device_index}")
+                self._views = n, tuple(x.narrow(2, 0, n) for x in self._rows)
+        # objects of the caller's own, whatever is done to them in place (2 us; as narrow() makes them, 15)
+        k, v, pos, score = self._views[1]
+        return k.data, v.data, pos.data, score.data
 
     def set_state(self, k, v, pos, score=None, offset=None):
         n = k.shape[2]

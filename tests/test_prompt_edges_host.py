@@ -118,3 +118,25 @@ def test_views_are_made_on_the_caches_device(lib, monkeypatch):
     cache, asked = fake_rows(monkeypatch, 3)
     cache._kept(binding.EvictView(A, A, A, A, 5, 8))
     assert asked == ["cuda:3"] * 4
+
+
+def test_views_are_the_callers_own_objects(lib, monkeypatch):
+    torch = pytest.importorskip("torch")
+    cache, asked = fake_rows(monkeypatch, 0)
+    view = binding.EvictView(A, A, A, A, 5, 8)
+    first = cache._kept(view)
+    first[0].requires_grad_()
+    first[3].unsqueeze_(0)
+    first[2].transpose_(0, 1)
+    second = cache._kept(view)
+    assert [x.shape for x in second] == [(1, 2, 5, 128), (1, 2, 5, 128), (1, 2, 5), (1, 2, 5)]
+    assert not any(x.requires_grad for x in second) and len(asked) == 4
+    second[3].fill_(3.0)                            # the same rows
+    assert (first[3] == 3).all() and (cache._kept(view)[3] == 3).all()
+    versions = [x._version for x in first]
+    cache._kept(view)[0].add_(1.0)
+    assert [x._version for x in first] == versions and (first[0] == 1).all()
+    with torch.inference_mode():
+        third = cache._kept(view)
+    third[3].add_(1.0)
+    assert (second[3] == 4).all()
