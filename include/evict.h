@@ -541,7 +541,9 @@ int evict_prompt_weights_workspace(const evict_prompt* a, size_t* bytes);
  * do not divide, out's rows on top of each other or its data that of an input,
  * a workspace that is too small. EVICT_ELIMIT: more than EVICT_MAX_PROMPT_GROUP
  * query heads for a KV head or EVICT_MAX_PROMPT_SEQS sequences, batch *
- * n_q_heads * m of 2^30 or more, or 2^31 or more steps of 128 keys in all.
+ * n_q_heads * m of 2^30 or more, or 2^30 or more blocks of tokens by KV heads
+ * (for each sequence one block more than its tokens fill may be counted). However
+ * long a plane is, its sequences' own lengths are what the call's work goes by.
  * batch, m or n_seqs of 0 is a no-op. Device errors, reported through `error`:
  * starts that fall, or leave [0, m] (kind "index": then nothing is written);
  * a bounded wait that gave up. */

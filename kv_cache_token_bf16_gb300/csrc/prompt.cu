@@ -768,8 +768,7 @@ int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry
   w.longest_last = longest_last;
   const int seq_blocks = (a->m + tile - 1) / tile;
   const long long blocks = a->starts ? (long long)a->m / tile + a->n_seqs : (long long)a->batch * seq_blocks;
-  if (blocks * w.hkv >= (1ll << 30) || (double)blocks * w.hkv * (double)(most_steps + entry) >= 2147483648.0)
-    return fail(EVICT_ELIMIT, "the sequences are too many or too long for one call");
+  if (blocks * w.hkv >= (1ll << 30)) return fail(EVICT_ELIMIT, "sequences and KV heads make 2^30 units of work or more");
   w.blocks = (int)blocks;
   w.by_hkv = Divisor(w.hkv);
   w.by_tile = Divisor(tile);
@@ -780,6 +779,9 @@ int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry
   if (e != cudaSuccess) return cuda_fail(e, "looking up the device");
   P.dev = dev;
   w.whole = blocks * w.hkv >= (long long)whole_rounds * P.sms;
+  // Steps are counted together where units are cut alone: few units then, of planes that are no longer than their blocks.
+  if (!w.whole && (double)blocks * w.hkv * (double)(most_steps + entry) >= 2147483648.0)
+    return fail(EVICT_ELIMIT, "the sequences are too long for one call");
   size_t off = 256;                               // an error word, for callers without one
   auto take = [&](size_t bytes) {
     const size_t at = off;

@@ -1,6 +1,6 @@
 // Device side of the prompts' schedule: blocks, units, steps and the share of
 // them that a CTA takes (see prompt.h). The sequences' lengths are the device's.
-// Counts of steps fit 31 bits (the host refuses calls that might pass them).
+// Counts of units fit 30 bits, and of cut units' steps 31 (the host refuses calls that might pass them).
 #pragma once
 
 #include "attend.cuh"

@@ -1,0 +1,58 @@
+"""Prompts' attention and weights of keys where sizes and values are rare, against plain 64-bit forms."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from kv_cache_token_bf16_gb300 import prompt  # noqa: E402
+from tests.paged_util import D, U32  # noqa: E402
+from tests.prompt_util import SCALE, check_prompt, check_weights, weights64  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built(lib):
+    pass
+
+
+def big(seed, heads, m):
+    g = torch.Generator("cuda").manual_seed(seed)
+    return torch.randn(1, m, heads, D, device="cuda", generator=g, dtype=torch.bfloat16).transpose(1, 2)
+
+
+def test_a_plane_of_eight_million_tokens():
+    # 16385 sequences; by the plane's length its blocks would be 2^31 steps. Some sequences against calls' own bounds.
+    lens = [512] * 16384 + [77]
+    starts = torch.tensor([0] + lens).cumsum(0)
+    m = int(starts[-1])
+    pk = prompt.Packing(starts.int().cuda())
+    q, k, v = big(1, 1, m), big(2, 1, m), big(3, 1, m)
+    lse = torch.empty(1, 1, m, device="cuda")
+    out = prompt.attention(q, k, v, pk, out=torch.empty_like(q), lse=lse)
+    w = prompt.weights(q, k, lse, pk)
+    pk.sync()
+    for i in (0, 1, 8191, 16383, 16384):
+        a, b = int(starts[i]), int(starts[i + 1])
+        x = [t[:, :, a:b].contiguous() for t in (q, k, v, out, lse)]
+        check_prompt(*x[:3], [(0, 0, b - a)], *x[3:])
+        check_weights(w[:, :, a:b], *weights64(x[0], x[1], x[4], [(0, 0, b - a)]))
+    assert torch.isfinite(lse).all() and torch.isfinite(w).all()
+
+
+def test_a_window_over_four_million_tokens():
+    # the keys' weights of the last 64 queries: two steps a block, 2^31 if every query counted
+    m, h, last = 1 << 22, 4, 64
+    q, k = big(4, h, m), big(5, h, m)
+    lse = torch.randn(1, h, m, device="cuda", generator=torch.Generator("cuda").manual_seed(6)) + 16.0
+    w = prompt.weights(q, k, lse, last=last)
+    torch.cuda.synchronize()
+    at = torch.arange(m, device="cuda")
+    for i in range(h):
+        for a in (0, 1 << 21, m - 1000):
+            e = min(m, a + 100_000)
+            z = SCALE * (q[0, i, m - last:].double() @ k[0, i, a:e].double().T)
+            x = lse[0, i, m - last:].double()[:, None]
+            p = torch.where(at[a:e] <= at[m - last:, None], torch.exp(z - x), 0.0)
+            # the bound of weights64
+            off = 132 * U32 * SCALE * q[0, i, m - last:].double().norm(dim=1)[:, None] * k[0, i, a:e].double().norm(dim=1)
+            bound = (p * (off + 4 * U32 * (x.abs() + z.abs()) + 2.0 ** -20)).sum(0) + 180 * U32 * p.sum(0) + 1e-37
+            assert bool(((w[0, i, a:e].double() - p.sum(0)).abs() <= bound).all())

@@ -6,7 +6,7 @@ from types import SimpleNamespace
 import pytest
 
 from kv_cache_token_bf16_gb300 import binding
-from kv_cache_token_bf16_gb300.binding import EVICT_EINVAL
+from kv_cache_token_bf16_gb300.binding import EVICT_EINVAL, EVICT_ELIMIT
 from tests.test_prompt_host import A, call, refused, rows
 
 CSRC = os.path.join(os.path.dirname(os.path.abspath(binding.__file__)), "csrc")
@@ -140,3 +140,21 @@ def test_views_are_the_callers_own_objects(lib, monkeypatch):
         third = cache._kept(view)
     third[3].add_(1.0)
     assert (second[3] == 4).all()
+
+
+# a plane of 2^20 tokens and more in short sequences, or of which a window counts: by their plane's length alone these
+# would be 2^31 steps. (What they need, or without a GPU an error that there is none.)
+@pytest.mark.parametrize("fn", [binding.evict_prompt_attention_workspace, binding.evict_prompt_weights_workspace])
+@pytest.mark.parametrize("hq,hkv,m,n,last", [(64, 8, 1 << 20, 1024, 0), (1, 1, (1 << 23) + 77, 16385, 0), (64, 8, 1 << 21, 1, 64),
+                                             (128, 128, (1 << 23) - 1, 65536, 0)])
+def test_long_planes_are_no_long_sequences(lib, fn, hq, hkv, m, n, last):
+    a = call(hq=hq, hkv=hkv, m=m, starts=A, n_seqs=n, last=last)
+    try:
+        assert 0 < fn(a) < 1 << 30
+    except binding.EvictError as e:
+        assert e.code == binding.EVICT_ECUDA, e
+
+
+@pytest.mark.parametrize("fn", [binding.evict_prompt_attention_workspace, binding.evict_prompt_weights_workspace])
+def test_too_many_units_are_refused(lib, fn):
+    refused(EVICT_ELIMIT, "units", fn, call(hq=1 << 15, hkv=1 << 15, m=1000, starts=A, n_seqs=65536))
