@@ -87,6 +87,7 @@ struct WeightsShared {
     PromptScan scan;                              // before the first of them
   };
   float sums[kKeys];
+  alignas(16) uint32_t none[kRing][kTile / 32];   // columns of a step whose log-sum-exp is -infinity
 };
 // All of it is dynamic: seven tiles and this fill the 227 KB.
 constexpr int kSmem = (4 + kRing) * kTileBytes + (int)sizeof(WeightsShared);
@@ -228,8 +229,12 @@ __device__ void lse_loader(const PromptParams& p, WeightsShared& sh) {
       if (!warp_wait(&sh.lse_empty[r.i], r.parity ^ 1, &sh.fail)) return;
       // no weights of a query that saw nothing; log2 e in two parts, as all weights would lean to where its rounding does
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        sh.neg_lse2[r.i][32 * j + lane] = l[j] == -INFINITY ? l[j] : fmaf(-l[j], kLog2e, -l[j] * kLog2eRest);
+      for (int j = 0; j < 4; ++j) {
+        const bool none = l[j] == -INFINITY;
+        sh.neg_lse2[r.i][32 * j + lane] = none ? l[j] : fmaf(-l[j], kLog2e, -l[j] * kLog2eRest);
+        const uint32_t of = __ballot_sync(0xffffffffu, none);
+        if (lane == 0) sh.none[r.i][j] = of;
+      }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sh.lse_full[r.i]);
       r.next();
@@ -331,7 +336,9 @@ __device__ void sum_warp(const PromptParams& p, WeightsShared& sh, uint32_t tmem
         tc::fence_after_sync();
         const int columns = s.sees(u, kt) ? s.columns(p) : 0;
         const int before = u.key0 + key - s.tok0;                  // tokens that do not see this key
-        const bool masked = !s.full(p) || u.key0 + kt * kTile + kTile - 1 > s.tok0;
+        const uint32_t* none = sh.none[r.i];
+        const uint4 nones = *reinterpret_cast<const uint4*>(none);
+        const bool masked = !s.full(p) || u.key0 + kt * kTile + kTile - 1 > s.tok0 || (nones.x | nones.y | nones.z | nones.w);
         uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll 1
         for (int c0 = 0; c0 < columns; c0 += 32) {
@@ -352,8 +359,8 @@ __device__ void sum_warp(const PromptParams& p, WeightsShared& sh, uint32_t tmem
               acc[1] = add_f32x2(acc[1], ex2_f32x2(fma_f32x2(pack_f32x2(x[j + 2], x[j + 3]), sc2, pack_f32x2(l.z, l.w))));
             }
           } else {
-            // (a step's log-sum-exps of columns that do not count are -infinity, but their logits may be anything)
-            const uint32_t m = seen_columns(p, s, c0, columns, before);
+            // (log-sum-exps of columns that do not count are -infinity, but their logits may be anything)
+            const uint32_t m = seen_columns(p, s, c0, columns, before) & ~none[c0 / 32];
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
               const float4 l = l2[j / 4];

@@ -1,4 +1,6 @@
 """Prompts' attention and weights of keys where sizes and values are rare, against plain 64-bit forms."""
+import math
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -56,3 +58,26 @@ def test_a_window_over_four_million_tokens():
             off = 132 * U32 * SCALE * q[0, i, m - last:].double().norm(dim=1)[:, None] * k[0, i, a:e].double().norm(dim=1)
             bound = (p * (off + 4 * U32 * (x.abs() + z.abs()) + 2.0 ** -20)).sum(0) + 180 * U32 * p.sum(0) + 1e-37
             assert bool(((w[0, i, a:e].double() - p.sum(0)).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("hq,hkv,lens,last", [(4, 2, [300], 0), (8, 2, [1700], 0), (4, 4, [128, 640, 3], 0), (8, 1, [900, 300], 20)])
+def test_queries_without_a_log_sum_exp_may_hold_anything(hq, hkv, lens, last):
+    # no weights of a query whose log-sum-exp is -infinity, whatever its row is: padding, for one
+    m = sum(lens)
+    g = torch.Generator("cuda").manual_seed(7)
+    q, k = big(8, hq, m), big(9, hkv, m)
+    lse = torch.randn(1, hq, m, device="cuda", generator=g) + 5.0
+    starts = torch.tensor([0] + lens).cumsum(0).tolist()
+    drop = torch.rand(1, hq, m, device="cuda", generator=g) < 0.1
+    drop[:, :, 128:256] = False                     # whole steps of queries that all count
+    drop[:, 1, m - 1] = drop[:, :, 17] = True
+    lse[drop] = -math.inf
+    bad = q.clone()
+    for i, x in enumerate((math.nan, math.inf, -math.inf)):
+        bad[drop & (torch.arange(m, device="cuda") % 3 == i)] = x
+    pk = prompt.Packing(torch.tensor(starts, dtype=torch.int32).cuda())
+    w = prompt.weights(bad, k, lse, pk, last=last)
+    pk.sync()
+    spans = [(0, a, e - a) for a, e in zip(starts, starts[1:])]
+    check_weights(w, *weights64(q, k, lse, spans, last))
+    assert torch.equal(w, prompt.weights(q, k, lse, pk, last=last))
