@@ -515,7 +515,7 @@ typedef struct evict_prompt {
   const int32_t* starts;     /* device [n_seqs + 1], or NULL */
   int n_seqs;
   int last;                  /* weights: only the last `last` queries of every sequence count (0 = all) */
-  float scale;               /* 0 = 1 / sqrt(128) */
+  float scale;               /* below 2^127, of either sign; 0 = 1 / sqrt(128) */
   void* workspace;           /* device, 256-byte aligned; in use until the call's work is done */
   size_t workspace_bytes;    /* at least that of the call's _workspace function */
   int32_t* error;            /* device word as in evict_pages, or NULL */

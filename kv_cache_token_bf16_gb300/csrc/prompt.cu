@@ -723,7 +723,7 @@ int check_prompt_sizes(const evict_prompt* a) {
 
 int check_prompt(const evict_prompt* a, bool attention) {
   if (const int rc = check_prompt_sizes(a)) return rc;
-  if (!std::isfinite(a->scale)) return fail(EVICT_EINVAL, "scale must be finite");
+  if (!good_scale(a->scale)) return fail(EVICT_EINVAL, "scale must be finite and below 2^127");
   if (!multiple(a->starts, 4) || !multiple(a->lse, 4) || !multiple(a->weights, 4) || !multiple(a->error, 4))
     return fail(EVICT_EINVAL, "starts, lse, weights and error must be 4-byte aligned");
   if (a->batch == 0 || a->m == 0) return EVICT_OK;

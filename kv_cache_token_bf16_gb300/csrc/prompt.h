@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "../../include/evict.h"
 #include "attend.h"
 
@@ -46,6 +48,9 @@ constexpr float kLog2eRest = 1.92596299e-8f;       // log2 e beyond its fp32 val
 inline float scale_base2(float scale) {
   return (float)((scale == 0.f ? 0.08838834764831845 : (double)scale) * 1.4426950408889634 * (1.0 + 0x1p-23));
 }
+
+// Whether that is a number (NaN is not below anything).
+inline bool good_scale(float scale) { return std::fabs(scale) < 0x1p127f; }
 
 struct PromptParams {
   CUtensorMap q_map, k_map, v_map;

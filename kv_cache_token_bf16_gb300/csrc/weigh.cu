@@ -506,7 +506,7 @@ extern "C" int evict_weigh(evict_handle* h, const evict_rows* q, int batch, int 
   if (batch % h->cfg.batch) return fail(EVICT_EINVAL, "batch (%d) must be a multiple of the cache's (%d)", batch, h->cfg.batch);
   if (q->heads < 1 || q->heads % h->cfg.n_kv_heads)
     return fail(EVICT_EINVAL, "q's heads (%d) must be a multiple of the cache's (%d)", q->heads, h->cfg.n_kv_heads);
-  if (!std::isfinite(scale)) return fail(EVICT_EINVAL, "scale must be finite");
+  if (!good_scale(scale)) return fail(EVICT_EINVAL, "scale must be finite and below 2^127");
   if (!multiple(lse, 4) || !multiple(n_new, 4)) return fail(EVICT_EINVAL, "lse and n_new must be 4-byte aligned");
   if ((long long)batch * m >= (1ll << 30) || (long long)batch * m * q->heads >= (1ll << 30))
     return fail(EVICT_ELIMIT, "batch * heads * m is 2^30 or more");

@@ -122,6 +122,16 @@ def _like(t, name, shape, dtype, index):
     return t.data_ptr()
 
 
+def _scale(scale):
+    """The scale as the C calls take it: 0 stands for the default there, so what rounds to it is refused."""
+    if scale is None:
+        return 0.0
+    got = ctypes.c_float(scale).value
+    if got == 0:
+        raise ValueError(f"scale must not be 0, nor round to it in fp32 (got {scale})")
+    return got
+
+
 def _stream(index):
     """The current stream of a device (as an integer)."""
     raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
@@ -279,10 +289,7 @@ def shared_attention(q, prefix=None, pages: "PagedCache | None" = None, n_new=No
         outr = _new_rows(out)
     else:
         outr = _rows(out, "out", index, bf16, batch, m, hq)
-    if scale is None:
-        scale = 0.0
-    elif scale == 0:
-        raise ValueError("scale must not be 0")
+    scale = _scale(scale)
     hkv = pages_at = error = width = page = 0
     if pages is not None:
         if pages.batch != batch or pages.index != index:
@@ -341,10 +348,7 @@ def weigh_rows(cache, q, lse, n_new=None, scale=None):
         raise ValueError(f"q must be [batch, heads, m, {HEAD_DIM}], not {tuple(shape)}")
     batch, hq, m, _ = shape
     qr = _ROWS.pack(*_rows(q, "q", index, _torch.bfloat16, batch, m))
-    if scale is None:
-        scale = 0.0
-    elif scale == 0:
-        raise ValueError("scale must not be 0")
+    scale = _scale(scale)
     _call(index, _calls.evict_weigh, cache.handle, qr, batch, m, _like(lse, "lse", (batch, hq, m), _torch.float32, index),
           _like(n_new, "n_new", (batch,), _torch.int32, index) or None, scale, _stream(index))
 

@@ -116,11 +116,7 @@ def _sizes(q, k, packing, scale):
             raise ValueError(f"the packing is on {packing.starts.device}, q on {q.device}")
         if batch != 1:
             raise ValueError(f"packed sequences lie in a batch of 1, not of {batch}")
-    if scale is None:
-        scale = 0.0
-    elif scale == 0:
-        raise ValueError("scale must not be 0")
-    return index, batch, hq, k.shape[1], m, scale
+    return index, batch, hq, k.shape[1], m, paged._scale(scale)
 
 
 def attention(q, k, v, packing: Packing | None = None, scale=None, out=None, lse=None):

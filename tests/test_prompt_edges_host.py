@@ -1,4 +1,5 @@
 """Prompts' attention, weights of keys and of steps: rarer calls' refusals, and what reading alone can show (no GPU needed)."""
+import math
 import os
 import re
 from types import SimpleNamespace
@@ -158,3 +159,25 @@ def test_long_planes_are_no_long_sequences(lib, fn, hq, hkv, m, n, last):
 @pytest.mark.parametrize("fn", [binding.evict_prompt_attention_workspace, binding.evict_prompt_weights_workspace])
 def test_too_many_units_are_refused(lib, fn):
     refused(EVICT_ELIMIT, "units", fn, call(hq=1 << 15, hkv=1 << 15, m=1000, starts=A, n_seqs=65536))
+
+
+def test_scales_that_are_none_in_fp32_are_refused(lib):
+    # (0 is the C calls' default)
+    torch = pytest.importorskip("torch")
+    from kv_cache_token_bf16_gb300 import paged, prompt
+    q = SimpleNamespace(shape=(1, 4, 1, 128), requires_grad=False, get_device=lambda: 0, device="cuda:0", dtype=torch.bfloat16,
+                        stride=lambda: (512, 128, 512, 1), data_ptr=lambda: A)
+    lse = SimpleNamespace(requires_grad=False)
+    for scale in (0, 0.0, 1e-50, -1e-46):
+        with pytest.raises(ValueError, match="scale must not be 0"):
+            prompt.attention(q, q, q, scale=scale, out=q)
+        with pytest.raises(ValueError, match="scale must not be 0"):
+            prompt.weights(q, q, lse, scale=scale)
+        with pytest.raises(ValueError, match="scale must not be 0"):
+            paged.weigh_rows(SimpleNamespace(device_index=0, handle=None), q, lse, scale=scale)
+        with pytest.raises(ValueError, match="scale must not be 0"):
+            paged.shared_attention(q, scale=scale, out=q)
+    assert paged._scale(None) == 0 and paged._scale(1e-45) > 0 and paged._scale(-0.25) == -0.25
+    for fn in (binding.evict_prompt_attention, binding.evict_prompt_weights):
+        for scale in (math.inf, -math.inf, 2.0 ** 127, -3e38):
+            refused(EVICT_EINVAL, "finite", fn, call(scale=scale))
