@@ -128,7 +128,7 @@ def attention(q, k, v, packing: Packing | None = None, scale=None, out=None, lse
         _load()
     torch = paged._torch
     if paged._recording() and (q.requires_grad or k.requires_grad or v.requires_grad or
-                               (out is not None and out.requires_grad)):
+                               (out is not None and out.requires_grad) or (lse is not None and lse.requires_grad)):
         paged._no_history()
     index, batch, hq, hkv, m, scale = _sizes(q, k, packing, scale)
     bf16 = torch.bfloat16

@@ -181,3 +181,13 @@ def test_scales_that_are_none_in_fp32_are_refused(lib):
     for fn in (binding.evict_prompt_attention, binding.evict_prompt_weights):
         for scale in (math.inf, -math.inf, 2.0 ** 127, -3e38):
             refused(EVICT_EINVAL, "finite", fn, call(scale=scale))
+
+
+def test_log_sum_exps_that_require_a_gradient_are_refused(lib):
+    torch = pytest.importorskip("torch")
+    from kv_cache_token_bf16_gb300 import prompt
+    q = torch.zeros(1, 4, 3, 128, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="no gradient"):
+        prompt.attention(q, q, q, lse=torch.zeros(1, 4, 3, requires_grad=True))
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        prompt.attention(q, q, q, lse=torch.zeros(1, 4, 3, requires_grad=True))
