@@ -436,8 +436,8 @@ class _Ordered:
         if self.own is not None:
             self.here.wait_stream(self.own)
 
-    def __exit__(self, failed, *_):
-        if self.own is not None and failed is None:
+    def __exit__(self, *_):
+        if self.own is not None:                    # also where a second call was refused behind a first one's work
             self.own.wait_stream(self.here)
 
 

@@ -62,9 +62,9 @@ def test_queries_on_another_device_than_the_caches_are_refused(lib):
         paged.weigh_rows(SimpleNamespace(device_index=0, handle=None), q, lse)
 
 
-def test_streams_are_ordered_on_the_caches_device(lib, monkeypatch):
-    # the cache is on device 1, and device 0 current, whose current stream has the number of the cache's
-    torch = pytest.importorskip("torch")
+def fake_streams(monkeypatch, torch):
+    """Device 0 is current, whose current stream has the number of the cache's; the cache is on device 1. Returns it and
+    the log of who waited for whom."""
     log = []
 
     class Stream:
@@ -92,10 +92,33 @@ def test_streams_are_ordered_on_the_caches_device(lib, monkeypatch):
         monkeypatch.setattr(torch.cuda, name, fake)
     cache = binding.EvictCache.__new__(binding.EvictCache)
     cache.handle, cache.device_index, cache.method = None, 1, "attention"
+    return cache, log
+
+
+def test_streams_are_ordered_on_the_caches_device(lib, monkeypatch):
+    torch = pytest.importorskip("torch")
     from kv_cache_token_bf16_gb300 import paged
+    cache, log = fake_streams(monkeypatch, torch)
     monkeypatch.setattr(paged, "weigh_rows", lambda *a, **kw: log.append("weigh"))
     cache.weigh(None, None)
     assert log == [((1, 5), (1, 77)), "weigh", ((1, 77), (1, 5))]
+
+
+def test_work_before_a_refusal_is_ordered_all_the_same(lib, monkeypatch):
+    # the attention is on its way when the weights are refused: the cache's next update still comes behind it
+    torch = pytest.importorskip("torch")
+    from kv_cache_token_bf16_gb300 import paged
+    cache, log = fake_streams(monkeypatch, torch)
+
+    def refuse(*a, **kw):
+        raise ValueError("refused")
+
+    monkeypatch.setattr(paged, "shared_attention", lambda *a, **kw: log.append("attend"))
+    monkeypatch.setattr(paged, "weigh_rows", refuse)
+    monkeypatch.setattr(cache, "view", lambda: (None,) * 4, raising=False)
+    with pytest.raises(ValueError, match="refused"):
+        cache.attend(None, lse=0, weigh=True)
+    assert log == [((1, 5), (1, 77)), "attend", ((1, 77), (1, 5))]
 
 
 def fake_rows(monkeypatch, device_index):
