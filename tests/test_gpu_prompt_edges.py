@@ -6,9 +6,10 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from kv_cache_token_bf16_gb300 import prompt  # noqa: E402
+from kv_cache_token_bf16_gb300 import binding, prompt  # noqa: E402
 from tests.paged_util import D, U32  # noqa: E402
 from tests.prompt_util import SCALE, check_prompt, check_weights, weights64  # noqa: E402
+from tests.test_gpu_prompt import rows, run, starts_of  # noqa: E402
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -109,3 +110,99 @@ def test_weights_round_once_where_the_maximum_moves():
         ref = (torch.exp(b.double()) * (1 + side * 2.0 ** -16)).float().bfloat16().double() / total
         fits |= (got - ref).abs() <= (2.0 ** -8 + 2.0 ** -15) * got.abs()
     assert fits.all(), int((~fits).sum())
+
+
+# the largest plane whose units go uncut however few they are, and the first that is cut: some 50 units for 152 SMs
+@pytest.mark.parametrize("m", [1536, 1537])
+@pytest.mark.parametrize("cut", [False, True])
+def test_planes_around_the_longest_that_goes_uncut(m, cut):
+    q, k, v = rows(10, 1, 8, m, std=1.5), rows(11, 1, 2, m), rows(12, 1, 2, m)
+    run(q, k, v, starts_of([m - 700, 1, 699]) if cut else None)
+
+
+def test_a_key_of_nan_has_nan_weights_and_no_other_key():
+    m = 700
+    q, k = big(13, 8, m), big(14, 2, m)
+    lse = torch.randn(1, 8, m, device="cuda", generator=torch.Generator("cuda").manual_seed(15)) + 5.0
+    w, bound = weights64(q, k, lse, [(0, 0, m)])
+    k[0, 0, 300, 5], k[0, 1, 699] = math.nan, math.inf
+    got = prompt.weights(q, k, lse)
+    bad = torch.zeros(1, 2, m, dtype=torch.bool, device="cuda")
+    bad[0, 0, 300] = bad[0, 1, 699] = True          # (infinities of both signs among a row's products)
+    assert torch.isnan(got[bad]).all()
+    check_weights(got[~bad], w[~bad], bound[~bad])
+
+
+LOG2E = math.log2(math.e)
+
+
+def base2(scale):
+    """What the kernels multiply a product by: the header's scale, a little larger, in base 2 and rounded to fp32."""
+    return torch.tensor(scale * LOG2E * (1 + 2.0 ** -23), dtype=torch.float32).double().item()
+
+
+def test_weights_of_large_log_sum_exps_do_not_lean():
+    """Products of one element are exact, so a weight is 2^(z base2 - lse log2 e) but for roundings: of lse log2 e, half a
+    step of 2^-11 at up to 8192, either way, whose mean over 16384 terms is within six of its deviations, 6 ln 2
+    2^-11 / sqrt(12) / 128 < 5e-6; of the logit's difference to it (2^-22) and of ex2 (2^-22); of at most 300 additions
+    (2^-24 each). log2 e alone in fp32 is 1.3e-8 of itself short: 4000 of it would be 5.3e-5."""
+    m, hq = 2048, 8
+    g = torch.Generator().manual_seed(16)
+    q, k = torch.zeros(1, hq, m, D, dtype=torch.bfloat16), torch.zeros(1, 1, m, D, dtype=torch.bfloat16)
+    q[..., 0] = torch.randint(230, 254, (1, hq, m), generator=g) * 16.0
+    k[..., 0] = 1.0
+    lse = q[..., 0].float() + torch.rand(1, hq, m, generator=g) - 0.5
+    got = prompt.weights(q.cuda(), k.cuda(), lse.cuda(), scale=1.0)[0, 0].double().cpu()
+    p = torch.exp2(q[..., 0].double() * base2(1.0) - lse.double() * LOG2E)[0].sum(0)
+    ref = p.flip(0).cumsum(0).flip(0)
+    off = (got[0] / ref[0] - 1).abs()
+    assert off <= 5e-6 + 2 * 2.0 ** -22 + 300 * U32, float(off)
+
+
+@pytest.mark.parametrize("m,n", [(1, 300), (209, 2500)], ids=["few", "many"])
+def test_steps_of_large_log_sum_exps_are_exact(m, n):
+    """As above, and every query of a head is the same, so all roundings lean to one side: that of lse log2 e would be
+    2e-5 and more here, and is made up for. What stays: the difference's, half a step of 2^-18 at up to 64, times ln 2;
+    ex2 and the factor, 2^-22 and 2^-24; at most 66 additions."""
+    h = 8
+    g = torch.Generator().manual_seed(17)
+    l = []
+    while len(l) < h:                               # log-sum-exps whose product with log2 e is rounded by much
+        x = torch.rand((), generator=g) * 100 + 960
+        y = x.double().item() * LOG2E
+        if abs(torch.tensor(y).float().double().item() - y) * math.log(2) > 2e-5:
+            l.append(x.item())
+    lse = torch.tensor(l)[None, :, None].expand(1, h, m).contiguous()
+    q = torch.zeros(1, h, m, D, dtype=torch.bfloat16)
+    q[..., 0] = 1000.0
+    k = torch.zeros(1, h, n, D, dtype=torch.bfloat16)
+    k[..., 0] = 1 + torch.randint(-1, 2, (1, h, n), generator=g) / 128
+    k[..., 0] *= (torch.tensor(l)[None, :, None] / 1000).bfloat16()
+    cache = binding.EvictCache("attention", 1, h, budget=n, n_sink=0, max_block=n)
+    cache.update_and_fetch(k.cuda(), k.cuda())
+    cache.weigh(q.cuda(), lse.cuda(), scale=1.0)
+    cache.sync()
+    got = cache.view()[3].double().cpu()
+    x = 1000.0 * k[..., 0].double() * base2(1.0) - lse[:, :, :1].double() * LOG2E
+    assert x.abs().max() < 40
+    ref = m * torch.exp2(x)
+    off = ((got - ref).abs() / ref).max()
+    assert off <= 2.0 ** -19 * math.log(2) + 2.0 ** -22 + U32 + 66 * U32, float(off)
+    cache.close()
+
+
+def test_weights_of_random_rows_do_not_lean():
+    """Logits spread by 4: the weights are those of logits of some 13. The tensor cores cut 0.9e-7 of such a logit off in
+    the mean and the scale adds 1.2e-7, so what stays is 0.4e-6 of a weight, 1.2e-6 without. Its deviation from weight to
+    weight: half a step of 2^-19 of lse log2 e and as much of the products' sums, some 1e-6."""
+    m = 2048
+    q, k = rows(18, 1, 4, m, std=4.0), rows(19, 1, 4, m)
+    lse = torch.empty(1, 4, m, dtype=torch.float64, device="cuda")
+    for h in range(4):
+        z = SCALE * (q[0, h].double() @ k[0, h].double().T)
+        lse[0, h] = torch.logsumexp(z.masked_fill(torch.ones(m, m, dtype=torch.bool, device="cuda").triu_(1), -math.inf), 1)
+    lse = lse.float()
+    ref, _ = weights64(q, k, lse, [(0, 0, m)])
+    off = prompt.weights(q, k, lse).double() - ref
+    lean, norm = float(off.sum() / ref.sum()), float(off.norm() / ref.norm())
+    assert abs(lean) <= 0.8e-6 and norm <= 2.5e-6, (lean, norm)
