@@ -354,8 +354,7 @@ __device__ void mma_issuer(const PromptParams& p, AttentionShared& sh, int w, ui
 }
 
 // The reference of a row's exponents moved: its O (where there is one) and the half step's weights so far
-// (`columns` of them) follow by the factor f, a power of two: references are whole numbers, so weights that are
-// bf16 already are not rounded again. Whole warp; rare after a unit's first step.
+// (`columns` of them) follow by the factor f. Whole warp; rare after a unit's first step.
 __device__ __noinline__ void move_reference(uint32_t p_at, int columns, uint32_t o_at, float f) {
   tm::wait_stores();
   uint32_t x[16];
@@ -521,7 +520,7 @@ __device__ void softmax_group(const PromptParams& p, AttentionShared& sh, int w,
           float top = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 32; k += 2) top = fmax3(top, y[k] * scale, y[k + 1] * scale);
-          const float to = real ? fmaxf(ref, ceilf(top)) : ref, f = weight_of(ref, to);
+          const float to = real ? fmaxf(ref, top) : ref, f = weight_of(ref, to);
           ref = to;
           sum *= f;
           if (j > 0) wait_products(h);            // O follows once the products before this half step are through
