@@ -534,9 +534,10 @@ int evict_prompt_weights_workspace(const evict_prompt* a, size_t* bytes);
  * natural logarithm of the sum of exp(scale * q . k). Logits, softmax
  * statistics and sums are fp32, the result is rounded to bf16; the weights
  * that multiply the values (not those that are summed) are rounded to bf16,
- * within 2^-8. (The tensor cores' sums lose some 2^-23 of a logit; scale is
- * taken larger by as much, here and in the next two calls.) Results depend on
- * nothing but the arguments.
+ * within 2^-8, and a second time where 32 keys were weighed just before keys
+ * that weigh thousands of times as much. (The tensor cores' sums lose some
+ * 2^-23 of a logit; scale is taken larger by as much, here and in the next two
+ * calls.) Results depend on nothing but the arguments.
  * EVICT_EINVAL: NULL or misaligned pointers, bad sizes or strides, heads that
  * do not divide, out's rows on top of each other or its data that of an input,
  * a workspace that is too small. EVICT_ELIMIT: more than EVICT_MAX_PROMPT_GROUP

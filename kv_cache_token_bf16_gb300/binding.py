@@ -548,7 +548,7 @@ class EvictCache:
                     self._rows = view_tensors(every, self.batch, self.heads, self.dtype, self._held,
                                               f"cuda:{self.device_index}")
                 self._views = n, tuple(x.narrow(2, 0, n) for x in self._rows)
-        # objects of the caller's own, whatever is done to them in place (2 us; as narrow() makes them, 15)
+        # objects of the caller's own, whatever is done to them in place (2 to 4 us between launches; by narrow() 8)
         k, v, pos, score = self._views[1]
         return k.data, v.data, pos.data, score.data
 

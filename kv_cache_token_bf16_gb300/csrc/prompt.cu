@@ -17,11 +17,12 @@
 //
 // What bounds it: a half step of both groups is 1,280 clocks of the tensor cores (logits in halves of 64 columns take
 // 48 clocks a product instead of 32) and takes 1,450; beginning and leaving a unit takes 5,300, of which 3,000 are the
-// stores of its 64 KB. 8192 tokens with 28 / 4 heads 340 us (1.41 PFLOP/s of 1.90); 4 x 2048 with 40 / 8 148 us (1.16);
-// 24 sequences of up to 1021 tokens with 32 / 8 116 us (0.77), 45 tokens 8.2 us.
-// Tried and taken back: logits of 128 columns at once (518 us for the 8192 tokens, with a lone thread issuing), masked
-// and unmasked exponentials apart (10-20 % more on short prompts: instruction cache), the second group a step behind
-// the first (no gain), rows stored 128 bytes by four lanes (packed 124 instead of 129 at the time, but short prompts
+// stores of its 64 KB. 8192 tokens with 28 / 4 heads 333 to 352 us (1.37 to 1.44 PFLOP/s of 1.90); 4 x 2048 with 40 / 8
+// 148 to 156 us (1.10 to 1.16); 24 sequences of up to 1021 tokens with 32 / 8 116 us (0.77), 45 tokens 8.2 us.
+// Tried and taken back: logits of 128 columns at once (518 us for the 8192 tokens; a lone thread issued the products
+// then, and was what bound it, so this says nothing of them with the warps that issue now), masked and unmasked
+// exponentials apart (10-20 % more on short prompts: instruction cache), the second group a step behind the first (no
+// gain), rows stored 128 bytes by four lanes (packed 124 instead of 129 at the time, but short prompts
 // 9.0 instead of 8.7 and the batch as before), results stored by a warpgroup of its own while the groups go on (8192
 // tokens 333 instead of 337, packed 120 instead of 116, 64 sequences of up to 512 100 instead of 91), a ring of four
 // tiles (3-6 % more).
@@ -354,7 +355,10 @@ __device__ void mma_issuer(const PromptParams& p, AttentionShared& sh, int w, ui
 }
 
 // The reference of a row's exponents moved: its O (where there is one) and the half step's weights so far
-// (`columns` of them) follow by the factor f. Whole warp; rare after a unit's first step.
+// (`columns` of them) follow by the factor f, those weights with a second rounding to bf16. (Whole numbers as references
+// would spare them that, but round the largest weight, which is 1 otherwise: outputs were 0.0022 off instead of 0.0017
+// for prompts of up to 45 tokens, and 0.0023 instead of 0.0022 for 8192; with the maximum first and whole steps from
+// there on 0.0017 and 0.0023.) Whole warp; rare after a unit's first step.
 __device__ __noinline__ void move_reference(uint32_t p_at, int columns, uint32_t o_at, float f) {
   tm::wait_stores();
   uint32_t x[16];

@@ -5,8 +5,8 @@
 // Few queries (weigh_kernel): a warp takes 32 keys, straight from memory to the registers of m16n8k16 products (their
 // rows; a lane's 16-byte pieces of a row stand for the product's columns in another order, the same for the queries),
 // and goes through the queries eight at a time, which come from L1 and L2. A key's sum lies in four lanes. Keys are
-// read once: what bounds it is HBM, 4.2 of 6.8 TB/s for one token of 32 caches of 512 rows (32 / 8 heads; 7.9 us).
-// Where there are fewer warps of keys than the GPU has room for, the queries are dealt out to up to eight warps for
+// read once: what bounds it is HBM, 4.2 of 6.8 TB/s for one token of 32 caches of 512 rows (32 / 8 heads; 7.9 to 8.6
+// us). Where there are fewer warps of keys than the GPU has room for, the queries are dealt out to up to eight warps for
 // the same keys. 320 queries over 16384 rows were bound by these products (65 us).
 // Many (weigh_wide_kernel): the large products of the tensor cores, bound by HBM up to about a hundred queries and by
 // the exponentials behind that: 8 heads' 16384 rows by 64 queries 10.9 us (3.1 TB/s), by 320 22.2, by 1024 52 (0.66

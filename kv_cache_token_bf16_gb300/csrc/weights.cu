@@ -6,17 +6,17 @@
 // S^T = K Q^T, keys along the rows of tensor memory: a thread then holds one key and sums along its row, and
 // no sum crosses threads but that of the row's two halves at a unit's end. K is held (two buffers of two
 // 128-row tiles, the next unit's is fetched meanwhile), Q streams through a ring of three 32 KB tiles, and so
-// do its log-sum-exps through shared memory, negated, in base 2 and with -infinity for queries that do not
-// count, whose weights are then 0. Two accumulators for each of the two key tiles (512 columns): products run
+// do its log-sum-exps through shared memory, negated, in base 2 and with a bit for each that is -infinity: those
+// queries are masked, whatever their logits are. Two accumulators for each of the two key tiles (512 columns): products run
 // while the sixteen summing warps exponentiate the step before. Warps 16 and 17 issue the products of one key
 // tile each (of both by one warp they take some 300 clocks of 1,100 from the summing warps beside it) and take
-// turns, so that the one's waits run beside the other's products (8192 tokens, 28 / 4 heads: 183 us, without 190);
-// warp 18 goes through the schedule and fetches (TMA), warp 19 loads the log-sum-exps.
+// turns, so that the one's waits run beside the other's products (8192 tokens, 28 / 4 heads: 183 us, without 190, on one
+// GPU); warp 18 goes through the schedule and fetches (TMA), warp 19 loads the log-sum-exps.
 //
 // What bounds it: a step is 1,024 clocks of the tensor cores and as many of exponentials (at 32 a clock and SM) and
 // takes some 1,750: tensor memory holds no more than the four accumulators, whose products come one after the other,
-// 512 clocks each. 8192 tokens with 28 / 4 heads 183 us (1.31 PFLOP/s of 1.90); 24 sequences of up to 1021 tokens with
-// 32 / 8 heads 68 us, of which 23 would be the products of what queries see: tiles at the diagonal, and their masks;
+// 512 clocks each. 8192 tokens with 28 / 4 heads 183 to 197 us (1.22 to 1.31 PFLOP/s of 1.90); 24 sequences of up to
+// 1021 tokens with 32 / 8 heads 68 us, of which 23 would be the products of what queries see: tiles at the diagonal, and their masks;
 // windows of 64 tokens of 8 x 8192 41 us, 3.3 TB/s.
 // Tried and taken back: K in tensor memory (214 us), 64 columns at a time (190 -> 196), chunks of a masked step that no
 // query or every one sees left out or unmasked (packed no gain, 8192 tokens 200).

@@ -84,6 +84,29 @@ def test_queries_without_a_log_sum_exp_may_hold_anything(hq, hkv, lens, last):
     assert torch.equal(w, prompt.weights(q, k, lse, pk, last=last))
 
 
+def test_weights_round_twice_at_most_where_the_maximum_moves():
+    """The logits of a tile's first 32 columns are weighed before a far larger one is seen in the next, and their bf16
+    weights move along. The last query of each sequence has the logits a, b, c at keys 0, 1, 32 and far lower ones
+    elsewhere; row 1 alone has a 1 in its column of V. Its weight is rounded as it is made and as it moves, 2^-8 each, and
+    the result once more; exponents and sums add 2^-15 (their logits are exact, of up to 29 in base 2)."""
+    n, l = 1024, 64
+    g = torch.Generator().manual_seed(550)
+    a, b, c = [(lo + (hi - lo) * torch.rand(n, generator=g)).bfloat16() for lo, hi in ((4, 5), (2, 4), (14, 20))]
+    q = torch.zeros(n, l, D, dtype=torch.bfloat16)
+    q[:, -1, 0], q[:, -1, 1], q[:, -1, 2], q[:, -1, 3] = a, b, c, 1
+    k, v = torch.zeros_like(q), torch.zeros_like(q)
+    k[:, 0, 0] = k[:, 1, 1] = k[:, 32, 2] = 1
+    k[:, [j for j in range(l) if j not in (0, 1, 32)], 3] = -200
+    v[:, 1, 5] = 1
+    q, k, v = (x.view(1, 1, n * l, D).cuda() for x in (q, k, v))
+    pk = prompt.Packing((torch.arange(n + 1) * l).int().cuda())
+    got = prompt.attention(q, k, v, pk, scale=1.0)
+    pk.sync()
+    got = got.view(n, l, D)[:, -1, 5].double().cpu()
+    ref = torch.exp(b.double()) / sum(torch.exp(x.double()) for x in (a, b, c))
+    assert ((got / ref - 1).abs() <= (1 + 2.0 ** -8) ** 3 * (1 + 2.0 ** -15) - 1).all()
+
+
 # the largest plane whose units go uncut however few they are, and the first that is cut: some 50 units for 152 SMs
 @pytest.mark.parametrize("m", [1536, 1537])
 @pytest.mark.parametrize("cut", [False, True])
