@@ -201,3 +201,41 @@ def test_weights_of_random_rows_do_not_lean():
     off = prompt.weights(q, k, lse).double() - ref
     lean, norm = float(off.sum() / ref.sum()), float(off.norm() / ref.norm())
     assert abs(lean) <= 0.8e-6 and norm <= 2.5e-6, (lean, norm)
+
+
+@pytest.mark.parametrize("fan,m,n", [(1, 3, 300), (24, 4, 3000)], ids=["few", "many"])
+def test_steps_of_queries_without_a_log_sum_exp_may_hold_anything(fan, m, n):
+    hq, hkv = 32, 8
+    k = rows(20, 1, hkv, n, "head")
+    q, lse = rows(21, fan, hq, m), torch.full((fan, hq, m), 6.0, device="cuda")
+    drop = torch.rand(fan, hq, m, device="cuda", generator=torch.Generator("cuda").manual_seed(22)) < 0.2
+    drop[0, :2] = True
+    lse[drop] = -math.inf
+    bad = q.clone()
+    bad[drop] = math.nan
+    bad[0, 0] = math.inf
+    got = []
+    for x in (q, bad):
+        cache = binding.EvictCache("attention", 1, hkv, budget=n, n_sink=0, max_block=n)
+        cache.update_and_fetch(k, k)
+        cache.weigh(x, lse)
+        cache.sync()
+        got.append(cache.view()[3].clone())
+        cache.close()
+    assert torch.equal(*got) and torch.isfinite(got[0]).all() and (got[0] > 0).all()
+
+
+def test_views_are_the_callers_own_objects():
+    k = rows(23, 1, 2, 40, "head")
+    cache = binding.EvictCache("attention", 1, 2, budget=40, n_sink=0, max_block=40)
+    first = cache.update_and_fetch(k, k)
+    first[0].requires_grad_()
+    first[3].unsqueeze_(0)
+    q = rows(24, 1, 4, 1)
+    cache.attend(q, weigh=True)                     # (a K that requires a gradient would be refused)
+    second = cache.view()
+    cache.sync()
+    assert second[3].shape == (1, 2, 40) and not second[0].requires_grad and second[0].data_ptr() == first[0].data_ptr()
+    assert torch.equal(first[3][0], second[3]) and (second[3] > 0).all()
+    cache.close()
+    del first, second
