@@ -506,8 +506,8 @@ class EvictCache:
 
         Work goes on the current stream of the cache's device. Where that is not the cache's own, it is
         ordered behind the cache's last update, and the cache's next one behind it, also inside one graph
-        that captures both streams. A graph that captures the current stream alone cannot hold that order: it reads
-        the rows kept when it is replayed, and the replay has to be ordered like any other reader."""
+        that captures both streams. A graph that captures the current stream alone cannot hold that order:
+        it reads the rows kept when it is replayed, and the replay has to be ordered like any other reader."""
         from . import paged
         if weigh:
             import torch

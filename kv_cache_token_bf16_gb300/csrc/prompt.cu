@@ -212,11 +212,13 @@ __device__ void scrub(const PromptParams& p, AttentionShared& sh, uint32_t ring)
     uint32_t* bad = sh.bad[unit % kUnits];
     if (lane < kBadWords) bad[lane] = 0;
     __syncwarp();
+    // a wait for the unit's last tiles lasts as long as its steps do: of 2^20 tokens 8192 steps, some 13 ms
+    const uint32_t most = kPolls * (1 + (uint32_t)u.steps() / 4096);
 #pragma unroll 1
     for (int step = u.from; step < u.from + u.steps(); ++step) {
       slot.next();                                // the step's V
       if (u.partly(step)) {
-        if (!warp_wait(&sh.partly_full[count % kPartly], (count / kPartly) & 1, &sh.fail)) return;
+        if (!warp_wait(&sh.partly_full[count % kPartly], (count / kPartly) & 1, &sh.fail, most)) return;
 #pragma unroll 1
         for (int r = lane; r < kTile; r += 32) {
           const uint32_t at = ring + slot.i * kTileBytes + r * 128;
@@ -783,7 +785,7 @@ int plan_prompt(const evict_prompt* a, int tile, long long most_steps, int entry
   if (e != cudaSuccess) return cuda_fail(e, "looking up the device");
   P.dev = dev;
   w.whole = blocks * w.hkv >= (long long)whole_rounds * P.sms;
-  // Steps are counted together where units are cut alone: few units then, of planes that are no longer than their blocks.
+  // Steps are added up only where units are cut: the plane has few blocks then, and is short.
   if (!w.whole && (double)blocks * w.hkv * (double)(most_steps + entry) >= 2147483648.0)
     return fail(EVICT_ELIMIT, "the sequences are too long for one call");
   size_t off = 256;                               // an error word, for callers without one

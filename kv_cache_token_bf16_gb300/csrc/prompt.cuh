@@ -299,19 +299,19 @@ __device__ __forceinline__ bool split_unit(const PromptWork& w, int c, SplitUnit
 // Waits at many places, so little code: polls that sleep in hardware, a bounded number of them. The kernel's end
 // reports one that gave up.
 constexpr uint32_t kPolls = 100000;               // of a wait, each of up to 20 us
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* fail) {
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* fail, uint32_t most = kPolls) {
   if (tc::mbar_try_wait(bar, parity)) return true;
 #pragma unroll 1
   for (uint32_t polls = 0; !tc::mbar_try_wait_sleep(bar, parity, kWaitSleepNs);)
-    if (++polls == kPolls || *fail) {
+    if (++polls == most || *fail) {
       *fail = 1;
       return false;
     }
   return true;
 }
 // A warp's wait; the same for all its lanes.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* fail) {
-  return __all_sync(0xffffffffu, wait_for(bar, parity, fail));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* fail, uint32_t most = kPolls) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, fail, most));
 }
 // One lane's value for the warp, which the compiler then knows to be the same: what follows from it stays in uniform
 // registers, where products take their operands from. (A lone thread's, or what might differ, is moved there one by

@@ -7,8 +7,8 @@
 // no sum crosses threads but that of the row's two halves at a unit's end. K is held (two buffers of two
 // 128-row tiles, the next unit's is fetched meanwhile), Q streams through a ring of three 32 KB tiles, and so
 // do its log-sum-exps through shared memory, negated, in base 2 and with a bit for each that is -infinity: those
-// queries are masked, whatever their logits are. Two accumulators for each of the two key tiles (512 columns): products run
-// while the sixteen summing warps exponentiate the step before. Warps 16 and 17 issue the products of one key
+// queries are masked, whatever their logits are. Two accumulators for each of the two key tiles (512 columns):
+// products run while the sixteen summing warps exponentiate the step before. Warps 16 and 17 issue the products of one key
 // tile each (of both by one warp they take some 300 clocks of 1,100 from the summing warps beside it) and take
 // turns, so that the one's waits run beside the other's products (8192 tokens, 28 / 4 heads: 183 us, without 190, on one
 // GPU); warp 18 goes through the schedule and fetches (TMA), warp 19 loads the log-sum-exps.

@@ -7,7 +7,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 from kv_cache_token_bf16_gb300 import binding, prompt  # noqa: E402
-from tests.paged_util import D, U32  # noqa: E402
+from tests.paged_util import D, U32, attend_bounds  # noqa: E402
 from tests.prompt_util import SCALE, check_prompt, check_weights, weights64  # noqa: E402
 from tests.test_gpu_prompt import rows, run, starts_of  # noqa: E402
 
@@ -39,6 +39,31 @@ def test_a_plane_of_eight_million_tokens():
         check_prompt(*x[:3], [(0, 0, b - a)], *x[3:])
         check_weights(w[:, :, a:b], *weights64(x[0], x[1], x[4], [(0, 0, b - a)]))
     assert torch.isfinite(lse).all() and torch.isfinite(w).all()
+
+
+def test_a_sequence_of_a_million_tokens():
+    """Some queries and keys against 64 bits. The sum of a softmax is a chain of 2^15 additions, each rounded either way by
+    up to 2^-24 of the sum so far: six of their deviations are 6 2^-24 / 3 2^7.5 < 2^-15. A key's weight is one of 2^13."""
+    m = 1 << 20
+    q, k, v = big(30, 1, m), big(31, 1, m), big(32, 1, m)
+    lse = torch.empty(1, 1, m, device="cuda")
+    out = prompt.attention(q, k, v, out=torch.empty_like(q), lse=lse)
+    w = prompt.weights(q, k, lse)
+    torch.cuda.synchronize()
+    at = torch.tensor([0, 1, 5000, m // 2 + 77, m - 129, m - 2, m - 1], device="cuda")
+    kd, vd = k[0, 0].double(), v[0, 0].double()
+    z = SCALE * (q[0, 0, at].double() @ kd.T)
+    z = torch.where(torch.arange(m, device="cuda") <= at[:, None], z, -math.inf)
+    ref, p = torch.logsumexp(z, 1), torch.softmax(z, 1)
+    bo, bl = attend_bounds(q[0, 0, at], float(kd.norm(dim=1).max()), (p @ vd).cpu(), ref.cpu(), (p @ vd.abs()).cpu(), weights=2.0 ** -8)
+    assert bool(((lse[0, 0, at].double() - ref).abs().cpu() <= bl + 2.0 ** -15).all())
+    assert bool(((out[0, 0, at].double() - p @ vd).abs().cpu() <= bo).all())
+    for j in (0, 300, m - 1000, m - 1):
+        z = SCALE * (q[0, 0, j:].double() @ kd[j])
+        p = torch.exp(z - lse[0, 0, j:].double())
+        off = 132 * U32 * SCALE * q[0, 0, j:].double().norm(dim=1) * kd[j].norm() + 4 * U32 * (lse[0, 0, j:].double().abs() + z.abs())
+        bound = (p * (off + 2.0 ** -20)).sum() + 2.0 ** -15 * p.sum()
+        assert abs(float(w[0, 0, j] - p.sum())) <= float(bound), j
 
 
 def test_a_window_over_four_million_tokens():
